@@ -11,23 +11,29 @@
 // as the columns of m16n8k16 MMAs (f16 in, fp32 sums): S^T = K q, then
 // O^T += V^T P.  A code times its block's scale has at most six significant
 // bits, so it is exact in f16; q is brought to [1, 2) by a power of two per
-// query (bf16 fits f16 then), and P is formed as 2^(s - m + 7), which keeps
-// weights of 2^-21 normal in f16 and P times a V scale (at most 448) finite.
+// query (bf16 fits f16 then).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "hb_cache.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
+#include "tc_ptx.cuh"
 
 namespace hb {
 namespace {
 
 using namespace kv4;
+using namespace tc;
 
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float P_SHIFT = 7.f;
+constexpr float RAISE = 7.f;          // P <= 2^7: times a V scale (at most 448) it stays finite in f16
+constexpr float LOWEST = -3e38f;      // below every score, and finite: differences with it are too
 constexpr int WARPS = 4;
+constexpr int RING = 4;               // pages a warp has in flight
+constexpr int JOIN_WARPS = 4;
+constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int SPLIT_MIN = 256;        // keys of a split at least
 constexpr int MAX_KEYS = 1 << 27;
 
@@ -113,14 +119,31 @@ __device__ __forceinline__ Col column(const Kv4Attn &p, int seq, int kvh, int c)
     return r;
 }
 
+// Shared memory of a CTA: a ring of RING pages for each warp, and after the
+// key loop (in the same place) the warps' results.
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
+struct Smem {
+    static constexpr int RINGS = WARPS * RING * Layout<D>::BYTES;
+    static constexpr int ROW = D + 4;  // floats of a result row, off the banks of the next
+    static constexpr int JOIN = WARPS * 8 * ROW * 4;
+    static constexpr int BYTES = (RINGS > JOIN ? RINGS : JOIN);
+};
+
+// FEW: one query (d = 128) or two (d = 64) share the kv head.  The eight
+// columns are then the (query, scale block) pairs: column (c, i) holds query
+// c's block i and zeros elsewhere, so the MMAs give the scores block by block
+// and each is scaled once in fp32 instead of each code's value; and in V^T P
+// column (c, i) holds P times the scales of block i, of which channel block
+// i's MMA uses that column alone, so one B fragment serves every channel.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const Kv4Attn p)
 {
     using L = Layout<D>;
     constexpr int NB = L::NB, KW = NB / 2;  // words of a lane's 8- or 16-byte load
-    __shared__ float s_scale[8];
-    __shared__ float s_m[WARPS][8], s_l[WARPS][8];
-    __shared__ float s_o[WARPS][8][D + 4];
+    constexpr int COLS = FEW ? 8 / NB : 8;  // queries of a CTA
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[WARPS][RING];
+    __shared__ float s_scale[8], s_m[WARPS][8], s_l[WARPS][8];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -129,8 +152,15 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
     const int cg = rest % p.col_groups, kvh = rest / p.col_groups;
     const int seq = blockIdx.y;
     const int ncols = p.chunk_len > 0 ? p.chunk_len * p.group : p.group;
-    const int c0 = cg * 8, c1 = min(c0 + 8, ncols);  // this CTA's columns
+    const int c0 = cg * COLS, c1 = min(c0 + COLS, ncols);  // this CTA's queries
 
+    if (lane == 0) {
+        for (int i = 0; i < RING; ++i)
+            mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
     if (p.chunk_len == 0) {
         const int ctx = p.ctx_lens[seq];
         if (ctx < 0 || ctx > p.max_ctx) {  // padding: zeros; outside what the grid was sized for: NaN
@@ -144,21 +174,50 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
             return;
         }
     }
-    const int nkeys = column(p, seq, kvh, c1 - 1).nkeys;  // the most any column sees
+    const int nkeys = column(p, seq, kvh, c1 - 1).nkeys;  // the most any query sees
     const int k0 = split * p.split_len, k1 = min(nkeys, k0 + p.split_len);
     if (k0 >= k1)
         return;
-    const int fewest = column(p, seq, kvh, c0).nkeys;  // keys that every column sees
+    const int fewest = column(p, seq, kvh, c0).nkeys;  // keys that every query sees
 
-    // q of column c0 + g as B fragments, and what its scores are scaled by
+    // ---- this warp's pages: b0 + 4 i, i < n_tiles, through its ring
+    const int b0 = (k0 >> 4) + warp, n_tiles = max(0, (((k1 + 15) >> 4) - b0 + WARPS - 1) / WARPS);
+    const int *tab = p.tables + (size_t)seq * p.bt_stride + b0;
+    uint8_t *ring = smem + warp * RING * L::BYTES;
+    bool bad = false;
+    int ids = lane < n_tiles ? __ldg(tab + lane * WARPS) : 0;  // lane i: page of tile i of the current 32
+    auto issue = [&](int tile, int slot) {
+        if (tile >= n_tiles)
+            return;
+        if ((tile & 31) == 0 && tile > 0)
+            ids = tile + lane < n_tiles ? __ldg(tab + (tile + lane) * WARPS) : 0;
+        const int blk = __shfl_sync(0xffffffffu, ids, tile & 31);
+        const bool ok = blk >= 0 && blk < p.num_blocks;
+        bad |= !ok;
+        if (lane == 0) {
+            if (ok) {
+                mbar_expect_tx(&full[warp][slot], L::BYTES);
+                bulk_load(ring + slot * L::BYTES, p.pool + ((size_t)blk * p.n_kv + kvh) * L::BYTES, L::BYTES,
+                          &full[warp][slot]);
+            } else {
+                mbar_arrive(&full[warp][slot]);  // nothing is read there; what the slot holds is not used
+            }
+        }
+    };
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < RING; ++i)
+        issue(i, i);
+
+    // ---- q as B fragments, and what its scores are scaled by
     uint32_t qf[NB][2];
     {
-        const int c = c0 + g;
+        const int qi = FEW ? g / NB : g;
+        const bool have = c0 + qi < c1;
+        const Col co = column(p, seq, kvh, have ? c0 + qi : c0);
+        const bf16 *qr = p.q + co.row * p.q_stride + (size_t)co.head * D;
         float x[NB][4];
         float a = 0.f;
-        const bool have = c < c1;
-        const Col co = column(p, seq, kvh, have ? c : c0);
-        const bf16 *qr = p.q + co.row * p.q_stride + (size_t)co.head * D;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const uint2 u = *reinterpret_cast<const uint2 *>(qr + 16 * i + 4 * t);
@@ -171,26 +230,32 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
         }
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        const int e = a > 0.f ? ilogbf(a) : 0;
-        const int ec = min(max(e, -126), 127);
-        const float down = ldexpf(1.f, -ec);
+        const int e = a > 0.f ? min(max(ilogbf(a), -126), 127) : 0;
+        const float down = ldexpf(1.f, -e);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            qf[i][0] = have ? pack_h2(x[i][0] * down, x[i][1] * down) : 0u;
-            qf[i][1] = have ? pack_h2(x[i][2] * down, x[i][3] * down) : 0u;
+            const bool put = have && (!FEW || g % NB == i);
+            qf[i][0] = put ? pack_h2(x[i][0] * down, x[i][1] * down) : 0u;
+            qf[i][1] = put ? pack_h2(x[i][2] * down, x[i][3] * down) : 0u;
         }
         if (warp == 0 && t == 0)
-            s_scale[g] = ldexpf(p.ks * (rsqrtf((float)D) * LOG2E), ec);
+            s_scale[g] = ldexpf(p.ks * (rsqrtf((float)D) * LOG2E), e);
     }
     __syncthreads();
-    // columns 2t and 2t + 1 are this lane's in S and O
-    float sc[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int seen[2];
+
+    // Running reference of the softmax (log2).  It moves only when a score
+    // passes it by RAISE: P stays below 2^RAISE, and a tile costs one vote
+    // instead of a maximum over its lanes.
+    constexpr int Q = FEW ? 1 : 2;  // queries this lane keeps: its own column's, or columns 2t and 2t + 1
+    const int myq = FEW ? (2 * t) / NB : 2 * t;
+    float sc[Q], m[Q], l[Q];
+    int seen[Q];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int c = min(c0 + 2 * t + j, c1 - 1);
-        sc[j] = s_scale[2 * t + j];
-        seen[j] = column(p, seq, kvh, c).nkeys;
+    for (int j = 0; j < Q; ++j) {
+        sc[j] = s_scale[FEW ? myq * NB : myq + j];
+        seen[j] = column(p, seq, kvh, min(c0 + myq + j, c1 - 1)).nkeys;
+        m[j] = LOWEST;
+        l[j] = 0.f;
     }
     float o[NB][4];
 #pragma unroll
@@ -199,26 +264,46 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
         for (int j = 0; j < 4; ++j)
             o[i][j] = 0.f;
 
-    const int *tab = p.tables + (size_t)seq * p.bt_stride;
     const int tok0 = 4 * (g >> 1) + (g & 1);  // tokens tok0 and tok0 + 2 are rows g and g + 8 of S^T
-    bool bad = false;
-    for (int b = (k0 >> 4) + warp; b * 16 < k1; b += WARPS) {
-        const int blk = tab[b];
-        if (blk < 0 || blk >= p.num_blocks) {
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, nullptr, WAIT_NS))) {
+            // a page did not come: the rows get NaN, and no copy may land
+            // after the CTA has ended
             bad = true;
-            continue;
+            for (int j = i; j < min(i + RING, n_tiles); ++j)
+                mbar_wait(&full[warp][j % RING], (uint32_t)(j / RING) & 1u, nullptr, WAIT_NS / 8);
+            break;
         }
-        const uint8_t *page = p.pool + ((size_t)blk * p.n_kv + kvh) * L::BYTES;
-        // ---- S^T = K q
-        uint32_t kw[2][KW], kst[2][NB / 2];
+        const uint8_t *page = ring + slot * L::BYTES;
+        // everything of the page into registers, then the slot is free
+        uint32_t kw[2][KW], vw[2][KW], kst[2][FEW ? 1 : NB / 4], vst[FEW ? 1 : NB];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             load_words<KW>(page + L::k_code(tok0 + 2 * r, t, 0), kw[r]);
+            load_words<KW>(page + L::v_code(4 * t + 2 * r, g, 0), vw[r]);
+            if constexpr (FEW)
+                kst[r][0] = *reinterpret_cast<const uint16_t *>(page + L::k_scale(tok0 + 2 * r, (2 * t) % NB));
+            else
 #pragma unroll
-            for (int i = 0; i < NB; i += 2)
-                kst[r][i / 2] =
-                    from_e4m3x2(*reinterpret_cast<const uint16_t *>(page + L::k_scale(tok0 + 2 * r, i)));
+                for (int w = 0; w < NB / 4; ++w)
+                    kst[r][w] = *reinterpret_cast<const uint32_t *>(page + L::k_scale(tok0 + 2 * r, 4 * w));
         }
+        if constexpr (FEW)
+            vst[0] = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, g % NB));
+        else
+#pragma unroll
+            for (int w = 0; w < NB; ++w)
+                vst[w] = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, w));
+        __syncwarp();
+        issue(i + RING, slot);
+        if (++slot == RING) {
+            slot = 0;
+            phase ^= 1u;
+        }
+
+        // ---- S^T = K q
         float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
@@ -226,48 +311,78 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 from_e2m1x8(kw[r][w], a[r]);
-                const uint32_t lo = __byte_perm(kst[r][w], 0, 0x1010), hi = __byte_perm(kst[r][w], 0, 0x3232);
-                a[r][0] = hmul2(a[r][0], lo);
-                a[r][1] = hmul2(a[r][1], lo);
-                a[r][2] = hmul2(a[r][2], hi);
-                a[r][3] = hmul2(a[r][3], hi);
+                if constexpr (!FEW) {
+                    const uint32_t two = from_e4m3x2(kst[r][w / 2] >> (16 * (w & 1)));  // blocks 2w, 2w + 1
+                    const uint32_t lo = __byte_perm(two, 0, 0x1010), hi = __byte_perm(two, 0, 0x3232);
+                    a[r][0] = hmul2(a[r][0], lo);
+                    a[r][1] = hmul2(a[r][1], lo);
+                    a[r][2] = hmul2(a[r][2], hi);
+                    a[r][3] = hmul2(a[r][3], hi);
+                }
             }
             mma_f16(s, a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * w][0], qf[2 * w][1]);
             mma_f16(s, a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
         }
-        // ---- softmax over the 16 keys: rows are tokens, columns queries
+        if constexpr (FEW) {
+            // this lane holds blocks 2t, 2t + 1 (mod NB) of its query for two
+            // tokens; the lanes of the same query hold the rest
+            const float2 f0 = h2f2(from_e4m3x2(kst[0][0])), f1 = h2f2(from_e4m3x2(kst[1][0]));
+            s[0] = s[0] * f0.x + s[1] * f0.y;
+            s[2] = s[2] * f1.x + s[3] * f1.y;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = b * 16 + tok0;
-            const float s0 = k < seen[j] ? s[j] * sc[j] : -INFINITY;
-            const float s1 = k + 2 < seen[j] ? s[2 + j] * sc[j] : -INFINITY;
-            float mx = fmaxf(s0, s1);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m[j], mx);
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            const float corr = exp2f(m[j] - ref);
-            s[j] = exp2f(s0 - ref + P_SHIFT);
-            s[2 + j] = exp2f(s1 - ref + P_SHIFT);
-            l[j] = l[j] * corr + s[j] + s[2 + j];
-            m[j] = mn;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                o[i][j] *= corr;
-                o[i][2 + j] *= corr;
+            for (int x = 1; x < NB / 2; x *= 2) {
+                s[0] += __shfl_xor_sync(0xffffffffu, s[0], x);
+                s[2] += __shfl_xor_sync(0xffffffffu, s[2], x);
             }
         }
+        // ---- softmax: rows are tokens, columns queries
+        const int key = (b0 + i * WARPS) * 16 + tok0;
+        bool raise = false;
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            s[j] = key < seen[j] ? s[j] * sc[j] : -INFINITY;
+            s[2 + j] = key + 2 < seen[j] ? s[2 + j] * sc[j] : -INFINITY;
+            raise |= fmaxf(s[j], s[2 + j]) > m[j] + RAISE;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int j = 0; j < Q; ++j) {
+                float mx = fmaxf(s[j], s[2 + j]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m[j], mx), corr = exp2f(m[j] - mn);
+                m[j] = mn;
+                l[j] *= corr;
+#pragma unroll
+                for (int w = 0; w < NB; ++w) {
+                    o[w][j] *= corr;
+                    o[w][2 + j] *= corr;
+                    if constexpr (FEW) {
+                        o[w][1] *= corr;
+                        o[w][3] *= corr;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            s[j] = exp2f(s[j] - m[j]);
+            s[2 + j] = exp2f(s[2 + j] - m[j]);
+            l[j] += s[j] + s[2 + j];
+        }
         // ---- O^T += V^T P, a V scale times P in place of a scaled V
-        const uint32_t p0 = movmatrix(pack_h2(s[0], s[1]));  // column g, tokens 4t, 4t + 1
-        const uint32_t p1 = movmatrix(pack_h2(s[2], s[3]));  // tokens 4t + 2, 4t + 3
-        uint32_t vw[2][KW];
-        load_words<KW>(page + L::v_code(4 * t, g, 0), vw[0]);
-        load_words<KW>(page + L::v_code(4 * t + 2, g, 0), vw[1]);
+        const uint32_t p0 = movmatrix(pack_h2(s[0], s[FEW ? 0 : 1]));  // column g, tokens 4t, 4t + 1
+        const uint32_t p1 = movmatrix(pack_h2(s[2], s[FEW ? 2 : 3]));  // tokens 4t + 2, 4t + 3
         // a slot that a query does not see may hold anything, a NaN scale
         // among it: where P is 0 its product with the scale is 0 too
-        const bool edge = b * 16 + 16 > fewest;
+        const bool edge = (b0 + i * WARPS) * 16 + 16 > fewest;
         const uint32_t z0 = edge ? nonzero_mask(p0) : 0xffffffffu, z1 = edge ? nonzero_mask(p1) : 0xffffffffu;
+        uint32_t pb[2];
+        if constexpr (FEW) {
+            pb[0] = hmul2(p0, from_e4m3x2(vst[0])) & z0;
+            pb[1] = hmul2(p1, from_e4m3x2(vst[0] >> 16)) & z1;
+        }
 #pragma unroll
         for (int w = 0; w < KW / 2; ++w) {
             // bytes of two tokens (channels 2g, 2g + 1) to bytes of two channels
@@ -279,45 +394,59 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
                 from_e2m1x8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), a[2 * h + 1]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t vs = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, 4 * w + i));
-                const uint32_t b0 = hmul2(p0, from_e4m3x2(vs & 0xffffu)) & z0;
-                const uint32_t b1 = hmul2(p1, from_e4m3x2(vs >> 16)) & z1;
-                mma_f16(o[4 * w + i], a[0][i], a[1][i], a[2][i], a[3][i], b0, b1);
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (!FEW) {
+                    pb[0] = hmul2(p0, from_e4m3x2(vst[4 * w + j])) & z0;
+                    pb[1] = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16)) & z1;
+                }
+                mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb[0], pb[1]);
             }
         }
     }
 
     // ---- join the warps
+    __syncthreads();  // the rings are done with
+    float(*s_o)[8][Smem<D>::ROW] = reinterpret_cast<float(*)[8][Smem<D>::ROW]>(smem);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < Q; ++j) {
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
-        if (bad) {  // a block id outside the pool poisons every column
+        if (bad) {  // a block id outside the pool poisons every query
             l[j] = __int_as_float(0x7fc00000);
             m[j] = 0.f;
         }
-        if (g == 0) {
-            s_m[warp][2 * t + j] = m[j];
-            s_l[warp][2 * t + j] = l[j];
+        if (g == 0 && (!FEW || (2 * t) % NB == 0)) {
+            s_m[warp][myq + j] = m[j];
+            s_l[warp][myq + j] = l[j];
         }
+    }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            s_o[warp][2 * t + j][16 * i + 2 * g] = o[i][j];
-            s_o[warp][2 * t + j][16 * i + 2 * g + 1] = o[i][2 + j];
+    for (int i = 0; i < NB; ++i) {
+        if constexpr (FEW) {
+            // of channel block i, column i alone (of each query): 2t or 2t + 1
+            if ((2 * t) % NB == (i & ~1)) {
+                s_o[warp][myq][16 * i + 2 * g] = o[i][i & 1];
+                s_o[warp][myq][16 * i + 2 * g + 1] = o[i][2 + (i & 1)];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                s_o[warp][2 * t + j][16 * i + 2 * g] = o[i][j];
+                s_o[warp][2 * t + j][16 * i + 2 * g + 1] = o[i][2 + j];
+            }
         }
     }
     __syncthreads();
     for (int c = c0 + warp; c < c1; c += WARPS) {
         const Col co = column(p, seq, kvh, c);
-        float M = -INFINITY, lsum = 0.f, f[WARPS];
+        float M = LOWEST, lsum = 0.f, f[WARPS];
 #pragma unroll
         for (int w = 0; w < WARPS; ++w)
             M = fmaxf(M, s_m[w][c - c0]);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            f[w] = s_m[w][c - c0] == -INFINITY ? 0.f : exp2f(s_m[w][c - c0] - M);
+            f[w] = exp2f(s_m[w][c - c0] - M);
             lsum += s_l[w][c - c0] * f[w];
         }
         const bool whole = co.nkeys <= p.split_len;  // this split holds every key the query sees
@@ -325,57 +454,80 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv4_attention(const Kv4Attn p)
         const size_t at = ((size_t)co.row * p.n_heads + co.head) * p.n_splits + split;
         if (whole && split > 0)
             continue;
-        for (int e = lane; e < D; e += 32) {
-            float v = 0.f;
+        for (int e = 2 * lane; e < D; e += 64) {
+            float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w)
-                v += s_o[w][c - c0][e] * f[w];
+            for (int w = 0; w < WARPS; ++w) {
+                const float2 x = *reinterpret_cast<const float2 *>(&s_o[w][c - c0][e]);
+                v0 += x.x * f[w];
+                v1 += x.y * f[w];
+            }
             if (whole)
-                p.out[co.row * p.out_stride + (size_t)co.head * D + e] = f2bf(v * inv);
+                *reinterpret_cast<__nv_bfloat162 *>(p.out + co.row * p.out_stride + (size_t)co.head * D + e) =
+                    __floats2bfloat162_rn(v0 * inv, v1 * inv);
             else
-                p.part_o[at * D + e] = v;
+                *reinterpret_cast<float2 *>(p.part_o + at * D + e) = make_float2(v0, v1);
         }
         if (!whole && lane == 0)
             p.part_ml[at] = make_float2(M, lsum);
     }
 }
 
-// Joins the splits of one (row, head) per warp, in order.
+// Joins the splits of one (row, head): each warp some of them, then the warps
+// in order.
 template <int D>
-__global__ void __launch_bounds__(128) k_kv4_join(const Kv4Attn p, int n_rows)
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_kv4_join(const Kv4Attn p)
 {
-    const int lane = threadIdx.x & 31;
-    const long long idx = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    constexpr int E = D / 32;
+    __shared__ float s_l[JOIN_WARPS], s_o[JOIN_WARPS][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    if (idx >= (long long)n_rows * p.n_heads)
-        return;
-    const int row = (int)(idx / p.n_heads), head = (int)(idx - (long long)row * p.n_heads);
+    pdl_trigger();
+    const int row = blockIdx.x / p.n_heads, head = blockIdx.x - row * p.n_heads;
     const int nkeys = p.chunk_len > 0 ? p.chunk_offset + row + 1 : p.ctx_lens[row] + 1;
     if (nkeys <= p.split_len || (p.chunk_len == 0 && nkeys > p.max_ctx + 1))
         return;  // written by the first kernel
     const int n = (nkeys + p.split_len - 1) / p.split_len;
-    const float2 *ml = p.part_ml + (size_t)idx * p.n_splits;
-    const float *po = p.part_o + (size_t)idx * p.n_splits * D;
-    float M = -INFINITY;
-    for (int s = 0; s < n; ++s)
+    const float2 *ml = p.part_ml + (size_t)blockIdx.x * p.n_splits;
+    const float *po = p.part_o + (size_t)blockIdx.x * p.n_splits * D + lane * E;
+    float M = LOWEST;
+    for (int s = lane; s < n; s += 32)
         M = fmaxf(M, ml[s].x);
-    float l = 0.f, o[D / 32];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e)
+    for (int x = 16; x > 0; x >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
         o[e] = 0.f;
-    for (int s = 0; s < n; ++s) {
+#pragma unroll 4
+    for (int s = warp; s < n; s += JOIN_WARPS) {
         const float2 x = ml[s];
-        const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
+        const float f = exp2f(x.x - M);
         l += x.y * f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            o[e] += po[(size_t)s * D + e * 32 + lane] * f;
+        if constexpr (E == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
+            o[0] += v.x * f, o[1] += v.y * f, o[2] += v.z * f, o[3] += v.w * f;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(po + (size_t)s * D);
+            o[0] += v.x * f, o[1] += v.y * f;
+        }
     }
-    const float inv = p.vs / l;
-    bf16 *orow = p.out + row * p.out_stride + (size_t)head * D;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-        orow[e * 32 + lane] = f2bf(o[e] * inv);
+    for (int e = 0; e < E; ++e)
+        s_o[warp][lane * E + e] = o[e];
+    if (lane == 0)
+        s_l[warp] = l;
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += JOIN_WARPS * 32) {
+        float v = 0.f, lsum = 0.f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) {
+            v += s_o[w][e];
+            lsum += s_l[w];
+        }
+        p.out[row * p.out_stride + (size_t)head * D + e] = f2bf(v * (p.vs / lsum));
+    }
 }
 
 struct Split {
@@ -387,7 +539,7 @@ struct Split {
 Split plan_split(long long ctas, int max_keys)
 {
     const int sms = 152;
-    long long want = (4ll * sms + ctas - 1) / ctas;
+    long long want = (5ll * sms + ctas - 1) / ctas;
     const long long most = (max_keys + SPLIT_MIN - 1) / SPLIT_MIN;
     if (want > most)
         want = most;
@@ -410,18 +562,41 @@ bool dims_ok(int n_heads, int n_kv, int d)
 
 long long ctas_of(int cols, int n_kv, int seqs) { return (long long)((cols + 7) / 8) * n_kv * seqs; }
 
+// Queries a CTA takes: see k_kv4_attention.
+bool few(int cols, int d) { return cols <= (d == 128 ? 1 : 2); }
+
+template <int D, bool FEW>
+cudaError_t launch_d(const Kv4Attn &p, dim3 grid, cudaStream_t s)
+{
+    static std::once_flag once;
+    static cudaError_t set;
+    std::call_once(once, [] {
+        set = cudaFuncSetAttribute(k_kv4_attention<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
+    });
+    if (set != cudaSuccess)
+        return set;
+    return launch_kernel(true, k_kv4_attention<D, FEW>, grid, dim3(WARPS * 32), Smem<D>::BYTES, s, p);
+}
+
 int launch(Kv4Attn &p, int d, int seqs, int rows, cudaStream_t s)
 {
+    const int cols = p.chunk_len > 0 ? p.chunk_len * p.group : p.group;
+    const bool f = few(cols, d);
+    p.col_groups = f ? 1 : (cols + 7) / 8;
     const long long gx = (long long)p.n_splits * p.col_groups * p.n_kv;
     if (gx > 0x7fffffff)
         return HB_ERANGE;
-    auto kern = d == 128 ? k_kv4_attention<128> : k_kv4_attention<64>;
-    if (launch_kernel(false, kern, dim3((unsigned)gx, (unsigned)seqs), dim3(WARPS * 32), 0, s, p) != cudaSuccess)
+    const dim3 grid((unsigned)gx, (unsigned)seqs);
+    const cudaError_t e = d == 128 ? (f ? launch_d<128, true>(p, grid, s) : launch_d<128, false>(p, grid, s))
+                                   : (f ? launch_d<64, true>(p, grid, s) : launch_d<64, false>(p, grid, s));
+    if (e != cudaSuccess)
         return HB_ECUDA;
     if (p.n_splits > 1) {
         auto join = d == 128 ? k_kv4_join<128> : k_kv4_join<64>;
-        const long long warps = (long long)rows * p.n_heads;
-        if (launch_kernel(true, join, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, p, rows) != cudaSuccess)
+        const long long blocks = (long long)rows * p.n_heads;
+        if (blocks > 0x7fffffff)
+            return HB_ERANGE;
+        if (launch_kernel(true, join, dim3((unsigned)blocks), dim3(JOIN_WARPS * 32), 0, s, p) != cudaSuccess)
             return HB_ECUDA;
     }
     return HB_OK;
@@ -476,7 +651,6 @@ extern "C" int hb_kv4_decode(const hb_kv4_pool *pool, const void *q, long long q
     p.ctx_lens = ctx_lens;
     p.max_ctx = max_ctx;
     p.n_heads = n_heads;
-    p.col_groups = (p.group + 7) / 8;
     const Split sp = plan_split(ctas_of(p.group, p.n_kv, n_decodes), max_ctx + 1);
     p.split_len = sp.len;
     p.n_splits = sp.n;
@@ -541,7 +715,6 @@ extern "C" int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_
     p.chunk_len = chunk_len;
     p.n_heads = n_heads;
     const int cols = chunk_len * p.group;
-    p.col_groups = (cols + 7) / 8;
     const Split sp = plan_split(ctas_of(cols, p.n_kv, 1), (int)keys);
     p.split_len = sp.len;
     p.n_splits = sp.n;
