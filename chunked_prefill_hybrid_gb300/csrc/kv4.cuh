@@ -2,11 +2,13 @@
 // in a pool, and the conversions of its codes and scales.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace hb {
 namespace kv4 {
@@ -80,6 +82,80 @@ __device__ __forceinline__ uint32_t from_e4m3x2(uint32_t two)
 }
 
 __device__ __forceinline__ float2 h2f2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N])
+{
+    if constexpr (N == 4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        w[0] = u.x, w[1] = u.y;
+    }
+}
+
+// Power of two e that brings a query whose largest magnitude is a into [1, 4)
+// (0 for a = 0), and 2^e itself, e in [-126, 126].
+__device__ __forceinline__ int query_exponent(float a)
+{
+    const int e = (int)(__float_as_uint(a) >> 23) - 127;
+    return a > 0.f ? min(max(e, -126), 126) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// mbar_wait for waits that are mostly long: the thread sleeps inside
+// try_wait, up to 20 us at a time, and leaves the issue slots to others.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            "selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(ok)
+            : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok)
+            return true;
+        if (abort && *abort)
+            return false;
+        const uint64_t now = tc::globaltimer_ns();
+        if (t0 == 0)
+            t0 = now;
+        else if (now - t0 > limit_ns)
+            return false;
+    }
+}
+
+// 2^x to about 2 ulp (results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOWEST = -3e38f;  // below every score, and finite: differences with it are too
 
 }  // namespace kv4
 }  // namespace hb

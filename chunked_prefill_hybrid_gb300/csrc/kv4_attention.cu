@@ -10,7 +10,7 @@
 // A warp takes 16 keys at a time and up to eight queries that share a kv head
 // as the columns of m16n8k16 MMAs (f16 in, fp32 sums): S^T = K q, then
 // O^T += V^T P.  A code times its block's scale has at most six significant
-// bits, so it is exact in f16; q is brought to [1, 2) by a power of two per
+// bits, so it is exact in f16; q is brought to [1, 4) by a power of two per
 // query (bf16 fits f16 then).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "hb_cache.h"
 #include "kv4.cuh"
+#include "kv4_chunk.h"
 #include "kv4_host.h"
 #include "tc_ptx.cuh"
 
@@ -27,15 +28,15 @@ namespace {
 using namespace kv4;
 using namespace tc;
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RAISE = 7.f;          // P <= 2^7: times a V scale (at most 448) it stays finite in f16
-constexpr float LOWEST = -3e38f;      // below every score, and finite: differences with it are too
 constexpr int WARPS = 4;
 constexpr int RING = 4;               // pages a warp has in flight
 constexpr int JOIN_WARPS = 4;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int SPLIT_MIN = 256;        // keys of a split at least
 constexpr int MAX_KEYS = 1 << 27;
+constexpr int MAX_COLS = 1 << 24;     // queries of a kv head in a chunk
+constexpr int CHUNK_COLS = 8;         // queries of a kv head up to which a chunk runs as decode columns
 
 struct Kv4Attn {
     const uint8_t *pool;
@@ -73,36 +74,10 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
     return r;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // All ones in each half of x that is not 0.
 __device__ __forceinline__ uint32_t nonzero_mask(uint32_t x)
 {
     return ((x & 0x00007fffu) ? 0x0000ffffu : 0u) | ((x & 0x7fff0000u) ? 0xffff0000u : 0u);
-}
-
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N])
-{
-    if constexpr (N == 4) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        w[0] = u.x, w[1] = u.y;
-    }
 }
 
 // Row, head and visible keys of query column c of kv head kvh.
@@ -230,8 +205,8 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         }
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        const int e = a > 0.f ? min(max(ilogbf(a), -126), 127) : 0;
-        const float down = ldexpf(1.f, -e);
+        const int e = query_exponent(a);
+        const float down = pow2(-e);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const bool put = have && (!FEW || g % NB == i);
@@ -239,7 +214,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             qf[i][1] = put ? pack_h2(x[i][2] * down, x[i][3] * down) : 0u;
         }
         if (warp == 0 && t == 0)
-            s_scale[g] = ldexpf(p.ks * (rsqrtf((float)D) * LOG2E), e);
+            s_scale[g] = p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e);
     }
     __syncthreads();
 
@@ -268,7 +243,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     int slot = 0;
     uint32_t phase = 0;
     for (int i = 0; i < n_tiles; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, nullptr, WAIT_NS))) {
+        if (!__all_sync(0xffffffffu, mbar_sleep(&full[warp][slot], phase, nullptr, WAIT_NS))) {
             // a page did not come: the rows get NaN, and no copy may land
             // after the CTA has ended
             bad = true;
@@ -351,7 +326,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float mn = fmaxf(m[j], mx), corr = exp2f(m[j] - mn);
+                const float mn = fmaxf(m[j], mx), corr = ex2(m[j] - mn);
                 m[j] = mn;
                 l[j] *= corr;
 #pragma unroll
@@ -367,8 +342,8 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         }
 #pragma unroll
         for (int j = 0; j < Q; ++j) {
-            s[j] = exp2f(s[j] - m[j]);
-            s[2 + j] = exp2f(s[2 + j] - m[j]);
+            s[j] = ex2(s[j] - m[j]);
+            s[2 + j] = ex2(s[2 + j] - m[j]);
             l[j] += s[j] + s[2 + j];
         }
         // ---- O^T += V^T P, a V scale times P in place of a scaled V
@@ -446,7 +421,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             M = fmaxf(M, s_m[w][c - c0]);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            f[w] = exp2f(s_m[w][c - c0] - M);
+            f[w] = ex2(s_m[w][c - c0] - M);
             lsum += s_l[w][c - c0] * f[w];
         }
         const bool whole = co.nkeys <= p.split_len;  // this split holds every key the query sees
@@ -503,7 +478,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_kv4_join(const Kv4Attn p)
 #pragma unroll 4
     for (int s = warp; s < n; s += JOIN_WARPS) {
         const float2 x = ml[s];
-        const float f = exp2f(x.x - M);
+        const float f = ex2(x.x - M);
         l += x.y * f;
         if constexpr (E == 4) {
             const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
@@ -668,6 +643,33 @@ extern "C" int hb_kv4_decode(const hb_kv4_pool *pool, const void *q, long long q
     return launch(p, d, n_decodes, n_decodes, (cudaStream_t)cuda_stream);
 }
 
+// A chunk of few queries runs as columns of the decode kernel (`p` is filled
+// then, 0 returned), any other on the tcgen05 kernel (`c`, 1); -1: too large.
+static int plan_chunk(Kv4Attn &p, Kv4Chunk &c, int offset, int len, int n_heads, int n_kv, int d, long long *need)
+{
+    const int group = n_heads / n_kv;
+    if ((long long)len * group <= CHUNK_COLS) {
+        p.n_kv = n_kv;
+        p.group = group;
+        p.n_heads = n_heads;
+        p.chunk_offset = offset;
+        p.chunk_len = len;
+        const Split sp = plan_split(ctas_of(len * group, n_kv, 1), offset + len);
+        p.split_len = sp.len;
+        p.n_splits = sp.n;
+        *need = workspace_bytes_of(len, n_heads, d, sp.n);
+        return 0;
+    }
+    c.n_kv = n_kv;
+    c.group = group;
+    c.n_heads = n_heads;
+    c.offset = offset;
+    if (!kv4_chunk_plan(c, len))
+        return -1;
+    *need = kv4_chunk_workspace_bytes(c, d);
+    return 1;
+}
+
 extern "C" long long hb_kv4_chunk_workspace(int chunk_offset, int chunk_len, int n_heads, int n_kv_heads, int head_dim)
 {
     if (chunk_offset < 0 || chunk_len < 0 || !dims_ok(n_heads, n_kv_heads, head_dim) ||
@@ -675,10 +677,12 @@ extern "C" long long hb_kv4_chunk_workspace(int chunk_offset, int chunk_len, int
         return HB_EINVAL;
     if (chunk_len == 0)
         return 0;
-    if ((long long)chunk_len * (n_heads / n_kv_heads) > 0x7fffffff)
+    if ((long long)chunk_len * (n_heads / n_kv_heads) > MAX_COLS)
         return HB_EINVAL;
-    const Split sp = plan_split(ctas_of(chunk_len * (n_heads / n_kv_heads), n_kv_heads, 1), chunk_offset + chunk_len);
-    return workspace_bytes_of(chunk_len, n_heads, head_dim, sp.n);
+    Kv4Attn p{};
+    Kv4Chunk c;
+    long long need = 0;
+    return plan_chunk(p, c, chunk_offset, chunk_len, n_heads, n_kv_heads, head_dim, &need) < 0 ? HB_EINVAL : need;
 }
 
 extern "C" int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_stride, const int32_t *block_table,
@@ -698,36 +702,46 @@ extern "C" int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_
         kv4_check_rows(out, out_stride, chunk_len, width))
         return HB_EINVAL;
     const long long keys = (long long)chunk_offset + chunk_len;
-    if (keys > MAX_KEYS || n_blocks < (keys + 15) / 16 || (long long)chunk_len * (n_heads / pool->n_kv_heads) > 0x7fffffff)
+    if (keys > MAX_KEYS || n_blocks < (keys + 15) / 16 ||
+        (long long)chunk_len * (n_heads / pool->n_kv_heads) > MAX_COLS)
         return HB_ERANGE;
     Kv4Attn p{};
+    Kv4Chunk c;
+    long long need = 0;
+    const int which = plan_chunk(p, c, chunk_offset, chunk_len, n_heads, pool->n_kv_heads, d, &need);
+    if (which < 0)
+        return HB_ERANGE;
+    if (need > 0) {
+        if (workspace_bytes < need)
+            return HB_ERANGE;
+        if (!workspace || (uintptr_t)workspace % 16)
+            return HB_EINVAL;
+    }
+    if (which == 1) {
+        c.pool = (const uint8_t *)pool->data;
+        c.num_blocks = pool->num_blocks;
+        c.ks = pool->k_scale;
+        c.vs = pool->v_scale;
+        c.q = (const bf16 *)q;
+        c.q_stride = q_stride;
+        c.table = block_table;
+        c.out = (bf16 *)out;
+        c.out_stride = out_stride;
+        c.part_o = (float *)workspace;
+        c.part_ml = (float2 *)(c.part_o + (size_t)2 * c.ctas * KC_ROWS * d);
+        return launch_kv4_chunk(c, d, (cudaStream_t)cuda_stream) == cudaSuccess ? HB_OK : HB_ECUDA;
+    }
     p.pool = (const uint8_t *)pool->data;
     p.num_blocks = pool->num_blocks;
-    p.n_kv = pool->n_kv_heads;
-    p.group = n_heads / p.n_kv;
     p.ks = pool->k_scale;
     p.vs = pool->v_scale;
     p.q = (const bf16 *)q;
     p.q_stride = q_stride;
     p.tables = block_table;
     p.bt_stride = n_blocks;
-    p.chunk_offset = chunk_offset;
-    p.chunk_len = chunk_len;
-    p.n_heads = n_heads;
-    const int cols = chunk_len * p.group;
-    const Split sp = plan_split(ctas_of(cols, p.n_kv, 1), (int)keys);
-    p.split_len = sp.len;
-    p.n_splits = sp.n;
     p.out = (bf16 *)out;
     p.out_stride = out_stride;
-    const long long need = workspace_bytes_of(chunk_len, n_heads, d, sp.n);
-    if (need > 0) {
-        if (workspace_bytes < need)
-            return HB_ERANGE;
-        if (!workspace || (uintptr_t)workspace % 16)
-            return HB_EINVAL;
-        p.part_o = (float *)workspace;
-        p.part_ml = (float2 *)(p.part_o + (size_t)chunk_len * n_heads * sp.n * d);
-    }
+    p.part_o = (float *)workspace;
+    p.part_ml = (float2 *)(p.part_o + (size_t)chunk_len * n_heads * p.n_splits * d);
     return launch(p, d, 1, chunk_len, (cudaStream_t)cuda_stream);
 }

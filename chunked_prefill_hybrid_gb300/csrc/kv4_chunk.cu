@@ -1,0 +1,877 @@
+// kv4_chunk.cu -- a prefill chunk's attention over the 4-bit paged cache on
+// the tcgen05 tensor cores.
+//
+//   S = Q K^T,  P = 2^(S c - m),  O += P V,  o = O / sum P
+//
+// For one kv head the chunk's (row, head) pairs are the columns of an item,
+// 256 at a time; an item's keys come in tiles of 128.  A CTA works through a
+// contiguous range of (item, key tile) units, as many to every CTA; an item
+// that several CTAs share leaves fp32 partials, which a second kernel joins.
+//
+//   warp 13      loader: one bulk copy per page (16 keys) into a ring
+//   warps 8..11, codes and scales -> f16 K and V tiles (128-byte swizzle);
+//     14, 15     code x scale is exact in f16
+//   warp 12      issues the MMAs: S of both 128-row halves, and O += P V with
+//                P read from tensor memory
+//   warps 0..7   softmax, one thread per query: S from tensor memory, P back
+//                into it as f16; O is rescaled only when a maximum rises by
+//                more than 2^8
+//
+// While one half's softmax runs, the tensor pipe works on the other's
+// products.  256 rows share each dequantised tile: its conversion takes the
+// four warps about 800 shared-memory cycles against 2048 of MMA.
+//
+// Every wait is bounded; when one runs out, the CTA writes NaN for the rows
+// it has left, drains and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "kv4.cuh"
+#include "kv4_chunk.h"
+#include "tc_ptx.cuh"
+
+namespace hb {
+namespace {
+
+using namespace kv4;
+using namespace tc;
+
+constexpr int THREADS = 16 * 32;
+constexpr int RING = 12;                 // pages in flight
+constexpr float RAISE = 8.f;             // P <= 2^8
+constexpr uint64_t WAIT_NS = 2000000000ull;
+
+template <int D>
+struct Ck {
+    static constexpr int CB = D / 64;                 // column blocks of 64 channels
+    static constexpr int BLK = 128 * 128;             // one column block of a 128-row tile
+    static constexpr int TILE = CB * BLK;
+    static constexpr int RAW = Layout<D>::BYTES;
+    static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, R = 6 * TILE;
+    static constexpr int BAR = R + RING * RAW;
+    static constexpr int BYTES = BAR + 512 + 1024;    // barriers, alignment
+    static constexpr uint32_t S_COL = 128, O0 = 256, O_COL = D;
+};
+
+// byte offset of (row, 16-byte chunk c) in a 128-byte-swizzled column block
+__device__ __forceinline__ uint32_t swz(int row, int c)
+{
+    return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// MN-major operand, 128-byte swizzle: 64-element column blocks block_stride
+// bytes apart, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block_stride)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((block_stride >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// f16 A and B, fp32 D, A K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
+{
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D (+)= A B with A in tensor memory (one elected lane issues).
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+        "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
+        "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t x, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// x times the low (high) half of s.
+__device__ __forceinline__ uint32_t mul_lo(uint32_t x, uint32_t s)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __low2half2(*reinterpret_cast<__half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t mul_hi(uint32_t x, uint32_t s)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __high2half2(*reinterpret_cast<__half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------------- work
+
+// Key tiles of item qt.
+__host__ __device__ inline int item_tiles(const Kv4Chunk &p, int qt)
+{
+    const long long last = (long long)(qt + 1) * KC_ROWS < p.cols ? (long long)(qt + 1) * KC_ROWS : p.cols;
+    return (p.offset + (int)((last - 1) / p.group)) / KC_KEYS + 1;
+}
+
+// The segments of a CTA: the parts of items in its range, in order.
+struct Segments {
+    int left;         // units of the range still to come
+    int kvh, qt, kt0, kt1, n_tiles;
+    bool first;       // the segment starts with the range
+
+    __device__ Segments(const Kv4Chunk &p, int cta)
+    {
+        const KcStart s = p.start[cta];
+        kvh = s.kvh;
+        qt = s.qt;
+        kt0 = s.kt0;
+        left = s.units;
+        first = true;
+        size(p);
+    }
+    __device__ void size(const Kv4Chunk &p)
+    {
+        n_tiles = item_tiles(p, qt);
+        kt1 = min(n_tiles, kt0 + left);
+    }
+    __device__ bool more() const { return left > 0; }
+    __device__ void next(const Kv4Chunk &p)
+    {
+        left -= kt1 - kt0;
+        kt0 = 0;
+        first = false;
+        if (++qt == p.n_qt) {
+            qt = 0;
+            ++kvh;
+        }
+        if (left > 0)
+            size(p);
+    }
+    __device__ int halves(const Kv4Chunk &p) const { return p.cols - (long long)qt * KC_ROWS > 128 ? 2 : 1; }
+    // keys that the item's last column sees
+    __device__ int keys(const Kv4Chunk &p) const
+    {
+        const long long last = min((long long)(qt + 1) * KC_ROWS, (long long)p.cols) - 1;
+        return p.offset + (int)(last / p.group) + 1;
+    }
+};
+
+// ---------------------------------------------------------------- dequant
+
+// K of one page into rows row0.. (a multiple of 16) of a tile.  Lane 4 g + t:
+// tokens g and g + 8, channels 4t..4t+3 of every block.  The four chunks that
+// a lane writes in a row lie at four lane constants; everything else is an
+// immediate.
+template <int D>
+__device__ __forceinline__ void page_k(const uint8_t *raw, uint8_t *tile, int row0, int lane)
+{
+    using L = Layout<D>;
+    constexpr int KW = L::NB / 2;
+    const int g = lane >> 2, t = lane & 3;
+    uint8_t *base = tile + row0 * 128 + g * 128 + 8 * (t & 1);
+    uint8_t *at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        at[k] = base + (((2 * k + (t >> 1)) ^ g) << 4);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        uint32_t w[KW], sb[L::NB / 4];
+        load_words<KW>(raw + L::k_code(g + 8 * r, t, 0), w);
+#pragma unroll
+        for (int i = 0; i < L::NB / 4; ++i)
+            sb[i] = *reinterpret_cast<const uint32_t *>(raw + L::k_scale(g + 8 * r, 4 * i));
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {  // blocks 2i, 2i + 1
+            uint32_t a[4];
+            from_e2m1x8(w[i], a);
+            const uint32_t two = from_e4m3x2(sb[i / 2] >> (16 * (i & 1)));
+            const int off = (i / 2) * Ck<D>::BLK + r * 1024;
+            *reinterpret_cast<uint2 *>(at[2 * (i & 1)] + off) = make_uint2(mul_lo(a[0], two), mul_lo(a[1], two));
+            *reinterpret_cast<uint2 *>(at[2 * (i & 1) + 1] + off) = make_uint2(mul_hi(a[2], two), mul_hi(a[3], two));
+        }
+    }
+}
+
+// V of one page.  Lane 4 g + t: channels 2g, 2g + 1 of every block, tokens
+// 4t..4t+3, two at a time in an order that keeps the four t on different
+// banks of the swizzle.  NaN scales become 0 when scrub is set (what they
+// hide is found again at the end of the segment).
+template <int D>
+__device__ __forceinline__ void page_v(const uint8_t *raw, uint8_t *tile, int row0, int lane, bool scrub)
+{
+    using L = Layout<D>;
+    constexpr int KW = L::NB / 2;
+    const int g = lane >> 2, t = lane & 3;
+    const int h0 = t >> 1;  // lanes of the upper tokens start with the other two
+    // token 4t + 2h + u is row 4t + 2h + u: 8-row group t / 2, row 4 (t & 1) + 2h + u in it
+    uint8_t *base = tile + row0 * 128 + (t >> 1) * 1024 + (t & 1) * 512 + 4 * (g & 3);
+    const int r4 = 4 * (t & 1) + 2 * h0;
+    uint8_t *at[2][4];  // [u][j]: chunk 2j + g / 4 of row 4t + 2 h0 + u
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            at[u][j] = base + (((2 * j + (g >> 2)) ^ (r4 + u)) << 4) + u * 128;
+    uint32_t sb[L::NB];
+#pragma unroll
+    for (int i = 0; i < L::NB; ++i) {
+        sb[i] = *reinterpret_cast<const uint32_t *>(raw + L::v_scale(4 * t, i));
+        if (scrub)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if ((sb[i] >> (8 * k) & 0x7fu) == 0x7fu)
+                    sb[i] &= ~(0xffu << (8 * k));
+        if (h0)
+            sb[i] = __byte_perm(sb[i], 0, 0x1032);  // the two tokens taken first in the low half
+    }
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        const int h = h0 ^ hh;
+        uint32_t w[KW];
+        load_words<KW>(raw + L::v_code(4 * t + 2 * h, g, 0), w);
+#pragma unroll
+        for (int i4 = 0; i4 < L::NB / 4; ++i4) {
+            uint32_t a[2][4];
+            from_e2m1x8(w[i4], a[0]);
+            from_e2m1x8(w[KW / 2 + i4], a[1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = from_e4m3x2(hh ? sb[4 * i4 + j] >> 16 : sb[4 * i4 + j]);
+                // the other two rows have chunk c where these have c ^ 2
+                const int off = i4 * Ck<D>::BLK + h * 256;
+                *reinterpret_cast<uint32_t *>(at[0][j ^ hh] + off) = mul_lo(a[0][j], two);
+                *reinterpret_cast<uint32_t *>(at[1][j ^ hh] + off) = mul_hi(a[1][j], two);
+            }
+        }
+    }
+}
+
+// Channel blocks of kv head kvh whose V is NaN at some key in [k0, k1): slow,
+// run only when the CTA met a NaN scale.
+template <int D>
+__device__ __noinline__ uint32_t nan_blocks(const Kv4Chunk &p, int kvh, int k0, int k1)
+{
+    using L = Layout<D>;
+    uint32_t m = 0;
+    for (int key = k0; key < k1; ++key) {
+        const int blk = p.table[key >> 4];
+        if (blk < 0 || blk >= p.num_blocks)
+            continue;
+        const uint8_t *page = p.pool + ((size_t)blk * p.n_kv + kvh) * L::BYTES;
+        for (int i = 0; i < L::NB; ++i)
+            if ((page[L::v_scale(key & 15, i)] & 0x7f) == 0x7f)
+                m |= 1u << i;
+    }
+    return m;
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant__ Kv4Chunk p)
+{
+    using C = Ck<D>;
+    using L = Layout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t *raw_full = (uint64_t *)(smem + C::BAR);
+    uint64_t *raw_empty = raw_full + RING;
+    uint64_t *k_full = raw_empty + RING, *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
+    uint64_t *s_full = v_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
+    uint64_t *q_full = pv_done + 2, *drain = q_full + 1;
+    uint32_t *tmem_slot = (uint32_t *)(drain + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    volatile int *bad_key = abort_flag + 1;   // lowest key met whose page lies outside the pool
+    volatile int *nan_seen = bad_key + 1;     // a NaN scale of V was met
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 2);  // its K and its V
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 4);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 6);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_full, 8);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *bad_key = 0x7fffffff;
+        *nan_seen = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12)
+        tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Segments sg(p, blockIdx.x);
+    pdl_wait();
+    pdl_trigger();
+
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !__all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, WAIT_NS))) {
+            *abort_flag = 1;
+            ok = false;
+        }
+        return ok;
+    };
+
+    if (warp < 8) {
+        // -------------------------------------------------------- softmax
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t sT = lanes + half * C::S_COL, oT = lanes + C::O0 + half * C::O_COL;
+        uint32_t n_s = 0, n_pv = 0;  // tiles whose S and whose O this half has waited for or may
+        for (; sg.more(); sg.next(p)) {
+            const bool mine = half < sg.halves(p);
+            const long long col0 = (long long)sg.qt * KC_ROWS + half * 128;
+            const long long col = min(col0 + r, (long long)p.cols - 1);
+            const bool valid = mine && col0 + r < p.cols;
+            const int row = (int)(col / p.group), head = sg.kvh * p.group + (int)(col - (long long)row * p.group);
+            const int seen = p.offset + row + 1;
+            float sc = 0.f;
+            if (mine) {
+                // Q row, scaled by a power of two into [1, 4), as f16
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * p.q_stride + (size_t)head * D);
+                uint4 u[D / 8];
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    u[i] = __ldg(src + i);
+                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
+                        a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                const int e = query_exponent(a);
+                const float down = pow2(-e);
+                sc = fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e), 1e-38f);  // never 0: a masked score stays -inf
+                uint8_t *q = smem + C::Q + half * C::TILE;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
+                        o[j] = valid ? pack_h2(f.x * down, f.y * down) : 0u;
+                    }
+                    *reinterpret_cast<uint4 *>(q + (i >> 3) * C::BLK + swz(r, i & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_full);
+            if (!mine)
+                continue;
+            const int seen0 = p.offset + (int)(col0 / p.group) + 1;  // of the half's first column
+            float m = LOWEST, l = 0.f;
+            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt) {
+                if (!wait(&s_full[half], n_s & 1u))
+                    break;
+                ++n_s;
+                tc_fence_after();
+                const int lim = seen - kt * KC_KEYS;              // keys of the tile this row sees
+                const bool edge = seen0 < (kt + 1) * KC_KEYS;     // some row does not see them all
+                float mx = -INFINITY;
+                if (edge) {
+#pragma unroll 1
+                    for (int c = 0; c < KC_KEYS; c += 32) {
+                        float v[32];
+                        tmem_ld_x32(sT + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            mx = fmaxf(mx, c + j < lim ? v[j] : -INFINITY);
+                    }
+                } else {
+                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = 0; c < KC_KEYS; c += 64) {
+                        float v[2][32];
+                        tmem_ld_x32(sT + c, v[0]);
+                        tmem_ld_x32(sT + c + 32, v[1]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
+                    }
+                    mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                }
+                mx *= sc;
+                if (__any_sync(0xffffffffu, mx > m + RAISE)) {
+                    const float mn = fmaxf(m, mx), corr = ex2(m - mn);
+                    m = mn;
+                    l *= corr;
+                    if (kt > sg.kt0) {  // O holds the tiles before this one
+                        if (!wait(&pv_done[half], (n_pv - 1) & 1u))
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float v[32];
+                            tmem_ld_x32(oT + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] *= corr;
+                            tmem_st_x32(oT + c, v);
+                        }
+                    }
+                }
+                const uint64_t sc2 = pack_f2(sc, sc), m2 = pack_f2(-m, -m);
+                uint64_t sum2[2] = {0, 0};
+                // 32 keys at a time; the next 32 are on their way meanwhile
+                auto weights = [&](float (&v)[32], int c) {
+                    uint32_t ph[16];
+                    if (edge)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = c + j < lim ? v[j] : -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a, b;
+                        unpack_f2(fma_f2(pack_f2(v[2 * j], v[2 * j + 1]), sc2, m2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum2[j & 1] = add_f2(sum2[j & 1], pack_f2(a, b));
+                        ph[j] = pack_h2(a, b);
+                    }
+                    tmem_st_x16(sT + c / 2, ph);  // over columns of S that are read already
+                };
+                float va[32], vb[32];
+                tmem_ld_x32(sT, va);
+                tmem_ld_wait();
+#pragma unroll 1
+                for (int c = 0; c < KC_KEYS; c += 64) {
+                    tmem_ld_x32(sT + c + 32, vb);
+                    weights(va, c);
+                    tmem_ld_wait();
+                    if (c + 64 < KC_KEYS)
+                        tmem_ld_x32(sT + c + 64, va);
+                    weights(vb, c + 32);
+                    tmem_ld_wait();
+                }
+                {
+                    float a, b;
+                    unpack_f2(add_f2(sum2[0], sum2[1]), a, b);
+                    l += a + b;
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[half]);
+                ++n_pv;
+            }
+            // ---- the segment's result
+            if (ok && wait(&pv_done[half], (n_pv - 1) & 1u))
+                tc_fence_after();
+            uint32_t nans = 0;
+            if (*nan_seen)
+                nans = nan_blocks<D>(p, sg.kvh, sg.kt0 * KC_KEYS, min(seen, sg.kt1 * KC_KEYS));
+            __syncwarp();
+            if (!ok || *bad_key < seen) {  // one table serves every item, so the key found in any of them counts
+                l = __int_as_float(0x7fc00000);
+                m = 0.f;
+            }
+            const bool whole = sg.kt0 == 0 && sg.kt1 == sg.n_tiles;
+            const size_t part = ((size_t)blockIdx.x * 2 + (sg.first ? 0 : 1)) * KC_ROWS + half * 128 + r;
+            const float inv = p.vs / l;
+            bf16 *orow = p.out + row * p.out_stride + (size_t)head * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float v[32];
+                if (ok) {
+                    tmem_ld_x32(oT + c, v);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = 0.f;
+                }
+                if (nans) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (nans >> ((c + j) / 16) & 1u)
+                            v[j] = __int_as_float(0x7fc00000);
+                }
+                if (valid && whole) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = v[8 * k + j] * inv;
+                        *reinterpret_cast<uint4 *>(orow + c + 8 * k) = pack8_bf16(x);
+                    }
+                } else if (valid) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4 *>(p.part_o + part * D + c + 4 * k) =
+                            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                }
+                __syncwarp();
+            }
+            if (!whole && valid)
+                p.part_ml[part] = make_float2(m, l);
+            tc_fence_before();  // the next segment's MMAs overwrite O
+        }
+    } else if (warp < 12 || warp >= 14) {
+        // -------------------------------------------------------- dequant
+        // warps 8..11: K of pages w and w + 4, V of page w; warps 14, 15: V
+        // of two of the pages 4..7
+        const bool both = warp < 12;
+        const int w = both ? warp - 8 : warp - 14;
+        uint32_t it = 0;
+        for (; sg.more() && ok; sg.next(p)) {
+            const int keys = sg.keys(p);
+            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, ++it) {
+                const int st = it & 1;
+                uint8_t *K = smem + C::K + st * C::TILE, *V = smem + C::V + st * C::TILE;
+                if (both) {
+                    if (it >= 2 && !wait(&k_empty[st], ((it >> 1) - 1) & 1u))
+                        break;
+#pragma unroll 1
+                    for (int pg = w; pg < 8 && ok; pg += 4) {
+                        const uint32_t n = it * 8 + pg, slot = n % RING;  // pages since the start
+                        if (!wait(&raw_full[slot], (n / RING) & 1u))
+                            break;
+                        page_k<D>(smem + C::R + slot * C::RAW, K, pg * 16, lane);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&raw_empty[slot]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&k_full[st]);
+                }
+                if (it >= 2 && !wait(&v_empty[st], ((it >> 1) - 1) & 1u))
+                    break;
+#pragma unroll 1
+                for (int pg = both ? w : 4 + 2 * w; pg < (both ? w + 1 : 6 + 2 * w) && ok; ++pg) {
+                    const uint32_t n = it * 8 + pg, slot = n % RING;
+                    const uint8_t *raw = smem + C::R + slot * C::RAW;
+                    if (!wait(&raw_full[slot], (n / RING) & 1u))
+                        break;
+                    // NaN scales: four scale bytes a lane (half of the lanes for d = 64)
+                    const uint32_t sb = lane < D / 4 ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * lane) : 0u;
+                    if (__any_sync(0xffffffffu, (((sb & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
+                        if (kt * KC_KEYS + pg * 16 < keys)
+                            *nan_seen = 1;  // or a slot past the last key: the search will tell
+                        page_v<D>(raw, V, pg * 16, lane, true);
+                    } else {
+                        page_v<D>(raw, V, pg * 16, lane, false);
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&raw_empty[slot]);
+                }
+                __threadfence_block();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&v_full[st]);
+            }
+        }
+    } else if (warp == 12) {
+        // -------------------------------------------------------- MMA issue
+        const uint32_t id_s = idesc_f16(128, KC_KEYS, false), id_o = idesc_f16(128, D, true);
+        const uint32_t sQ = smem_u32(smem + C::Q), sK = smem_u32(smem + C::K), sV = smem_u32(smem + C::V);
+        uint32_t it = 0, n_p[2] = {0, 0};
+        int seg_i = 0;
+        auto issue_s = [&](int half, int st) {
+#pragma unroll
+            for (int cb = 0; cb < C::CB; ++cb)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16_elect(tmem + half * C::S_COL,
+                                   sdesc_kmajor_sw128(sQ + half * C::TILE + cb * C::BLK + k * 32),
+                                   sdesc_kmajor_sw128(sK + st * C::TILE + cb * C::BLK + k * 32), id_s,
+                                   (cb | k) ? 1u : 0u);
+            mma_commit_elect(&s_full[half]);
+        };
+        for (; sg.more() && ok; sg.next(p), ++seg_i) {
+            const int halves = sg.halves(p);
+            const int T = sg.kt1 - sg.kt0;
+            if (!wait(q_full, (uint32_t)seg_i & 1u) || !wait(&k_full[it & 1], (it >> 1) & 1u))
+                break;
+            tc_fence_after();
+            for (int h = 0; h < halves; ++h)
+                issue_s(h, it & 1);
+            mma_commit_elect(&k_empty[it & 1]);
+            for (int t = 0; t < T && ok; ++t, ++it) {
+                const int st = it & 1, nst = (it + 1) & 1;
+                for (int h = 0; h < halves; ++h) {
+                    if (!wait(&p_full[h], n_p[h] & 1u))
+                        break;
+                    ++n_p[h];
+                    if (h == 0 && !wait(&v_full[st], (it >> 1) & 1u))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < KC_KEYS / 16; ++k)
+                        mma_ts_elect(tmem + C::O0 + h * C::O_COL, tmem + h * C::S_COL + k * 8,
+                                     sdesc_mn(sV + st * C::TILE + k * 2048, C::BLK), id_o, (t | k) ? 1u : 0u);
+                    mma_commit_elect(&pv_done[h]);
+                    if (h == halves - 1)
+                        mma_commit_elect(&v_empty[st]);
+                    if (t + 1 < T) {
+                        if (h == 0 && !wait(&k_full[nst], ((it + 1) >> 1) & 1u))
+                            break;
+                        tc_fence_after();
+                        issue_s(h, nst);
+                        if (h == halves - 1)
+                            mma_commit_elect(&k_empty[nst]);
+                    }
+                }
+            }
+        }
+        if (!ok) {
+            mma_commit_elect(drain);
+            mbar_wait(drain, 0, nullptr, WAIT_NS / 4);
+        }
+    } else {
+        // -------------------------------------------------------- loader
+        uint32_t it = 0;
+        for (; sg.more() && ok; sg.next(p)) {
+            const int keys = sg.keys(p);
+            for (int kt = sg.kt0; kt < sg.kt1; ++kt, ++it) {
+                const int pg = kt * 8 + (lane & 7);
+                const uint32_t n = it * 8 + (lane & 7), slot = n % RING;
+                const bool need = lane < 8 && pg * 16 < keys;
+                const int blk = need ? __ldg(p.table + pg) : 0;
+                const bool in = need && blk >= 0 && blk < p.num_blocks;
+                if (need && !in)
+                    atomicMin((int *)bad_key, pg * 16);
+                bool got = true;
+                if (lane < 8 && n >= RING)
+                    got = mbar_sleep(&raw_empty[slot], (n / RING - 1) & 1u, abort_flag, WAIT_NS);
+                if (!__all_sync(0xffffffffu, got)) {
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                if (lane < 8) {
+                    if (in) {
+                        mbar_expect_tx(&raw_full[slot], C::RAW);
+                        bulk_load(smem + C::R + slot * C::RAW, p.pool + ((size_t)blk * p.n_kv + sg.kvh) * C::RAW,
+                                  C::RAW, &raw_full[slot]);
+                    } else {
+                        mbar_arrive(&raw_full[slot]);  // past the keys or outside the pool: what the slot holds is masked
+                    }
+                }
+            }
+        }
+        // no copy may land after the CTA has ended: the last RING pages
+        const uint32_t pages = it * 8;
+        for (uint32_t n = pages > RING ? pages - RING : 0; n < pages; ++n)
+            mbar_wait(&raw_full[n % RING], (n / RING) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the partials of an item, 32 columns a block, in the order of its
+// keys.  Block x belongs to the item that CTA x + 1 begins inside, unless CTA
+// x did so too (then an earlier block has it).
+template <int D>
+__global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ Kv4Chunk p)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int ca = blockIdx.x;
+    const KcStart a = p.start[ca], item = p.start[ca + 1];
+    const bool same = a.kvh == item.kvh && a.qt == item.qt;
+    pdl_wait();
+    pdl_trigger();
+    if (item.kt0 == 0 || (same && a.kt0 > 0))
+        return;
+    int cb = ca + 1;  // the last CTA with a part of the item
+    while (cb + 1 < p.ctas && p.start[cb + 1].kvh == item.kvh && p.start[cb + 1].qt == item.qt)
+        ++cb;
+    // of the CTAs only ca can have come to the item from another one
+    const int first = 2 * ca + (same ? 0 : 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = blockIdx.y * 32 + warp * 4 + k;
+        const long long col = (long long)item.qt * KC_ROWS + r;
+        if (col >= p.cols)
+            return;
+        const float2 *ml = p.part_ml + r;
+        float M = LOWEST;
+        for (int c = ca + lane; c <= cb; c += 32)
+            M = fmaxf(M, ml[(size_t)(c == ca ? first : 2 * c) * KC_ROWS].x);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        float l = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = 0.f;
+#pragma unroll 4
+        for (int c = ca; c <= cb; ++c) {
+            const size_t part = (size_t)(c == ca ? first : 2 * c) * KC_ROWS;
+            const float2 x = ml[part];
+            const float f = ex2(x.x - M);
+            l += x.y * f;
+            const float *po = p.part_o + (part + r) * D + lane * E;
+            float v[E];
+            if constexpr (E == 4)
+                *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(po);
+            else
+                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                o[e] += v[e] * f;
+        }
+        const int row = (int)(col / p.group), head = item.kvh * p.group + (int)(col - (long long)row * p.group);
+        bf16 *orow = p.out + row * p.out_stride + (size_t)head * D + lane * E;
+        const float inv = p.vs / l;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(orow + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    }
+}
+
+template <int D>
+cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
+{
+    static std::once_flag once;
+    static cudaError_t set;
+    std::call_once(once, [] {
+        set = cudaFuncSetAttribute(k_kv4_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ck<D>::BYTES);
+    });
+    if (set != cudaSuccess)
+        return set;
+    cudaError_t e = launch_kernel(true, k_kv4_chunk<D>, dim3(p.ctas), dim3(THREADS), Ck<D>::BYTES, s, p);
+    if (e != cudaSuccess)
+        return e;
+    if (kv4_chunk_workspace_bytes(p, D) == 0)
+        return cudaSuccess;
+    return launch_kernel(true, k_kv4_chunk_join<D>, dim3(p.ctas - 1, KC_ROWS / 32), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len)
+{
+    p.cols = chunk_len * p.group;
+    p.n_qt = (p.cols + KC_ROWS - 1) / KC_ROWS;
+    long long head_units = 0;
+    for (int qt = 0; qt < p.n_qt; ++qt)
+        head_units += item_tiles(p, qt);
+    const long long units = head_units * p.n_kv;
+    p.ctas = (int)(units < KC_CTAS ? units : KC_CTAS);
+    if (units / p.ctas >= 0x7fffffff)
+        return false;
+    long long at = 0, item_at = 0;  // first unit of (kvh, qt)
+    int kvh = 0, qt = 0;
+    for (int c = 0; c < p.ctas; ++c) {
+        for (int n; item_at + (n = item_tiles(p, qt)) <= at; item_at += n)
+            if (++qt == p.n_qt) {
+                qt = 0;
+                ++kvh;
+            }
+        const long long next = units * (c + 1) / p.ctas;
+        p.start[c] = KcStart{kvh, qt, (int)(at - item_at), (int)(next - at)};
+        at = next;
+    }
+    return true;
+}
+
+long long kv4_chunk_workspace_bytes(const Kv4Chunk &p, int d)
+{
+    bool parts = false;
+    for (int c = 1; c < p.ctas; ++c)
+        parts |= p.start[c].kt0 > 0;
+    return parts ? 2ll * p.ctas * KC_ROWS * (8 + 4ll * d) : 0;
+}
+
+cudaError_t launch_kv4_chunk(const Kv4Chunk &p, int head_dim, cudaStream_t s)
+{
+    return head_dim == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
+}
+
+}  // namespace hb

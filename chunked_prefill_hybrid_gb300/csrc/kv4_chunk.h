@@ -1,0 +1,44 @@
+// kv4_chunk.h -- host interface of the tcgen05 chunk attention over the 4-bit
+// cache (kv4_chunk.cu).
+#pragma once
+
+#include "common.cuh"
+
+namespace hb {
+
+constexpr int KC_ROWS = 256;    // query columns (row x head of a kv head) of an item: two MMA tiles of 128
+constexpr int KC_KEYS = 128;    // keys of a tile
+constexpr int KC_CTAS = 152;    // CTAs at most: one per SM
+
+// Where a CTA's work begins: key tile kt0 of item (kvh, qt), and how many
+// units it has.
+struct KcStart {
+    int kvh, qt, kt0, units;
+};
+
+struct Kv4Chunk {
+    const uint8_t *pool;
+    int num_blocks, n_kv, group, n_heads;
+    float ks, vs;
+    const bf16 *q;
+    long long q_stride;
+    const int *table;
+    int offset, cols;           // cols = chunk_len * group
+    bf16 *out;
+    long long out_stride;
+    // work: units are (item, key tile); item = (kv head, 256 columns), kv head
+    // major; CTA c takes the units of start[c], as many as any other CTA or one
+    // more
+    int n_qt, ctas;             // items of a kv head; CTAs
+    KcStart start[KC_CTAS];
+    float *part_o;              // [2 ctas][256][D]: CTA c's segment that starts with it, and its last
+    float2 *part_ml;            // [2 ctas][256] (m in log2, l)
+};
+
+// Plan the work of a chunk (host): everything but the pointers.  False when a
+// CTA's units would not fit 32 bits.
+bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len);
+long long kv4_chunk_workspace_bytes(const Kv4Chunk &p, int head_dim);
+cudaError_t launch_kv4_chunk(const Kv4Chunk &p, int head_dim, cudaStream_t s);
+
+}  // namespace hb

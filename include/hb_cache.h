@@ -125,7 +125,8 @@ long long hb_kv4_decode_workspace(int n_decodes, int n_heads, int n_kv_heads, in
  *                too small).  A block id outside the pool makes the rows that
  *                attend to it NaN (and may make other rows of the chunk NaN)
  * Workspace, errors and rounding as for hb_kv4_decode; chunk_offset +
- * chunk_len is at most 2^27.  chunk_len = 0 does nothing. */
+ * chunk_len is at most 2^27, chunk_len times the heads of a kv head at most
+ * 2^24 (HB_ERANGE).  chunk_len = 0 does nothing. */
 int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_stride, const int32_t *block_table, int n_blocks,
                  int chunk_offset, int chunk_len, int n_heads, void *out, long long out_stride, void *workspace,
                  long long workspace_bytes, void *cuda_stream);
