@@ -8,18 +8,18 @@
 // contiguous range of (item, key tile) units, as many to every CTA; an item
 // that several CTAs share leaves fp32 partials, which a second kernel joins.
 //
-//   warp 13      loader: one bulk copy per page (16 keys) into a ring
-//   warps 8..11, codes and scales -> f16 K and V tiles (128-byte swizzle);
-//     14, 15     code x scale is exact in f16
-//   warp 12      issues the MMAs: S of both 128-row halves, and O += P V with
-//                P read from tensor memory
-//   warps 0..7   softmax, one thread per query: S from tensor memory, P back
-//                into it as f16; O is rescaled only when a maximum rises by
-//                more than 2^8
+//   warps 0..7    softmax, one thread per query: S from tensor memory, P back
+//                 into it as f16; O is rescaled only when a maximum rises by
+//                 more than 2^8
+//   warps 8..15   codes and scales of one page each -> f16 rows of the K and V
+//                 tiles (128-byte swizzle); code x scale is exact in f16
+//   warps 16, 17  issue the MMAs of the two 128-row halves: S, and O += P V
+//                 with P read from tensor memory
+//   warp 18       loader: one bulk copy per page (16 keys) into a ring
 //
-// While one half's softmax runs, the tensor pipe works on the other's
-// products.  256 rows share each dequantised tile: its conversion takes the
-// four warps about 800 shared-memory cycles against 2048 of MMA.
+// S comes in sub-tiles of 64 keys, two for each half, each in tensor memory of
+// its own: while one is in the softmax the tensor pipe fills the other.  The
+// softmax warps take the registers that the others do not need.
 //
 // Every wait is bounded; when one runs out, the CTA writes NaN for the rows
 // it has left, drains and returns.
@@ -38,7 +38,8 @@ namespace {
 using namespace kv4;
 using namespace tc;
 
-constexpr int THREADS = 16 * 32;
+constexpr int THREADS = 20 * 32;
+constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 64;  // 256 and 384 threads: 61440 registers, 96 for each thread at launch
 constexpr int RING = 12;                 // pages in flight
 constexpr float RAISE = 8.f;             // P <= 2^8
 constexpr uint64_t WAIT_NS = 2000000000ull;
@@ -109,17 +110,9 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&r)[32])
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float (&r)[32])
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, float (&r)[16])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
-        "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
-        "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
-        : "memory");
+    tmem_ld_32x32b_x16(taddr, reinterpret_cast<uint32_t(&)[16]>(r));
 }
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
@@ -225,27 +218,28 @@ struct Segments {
 // ---------------------------------------------------------------- dequant
 
 // K of one page into rows row0.. (a multiple of 16) of a tile.  Lane 4 g + t:
-// tokens g and g + 8, channels 4t..4t+3 of every block.  The four chunks that
-// a lane writes in a row lie at four lane constants; everything else is an
-// immediate.
+// tokens tok and tok + 8, channels 4t..4t+3 of every block.  The four chunks
+// that a lane writes in a row lie at four lane constants; everything else is
+// an immediate.  A half-warp's 8-byte stores go to four rows whose swizzles
+// differ (tokens 0, 2, 4, 6 or 1, 3, 5, 7): no bank conflict.
 template <int D>
 __device__ __forceinline__ void page_k(const uint8_t *raw, uint8_t *tile, int row0, int lane)
 {
     using L = Layout<D>;
     constexpr int KW = L::NB / 2;
-    const int g = lane >> 2, t = lane & 3;
-    uint8_t *base = tile + row0 * 128 + g * 128 + 8 * (t & 1);
+    const int g = lane >> 2, t = lane & 3, tok = ((g & 3) << 1) | (g >> 2);
+    uint8_t *base = tile + row0 * 128 + tok * 128 + 8 * (t & 1);
     uint8_t *at[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        at[k] = base + (((2 * k + (t >> 1)) ^ g) << 4);
+        at[k] = base + (((2 * k + (t >> 1)) ^ tok) << 4);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         uint32_t w[KW], sb[L::NB / 4];
-        load_words<KW>(raw + L::k_code(g + 8 * r, t, 0), w);
+        load_words<KW>(raw + L::k_code(tok + 8 * r, t, 0), w);
 #pragma unroll
         for (int i = 0; i < L::NB / 4; ++i)
-            sb[i] = *reinterpret_cast<const uint32_t *>(raw + L::k_scale(g + 8 * r, 4 * i));
+            sb[i] = *reinterpret_cast<const uint32_t *>(raw + L::k_scale(tok + 8 * r, 4 * i));
 #pragma unroll
         for (int i = 0; i < KW; ++i) {  // blocks 2i, 2i + 1
             uint32_t a[4];
@@ -312,6 +306,13 @@ __device__ __forceinline__ void page_v(const uint8_t *raw, uint8_t *tile, int ro
     }
 }
 
+// The rare page with NaN scales, kept out of the way of the others' code.
+template <int D>
+__device__ __noinline__ void page_v_scrub(const uint8_t *raw, uint8_t *tile, int row0, int lane)
+{
+    page_v<D>(raw, tile, row0, lane, true);
+}
+
 // Channel blocks of kv head kvh whose V is NaN at some key in [k0, k1): slow,
 // run only when the CTA met a NaN scale.
 template <int D>
@@ -331,6 +332,16 @@ __device__ __noinline__ uint32_t nan_blocks(const Kv4Chunk &p, int kvh, int k0, 
     return m;
 }
 
+// The wait of a whole warp that its first look did not end (one copy of the
+// loop: the roles' code together has to stay in the instruction caches).
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (__all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, WAIT_NS)))
+        return true;
+    *abort_flag = 1;
+    return false;
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant__ Kv4Chunk p)
 {
@@ -341,9 +352,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     uint64_t *raw_full = (uint64_t *)(smem + C::BAR);
     uint64_t *raw_empty = raw_full + RING;
     uint64_t *k_full = raw_empty + RING, *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
-    uint64_t *s_full = v_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
-    uint64_t *q_full = pv_done + 2, *drain = q_full + 1;
-    uint32_t *tmem_slot = (uint32_t *)(drain + 1);
+    uint64_t *s_full = v_empty + 2, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][sub-tile]
+    uint64_t *q_full = pv_done + 4, *drain = q_full + 1;                          // drain [half]
+    uint32_t *tmem_slot = (uint32_t *)(drain + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad_key = abort_flag + 1;   // lowest key met whose page lies outside the pool
     volatile int *nan_seen = bad_key + 1;     // a NaN scale of V was met
@@ -352,25 +363,27 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     if (threadIdx.x == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 2);  // its K and its V
+            mbar_init(&raw_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], 4);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 6);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&k_full[i], 8);
+            mbar_init(&k_empty[i], 2);
+            mbar_init(&v_full[i], 8);
+            mbar_init(&v_empty[i], 2);
+            mbar_init(&drain[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(q_full, 8);
-        mbar_init(drain, 1);
         *abort_flag = 0;
         *bad_key = 0x7fffffff;
         *nan_seen = 0;
         fence_mbar_init();
     }
-    if (warp == 12)
+    if (warp == 16)
         tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
@@ -382,57 +395,68 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, WAIT_NS))) {
-            *abort_flag = 1;
-            ok = false;
-        }
+        if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+            ok = ok && wait_long(bar, parity, abort_flag);
         return ok;
     };
 
     if (warp < 8) {
         // -------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t sT = lanes + half * C::S_COL, oT = lanes + C::O0 + half * C::O_COL;
-        uint32_t n_s = 0, n_pv = 0;  // tiles whose S and whose O this half has waited for or may
+        uint32_t n_t = 0;  // key tiles this half has been through
         for (; sg.more(); sg.next(p)) {
             const bool mine = half < sg.halves(p);
             const long long col0 = (long long)sg.qt * KC_ROWS + half * 128;
+            const int valid = (int)min(128ll, p.cols - col0);  // columns of this half (<= 0 unless mine)
             const long long col = min(col0 + r, (long long)p.cols - 1);
-            const bool valid = mine && col0 + r < p.cols;
             const int row = (int)(col / p.group), head = sg.kvh * p.group + (int)(col - (long long)row * p.group);
             const int seen = p.offset + row + 1;
+            uint8_t *q = smem + C::Q + half * C::TILE;
+            constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows a warp-wide access
+            const int lr = lane / LPR, lc = lane % LPR;
             float sc = 0.f;
             if (mine) {
-                // Q row, scaled by a power of two into [1, 4), as f16
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * p.q_stride + (size_t)head * D);
-                uint4 u[D / 8];
-                float a = 0.f;
+                // this warp's 32 rows of Q, each scaled by a power of two into [1, 4), as f16
+                const long long src = row * p.q_stride + (size_t)head * D;
+                int e = 0;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += 4 * RPI) {
+                    uint4 u[4];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    u[i] = __ldg(src + i);
-                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    for (int k = 0; k < 4; ++k)
+                        u[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                         p.q + __shfl_sync(0xffffffffu, src, i0 + k * RPI + lr)) + lc);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-                        a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                        float2 f[4];
+                        float a = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            f[j] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
+                            a = fmaxf(a, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+                        }
+#pragma unroll
+                        for (int x = 1; x < LPR; x *= 2)
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, x));
+                        const int er = query_exponent(a), i = i0 + k * RPI;
+                        const float down = pow2(-er);
+                        const bool have = (warp & 3) * 32 + i + lr < valid;
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            o[j] = have ? pack_h2(f[j].x * down, f[j].y * down) : 0u;
+                        *reinterpret_cast<uint4 *>(q + (lc >> 3) * C::BLK + swz((warp & 3) * 32 + i + lr, lc & 7)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                        const int mine_e = __shfl_sync(0xffffffffu, er, (lane % RPI) * LPR);  // of row i + lane % RPI
+                        if (lane / RPI == i / RPI)
+                            e = mine_e;
                     }
                 }
-                const int e = query_exponent(a);
-                const float down = pow2(-e);
                 sc = fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e), 1e-38f);  // never 0: a masked score stays -inf
-                uint8_t *q = smem + C::Q + half * C::TILE;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-                        o[j] = valid ? pack_h2(f.x * down, f.y * down) : 0u;
-                    }
-                    *reinterpret_cast<uint4 *>(q + (i >> 3) * C::BLK + swz(r, i & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             __syncwarp();
@@ -442,106 +466,79 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 continue;
             const int seen0 = p.offset + (int)(col0 / p.group) + 1;  // of the half's first column
             float m = LOWEST, l = 0.f;
-            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt) {
-                if (!wait(&s_full[half], n_s & 1u))
-                    break;
-                ++n_s;
-                tc_fence_after();
-                const int lim = seen - kt * KC_KEYS;              // keys of the tile this row sees
-                const bool edge = seen0 < (kt + 1) * KC_KEYS;     // some row does not see them all
-                float mx = -INFINITY;
-                if (edge) {
+            bool fresh = true;  // no O yet
+            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, ++n_t) {
 #pragma unroll 1
-                    for (int c = 0; c < KC_KEYS; c += 32) {
-                        float v[32];
-                        tmem_ld_x32(sT + c, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            mx = fmaxf(mx, c + j < lim ? v[j] : -INFINITY);
-                    }
-                } else {
-                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < KC_KEYS; c += 64) {
-                        float v[2][32];
-                        tmem_ld_x32(sT + c, v[0]);
-                        tmem_ld_x32(sT + c + 32, v[1]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
-                    }
-                    mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                }
-                mx *= sc;
-                if (__any_sync(0xffffffffu, mx > m + RAISE)) {
-                    const float mn = fmaxf(m, mx), corr = ex2(m - mn);
-                    m = mn;
-                    l *= corr;
-                    if (kt > sg.kt0) {  // O holds the tiles before this one
-                        if (!wait(&pv_done[half], (n_pv - 1) & 1u))
-                            break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float v[32];
-                            tmem_ld_x32(oT + c, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] *= corr;
-                            tmem_st_x32(oT + c, v);
-                        }
-                    }
-                }
-                const uint64_t sc2 = pack_f2(sc, sc), m2 = pack_f2(-m, -m);
-                uint64_t sum2[2] = {0, 0};
-                // 32 keys at a time; the next 32 are on their way meanwhile
-                auto weights = [&](float (&v)[32], int c) {
-                    uint32_t ph[16];
+                for (int s = 0; s < 2; ++s) {
+                    if (!wait(&s_full[2 * half + s], n_t & 1u))
+                        break;
+                    tc_fence_after();
+                    const int lim = seen - kt * KC_KEYS - s * 64;           // keys of the 64 this row sees
+                    const bool edge = seen0 < kt * KC_KEYS + s * 64 + 64;   // some row does not see them all
+                    float v[2][32];
+                    tmem_ld_x32(sT + s * 64, v[0]);
+                    tmem_ld_x32(sT + s * 64 + 32, v[1]);
+                    tmem_ld_wait();
                     if (edge)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = c + j < lim ? v[j] : -INFINITY;
+                        for (int j = 0; j < 32; ++j) {
+                            v[0][j] = j < lim ? v[0][j] : -INFINITY;
+                            v[1][j] = 32 + j < lim ? v[1][j] : -INFINITY;
+                        }
+                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float a, b;
-                        unpack_f2(fma_f2(pack_f2(v[2 * j], v[2 * j + 1]), sc2, m2), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        sum2[j & 1] = add_f2(sum2[j & 1], pack_f2(a, b));
-                        ph[j] = pack_h2(a, b);
-                    }
-                    tmem_st_x16(sT + c / 2, ph);  // over columns of S that are read already
-                };
-                float va[32], vb[32];
-                tmem_ld_x32(sT, va);
-                tmem_ld_wait();
+                    for (int j = 0; j < 32; ++j)
+                        x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
+                    const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sc;
+                    if (__any_sync(0xffffffffu, mx > m + RAISE)) {
+                        const float mn = fmaxf(m, mx), corr = ex2(m - mn);
+                        m = mn;
+                        l *= corr;
+                        if (!fresh) {  // O holds the products before this one: let the last of them end
+                            if (!wait(&pv_done[2 * half + (s ^ 1)], (s ? n_t : n_t - 1) & 1u))
+                                break;
+                            tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < KC_KEYS; c += 64) {
-                    tmem_ld_x32(sT + c + 32, vb);
-                    weights(va, c);
-                    tmem_ld_wait();
-                    if (c + 64 < KC_KEYS)
-                        tmem_ld_x32(sT + c + 64, va);
-                    weights(vb, c + 32);
-                    tmem_ld_wait();
-                }
-                {
+                            for (int c = 0; c < D; c += 16) {
+                                float y[16];
+                                tmem_ld_x16(oT + c, y);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    y[j] *= corr;
+                                tmem_st_x16(oT + c, reinterpret_cast<uint32_t(&)[16]>(y));
+                            }
+                        }
+                    }
+                    fresh = false;
+                    const uint64_t sc2 = pack_f2(sc, sc), m2 = pack_f2(-m, -m);
+                    uint64_t sum2[2] = {0, 0};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t ph[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float a, b;
+                            unpack_f2(fma_f2(pack_f2(v[k][2 * j], v[k][2 * j + 1]), sc2, m2), a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum2[j & 1] = add_f2(sum2[j & 1], pack_f2(a, b));
+                            ph[j] = pack_h2(a, b);
+                        }
+                        tmem_st_x16(sT + s * 64 + k * 16, ph);  // over S, which is read already
+                    }
                     float a, b;
                     unpack_f2(add_f2(sum2[0], sum2[1]), a, b);
                     l += a + b;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&p_full[2 * half + s]);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&p_full[half]);
-                ++n_pv;
             }
             // ---- the segment's result
-            if (ok && wait(&pv_done[half], (n_pv - 1) & 1u))
+            if (ok && wait(&pv_done[2 * half + 1], (n_t - 1) & 1u))
                 tc_fence_after();
             uint32_t nans = 0;
             if (*nan_seen)
@@ -552,202 +549,207 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 m = 0.f;
             }
             const bool whole = sg.kt0 == 0 && sg.kt1 == sg.n_tiles;
-            const size_t part = ((size_t)blockIdx.x * 2 + (sg.first ? 0 : 1)) * KC_ROWS + half * 128 + r;
+            const size_t part = (size_t)blockIdx.x * 2 + (sg.first ? 0 : 1);
             const float inv = p.vs / l;
-            bf16 *orow = p.out + row * p.out_stride + (size_t)head * D;
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float v[32];
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                float v[16];
                 if (ok) {
-                    tmem_ld_x32(oT + c, v);
+                    tmem_ld_x16(oT + c, v);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 16; ++j)
                         v[j] = 0.f;
                 }
-                if (nans) {
+                if (nans >> (c / 16) & 1u)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (nans >> ((c + j) / 16) & 1u)
-                            v[j] = __int_as_float(0x7fc00000);
-                }
-                if (valid && whole) {
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __int_as_float(0x7fc00000);
+                if (whole) {
+                    // through the half's Q tile, which no MMA reads any more
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         float x[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             x[j] = v[8 * k + j] * inv;
-                        *reinterpret_cast<uint4 *>(orow + c + 8 * k) = pack8_bf16(x);
+                        const int ch = c / 8 + k;
+                        *reinterpret_cast<uint4 *>(q + (ch >> 3) * C::BLK + swz(r, ch & 7)) = pack8_bf16(x);
                     }
-                } else if (valid) {
+                } else if (r < valid) {
+                    float4 *po = reinterpret_cast<float4 *>(p.part_o) + (part * (D / 4) + c / 4) * KC_ROWS + half * 128 + r;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4 *>(p.part_o + part * D + c + 4 * k) =
-                            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k)
+                        po[k * KC_ROWS] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
                 __syncwarp();
             }
-            if (!whole && valid)
-                p.part_ml[part] = make_float2(m, l);
+            if (whole) {
+                const long long dst = row * p.out_stride + (size_t)head * D;
+#pragma unroll 4
+                for (int i = 0; i < 32; i += RPI) {
+                    const long long at = __shfl_sync(0xffffffffu, dst, i + lr);
+                    const int rr = (warp & 3) * 32 + i + lr;
+                    if (rr < valid)
+                        reinterpret_cast<uint4 *>(p.out + at)[lc] =
+                            *reinterpret_cast<const uint4 *>(q + (lc >> 3) * C::BLK + swz(rr, lc & 7));
+                }
+                __syncwarp();  // the next segment's Q goes there
+            } else if (r < valid) {
+                p.part_ml[part * KC_ROWS + half * 128 + r] = make_float2(m, l);
+            }
             tc_fence_before();  // the next segment's MMAs overwrite O
         }
-    } else if (warp < 12 || warp >= 14) {
+    } else if (warp < 16) {
         // -------------------------------------------------------- dequant
-        // warps 8..11: K of pages w and w + 4, V of page w; warps 14, 15: V
-        // of two of the pages 4..7
-        const bool both = warp < 12;
-        const int w = both ? warp - 8 : warp - 14;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        const int pg = warp - 8;  // page of every tile
         uint32_t it = 0;
         for (; sg.more() && ok; sg.next(p)) {
             const int keys = sg.keys(p);
             for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, ++it) {
                 const int st = it & 1;
-                uint8_t *K = smem + C::K + st * C::TILE, *V = smem + C::V + st * C::TILE;
-                if (both) {
-                    if (it >= 2 && !wait(&k_empty[st], ((it >> 1) - 1) & 1u))
-                        break;
-#pragma unroll 1
-                    for (int pg = w; pg < 8 && ok; pg += 4) {
-                        const uint32_t n = it * 8 + pg, slot = n % RING;  // pages since the start
-                        if (!wait(&raw_full[slot], (n / RING) & 1u))
-                            break;
-                        page_k<D>(smem + C::R + slot * C::RAW, K, pg * 16, lane);
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&raw_empty[slot]);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&k_full[st]);
-                }
-                if (it >= 2 && !wait(&v_empty[st], ((it >> 1) - 1) & 1u))
+                const uint32_t n = it * 8 + pg, slot = n % RING;  // pages since the start
+                const uint8_t *raw = smem + C::R + slot * C::RAW;
+                if ((it >= 2 && !wait(&k_empty[st], ((it >> 1) - 1) & 1u)) || !wait(&raw_full[slot], (n / RING) & 1u))
                     break;
-#pragma unroll 1
-                for (int pg = both ? w : 4 + 2 * w; pg < (both ? w + 1 : 6 + 2 * w) && ok; ++pg) {
-                    const uint32_t n = it * 8 + pg, slot = n % RING;
-                    const uint8_t *raw = smem + C::R + slot * C::RAW;
-                    if (!wait(&raw_full[slot], (n / RING) & 1u))
-                        break;
-                    // NaN scales: four scale bytes a lane (half of the lanes for d = 64)
-                    const uint32_t sb = lane < D / 4 ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * lane) : 0u;
-                    if (__any_sync(0xffffffffu, (((sb & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
-                        if (kt * KC_KEYS + pg * 16 < keys)
-                            *nan_seen = 1;  // or a slot past the last key: the search will tell
-                        page_v<D>(raw, V, pg * 16, lane, true);
-                    } else {
-                        page_v<D>(raw, V, pg * 16, lane, false);
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&raw_empty[slot]);
-                }
-                __threadfence_block();
+                page_k<D>(raw, smem + C::K + st * C::TILE, pg * 16, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
+                    mbar_arrive(&k_full[st]);
+                if (it >= 2 && !wait(&v_empty[st], ((it >> 1) - 1) & 1u))
+                    break;
+                // NaN scales: four scale bytes a lane (half of the lanes for d = 64)
+                const uint32_t sb = lane < D / 4 ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * lane) : 0u;
+                uint8_t *V = smem + C::V + st * C::TILE;
+                if (__any_sync(0xffffffffu, (((sb & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
+                    if (kt * KC_KEYS + pg * 16 < keys)
+                        *nan_seen = 1;  // or a slot past the last key: the search will tell
+                    page_v_scrub<D>(raw, V, pg * 16, lane);
+                    __threadfence_block();
+                } else {
+                    page_v<D>(raw, V, pg * 16, lane, false);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&raw_empty[slot]);
                     mbar_arrive(&v_full[st]);
-            }
-        }
-    } else if (warp == 12) {
-        // -------------------------------------------------------- MMA issue
-        const uint32_t id_s = idesc_f16(128, KC_KEYS, false), id_o = idesc_f16(128, D, true);
-        const uint32_t sQ = smem_u32(smem + C::Q), sK = smem_u32(smem + C::K), sV = smem_u32(smem + C::V);
-        uint32_t it = 0, n_p[2] = {0, 0};
-        int seg_i = 0;
-        auto issue_s = [&](int half, int st) {
-#pragma unroll
-            for (int cb = 0; cb < C::CB; ++cb)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16_elect(tmem + half * C::S_COL,
-                                   sdesc_kmajor_sw128(sQ + half * C::TILE + cb * C::BLK + k * 32),
-                                   sdesc_kmajor_sw128(sK + st * C::TILE + cb * C::BLK + k * 32), id_s,
-                                   (cb | k) ? 1u : 0u);
-            mma_commit_elect(&s_full[half]);
-        };
-        for (; sg.more() && ok; sg.next(p), ++seg_i) {
-            const int halves = sg.halves(p);
-            const int T = sg.kt1 - sg.kt0;
-            if (!wait(q_full, (uint32_t)seg_i & 1u) || !wait(&k_full[it & 1], (it >> 1) & 1u))
-                break;
-            tc_fence_after();
-            for (int h = 0; h < halves; ++h)
-                issue_s(h, it & 1);
-            mma_commit_elect(&k_empty[it & 1]);
-            for (int t = 0; t < T && ok; ++t, ++it) {
-                const int st = it & 1, nst = (it + 1) & 1;
-                for (int h = 0; h < halves; ++h) {
-                    if (!wait(&p_full[h], n_p[h] & 1u))
-                        break;
-                    ++n_p[h];
-                    if (h == 0 && !wait(&v_full[st], (it >> 1) & 1u))
-                        break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < KC_KEYS / 16; ++k)
-                        mma_ts_elect(tmem + C::O0 + h * C::O_COL, tmem + h * C::S_COL + k * 8,
-                                     sdesc_mn(sV + st * C::TILE + k * 2048, C::BLK), id_o, (t | k) ? 1u : 0u);
-                    mma_commit_elect(&pv_done[h]);
-                    if (h == halves - 1)
-                        mma_commit_elect(&v_empty[st]);
-                    if (t + 1 < T) {
-                        if (h == 0 && !wait(&k_full[nst], ((it + 1) >> 1) & 1u))
-                            break;
-                        tc_fence_after();
-                        issue_s(h, nst);
-                        if (h == halves - 1)
-                            mma_commit_elect(&k_empty[nst]);
-                    }
                 }
             }
-        }
-        if (!ok) {
-            mma_commit_elect(drain);
-            mbar_wait(drain, 0, nullptr, WAIT_NS / 4);
         }
     } else {
-        // -------------------------------------------------------- loader
-        uint32_t it = 0;
-        for (; sg.more() && ok; sg.next(p)) {
-            const int keys = sg.keys(p);
-            for (int kt = sg.kt0; kt < sg.kt1; ++kt, ++it) {
-                const int pg = kt * 8 + (lane & 7);
-                const uint32_t n = it * 8 + (lane & 7), slot = n % RING;
-                const bool need = lane < 8 && pg * 16 < keys;
-                const int blk = need ? __ldg(p.table + pg) : 0;
-                const bool in = need && blk >= 0 && blk < p.num_blocks;
-                if (need && !in)
-                    atomicMin((int *)bad_key, pg * 16);
-                bool got = true;
-                if (lane < 8 && n >= RING)
-                    got = mbar_sleep(&raw_empty[slot], (n / RING - 1) & 1u, abort_flag, WAIT_NS);
-                if (!__all_sync(0xffffffffu, got)) {
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        if (warp < 18) {
+            // ---------------------------------------------------- MMA issue
+            const int h = warp - 16;
+            const uint32_t id_s = idesc_f16(128, 64, false), id_o = idesc_f16(128, D, true);
+            const uint32_t sQ = smem_u32(smem + C::Q) + h * C::TILE;
+            const uint32_t sK = smem_u32(smem + C::K), sV = smem_u32(smem + C::V);
+            const uint32_t S = tmem + h * C::S_COL, O = tmem + C::O0 + h * C::O_COL;
+            uint32_t it = 0, n_p = 0;
+            int seg_i = 0;
+            auto issue_s = [&](int sub, int st) {
+                const uint32_t b = sK + st * C::TILE + sub * 8192;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_bf16_elect(S + sub * 64, sdesc_kmajor_sw128(sQ + (k >> 2) * C::BLK + (k & 3) * 32),
+                                   sdesc_kmajor_sw128(b + (k >> 2) * C::BLK + (k & 3) * 32), id_s, k ? 1u : 0u);
+                mma_commit_elect(&s_full[2 * h + sub]);
+            };
+            for (; sg.more() && ok; sg.next(p), ++seg_i) {
+                const int T = sg.kt1 - sg.kt0;
+                if (h >= sg.halves(p)) {  // no rows: the stages are free as soon as they are filled
+                    for (int t = 0; t < T && ok; ++t, ++it) {
+                        if (!wait(&k_full[it & 1], (it >> 1) & 1u))
+                            break;
+                        if (lane == 0)
+                            mbar_arrive(&k_empty[it & 1]);
+                        if (!wait(&v_full[it & 1], (it >> 1) & 1u))
+                            break;
+                        if (lane == 0)
+                            mbar_arrive(&v_empty[it & 1]);
+                    }
+                    continue;
                 }
-                if (lane < 8) {
-                    if (in) {
-                        mbar_expect_tx(&raw_full[slot], C::RAW);
-                        bulk_load(smem + C::R + slot * C::RAW, p.pool + ((size_t)blk * p.n_kv + sg.kvh) * C::RAW,
-                                  C::RAW, &raw_full[slot]);
-                    } else {
-                        mbar_arrive(&raw_full[slot]);  // past the keys or outside the pool: what the slot holds is masked
+                if (!wait(q_full, (uint32_t)seg_i & 1u) || !wait(&k_full[it & 1], (it >> 1) & 1u))
+                    break;
+                tc_fence_after();
+                issue_s(0, it & 1);
+                issue_s(1, it & 1);
+                mma_commit_elect(&k_empty[it & 1]);
+                for (int t = 0; t < T && ok; ++t, ++it) {
+                    const int st = it & 1, nst = (it + 1) & 1;
+#pragma unroll 1
+                    for (int s = 0; s < 2; ++s) {
+                        if (!wait(&p_full[2 * h + s], n_p & 1u) || (s == 0 && !wait(&v_full[st], (it >> 1) & 1u)))
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts_elect(O, S + s * 64 + k * 8, sdesc_mn(sV + st * C::TILE + s * 8192 + k * 2048, C::BLK),
+                                         id_o, t | s | k);
+                        mma_commit_elect(&pv_done[2 * h + s]);
+                        if (t + 1 < T) {
+                            if (s == 0 && !wait(&k_full[nst], ((it + 1) >> 1) & 1u))
+                                break;
+                            tc_fence_after();
+                            issue_s(s, nst);
+                        }
+                    }
+                    ++n_p;
+                    mma_commit_elect(&v_empty[st]);
+                    if (t + 1 < T)
+                        mma_commit_elect(&k_empty[nst]);
+                }
+            }
+            if (!ok) {
+                mma_commit_elect(&drain[h]);
+                mbar_wait(&drain[h], 0, nullptr, WAIT_NS / 4);
+            }
+        } else if (warp == 18) {
+            // ---------------------------------------------------- loader
+            uint32_t it = 0;
+            for (; sg.more() && ok; sg.next(p)) {
+                const int keys = sg.keys(p);
+                for (int kt = sg.kt0; kt < sg.kt1; ++kt, ++it) {
+                    const int pg = kt * 8 + (lane & 7);
+                    const uint32_t n = it * 8 + (lane & 7), slot = n % RING;
+                    const bool need = lane < 8 && pg * 16 < keys;
+                    const int blk = need ? __ldg(p.table + pg) : 0;
+                    const bool in = need && blk >= 0 && blk < p.num_blocks;
+                    if (need && !in)
+                        atomicMin((int *)bad_key, pg * 16);
+                    bool got = true;
+                    if (lane < 8 && n >= RING)
+                        got = mbar_sleep(&raw_empty[slot], (n / RING - 1) & 1u, abort_flag, WAIT_NS);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (lane < 8) {
+                        if (in) {
+                            mbar_expect_tx(&raw_full[slot], C::RAW);
+                            bulk_load(smem + C::R + slot * C::RAW, p.pool + ((size_t)blk * p.n_kv + sg.kvh) * C::RAW,
+                                      C::RAW, &raw_full[slot]);
+                        } else {
+                            mbar_arrive(&raw_full[slot]);  // past the keys or outside the pool: what the slot holds is masked
+                        }
                     }
                 }
             }
+            // no copy may land after the CTA has ended: the last RING pages
+            const uint32_t pages = it * 8;
+            for (uint32_t n = pages > RING ? pages - RING : 0; n < pages; ++n)
+                mbar_wait(&raw_full[n % RING], (n / RING) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
         }
-        // no copy may land after the CTA has ended: the last RING pages
-        const uint32_t pages = it * 8;
-        for (uint32_t n = pages > RING ? pages - RING : 0; n < pages; ++n)
-            mbar_wait(&raw_full[n % RING], (n / RING) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -759,7 +761,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 template <int D>
 __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ Kv4Chunk p)
 {
-    constexpr int E = D / 32;
+    constexpr int G = D / 32;  // groups of four channels a warp takes
+    __shared__ __align__(16) bf16 s_o[32][D + 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ca = blockIdx.x;
     const KcStart a = p.start[ca], item = p.start[ca + 1];
@@ -773,45 +776,50 @@ __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ 
         ++cb;
     // of the CTAs only ca can have come to the item from another one
     const int first = 2 * ca + (same ? 0 : 1);
+    const int r = blockIdx.y * 32 + lane;  // this lane's column of the item
+    const int valid = (int)min((long long)KC_ROWS, p.cols - (long long)item.qt * KC_ROWS);
+    if (blockIdx.y * 32 >= valid)
+        return;
+    const float2 *ml = p.part_ml + r;
+    const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + (size_t)warp * G * KC_ROWS + r;
+    float M = LOWEST, l = 0.f;
+    float4 o[G];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int r = blockIdx.y * 32 + warp * 4 + k;
-        const long long col = (long long)item.qt * KC_ROWS + r;
-        if (col >= p.cols)
-            return;
-        const float2 *ml = p.part_ml + r;
-        float M = LOWEST;
-        for (int c = ca + lane; c <= cb; c += 32)
+    for (int k = 0; k < G; ++k)
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < valid) {
+#pragma unroll 4
+        for (int c = ca; c <= cb; ++c)
             M = fmaxf(M, ml[(size_t)(c == ca ? first : 2 * c) * KC_ROWS].x);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        float l = 0.f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = 0.f;
 #pragma unroll 4
         for (int c = ca; c <= cb; ++c) {
-            const size_t part = (size_t)(c == ca ? first : 2 * c) * KC_ROWS;
-            const float2 x = ml[part];
+            const size_t part = c == ca ? first : 2 * c;
+            const float2 x = ml[part * KC_ROWS];
             const float f = ex2(x.x - M);
             l += x.y * f;
-            const float *po = p.part_o + (part + r) * D + lane * E;
-            float v[E];
-            if constexpr (E == 4)
-                *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(po);
-            else
-                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                o[e] += v[e] * f;
+            for (int k = 0; k < G; ++k) {
+                const float4 v = po[(part * (D / 4) + k) * KC_ROWS];
+                o[k].x += v.x * f, o[k].y += v.y * f, o[k].z += v.z * f, o[k].w += v.w * f;
+            }
         }
-        const int row = (int)(col / p.group), head = item.kvh * p.group + (int)(col - (long long)row * p.group);
-        bf16 *orow = p.out + row * p.out_stride + (size_t)head * D + lane * E;
-        const float inv = p.vs / l;
+    }
+    const float inv = p.vs / l;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<__nv_bfloat162 *>(orow + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    for (int k = 0; k < G; ++k) {
+        __nv_bfloat162 *s = reinterpret_cast<__nv_bfloat162 *>(&s_o[lane][(warp * G + k) * 4]);
+        s[0] = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
+        s[1] = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
+        const int rr = i / (D / 8), ch = i % (D / 8);
+        if (blockIdx.y * 32 + rr >= valid)
+            break;
+        const int col = item.qt * KC_ROWS + blockIdx.y * 32 + rr;
+        const int row = col / p.group, head = item.kvh * p.group + col - row * p.group;
+        reinterpret_cast<uint4 *>(p.out + row * p.out_stride + (size_t)head * D)[ch] =
+            *reinterpret_cast<const uint4 *>(&s_o[rr][ch * 8]);
     }
 }
 

@@ -31,7 +31,7 @@ struct Kv4Chunk {
     // more
     int n_qt, ctas;             // items of a kv head; CTAs
     KcStart start[KC_CTAS];
-    float *part_o;              // [2 ctas][256][D]: CTA c's segment that starts with it, and its last
+    float *part_o;              // [2 ctas][D / 4][256][4]: CTA c's segment that starts with it, and its last
     float2 *part_ml;            // [2 ctas][256] (m in log2, l)
 };
 
