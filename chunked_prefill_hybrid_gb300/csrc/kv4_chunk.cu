@@ -40,7 +40,8 @@ using namespace tc;
 
 constexpr int THREADS = 20 * 32;
 constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 64;  // 256 and 384 threads: 61440 registers, 96 for each thread at launch
-constexpr int RING = 12;                 // pages in flight
+constexpr int RING = 24;                 // pages in flight
+constexpr int STAGES = 3;                // sub-tiles of 64 keys of K, and of V, in f16
 constexpr float RAISE = 8.f;             // P <= 2^8
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
@@ -49,10 +50,12 @@ struct Ck {
     static constexpr int CB = D / 64;                 // column blocks of 64 channels
     static constexpr int BLK = 128 * 128;             // one column block of a 128-row tile
     static constexpr int TILE = CB * BLK;
+    static constexpr int SBLK = 64 * 128;             // the same of a 64-key sub-tile
+    static constexpr int SUB = CB * SBLK;
     static constexpr int RAW = Layout<D>::BYTES;
-    static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, R = 6 * TILE;
+    static constexpr int Q = 0, K = 2 * TILE, V = K + STAGES * SUB, R = V + STAGES * SUB;
     static constexpr int BAR = R + RING * RAW;
-    static constexpr int BYTES = BAR + 512 + 1024;    // barriers, alignment
+    static constexpr int BYTES = BAR + 1024 + 1024;   // barriers, alignment
     static constexpr uint32_t S_COL = 128, O0 = 256, O_COL = D;
 };
 
@@ -245,7 +248,7 @@ __device__ __forceinline__ void page_k(const uint8_t *raw, uint8_t *tile, int ro
             uint32_t a[4];
             from_e2m1x8(w[i], a);
             const uint32_t two = from_e4m3x2(sb[i / 2] >> (16 * (i & 1)));
-            const int off = (i / 2) * Ck<D>::BLK + r * 1024;
+            const int off = (i / 2) * Ck<D>::SBLK + r * 1024;
             *reinterpret_cast<uint2 *>(at[2 * (i & 1)] + off) = make_uint2(mul_lo(a[0], two), mul_lo(a[1], two));
             *reinterpret_cast<uint2 *>(at[2 * (i & 1) + 1] + off) = make_uint2(mul_hi(a[2], two), mul_hi(a[3], two));
         }
@@ -298,7 +301,7 @@ __device__ __forceinline__ void page_v(const uint8_t *raw, uint8_t *tile, int ro
             for (int j = 0; j < 4; ++j) {
                 const uint32_t two = from_e4m3x2(hh ? sb[4 * i4 + j] >> 16 : sb[4 * i4 + j]);
                 // the other two rows have chunk c where these have c ^ 2
-                const int off = i4 * Ck<D>::BLK + h * 256;
+                const int off = i4 * Ck<D>::SBLK + h * 256;
                 *reinterpret_cast<uint32_t *>(at[0][j ^ hh] + off) = mul_lo(a[0][j], two);
                 *reinterpret_cast<uint32_t *>(at[1][j ^ hh] + off) = mul_hi(a[1][j], two);
             }
@@ -351,8 +354,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *raw_full = (uint64_t *)(smem + C::BAR);
     uint64_t *raw_empty = raw_full + RING;
-    uint64_t *k_full = raw_empty + RING, *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
-    uint64_t *s_full = v_empty + 2, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][sub-tile]
+    uint64_t *k_full = raw_empty + RING, *k_empty = k_full + STAGES, *v_full = k_empty + STAGES, *v_empty = v_full + STAGES;
+    uint64_t *s_full = v_empty + STAGES, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][sub-tile]
     uint64_t *q_full = pv_done + 4, *drain = q_full + 1;                          // drain [half]
     uint32_t *tmem_slot = (uint32_t *)(drain + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
@@ -365,13 +368,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             mbar_init(&raw_full[i], 1);
             mbar_init(&raw_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], 8);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&k_full[i], 4);
             mbar_init(&k_empty[i], 2);
-            mbar_init(&v_full[i], 8);
+            mbar_init(&v_full[i], 4);
             mbar_init(&v_empty[i], 2);
-            mbar_init(&drain[i], 1);
         }
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
@@ -604,28 +608,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     } else if (warp < 16) {
         // -------------------------------------------------------- dequant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        const int pg = warp - 8;  // page of every tile
-        uint32_t it = 0;
+        // warps 8..11 take the even sub-tiles, 12..15 the odd ones: a page each
+        const int sub = (warp - 8) >> 2, pg = (warp - 8) & 3;
+        uint32_t j = sub;  // sub-tiles since the start
         for (; sg.more() && ok; sg.next(p)) {
             const int keys = sg.keys(p);
-            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, ++it) {
-                const int st = it & 1;
-                const uint32_t n = it * 8 + pg, slot = n % RING;  // pages since the start
+            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, j += 2) {
+                const uint32_t st = j % STAGES, use = j / STAGES;
+                const uint32_t n = j * 4 + pg, slot = n % RING;  // pages since the start
                 const uint8_t *raw = smem + C::R + slot * C::RAW;
-                if ((it >= 2 && !wait(&k_empty[st], ((it >> 1) - 1) & 1u)) || !wait(&raw_full[slot], (n / RING) & 1u))
+                if ((use > 0 && !wait(&k_empty[st], (use - 1) & 1u)) || !wait(&raw_full[slot], (n / RING) & 1u))
                     break;
-                page_k<D>(raw, smem + C::K + st * C::TILE, pg * 16, lane);
+                page_k<D>(raw, smem + C::K + st * C::SUB, pg * 16, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&k_full[st]);
-                if (it >= 2 && !wait(&v_empty[st], ((it >> 1) - 1) & 1u))
+                if (use > 0 && !wait(&v_empty[st], (use - 1) & 1u))
                     break;
                 // NaN scales: four scale bytes a lane (half of the lanes for d = 64)
                 const uint32_t sb = lane < D / 4 ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * lane) : 0u;
-                uint8_t *V = smem + C::V + st * C::TILE;
+                uint8_t *V = smem + C::V + st * C::SUB;
                 if (__any_sync(0xffffffffu, (((sb & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
-                    if (kt * KC_KEYS + pg * 16 < keys)
+                    if (kt * KC_KEYS + sub * 64 + pg * 16 < keys)
                         *nan_seen = 1;  // or a slot past the last key: the search will tell
                     page_v_scrub<D>(raw, V, pg * 16, lane);
                     __threadfence_block();
@@ -649,60 +654,65 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             const uint32_t sQ = smem_u32(smem + C::Q) + h * C::TILE;
             const uint32_t sK = smem_u32(smem + C::K), sV = smem_u32(smem + C::V);
             const uint32_t S = tmem + h * C::S_COL, O = tmem + C::O0 + h * C::O_COL;
-            uint32_t it = 0, n_p = 0;
+            uint32_t j = 0;  // sub-tiles since the start
             int seg_i = 0;
-            auto issue_s = [&](int sub, int st) {
-                const uint32_t b = sK + st * C::TILE + sub * 8192;
+            // a short, busy wait: two warps, and everything waits for them
+            auto spin = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, WAIT_NS));
+                if (!ok)
+                    *abort_flag = 1;
+                return ok;
+            };
+            uint32_t n_own = 0;  // sub-tiles of this half
+            auto issue_s = [&](uint32_t sub, uint32_t buf) {
+                const uint32_t b = sK + (sub % STAGES) * C::SUB;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_bf16_elect(S + sub * 64, sdesc_kmajor_sw128(sQ + (k >> 2) * C::BLK + (k & 3) * 32),
-                                   sdesc_kmajor_sw128(b + (k >> 2) * C::BLK + (k & 3) * 32), id_s, k ? 1u : 0u);
-                mma_commit_elect(&s_full[2 * h + sub]);
+                    mma_bf16_elect(S + buf * 64, sdesc_kmajor_sw128(sQ + (k >> 2) * C::BLK + (k & 3) * 32),
+                                   sdesc_kmajor_sw128(b + (k >> 2) * C::SBLK + (k & 3) * 32), id_s, k ? 1u : 0u);
+                mma_commit_elect(&s_full[2 * h + buf]);
+                mma_commit_elect(&k_empty[sub % STAGES]);
             };
             for (; sg.more() && ok; sg.next(p), ++seg_i) {
-                const int T = sg.kt1 - sg.kt0;
+                const int T = 2 * (sg.kt1 - sg.kt0);
                 if (h >= sg.halves(p)) {  // no rows: the stages are free as soon as they are filled
-                    for (int t = 0; t < T && ok; ++t, ++it) {
-                        if (!wait(&k_full[it & 1], (it >> 1) & 1u))
+                    for (int t = 0; t < T && ok; ++t, ++j) {
+                        if (!wait(&k_full[j % STAGES], (j / STAGES) & 1u))
                             break;
                         if (lane == 0)
-                            mbar_arrive(&k_empty[it & 1]);
-                        if (!wait(&v_full[it & 1], (it >> 1) & 1u))
+                            mbar_arrive(&k_empty[j % STAGES]);
+                        if (!wait(&v_full[j % STAGES], (j / STAGES) & 1u))
                             break;
                         if (lane == 0)
-                            mbar_arrive(&v_empty[it & 1]);
+                            mbar_arrive(&v_empty[j % STAGES]);
                     }
                     continue;
                 }
-                if (!wait(q_full, (uint32_t)seg_i & 1u) || !wait(&k_full[it & 1], (it >> 1) & 1u))
+                if (!wait(q_full, (uint32_t)seg_i & 1u))
                     break;
-                tc_fence_after();
-                issue_s(0, it & 1);
-                issue_s(1, it & 1);
-                mma_commit_elect(&k_empty[it & 1]);
-                for (int t = 0; t < T && ok; ++t, ++it) {
-                    const int st = it & 1, nst = (it + 1) & 1;
+                for (int t = 0; t < 2; ++t) {
+                    if (!wait(&k_full[(j + t) % STAGES], ((j + t) / STAGES) & 1u))
+                        break;
+                    tc_fence_after();
+                    issue_s(j + t, t);
+                }
 #pragma unroll 1
-                    for (int s = 0; s < 2; ++s) {
-                        if (!wait(&p_full[2 * h + s], n_p & 1u) || (s == 0 && !wait(&v_full[st], (it >> 1) & 1u)))
+                for (int t = 0; t < T && ok; ++t, ++j, ++n_own) {
+                    const uint32_t st = j % STAGES, buf = t & 1;
+                    if (!spin(&v_full[st], (j / STAGES) & 1u) || !spin(&p_full[2 * h + buf], (n_own >> 1) & 1u))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts_elect(O, S + buf * 64 + k * 8, sdesc_mn(sV + st * C::SUB + k * 2048, C::SBLK), id_o, t | k);
+                    mma_commit_elect(&pv_done[2 * h + buf]);
+                    mma_commit_elect(&v_empty[st]);
+                    if (t + 2 < T) {
+                        if (!spin(&k_full[(j + 2) % STAGES], ((j + 2) / STAGES) & 1u))
                             break;
                         tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ts_elect(O, S + s * 64 + k * 8, sdesc_mn(sV + st * C::TILE + s * 8192 + k * 2048, C::BLK),
-                                         id_o, t | s | k);
-                        mma_commit_elect(&pv_done[2 * h + s]);
-                        if (t + 1 < T) {
-                            if (s == 0 && !wait(&k_full[nst], ((it + 1) >> 1) & 1u))
-                                break;
-                            tc_fence_after();
-                            issue_s(s, nst);
-                        }
+                        issue_s(j + 2, buf);
                     }
-                    ++n_p;
-                    mma_commit_elect(&v_empty[st]);
-                    if (t + 1 < T)
-                        mma_commit_elect(&k_empty[nst]);
                 }
             }
             if (!ok) {
