@@ -42,7 +42,10 @@ constexpr int THREADS = 20 * 32;
 constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 64;  // 256 and 384 threads: 61440 registers, 96 for each thread at launch
 constexpr int RING = 24;                 // pages in flight
 constexpr int STAGES = 3;                // sub-tiles of 64 keys of K, and of V, in f16
+constexpr int STAGES_DUAL = 4;           // the same where both halves share one Q tile
 constexpr float RAISE = 8.f;             // P <= 2^8
+constexpr int DUAL_UNITS = 8;            // (256 columns x 128 keys) a CTA up to which items have 128 columns
+constexpr int WHOLE_TILES = 12;          // key tiles by which an unshared item may be longer than an even share
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int D>
@@ -53,9 +56,11 @@ struct Ck {
     static constexpr int SBLK = 64 * 128;             // the same of a 64-key sub-tile
     static constexpr int SUB = CB * SBLK;
     static constexpr int RAW = Layout<D>::BYTES;
-    static constexpr int Q = 0, K = 2 * TILE, V = K + STAGES * SUB, R = V + STAGES * SUB;
+    static constexpr int Q = 0, K = 2 * TILE, R = K + 2 * STAGES * SUB;
+    static constexpr int K_DUAL = TILE;               // one Q tile less, one stage of K and of V more
+    static_assert(K_DUAL + 2 * STAGES_DUAL * SUB <= R);
     static constexpr int BAR = R + RING * RAW;
-    static constexpr int BYTES = BAR + 1024 + 1024;   // barriers, alignment
+    static constexpr int BYTES = BAR + 1024 + 2048 + 1024;  // barriers, (m, l) pairs, alignment
     static constexpr uint32_t S_COL = 128, O0 = 256, O_COL = D;
 };
 
@@ -84,18 +89,56 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D (+)= A B with A in tensor memory (one elected lane issues).
-__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate)
+// Four k-steps of D (+)= A B, both operands in shared memory: a and b advance
+// by 32 bytes a step.  One elected lane issues.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
         "{\n"
-        ".reg .pred p, e;\n"
+        ".reg .pred p, t, e;\n"
+        ".reg .b64 a1, a2, a3, b1, b2, b3;\n"
         "elect.sync _|e, 0xffffffff;\n"
         "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "add.s64 a1, %1, 2;\n"
+        "add.s64 b1, %2, 2;\n"
+        "add.s64 a2, %1, 4;\n"
+        "add.s64 b2, %2, 4;\n"
+        "add.s64 a3, %1, 6;\n"
+        "add.s64 b3, %2, 6;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Four k-steps of D (+)= A B with A in tensor memory (8 columns a step) and B
+// MN-major in shared memory (16 rows of 128 bytes a step).
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p, t, e;\n"
+        ".reg .b64 b1, b2, b3;\n"
+        ".reg .b32 a1, a2, a3;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "add.s32 a1, %1, 8;\n"
+        "add.s64 b1, %2, 128;\n"
+        "add.s32 a2, %1, 16;\n"
+        "add.s64 b2, %2, 256;\n"
+        "add.s32 a3, %1, 24;\n"
+        "add.s64 b3, %2, 384;\n"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -171,7 +214,7 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // Key tiles of item qt.
 __host__ __device__ inline int item_tiles(const Kv4Chunk &p, int qt)
 {
-    const long long last = (long long)(qt + 1) * KC_ROWS < p.cols ? (long long)(qt + 1) * KC_ROWS : p.cols;
+    const long long last = (long long)(qt + 1) * p.rows < p.cols ? (long long)(qt + 1) * p.rows : p.cols;
     return (p.offset + (int)((last - 1) / p.group)) / KC_KEYS + 1;
 }
 
@@ -209,12 +252,31 @@ struct Segments {
         if (left > 0)
             size(p);
     }
-    __device__ int halves(const Kv4Chunk &p) const { return p.cols - (long long)qt * KC_ROWS > 128 ? 2 : 1; }
+    // key tiles of half h: all of the segment's, or (both halves on the same
+    // columns) every other one
+    __device__ int tiles_of(const Kv4Chunk &p, int h) const
+    {
+        if (p.rows == 128)
+            return (kt1 - kt0 - h + 1) >> 1;
+        return h == 0 || p.cols - (long long)qt * KC_ROWS > 128 ? kt1 - kt0 : 0;
+    }
     // keys that the item's last column sees
     __device__ int keys(const Kv4Chunk &p) const
     {
-        const long long last = min((long long)(qt + 1) * KC_ROWS, (long long)p.cols) - 1;
+        const long long last = min((long long)(qt + 1) * p.rows, (long long)p.cols) - 1;
         return p.offset + (int)(last / p.group) + 1;
+    }
+};
+
+// A place in a ring of n stages: the stage, and the parity of its full barrier.
+struct Place {
+    uint32_t st = 0, ph = 0;
+    __device__ __forceinline__ void next(uint32_t n)
+    {
+        if (++st == n) {
+            st = 0;
+            ph ^= 1u;
+        }
     }
 };
 
@@ -225,6 +287,13 @@ struct Segments {
 // that a lane writes in a row lie at four lane constants; everything else is
 // an immediate.  A half-warp's 8-byte stores go to four rows whose swizzles
 // differ (tokens 0, 2, 4, 6 or 1, 3, 5, 7): no bank conflict.
+// The largest of eight bf16 magnitudes, as bits (NaNs count as large).
+__device__ __forceinline__ uint32_t largest_bits(uint4 u)
+{
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
+}
+
 template <int D>
 __device__ __forceinline__ void page_k(const uint8_t *raw, uint8_t *tile, int row0, int lane)
 {
@@ -354,34 +423,40 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *raw_full = (uint64_t *)(smem + C::BAR);
     uint64_t *raw_empty = raw_full + RING;
-    uint64_t *k_full = raw_empty + RING, *k_empty = k_full + STAGES, *v_full = k_empty + STAGES, *v_empty = v_full + STAGES;
-    uint64_t *s_full = v_empty + STAGES, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][sub-tile]
-    uint64_t *q_full = pv_done + 4, *drain = q_full + 1;                          // drain [half]
+    uint64_t *k_full = raw_empty + RING, *k_empty = k_full + STAGES_DUAL, *v_full = k_empty + STAGES_DUAL;
+    uint64_t *v_empty = v_full + STAGES_DUAL, *s_full = v_empty + STAGES_DUAL, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][sub-tile]
+    uint64_t *q_full = pv_done + 4, *drain = q_full + 2;                          // [half]
     uint32_t *tmem_slot = (uint32_t *)(drain + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad_key = abort_flag + 1;   // lowest key met whose page lies outside the pool
     volatile int *nan_seen = bad_key + 1;     // a NaN scale of V was met
 
+    float2 *ml_x = (float2 *)(smem + C::BAR + 1024);  // [half][128]: m and l for the other half
+
+    const bool dual = p.rows == 128;
+    const uint32_t stages = dual ? STAGES_DUAL : STAGES;
+    uint8_t *sK = smem + (dual ? C::K_DUAL : C::K), *sV = sK + stages * C::SUB;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(&raw_full[i], 1);
             mbar_init(&raw_empty[i], 1);
         }
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < STAGES_DUAL; ++i) {
             mbar_init(&k_full[i], 4);
             mbar_init(&k_empty[i], 2);
             mbar_init(&v_full[i], 4);
             mbar_init(&v_empty[i], 2);
         }
-        mbar_init(&drain[0], 1);
-        mbar_init(&drain[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 4);
+            mbar_init(&drain[i], 1);
+        }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
         }
-        mbar_init(q_full, 8);
         *abort_flag = 0;
         *bad_key = 0x7fffffff;
         *nan_seen = 0;
@@ -412,49 +487,68 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         const uint32_t sT = lanes + half * C::S_COL, oT = lanes + C::O0 + half * C::O_COL;
         uint32_t n_t = 0;  // key tiles this half has been through
         for (; sg.more(); sg.next(p)) {
-            const bool mine = half < sg.halves(p);
-            const long long col0 = (long long)sg.qt * KC_ROWS + half * 128;
-            const int valid = (int)min(128ll, p.cols - col0);  // columns of this half (<= 0 unless mine)
+            const int own = sg.tiles_of(p, half);
+            const long long col0 = (long long)sg.qt * p.rows + (dual ? 0 : half * 128);
+            const int valid = (int)min(128ll, p.cols - col0);  // columns of this half (<= 0 if it has none)
             const long long col = min(col0 + r, (long long)p.cols - 1);
             const int row = (int)(col / p.group), head = sg.kvh * p.group + (int)(col - (long long)row * p.group);
             const int seen = p.offset + row + 1;
-            uint8_t *q = smem + C::Q + half * C::TILE;
+            uint8_t *q = smem + C::Q + (dual ? 0 : half * C::TILE);
             constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows a warp-wide access
             const int lr = lane / LPR, lc = lane % LPR;
             float sc = 0.f;
-            if (mine) {
-                // this warp's 32 rows of Q, each scaled by a power of two into [1, 4), as f16
+            if (own > 0) {
+                // this warp's 32 rows of Q as f16.  Rows of ordinary size go as
+                // they are; if any has its largest magnitude outside [2^-6,
+                // 2^15), each is scaled by a power of two into [1, 4) first
                 const long long src = row * p.q_stride + (size_t)head * D;
+                constexpr int N = 32 / RPI;
+                uint4 u[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    u[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, k * RPI + lr)) + lc);
+                bool plain = true;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    if (k * RPI + lr + (warp & 3) * 32 >= valid)
+                        u[k] = make_uint4(0, 0, 0, 0);
+                    const uint32_t a = largest_bits(u[k]);
+                    plain = plain && a < 0x4700u;
+                    // a row is small if all of its lanes are
+                    const uint32_t big = __ballot_sync(0xffffffffu, a >= 0x3c80u), any = __ballot_sync(0xffffffffu, a != 0u);
+                    constexpr uint32_t row_mask = LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u;
+#pragma unroll
+                    for (int x = 0; x < RPI; ++x)
+                        plain = plain && ((any >> (x * LPR) & row_mask) == 0u || (big >> (x * LPR) & row_mask) != 0u);
+                }
                 int e = 0;
+                auto put = [&](uint4 x, int i, float down) {
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
+                        o[j] = pack_h2(f.x * down, f.y * down);
+                    }
+                    *reinterpret_cast<uint4 *>(q + (lc >> 3) * C::BLK + swz((warp & 3) * 32 + i + lr, lc & 7)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                };
+                if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        put(u[k], k * RPI, 1.f);
+                } else {
 #pragma unroll 1
-                for (int i0 = 0; i0 < 32; i0 += 4 * RPI) {
-                    uint4 u[4];
+                    for (int i = 0; i < 32; i += RPI) {
+                        uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, i + lr)) + lc);
+                        if (i + lr + (warp & 3) * 32 >= valid)
+                            x = make_uint4(0, 0, 0, 0);
+                        uint32_t a = largest_bits(x);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        u[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                         p.q + __shfl_sync(0xffffffffu, src, i0 + k * RPI + lr)) + lc);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                        float2 f[4];
-                        float a = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            f[j] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-                            a = fmaxf(a, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
-                        }
-#pragma unroll
-                        for (int x = 1; x < LPR; x *= 2)
-                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, x));
-                        const int er = query_exponent(a), i = i0 + k * RPI;
-                        const float down = pow2(-er);
-                        const bool have = (warp & 3) * 32 + i + lr < valid;
-                        uint32_t o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[j] = have ? pack_h2(f[j].x * down, f[j].y * down) : 0u;
-                        *reinterpret_cast<uint4 *>(q + (lc >> 3) * C::BLK + swz((warp & 3) * 32 + i + lr, lc & 7)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int k = 1; k < LPR; k *= 2)
+                            a = max(a, __shfl_xor_sync(0xffffffffu, a, k));
+                        const int er = query_exponent(__uint_as_float(a << 16));
+                        put(x, i, pow2(-er));
                         const int mine_e = __shfl_sync(0xffffffffu, er, (lane % RPI) * LPR);  // of row i + lane % RPI
                         if (lane / RPI == i / RPI)
                             e = mine_e;
@@ -462,16 +556,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 }
                 sc = fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e), 1e-38f);  // never 0: a masked score stays -inf
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(q_full);
-            if (!mine)
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&q_full[half]);
+            } else if (!dual) {
                 continue;
+            }
             const int seen0 = p.offset + (int)(col0 / p.group) + 1;  // of the half's first column
             float m = LOWEST, l = 0.f;
             bool fresh = true;  // no O yet
-            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, ++n_t) {
+            for (int kt = sg.kt0 + (dual ? half : 0); kt < sg.kt1 && ok; kt += dual ? 2 : 1, ++n_t) {
 #pragma unroll 1
                 for (int s = 0; s < 2; ++s) {
                     if (!wait(&s_full[2 * half + s], n_t & 1u))
@@ -542,25 +636,60 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 }
             }
             // ---- the segment's result
-            if (ok && wait(&pv_done[2 * half + 1], (n_t - 1) & 1u))
+            if (ok && own > 0 && wait(&pv_done[2 * half + 1], (n_t - 1) & 1u))
                 tc_fence_after();
             uint32_t nans = 0;
             if (*nan_seen)
                 nans = nan_blocks<D>(p, sg.kvh, sg.kt0 * KC_KEYS, min(seen, sg.kt1 * KC_KEYS));
             __syncwarp();
+            // with both halves on the same columns, each takes half of the
+            // channels and joins the two O there: f, f2 are their factors
+            float f = 1.f, f2 = 0.f;
+            const int c0 = dual ? half * (D / 2) : 0, c1 = dual ? c0 + D / 2 : D;
+            const bool two = dual && sg.tiles_of(p, 1) > 0;
+            if (dual) {
+                ml_x[half * 128 + r] = make_float2(m, l);
+                tc_fence_before();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                tc_fence_after();
+                const float2 o = ml_x[(half ^ 1) * 128 + r];
+                const float M = fmaxf(m, o.x);
+                f = ex2(m - M);
+                f2 = ex2(o.x - M);
+                l = l * f + o.y * f2;
+                m = M;
+                if (half == 1) {  // f belongs to the first half's O, f2 to the second's
+                    const float x = f;
+                    f = f2;
+                    f2 = x;
+                }
+                ok = ok && !__any_sync(0xffffffffu, *abort_flag);
+            }
             if (!ok || *bad_key < seen) {  // one table serves every item, so the key found in any of them counts
                 l = __int_as_float(0x7fc00000);
                 m = 0.f;
             }
             const bool whole = sg.kt0 == 0 && sg.kt1 == sg.n_tiles;
             const size_t part = (size_t)blockIdx.x * 2 + (sg.first ? 0 : 1);
+            const int pr = (dual ? 0 : half * 128) + r;  // row of the item's partial
             const float inv = p.vs / l;
+            const uint32_t oA = dual ? lanes + C::O0 : oT, oB = lanes + C::O0 + C::O_COL;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = c0; c < c1; c += 16) {
                 float v[16];
                 if (ok) {
-                    tmem_ld_x16(oT + c, v);
+                    tmem_ld_x16(oA + c, v);
                     tmem_ld_wait();
+                    if (dual) {
+                        float y[16];
+                        if (two) {
+                            tmem_ld_x16(oB + c, y);
+                            tmem_ld_wait();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = v[j] * f + (two ? y[j] * f2 : 0.f);
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -571,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                     for (int j = 0; j < 16; ++j)
                         v[j] = __int_as_float(0x7fc00000);
                 if (whole) {
-                    // through the half's Q tile, which no MMA reads any more
+                    // through the Q tile, which no MMA reads any more
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float x[8];
@@ -582,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         *reinterpret_cast<uint4 *>(q + (ch >> 3) * C::BLK + swz(r, ch & 7)) = pack8_bf16(x);
                     }
                 } else if (r < valid) {
-                    float4 *po = reinterpret_cast<float4 *>(p.part_o) + (part * (D / 4) + c / 4) * KC_ROWS + half * 128 + r;
+                    float4 *po = reinterpret_cast<float4 *>(p.part_o) + (part * (D / 4) + c / 4) * KC_ROWS + pr;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         po[k * KC_ROWS] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -591,19 +720,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             }
             if (whole) {
                 const long long dst = row * p.out_stride + (size_t)head * D;
+                const int shift = (D == 128 ? 4 : 3) - (dual ? 1 : 0);  // log2 of the 16-byte chunks of a row here
+                const int rl = lane >> shift, cl = (lane & ((1 << shift) - 1)) + c0 / 8;
 #pragma unroll 4
-                for (int i = 0; i < 32; i += RPI) {
-                    const long long at = __shfl_sync(0xffffffffu, dst, i + lr);
-                    const int rr = (warp & 3) * 32 + i + lr;
+                for (int i = 0; i < 32; i += 32 >> shift) {
+                    const long long at = __shfl_sync(0xffffffffu, dst, i + rl);
+                    const int rr = (warp & 3) * 32 + i + rl;
                     if (rr < valid)
-                        reinterpret_cast<uint4 *>(p.out + at)[lc] =
-                            *reinterpret_cast<const uint4 *>(q + (lc >> 3) * C::BLK + swz(rr, lc & 7));
+                        reinterpret_cast<uint4 *>(p.out + at)[cl] =
+                            *reinterpret_cast<const uint4 *>(q + (cl >> 3) * C::BLK + swz(rr, cl & 7));
                 }
                 __syncwarp();  // the next segment's Q goes there
-            } else if (r < valid) {
-                p.part_ml[part * KC_ROWS + half * 128 + r] = make_float2(m, l);
+            } else if (r < valid && (!dual || half == 0)) {
+                p.part_ml[part * KC_ROWS + pr] = make_float2(m, l);
             }
             tc_fence_before();  // the next segment's MMAs overwrite O
+            if (dual)           // and both halves have read both
+                asm volatile("bar.sync 1, 256;" ::: "memory");
         }
     } else if (warp < 16) {
         // -------------------------------------------------------- dequant
@@ -611,24 +744,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         // warps 8..11 take the even sub-tiles, 12..15 the odd ones: a page each
         const int sub = (warp - 8) >> 2, pg = (warp - 8) & 3;
         uint32_t j = sub;  // sub-tiles since the start
+        Place at;
+        if (sub)
+            at.next(stages);
         for (; sg.more() && ok; sg.next(p)) {
             const int keys = sg.keys(p);
             for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, j += 2) {
-                const uint32_t st = j % STAGES, use = j / STAGES;
                 const uint32_t n = j * 4 + pg, slot = n % RING;  // pages since the start
                 const uint8_t *raw = smem + C::R + slot * C::RAW;
-                if ((use > 0 && !wait(&k_empty[st], (use - 1) & 1u)) || !wait(&raw_full[slot], (n / RING) & 1u))
+                if ((j >= stages && !wait(&k_empty[at.st], at.ph ^ 1u)) || !wait(&raw_full[slot], (n / RING) & 1u))
                     break;
-                page_k<D>(raw, smem + C::K + st * C::SUB, pg * 16, lane);
+                page_k<D>(raw, sK + at.st * C::SUB, pg * 16, lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&k_full[st]);
-                if (use > 0 && !wait(&v_empty[st], (use - 1) & 1u))
+                    mbar_arrive(&k_full[at.st]);
+                if (j >= stages && !wait(&v_empty[at.st], at.ph ^ 1u))
                     break;
                 // NaN scales: four scale bytes a lane (half of the lanes for d = 64)
                 const uint32_t sb = lane < D / 4 ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * lane) : 0u;
-                uint8_t *V = smem + C::V + st * C::SUB;
+                uint8_t *V = sV + at.st * C::SUB;
                 if (__any_sync(0xffffffffu, (((sb & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
                     if (kt * KC_KEYS + sub * 64 + pg * 16 < keys)
                         *nan_seen = 1;  // or a slot past the last key: the search will tell
@@ -641,8 +776,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&raw_empty[slot]);
-                    mbar_arrive(&v_full[st]);
+                    mbar_arrive(&v_full[at.st]);
                 }
+                at.next(stages);
+                at.next(stages);
             }
         }
     } else {
@@ -651,68 +788,83 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             // ---------------------------------------------------- MMA issue
             const int h = warp - 16;
             const uint32_t id_s = idesc_f16(128, 64, false), id_o = idesc_f16(128, D, true);
-            const uint32_t sQ = smem_u32(smem + C::Q) + h * C::TILE;
-            const uint32_t sK = smem_u32(smem + C::K), sV = smem_u32(smem + C::V);
             const uint32_t S = tmem + h * C::S_COL, O = tmem + C::O0 + h * C::O_COL;
-            uint32_t j = 0;  // sub-tiles since the start
-            int seg_i = 0;
-            // a short, busy wait: two warps, and everything waits for them
+            const uint64_t dQ = sdesc_kmajor_sw128(smem_u32(smem + C::Q) + (dual ? 0 : h * C::TILE));
+            const uint64_t dK = sdesc_kmajor_sw128(smem_u32(sK)), dV = sdesc_mn(smem_u32(sV), C::SBLK);
+            // Both warps pass over every stage in order, so that neither ever
+            // waits for a phase two ahead; a sub-tile of the other half is let
+            // go as soon as it is filled.
+            Place k, v;
+            uint32_t n_seg = 0, n_own = 0;  // segments in which this half has rows; its sub-tiles
+            // a busy wait: two warps, and everything waits for them
             auto spin = [&](uint64_t *bar, uint32_t parity) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, WAIT_NS));
                 if (!ok)
                     *abort_flag = 1;
                 return ok;
             };
-            uint32_t n_own = 0;  // sub-tiles of this half
-            auto issue_s = [&](uint32_t sub, uint32_t buf) {
-                const uint32_t b = sK + (sub % STAGES) * C::SUB;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_bf16_elect(S + buf * 64, sdesc_kmajor_sw128(sQ + (k >> 2) * C::BLK + (k & 3) * 32),
-                                   sdesc_kmajor_sw128(b + (k >> 2) * C::SBLK + (k & 3) * 32), id_s, k ? 1u : 0u);
-                mma_commit_elect(&s_full[2 * h + buf]);
-                mma_commit_elect(&k_empty[sub % STAGES]);
+            auto pass = [&](Place &at, uint64_t *full, uint64_t *empty) {
+                if (wait(&full[at.st], at.ph) && lane == 0)
+                    mbar_arrive(&empty[at.st]);
+                at.next(stages);
             };
-            for (; sg.more() && ok; sg.next(p), ++seg_i) {
-                const int T = 2 * (sg.kt1 - sg.kt0);
-                if (h >= sg.halves(p)) {  // no rows: the stages are free as soon as they are filled
-                    for (int t = 0; t < T && ok; ++t, ++j) {
-                        if (!wait(&k_full[j % STAGES], (j / STAGES) & 1u))
-                            break;
-                        if (lane == 0)
-                            mbar_arrive(&k_empty[j % STAGES]);
-                        if (!wait(&v_full[j % STAGES], (j / STAGES) & 1u))
-                            break;
-                        if (lane == 0)
-                            mbar_arrive(&v_empty[j % STAGES]);
-                    }
-                    continue;
-                }
-                if (!wait(q_full, (uint32_t)seg_i & 1u))
+            auto issue_s = [&](uint32_t buf) {  // S of the sub-tile at k
+                if (!spin(&k_full[k.st], k.ph))
+                    return;
+                tc_fence_after();
+#pragma unroll
+                for (int cb = 0; cb < C::CB; ++cb)
+                    mma_ss4(S + buf * 64, dQ + cb * (C::BLK >> 4), dK + k.st * (C::SUB >> 4) + cb * (C::SBLK >> 4), id_s, cb);
+                mma_commit_elect(&s_full[2 * h + buf]);
+                mma_commit_elect(&k_empty[k.st]);
+                k.next(stages);
+            };
+            for (; sg.more() && ok; sg.next(p)) {
+                const int T = 2 * sg.tiles_of(p, h), all = 2 * (sg.kt1 - sg.kt0);  // sub-tiles: own, and of the segment
+                if (T > 0 && !wait(&q_full[h], n_seg++ & 1u))
                     break;
-                for (int t = 0; t < 2; ++t) {
-                    if (!wait(&k_full[(j + t) % STAGES], ((j + t) / STAGES) & 1u))
-                        break;
-                    tc_fence_after();
-                    issue_s(j + t, t);
+                int pk = T, pv = T;  // sub-tiles of the segment passed, once the own ones are
+                // where the halves take every other tile, the two sub-tiles
+                // before each of this half's tiles are the other's
+                auto skip = [&](int t) { return dual && (t & 1) == 0 && (h == 1 || t > 0); };
+                auto skip_k = [&](int t) {
+                    if (skip(t)) {
+                        pass(k, k_full, k_empty);
+                        pass(k, k_full, k_empty);
+                        pk += 2;
+                    }
+                };
+                for (int t = 0; t < min(2, T) && ok; ++t) {
+                    skip_k(t);
+                    issue_s(t);
                 }
 #pragma unroll 1
-                for (int t = 0; t < T && ok; ++t, ++j, ++n_own) {
-                    const uint32_t st = j % STAGES, buf = t & 1;
-                    if (!spin(&v_full[st], (j / STAGES) & 1u) || !spin(&p_full[2 * h + buf], (n_own >> 1) & 1u))
+                for (int t = 0; t < T && ok; ++t, ++n_own) {
+                    const uint32_t buf = t & 1;
+                    if (skip(t)) {
+                        pass(v, v_full, v_empty);
+                        pass(v, v_full, v_empty);
+                        pv += 2;
+                    }
+                    if (!spin(&v_full[v.st], v.ph) || !spin(&p_full[2 * h + buf], (n_own >> 1) & 1u))
                         break;
                     tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ts_elect(O, S + buf * 64 + k * 8, sdesc_mn(sV + st * C::SUB + k * 2048, C::SBLK), id_o, t | k);
+                    mma_ts4(O, S + buf * 64, dV + v.st * (C::SUB >> 4), id_o, t);
                     mma_commit_elect(&pv_done[2 * h + buf]);
-                    mma_commit_elect(&v_empty[st]);
+                    mma_commit_elect(&v_empty[v.st]);
+                    v.next(stages);
                     if (t + 2 < T) {
-                        if (!spin(&k_full[(j + 2) % STAGES], ((j + 2) / STAGES) & 1u))
-                            break;
-                        tc_fence_after();
-                        issue_s(j + 2, buf);
+                        skip_k(t + 2);
+                        issue_s(buf);
                     }
+                }
+                // what is left is the other half's
+                for (; pv < all && ok; ++pv) {
+                    if (pk == pv) {
+                        pass(k, k_full, k_empty);
+                        ++pk;
+                    }
+                    pass(v, v_full, v_empty);
                 }
             }
             if (!ok) {
@@ -787,7 +939,7 @@ __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ 
     // of the CTAs only ca can have come to the item from another one
     const int first = 2 * ca + (same ? 0 : 1);
     const int r = blockIdx.y * 32 + lane;  // this lane's column of the item
-    const int valid = (int)min((long long)KC_ROWS, p.cols - (long long)item.qt * KC_ROWS);
+    const int valid = (int)min((long long)p.rows, p.cols - (long long)item.qt * p.rows);
     if (blockIdx.y * 32 >= valid)
         return;
     const float2 *ml = p.part_ml + r;
@@ -826,7 +978,7 @@ __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ 
         const int rr = i / (D / 8), ch = i % (D / 8);
         if (blockIdx.y * 32 + rr >= valid)
             break;
-        const int col = item.qt * KC_ROWS + blockIdx.y * 32 + rr;
+        const int col = item.qt * p.rows + blockIdx.y * 32 + rr;
         const int row = col / p.group, head = item.kvh * p.group + col - row * p.group;
         reinterpret_cast<uint4 *>(p.out + row * p.out_stride + (size_t)head * D)[ch] =
             *reinterpret_cast<const uint4 *>(&s_o[rr][ch * 8]);
@@ -848,7 +1000,7 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
         return e;
     if (kv4_chunk_workspace_bytes(p, D) == 0)
         return cudaSuccess;
-    return launch_kernel(true, k_kv4_chunk_join<D>, dim3(p.ctas - 1, KC_ROWS / 32), dim3(256), 0, s, p);
+    return launch_kernel(true, k_kv4_chunk_join<D>, dim3(p.ctas - 1, p.rows / 32), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -856,14 +1008,28 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
 bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len)
 {
     p.cols = chunk_len * p.group;
-    p.n_qt = (p.cols + KC_ROWS - 1) / KC_ROWS;
-    long long head_units = 0;
-    for (int qt = 0; qt < p.n_qt; ++qt)
-        head_units += item_tiles(p, qt);
-    const long long units = head_units * p.n_kv;
+    // Items of 256 columns convert each key once for both halves; items of 128
+    // (both halves on them, on alternate tiles) make more CTAs of the same
+    // work and leave fewer partials.  Few units: 128.
+    long long units = 0;
+    for (p.rows = 256;; p.rows = 128) {
+        p.n_qt = (p.cols + p.rows - 1) / p.rows;
+        long long head_units = 0;
+        for (int qt = 0; qt < p.n_qt; ++qt)
+            head_units += item_tiles(p, qt);
+        units = head_units * p.n_kv;
+        if (p.rows == 128 || units > (long long)DUAL_UNITS * KC_CTAS)
+            break;
+    }
     p.ctas = (int)(units < KC_CTAS ? units : KC_CTAS);
+    // one CTA per item, if the partials that this saves are worth more than
+    // the SMs that it leaves idle
+    const long long items = (long long)p.n_qt * p.n_kv;
+    if (items < p.ctas && units / items - units / p.ctas <= WHOLE_TILES)
+        p.ctas = (int)items;
     if (units / p.ctas >= 0x7fffffff)
         return false;
+    const bool whole = p.ctas == items;
     long long at = 0, item_at = 0;  // first unit of (kvh, qt)
     int kvh = 0, qt = 0;
     for (int c = 0; c < p.ctas; ++c) {
@@ -872,7 +1038,7 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len)
                 qt = 0;
                 ++kvh;
             }
-        const long long next = units * (c + 1) / p.ctas;
+        const long long next = whole ? at + item_tiles(p, qt) : units * (c + 1) / p.ctas;
         p.start[c] = KcStart{kvh, qt, (int)(at - item_at), (int)(next - at)};
         at = next;
     }

@@ -6,7 +6,7 @@
 
 namespace hb {
 
-constexpr int KC_ROWS = 256;    // query columns (row x head of a kv head) of an item: two MMA tiles of 128
+constexpr int KC_ROWS = 256;    // query columns (row x head of a kv head) of an item at most: two MMA tiles of 128
 constexpr int KC_KEYS = 128;    // keys of a tile
 constexpr int KC_CTAS = 152;    // CTAs at most: one per SM
 
@@ -26,9 +26,10 @@ struct Kv4Chunk {
     int offset, cols;           // cols = chunk_len * group
     bf16 *out;
     long long out_stride;
-    // work: units are (item, key tile); item = (kv head, 256 columns), kv head
-    // major; CTA c takes the units of start[c], as many as any other CTA or one
-    // more
+    // work: units are (item, key tile); item = (kv head, `rows` columns), kv
+    // head major; CTA c takes the units of start[c]: a whole item, or as many as
+    // any other CTA or one more
+    int rows;                   // 256, or 128: both halves of a CTA on the same columns, on alternate key tiles
     int n_qt, ctas;             // items of a kv head; CTAs
     KcStart start[KC_CTAS];
     float *part_o;              // [2 ctas][D / 4][256][4]: CTA c's segment that starts with it, and its last
