@@ -36,7 +36,6 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int SPLIT_MIN = 256;        // keys of a split at least
 constexpr int MAX_KEYS = 1 << 27;
 constexpr int MAX_COLS = 1 << 24;     // queries of a kv head in a chunk
-constexpr int CHUNK_COLS = 8;         // queries of a kv head up to which a chunk runs as decode columns
 
 struct Kv4Attn {
     const uint8_t *pool;
@@ -643,31 +642,52 @@ extern "C" int hb_kv4_decode(const hb_kv4_pool *pool, const void *q, long long q
     return launch(p, d, n_decodes, n_decodes, (cudaStream_t)cuda_stream);
 }
 
-// A chunk of few queries runs as columns of the decode kernel (`p` is filled
-// then, 0 returned), any other on the tcgen05 kernel (`c`, 1); -1: too large.
+// Microseconds that a chunk takes as columns of the decode kernel, and on the
+// tcgen05 kernel: fits of measured times, good to about a quarter.  With 40
+// heads of 128 and 1000 cached keys, 32 rows take 16.2 us against 19.4, 64
+// rows 22.8 against 19.5; with 16000 keys, 16 rows 56 against 74, 32 rows 97
+// against 75; with one kv head and 16000 keys, 256 rows 27 against 57.
+static double decode_kernel_us(int offset, int len, int group, int n_kv)
+{
+    const double pages = (offset + 0.5 * len) / 16 + 1;
+    return 5 + n_kv * (double)(((long long)len * group + 7) / 8) * pages / 1500;
+}
+static double tensor_kernel_us(const Kv4Chunk &c)
+{
+    double units = 0;
+    for (int i = 0; i < c.ctas; ++i)
+        units += c.start[i].units;
+    const double items = (double)c.n_qt * c.n_kv, tiles = units / c.ctas;
+    return c.ctas == items ? 8 + 1.25 * tiles : 8 + 1.7 * tiles + 0.7 * (c.ctas / items + 1);
+}
+
+// Plan a chunk: 0, `p` filled, as columns of the decode kernel; 1, `c` filled,
+// on the tcgen05 kernel; -1: too large.
 static int plan_chunk(Kv4Attn &p, Kv4Chunk &c, int offset, int len, int n_heads, int n_kv, int d, long long *need)
 {
     const int group = n_heads / n_kv;
-    if ((long long)len * group <= CHUNK_COLS) {
-        p.n_kv = n_kv;
-        p.group = group;
-        p.n_heads = n_heads;
-        p.chunk_offset = offset;
-        p.chunk_len = len;
-        const Split sp = plan_split(ctas_of(len * group, n_kv, 1), offset + len);
-        p.split_len = sp.len;
-        p.n_splits = sp.n;
-        *need = workspace_bytes_of(len, n_heads, d, sp.n);
-        return 0;
-    }
     c.n_kv = n_kv;
     c.group = group;
     c.n_heads = n_heads;
     c.offset = offset;
-    if (!kv4_chunk_plan(c, len))
+    const double few = decode_kernel_us(offset, len, group, n_kv);
+    const bool tensor = (long long)len * group > 8 && few > 8;
+    if (tensor && !kv4_chunk_plan(c, len))
         return -1;
-    *need = kv4_chunk_workspace_bytes(c, d);
-    return 1;
+    if (tensor && tensor_kernel_us(c) < few) {
+        *need = kv4_chunk_workspace_bytes(c, d);
+        return 1;
+    }
+    p.n_kv = n_kv;
+    p.group = group;
+    p.n_heads = n_heads;
+    p.chunk_offset = offset;
+    p.chunk_len = len;
+    const Split sp = plan_split(ctas_of(len * group, n_kv, 1), offset + len);
+    p.split_len = sp.len;
+    p.n_splits = sp.n;
+    *need = workspace_bytes_of(len, n_heads, d, sp.n);
+    return 0;
 }
 
 extern "C" long long hb_kv4_chunk_workspace(int chunk_offset, int chunk_len, int n_heads, int n_kv_heads, int head_dim)
