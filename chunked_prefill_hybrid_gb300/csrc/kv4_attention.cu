@@ -93,6 +93,21 @@ __device__ __forceinline__ Col column(const Kv4Attn &p, int seq, int kvh, int c)
     return r;
 }
 
+// A fragments of V^T for channel blocks 4w..4w+3: the bytes of two tokens
+// (channels 2g, 2g + 1) become bytes of two channels, and those f16 pairs of
+// tokens.  a[0], a[1]: the first two tokens of rows g and g + 8, a[2], a[3] the
+// other two.
+template <int KW>
+__device__ __forceinline__ void pair_tokens(const uint32_t (&vw)[2][KW], int w, uint32_t (&a)[4][4])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t x = vw[h][w], y = vw[h][KW / 2 + w];
+        from_e2m1x8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), a[2 * h]);
+        from_e2m1x8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), a[2 * h + 1]);
+    }
+}
+
 // Shared memory of a CTA: a ring of RING pages for each warp, and after the
 // key loop (in the same place) the warps' results.
 template <int D>
@@ -239,53 +254,184 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             o[i][j] = 0.f;
 
     const int tok0 = 4 * (g >> 1) + (g & 1);  // tokens tok0 and tok0 + 2 are rows g and g + 8 of S^T
-    int slot = 0;
-    uint32_t phase = 0;
-    for (int i = 0; i < n_tiles; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_sleep(&full[warp][slot], phase, nullptr, WAIT_NS))) {
-            // a page did not come: the rows get NaN, and no copy may land
-            // after the CTA has ended
-            bad = true;
-            for (int j = i; j < min(i + RING, n_tiles); ++j)
-                mbar_wait(&full[warp][j % RING], (uint32_t)(j / RING) & 1u, nullptr, WAIT_NS / 8);
-            break;
-        }
-        const uint8_t *page = ring + slot * L::BYTES;
-        // everything of the page into registers, then the slot is free
-        uint32_t kw[2][KW], vw[2][KW], kst[2][FEW ? 1 : NB / 4], vst[FEW ? 1 : NB];
+    // a page that did not come: the rows get NaN, and no copy may land after
+    // the CTA has ended
+    auto lost = [&](int i) {
+        bad = true;
+        for (int j = i; j < min(i + RING, n_tiles); ++j)
+            mbar_wait(&full[warp][j % RING], (uint32_t)(j / RING) & 1u, nullptr, WAIT_NS / 8);
+    };
+    auto arrived = [&](int i) {
+        return __all_sync(0xffffffffu,
+                          mbar_sleep(&full[warp][i % RING], (uint32_t)(i / RING) & 1u, nullptr, WAIT_NS));
+    };
+    if constexpr (FEW) {
+        // two pages at a time: the four lanes of a quad hold the parts of four
+        // tokens' scores and end up with one token each (d = 128)
+        const int lim = min(seen[0], k1);
+        const bool b0_ = t & 1, b1_ = t & 2;
+        const int my_x = D == 128 ? t >> 1 : t & 1;  // page whose tokens this lane keeps
+        for (int i = 0; i < n_tiles; i += 2) {
+            if (!arrived(i) || (i + 1 < n_tiles && !arrived(i + 1))) {
+                lost(i);
+                break;
+            }
+            const uint8_t *page = ring + (i % RING) * L::BYTES;
+            // ---- S^T = K q, a scale block a column
+            float part[2][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            load_words<KW>(page + L::k_code(tok0 + 2 * r, t, 0), kw[r]);
-            load_words<KW>(page + L::v_code(4 * t + 2 * r, g, 0), vw[r]);
-            if constexpr (FEW)
-                kst[r][0] = *reinterpret_cast<const uint16_t *>(page + L::k_scale(tok0 + 2 * r, (2 * t) % NB));
-            else
+            for (int x = 0; x < 2; ++x) {
+                const uint8_t *pg = page + x * L::BYTES;  // past the last page: whatever the slot holds, masked below
+                uint32_t kw[2][KW], ks[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    load_words<KW>(pg + L::k_code(tok0 + 2 * r, t, 0), kw[r]);
+                    ks[r] = *reinterpret_cast<const uint16_t *>(pg + L::k_scale(tok0 + 2 * r, (2 * t) % NB));
+                }
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t a[2][4];
+                    from_e2m1x8(kw[0][w], a[0]);
+                    from_e2m1x8(kw[1][w], a[1]);
+                    mma_f16(s, a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * w][0], qf[2 * w][1]);
+                    mma_f16(s, a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+                }
+                const float2 f0 = h2f2(from_e4m3x2(ks[0])), f1 = h2f2(from_e4m3x2(ks[1]));
+                part[x][0] = s[0] * f0.x + s[1] * f0.y;
+                part[x][1] = s[2] * f1.x + s[3] * f1.y;
+            }
+            // ---- sum over the blocks of a query: reduce-scatter over its lanes
+            constexpr int M = D == 128 ? 1 : 2;  // tokens this lane ends up with
+            float s[M];
+            {
+                const bool b = my_x != 0;
+                float keep[2], send[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    keep[r] = b ? part[1][r] : part[0][r];
+                    send[r] = b ? part[0][r] : part[1][r];
+                    keep[r] += __shfl_xor_sync(0xffffffffu, send[r], D == 128 ? 2 : 1);
+                }
+                if constexpr (D == 128) {
+                    s[0] = (b0_ ? keep[1] : keep[0]) + __shfl_xor_sync(0xffffffffu, b0_ ? keep[0] : keep[1], 1);
+                } else {
+                    s[0] = keep[0];
+                    s[1] = keep[1];
+                }
+            }
+            // ---- softmax
+            const int base = (b0 + (i + my_x) * WARPS) * 16;
+            const bool edge = (b0 + (i + 1) * WARPS) * 16 + 16 > min(fewest, k1);
+            bool raise = false;
+#pragma unroll
+            for (int j = 0; j < M; ++j) {
+                s[j] *= sc[0];
+                if (edge)
+                    s[j] = base + tok0 + 2 * (D == 128 ? (int)b0_ : j) < lim ? s[j] : -INFINITY;
+                raise |= s[j] > m[0] + RAISE;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+                float mx = M == 2 ? fmaxf(s[0], s[M - 1]) : s[0];
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                if (D == 128)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float mn = fmaxf(m[0], mx), corr = ex2(m[0] - mn);
+                m[0] = mn;
+                l[0] *= corr;
+#pragma unroll
+                for (int w = 0; w < NB; ++w)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[w][j] *= corr;
+            }
+#pragma unroll
+            for (int j = 0; j < M; ++j) {
+                s[j] = ex2(s[j] - m[0]);
+                l[0] += s[j];
+            }
+            // ---- every lane gets the weights of both pages' rows g and g + 8
+            uint32_t pr[2];
+            if constexpr (D == 128) {
+                const uint32_t own = pack_h2(s[0], s[0]);
+                const uint32_t pair = __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, 1), b0_ ? 0x3254 : 0x7610);
+                const uint32_t far = __shfl_xor_sync(0xffffffffu, pair, 2);
+                pr[0] = b1_ ? far : pair;
+                pr[1] = b1_ ? pair : far;
+            } else {
+                const uint32_t own = pack_h2(s[0], s[M - 1]);
+                const uint32_t far = __shfl_xor_sync(0xffffffffu, own, 1);
+                pr[0] = b0_ ? far : own;
+                pr[1] = b0_ ? own : far;
+            }
+            // ---- O^T += V^T P, P times the scales of a column's block
+            uint32_t vw[2][2][KW], pb[2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint8_t *pg = page + x * L::BYTES;
+                const uint32_t vs = *reinterpret_cast<const uint32_t *>(pg + L::v_scale(4 * t, g % NB));
+                load_words<KW>(pg + L::v_code(4 * t, g, 0), vw[x][0]);
+                load_words<KW>(pg + L::v_code(4 * t + 2, g, 0), vw[x][1]);
+                const uint32_t p0 = movmatrix(__byte_perm(pr[x], 0, 0x1010));  // tokens 4t, 4t + 1
+                const uint32_t p1 = movmatrix(__byte_perm(pr[x], 0, 0x3232));  // tokens 4t + 2, 4t + 3
+                pb[x][0] = hmul2(p0, from_e4m3x2(vs & 0xffffu));
+                pb[x][1] = hmul2(p1, from_e4m3x2(vs >> 16));
+                if (edge) {
+                    // a slot that a query does not see may hold anything, a NaN
+                    // scale among it: where P is 0 so is its product
+                    pb[x][0] &= nonzero_mask(p0);
+                    pb[x][1] &= nonzero_mask(p1);
+                }
+            }
+            __syncwarp();  // the slots are read
+            issue(i + RING, i % RING);
+            issue(i + RING + 1, i % RING + 1);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int w = 0; w < KW / 2; ++w) {
+                    uint32_t a[4][4];
+                    pair_tokens<KW>(vw[x], w, a);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb[x][0], pb[x][1]);
+                }
+        }
+    } else {
+        for (int i = 0; i < n_tiles; ++i) {
+            if (!arrived(i)) {
+                lost(i);
+                break;
+            }
+            const int slot = i % RING;
+            const uint8_t *page = ring + slot * L::BYTES;
+            // everything of the page into registers, then the slot is free
+            uint32_t kw[2][KW], vw[2][KW], kst[2][NB / 4], vst[NB];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                load_words<KW>(page + L::k_code(tok0 + 2 * r, t, 0), kw[r]);
+                load_words<KW>(page + L::v_code(4 * t + 2 * r, g, 0), vw[r]);
 #pragma unroll
                 for (int w = 0; w < NB / 4; ++w)
                     kst[r][w] = *reinterpret_cast<const uint32_t *>(page + L::k_scale(tok0 + 2 * r, 4 * w));
-        }
-        if constexpr (FEW)
-            vst[0] = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, g % NB));
-        else
+            }
 #pragma unroll
             for (int w = 0; w < NB; ++w)
                 vst[w] = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, w));
-        __syncwarp();
-        issue(i + RING, slot);
-        if (++slot == RING) {
-            slot = 0;
-            phase ^= 1u;
-        }
+            __syncwarp();
+            issue(i + RING, slot);
 
-        // ---- S^T = K q
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+            // ---- S^T = K q
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            uint32_t a[2][4];
+            for (int w = 0; w < KW; ++w) {
+                uint32_t a[2][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                from_e2m1x8(kw[r][w], a[r]);
-                if constexpr (!FEW) {
+                for (int r = 0; r < 2; ++r) {
+                    from_e2m1x8(kw[r][w], a[r]);
                     const uint32_t two = from_e4m3x2(kst[r][w / 2] >> (16 * (w & 1)));  // blocks 2w, 2w + 1
                     const uint32_t lo = __byte_perm(two, 0, 0x1010), hi = __byte_perm(two, 0, 0x3232);
                     a[r][0] = hmul2(a[r][0], lo);
@@ -293,87 +439,58 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                     a[r][2] = hmul2(a[r][2], hi);
                     a[r][3] = hmul2(a[r][3], hi);
                 }
+                mma_f16(s, a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * w][0], qf[2 * w][1]);
+                mma_f16(s, a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
             }
-            mma_f16(s, a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * w][0], qf[2 * w][1]);
-            mma_f16(s, a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
-        }
-        if constexpr (FEW) {
-            // this lane holds blocks 2t, 2t + 1 (mod NB) of its query for two
-            // tokens; the lanes of the same query hold the rest
-            const float2 f0 = h2f2(from_e4m3x2(kst[0][0])), f1 = h2f2(from_e4m3x2(kst[1][0]));
-            s[0] = s[0] * f0.x + s[1] * f0.y;
-            s[2] = s[2] * f1.x + s[3] * f1.y;
-#pragma unroll
-            for (int x = 1; x < NB / 2; x *= 2) {
-                s[0] += __shfl_xor_sync(0xffffffffu, s[0], x);
-                s[2] += __shfl_xor_sync(0xffffffffu, s[2], x);
-            }
-        }
-        // ---- softmax: rows are tokens, columns queries
-        const int key = (b0 + i * WARPS) * 16 + tok0;
-        bool raise = false;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            s[j] = key < seen[j] ? s[j] * sc[j] : -INFINITY;
-            s[2 + j] = key + 2 < seen[j] ? s[2 + j] * sc[j] : -INFINITY;
-            raise |= fmaxf(s[j], s[2 + j]) > m[j] + RAISE;
-        }
-        if (__any_sync(0xffffffffu, raise)) {
+            // ---- softmax: rows are tokens, columns queries
+            const int key = (b0 + i * WARPS) * 16 + tok0;
+            bool raise = false;
 #pragma unroll
             for (int j = 0; j < Q; ++j) {
-                float mx = fmaxf(s[j], s[2 + j]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float mn = fmaxf(m[j], mx), corr = ex2(m[j] - mn);
-                m[j] = mn;
-                l[j] *= corr;
+                s[j] = key < seen[j] ? s[j] * sc[j] : -INFINITY;
+                s[2 + j] = key + 2 < seen[j] ? s[2 + j] * sc[j] : -INFINITY;
+                raise |= fmaxf(s[j], s[2 + j]) > m[j] + RAISE;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int w = 0; w < NB; ++w) {
-                    o[w][j] *= corr;
-                    o[w][2 + j] *= corr;
-                    if constexpr (FEW) {
-                        o[w][1] *= corr;
-                        o[w][3] *= corr;
+                for (int j = 0; j < Q; ++j) {
+                    float mx = fmaxf(s[j], s[2 + j]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float mn = fmaxf(m[j], mx), corr = ex2(m[j] - mn);
+                    m[j] = mn;
+                    l[j] *= corr;
+#pragma unroll
+                    for (int w = 0; w < NB; ++w) {
+                        o[w][j] *= corr;
+                        o[w][2 + j] *= corr;
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            s[j] = ex2(s[j] - m[j]);
-            s[2 + j] = ex2(s[2 + j] - m[j]);
-            l[j] += s[j] + s[2 + j];
-        }
-        // ---- O^T += V^T P, a V scale times P in place of a scaled V
-        const uint32_t p0 = movmatrix(pack_h2(s[0], s[FEW ? 0 : 1]));  // column g, tokens 4t, 4t + 1
-        const uint32_t p1 = movmatrix(pack_h2(s[2], s[FEW ? 2 : 3]));  // tokens 4t + 2, 4t + 3
-        // a slot that a query does not see may hold anything, a NaN scale
-        // among it: where P is 0 its product with the scale is 0 too
-        const bool edge = (b0 + i * WARPS) * 16 + 16 > fewest;
-        const uint32_t z0 = edge ? nonzero_mask(p0) : 0xffffffffu, z1 = edge ? nonzero_mask(p1) : 0xffffffffu;
-        uint32_t pb[2];
-        if constexpr (FEW) {
-            pb[0] = hmul2(p0, from_e4m3x2(vst[0])) & z0;
-            pb[1] = hmul2(p1, from_e4m3x2(vst[0] >> 16)) & z1;
-        }
-#pragma unroll
-        for (int w = 0; w < KW / 2; ++w) {
-            // bytes of two tokens (channels 2g, 2g + 1) to bytes of two channels
-            uint32_t a[4][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t x = vw[h][w], y = vw[h][KW / 2 + w];
-                from_e2m1x8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), a[2 * h]);
-                from_e2m1x8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), a[2 * h + 1]);
+            for (int j = 0; j < Q; ++j) {
+                s[j] = ex2(s[j] - m[j]);
+                s[2 + j] = ex2(s[2 + j] - m[j]);
+                l[j] += s[j] + s[2 + j];
             }
+            // ---- O^T += V^T P, a V scale times P in place of a scaled V
+            const uint32_t p0 = movmatrix(pack_h2(s[0], s[1]));  // column g, tokens 4t, 4t + 1
+            const uint32_t p1 = movmatrix(pack_h2(s[2], s[3]));  // tokens 4t + 2, 4t + 3
+            // a slot that a query does not see may hold anything, a NaN scale
+            // among it: where P is 0 its product with the scale is 0 too
+            const bool edge = (b0 + i * WARPS) * 16 + 16 > fewest;
+            const uint32_t z0 = edge ? nonzero_mask(p0) : 0xffffffffu, z1 = edge ? nonzero_mask(p1) : 0xffffffffu;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (!FEW) {
-                    pb[0] = hmul2(p0, from_e4m3x2(vst[4 * w + j])) & z0;
-                    pb[1] = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16)) & z1;
+            for (int w = 0; w < KW / 2; ++w) {
+                uint32_t a[4][4];
+                pair_tokens<KW>(vw, w, a);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t pb0 = hmul2(p0, from_e4m3x2(vst[4 * w + j])) & z0;
+                    const uint32_t pb1 = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16)) & z1;
+                    mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb0, pb1);
                 }
-                mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb[0], pb[1]);
             }
         }
     }
@@ -383,6 +500,10 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     float(*s_o)[8][Smem<D>::ROW] = reinterpret_cast<float(*)[8][Smem<D>::ROW]>(smem);
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
+        if (FEW)
+            l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+        if (FEW && D == 128)
+            l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
@@ -508,20 +629,29 @@ struct Split {
     int len, n;
 };
 
-// Keys of a split: as many splits as give every SM work, but at least
-// SPLIT_MIN keys each, a multiple of 16 WARPS.
+// Keys of a split (a multiple of 16 WARPS) and the number of splits: the one
+// with the least estimated time.  An SM shares its throughput among its CTAs
+// and needs three of them to reach it; joining splits takes about as long as an
+// SM takes for 64 pages of a head.
 Split plan_split(long long ctas, int max_keys)
 {
-    const int sms = 152;
-    long long want = (5ll * sms + ctas - 1) / ctas;
+    constexpr int SMS = 152, UNIT = 16 * WARPS;
+    constexpr double FULL = 3, JOIN = 64;
+    Split best{0, 1};
+    double least = 0;
     const long long most = (max_keys + SPLIT_MIN - 1) / SPLIT_MIN;
-    if (want > most)
-        want = most;
-    if (want < 1)
-        want = 1;
-    long long len = (max_keys + want - 1) / want;
-    len = (len + 16 * WARPS - 1) / (16 * WARPS) * (16 * WARPS);
-    return Split{(int)len, (int)((max_keys + len - 1) / len)};
+    for (long long s = 1; s <= most; s += s < 16 ? 1 : s / 8) {
+        const long long len = ((max_keys + s - 1) / s + UNIT - 1) / UNIT * UNIT, n = (max_keys + len - 1) / len;
+        const double per_sm = (double)((ctas * n + SMS - 1) / SMS);
+        const double t = (per_sm > FULL ? per_sm : FULL) * (len / 16) + (n > 1 ? JOIN : 0);
+        if (best.len == 0 || t < least) {
+            best = Split{(int)len, (int)n};
+            least = t;
+        }
+        if (ctas * n > 16ll * SMS)
+            break;
+    }
+    return best;
 }
 
 long long workspace_bytes_of(long long rows, int n_heads, int d, int n_splits)
