@@ -175,28 +175,30 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     uint8_t *ring = smem + warp * RING * L::BYTES;
     bool bad = false;
     int ids = lane < n_tiles ? __ldg(tab + lane * WARPS) : 0;  // lane i: page of tile i of the current 32
-    auto issue = [&](int tile, int slot) {
+    const uint8_t *head = p.pool + (size_t)kvh * L::BYTES;
+    // copy pages tile..tile + N - 1 (tile a multiple of N), lane i the i-th
+    auto issue = [&](int tile, auto n) {
+        constexpr int N = decltype(n)::value;
         if (tile >= n_tiles)
             return;
         if ((tile & 31) == 0 && tile > 0)
             ids = tile + lane < n_tiles ? __ldg(tab + (tile + lane) * WARPS) : 0;
-        const int blk = __shfl_sync(0xffffffffu, ids, tile & 31);
+        const int mine = tile + (lane & (N - 1));
+        const int blk = __shfl_sync(0xffffffffu, ids, mine & 31);
         const bool ok = blk >= 0 && blk < p.num_blocks;
-        bad |= !ok;
-        if (lane == 0) {
+        if (lane < N && mine < n_tiles) {
+            bad |= !ok;
+            uint64_t *bar = &full[warp][mine % RING];
             if (ok) {
-                mbar_expect_tx(&full[warp][slot], L::BYTES);
-                bulk_load(ring + slot * L::BYTES, p.pool + ((size_t)blk * p.n_kv + kvh) * L::BYTES, L::BYTES,
-                          &full[warp][slot]);
+                mbar_expect_tx(bar, L::BYTES);
+                bulk_load(ring + mine % RING * L::BYTES, head + (size_t)blk * (p.n_kv * L::BYTES), L::BYTES, bar);
             } else {
-                mbar_arrive(&full[warp][slot]);  // nothing is read there; what the slot holds is not used
+                mbar_arrive(bar);  // nothing is read there; what the slot holds is not used
             }
         }
     };
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < RING; ++i)
-        issue(i, i);
+    issue(0, std::integral_constant<int, RING>());
 
     // ---- q as B fragments, and what its scores are scaled by
     uint32_t qf[NB][2];
@@ -261,9 +263,11 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         for (int j = i; j < min(i + RING, n_tiles); ++j)
             mbar_wait(&full[warp][j % RING], (uint32_t)(j / RING) & 1u, nullptr, WAIT_NS / 8);
     };
-    auto arrived = [&](int i) {
+    // tile i, or tiles i and i + 1: some lanes look at one, some at the other
+    auto arrived = [&](int i, bool two) {
+        const int mine = i + (two ? lane & 1 : 0);
         return __all_sync(0xffffffffu,
-                          mbar_sleep(&full[warp][i % RING], (uint32_t)(i / RING) & 1u, nullptr, WAIT_NS));
+                          mbar_sleep(&full[warp][mine % RING], (uint32_t)(mine / RING) & 1u, nullptr, WAIT_NS));
     };
     if constexpr (FEW) {
         // two pages at a time: the four lanes of a quad hold the parts of four
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         const bool b0_ = t & 1, b1_ = t & 2;
         const int my_x = D == 128 ? t >> 1 : t & 1;  // page whose tokens this lane keeps
         for (int i = 0; i < n_tiles; i += 2) {
-            if (!arrived(i) || (i + 1 < n_tiles && !arrived(i + 1))) {
+            if (!arrived(i, i + 1 < n_tiles)) {
                 lost(i);
                 break;
             }
@@ -387,8 +391,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 }
             }
             __syncwarp();  // the slots are read
-            issue(i + RING, i % RING);
-            issue(i + RING + 1, i % RING + 1);
+            issue(i + RING, std::integral_constant<int, 2>());
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         }
     } else {
         for (int i = 0; i < n_tiles; ++i) {
-            if (!arrived(i)) {
+            if (!arrived(i, false)) {
                 lost(i);
                 break;
             }
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             for (int w = 0; w < NB; ++w)
                 vst[w] = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, w));
             __syncwarp();
-            issue(i + RING, slot);
+            issue(i + RING, std::integral_constant<int, 1>());
 
             // ---- S^T = K q
             float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -496,6 +499,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     }
 
     // ---- join the warps
+    bad = __any_sync(0xffffffffu, bad);
     __syncthreads();  // the rings are done with
     float(*s_o)[8][Smem<D>::ROW] = reinterpret_cast<float(*)[8][Smem<D>::ROW]>(smem);
 #pragma unroll
