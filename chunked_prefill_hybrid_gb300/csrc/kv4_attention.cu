@@ -122,8 +122,9 @@ struct Smem {
 // columns are then the (query, scale block) pairs: column (c, i) holds query
 // c's block i and zeros elsewhere, so the MMAs give the scores block by block
 // and each is scaled once in fp32 instead of each code's value; and in V^T P
-// column (c, i) holds P times the scales of block i, of which channel block
-// i's MMA uses that column alone, so one B fragment serves every channel.
+// column (c, i) holds P times the scales of block i, for channel block i's MMA
+// alone (zeros for the others'), so that one accumulator of four registers
+// takes every channel.
 template <int D, bool FEW>
 __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const Kv4Attn p)
 {
@@ -248,9 +249,10 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         m[j] = LOWEST;
         l[j] = 0.f;
     }
-    float o[NB][4];
+    constexpr int OT = FEW ? 2 : NB;  // accumulators: one for each page in hand, or for each channel block
+    float o[OT][4];
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < OT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             o[i][j] = 0.f;
@@ -275,6 +277,10 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         const int lim = min(seen[0], k1);
         const bool b0_ = t & 1, b1_ = t & 2;
         const int my_x = D == 128 ? t >> 1 : t & 1;  // page whose tokens this lane keeps
+        uint32_t only[NB];                           // 1 for a column of block i, 0 for the others
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            only[i] = g % NB == i ? 0x3c003c00u : 0u;
         for (int i = 0; i < n_tiles; i += 2) {
             if (!arrived(i, i + 1 < n_tiles)) {
                 lost(i);
@@ -347,10 +353,10 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 m[0] = mn;
                 l[0] *= corr;
 #pragma unroll
-                for (int w = 0; w < NB; ++w)
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        o[w][j] *= corr;
+                        o[x][j] *= corr;
             }
 #pragma unroll
             for (int j = 0; j < M; ++j) {
@@ -400,7 +406,8 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                     pair_tokens<KW>(vw[x], w, a);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb[x][0], pb[x][1]);
+                        mma_f16(o[x], a[0][j], a[1][j], a[2][j], a[3][j], hmul2(pb[x][0], only[4 * w + j]),
+                                hmul2(pb[x][1], only[4 * w + j]));
                 }
         }
     } else {
@@ -520,21 +527,18 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             s_l[warp][myq + j] = l[j];
         }
     }
+    if constexpr (FEW) {
+        // columns 2t and 2t + 1 are two channel blocks of this lane's query
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        if constexpr (FEW) {
-            // of channel block i, column i alone (of each query): 2t or 2t + 1
-            if ((2 * t) % NB == (i & ~1)) {
-                s_o[warp][myq][16 * i + 2 * g] = o[i][i & 1];
-                s_o[warp][myq][16 * i + 2 * g + 1] = o[i][2 + (i & 1)];
-            }
-        } else {
+        for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<float2 *>(&s_o[warp][myq][16 * ((2 * t) % NB + j) + 2 * g]) =
+                make_float2(o[0][j] + o[1][j], o[0][2 + j] + o[1][2 + j]);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                s_o[warp][2 * t + j][16 * i + 2 * g] = o[i][j];
-                s_o[warp][2 * t + j][16 * i + 2 * g + 1] = o[i][2 + j];
-            }
-        }
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<float2 *>(&s_o[warp][2 * t + j][16 * i + 2 * g]) = make_float2(o[i][j], o[i][2 + j]);
     }
     __syncthreads();
     for (int c = c0 + warp; c < c1; c += WARPS) {
