@@ -97,6 +97,18 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
     return r;
 }
 
+// x times the low (high) half of s.
+__device__ __forceinline__ uint32_t mul_lo(uint32_t x, uint32_t s)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __low2half2(*reinterpret_cast<__half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t mul_hi(uint32_t x, uint32_t s)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __high2half2(*reinterpret_cast<__half2 *>(&s)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N])
 {

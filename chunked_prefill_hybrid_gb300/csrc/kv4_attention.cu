@@ -31,7 +31,7 @@ using namespace tc;
 constexpr float RAISE = 7.f;          // P <= 2^7: times a V scale (at most 448) it stays finite in f16
 constexpr int WARPS = 4;
 constexpr int RING = 4;               // pages a warp has in flight
-constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_WARPS = 8;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int SPLIT_MIN = 256;        // keys of a split at least
 constexpr int MAX_KEYS = 1 << 27;
@@ -411,60 +411,70 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 }
         }
     } else {
-        for (int i = 0; i < n_tiles; ++i) {
-            if (!arrived(i, false)) {
+        // two pages at a time, scaled by their blocks' scales
+        for (int i = 0; i < n_tiles; i += 2) {
+            if (!arrived(i, i + 1 < n_tiles)) {
                 lost(i);
                 break;
             }
-            const int slot = i % RING;
-            const uint8_t *page = ring + slot * L::BYTES;
-            // everything of the page into registers, then the slot is free
-            uint32_t kw[2][KW], vw[2][KW], kst[2][NB / 4], vst[NB];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                load_words<KW>(page + L::k_code(tok0 + 2 * r, t, 0), kw[r]);
-                load_words<KW>(page + L::v_code(4 * t + 2 * r, g, 0), vw[r]);
-#pragma unroll
-                for (int w = 0; w < NB / 4; ++w)
-                    kst[r][w] = *reinterpret_cast<const uint32_t *>(page + L::k_scale(tok0 + 2 * r, 4 * w));
-            }
-#pragma unroll
-            for (int w = 0; w < NB; ++w)
-                vst[w] = *reinterpret_cast<const uint32_t *>(page + L::v_scale(4 * t, w));
-            __syncwarp();
-            issue(i + RING, std::integral_constant<int, 1>());
-
+            const uint8_t *page = ring + (i % RING) * L::BYTES;
             // ---- S^T = K q
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[2][4];
 #pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                uint32_t a[2][4];
+            for (int x = 0; x < 2; ++x) {
+                const uint8_t *pg = page + x * L::BYTES;  // past the last page: whatever the slot holds, masked below
+                uint32_t kw[2][KW], kst[2][NB / 4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    from_e2m1x8(kw[r][w], a[r]);
-                    const uint32_t two = from_e4m3x2(kst[r][w / 2] >> (16 * (w & 1)));  // blocks 2w, 2w + 1
-                    const uint32_t lo = __byte_perm(two, 0, 0x1010), hi = __byte_perm(two, 0, 0x3232);
-                    a[r][0] = hmul2(a[r][0], lo);
-                    a[r][1] = hmul2(a[r][1], lo);
-                    a[r][2] = hmul2(a[r][2], hi);
-                    a[r][3] = hmul2(a[r][3], hi);
+                    load_words<KW>(pg + L::k_code(tok0 + 2 * r, t, 0), kw[r]);
+                    if constexpr (NB == 8) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(pg + L::k_scale(tok0 + 2 * r, 0));
+                        kst[r][0] = u.x, kst[r][NB / 4 - 1] = u.y;
+                    } else {
+                        kst[r][0] = *reinterpret_cast<const uint32_t *>(pg + L::k_scale(tok0 + 2 * r, 0));
+                    }
                 }
-                mma_f16(s, a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * w][0], qf[2 * w][1]);
-                mma_f16(s, a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[x][j] = 0.f;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        from_e2m1x8(kw[r][w], a[r]);
+                        const uint32_t two = from_e4m3x2(kst[r][w / 2] >> (16 * (w & 1)));  // blocks 2w, 2w + 1
+                        a[r][0] = mul_lo(a[r][0], two);
+                        a[r][1] = mul_lo(a[r][1], two);
+                        a[r][2] = mul_hi(a[r][2], two);
+                        a[r][3] = mul_hi(a[r][3], two);
+                    }
+                    mma_f16(s[x], a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * w][0], qf[2 * w][1]);
+                    mma_f16(s[x], a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
+                }
             }
             // ---- softmax: rows are tokens, columns queries
             const int key = (b0 + i * WARPS) * 16 + tok0;
+            const bool edge = (b0 + (i + 1) * WARPS) * 16 + 16 > min(fewest, k1);
             bool raise = false;
 #pragma unroll
             for (int j = 0; j < Q; ++j) {
-                s[j] = key < seen[j] ? s[j] * sc[j] : -INFINITY;
-                s[2 + j] = key + 2 < seen[j] ? s[2 + j] * sc[j] : -INFINITY;
-                raise |= fmaxf(s[j], s[2 + j]) > m[j] + RAISE;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    s[x][j] *= sc[j];
+                    s[x][2 + j] *= sc[j];
+                    if (edge) {
+                        const int lim = min(seen[j], k1) - key - x * WARPS * 16;
+                        s[x][j] = lim > 0 ? s[x][j] : -INFINITY;
+                        s[x][2 + j] = lim > 2 ? s[x][2 + j] : -INFINITY;
+                    }
+                }
+                raise |= fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j])) > m[j] + RAISE;
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int j = 0; j < Q; ++j) {
-                    float mx = fmaxf(s[j], s[2 + j]);
+                    float mx = fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -479,27 +489,45 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 }
             }
 #pragma unroll
-            for (int j = 0; j < Q; ++j) {
-                s[j] = ex2(s[j] - m[j]);
-                s[2 + j] = ex2(s[2 + j] - m[j]);
-                l[j] += s[j] + s[2 + j];
-            }
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int j = 0; j < Q; ++j) {
+                    s[x][j] = ex2(s[x][j] - m[j]);
+                    s[x][2 + j] = ex2(s[x][2 + j] - m[j]);
+                    l[j] += s[x][j] + s[x][2 + j];
+                }
             // ---- O^T += V^T P, a V scale times P in place of a scaled V
-            const uint32_t p0 = movmatrix(pack_h2(s[0], s[1]));  // column g, tokens 4t, 4t + 1
-            const uint32_t p1 = movmatrix(pack_h2(s[2], s[3]));  // tokens 4t + 2, 4t + 3
-            // a slot that a query does not see may hold anything, a NaN scale
-            // among it: where P is 0 its product with the scale is 0 too
-            const bool edge = (b0 + i * WARPS) * 16 + 16 > fewest;
-            const uint32_t z0 = edge ? nonzero_mask(p0) : 0xffffffffu, z1 = edge ? nonzero_mask(p1) : 0xffffffffu;
 #pragma unroll
-            for (int w = 0; w < KW / 2; ++w) {
-                uint32_t a[4][4];
-                pair_tokens<KW>(vw, w, a);
+            for (int x = 0; x < 2; ++x) {
+                const uint8_t *pg = page + x * L::BYTES;
+                uint32_t vw[2][KW], vst[NB];
+                load_words<KW>(pg + L::v_code(4 * t, g, 0), vw[0]);
+                load_words<KW>(pg + L::v_code(4 * t + 2, g, 0), vw[1]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t pb0 = hmul2(p0, from_e4m3x2(vst[4 * w + j])) & z0;
-                    const uint32_t pb1 = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16)) & z1;
-                    mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb0, pb1);
+                for (int w = 0; w < NB; ++w)
+                    vst[w] = *reinterpret_cast<const uint32_t *>(pg + L::v_scale(4 * t, w));
+                if (x == 1) {
+                    __syncwarp();  // the slots are read
+                    issue(i + RING, std::integral_constant<int, 2>());
+                }
+                const uint32_t p0 = movmatrix(pack_h2(s[x][0], s[x][Q - 1]));      // column g, tokens 4t, 4t + 1
+                const uint32_t p1 = movmatrix(pack_h2(s[x][2], s[x][2 + Q - 1]));  // tokens 4t + 2, 4t + 3
+                // a slot that a query does not see may hold anything, a NaN
+                // scale among it: where P is 0 so is its product
+                const uint32_t z0 = edge ? nonzero_mask(p0) : 0xffffffffu, z1 = edge ? nonzero_mask(p1) : 0xffffffffu;
+#pragma unroll
+                for (int w = 0; w < KW / 2; ++w) {
+                    uint32_t a[4][4];
+                    pair_tokens<KW>(vw, w, a);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t pb0 = hmul2(p0, from_e4m3x2(vst[4 * w + j])), pb1 = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16));
+                        if (edge) {
+                            pb0 &= z0;
+                            pb1 &= z1;
+                        }
+                        mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb0, pb1);
+                    }
                 }
             }
         }

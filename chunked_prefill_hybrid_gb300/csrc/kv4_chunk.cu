@@ -195,18 +195,6 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b)
     return r;
 }
 
-// x times the low (high) half of s.
-__device__ __forceinline__ uint32_t mul_lo(uint32_t x, uint32_t s)
-{
-    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __low2half2(*reinterpret_cast<__half2 *>(&s)));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t mul_hi(uint32_t x, uint32_t s)
-{
-    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&x), __high2half2(*reinterpret_cast<__half2 *>(&s)));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------- work
