@@ -12,7 +12,7 @@
 namespace hb {
 namespace {
 
-constexpr int CP_VECS = 8;                   // 16-byte loads in flight per lane
+constexpr int CP_VECS = 4;                   // 16-byte loads in flight per lane
 constexpr int CP_UNIT = 32 * CP_VECS * 16;   // bytes a warp copies at a time
 constexpr int CP_WARPS = 8;
 
@@ -23,7 +23,7 @@ struct PagePairs {
     int32_t src[CAP], dst[CAP];
 };
 
-// One warp copies 4 KB of one page of one pool at a time.
+// One warp copies 2 KB of one page of one pool at a time.
 template <int CAP>
 __global__ void __launch_bounds__(CP_WARPS * 32)
     k_copy_pages(const __grid_constant__ PagePairs<CAP> pairs, uint8_t *data, long long pool_stride, int n_pools,
@@ -31,6 +31,8 @@ __global__ void __launch_bounds__(CP_WARPS * 32)
 {
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * CP_WARPS;
+    pdl_wait();
+    pdl_trigger();
     for (long long u = (long long)blockIdx.x * CP_WARPS + (threadIdx.x >> 5); u < units; u += warps) {
         const long long r = u / segs;
         const long long at = (u - r * segs) * CP_UNIT + lane * 16;
@@ -63,7 +65,7 @@ cudaError_t launch_copy(const int32_t *src, const int32_t *dst, int n, uint8_t *
     const long long units = (long long)n * n_pools * segs;
     const long long want = (units + CP_WARPS - 1) / CP_WARPS;
     const unsigned grid = (unsigned)(want < (1 << 20) ? want : (1 << 20));
-    return launch_kernel(false, k_copy_pages<CAP>, dim3(grid), dim3(CP_WARPS * 32), 0, s, pp, data, pool_stride,
+    return launch_kernel(true, k_copy_pages<CAP>, dim3(grid), dim3(CP_WARPS * 32), 0, s, pp, data, pool_stride,
                          n_pools, page_bytes, segs, units);
 }
 

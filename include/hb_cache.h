@@ -77,7 +77,8 @@ long long hb_kv4_pool_bytes(int num_blocks, int n_kv_heads, int head_dim);
  *   slots: device int32 [n_tokens].  A slot outside [0, 16 num_blocks) (-1
  *          marks padding) stores nothing.  Two rows with one slot race: the
  *          slot then holds a mix of the two.
- * Errors: HB_EINVAL (bad argument), HB_ECUDA.  n_tokens = 0 does nothing. */
+ * Errors: HB_EINVAL (bad argument), HB_ERANGE (more work than one
+ * launch holds: n_tokens * n_kv_heads of the order of 10^10), HB_ECUDA.  n_tokens = 0 does nothing. */
 int hb_kv4_append(const hb_kv4_pool *pool, const void *k, long long k_stride, const void *v, long long v_stride,
                   const int32_t *slots, int n_tokens, void *cuda_stream);
 
