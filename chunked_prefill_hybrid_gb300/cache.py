@@ -9,7 +9,6 @@ the library refuses) or ValueError (what only the tensors show).
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -64,67 +63,65 @@ def _check(rc: int, what: str) -> int:
     return rc
 
 
-def _launch(dev: int, stream, fn, *args) -> int:
-    """fn(*args, stream) with the tensors' device current, where its kernels must launch."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _launch(dev, stream, fn, *args)
+def _raw_stream(dev: int, stream) -> int:
     if stream is None:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device.index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
-    return fn(*args, stream.cuda_stream)
+    return stream.cuda_stream
 
 
-def _same_device(dev: int, *tensors):
-    if dev < 0:
-        raise ValueError("the tensors must lie on a CUDA device")
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError("the tensors must lie on one CUDA device")
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits as elsewhere in the package
+_I32 = torch.int32
 
 
-_TWO_BYTES = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits as elsewhere in the package
+def _refuse(rows, ints):
+    """Say what is wrong with a call's tensors: rows of (tensor, name, n, heads, d), ints of (tensor, name, dim, n)."""
+    for t, name, n, heads, d in rows:
+        if t.shape != (n, heads, d):
+            raise ValueError(f"{name} must be [{n}][{heads}][{d}], not {list(t.shape)}")
+        if t.dtype not in _BF16:
+            raise ValueError(f"{name} must be bf16, not {t.dtype}")
+        if t.stride(2) != 1 or (t.stride(1) != d and heads > 1):
+            raise ValueError(f"{name}: the heads of a row must be dense")
+    for t, name, dim, n in ints:
+        if t.dtype != _I32 or t.dim() != dim or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
+        if n >= 0 and t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} rows, not {t.shape[0]}")
+    raise ValueError("the tensors must lie on one CUDA device")
 
 
-def _rows(t, name: str, n: int, heads: int, d: int) -> int:
-    """Row stride of a [n][heads][d] operand whose rows are dense inside."""
-    if t.shape != (n, heads, d):
-        raise ValueError(f"{name} must be [{n}][{heads}][{d}], not {list(t.shape)}")
-    if t.dtype not in _TWO_BYTES:
-        raise ValueError(f"{name} must be bf16, not {t.dtype}")
-    rs, hs, es = t.stride()
-    if es != 1 or (hs != d and heads > 1):
-        raise ValueError(f"{name}: the heads of a row must be dense")
-    return rs if n > 1 else heads * d
-
-
-def _i32(t, name: str, dim: int):
-    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s)")
+# Each call below looks at its tensors in one expression (a call takes some 8 us
+# of host time, half of it here), and says what is wrong in _refuse.  Kernels
+# launch on the current device, so a call on tensors of another one makes that
+# current first.
 
 
 def kv4_pool_bytes(num_blocks: int, n_kv_heads: int, head_dim: int) -> int:
     return _check(_lib().hb_kv4_pool_bytes(num_blocks, n_kv_heads, head_dim), "hb_kv4_pool_bytes")
 
 
-@dataclass(frozen=True, eq=False)
 class Kv4Pool:
     """A pool of the 4-bit cache over a uint8 tensor [num_blocks][n_kv_heads][18 head_dim], whose memory must stay
-    where it is."""
-    data: torch.Tensor
-    k_scale: float = 1.0
-    v_scale: float = 1.0
+    where it is.  Read-only once made."""
+    __slots__ = ("_data", "_c", "_addr", "_dev", "_kv", "_d")
 
-    def __post_init__(self):
-        t = self.data
-        if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous() or t.shape[2] % 18:
+    def __init__(self, data: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        shape = data.shape
+        if data.dtype != torch.uint8 or len(shape) != 3 or shape[2] % 18 or not data.is_contiguous():
             raise ValueError("a 4-bit pool is a contiguous uint8 tensor [num_blocks][n_kv_heads][18 head_dim]")
-        blocks, kv, d = int(t.shape[0]), int(t.shape[1]), int(t.shape[2]) // 18
-        c = _Pool(t.data_ptr(), blocks, kv, d, self.k_scale, self.v_scale)
-        for name, value in (("num_blocks", blocks), ("n_kv_heads", kv), ("head_dim", d), ("c", c),
-                            ("c_addr", ctypes.addressof(c))):
-            object.__setattr__(self, name, value)
+        self._kv, self._d = shape[1], shape[2] // 18
+        self._data, self._dev = data, data.get_device()
+        self._c = _Pool(data.data_ptr(), shape[0], self._kv, self._d, k_scale, v_scale)
+        self._addr = ctypes.addressof(self._c)
+
+    data = property(lambda self: self._data)
+    num_blocks = property(lambda self: self._c.num_blocks)
+    n_kv_heads = property(lambda self: self._kv)
+    head_dim = property(lambda self: self._d)
+    k_scale = property(lambda self: self._c.k_scale)  # as the library uses it, in 32 bits
+    v_scale = property(lambda self: self._c.v_scale)
 
     @classmethod
     def empty(cls, num_blocks: int, n_kv_heads: int, head_dim: int, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -137,27 +134,41 @@ class Kv4Pool:
 
 def kv4_append(pool: Kv4Pool, k, v, slots, stream=None):
     """Quantise rows k, v [n][n_kv_heads][head_dim] into the pool at slots (device int32 [n]; -1 skips a row)."""
-    _i32(slots, "slots", 1)
-    n = slots.shape[0]
-    ks, vs = _rows(k, "k", n, pool.n_kv_heads, pool.head_dim), _rows(v, "v", n, pool.n_kv_heads, pool.head_dim)
-    dev = pool.data.get_device()
-    _same_device(dev, k, v, slots)
-    if n:
-        _check(_launch(dev, stream, _lib().hb_kv4_append, pool.c_addr, k.data_ptr(), ks, v.data_ptr(), vs,
-                       slots.data_ptr(), n), "hb_kv4_append")
+    n, kv, d, dev = slots.shape[0], pool._kv, pool._d, pool._dev
+    if (k.shape != (n, kv, d) or v.shape != (n, kv, d) or k.dtype not in _BF16 or v.dtype not in _BF16
+            or (ks := k.stride())[2] != 1 or (vs := v.stride())[2] != 1 or (kv > 1 and (ks[1] != d or vs[1] != d))
+            or slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous() or dev < 0
+            or k.get_device() != dev or v.get_device() != dev or slots.get_device() != dev):
+        _refuse(((k, "k", n, kv, d), (v, "v", n, kv, d)), ((slots, "slots", 1, n),))
+    if not n:
+        return
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_append(pool, k, v, slots, stream)
+    rc = _lib().hb_kv4_append(pool._addr, k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(), n,
+                              _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "hb_kv4_append")
 
 
 def kv4_read(pool: Kv4Pool, slots, k_out, v_out, stream=None):
     """The values at slots as bf16 rows, into k_out, v_out [n][n_kv_heads][head_dim]."""
-    _i32(slots, "slots", 1)
-    n = slots.shape[0]
-    ks = _rows(k_out, "k_out", n, pool.n_kv_heads, pool.head_dim)
-    vs = _rows(v_out, "v_out", n, pool.n_kv_heads, pool.head_dim)
-    dev = pool.data.get_device()
-    _same_device(dev, k_out, v_out, slots)
-    if n:
-        _check(_launch(dev, stream, _lib().hb_kv4_read, pool.c_addr, slots.data_ptr(), n, k_out.data_ptr(), ks,
-                       v_out.data_ptr(), vs), "hb_kv4_read")
+    n, kv, d, dev = slots.shape[0], pool._kv, pool._d, pool._dev
+    if (k_out.shape != (n, kv, d) or v_out.shape != (n, kv, d) or k_out.dtype not in _BF16 or v_out.dtype not in _BF16
+            or (ks := k_out.stride())[2] != 1 or (vs := v_out.stride())[2] != 1
+            or (kv > 1 and (ks[1] != d or vs[1] != d))
+            or slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous() or dev < 0
+            or k_out.get_device() != dev or v_out.get_device() != dev or slots.get_device() != dev):
+        _refuse(((k_out, "k_out", n, kv, d), (v_out, "v_out", n, kv, d)), ((slots, "slots", 1, n),))
+    if not n:
+        return
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_read(pool, slots, k_out, v_out, stream)
+    rc = _lib().hb_kv4_read(pool._addr, slots.data_ptr(), n, k_out.data_ptr(), ks[0], v_out.data_ptr(), vs[0],
+                            _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "hb_kv4_read")
 
 
 def kv4_decode_workspace(n_decodes: int, n_heads: int, n_kv_heads: int, head_dim: int, max_ctx: int) -> int:
@@ -188,20 +199,28 @@ def kv4_decode(pool: Kv4Pool, q, block_tables, ctx_lens, max_ctx: int, out, work
     current stream)."""
     if q.dim() != 3:
         raise ValueError("q must be [n][n_heads][head_dim]")
-    n, heads, _ = q.shape
-    qs, os_ = _rows(q, "q", n, heads, pool.head_dim), _rows(out, "out", n, heads, pool.head_dim)
-    _i32(block_tables, "block_tables", 2)
-    _i32(ctx_lens, "ctx_lens", 1)
-    if block_tables.shape[0] != n or ctx_lens.shape[0] != n:
-        raise ValueError("block_tables and ctx_lens must have one row for each row of q")
-    dev = pool.data.get_device()
-    _same_device(dev, q, block_tables, ctx_lens, out)
+    n, heads, d = shape = q.shape
+    dev, lens_ok = pool._dev, block_tables.dim() == 2 and ctx_lens.dim() == 1
+    if (d != pool._d or out.shape != shape or q.dtype not in _BF16 or out.dtype not in _BF16
+            or (qs := q.stride())[2] != 1 or (os_ := out.stride())[2] != 1
+            or (heads > 1 and (qs[1] != d or os_[1] != d)) or not lens_ok
+            or block_tables.dtype != _I32 or ctx_lens.dtype != _I32 or block_tables.shape[0] != n
+            or ctx_lens.shape[0] != n or not block_tables.is_contiguous() or not ctx_lens.is_contiguous() or dev < 0
+            or q.get_device() != dev or out.get_device() != dev or block_tables.get_device() != dev
+            or ctx_lens.get_device() != dev):
+        _refuse(((q, "q", n, heads, pool._d), (out, "out", n, heads, pool._d)),
+                ((block_tables, "block_tables", 2, n), (ctx_lens, "ctx_lens", 1, n)))
     if not n:
         return
-    ws = _work(workspace, stream, dev, kv4_decode_workspace, n, heads, pool.n_kv_heads, pool.head_dim, max_ctx)
-    _check(_launch(dev, stream, _lib().hb_kv4_decode, pool.c_addr, q.data_ptr(), qs, block_tables.data_ptr(),
-                   block_tables.shape[1], ctx_lens.data_ptr(), n, heads, max_ctx, out.data_ptr(), os_, ws.data_ptr(),
-                   ws.nbytes), "hb_kv4_decode")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_decode(pool, q, block_tables, ctx_lens, max_ctx, out, workspace, stream)
+    ws = _work(workspace, stream, dev, kv4_decode_workspace, n, heads, pool._kv, d, max_ctx)
+    rc = _lib().hb_kv4_decode(pool._addr, q.data_ptr(), qs[0], block_tables.data_ptr(), block_tables.shape[1],
+                              ctx_lens.data_ptr(), n, heads, max_ctx, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
+                              _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "hb_kv4_decode")
 
 
 def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=None, stream=None):
@@ -209,17 +228,25 @@ def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=N
     workspace: as for kv4_decode, of kv4_chunk_workspace() bytes."""
     if q.dim() != 3:
         raise ValueError("q must be [chunk_len][n_heads][head_dim]")
-    n, heads, _ = q.shape
-    qs, os_ = _rows(q, "q", n, heads, pool.head_dim), _rows(out, "out", n, heads, pool.head_dim)
-    _i32(block_table, "block_table", 1)
-    dev = pool.data.get_device()
-    _same_device(dev, q, block_table, out)
+    n, heads, d = shape = q.shape
+    dev = pool._dev
+    if (d != pool._d or out.shape != shape or q.dtype not in _BF16 or out.dtype not in _BF16
+            or (qs := q.stride())[2] != 1 or (os_ := out.stride())[2] != 1
+            or (heads > 1 and (qs[1] != d or os_[1] != d))
+            or block_table.dtype != _I32 or block_table.dim() != 1 or not block_table.is_contiguous() or dev < 0
+            or q.get_device() != dev or out.get_device() != dev or block_table.get_device() != dev):
+        _refuse(((q, "q", n, heads, pool._d), (out, "out", n, heads, pool._d)), ((block_table, "block_table", 1, -1),))
     if not n:
         return
-    ws = _work(workspace, stream, dev, kv4_chunk_workspace, chunk_offset, n, heads, pool.n_kv_heads, pool.head_dim)
-    _check(_launch(dev, stream, _lib().hb_kv4_chunk, pool.c_addr, q.data_ptr(), qs, block_table.data_ptr(),
-                   block_table.shape[0], chunk_offset, n, heads, out.data_ptr(), os_, ws.data_ptr(), ws.nbytes),
-           "hb_kv4_chunk")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return kv4_chunk(pool, q, block_table, chunk_offset, out, workspace, stream)
+    ws = _work(workspace, stream, dev, kv4_chunk_workspace, chunk_offset, n, heads, pool._kv, d)
+    rc = _lib().hb_kv4_chunk(pool._addr, q.data_ptr(), qs[0], block_table.data_ptr(), block_table.shape[0],
+                             chunk_offset, n, heads, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
+                             _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "hb_kv4_chunk")
 
 
 def _host_pages(a, name: str) -> np.ndarray:
@@ -256,13 +283,19 @@ def copy_pages(pools, src: Sequence[int], dst: Sequence[int], stream=None):
     if not dense or (strides[1] != page and shape[1] > 1):
         raise ValueError("pools must be a tensor [n_pools][num_blocks][...] with the pages of each pool dense")
     dev = pools.get_device()
-    _same_device(dev)
+    if dev < 0:
+        raise ValueError("pools must lie on a CUDA device")
     if not n:
         return
-    page *= pools.element_size()
-    stride = strides[0] * pools.element_size() if shape[0] > 1 else page * shape[1]
-    _check(_launch(dev, stream, _lib().hb_copy_pages, pools.data_ptr(), stride, shape[0], page, shape[1],
-                   _page_addr(s), _page_addr(d), n), "hb_copy_pages")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return copy_pages(pools, s, d, stream)
+    es = pools.element_size()
+    page *= es
+    rc = _lib().hb_copy_pages(pools.data_ptr(), strides[0] * es if shape[0] > 1 else page * shape[1], shape[0], page,
+                              shape[1], _page_addr(s), _page_addr(d), n, _raw_stream(dev, stream))
+    if rc:
+        _check(rc, "hb_copy_pages")
 
 
 def copy_blocks(ctx: "native.Context", src: Sequence[int], dst: Sequence[int]):

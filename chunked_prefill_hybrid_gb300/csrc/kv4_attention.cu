@@ -820,11 +820,8 @@ static double decode_kernel_us(int offset, int len, int group, int n_kv)
 }
 static double tensor_kernel_us(const Kv4Chunk &c)
 {
-    double units = 0;
-    for (int i = 0; i < c.ctas; ++i)
-        units += c.start[i].units;
-    const double items = (double)c.n_qt * c.n_kv, tiles = units / c.ctas;
-    return c.ctas == items ? 8 + 1.25 * tiles : 8 + 1.7 * tiles + 0.7 * (c.ctas / items + 1);
+    const double items = (double)c.n_qt * c.n_kv, tiles = (double)c.units / c.ctas;
+    return !c.shared ? 8 + 1.25 * tiles : 8 + 1.7 * tiles + 0.7 * (c.ctas / items + 1);
 }
 
 // Plan a chunk: 0, `p` filled, as columns of the decode kernel; 1, `c` filled,

@@ -975,35 +975,39 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len)
     // Items of 256 columns convert each key once for both halves; items of 128
     // (both halves on them, on alternate tiles) make more CTAs of the same
     // work and leave fewer partials.  Few units: 128.
-    long long units = 0;
     for (p.rows = 256;; p.rows = 128) {
         p.n_qt = (p.cols + p.rows - 1) / p.rows;
         long long head_units = 0;
         for (int qt = 0; qt < p.n_qt; ++qt)
             head_units += item_tiles(p, qt);
-        units = head_units * p.n_kv;
-        if (p.rows == 128 || units > (long long)DUAL_UNITS * KC_CTAS)
+        p.units = head_units * p.n_kv;
+        if (p.rows == 128 || p.units > (long long)DUAL_UNITS * KC_CTAS)
             break;
     }
-    p.ctas = (int)(units < KC_CTAS ? units : KC_CTAS);
+    p.ctas = (int)(p.units < KC_CTAS ? p.units : KC_CTAS);
     // one CTA per item, if the partials that this saves are worth more than
     // the SMs that it leaves idle
     const long long items = (long long)p.n_qt * p.n_kv;
-    if (items < p.ctas && units / items - units / p.ctas <= WHOLE_TILES)
+    if (items < p.ctas && p.units / items - p.units / p.ctas <= WHOLE_TILES)
         p.ctas = (int)items;
-    if (units / p.ctas >= 0x7fffffff)
+    if (p.units / p.ctas >= 0x7fffffff)
         return false;
     const bool whole = p.ctas == items;
     long long at = 0, item_at = 0;  // first unit of (kvh, qt)
-    int kvh = 0, qt = 0;
+    int kvh = 0, qt = 0, n = item_tiles(p, 0);
+    p.shared = false;
     for (int c = 0; c < p.ctas; ++c) {
-        for (int n; item_at + (n = item_tiles(p, qt)) <= at; item_at += n)
+        while (item_at + n <= at) {
+            item_at += n;
             if (++qt == p.n_qt) {
                 qt = 0;
                 ++kvh;
             }
-        const long long next = whole ? at + item_tiles(p, qt) : units * (c + 1) / p.ctas;
+            n = item_tiles(p, qt);
+        }
+        const long long next = whole ? at + n : p.units * (c + 1) / p.ctas;
         p.start[c] = KcStart{kvh, qt, (int)(at - item_at), (int)(next - at)};
+        p.shared |= at > item_at;
         at = next;
     }
     return true;
@@ -1011,10 +1015,7 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len)
 
 long long kv4_chunk_workspace_bytes(const Kv4Chunk &p, int d)
 {
-    bool parts = false;
-    for (int c = 1; c < p.ctas; ++c)
-        parts |= p.start[c].kt0 > 0;
-    return parts ? 2ll * p.ctas * KC_ROWS * (8 + 4ll * d) : 0;
+    return p.shared ? 2ll * p.ctas * KC_ROWS * (8 + 4ll * d) : 0;
 }
 
 cudaError_t launch_kv4_chunk(const Kv4Chunk &p, int head_dim, cudaStream_t s)

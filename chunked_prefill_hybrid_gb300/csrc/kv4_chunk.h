@@ -31,6 +31,8 @@ struct Kv4Chunk {
     // any other CTA or one more
     int rows;                   // 256, or 128: both halves of a CTA on the same columns, on alternate key tiles
     int n_qt, ctas;             // items of a kv head; CTAs
+    long long units;
+    bool shared;                // some item is shared by several CTAs
     KcStart start[KC_CTAS];
     float *part_o;              // [2 ctas][D / 4][256][4]: CTA c's segment that starts with it, and its last
     float2 *part_ml;            // [2 ctas][256] (m in log2, l)
