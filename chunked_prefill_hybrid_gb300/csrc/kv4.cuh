@@ -160,12 +160,15 @@ __device__ __forceinline__ int query_exponent(float a)
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// mbar_wait for waits that are mostly long: the thread sleeps inside
-// try_wait, up to 20 us at a time, and leaves the issue slots to others.
-__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
+// Wait for the phase of the given parity, asleep inside try_wait (up to some 20
+// us at a time), so that the issue slots are left to others.  Gives up after
+// WAIT_TRIES looks, two seconds or less, or when *abort is set.
+constexpr int WAIT_TRIES = 100000;
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    uint64_t t0 = 0;
-    for (;;) {
+    const uint32_t addr = tc::smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < WAIT_TRIES; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n"
@@ -174,18 +177,14 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity, volat
             "selp.u32 %0, 1, 0, p;\n"
             "}\n"
             : "=r"(ok)
-            : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "r"(addr), "r"(parity), "r"(20000u)
             : "memory");
         if (ok)
             return true;
         if (abort && *abort)
             return false;
-        const uint64_t now = tc::globaltimer_ns();
-        if (t0 == 0)
-            t0 = now;
-        else if (now - t0 > limit_ns)
-            return false;
     }
+    return false;
 }
 
 // 2^x to about 2 ulp (results below 2^-126 are 0).

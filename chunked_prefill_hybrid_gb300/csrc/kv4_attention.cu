@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     auto arrived = [&](int i, bool two) {
         const int mine = i + (two ? lane & 1 : 0);
         return __all_sync(0xffffffffu,
-                          mbar_sleep(&full[warp][mine % RING], (uint32_t)(mine / RING) & 1u, nullptr, WAIT_NS));
+                          mbar_sleep(&full[warp][mine % RING], (uint32_t)(mine / RING) & 1u, nullptr));
     };
     if constexpr (FEW) {
         // two pages at a time: the four lanes of a quad hold the parts of four

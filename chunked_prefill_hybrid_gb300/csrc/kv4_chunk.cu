@@ -47,6 +47,7 @@ constexpr float RAISE = 8.f;             // P <= 2^8
 constexpr int DUAL_UNITS = 8;            // (256 columns x 128 keys) a CTA up to which items have 128 columns
 constexpr int WHOLE_TILES = 12;          // key tiles by which an unshared item may be longer than an even share
 constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr int LOOKS = 1 << 22;           // looks at a barrier before a wait is given up: a second or more
 
 template <int D>
 struct Ck {
@@ -251,11 +252,16 @@ struct Place {
 // that a lane writes in a row lie at four lane constants; everything else is
 // an immediate.  A half-warp's 8-byte stores go to four rows whose swizzles
 // differ (tokens 0, 2, 4, 6 or 1, 3, 5, 7): no bank conflict.
-// The largest of eight bf16 magnitudes, as bits (NaNs count as large).
+// The largest of eight bf16 magnitudes, as bits (above 0x7f80 with a NaN).
 __device__ __forceinline__ uint32_t largest_bits(uint4 u)
 {
-    const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
-    return max(m & 0xffffu, m >> 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+    const uint32_t b = *reinterpret_cast<const uint32_t *>(&m);
+    return max(b & 0xffffu, b >> 16);
 }
 
 template <int D>
@@ -368,16 +374,6 @@ __device__ __noinline__ uint32_t nan_blocks(const Kv4Chunk &p, int kvh, int k0, 
     return m;
 }
 
-// The wait of a whole warp that its first look did not end (one copy of the
-// loop: the roles' code together has to stay in the instruction caches).
-__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
-{
-    if (__all_sync(0xffffffffu, mbar_sleep(bar, parity, abort_flag, WAIT_NS)))
-        return true;
-    *abort_flag = 1;
-    return false;
-}
-
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant__ Kv4Chunk p)
 {
@@ -437,9 +433,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     pdl_trigger();
 
     bool ok = true;
+    // A whole warp's wait, short of code: the roles together have to stay in
+    // the instruction caches.  Plain looks, without a time to sleep: S, P and
+    // the stages are waited for all the time (155 us against 167 for 512 rows
+    // at 15872).
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-            ok = ok && wait_long(bar, parity, abort_flag);
+        int i = 0;
+#pragma unroll 1
+        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+            if (++i == LOOKS || *abort_flag) {
+                *abort_flag = 1;
+                return ok = false;
+            }
         return ok;
     };
 
@@ -462,7 +467,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             const int lr = lane / LPR, lc = lane % LPR;
             float sc = 0.f;
             if (own > 0) {
-                // this warp's 32 rows of Q as f16.  Rows of ordinary size go as
+                // this warp's 32 rows of Q as f16 (past the last column, that
+                // column's again: their results go nowhere).  Rows of ordinary size go as
                 // they are; if any has its largest magnitude outside [2^-6,
                 // 2^15), each is scaled by a power of two into [1, 4) first
                 const long long src = row * p.q_stride + (size_t)head * D;
@@ -471,20 +477,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < N; ++k)
                     u[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, k * RPI + lr)) + lc);
-                bool plain = true;
+                // bit k: some lane of the k-th row has a value of 2^-6 or more;
+                // bit 16 + k: has one that is not 0
+                uint32_t bits = 0, top = 0;
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    if (k * RPI + lr + (warp & 3) * 32 >= valid)
-                        u[k] = make_uint4(0, 0, 0, 0);
                     const uint32_t a = largest_bits(u[k]);
-                    plain = plain && a < 0x4700u;
-                    // a row is small if all of its lanes are
-                    const uint32_t big = __ballot_sync(0xffffffffu, a >= 0x3c80u), any = __ballot_sync(0xffffffffu, a != 0u);
-                    constexpr uint32_t row_mask = LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u;
-#pragma unroll
-                    for (int x = 0; x < RPI; ++x)
-                        plain = plain && ((any >> (x * LPR) & row_mask) == 0u || (big >> (x * LPR) & row_mask) != 0u);
+                    top = max(top, a);
+                    bits |= (a >= 0x3c80u ? 1u << k : 0u) | (a != 0u ? 0x10000u << k : 0u);
                 }
+#pragma unroll
+                for (int x = 1; x < LPR; x *= 2)
+                    bits |= __shfl_xor_sync(0xffffffffu, bits, x);
+                const bool plain = top < 0x4700u && (bits & 0xffffu) == bits >> 16;
                 int e = 0;
                 auto put = [&](uint4 x, int i, float down) {
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -504,9 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 } else {
 #pragma unroll 1
                     for (int i = 0; i < 32; i += RPI) {
-                        uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, i + lr)) + lc);
-                        if (i + lr + (warp & 3) * 32 >= valid)
-                            x = make_uint4(0, 0, 0, 0);
+                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, i + lr)) + lc);
                         uint32_t a = largest_bits(x);
 #pragma unroll
                         for (int k = 1; k < LPR; k *= 2)
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 const long long dst = row * p.out_stride + (size_t)head * D;
                 const int shift = (D == 128 ? 4 : 3) - (dual ? 1 : 0);  // log2 of the 16-byte chunks of a row here
                 const int rl = lane >> shift, cl = (lane & ((1 << shift) - 1)) + c0 / 8;
-#pragma unroll 4
+#pragma unroll 2
                 for (int i = 0; i < 32; i += 32 >> shift) {
                     const long long at = __shfl_sync(0xffffffffu, dst, i + rl);
                     const int rr = (warp & 3) * 32 + i + rl;
@@ -760,20 +763,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             // go as soon as it is filled.
             Place k, v;
             uint32_t n_seg = 0, n_own = 0;  // segments in which this half has rows; its sub-tiles
-            // a busy wait: two warps, and everything waits for them
-            auto spin = [&](uint64_t *bar, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, WAIT_NS));
-                if (!ok)
-                    *abort_flag = 1;
-                return ok;
-            };
             auto pass = [&](Place &at, uint64_t *full, uint64_t *empty) {
                 if (wait(&full[at.st], at.ph) && lane == 0)
                     mbar_arrive(&empty[at.st]);
                 at.next(stages);
             };
             auto issue_s = [&](uint32_t buf) {  // S of the sub-tile at k
-                if (!spin(&k_full[k.st], k.ph))
+                if (!wait(&k_full[k.st], k.ph))
                     return;
                 tc_fence_after();
 #pragma unroll
@@ -810,7 +806,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         pass(v, v_full, v_empty);
                         pv += 2;
                     }
-                    if (!spin(&v_full[v.st], v.ph) || !spin(&p_full[2 * h + buf], (n_own >> 1) & 1u))
+                    if (!wait(&v_full[v.st], v.ph) || !wait(&p_full[2 * h + buf], (n_own >> 1) & 1u))
                         break;
                     tc_fence_after();
                     mma_ts4(O, S + buf * 64, dV + v.st * (C::SUB >> 4), id_o, t);
@@ -850,7 +846,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         atomicMin((int *)bad_key, pg * 16);
                     bool got = true;
                     if (lane < 8 && n >= RING)
-                        got = mbar_sleep(&raw_empty[slot], (n / RING - 1) & 1u, abort_flag, WAIT_NS);
+                        got = mbar_sleep(&raw_empty[slot], (n / RING - 1) & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) {
                         *abort_flag = 1;
                         ok = false;
