@@ -237,7 +237,9 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
 
     // Running reference of the softmax (log2).  It moves only when a score
     // passes it by RAISE: P stays below 2^RAISE, and a tile costs one vote
-    // instead of a maximum over its lanes.
+    // instead of a maximum over its lanes.  Scores may be so large that their
+    // last place is worth more than RAISE: the sum is rounded down, and the
+    // products that are compared are those that the exponent is taken of.
     constexpr int Q = FEW ? 1 : 2;  // queries this lane keeps: its own column's, or columns 2t and 2t + 1
     const int myq = FEW ? (2 * t) / NB : 2 * t;
     float sc[Q], m[Q], l[Q];
@@ -336,10 +338,10 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             bool raise = false;
 #pragma unroll
             for (int j = 0; j < M; ++j) {
-                s[j] *= sc[0];
+                s[j] = __fmul_rn(s[j], sc[0]);
                 if (edge)
                     s[j] = base + tok0 + 2 * (D == 128 ? (int)b0_ : j) < lim ? s[j] : -INFINITY;
-                raise |= s[j] > m[0] + RAISE;
+                raise |= s[j] > __fadd_rd(m[0], RAISE);
             }
             if (__any_sync(0xffffffffu, raise)) {
                 float mx = M == 2 ? fmaxf(s[0], s[M - 1]) : s[0];
@@ -461,15 +463,15 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
             for (int j = 0; j < Q; ++j) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    s[x][j] *= sc[j];
-                    s[x][2 + j] *= sc[j];
+                    s[x][j] = __fmul_rn(s[x][j], sc[j]);
+                    s[x][2 + j] = __fmul_rn(s[x][2 + j], sc[j]);
                     if (edge) {
                         const int lim = min(seen[j], k1) - key - x * WARPS * 16;
                         s[x][j] = lim > 0 ? s[x][j] : -INFINITY;
                         s[x][2 + j] = lim > 2 ? s[x][2 + j] : -INFINITY;
                     }
                 }
-                raise |= fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j])) > m[j] + RAISE;
+                raise |= fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j])) > __fadd_rd(m[j], RAISE);
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -604,13 +606,13 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     }
 }
 
-// Joins the splits of one (row, head): each warp some of them, then the warps
-// in order.
+// Joins the splits of one (row, head): each warp some of them, eight loads of
+// a lane under way at a time, then the warps in order.
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_kv4_join(const Kv4Attn p)
 {
-    constexpr int E = D / 32;
-    __shared__ float s_l[JOIN_WARPS], s_o[JOIN_WARPS][D];
+    constexpr int E = D / 32, BATCH = 8;
+    __shared__ float s_m[JOIN_WARPS], s_l[JOIN_WARPS], s_o[JOIN_WARPS][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
@@ -621,41 +623,60 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_kv4_join(const Kv4Attn p)
     const int n = (nkeys + p.split_len - 1) / p.split_len;
     const float2 *ml = p.part_ml + (size_t)blockIdx.x * p.n_splits;
     const float *po = p.part_o + (size_t)blockIdx.x * p.n_splits * D + lane * E;
-    float M = LOWEST;
-    for (int s = lane; s < n; s += 32)
-        M = fmaxf(M, ml[s].x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    float l = 0.f, o[E];
+    float M = LOWEST, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         o[e] = 0.f;
-#pragma unroll 4
-    for (int s = warp; s < n; s += JOIN_WARPS) {
-        const float2 x = ml[s];
-        const float f = ex2(x.x - M);
-        l += x.y * f;
-        if constexpr (E == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
-            o[0] += v.x * f, o[1] += v.y * f, o[2] += v.z * f, o[3] += v.w * f;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(po + (size_t)s * D);
-            o[0] += v.x * f, o[1] += v.y * f;
+    for (int s0 = warp; s0 < n; s0 += JOIN_WARPS * BATCH) {
+        float2 x[BATCH];
+        float v[BATCH][E];
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int s = min(s0 + i * JOIN_WARPS, n - 1);
+            x[i] = ml[s];
+            if constexpr (E == 4)
+                *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(po + (size_t)s * D);
+            else
+                *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(po + (size_t)s * D);
         }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            top = fmaxf(top, x[i].x);
+        const float corr = ex2(M - top);
+        M = top;
+        l *= corr;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] *= corr;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (s0 + i * JOIN_WARPS < n) {
+                const float f = ex2(x[i].x - M);
+                l += x[i].y * f;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o[e] += v[i][e] * f;
+            }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e)
         s_o[warp][lane * E + e] = o[e];
-    if (lane == 0)
+    if (lane == 0) {
+        s_m[warp] = M;
         s_l[warp] = l;
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < D; e += JOIN_WARPS * 32) {
-        float v = 0.f, lsum = 0.f;
+        float top = LOWEST, v = 0.f, lsum = 0.f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w)
+            top = fmaxf(top, s_m[w]);
 #pragma unroll
         for (int w = 0; w < JOIN_WARPS; ++w) {
-            v += s_o[w][e];
-            lsum += s_l[w];
+            const float f = ex2(s_m[w] - top);
+            v += s_o[w][e] * f;
+            lsum += s_l[w] * f;
         }
         p.out[row * p.out_stride + (size_t)head * D + e] = f2bf(v * (p.vs / lsum));
     }

@@ -11,11 +11,12 @@
 //   warps 0..7    softmax, one thread per query: S from tensor memory, P back
 //                 into it as f16; O is rescaled only when a maximum rises by
 //                 more than 2^8
-//   warps 8..15   codes and scales of one page each -> f16 rows of the K and V
-//                 tiles (128-byte swizzle); code x scale is exact in f16
-//   warps 16, 17  issue the MMAs of the two 128-row halves: S, and O += P V
+//   warps 8..19   three groups of four, a group a sub-tile of 64 keys, a warp a
+//                 page: codes and scales -> f16 rows of the K and V tiles
+//                 (128-byte swizzle); code x scale is exact in f16
+//   warps 20, 21  issue the MMAs of the two 128-row halves: S, and O += P V
 //                 with P read from tensor memory
-//   warp 18       loader: one bulk copy per page (16 keys) into a ring
+//   warp 22       loader: one bulk copy per page (16 keys) into a ring
 //
 // S comes in sub-tiles of 64 keys, two for each half, each in tensor memory of
 // its own: while one is in the softmax the tensor pipe fills the other.  The
@@ -38,12 +39,15 @@ namespace {
 using namespace kv4;
 using namespace tc;
 
-constexpr int THREADS = 20 * 32;
-constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 64;  // 256 and 384 threads: 61440 registers, 96 for each thread at launch
+constexpr int GROUPS = 3;                // of four warps that convert sub-tiles of K and V
+constexpr int MMA_WARP = 8 + 4 * GROUPS;
+constexpr int THREADS = (MMA_WARP + 4) * 32;
+constexpr int REGS_SOFTMAX = 128, REGS_OTHER = 56;  // 256 and 512 threads: 61440 registers, 80 for each thread at launch
 constexpr int RING = 24;                 // pages in flight
 constexpr int STAGES = 3;                // sub-tiles of 64 keys of K, and of V, in f16
 constexpr int STAGES_DUAL = 4;           // the same where both halves share one Q tile
 constexpr float RAISE = 8.f;             // P <= 2^8
+constexpr float HUGE_SCORE = 1 << 20;    // up to it v sc - m may be fused: m is rounded by 2^-4 at most, for all P alike
 constexpr int DUAL_UNITS = 8;            // (256 columns x 128 keys) a CTA up to which items have 128 columns
 constexpr int WHOLE_TILES = 12;          // key tiles by which an unshared item may be longer than an even share
 constexpr uint64_t WAIT_NS = 2000000000ull;
@@ -247,11 +251,6 @@ struct Place {
 
 // ---------------------------------------------------------------- dequant
 
-// K of one page into rows row0.. (a multiple of 16) of a tile.  Lane 4 g + t:
-// tokens tok and tok + 8, channels 4t..4t+3 of every block.  The four chunks
-// that a lane writes in a row lie at four lane constants; everything else is
-// an immediate.  A half-warp's 8-byte stores go to four rows whose swizzles
-// differ (tokens 0, 2, 4, 6 or 1, 3, 5, 7): no bank conflict.
 // The largest of eight bf16 magnitudes, as bits (above 0x7f80 with a NaN).
 __device__ __forceinline__ uint32_t largest_bits(uint4 u)
 {
@@ -264,6 +263,11 @@ __device__ __forceinline__ uint32_t largest_bits(uint4 u)
     return max(b & 0xffffu, b >> 16);
 }
 
+// K of one page into rows row0.. (a multiple of 16) of a tile.  Lane 4 g + t:
+// tokens tok and tok + 8, channels 4t..4t+3 of every block.  The four chunks
+// that a lane writes in a row lie at four lane constants; everything else is
+// an immediate.  A half-warp's 8-byte stores go to four rows whose swizzles
+// differ (tokens 0, 2, 4, 6 or 1, 3, 5, 7): no bank conflict.
 template <int D>
 __device__ __forceinline__ void page_k(const uint8_t *raw, uint8_t *tile, int row0, int lane)
 {
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         *nan_seen = 0;
         fence_mbar_init();
     }
-    if (warp == 16)
+    if (warp == MMA_WARP)
         tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
@@ -531,6 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             }
             const int seen0 = p.offset + (int)(col0 / p.group) + 1;  // of the half's first column
             float m = LOWEST, l = 0.f;
+            float raise_at = LOWEST;  // a maximum above it moves m
             bool fresh = true;  // no O yet
             for (int kt = sg.kt0 + (dual ? half : 0); kt < sg.kt1 && ok; kt += dual ? 2 : 1, ++n_t) {
 #pragma unroll 1
@@ -554,11 +559,25 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
-                    const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sc;
-                    if (__any_sync(0xffffffffu, mx > m + RAISE)) {
+                    const float mx = __fmul_rn(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sc);
+                    float by = sc, off = -m;  // P = 2^(v by + off)
+                    if (__any_sync(0xffffffffu, mx > raise_at)) {
                         const float mn = fmaxf(m, mx), corr = ex2(m - mn);
                         m = mn;
                         l *= corr;
+                        raise_at = m + RAISE;
+                        off = -m;
+                        if (fabsf(m) > HUGE_SCORE) {
+                            // the product rounded as m was, then m off; and here again with every sub-tile
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                v[0][j] = __fmul_rn(v[0][j], sc) - m;
+                                v[1][j] = __fmul_rn(v[1][j], sc) - m;
+                            }
+                            by = 1.f;
+                            off = 0.f;
+                            raise_at = -INFINITY;
+                        }
                         if (!fresh) {  // O holds the products before this one: let the last of them end
                             if (!wait(&pv_done[2 * half + (s ^ 1)], (s ? n_t : n_t - 1) & 1u))
                                 break;
@@ -576,7 +595,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         }
                     }
                     fresh = false;
-                    const uint64_t sc2 = pack_f2(sc, sc), m2 = pack_f2(-m, -m);
+                    const uint64_t sc2 = pack_f2(by, by), m2 = pack_f2(off, off);
                     uint64_t sum2[2] = {0, 0};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -605,10 +624,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             // ---- the segment's result
             if (ok && own > 0 && wait(&pv_done[2 * half + 1], (n_t - 1) & 1u))
                 tc_fence_after();
-            uint32_t nans = 0;
-            if (*nan_seen)
-                nans = nan_blocks<D>(p, sg.kvh, sg.kt0 * KC_KEYS, min(seen, sg.kt1 * KC_KEYS));
-            __syncwarp();
             // with both halves on the same columns, each takes half of the
             // channels and joins the two O there: f, f2 are their factors
             float f = 1.f, f2 = 0.f;
@@ -632,6 +647,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 }
                 ok = ok && !__any_sync(0xffffffffu, *abort_flag);
             }
+            uint32_t nans = 0;
+            if (*nan_seen)  // after the barrier above: the other half's tiles count too
+                nans = nan_blocks<D>(p, sg.kvh, sg.kt0 * KC_KEYS, min(seen, sg.kt1 * KC_KEYS));
+            __syncwarp();
             if (!ok || *bad_key < seen) {  // one table serves every item, so the key found in any of them counts
                 l = __int_as_float(0x7fc00000);
                 m = 0.f;
@@ -705,18 +724,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             if (dual)           // and both halves have read both
                 asm volatile("bar.sync 1, 256;" ::: "memory");
         }
-    } else if (warp < 16) {
+    } else if (warp < MMA_WARP) {
         // -------------------------------------------------------- dequant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        // warps 8..11 take the even sub-tiles, 12..15 the odd ones: a page each
+        // each group of four warps takes every third sub-tile, a warp a page
         const int sub = (warp - 8) >> 2, pg = (warp - 8) & 3;
-        uint32_t j = sub;  // sub-tiles since the start
+        uint32_t j = sub, base = 0;  // sub-tiles since the start: this group's next, and the segment's first
         Place at;
-        if (sub)
+        for (int i = 0; i < sub; ++i)
             at.next(stages);
-        for (; sg.more() && ok; sg.next(p)) {
+        for (; sg.more() && ok; base += 2 * (sg.kt1 - sg.kt0), sg.next(p)) {
             const int keys = sg.keys(p);
-            for (int kt = sg.kt0; kt < sg.kt1 && ok; ++kt, j += 2) {
+            for (; j < base + 2 * (sg.kt1 - sg.kt0) && ok; j += GROUPS) {
                 const uint32_t n = j * 4 + pg, slot = n % RING;  // pages since the start
                 const uint8_t *raw = smem + C::R + slot * C::RAW;
                 if ((j >= stages && !wait(&k_empty[at.st], at.ph ^ 1u)) || !wait(&raw_full[slot], (n / RING) & 1u))
@@ -732,7 +751,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 const uint32_t sb = lane < D / 4 ? *reinterpret_cast<const uint32_t *>(raw + L::VS + 4 * lane) : 0u;
                 uint8_t *V = sV + at.st * C::SUB;
                 if (__any_sync(0xffffffffu, (((sb & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u)) {
-                    if (kt * KC_KEYS + sub * 64 + pg * 16 < keys)
+                    if (sg.kt0 * KC_KEYS + (int)(j - base) * 64 + pg * 16 < keys)
                         *nan_seen = 1;  // or a slot past the last key: the search will tell
                     page_v_scrub<D>(raw, V, pg * 16, lane);
                     __threadfence_block();
@@ -745,15 +764,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                     mbar_arrive(&raw_empty[slot]);
                     mbar_arrive(&v_full[at.st]);
                 }
-                at.next(stages);
-                at.next(stages);
+#pragma unroll
+                for (int i = 0; i < GROUPS; ++i)
+                    at.next(stages);
             }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        if (warp < 18) {
+        if (warp < MMA_WARP + 2) {
             // ---------------------------------------------------- MMA issue
-            const int h = warp - 16;
+            const int h = warp - MMA_WARP;
             const uint32_t id_s = idesc_f16(128, 64, false), id_o = idesc_f16(128, D, true);
             const uint32_t S = tmem + h * C::S_COL, O = tmem + C::O0 + h * C::O_COL;
             const uint64_t dQ = sdesc_kmajor_sw128(smem_u32(smem + C::Q) + (dual ? 0 : h * C::TILE));
@@ -831,7 +851,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 mma_commit_elect(&drain[h]);
                 mbar_wait(&drain[h], 0, nullptr, WAIT_NS / 4);
             }
-        } else if (warp == 18) {
+        } else if (warp == MMA_WARP + 2) {
             // ---------------------------------------------------- loader
             uint32_t it = 0;
             for (; sg.more() && ok; sg.next(p)) {
@@ -871,7 +891,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -909,23 +929,42 @@ __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < G; ++k)
         o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < valid) {
-#pragma unroll 4
-        for (int c = ca; c <= cb; ++c)
-            M = fmaxf(M, ml[(size_t)(c == ca ? first : 2 * c) * KC_ROWS].x);
-#pragma unroll 4
-        for (int c = ca; c <= cb; ++c) {
-            const size_t part = c == ca ? first : 2 * c;
-            const float2 x = ml[part * KC_ROWS];
-            const float f = ex2(x.x - M);
-            l += x.y * f;
+    constexpr int BATCH = 4;
+    if (r < valid)
+        for (int c0 = ca; c0 <= cb; c0 += BATCH) {
+            float2 x[BATCH];
+            float4 v[BATCH][G];
+            float top = M;
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const float4 v = po[(part * (D / 4) + k) * KC_ROWS];
-                o[k].x += v.x * f, o[k].y += v.y * f, o[k].z += v.z * f, o[k].w += v.w * f;
+            for (int i = 0; i < BATCH; ++i) {
+                const int c = min(c0 + i, cb);
+                const size_t part = c == ca ? first : 2 * c;
+                x[i] = ml[part * KC_ROWS];
+#pragma unroll
+                for (int k = 0; k < G; ++k)
+                    v[i][k] = po[(part * (D / 4) + k) * KC_ROWS];
             }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                top = fmaxf(top, x[i].x);
+            const float corr = ex2(M - top);
+            M = top;
+            l *= corr;
+#pragma unroll
+            for (int k = 0; k < G; ++k)
+                o[k].x *= corr, o[k].y *= corr, o[k].z *= corr, o[k].w *= corr;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (c0 + i <= cb) {
+                    const float f = ex2(x[i].x - M);
+                    l += x[i].y * f;
+#pragma unroll
+                    for (int k = 0; k < G; ++k) {
+                        o[k].x += v[i][k].x * f, o[k].y += v[i][k].y * f;
+                        o[k].z += v[i][k].z * f, o[k].w += v[i][k].w * f;
+                    }
+                }
         }
-    }
     const float inv = p.vs / l;
 #pragma unroll
     for (int k = 0; k < G; ++k) {

@@ -314,6 +314,145 @@ def test_chunk_with_a_bad_block():
     assert torch.equal(out, good)
 
 
+# kv heads, group, head size, offset, rows, partials: many rows over many keys, in each way the work is cut (128 or 256
+# columns an item, items whole or shared by several CTAs), with last items of a few columns
+LARGE = [(40, 1, 128, 1000, 130, False), (8, 4, 64, 700, 333, False), (8, 12, 64, 1800, 40, False),
+         (4, 2, 128, 2000, 257, True), (2, 5, 64, 5000, 129, True), (1, 8, 128, 20000, 64, True),
+         (2, 3, 128, 3000, 1500, True), (8, 1, 64, 0, 3000, False), (8, 2, 128, 15000, 130, True),
+         (5, 3, 64, 12001, 301, True)]
+
+
+def _check_rows(got, q64, k, v, offset, rows):
+    for i in rows:
+        o, bound = ref.attention_row(q64[i], k[:offset + i + 1], v[:offset + i + 1])
+        assert (np.abs(got[i] - o) <= bound).all(), (i, np.max(np.abs(got[i] - o) / bound))
+
+
+@pytest.mark.parametrize("kv,group,d,offset,n,shared", LARGE)
+def test_large_chunk(kv, group, d, offset, n, shared):
+    f = Filled([5, offset + n], kv, d, 15, ks=1.25, vs=0.5)
+    heads = kv * group
+    need = cache.kv4_chunk_workspace(offset, n, heads, kv, d)
+    assert (need > 0) == shared
+    wide, q64 = _bf(np.random.default_rng(7).standard_normal((n, heads + 2, d)) * 2)
+    q = wide[:, :heads]
+    ws = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = []
+    for _ in range(3):
+        out = torch.full((n, heads + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        cache.kv4_chunk(f.pool, q, f.dev_tables[1], offset, out[:, :heads], ws)
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    assert (outs[0][:, heads] == 7.0).all() and (ws[need:] == 0xFF).all()
+    k, v = f.kv_of(1, offset + n)
+    _check_rows(_f64(outs[0][:, :heads]), q64[:, :heads], k, v, offset,
+                sorted({0, 1, 127 // group, 128 // group, 255 // group, 256 // group, n // 2, n - 2, n - 1} & set(range(n))))
+
+
+@pytest.mark.parametrize("kv,group,d,offset,n", [(40, 1, 128, 1000, 130), (4, 2, 64, 2000, 257), (8, 2, 128, 15000, 130)])
+def test_large_chunk_sees_nan_and_bad_blocks_where_they_count(kv, group, d, offset, n):
+    f = Filled([offset + n], kv, d, 16)
+    heads = kv * group
+    q, q64 = _bf(np.random.default_rng(9).standard_normal((n, heads, d)))
+    out, good = torch.empty_like(q), torch.empty_like(q)
+    cache.kv4_chunk(f.pool, q, f.dev_tables[0], offset, good)
+    row = torch.ones(1, kv, d, device="cuda").to(torch.bfloat16)
+    nan = row.clone()
+    nan[0, kv - 1, 20] = float("nan")                       # block 1 of the last head
+    mine = slice((kv - 1) * group, heads)
+    held = f.pool.data.clone()
+    # keys of both halves' tiles, the first, and ones that only the chunk's later rows see
+    for key in (3, 130, offset - 1, offset + n // 2, offset + n - 1):
+        first = max(0, key - offset)                        # the first row that sees it
+        slot = torch.tensor([int(f.tables[0, key // 16]) * 16 + key % 16], dtype=torch.int32, device="cuda")
+        for kr, vr in ((row, nan), (nan, row)):
+            f.pool.data.copy_(held)
+            cache.kv4_append(f.pool, kr, vr, slot)
+            for _ in range(3):
+                out.fill_(7.0)
+                cache.kv4_chunk(f.pool, q, f.dev_tables[0], offset, out)
+                assert torch.isfinite(out[:first]).all()
+                assert torch.isnan(out[first:, mine, 16:32]).all(), key
+                if vr is nan:
+                    assert torch.isfinite(out[:, mine, :16]).all() and torch.isfinite(out[:, mine, 32:]).all()
+                else:
+                    assert torch.isnan(out[first:, mine]).all()
+                assert torch.isfinite(out[:, :mine.start]).all()
+        f.pool.data.copy_(held)
+        for bad in (f.pool.num_blocks, -1, 2 ** 31 - 1):
+            tab = f.dev_tables[0].clone()
+            tab[key // 16] = bad
+            cache.kv4_chunk(f.pool, q, tab, offset, out)
+            seen = max(0, key // 16 * 16 - offset)
+            assert torch.isnan(out[seen:]).all() and torch.isfinite(out[:seen]).all(), (key, bad)
+    cache.kv4_chunk(f.pool, q, f.dev_tables[0], offset, out)
+    assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("kv,group,d,offset,n", [(40, 1, 128, 1000, 130), (5, 3, 64, 12001, 301)])
+def test_large_chunk_with_queries_of_any_size(kv, group, d, offset, n):
+    """Rows of every size side by side: each keeps its own precision, and none spoils another."""
+    f = Filled([offset + n], kv, d, 17)
+    heads = kv * group
+    size = np.array([1.0, 0.0, 1e-30, 1e30, 3e4, 1e-4, 30.0])
+    x = np.random.default_rng(10).standard_normal((n, heads, d)) * size[np.arange(n) % 7][:, None, None]
+    x[14, 0, 5], x[21, 0, 6] = np.nan, np.inf
+    q, q64 = _bf(x)
+    out = torch.empty_like(q)
+    cache.kv4_chunk(f.pool, q, f.dev_tables[0], offset, out)
+    got = _f64(out)
+    assert np.isnan(got[14, 0]).all() and np.isnan(got[21, 0]).all()
+    k, v = f.kv_of(0, offset + n)
+    # 1, 0, 1e-30, 1e-4, 30, beside and between the odd ones; the other heads of the odd rows
+    _check_rows(got, q64, k, v, offset, [0, 1, 2, 5, 6, 7, 8, 9, 12, 13, n - n % 7 - 7])
+    for i in (14, 21):
+        o, bound = ref.attention_row(q64[i, group:], k[:offset + i + 1, 1:], v[:offset + i + 1, 1:])
+        assert (np.abs(got[i, group:] - o) <= bound).all()
+    for i in (3, 10):  # the largest score wins by far more than any rounding
+        for h in range(heads):
+            s = k[:offset + i + 1, h // group] @ q64[i, h]
+            top = np.sort(s)[-2:]
+            if top[1] - top[0] > 2.0 ** -16 * (np.abs(k[:offset + i + 1, h // group]) @ np.abs(q64[i, h])).max():
+                o = v[np.argmax(s), h // group]
+                good = np.abs(got[i, h] - o) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(o) + 1e-6
+                assert good.all(), (i, h)
+
+
+def test_captured_large_chunks_replay_on_two_streams():
+    """Chunks of both item sizes in two graphs with workspaces of their own, replayed at once with new queries and
+    another block table; the same answers as calls made one by one."""
+    shapes = [(4, 2, 128, 2000, 257), (5, 3, 64, 12001, 301)]
+    sets, graphs = [], []
+    for kv, group, d, offset, n in shapes:
+        f = Filled([offset + n, offset + n], kv, d, 18)
+        x = dict(q=torch.randn(n, kv * group, d, device="cuda").to(torch.bfloat16), tab=f.dev_tables[0].clone(), offset=offset)
+        x["out"] = torch.empty_like(x["q"])
+        x["ws"] = torch.empty(cache.kv4_chunk_workspace(offset, n, kv * group, kv, d), dtype=torch.uint8, device="cuda")
+        cache.kv4_chunk(f.pool, x["q"], x["tab"], offset, x["out"], x["ws"])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(2):
+                cache.kv4_chunk(f.pool, x["q"], x["tab"], offset, x["out"], x["ws"])
+        sets.append((f, x))
+        graphs.append(g)
+    for f, x in sets:
+        x["q"].copy_(torch.randn_like(x["q"], dtype=torch.float32))
+        x["tab"].copy_(f.dev_tables[1])
+        x["out"].fill_(7.0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for f, x in sets:
+        want = torch.empty_like(x["out"])
+        cache.kv4_chunk(f.pool, x["q"], x["tab"], x["offset"], want, x["ws"])
+        assert torch.equal(want, x["out"])
+
+
 def test_captured_calls_replay_with_new_contents_and_other_streams():
     """A step (append, decode, chunk) in two graphs, each with a workspace of its own, replayed at once on two
     streams with changed inputs; the same answers as calls made one by one."""
