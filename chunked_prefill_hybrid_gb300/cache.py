@@ -9,6 +9,7 @@ the library refuses) or ValueError (what only the tensors show).
 from __future__ import annotations
 
 import ctypes
+from operator import index
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -71,6 +72,14 @@ def _raw_stream(dev: int, stream) -> int:
     return stream.cuda_stream
 
 
+def _int32(x) -> int:
+    """An integer argument of the library (ctypes would cut it to 32 bits without a word)."""
+    x = index(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise HbError(native.HB_ERANGE, f"{x} does not fit 32 bits")
+    return x
+
+
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits as elsewhere in the package
 _I32 = torch.int32
 
@@ -99,7 +108,8 @@ def _refuse(rows, ints):
 
 
 def kv4_pool_bytes(num_blocks: int, n_kv_heads: int, head_dim: int) -> int:
-    return _check(_lib().hb_kv4_pool_bytes(num_blocks, n_kv_heads, head_dim), "hb_kv4_pool_bytes")
+    return _check(_lib().hb_kv4_pool_bytes(_int32(num_blocks), _int32(n_kv_heads), _int32(head_dim)),
+                  "hb_kv4_pool_bytes")
 
 
 class Kv4Pool:
@@ -134,7 +144,7 @@ class Kv4Pool:
 
 def kv4_append(pool: Kv4Pool, k, v, slots, stream=None):
     """Quantise rows k, v [n][n_kv_heads][head_dim] into the pool at slots (device int32 [n]; -1 skips a row)."""
-    n, kv, d, dev = slots.shape[0], pool._kv, pool._d, pool._dev
+    n, kv, d, dev = slots.numel(), pool._kv, pool._d, pool._dev
     if (k.shape != (n, kv, d) or v.shape != (n, kv, d) or k.dtype not in _BF16 or v.dtype not in _BF16
             or (ks := k.stride())[2] != 1 or (vs := v.stride())[2] != 1 or (kv > 1 and (ks[1] != d or vs[1] != d))
             or slots.dtype != _I32 or slots.dim() != 1 or not slots.is_contiguous() or dev < 0
@@ -153,7 +163,7 @@ def kv4_append(pool: Kv4Pool, k, v, slots, stream=None):
 
 def kv4_read(pool: Kv4Pool, slots, k_out, v_out, stream=None):
     """The values at slots as bf16 rows, into k_out, v_out [n][n_kv_heads][head_dim]."""
-    n, kv, d, dev = slots.shape[0], pool._kv, pool._d, pool._dev
+    n, kv, d, dev = slots.numel(), pool._kv, pool._d, pool._dev
     if (k_out.shape != (n, kv, d) or v_out.shape != (n, kv, d) or k_out.dtype not in _BF16 or v_out.dtype not in _BF16
             or (ks := k_out.stride())[2] != 1 or (vs := v_out.stride())[2] != 1
             or (kv > 1 and (ks[1] != d or vs[1] != d))
@@ -172,13 +182,14 @@ def kv4_read(pool: Kv4Pool, slots, k_out, v_out, stream=None):
 
 
 def kv4_decode_workspace(n_decodes: int, n_heads: int, n_kv_heads: int, head_dim: int, max_ctx: int) -> int:
-    return _check(_lib().hb_kv4_decode_workspace(n_decodes, n_heads, n_kv_heads, head_dim, max_ctx),
+    return _check(_lib().hb_kv4_decode_workspace(*map(_int32, (n_decodes, n_heads, n_kv_heads, head_dim, max_ctx))),
                   "hb_kv4_decode_workspace")
 
 
 def kv4_chunk_workspace(chunk_offset: int, chunk_len: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
-    return _check(_lib().hb_kv4_chunk_workspace(chunk_offset, chunk_len, n_heads, n_kv_heads, head_dim),
-                  "hb_kv4_chunk_workspace")
+    return _check(
+        _lib().hb_kv4_chunk_workspace(*map(_int32, (chunk_offset, chunk_len, n_heads, n_kv_heads, head_dim))),
+        "hb_kv4_chunk_workspace")
 
 
 def _work(workspace, stream, dev: int, need, *args):
@@ -217,7 +228,7 @@ def kv4_decode(pool: Kv4Pool, q, block_tables, ctx_lens, max_ctx: int, out, work
             return kv4_decode(pool, q, block_tables, ctx_lens, max_ctx, out, workspace, stream)
     ws = _work(workspace, stream, dev, kv4_decode_workspace, n, heads, pool._kv, d, max_ctx)
     rc = _lib().hb_kv4_decode(pool._addr, q.data_ptr(), qs[0], block_tables.data_ptr(), block_tables.shape[1],
-                              ctx_lens.data_ptr(), n, heads, max_ctx, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
+                              ctx_lens.data_ptr(), n, heads, _int32(max_ctx), out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
                               _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_decode")
@@ -243,7 +254,7 @@ def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=N
             return kv4_chunk(pool, q, block_table, chunk_offset, out, workspace, stream)
     ws = _work(workspace, stream, dev, kv4_chunk_workspace, chunk_offset, n, heads, pool._kv, d)
     rc = _lib().hb_kv4_chunk(pool._addr, q.data_ptr(), qs[0], block_table.data_ptr(), block_table.shape[0],
-                             chunk_offset, n, heads, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
+                             _int32(chunk_offset), n, heads, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
                              _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_chunk")
@@ -313,39 +324,39 @@ class PageTable:
         self.num_blocks = num_blocks
         self.L = _lib()
         h = ctypes.c_void_p()
-        _check(self.L.hb_pages_create(num_blocks, ctypes.byref(h)), "hb_pages_create")
+        _check(self.L.hb_pages_create(_int32(num_blocks), ctypes.byref(h)), "hb_pages_create")
         self.h = h
 
     def extend(self, seq: int, n_tokens: int) -> Optional[Tuple[int, int]]:
         """Grow seq to n_tokens tokens; returns the (source, destination) of the page to copy first, if any."""
         s, d = ctypes.c_int32(), ctypes.c_int32()
-        _check(self.L.hb_pages_extend(self.h, seq, n_tokens, ctypes.addressof(s), ctypes.addressof(d)),
+        _check(self.L.hb_pages_extend(self.h, _int32(seq), _int32(n_tokens), ctypes.addressof(s), ctypes.addressof(d)),
                "hb_pages_extend")
         return (s.value, d.value) if s.value >= 0 else None
 
     def fork(self, parent: int, child: int, n_tokens: int = -1):
         """child shares the pages of parent's first n_tokens tokens (all of them by default)."""
-        _check(self.L.hb_pages_fork(self.h, parent, child, n_tokens), "hb_pages_fork")
+        _check(self.L.hb_pages_fork(self.h, _int32(parent), _int32(child), _int32(n_tokens)), "hb_pages_fork")
 
     def release(self, seq: int):
-        _check(self.L.hb_pages_release(self.h, seq), "hb_pages_release")
+        _check(self.L.hb_pages_release(self.h, _int32(seq)), "hb_pages_release")
 
     def compact(self, max_moves: Optional[int] = None) -> Tuple[np.ndarray, np.ndarray]:
         """(src, dst) of the page moves that bring held pages to the front, for copy_pages."""
-        m = self.num_blocks if max_moves is None else max_moves
+        m = self.num_blocks if max_moves is None else min(index(max_moves), self.num_blocks)
         src, dst = np.empty(max(m, 1), np.int32), np.empty(max(m, 1), np.int32)
         n = _check(self.L.hb_pages_compact(self.h, src.ctypes.data, dst.ctypes.data, m), "hb_pages_compact")
         return src[:n], dst[:n]
 
     def table(self, seq: int) -> np.ndarray:
-        n = _check(self.L.hb_pages_table(self.h, seq, None, 0, None), "hb_pages_table")
+        n = _check(self.L.hb_pages_table(self.h, _int32(seq), None, 0, None), "hb_pages_table")
         out = np.empty(max(n, 1), np.int32)
         _check(self.L.hb_pages_table(self.h, seq, out.ctypes.data, n, None), "hb_pages_table")
         return out[:n]
 
     def length(self, seq: int) -> int:
         n = ctypes.c_int()
-        _check(self.L.hb_pages_table(self.h, seq, None, 0, ctypes.addressof(n)), "hb_pages_table")
+        _check(self.L.hb_pages_table(self.h, _int32(seq), None, 0, ctypes.addressof(n)), "hb_pages_table")
         return n.value
 
     @property
@@ -353,7 +364,7 @@ class PageTable:
         return _check(self.L.hb_pages_num_free(self.h), "hb_pages_num_free")
 
     def refcount(self, block: int) -> int:
-        return _check(self.L.hb_pages_refcount(self.h, block), "hb_pages_refcount")
+        return _check(self.L.hb_pages_refcount(self.h, _int32(block)), "hb_pages_refcount")
 
     def free(self):
         if getattr(self, "h", None):

@@ -729,13 +729,10 @@ bool few(int cols, int d) { return cols <= (d == 128 ? 1 : 2); }
 template <int D, bool FEW>
 cudaError_t launch_d(const Kv4Attn &p, dim3 grid, cudaStream_t s)
 {
-    static std::once_flag once;
-    static cudaError_t set;
-    std::call_once(once, [] {
-        set = cudaFuncSetAttribute(k_kv4_attention<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
-    });
-    if (set != cudaSuccess)
-        return set;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = kv4_allow_smem((const void *)k_kv4_attention<D, FEW>, Smem<D>::BYTES, done);
+    if (e != cudaSuccess)
+        return e;
     return launch_kernel(true, k_kv4_attention<D, FEW>, grid, dim3(WARPS * 32), Smem<D>::BYTES, s, p);
 }
 
@@ -745,7 +742,8 @@ int launch(Kv4Attn &p, int d, int seqs, int rows, cudaStream_t s)
     const bool f = few(cols, d);
     p.col_groups = f ? 1 : (cols + 7) / 8;
     const long long gx = (long long)p.n_splits * p.col_groups * p.n_kv;
-    if (gx > 0x7fffffff)
+    const long long joins = (long long)rows * p.n_heads;
+    if (gx > 0x7fffffff || (p.n_splits > 1 && joins > 0x7fffffff))
         return HB_ERANGE;
     const dim3 grid((unsigned)gx, (unsigned)seqs);
     const cudaError_t e = d == 128 ? (f ? launch_d<128, true>(p, grid, s) : launch_d<128, false>(p, grid, s))
@@ -754,10 +752,7 @@ int launch(Kv4Attn &p, int d, int seqs, int rows, cudaStream_t s)
         return HB_ECUDA;
     if (p.n_splits > 1) {
         auto join = d == 128 ? k_kv4_join<128> : k_kv4_join<64>;
-        const long long blocks = (long long)rows * p.n_heads;
-        if (blocks > 0x7fffffff)
-            return HB_ERANGE;
-        if (launch_kernel(true, join, dim3((unsigned)blocks), dim3(JOIN_WARPS * 32), 0, s, p) != cudaSuccess)
+        if (launch_kernel(true, join, dim3((unsigned)joins), dim3(JOIN_WARPS * 32), 0, s, p) != cudaSuccess)
             return HB_ECUDA;
     }
     return HB_OK;

@@ -27,10 +27,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "kv4.cuh"
 #include "kv4_chunk.h"
+#include "kv4_host.h"
 #include "tc_ptx.cuh"
 
 namespace hb {
@@ -987,14 +986,11 @@ __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ 
 template <int D>
 cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
 {
-    static std::once_flag once;
-    static cudaError_t set;
-    std::call_once(once, [] {
-        set = cudaFuncSetAttribute(k_kv4_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ck<D>::BYTES);
-    });
-    if (set != cudaSuccess)
-        return set;
-    cudaError_t e = launch_kernel(true, k_kv4_chunk<D>, dim3(p.ctas), dim3(THREADS), Ck<D>::BYTES, s, p);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = kv4_allow_smem((const void *)k_kv4_chunk<D>, Ck<D>::BYTES, done);
+    if (e != cudaSuccess)
+        return e;
+    e = launch_kernel(true, k_kv4_chunk<D>, dim3(p.ctas), dim3(THREADS), Ck<D>::BYTES, s, p);
     if (e != cudaSuccess)
         return e;
     if (kv4_chunk_workspace_bytes(p, D) == 0)

@@ -2,17 +2,19 @@
 // each sequence holds, with reference counts, so that a fork shares pages, a
 // write to a shared page copies it first, and compaction moves each page once
 // however many sequences hold it.
+#include <stdint.h>
+
 #include <algorithm>
 #include <map>
 #include <new>
-#include <set>
 #include <vector>
 
 #include "hb_cache.h"
 
 namespace {
 
-constexpr int kPage = 16;  // tokens a page
+constexpr int kPage = 16;                   // tokens a page
+constexpr int kMaxPages = (1 << 27) - 1;    // slots (16 x page + offset) fit 32 bits
 
 struct Seq {
     int n_tokens = 0;
@@ -22,9 +24,28 @@ struct Seq {
 }  // namespace
 
 struct hb_pages {
-    std::vector<int> refs;   // sequences that hold each page
-    std::set<int32_t> free;  // ordered: the lowest id is handed out first
+    std::vector<int> refs;       // sequences that hold each page
+    std::vector<uint64_t> free;  // a bit for each page that none holds
+    size_t first = 0;            // no word before it has a bit set
+    int n_free = 0;
     std::map<int, Seq> seqs;
+
+    void give(int32_t b)
+    {
+        free[b / 64] |= 1ull << (b % 64);
+        first = std::min(first, (size_t)b / 64);
+        ++n_free;
+    }
+    // The lowest free page; there is one.
+    int32_t take()
+    {
+        while (!free[first])
+            ++first;
+        const int bit = __builtin_ctzll(free[first]);
+        free[first] &= free[first] - 1;
+        --n_free;
+        return (int32_t)(first * 64 + bit);
+    }
 };
 
 extern "C" int hb_pages_create(int num_blocks, hb_pages **out)
@@ -32,14 +53,16 @@ extern "C" int hb_pages_create(int num_blocks, hb_pages **out)
     if (!out)
         return HB_EINVAL;
     *out = nullptr;
-    if (num_blocks < 1)
+    if (num_blocks < 1 || num_blocks > kMaxPages)
         return HB_EINVAL;
     hb_pages *p = nullptr;
     try {
         p = new hb_pages();
         p->refs.assign((size_t)num_blocks, 0);
-        for (int32_t b = 0; b < num_blocks; ++b)
-            p->free.insert(p->free.end(), b);
+        p->free.assign(((size_t)num_blocks + 63) / 64, ~0ull);
+        if (num_blocks % 64)
+            p->free.back() = (1ull << (num_blocks % 64)) - 1;
+        p->n_free = num_blocks;
     } catch (...) {
         delete p;
         return HB_ENOMEM;
@@ -66,7 +89,7 @@ extern "C" int hb_pages_extend(hb_pages *p, int seq, int n_tokens, int32_t *copy
         // the first new token's page, if it is part-filled and shared
         const bool copy = n_tokens > have && have % kPage != 0 && p->refs[it->second.pages[held - 1]] > 1;
         const size_t take = want - held + (copy ? 1 : 0);
-        if (take > p->free.size())
+        if (take > (size_t)p->n_free)
             return HB_ENOMEM;
         // everything that may throw comes before the first change
         if (fresh)
@@ -80,8 +103,7 @@ extern "C" int hb_pages_extend(hb_pages *p, int seq, int n_tokens, int32_t *copy
             throw;
         }
         auto next = [&]() {
-            const int32_t b = *p->free.begin();
-            p->free.erase(p->free.begin());
+            const int32_t b = p->take();
             p->refs[b] = 1;
             return b;
         };
@@ -128,21 +150,9 @@ extern "C" int hb_pages_release(hb_pages *p, int seq)
     auto it = p->seqs.find(seq);
     if (it == p->seqs.end())
         return HB_EINVAL;
-    // a page leaves the sequence before it becomes free, so a failed
-    // allocation leaves every count as true as before
-    std::vector<int32_t> &pages = it->second.pages;
-    try {
-        while (!pages.empty()) {
-            const int32_t b = pages.back();
-            if (p->refs[b] == 1)
-                p->free.insert(b);
-            --p->refs[b];
-            pages.pop_back();
-            it->second.n_tokens = std::min(it->second.n_tokens, (int)pages.size() * kPage);
-        }
-    } catch (...) {
-        return HB_ENOMEM;
-    }
+    for (int32_t b : it->second.pages)
+        if (--p->refs[b] == 0)
+            p->give(b);
     p->seqs.erase(it);
     return HB_OK;
 }
@@ -152,30 +162,30 @@ extern "C" int hb_pages_compact(hb_pages *p, int32_t *src, int32_t *dst, int max
     if (!p || max_moves < 0 || (max_moves > 0 && (!src || !dst)))
         return HB_EINVAL;
     try {
-        // what moves: the highest held pages to the lowest free ones.  All
+        // The highest held pages move to the lowest free ones.  All
         // destinations were free and all sources held, so none is both.
         std::vector<int32_t> where(p->refs.size(), -1);
         int n = 0;
         int32_t hi = (int32_t)p->refs.size() - 1;
-        for (auto f = p->free.begin(); f != p->free.end() && n < max_moves; ++f) {
-            while (hi > *f && p->refs[hi] == 0)
+        while (n < max_moves && p->n_free > 0) {
+            while (p->first < p->free.size() && !p->free[p->first])
+                ++p->first;
+            const int32_t lo = (int32_t)(p->first * 64 + __builtin_ctzll(p->free[p->first]));
+            while (hi > lo && p->refs[hi] == 0)
                 --hi;
-            if (hi <= *f)
+            if (hi <= lo)
                 break;
+            p->take();  // lo; what was held above it is given back below
+            p->refs[lo] = p->refs[hi];
+            p->refs[hi] = 0;
             src[n] = hi;
-            dst[n] = *f;
-            where[hi] = *f;
+            dst[n] = lo;
+            where[hi] = lo;
             ++n;
             --hi;
         }
-        // a page's node moves with it inside the set, without allocation
-        for (int i = 0; i < n; ++i) {
-            auto node = p->free.extract(dst[i]);
-            node.value() = src[i];
-            p->free.insert(std::move(node));
-            p->refs[dst[i]] = p->refs[src[i]];
-            p->refs[src[i]] = 0;
-        }
+        for (int i = 0; i < n; ++i)
+            p->give(src[i]);
         for (auto &kv : p->seqs)
             for (int32_t &b : kv.second.pages)
                 if (where[b] >= 0)
@@ -200,7 +210,7 @@ extern "C" int hb_pages_table(hb_pages *p, int seq, int32_t *table, int max_bloc
     return (int)pages.size();
 }
 
-extern "C" int hb_pages_num_free(hb_pages *p) { return p ? (int)p->free.size() : HB_EINVAL; }
+extern "C" int hb_pages_num_free(hb_pages *p) { return p ? p->n_free : HB_EINVAL; }
 
 extern "C" int hb_pages_refcount(hb_pages *p, int block)
 {

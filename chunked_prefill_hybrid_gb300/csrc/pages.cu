@@ -2,7 +2,7 @@
 // fork's copy-on-write and for compaction.
 #include <cuda_runtime.h>
 
-#include <new>
+#include <algorithm>
 #include <vector>
 
 #include "common.cuh"
@@ -15,6 +15,7 @@ namespace {
 constexpr int CP_VECS = 4;                   // 16-byte loads in flight per lane
 constexpr int CP_UNIT = 32 * CP_VECS * 16;   // bytes a warp copies at a time
 constexpr int CP_WARPS = 8;
+constexpr long long MAX_BYTES = 1ll << 47;   // keeps the kernel's arithmetic inside 64 bits
 
 // The page pairs travel as kernel parameters: nothing to stage, to keep
 // alive after the call, or to free, and a captured launch holds its own copy.
@@ -78,16 +79,14 @@ int check_pairs(const int32_t *src, const int32_t *dst, int n, int num_blocks, c
             return HB_ERANGE;
         }
     try {
-        // bit 0: some copy's source, bit 1: some copy's destination
-        std::vector<uint8_t> use((size_t)num_blocks, 0);
-        for (int i = 0; i < n; ++i)
-            use[src[i]] |= 1;
-        for (int i = 0; i < n; ++i) {
-            if (use[dst[i]]) {
-                *why = "a destination page is repeated, or is also a source";
-                return HB_EINVAL;
-            }
-            use[dst[i]] = 2;
+        std::vector<int32_t> to(dst, dst + n);
+        std::sort(to.begin(), to.end());
+        bool bad = std::adjacent_find(to.begin(), to.end()) != to.end();
+        for (int i = 0; i < n && !bad; ++i)
+            bad = std::binary_search(to.begin(), to.end(), src[i]);
+        if (bad) {
+            *why = "a destination page is repeated, or is also a source";
+            return HB_EINVAL;
         }
     } catch (...) {
         *why = "no host memory";
@@ -121,10 +120,12 @@ extern "C" int hb_copy_pages(void *data, long long pool_stride, int n_pools, lon
                              const int32_t *src, const int32_t *dst, int n, void *cuda_stream)
 {
     if (!data || n < 0 || n_pools < 1 || num_blocks < 1 || page_bytes < 16 || page_bytes % 16 || pool_stride % 16 ||
-        (uintptr_t)data % 16 || page_bytes > (1ll << 40) || (n > 0 && (!src || !dst)))
+        (uintptr_t)data % 16 || (n > 0 && (!src || !dst)))
         return HB_EINVAL;
-    if (n_pools > 1 && pool_stride < page_bytes * num_blocks)
-        return HB_EINVAL;  // pools would overlap
+    // no pool is larger than the address space, and none overlaps the next
+    if (page_bytes > MAX_BYTES / num_blocks ||
+        (n_pools > 1 && (pool_stride < page_bytes * num_blocks || pool_stride > MAX_BYTES / n_pools)))
+        return HB_EINVAL;
     const char *why = nullptr;
     const int rc = check_pairs(src, dst, n, num_blocks, &why);
     if (rc)

@@ -78,7 +78,8 @@ long long hb_kv4_pool_bytes(int num_blocks, int n_kv_heads, int head_dim);
  *          marks padding) stores nothing.  Two rows with one slot race: the
  *          slot then holds a mix of the two.
  * Errors: HB_EINVAL (bad argument), HB_ERANGE (more work than one
- * launch holds: n_tokens * n_kv_heads of the order of 10^10), HB_ECUDA.  n_tokens = 0 does nothing. */
+ * launch holds: n_tokens * n_kv_heads of the order of 10^10), HB_ECUDA.
+ * n_tokens = 0 does nothing. */
 int hb_kv4_append(const hb_kv4_pool *pool, const void *k, long long k_stride, const void *v, long long v_stride,
                   const int32_t *slots, int n_tokens, void *cuda_stream);
 
@@ -111,7 +112,8 @@ int hb_kv4_read(const hb_kv4_pool *pool, const int32_t *slots, int n_tokens, voi
  * results of differently shaped calls agree to fp32 rounding, not bit for
  * bit; one call repeated gives the same bits.
  * Errors: HB_EINVAL, HB_ERANGE (bt_stride too small, workspace too small, more
- * than 65535 rows, or max_ctx above 2^27), HB_ECUDA.  n_decodes = 0 does nothing. */
+ * than 65535 rows, or max_ctx of 2^27 or more), HB_ECUDA.  n_decodes = 0 does
+ * nothing. */
 int hb_kv4_decode(const hb_kv4_pool *pool, const void *q, long long q_stride, const int32_t *block_tables,
                   int bt_stride, const int32_t *ctx_lens, int n_decodes, int n_heads, int max_ctx, void *out,
                   long long out_stride, void *workspace, long long workspace_bytes, void *cuda_stream);
@@ -127,7 +129,8 @@ long long hb_kv4_decode_workspace(int n_decodes, int n_heads, int n_kv_heads, in
  *                attend to it NaN (and may make other rows of the chunk NaN)
  * Workspace, errors and rounding as for hb_kv4_decode; chunk_offset +
  * chunk_len is at most 2^27, chunk_len times the heads of a kv head at most
- * 2^24 (HB_ERANGE).  chunk_len = 0 does nothing. */
+ * 2^24 (HB_ERANGE, also for a chunk of more work than a launch can count, of
+ * the order of 10^18 scores).  chunk_len = 0 does nothing. */
 int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_stride, const int32_t *block_table, int n_blocks,
                  int chunk_offset, int chunk_len, int n_heads, void *out, long long out_stride, void *workspace,
                  long long workspace_bytes, void *cuda_stream);
@@ -138,7 +141,8 @@ long long hb_kv4_chunk_workspace(int chunk_offset, int chunk_len, int n_heads, i
  * Copy page src[i] to page dst[i], i < n, in each of n_pools pools: pool p's
  * page b is the page_bytes bytes at data + p * pool_stride + b * page_bytes.
  * A pool is any array of pages (a bf16 K or V pool of a layer, an hb_kv4_pool),
- * device memory; data, pool_stride and page_bytes are multiples of 16.
+ * device memory; data, pool_stride and page_bytes are multiples of 16, and no
+ * pool reaches into the next.
  *   src, dst: host int32 [n], in [0, num_blocks); read during the call.  A
  *             page may be the source of several copies (forks), but a
  *             destination may be neither repeated nor a source of the same
@@ -161,7 +165,8 @@ int hb_copy_blocks(hb_ctx *ctx, const int32_t *src, const int32_t *dst, int n);
  * host memory of the caller. */
 typedef struct hb_pages hb_pages;
 
-/* A table of num_blocks free pages of 16 tokens.  HB_EINVAL, HB_ENOMEM. */
+/* A table of num_blocks free pages of 16 tokens (at most 2^27 - 1, as many as
+ * a pool of the 4-bit cache may have).  HB_EINVAL, HB_ENOMEM. */
 int hb_pages_create(int num_blocks, hb_pages **out);
 void hb_pages_destroy(hb_pages *p);
 

@@ -235,6 +235,45 @@ def test_page_table_refusals(L):
     assert t.length(2) == 0
 
 
+def test_large_tables_cost_little(L):
+    """Free pages are a bit each; pairs are checked without a look at the pages that they do not name."""
+    with pytest.raises(HbError):
+        cache.PageTable(1 << 27)
+    t = cache.PageTable((1 << 27) - 1)
+    assert t.extend(1, 33) is None and t.table(1).tolist() == [0, 1, 2] and t.num_free == (1 << 27) - 4
+    t.free()
+    for n in (63, 64, 65, 200):                              # every page, whatever the last word holds
+        t = cache.PageTable(n)
+        t.extend(1, 16 * n)
+        assert t.table(1).tolist() == list(range(n)) and t.num_free == 0
+        with pytest.raises(HbError):
+            t.extend(2, 1)
+        assert t.compact()[0].size == 0
+        t.release(1)
+        assert t.num_free == n
+    assert _copy(L, _i32(1, 5), _i32(2, 1), nb=1 << 20, stride=256 << 20) == HB_EINVAL
+    for over in (dict(page=1 << 47), dict(page=1 << 40, nb=1 << 20), dict(stride=1 << 60), dict(stride=1 << 46, pools=4)):
+        assert _copy(L, _i32(1), _i32(2), **over) == HB_EINVAL, over
+
+
+def test_numbers_past_32_bits_are_refused_not_cut(L):
+    t = cache.PageTable(4)
+    t.extend(1, 20)
+    big = 1 << 32
+    for bad in (lambda: cache.PageTable(big + 4), lambda: t.extend(big + 1, 30), lambda: t.extend(1, big + 30),
+                lambda: t.fork(1, big + 2), lambda: t.fork(big + 1, 2), lambda: t.release(big + 1),
+                lambda: t.table(big + 1), lambda: t.length(big + 1), lambda: t.refcount(big),
+                lambda: cache.kv4_pool_bytes(big + 3, 5, 128), lambda: cache.kv4_decode_workspace(4, 4, 2, 64, big),
+                lambda: cache.kv4_chunk_workspace(big, 4, 4, 2, 64)):
+        with pytest.raises(HbError) as e:
+            bad()
+        assert e.value.code == HB_ERANGE
+    assert t.length(np.int64(1)) == 20 and t.table(np.int32(1)).tolist() == [0, 1]
+    assert t.compact(1 << 40)[0].size == 0
+    with pytest.raises(TypeError):
+        t.extend(1, 30.5)
+
+
 def test_binding_checks_tensors(L):
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError):
