@@ -505,6 +505,39 @@ def test_captured_calls_replay_with_new_contents_and_other_streams():
         assert torch.equal(x["od"], od) and torch.equal(x["oc"], oc)
 
 
+@pytest.mark.parametrize("kv,d", [(8, 128), (16, 64)])
+def test_pages_past_four_gigabytes(kv, d):
+    """The same rows in the low pages of one pool and in the last pages of one of 5 GB: the same bytes, the same
+    answers, and pages copied from one end to the other."""
+    n, heads, blocks = 2200, 2 * kv, 5 * (1 << 30) // (kv * 18 * d)
+    need = (n + 15) // 16
+    big = torch.empty(blocks, kv, 18 * d, dtype=torch.uint8, device="cuda")
+    pools = [cache.Kv4Pool.empty(need, kv, d), cache.Kv4Pool(big)]
+    assert big.numel() > 1 << 32
+    tabs = [torch.arange(need, dtype=torch.int32, device="cuda")]
+    tabs.append(blocks - 1 - tabs[0])
+    big[tabs[1].long()] = 0
+    k, v = (torch.randn(n, kv, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(n, heads, d, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(n, device="cuda")
+    lens = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    got = []
+    for pool, tab in zip(pools, tabs):
+        slots = (tab.long()[pos // 16] * 16 + pos % 16).to(torch.int32)
+        cache.kv4_append(pool, k, v, slots)
+        o = [torch.empty_like(k), torch.empty_like(v), torch.empty_like(q[:1]), torch.empty_like(q[:3]), torch.empty_like(q[:900])]
+        cache.kv4_read(pool, slots, o[0], o[1])
+        cache.kv4_decode(pool, q[:1], tab[None], lens, n - 1, o[2])
+        for chunk in (3, 900):                              # few rows, and many
+            cache.kv4_chunk(pool, q[:chunk], tab, n - chunk, o[3 if chunk == 3 else 4])
+        got.append(o)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.equal(big[tabs[1].long()], pools[0].data)
+    cache.copy_pages(big[None], [blocks - 1, blocks - 2], [0, 1])
+    assert torch.equal(big[:2], pools[0].data[:2])
+
+
 def test_binding_refuses_what_it_cannot_order():
     f = Filled([300], 1, 64, 14)
     q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
