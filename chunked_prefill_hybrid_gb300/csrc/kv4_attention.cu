@@ -32,6 +32,7 @@ constexpr float RAISE = 7.f;          // P <= 2^7: times a V scale (at most 448)
 constexpr int WARPS = 4;
 constexpr int RING = 4;               // pages a warp has in flight
 constexpr int JOIN_WARPS = 8;
+constexpr int SMS = 152;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int SPLIT_MIN = 256;        // keys of a split at least
 constexpr int MAX_KEYS = 1 << 27;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     __shared__ uint64_t full[WARPS][RING];
     __shared__ float s_scale[8], s_m[WARPS][8], s_l[WARPS][8];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.n_splits;
     const int rest = blockIdx.x / p.n_splits;
@@ -692,7 +693,7 @@ struct Split {
 // SM takes for 64 pages of a head.
 Split plan_split(long long ctas, int max_keys)
 {
-    constexpr int SMS = 152, UNIT = 16 * WARPS;
+    constexpr int UNIT = 16 * WARPS;
     constexpr double FULL = 3, JOIN = 64;
     Split best{0, 1};
     double least = 0;
@@ -729,11 +730,16 @@ bool few(int cols, int d) { return cols <= (d == 128 ? 1 : 2); }
 template <int D, bool FEW>
 cudaError_t launch_d(const Kv4Attn &p, dim3 grid, cudaStream_t s)
 {
+    // Six CTAs fit an SM.  Where five on each hold the whole grid they lie
+    // more evenly with no room for a sixth: 720 CTAs (18 rows of 1024 keys, 40
+    // heads) take 23.3 us so and 25.9 with room; 5120 (128 rows) 95.7 and 94.1.
+    constexpr int PAD = FEW && D == 128 ? 1024 : 0;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = kv4_allow_smem((const void *)k_kv4_attention<D, FEW>, Smem<D>::BYTES, done);
+    const cudaError_t e = kv4_allow_smem((const void *)k_kv4_attention<D, FEW>, Smem<D>::BYTES + PAD, done);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(true, k_kv4_attention<D, FEW>, grid, dim3(WARPS * 32), Smem<D>::BYTES, s, p);
+    const int bytes = Smem<D>::BYTES + ((long long)grid.x * grid.y <= 5 * SMS ? PAD : 0);
+    return launch_kernel(true, k_kv4_attention<D, FEW>, grid, dim3(WARPS * 32), bytes, s, p);
 }
 
 int launch(Kv4Attn &p, int d, int seqs, int rows, cudaStream_t s)

@@ -65,7 +65,7 @@ struct Ck {
     static_assert(K_DUAL + 2 * STAGES_DUAL * SUB <= R);
     static constexpr int BAR = R + RING * RAW;
     static constexpr int BYTES = BAR + 1024 + 2048 + 1024;  // barriers, (m, l) pairs, alignment
-    static constexpr uint32_t S_COL = 128, O0 = 256, O_COL = D;
+    static constexpr uint32_t S_COL = 128, O0 = 256, O_COL = D;  // S: 64 columns for each (half, buffer)
 };
 
 // byte offset of (row, 16-byte chunk c) in a 128-byte-swizzled column block
@@ -220,13 +220,14 @@ struct Segments {
         if (left > 0)
             size(p);
     }
-    // key tiles of half h: all of the segment's, or (both halves on the same
-    // columns) every other one
-    __device__ int tiles_of(const Kv4Chunk &p, int h) const
+    // 64-key sub-tiles: of the segment, and of half h: all of them, or (both
+    // halves on the same columns) every other one
+    __device__ int subs() const { return 2 * (kt1 - kt0); }
+    __device__ int subs_of(const Kv4Chunk &p, int h) const
     {
         if (p.rows == 128)
-            return (kt1 - kt0 - h + 1) >> 1;
-        return h == 0 || p.cols - (long long)qt * KC_ROWS > 128 ? kt1 - kt0 : 0;
+            return kt1 - kt0;
+        return h == 0 || p.cols - (long long)qt * KC_ROWS > 128 ? subs() : 0;
     }
     // keys that the item's last column sees
     __device__ int keys(const Kv4Chunk &p) const
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     const bool dual = p.rows == 128;
     const uint32_t stages = dual ? STAGES_DUAL : STAGES;
     uint8_t *sK = smem + (dual ? C::K_DUAL : C::K), *sV = sK + stages * C::SUB;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(&raw_full[i], 1);
@@ -407,9 +408,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         }
         for (int i = 0; i < STAGES_DUAL; ++i) {
             mbar_init(&k_full[i], 4);
-            mbar_init(&k_empty[i], 2);
+            mbar_init(&k_empty[i], dual ? 1 : 2);
             mbar_init(&v_full[i], 4);
-            mbar_init(&v_empty[i], 2);
+            mbar_init(&v_empty[i], dual ? 1 : 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;  // all 512 columns: they begin at 0
     Segments sg(p, blockIdx.x);
     pdl_wait();
     pdl_trigger();
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         int i = 0;
 #pragma unroll 1
         while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-            if (++i == LOOKS || *abort_flag) {
+            if (++i == LOOKS || __any_sync(0xffffffffu, *abort_flag)) {
                 *abort_flag = 1;
                 return ok = false;
             }
@@ -457,9 +458,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t sT = lanes + half * C::S_COL, oT = lanes + C::O0 + half * C::O_COL;
-        uint32_t n_t = 0;  // key tiles this half has been through
+        uint32_t n = 0;  // sub-tiles this half has been through
         for (; sg.more(); sg.next(p)) {
-            const int own = sg.tiles_of(p, half);
+            const int own = sg.subs_of(p, half);
             const long long col0 = (long long)sg.qt * p.rows + (dual ? 0 : half * 128);
             const int valid = (int)min(128ll, p.cols - col0);  // columns of this half (<= 0 if it has none)
             const long long col = min(col0 + r, (long long)p.cols - 1);
@@ -536,98 +537,97 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             float m = LOWEST, l = 0.f;
             float raise_at = LOWEST;  // a maximum above it moves m
             bool fresh = true;  // no O yet
-            for (int kt = sg.kt0 + (dual ? half : 0); kt < sg.kt1 && ok; kt += dual ? 2 : 1, ++n_t) {
 #pragma unroll 1
-                for (int s = 0; s < 2; ++s) {
-                    if (!wait(&s_full[2 * half + s], n_t & 1u))
-                        break;
-                    tc_fence_after();
-                    const int lim = seen - kt * KC_KEYS - s * 64;           // keys of the 64 this row sees
-                    const bool edge = seen0 < kt * KC_KEYS + s * 64 + 64;   // some row does not see them all
-                    float v[2][32];
-                    tmem_ld_x32(sT + s * 64, v[0]);
-                    tmem_ld_x32(sT + s * 64 + 32, v[1]);
-                    tmem_ld_wait();
-                    if (edge)
+            for (int i = 0; i < own; ++i, ++n) {
+                const uint32_t buf = n & 1u;
+                if (!wait(&s_full[2 * half + buf], (n >> 1) & 1u))
+                    break;
+                tc_fence_after();
+                const int key = sg.kt0 * KC_KEYS + (dual ? 2 * i + half : i) * 64;
+                const int lim = seen - key;          // keys of the 64 this row sees
+                const bool edge = seen0 < key + 64;  // some row does not see them all
+                float v[2][32];
+                tmem_ld_x32(sT + buf * 64, v[0]);
+                tmem_ld_x32(sT + buf * 64 + 32, v[1]);
+                tmem_ld_wait();
+                if (edge)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        v[0][j] = j < lim ? v[0][j] : -INFINITY;
+                        v[1][j] = 32 + j < lim ? v[1][j] : -INFINITY;
+                    }
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
+                const float mx = __fmul_rn(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sc);
+                float by = sc, off = -m;  // P = 2^(v by + off)
+                if (__any_sync(0xffffffffu, mx > raise_at)) {
+                    const float mn = fmaxf(m, mx), corr = ex2(m - mn);
+                    m = mn;
+                    l *= corr;
+                    raise_at = m + RAISE;
+                    off = -m;
+                    if (fabsf(m) > HUGE_SCORE) {
+                        // the product rounded as m was, then m off; and here again with every sub-tile
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            v[0][j] = j < lim ? v[0][j] : -INFINITY;
-                            v[1][j] = 32 + j < lim ? v[1][j] : -INFINITY;
+                            v[0][j] = __fmul_rn(v[0][j], sc) - m;
+                            v[1][j] = __fmul_rn(v[1][j], sc) - m;
                         }
-                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
-                    const float mx = __fmul_rn(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sc);
-                    float by = sc, off = -m;  // P = 2^(v by + off)
-                    if (__any_sync(0xffffffffu, mx > raise_at)) {
-                        const float mn = fmaxf(m, mx), corr = ex2(m - mn);
-                        m = mn;
-                        l *= corr;
-                        raise_at = m + RAISE;
-                        off = -m;
-                        if (fabsf(m) > HUGE_SCORE) {
-                            // the product rounded as m was, then m off; and here again with every sub-tile
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                v[0][j] = __fmul_rn(v[0][j], sc) - m;
-                                v[1][j] = __fmul_rn(v[1][j], sc) - m;
-                            }
-                            by = 1.f;
-                            off = 0.f;
-                            raise_at = -INFINITY;
-                        }
-                        if (!fresh) {  // O holds the products before this one: let the last of them end
-                            if (!wait(&pv_done[2 * half + (s ^ 1)], (s ? n_t : n_t - 1) & 1u))
-                                break;
-                            tc_fence_after();
+                        by = 1.f;
+                        off = 0.f;
+                        raise_at = -INFINITY;
+                    }
+                    if (!fresh) {  // O holds the products before this one: let the last of them end
+                        if (!wait(&pv_done[2 * half + (buf ^ 1u)], ((n - 1) >> 1) & 1u))
+                            break;
+                        tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                float y[16];
-                                tmem_ld_x16(oT + c, y);
-                                tmem_ld_wait();
+                        for (int c = 0; c < D; c += 16) {
+                            float y[16];
+                            tmem_ld_x16(oT + c, y);
+                            tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    y[j] *= corr;
-                                tmem_st_x16(oT + c, reinterpret_cast<uint32_t(&)[16]>(y));
-                            }
+                            for (int j = 0; j < 16; ++j)
+                                y[j] *= corr;
+                            tmem_st_x16(oT + c, reinterpret_cast<uint32_t(&)[16]>(y));
                         }
                     }
-                    fresh = false;
-                    const uint64_t sc2 = pack_f2(by, by), m2 = pack_f2(off, off);
-                    uint64_t sum2[2] = {0, 0};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t ph[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float a, b;
-                            unpack_f2(fma_f2(pack_f2(v[k][2 * j], v[k][2 * j + 1]), sc2, m2), a, b);
-                            a = ex2(a);
-                            b = ex2(b);
-                            sum2[j & 1] = add_f2(sum2[j & 1], pack_f2(a, b));
-                            ph[j] = pack_h2(a, b);
-                        }
-                        tmem_st_x16(sT + s * 64 + k * 16, ph);  // over S, which is read already
-                    }
-                    float a, b;
-                    unpack_f2(add_f2(sum2[0], sum2[1]), a, b);
-                    l += a + b;
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&p_full[2 * half + s]);
                 }
+                fresh = false;
+                const uint64_t sc2 = pack_f2(by, by), m2 = pack_f2(off, off);
+                uint64_t sum2[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t ph[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a, b;
+                        unpack_f2(fma_f2(pack_f2(v[k][2 * j], v[k][2 * j + 1]), sc2, m2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum2[j & 1] = add_f2(sum2[j & 1], pack_f2(a, b));
+                        ph[j] = pack_h2(a, b);
+                    }
+                    tmem_st_x16(sT + buf * 64 + k * 16, ph);  // over S, which is read already
+                }
+                float a, b;
+                unpack_f2(add_f2(sum2[0], sum2[1]), a, b);
+                l += a + b;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[2 * half + buf]);
             }
             // ---- the segment's result
-            if (ok && own > 0 && wait(&pv_done[2 * half + 1], (n_t - 1) & 1u))
+            if (ok && own > 0 && wait(&pv_done[2 * half + ((n - 1) & 1u)], ((n - 1) >> 1) & 1u))
                 tc_fence_after();
             // with both halves on the same columns, each takes half of the
             // channels and joins the two O there: f, f2 are their factors
             float f = 1.f, f2 = 0.f;
             const int c0 = dual ? half * (D / 2) : 0, c1 = dual ? c0 + D / 2 : D;
-            const bool two = dual && sg.tiles_of(p, 1) > 0;
             if (dual) {
                 ml_x[half * 128 + r] = make_float2(m, l);
                 tc_fence_before();
@@ -667,13 +667,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                     tmem_ld_wait();
                     if (dual) {
                         float y[16];
-                        if (two) {
-                            tmem_ld_x16(oB + c, y);
-                            tmem_ld_wait();
-                        }
+                        tmem_ld_x16(oB + c, y);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            v[j] = v[j] * f + (two ? y[j] * f2 : 0.f);
+                            v[j] = v[j] * f + y[j] * f2;
                     }
                 } else {
 #pragma unroll
@@ -770,80 +768,69 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        if (warp < MMA_WARP + 2) {
+        if (warp == MMA_WARP || (warp == MMA_WARP + 1 && !dual)) {
             // ---------------------------------------------------- MMA issue
+            // a warp for each half; where the halves take the sub-tiles in
+            // turn, one for both, so that the stages are let go in order
             const int h = warp - MMA_WARP;
             const uint32_t id_s = idesc_f16(128, 64, false), id_o = idesc_f16(128, D, true);
-            const uint32_t S = tmem + h * C::S_COL, O = tmem + C::O0 + h * C::O_COL;
             const uint64_t dQ = sdesc_kmajor_sw128(smem_u32(smem + C::Q) + (dual ? 0 : h * C::TILE));
             const uint64_t dK = sdesc_kmajor_sw128(smem_u32(sK)), dV = sdesc_mn(smem_u32(sV), C::SBLK);
-            // Both warps pass over every stage in order, so that neither ever
-            // waits for a phase two ahead; a sub-tile of the other half is let
-            // go as soon as it is filled.
+            const uint32_t turn = dual ? 1 : 0, ahead = 2u << turn;  // S is two sub-tiles of a half ahead of O
             Place k, v;
-            uint32_t n_seg = 0, n_own = 0;  // segments in which this half has rows; its sub-tiles
-            auto pass = [&](Place &at, uint64_t *full, uint64_t *empty) {
-                if (wait(&full[at.st], at.ph) && lane == 0)
-                    mbar_arrive(&empty[at.st]);
-                at.next(stages);
-            };
-            auto issue_s = [&](uint32_t buf) {  // S of the sub-tile at k
-                if (!wait(&k_full[k.st], k.ph))
-                    return;
-                tc_fence_after();
+            uint32_t n_s = 0, n_o = 0, n_q = 0;  // S and O products, and segments with rows for this warp
+            auto half_of = [&](uint32_t n) { return dual ? n & 1u : (uint32_t)h; };
+            auto slot_of = [&](uint32_t n) { return 2 * half_of(n) + (n >> turn & 1u); };  // half and buffer
+            auto issue_s = [&]() {  // S of the sub-tile at k
+                const uint32_t slot = slot_of(n_s++);
 #pragma unroll
                 for (int cb = 0; cb < C::CB; ++cb)
-                    mma_ss4(S + buf * 64, dQ + cb * (C::BLK >> 4), dK + k.st * (C::SUB >> 4) + cb * (C::SBLK >> 4), id_s, cb);
-                mma_commit_elect(&s_full[2 * h + buf]);
+                    mma_ss4(slot * 64, dQ + cb * (C::BLK >> 4), dK + k.st * (C::SUB >> 4) + cb * (C::SBLK >> 4), id_s, cb);
+                mma_commit_elect(&s_full[slot]);
                 mma_commit_elect(&k_empty[k.st]);
                 k.next(stages);
             };
             for (; sg.more() && ok; sg.next(p)) {
-                const int T = 2 * sg.tiles_of(p, h), all = 2 * (sg.kt1 - sg.kt0);  // sub-tiles: own, and of the segment
-                if (T > 0 && !wait(&q_full[h], n_seg++ & 1u))
-                    break;
-                int pk = T, pv = T;  // sub-tiles of the segment passed, once the own ones are
-                // where the halves take every other tile, the two sub-tiles
-                // before each of this half's tiles are the other's
-                auto skip = [&](int t) { return dual && (t & 1) == 0 && (h == 1 || t > 0); };
-                auto skip_k = [&](int t) {
-                    if (skip(t)) {
-                        pass(k, k_full, k_empty);
-                        pass(k, k_full, k_empty);
-                        pk += 2;
+                const uint32_t subs = sg.subs();
+                if (sg.subs_of(p, h) == 0) {  // the other half's alone: let each stage go as soon as it is filled
+                    for (uint32_t t = 0; t < subs && ok; ++t) {
+                        if (wait(&k_full[k.st], k.ph) && lane == 0)
+                            mbar_arrive(&k_empty[k.st]);
+                        if (wait(&v_full[v.st], v.ph) && lane == 0)
+                            mbar_arrive(&v_empty[v.st]);
+                        k.next(stages);
+                        v.next(stages);
                     }
-                };
-                for (int t = 0; t < min(2, T) && ok; ++t) {
-                    skip_k(t);
-                    issue_s(t);
+                    continue;
+                }
+                wait(&q_full[dual ? lane & 1 : h], n_q++ & 1u);
+#pragma unroll 1
+                for (uint32_t t = 0; t < min(ahead, subs) && ok; ++t) {
+                    wait(&k_full[k.st], k.ph);
+                    tc_fence_after();
+                    issue_s();
                 }
 #pragma unroll 1
-                for (int t = 0; t < T && ok; ++t, ++n_own) {
-                    const uint32_t buf = t & 1;
-                    if (skip(t)) {
-                        pass(v, v_full, v_empty);
-                        pass(v, v_full, v_empty);
-                        pv += 2;
-                    }
-                    if (!wait(&v_full[v.st], v.ph) || !wait(&p_full[2 * h + buf], (n_own >> 1) & 1u))
+                for (uint32_t t = 0; t < subs && ok; ++t) {
+                    // lanes look at several barriers at once: P and V of this
+                    // sub-tile, and K of the one whose S comes next
+                    const uint32_t slot = slot_of(n_o);
+                    uint64_t *bar = &p_full[slot];
+                    uint32_t ph = n_o >> (1 + turn) & 1u;
+                    if (lane == 1)
+                        bar = &v_full[v.st], ph = v.ph;
+                    if (lane == 2 && t + ahead < subs)
+                        bar = &k_full[k.st], ph = k.ph;
+                    if (!wait(bar, ph))
                         break;
                     tc_fence_after();
-                    mma_ts4(O, S + buf * 64, dV + v.st * (C::SUB >> 4), id_o, t);
-                    mma_commit_elect(&pv_done[2 * h + buf]);
+                    mma_ts4(C::O0 + half_of(n_o) * C::O_COL, slot * 64, dV + v.st * (C::SUB >> 4), id_o, t >> turn);
+                    mma_commit_elect(&pv_done[slot]);
                     mma_commit_elect(&v_empty[v.st]);
                     v.next(stages);
-                    if (t + 2 < T) {
-                        skip_k(t + 2);
-                        issue_s(buf);
-                    }
-                }
-                // what is left is the other half's
-                for (; pv < all && ok; ++pv) {
-                    if (pk == pv) {
-                        pass(k, k_full, k_empty);
-                        ++pk;
-                    }
-                    pass(v, v_full, v_empty);
+                    ++n_o;
+                    if (t + ahead < subs)
+                        issue_s();
                 }
             }
             if (!ok) {
