@@ -840,12 +840,6 @@ static double decode_kernel_us(int offset, int len, int group, int n_kv)
     const double pages = (offset + 0.5 * len) / 16 + 1;
     return 5 + n_kv * (double)(((long long)len * group + 7) / 8) * pages / 1500;
 }
-static double tensor_kernel_us(const Kv4Chunk &c)
-{
-    const double items = (double)c.n_qt * c.n_kv, tiles = (double)c.units / c.ctas;
-    return !c.shared ? 8 + 1.25 * tiles : 8 + 1.7 * tiles + 0.7 * (c.ctas / items + 1);
-}
-
 // Plan a chunk: 0, `p` filled, as columns of the decode kernel; 1, `c` filled,
 // on the tcgen05 kernel; -1: too large.
 static int plan_chunk(Kv4Attn &p, Kv4Chunk &c, int offset, int len, int n_heads, int n_kv, int d, long long *need)
@@ -857,9 +851,9 @@ static int plan_chunk(Kv4Attn &p, Kv4Chunk &c, int offset, int len, int n_heads,
     c.offset = offset;
     const double few = decode_kernel_us(offset, len, group, n_kv);
     const bool tensor = (long long)len * group > 8 && few > 8;
-    if (tensor && !kv4_chunk_plan(c, len))
+    if (tensor && !kv4_chunk_plan(c, len, d))
         return -1;
-    if (tensor && tensor_kernel_us(c) < few) {
+    if (tensor && c.us < few) {
         *need = kv4_chunk_workspace_bytes(c, d);
         return 1;
     }

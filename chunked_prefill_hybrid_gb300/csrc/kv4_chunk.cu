@@ -47,8 +47,6 @@ constexpr int STAGES = 3;                // sub-tiles of 64 keys of K, and of V,
 constexpr int STAGES_DUAL = 4;           // the same where both halves share one Q tile
 constexpr float RAISE = 8.f;             // P <= 2^8
 constexpr float HUGE_SCORE = 1 << 20;    // up to it v sc - m may be fused: m is rounded by 2^-4 at most, for all P alike
-constexpr int DUAL_UNITS = 8;            // (256 columns x 128 keys) a CTA up to which items have 128 columns
-constexpr int WHOLE_TILES = 12;          // key tiles by which an unshared item may be longer than an even share
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int LOOKS = 1 << 22;           // looks at a barrier before a wait is given up: a second or more
 
@@ -883,14 +881,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     }
 }
 
-// Joins the partials of an item, 32 columns a block, in the order of its
-// keys.  Block x belongs to the item that CTA x + 1 begins inside, unless CTA
-// x did so too (then an earlier block has it).
+// Joins the partials of an item, in the order of its keys: 32 columns and 32
+// channels a block, four parts at a time.  Block x belongs to the item that
+// CTA x + 1 begins inside, unless CTA x did so too (then an earlier block has
+// it).  Few registers a thread, so that an SM has enough loads under way.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ Kv4Chunk p)
+__global__ void __launch_bounds__(256, 6) k_kv4_chunk_join(const __grid_constant__ Kv4Chunk p)
 {
-    constexpr int G = D / 32;  // groups of four channels a warp takes
-    __shared__ __align__(16) bf16 s_o[32][D + 8];
+    constexpr int BATCH = 4;
+    __shared__ __align__(16) bf16 s_o[32][32 + 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ca = blockIdx.x;
     const KcStart a = p.start[ca], item = p.start[ca + 1];
@@ -909,63 +908,49 @@ __global__ void __launch_bounds__(256) k_kv4_chunk_join(const __grid_constant__ 
     if (blockIdx.y * 32 >= valid)
         return;
     const float2 *ml = p.part_ml + r;
-    const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + (size_t)warp * G * KC_ROWS + r;
+    const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + (size_t)(blockIdx.z * 8 + warp) * KC_ROWS + r;
     float M = LOWEST, l = 0.f;
-    float4 o[G];
-#pragma unroll
-    for (int k = 0; k < G; ++k)
-        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int BATCH = 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < valid)
         for (int c0 = ca; c0 <= cb; c0 += BATCH) {
             float2 x[BATCH];
-            float4 v[BATCH][G];
-            float top = M;
+            float4 v[BATCH];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int c = min(c0 + i, cb);
+                const int c = c0 + i;
                 const size_t part = c == ca ? first : 2 * c;
-                x[i] = ml[part * KC_ROWS];
-#pragma unroll
-                for (int k = 0; k < G; ++k)
-                    v[i][k] = po[(part * (D / 4) + k) * KC_ROWS];
+                x[i] = make_float2(LOWEST, 0.f);
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c <= cb) {
+                    x[i] = ml[part * KC_ROWS];
+                    v[i] = po[part * (D / 4) * KC_ROWS];
+                }
             }
+            float top = M;
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
                 top = fmaxf(top, x[i].x);
             const float corr = ex2(M - top);
             M = top;
             l *= corr;
+            o.x *= corr, o.y *= corr, o.z *= corr, o.w *= corr;
 #pragma unroll
-            for (int k = 0; k < G; ++k)
-                o[k].x *= corr, o[k].y *= corr, o[k].z *= corr, o[k].w *= corr;
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i)
-                if (c0 + i <= cb) {
-                    const float f = ex2(x[i].x - M);
-                    l += x[i].y * f;
-#pragma unroll
-                    for (int k = 0; k < G; ++k) {
-                        o[k].x += v[i][k].x * f, o[k].y += v[i][k].y * f;
-                        o[k].z += v[i][k].z * f, o[k].w += v[i][k].w * f;
-                    }
-                }
+            for (int i = 0; i < BATCH; ++i) {
+                const float f = ex2(x[i].x - M);
+                l += x[i].y * f;
+                o.x += v[i].x * f, o.y += v[i].y * f, o.z += v[i].z * f, o.w += v[i].w * f;
+            }
         }
     const float inv = p.vs / l;
-#pragma unroll
-    for (int k = 0; k < G; ++k) {
-        __nv_bfloat162 *s = reinterpret_cast<__nv_bfloat162 *>(&s_o[lane][(warp * G + k) * 4]);
-        s[0] = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
-        s[1] = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
-    }
+    __nv_bfloat162 *s = reinterpret_cast<__nv_bfloat162 *>(&s_o[lane][warp * 4]);
+    s[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    s[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
-        const int rr = i / (D / 8), ch = i % (D / 8);
-        if (blockIdx.y * 32 + rr >= valid)
-            break;
+    const int rr = threadIdx.x >> 2, ch = threadIdx.x & 3;
+    if (rr < 32 && blockIdx.y * 32 + rr < valid) {
         const int col = item.qt * p.rows + blockIdx.y * 32 + rr;
         const int row = col / p.group, head = item.kvh * p.group + col - row * p.group;
-        reinterpret_cast<uint4 *>(p.out + row * p.out_stride + (size_t)head * D)[ch] =
+        *reinterpret_cast<uint4 *>(p.out + row * p.out_stride + (size_t)head * D + blockIdx.z * 32 + ch * 8) =
             *reinterpret_cast<const uint4 *>(&s_o[rr][ch * 8]);
     }
 }
@@ -982,52 +967,168 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
         return e;
     if (kv4_chunk_workspace_bytes(p, D) == 0)
         return cudaSuccess;
-    return launch_kernel(true, k_kv4_chunk_join<D>, dim3(p.ctas - 1, p.rows / 32), dim3(256), 0, s, p);
+    return launch_kernel(true, k_kv4_chunk_join<D>, dim3(p.ctas - 1, p.rows / 32, D / 32), dim3(256), 0, s, p);
 }
 
 }  // namespace
 
-bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len)
+// How the work of a chunk may be cut, and about how long each way takes: fits
+// of measured times of 170 shapes, good to a quarter.
+//
+//   parts  an item to one CTA, or to several that share its tiles evenly
+//   whole  more items than CTAs: each takes some that follow one another
+//   even   every CTA as many units as any other, or one more, wherever that
+//          ends: most even, but each CTA may leave two partials of 256 x d
+//          fp32, written and read at some 2.5 MB a microsecond
+//
+// Items of 256 columns convert each key once for both halves; items of 128
+// (both halves on them) make twice as many.  With 40 heads of 128, 512 rows at
+// offset 0 take 24.1 us cut evenly into items of 128 and 12 us as whole items; 512 rows at
+// 15872 keys 140 us cut evenly into items of 256 (1.9 CTAs an item), 170 us as whole items.
+namespace {
+
+constexpr double START_US = 6, SWITCH_US = 2.5, JOIN_US = 3, PART_US = 0.3, BYTES_PER_US = 2.5e6;
+constexpr int MANY_ITEMS = 640;  // from here on an even cut loses little, and a search would cost the host
+
+enum Way { PARTS, WHOLE, EVEN };
+struct Cut {
+    int rows;
+    Way way;
+    long long tiles;  // PARTS, WHOLE: of a CTA at most (WHOLE: with switches counted as tiles)
+    double us;
+};
+
+// A key tile of an item, and how many of them a change from one item to the next costs.
+double tile_us(int rows, int d) { return (rows == 256 ? 1.85 : 1.25) * (d == 64 ? 0.8 : 1); }
+int change_tiles(int rows, int d) { return (int)(SWITCH_US / tile_us(rows, d)) + 1; }
+
+// Cuts of items of p.rows columns: takes over any that beats best.
+void try_cuts(const Kv4Chunk &p, int d, Cut &best)
+{
+    const double tile = tile_us(p.rows, d);
+    const long long items = (long long)p.n_qt * p.n_kv;
+    const double part_us = (p.cols < p.rows ? p.cols : p.rows) * (4.0 * d + 8) / BYTES_PER_US;
+    auto take = [&](Way way, long long tiles, double us) {
+        if (us < best.us)
+            best = Cut{p.rows, way, tiles, us};
+    };
+    const long long ctas = p.units < KC_CTAS ? p.units : KC_CTAS;
+    const double shared = items < ctas ? ctas + items : 2 * ctas, across = (double)items / ctas;
+    take(EVEN, 0,
+         START_US + (double)p.units / ctas * tile + SWITCH_US * (across < 2 ? across : 2) + shared * part_us +
+             JOIN_US + PART_US * ctas / items);
+    if (items > MANY_ITEMS)
+        return;
+    int n[MANY_ITEMS];
+    for (int qt = 0; qt < p.n_qt; ++qt)
+        n[qt] = item_tiles(p, qt);
+    const int most = n[p.n_qt - 1];
+    if (items <= KC_CTAS) {
+        for (int k = 1; k <= most; ++k) {  // CTAs of the longest item
+            const int tiles = (most + k - 1) / k;
+            long long used = 0, parts = 0;
+            for (int qt = 0; qt < p.n_qt; ++qt) {
+                const int share = (n[qt] + tiles - 1) / tiles;
+                used += share;
+                parts += share > 1 ? share : 0;
+            }
+            if (used * p.n_kv > KC_CTAS)
+                break;
+            take(PARTS, tiles,
+                 START_US + tiles * tile + (parts ? parts * p.n_kv * part_us + JOIN_US + PART_US * k : 0));
+        }
+    } else {
+        const int change = change_tiles(p.rows, d);
+        // the least load for which the CTAs suffice, to one part in 32
+        long long lo = (p.units + items * change) / KC_CTAS, hi = lo + most + change;
+        while (hi - lo > 1 + lo / 32) {
+            const long long mid = (lo + hi) / 2;
+            long long load = 0, used = 1;
+            for (int kvh = 0; kvh < p.n_kv; ++kvh)
+                for (int qt = 0; qt < p.n_qt; ++qt) {
+                    if (load > 0 && load + n[qt] + change > mid) {
+                        ++used;
+                        load = 0;
+                    }
+                    load += n[qt] + change;
+                }
+            (used <= KC_CTAS && most + change <= mid ? hi : lo) = mid;
+        }
+        take(WHOLE, hi, START_US + (hi - change) * tile);
+    }
+}
+
+void count_units(Kv4Chunk &p, int rows)
+{
+    p.rows = rows;
+    p.n_qt = (p.cols + rows - 1) / rows;
+    p.units = 0;
+    for (int qt = 0; qt < p.n_qt; ++qt)
+        p.units += item_tiles(p, qt);
+    p.units *= p.n_kv;
+}
+
+}  // namespace
+
+bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int d)
 {
     p.cols = chunk_len * p.group;
-    // Items of 256 columns convert each key once for both halves; items of 128
-    // (both halves on them, on alternate tiles) make more CTAs of the same
-    // work and leave fewer partials.  Few units: 128.
-    for (p.rows = 256;; p.rows = 128) {
-        p.n_qt = (p.cols + p.rows - 1) / p.rows;
-        long long head_units = 0;
-        for (int qt = 0; qt < p.n_qt; ++qt)
-            head_units += item_tiles(p, qt);
-        p.units = head_units * p.n_kv;
-        if (p.rows == 128 || p.units > (long long)DUAL_UNITS * KC_CTAS)
-            break;
+    Cut cut{256, EVEN, 0, 1e300};
+    count_units(p, 256);
+    try_cuts(p, d, cut);
+    if (p.units <= 16ll * KC_CTAS) {  // beyond, 256 columns are always better
+        count_units(p, 128);
+        try_cuts(p, d, cut);
     }
-    p.ctas = (int)(p.units < KC_CTAS ? p.units : KC_CTAS);
-    // one CTA per item, if the partials that this saves are worth more than
-    // the SMs that it leaves idle
-    const long long items = (long long)p.n_qt * p.n_kv;
-    if (items < p.ctas && p.units / items - p.units / p.ctas <= WHOLE_TILES)
-        p.ctas = (int)items;
-    if (p.units / p.ctas >= 0x7fffffff)
-        return false;
-    const bool whole = p.ctas == items;
-    long long at = 0, item_at = 0;  // first unit of (kvh, qt)
-    int kvh = 0, qt = 0, n = item_tiles(p, 0);
+    if (p.rows != cut.rows)
+        count_units(p, cut.rows);
+    p.us = cut.us;
     p.shared = false;
-    for (int c = 0; c < p.ctas; ++c) {
-        while (item_at + n <= at) {
-            item_at += n;
-            if (++qt == p.n_qt) {
-                qt = 0;
-                ++kvh;
+    p.ctas = 0;
+    auto add = [&](int kvh, int qt, int kt0, long long units) {
+        p.start[p.ctas++] = KcStart{kvh, qt, kt0, (int)units};
+        p.shared |= kt0 > 0;
+    };
+    if (cut.way == EVEN) {
+        const int ctas = (int)(p.units < KC_CTAS ? p.units : KC_CTAS);
+        if (p.units / ctas >= 0x7fffffff)
+            return false;
+        long long at = 0, item_at = 0;  // first unit of (kvh, qt)
+        int kvh = 0, qt = 0, n = item_tiles(p, 0);
+        for (int c = 0; c < ctas; ++c) {
+            while (item_at + n <= at) {
+                item_at += n;
+                if (++qt == p.n_qt) {
+                    qt = 0;
+                    ++kvh;
+                }
+                n = item_tiles(p, qt);
             }
-            n = item_tiles(p, qt);
+            const long long next = p.units * (c + 1) / ctas;
+            add(kvh, qt, (int)(at - item_at), next - at);
+            at = next;
         }
-        const long long next = whole ? at + n : p.units * (c + 1) / p.ctas;
-        p.start[c] = KcStart{kvh, qt, (int)(at - item_at), (int)(next - at)};
-        p.shared |= at > item_at;
-        at = next;
+        return true;
     }
+    const int change = change_tiles(p.rows, d);
+    long long load = 0;
+    for (int kvh = 0; kvh < p.n_kv; ++kvh)
+        for (int qt = 0; qt < p.n_qt; ++qt) {
+            const int n = item_tiles(p, qt);
+            if (cut.way == PARTS) {
+                const int share = (int)((n + cut.tiles - 1) / cut.tiles);
+                for (int i = 0; i < share; ++i) {
+                    const int from = (int)((long long)n * i / share), to = (int)((long long)n * (i + 1) / share);
+                    add(kvh, qt, from, to - from);
+                }
+            } else if (load == 0 || load + n + change > cut.tiles) {
+                add(kvh, qt, 0, n);
+                load = n + change;
+            } else {
+                p.start[p.ctas - 1].units += n;
+                load += n + change;
+            }
+        }
     return true;
 }
 

@@ -27,12 +27,12 @@ struct Kv4Chunk {
     bf16 *out;
     long long out_stride;
     // work: units are (item, key tile); item = (kv head, `rows` columns), kv
-    // head major; CTA c takes the units of start[c]: a whole item, or as many as
-    // any other CTA or one more
+    // head major; CTA c takes the units of start[c]
     int rows;                   // 256, or 128: both halves of a CTA on the same columns, on alternate key tiles
     int n_qt, ctas;             // items of a kv head; CTAs
     long long units;
     bool shared;                // some item is shared by several CTAs
+    double us;                  // estimated time
     KcStart start[KC_CTAS];
     float *part_o;              // [2 ctas][D / 4][256][4]: CTA c's segment that starts with it, and its last
     float2 *part_ml;            // [2 ctas][256] (m in log2, l)
@@ -40,7 +40,7 @@ struct Kv4Chunk {
 
 // Plan the work of a chunk (host): everything but the pointers.  False when a
 // CTA's units would not fit 32 bits.
-bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len);
+bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int head_dim);
 long long kv4_chunk_workspace_bytes(const Kv4Chunk &p, int head_dim);
 cudaError_t launch_kv4_chunk(const Kv4Chunk &p, int head_dim, cudaStream_t s);
 
