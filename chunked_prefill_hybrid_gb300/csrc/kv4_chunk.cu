@@ -62,7 +62,7 @@ struct Ck {
     static constexpr int K_DUAL = TILE;               // one Q tile less, one stage of K and of V more
     static_assert(K_DUAL + 2 * STAGES_DUAL * SUB <= R);
     static constexpr int BAR = R + RING * RAW;
-    static constexpr int BYTES = BAR + 1024 + 2048 + 1024;  // barriers, (m, l) pairs, alignment
+    static constexpr int BYTES = BAR + 1024 + 2048 + 1024 + 1024;  // barriers, (m, l) pairs, exponents, alignment
     static constexpr uint32_t S_COL = 128, O0 = 256, O_COL = D;  // S: 64 columns for each (half, buffer)
 };
 
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     using C = Ck<D>;
     using L = Layout<D>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // not by a cast, which would lose that it is shared memory
     uint64_t *raw_full = (uint64_t *)(smem + C::BAR);
     uint64_t *raw_empty = raw_full + RING;
     uint64_t *k_full = raw_empty + RING, *k_empty = k_full + STAGES_DUAL, *v_full = k_empty + STAGES_DUAL;
@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
     volatile int *nan_seen = bad_key + 1;     // a NaN scale of V was met
 
     float2 *ml_x = (float2 *)(smem + C::BAR + 1024);  // [half][128]: m and l for the other half
+    int *s_exp = (int *)(ml_x + 256);                 // [half][128]: by what power of two a row of Q was scaled down
 
     const bool dual = p.rows == 128;
     const uint32_t stages = dual ? STAGES_DUAL : STAGES;
@@ -459,40 +460,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
         uint32_t n = 0;  // sub-tiles this half has been through
         for (; sg.more(); sg.next(p)) {
             const int own = sg.subs_of(p, half);
-            const long long col0 = (long long)sg.qt * p.rows + (dual ? 0 : half * 128);
-            const int valid = (int)min(128ll, p.cols - col0);  // columns of this half (<= 0 if it has none)
-            const long long col = min(col0 + r, (long long)p.cols - 1);
-            const int row = (int)(col / p.group), head = sg.kvh * p.group + (int)(col - (long long)row * p.group);
+            const int col0 = sg.qt * p.rows + (dual ? 0 : half * 128);
+            const int valid = min(128, p.cols - col0);  // columns of this half (<= 0 if it has none)
+            const int col = min(col0 + r, p.cols - 1);
+            const int row = col / p.group, head = sg.kvh * p.group + (col - row * p.group);
             const int seen = p.offset + row + 1;
             uint8_t *q = smem + C::Q + (dual ? 0 : half * C::TILE);
+            int *exps = s_exp + (dual ? 0 : half * 128);
             constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows a warp-wide access
             const int lr = lane / LPR, lc = lane % LPR;
-            float sc = 0.f;
             if (own > 0) {
-                // this warp's 32 rows of Q as f16 (past the last column, that
-                // column's again: their results go nowhere).  Rows of ordinary size go as
-                // they are; if any has its largest magnitude outside [2^-6,
-                // 2^15), each is scaled by a power of two into [1, 4) first
+                // this warp's 32 rows of Q as f16, or 16 of them where the
+                // other half has the same (past the last column, that column's
+                // again: their results go nowhere).  Rows of ordinary size go
+                // as they are; if any of a batch has its largest magnitude
+                // outside [2^-6, 2^15), each is scaled by a power of two into
+                // [1, 4) first
                 const long long src = row * p.q_stride + (size_t)head * D;
-                constexpr int N = 32 / RPI;
-                uint4 u[N];
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    u[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, k * RPI + lr)) + lc);
-                // bit k: some lane of the k-th row has a value of 2^-6 or more;
-                // bit 16 + k: has one that is not 0
-                uint32_t bits = 0, top = 0;
-#pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const uint32_t a = largest_bits(u[k]);
-                    top = max(top, a);
-                    bits |= (a >= 0x3c80u ? 1u << k : 0u) | (a != 0u ? 0x10000u << k : 0u);
-                }
-#pragma unroll
-                for (int x = 1; x < LPR; x *= 2)
-                    bits |= __shfl_xor_sync(0xffffffffu, bits, x);
-                const bool plain = top < 0x4700u && (bits & 0xffffu) == bits >> 16;
-                int e = 0;
+                constexpr int N = 16 / RPI;  // 16 rows a batch, the next one's loads under way meanwhile
+                const int i0 = dual ? half * 16 : 0, i1 = dual ? i0 + 16 : 32;
+                auto load = [&](int i) {
+                    return __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, i + lr)) + lc);
+                };
                 auto put = [&](uint4 x, int i, float down) {
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[4];
@@ -504,26 +493,54 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                     *reinterpret_cast<uint4 *>(q + (lc >> 3) * C::BLK + swz((warp & 3) * 32 + i + lr, lc & 7)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
                 };
-                if (__all_sync(0xffffffffu, plain)) {
+                uint4 u[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    u[k] = load(i0 + k * RPI);
+#pragma unroll 1
+                for (int i = i0; i < i1; i += N * RPI) {
+                    uint4 next[N];
+                    if (i + N * RPI < i1)
+#pragma unroll
+                        for (int k = 0; k < N; ++k)
+                            next[k] = load(i + (N + k) * RPI);
+                    // bit k: some lane of the k-th row has a value of 2^-6 or
+                    // more; bit 16 + k: has one that is not 0
+                    uint32_t bits = 0, top = 0;
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        const uint32_t a = largest_bits(u[k]);
+                        top = max(top, a);
+                        bits |= (a >= 0x3c80u ? 1u << k : 0u) | (a != 0u ? 0x10000u << k : 0u);
+                    }
+#pragma unroll
+                    for (int x = 1; x < LPR; x *= 2)
+                        bits |= __shfl_xor_sync(0xffffffffu, bits, x);
+                    const bool plain = top < 0x4700u && (bits & 0xffffu) == bits >> 16;
+                    if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+                        for (int k = 0; k < N; ++k)
+                            put(u[k], i + k * RPI, 1.f);
+                        if (lane < N * RPI)
+                            exps[(warp & 3) * 32 + i + lane] = 0;
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < N; ++k) {
+                            const uint4 x = load(i + k * RPI);
+                            uint32_t a = largest_bits(x);
+#pragma unroll
+                            for (int y = 1; y < LPR; y *= 2)
+                                a = max(a, __shfl_xor_sync(0xffffffffu, a, y));
+                            const int e = query_exponent(__uint_as_float(a << 16));
+                            put(x, i + k * RPI, pow2(-e));
+                            if (lc == 0)
+                                exps[(warp & 3) * 32 + i + k * RPI + lr] = e;
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < N; ++k)
-                        put(u[k], k * RPI, 1.f);
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < 32; i += RPI) {
-                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.q + __shfl_sync(0xffffffffu, src, i + lr)) + lc);
-                        uint32_t a = largest_bits(x);
-#pragma unroll
-                        for (int k = 1; k < LPR; k *= 2)
-                            a = max(a, __shfl_xor_sync(0xffffffffu, a, k));
-                        const int er = query_exponent(__uint_as_float(a << 16));
-                        put(x, i, pow2(-er));
-                        const int mine_e = __shfl_sync(0xffffffffu, er, (lane % RPI) * LPR);  // of row i + lane % RPI
-                        if (lane / RPI == i / RPI)
-                            e = mine_e;
-                    }
+                        u[k] = next[k];
                 }
-                sc = fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e), 1e-38f);  // never 0: a masked score stays -inf
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
@@ -531,7 +548,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             } else if (!dual) {
                 continue;
             }
-            const int seen0 = p.offset + (int)(col0 / p.group) + 1;  // of the half's first column
+            if (dual)  // half of this warp's exponents are the other half's
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            // never 0: a masked score stays -inf
+            const float sc = fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(exps[r]), 1e-38f);
+            const int seen0 = p.offset + col0 / p.group + 1;  // of the half's first column
             float m = LOWEST, l = 0.f;
             float raise_at = LOWEST;  // a maximum above it moves m
             bool fresh = true;  // no O yet
@@ -658,32 +679,32 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             const float inv = p.vs / l;
             const uint32_t oA = dual ? lanes + C::O0 : oT, oB = lanes + C::O0 + C::O_COL;
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 16) {
-                float v[16];
+            for (int c = c0; c < c1; c += 32) {
+                float v[32];
                 if (ok) {
-                    tmem_ld_x16(oA + c, v);
+                    float y[32];
+                    tmem_ld_x32(oA + c, v);
+                    if (dual)
+                        tmem_ld_x32(oB + c, y);
                     tmem_ld_wait();
-                    if (dual) {
-                        float y[16];
-                        tmem_ld_x16(oB + c, y);
-                        tmem_ld_wait();
+                    if (dual)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < 32; ++j)
                             v[j] = v[j] * f + y[j] * f2;
-                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         v[j] = 0.f;
                 }
-                if (nans >> (c / 16) & 1u)
+                if (nans >> (c / 16) & 3u)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] = __int_as_float(0x7fc00000);
+                    for (int j = 0; j < 32; ++j)
+                        if (nans >> (c / 16 + j / 16) & 1u)
+                            v[j] = __int_as_float(0x7fc00000);
                 if (whole) {
                     // through the Q tile, which no MMA reads any more
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         float x[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -694,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 } else if (r < valid) {
                     float4 *po = reinterpret_cast<float4 *>(p.part_o) + (part * (D / 4) + c / 4) * KC_ROWS + pr;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 8; ++k)
                         po[k * KC_ROWS] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
                 __syncwarp();
@@ -703,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 const long long dst = row * p.out_stride + (size_t)head * D;
                 const int shift = (D == 128 ? 4 : 3) - (dual ? 1 : 0);  // log2 of the 16-byte chunks of a row here
                 const int rl = lane >> shift, cl = (lane & ((1 << shift) - 1)) + c0 / 8;
-#pragma unroll 2
+#pragma unroll 4
                 for (int i = 0; i < 32; i += 32 >> shift) {
                     const long long at = __shfl_sync(0xffffffffu, dst, i + rl);
                     const int rr = (warp & 3) * 32 + i + rl;

@@ -314,12 +314,15 @@ def test_chunk_with_a_bad_block():
     assert torch.equal(out, good)
 
 
-# kv heads, group, head size, offset, rows, partials: many rows over many keys, in each way the work is cut (128 or 256
-# columns an item, items whole or shared by several CTAs), with last items of a few columns
-LARGE = [(40, 1, 128, 1000, 130, False), (8, 4, 64, 700, 333, False), (8, 12, 64, 1800, 40, False),
-         (4, 2, 128, 2000, 257, True), (2, 5, 64, 5000, 129, True), (1, 8, 128, 20000, 64, True),
-         (2, 3, 128, 3000, 1500, True), (8, 1, 64, 0, 3000, False), (8, 2, 128, 15000, 130, True),
-         (5, 3, 64, 12001, 301, True)]
+# kv heads, group, head size, offset, rows, whether items are shared: many rows over many keys, in each way the work is
+# cut, with last items of a few columns
+LARGE = [(40, 1, 128, 1000, 130, False), (8, 4, 64, 700, 333, False),      # a CTA for each item of 128 columns
+         (8, 12, 64, 1800, 40, True), (4, 2, 128, 2000, 257, True),        # several
+         (2, 5, 64, 5000, 129, True), (1, 8, 128, 20000, 64, True), (8, 2, 128, 15000, 130, True),
+         (8, 1, 128, 0, 3000, False),                                      # several items for each CTA
+         (2, 3, 128, 3000, 1500, True), (5, 3, 64, 12001, 301, True),      # items of 256, a few CTAs each
+         (8, 8, 64, 0, 1000, False), (40, 1, 128, 0, 1500, False),         # several for each CTA
+         (8, 8, 64, 0, 3000, True)]                                        # evenly, whatever the items
 
 
 def _check_rows(got, q64, k, v, offset, rows):
