@@ -830,11 +830,13 @@ extern "C" int hb_kv4_decode(const hb_kv4_pool *pool, const void *q, long long q
     return launch(p, d, n_decodes, n_decodes, (cudaStream_t)cuda_stream);
 }
 
-// Microseconds that a chunk takes as columns of the decode kernel, and on the
-// tcgen05 kernel: fits of measured times, good to about a quarter.  With 40
-// heads of 128 and 1000 cached keys, 32 rows take 16.2 us against 19.4, 64
-// rows 22.8 against 19.5; with 16000 keys, 16 rows 56 against 74, 32 rows 97
-// against 75; with one kv head and 16000 keys, 256 rows 27 against 57.
+// Microseconds that a chunk takes as columns of the decode kernel: a fit of
+// measured times, good to about a third, for the choice between it and the
+// tcgen05 kernel, whose plan has an estimate of its own.  With 40 heads of 128
+// and 1000 cached keys, 16 rows take 10.1 us against 12.9 on the tcgen05
+// kernel, 64 rows 20.8 against 12.4; with 16000 keys, 16 rows 52 against 58,
+// 32 rows 81 against 59; with eight heads on one kv head and 16000 keys, 16
+// rows 14.3 against 17.6, 64 rows 42 against 20.
 static double decode_kernel_us(int offset, int len, int group, int n_kv)
 {
     const double pages = (offset + 0.5 * len) / 16 + 1;

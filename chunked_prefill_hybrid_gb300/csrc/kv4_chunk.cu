@@ -994,50 +994,52 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
 }  // namespace
 
 // How the work of a chunk may be cut, and about how long each way takes: fits
-// of measured times of 170 shapes, good to a quarter.
+// of measured times of 210 shapes, most of them good to a quarter.
 //
 //   parts  an item to one CTA, or to several that share its tiles evenly
 //   whole  more items than CTAs: each takes some that follow one another
-//   even   every CTA as many units as any other, or one more, wherever that
-//          ends: most even, but each CTA may leave two partials of 256 x d
-//          fp32, written and read at some 2.5 MB a microsecond
+//   even   every CTA the same load, wherever that ends: most even, but each CTA
+//          may leave two partials of 256 x d fp32, written and read at some
+//          2.5 MB a microsecond
 //
-// Items of 256 columns convert each key once for both halves; items of 128
-// (both halves on them) make twice as many.  With 40 heads of 128, 512 rows at
-// offset 0 take 24.1 us cut evenly into items of 128 and 12 us as whole items; 512 rows at
-// 15872 keys 140 us cut evenly into items of 256 (1.9 CTAs an item), 170 us as whole items.
+// A load is key tiles, and for each item the tiles' worth of a change of items
+// (the queries, the pipeline's start and end, the result).  Items of 256
+// columns convert each key once for both halves; items of 128 (both halves on
+// them) make twice as many.  With 40 heads of 128, 512 rows at offset 0 take
+// 24 us cut evenly into items of 128 and 15 as whole items; 512 rows at 15872
+// keys 133 us cut evenly into items of 256, 1.9 CTAs an item, and 215 as whole ones.
 namespace {
 
-constexpr double START_US = 6, SWITCH_US = 2.5, JOIN_US = 3, PART_US = 0.3, BYTES_PER_US = 2.5e6;
+constexpr double SWITCH_US = 5, JOIN_US = 2, PART_US = 0.25, BYTES_PER_US = 2.5e6;
 constexpr int MANY_ITEMS = 640;  // from here on an even cut loses little, and a search would cost the host
 
 enum Way { PARTS, WHOLE, EVEN };
 struct Cut {
     int rows;
     Way way;
-    long long tiles;  // PARTS, WHOLE: of a CTA at most (WHOLE: with switches counted as tiles)
+    long long tiles;  // PARTS: of a CTA at most; WHOLE: its load
     double us;
 };
 
-// A key tile of an item, and how many of them a change from one item to the next costs.
-double tile_us(int rows, int d) { return (rows == 256 ? 1.85 : 1.25) * (d == 64 ? 0.8 : 1); }
+// A launch and an item's start and end; a key tile; the tiles' worth of a change of items.
+double start_us(int d) { return d == 64 ? 4.5 : 5.5; }
+double tile_us(int rows, int d) { return rows == 256 ? (d == 64 ? 1.5 : 1.65) : (d == 64 ? 0.8 : 1.05); }
 int change_tiles(int rows, int d) { return (int)(SWITCH_US / tile_us(rows, d)) + 1; }
 
 // Cuts of items of p.rows columns: takes over any that beats best.
 void try_cuts(const Kv4Chunk &p, int d, Cut &best)
 {
-    const double tile = tile_us(p.rows, d);
+    const double start = start_us(d), tile = tile_us(p.rows, d);
+    const int change = change_tiles(p.rows, d);
     const long long items = (long long)p.n_qt * p.n_kv;
     const double part_us = (p.cols < p.rows ? p.cols : p.rows) * (4.0 * d + 8) / BYTES_PER_US;
     auto take = [&](Way way, long long tiles, double us) {
         if (us < best.us)
             best = Cut{p.rows, way, tiles, us};
     };
-    const long long ctas = p.units < KC_CTAS ? p.units : KC_CTAS;
-    const double shared = items < ctas ? ctas + items : 2 * ctas, across = (double)items / ctas;
-    take(EVEN, 0,
-         START_US + (double)p.units / ctas * tile + SWITCH_US * (across < 2 ? across : 2) + shared * part_us +
-             JOIN_US + PART_US * ctas / items);
+    const long long ctas = p.units < KC_CTAS ? p.units : KC_CTAS, load = p.units + items * change;
+    const double shared = items < ctas ? ctas + items : 2 * ctas;
+    take(EVEN, 0, start + (double)load / ctas * tile + shared * part_us + JOIN_US + PART_US * ctas / items);
     if (items > MANY_ITEMS)
         return;
     int n[MANY_ITEMS];
@@ -1056,26 +1058,25 @@ void try_cuts(const Kv4Chunk &p, int d, Cut &best)
             if (used * p.n_kv > KC_CTAS)
                 break;
             take(PARTS, tiles,
-                 START_US + tiles * tile + (parts ? parts * p.n_kv * part_us + JOIN_US + PART_US * k : 0));
+                 start + tiles * tile + (parts ? parts * p.n_kv * part_us + JOIN_US + PART_US * k : 0));
         }
     } else {
-        const int change = change_tiles(p.rows, d);
         // the least load for which the CTAs suffice, to one part in 32
-        long long lo = (p.units + items * change) / KC_CTAS, hi = lo + most + change;
+        long long lo = load / KC_CTAS, hi = lo + most + change;
         while (hi - lo > 1 + lo / 32) {
             const long long mid = (lo + hi) / 2;
-            long long load = 0, used = 1;
+            long long sum = 0, used = 1;
             for (int kvh = 0; kvh < p.n_kv; ++kvh)
                 for (int qt = 0; qt < p.n_qt; ++qt) {
-                    if (load > 0 && load + n[qt] + change > mid) {
+                    if (sum > 0 && sum + n[qt] + change > mid) {
                         ++used;
-                        load = 0;
+                        sum = 0;
                     }
-                    load += n[qt] + change;
+                    sum += n[qt] + change;
                 }
             (used <= KC_CTAS && most + change <= mid ? hi : lo) = mid;
         }
-        take(WHOLE, hi, START_US + (hi - change) * tile);
+        take(WHOLE, hi, start + (hi - change) * tile);
     }
 }
 
@@ -1110,28 +1111,36 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int d)
         p.start[p.ctas++] = KcStart{kvh, qt, kt0, (int)units};
         p.shared |= kt0 > 0;
     };
+    const int change = change_tiles(p.rows, d);
     if (cut.way == EVEN) {
-        const int ctas = (int)(p.units < KC_CTAS ? p.units : KC_CTAS);
-        if (p.units / ctas >= 0x7fffffff)
+        const long long ctas = p.units < KC_CTAS ? p.units : KC_CTAS;
+        if (p.units / ctas >= 0x3fffffff)
             return false;
-        long long at = 0, item_at = 0;  // first unit of (kvh, qt)
+        const long long all = p.units + (long long)p.n_qt * p.n_kv * change;
+        // the item at hand: its load begins at `from`, its units at `before`
+        long long from = 0, before = 0, at = 0;
         int kvh = 0, qt = 0, n = item_tiles(p, 0);
-        for (int c = 0; c < ctas; ++c) {
-            while (item_at + n <= at) {
-                item_at += n;
+        int at_kvh = 0, at_qt = 0, at_kt = 0;  // where unit `at` lies
+        for (long long c = 1; c <= ctas; ++c) {
+            const long long to = all * c / ctas;
+            while (c < ctas && from + change + n <= to) {
+                from += change + n;
+                before += n;
                 if (++qt == p.n_qt) {
                     qt = 0;
                     ++kvh;
                 }
                 n = item_tiles(p, qt);
             }
-            const long long next = p.units * (c + 1) / ctas;
-            add(kvh, qt, (int)(at - item_at), next - at);
+            const int kt = c < ctas && to > from + change ? (int)(to - from - change) : 0;
+            const long long next = c < ctas ? before + kt : p.units;
+            if (next > at)
+                add(at_kvh, at_qt, at_kt, next - at);
             at = next;
+            at_kvh = kvh, at_qt = qt, at_kt = kt;
         }
         return true;
     }
-    const int change = change_tiles(p.rows, d);
     long long load = 0;
     for (int kvh = 0; kvh < p.n_kv; ++kvh)
         for (int qt = 0; qt < p.n_qt; ++qt) {

@@ -314,15 +314,13 @@ def test_chunk_with_a_bad_block():
     assert torch.equal(out, good)
 
 
-# kv heads, group, head size, offset, rows, whether items are shared: many rows over many keys, in each way the work is
-# cut, with last items of a few columns
-LARGE = [(40, 1, 128, 1000, 130, False), (8, 4, 64, 700, 333, False),      # a CTA for each item of 128 columns
-         (8, 12, 64, 1800, 40, True), (4, 2, 128, 2000, 257, True),        # several
-         (2, 5, 64, 5000, 129, True), (1, 8, 128, 20000, 64, True), (8, 2, 128, 15000, 130, True),
-         (8, 1, 128, 0, 3000, False),                                      # several items for each CTA
-         (2, 3, 128, 3000, 1500, True), (5, 3, 64, 12001, 301, True),      # items of 256, a few CTAs each
-         (8, 8, 64, 0, 1000, False), (40, 1, 128, 0, 1500, False),         # several for each CTA
-         (8, 8, 64, 0, 3000, True)]                                        # evenly, whatever the items
+# kv heads, group, head size, offset, rows: many rows over many keys, a last item of a few columns; between them they
+# have each way in which the work is cut (items of 128 and of 256 columns; a CTA for each, several, or several items a
+# CTA; evenly, whatever the items)
+LARGE = [(40, 1, 128, 1000, 130), (8, 4, 64, 700, 333), (8, 12, 64, 1800, 40), (4, 2, 128, 2000, 257),
+         (2, 5, 64, 5000, 129), (1, 8, 128, 20000, 64), (8, 2, 128, 15000, 130), (8, 1, 128, 0, 3000),
+         (2, 3, 128, 3000, 1500), (5, 3, 64, 12001, 301), (8, 8, 64, 0, 1000), (40, 1, 128, 0, 1500),
+         (8, 8, 64, 0, 3000), (8, 8, 128, 0, 500)]
 
 
 def _check_rows(got, q64, k, v, offset, rows):
@@ -331,12 +329,11 @@ def _check_rows(got, q64, k, v, offset, rows):
         assert (np.abs(got[i] - o) <= bound).all(), (i, np.max(np.abs(got[i] - o) / bound))
 
 
-@pytest.mark.parametrize("kv,group,d,offset,n,shared", LARGE)
-def test_large_chunk(kv, group, d, offset, n, shared):
+@pytest.mark.parametrize("kv,group,d,offset,n", LARGE)
+def test_large_chunk(kv, group, d, offset, n):
     f = Filled([5, offset + n], kv, d, 15, ks=1.25, vs=0.5)
     heads = kv * group
     need = cache.kv4_chunk_workspace(offset, n, heads, kv, d)
-    assert (need > 0) == shared
     wide, q64 = _bf(np.random.default_rng(7).standard_normal((n, heads + 2, d)) * 2)
     q = wide[:, :heads]
     ws = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device="cuda")
