@@ -4,9 +4,9 @@
 //   S = Q K^T,  P = 2^(S c - m),  O += P V,  o = O / sum P
 //
 // For one kv head the chunk's (row, head) pairs are the columns of an item,
-// 256 at a time; an item's keys come in tiles of 128.  A CTA works through a
-// contiguous range of (item, key tile) units, as many to every CTA; an item
-// that several CTAs share leaves fp32 partials, which a second kernel joins.
+// 128 or 256 at a time; an item's keys come in tiles of 128.  A CTA works
+// through (item, key tile) units that follow one another; an item that several
+// CTAs share leaves fp32 partials, which a second kernel joins.
 //
 //   warps 0..7    softmax, one thread per query: S from tensor memory, P back
 //                 into it as f16; O is rescaled only when a maximum rises by
@@ -14,13 +14,25 @@
 //   warps 8..19   three groups of four, a group a sub-tile of 64 keys, a warp a
 //                 page: codes and scales -> f16 rows of the K and V tiles
 //                 (128-byte swizzle); code x scale is exact in f16
-//   warps 20, 21  issue the MMAs of the two 128-row halves: S, and O += P V
-//                 with P read from tensor memory
+//   warps 20, 21  issue the MMAs of the two halves of 128 columns: S, and
+//                 O += P V with P read from tensor memory
 //   warp 22       loader: one bulk copy per page (16 keys) into a ring
 //
 // S comes in sub-tiles of 64 keys, two for each half, each in tensor memory of
-// its own: while one is in the softmax the tensor pipe fills the other.  The
-// softmax warps take the registers that the others do not need.
+// its own: while one is in the softmax the tensor pipe fills the other.  With
+// items of 128 columns ("dual") both halves have the same columns and take the
+// sub-tiles in turn; the CTA joins their two results.  The softmax warps take
+// the registers that the others do not need.
+//
+// What bounds it: at 512 rows over 15872 keys, 40 heads of 128 (169 GFLOP in
+// 130 us, 1.3 PFLOP/s of f16), two thirds of the issue slots and 56% of the
+// tensor pipe's time are taken: the softmax warps, whose exponentials and
+// conversions share the schedulers with the conversion of K and V, are the
+// longest way.  Small chunks (256 rows at 768 keys, 14.5 us) spend 3 us until
+// the first scores and 2.5 us on the last result.  Two groups of converting
+// warps in place of three: 14.7 us there, 132 above; one warp issuing for both
+// halves where they share the sub-tiles: 151 in place of 139; no maximum unless
+// a sum shows that one is needed: 145 in place of 128.
 //
 // Every wait is bounded; when one runs out, the CTA writes NaN for the rows
 // it has left, drains and returns.
@@ -41,14 +53,15 @@ using namespace tc;
 constexpr int GROUPS = 3;                // of four warps that convert sub-tiles of K and V
 constexpr int MMA_WARP = 8 + 4 * GROUPS;
 constexpr int THREADS = (MMA_WARP + 4) * 32;
-constexpr int REGS_SOFTMAX = 128, REGS_OTHER = 56;  // 256 and 512 threads: 61440 registers, 80 for each thread at launch
+// Of 256 and 512 threads: 61440 registers, 80 for each thread at launch.  512
+// rows at 15872 keys take 2% longer with 128 and 56, 15% with 112 and 64.
+constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 48;
 constexpr int RING = 24;                 // pages in flight
 constexpr int STAGES = 3;                // sub-tiles of 64 keys of K, and of V, in f16
 constexpr int STAGES_DUAL = 4;           // the same where both halves share one Q tile
 constexpr float RAISE = 8.f;             // P <= 2^8
 constexpr float HUGE_SCORE = 1 << 20;    // up to it v sc - m may be fused: m is rounded by 2^-4 at most, for all P alike
-constexpr uint64_t WAIT_NS = 2000000000ull;
-constexpr int LOOKS = 1 << 22;           // looks at a barrier before a wait is given up: a second or more
+constexpr uint64_t WAIT_NS = 2000000000ull;  // after which a wait is given up
 
 template <int D>
 struct Ck {
@@ -437,17 +450,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 
     bool ok = true;
     // A whole warp's wait, short of code: the roles together have to stay in
-    // the instruction caches.  Plain looks, without a time to sleep: S, P and
-    // the stages are waited for all the time (155 us against 167 for 512 rows
-    // at 15872).
+    // the instruction caches.  Plain looks, each as long as the hardware cares
+    // to make it (they hardly ever come to a second one), without a time to
+    // sleep: with one for the converting warps alone 148 us in place of 140,
+    // for all 158 (512 rows at 15872).  The votes tell the compiler that the
+    // warp stays together, so that addresses and descriptors are kept in
+    // uniform registers (154 us without).
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        int i = 0;
+        uint32_t looks = 0;
+        uint64_t since = 0;
 #pragma unroll 1
-        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-            if (++i == LOOKS || __any_sync(0xffffffffu, *abort_flag)) {
+        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+            bool over = *abort_flag;
+            if ((++looks & 63u) == 0) {
+                const uint64_t now = globaltimer_ns();
+                since = since ? since : now;
+                over |= now - since > WAIT_NS;
+            }
+            if (__any_sync(0xffffffffu, over)) {
                 *abort_flag = 1;
                 return ok = false;
             }
+        }
         return ok;
     };
 
@@ -905,7 +929,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 // Joins the partials of an item, in the order of its keys: 32 columns and 32
 // channels a block, four parts at a time.  Block x belongs to the item that
 // CTA x + 1 begins inside, unless CTA x did so too (then an earlier block has
-// it).  Few registers a thread, so that an SM has enough loads under way.
+// it).  Bound by the partials' traffic: 30 MB for 512 rows at 15872 keys, some
+// 7 us of 130.
 template <int D>
 __global__ void __launch_bounds__(256, 6) k_kv4_chunk_join(const __grid_constant__ Kv4Chunk p)
 {
