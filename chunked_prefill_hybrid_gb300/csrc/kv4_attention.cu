@@ -119,13 +119,21 @@ struct Smem {
     static constexpr int BYTES = (RINGS > JOIN ? RINGS : JOIN);
 };
 
+// A warp reads pages of its own through a ring of bulk copies, four under way,
+// and works on two at a time; four warps a CTA join their results in shared
+// memory.  128 rows of 128 to 2048 keys, 40 heads of 128, take 94 us (5.5 TB/s,
+// 0.81 of the copy rate); 18 rows of 1024 keys 23.4 us; one row of 130999 keys,
+// 8 kv heads of 8, 36.2 us with the join.  Bound by the issue of conversions (two
+// thirds of the slots) and, where there is one wave of CTAs, by their start.
+//
 // FEW: one query (d = 128) or two (d = 64) share the kv head.  The eight
 // columns are then the (query, scale block) pairs: column (c, i) holds query
 // c's block i and zeros elsewhere, so the MMAs give the scores block by block
 // and each is scaled once in fp32 instead of each code's value; and in V^T P
 // column (c, i) holds P times the scales of block i, for channel block i's MMA
 // alone (zeros for the others'), so that one accumulator of four registers
-// takes every channel.
+// takes every channel: 128 rows as above take 197 us with a multiplied K and V
+// and one page at a time, 97 so.
 template <int D, bool FEW>
 __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const Kv4Attn p)
 {
@@ -608,7 +616,9 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
 }
 
 // Joins the splits of one (row, head): each warp some of them, eight loads of
-// a lane under way at a time, then the warps in order.
+// a lane under way at a time, then the warps in order.  Bound by the loads'
+// latency: 76 splits of 64 heads (one row of 130999 keys) 1 us less than with
+// one load after the other.
 template <int D>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_kv4_join(const Kv4Attn p)
 {
@@ -689,8 +699,9 @@ struct Split {
 
 // Keys of a split (a multiple of 16 WARPS) and the number of splits: the one
 // with the least estimated time.  An SM shares its throughput among its CTAs
-// and needs three of them to reach it; joining splits takes about as long as an
-// SM takes for 64 pages of a head.
+// and needs three of them to reach it (4, 5 or 8 were no better over the shapes
+// that were measured); joining splits takes about as long as an SM takes for 64
+// pages of a head.
 Split plan_split(long long ctas, int max_keys)
 {
     constexpr int UNIT = 16 * WARPS;

@@ -171,7 +171,11 @@ struct Place {
     }
 };
 
-// One thread per (row, kv head, 16 channels), K and V.
+// One thread per (row, kv head, 16 channels), K and V.  Bound by instructions:
+// with k_kv4_read 3565 rows of 40 heads of 128 take 38.2 us, of which the
+// 187 MB that the two move would take 27.6 at the copy rate; 274 rows 5.3 us;
+// 18 rows 3.6 (two launches).  A byte store for each two channels took 51.4 us,
+// 7.8 and 5.2.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 6)
     k_kv4_append(uint8_t *pool, int num_blocks, int n_kv, int head_groups, float ks, float vs, float k6, float v6,
@@ -224,6 +228,7 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, float s)
     return pack8_bf16(x);
 }
 
+// The same the other way: a thread per (row, kv head, 16 channels), figures above.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 8)
     k_kv4_read(const uint8_t *pool, int num_blocks, int n_kv, int head_groups, float ks, float vs, const int *slots,
