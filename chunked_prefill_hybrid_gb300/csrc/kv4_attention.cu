@@ -160,6 +160,12 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     }
     pdl_wait();
     pdl_trigger();
+    // this warp's pages: b0 + 4 i, i < n_tiles, through its ring.  The first
+    // ids are fetched before it is known how many are needed (a table row has
+    // bt_stride of them): the context's length comes in the same time.
+    const int k0 = split * p.split_len, b0 = (k0 >> 4) + warp;
+    const int *tab = p.tables + (size_t)seq * p.bt_stride + b0;
+    int ids = b0 + lane * WARPS < p.bt_stride ? __ldg(tab + lane * WARPS) : 0;  // lane i: page of tile i of the current 32
     if (p.chunk_len == 0) {
         const int ctx = p.ctx_lens[seq];
         if (ctx < 0 || ctx > p.max_ctx) {  // padding: zeros; outside what the grid was sized for: NaN
@@ -174,17 +180,14 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         }
     }
     const int nkeys = column(p, seq, kvh, c1 - 1).nkeys;  // the most any query sees
-    const int k0 = split * p.split_len, k1 = min(nkeys, k0 + p.split_len);
+    const int k1 = min(nkeys, k0 + p.split_len);
     if (k0 >= k1)
         return;
     const int fewest = column(p, seq, kvh, c0).nkeys;  // keys that every query sees
 
-    // ---- this warp's pages: b0 + 4 i, i < n_tiles, through its ring
-    const int b0 = (k0 >> 4) + warp, n_tiles = max(0, (((k1 + 15) >> 4) - b0 + WARPS - 1) / WARPS);
-    const int *tab = p.tables + (size_t)seq * p.bt_stride + b0;
+    const int n_tiles = max(0, (((k1 + 15) >> 4) - b0 + WARPS - 1) / WARPS);
     uint8_t *ring = smem + warp * RING * L::BYTES;
     bool bad = false;
-    int ids = lane < n_tiles ? __ldg(tab + lane * WARPS) : 0;  // lane i: page of tile i of the current 32
     const uint8_t *head = p.pool + (size_t)kvh * L::BYTES;
     // copy pages tile..tile + N - 1 (tile a multiple of N), lane i the i-th
     auto issue = [&](int tile, auto n) {
