@@ -389,6 +389,19 @@ __device__ __noinline__ uint32_t nan_blocks(const Kv4Chunk &p, int kvh, int k0, 
     return m;
 }
 
+// 32 bytes to one place: at once where it is the start of a sector.
+__device__ __forceinline__ void store_sector(bf16 *at, uint4 a, uint4 b, bool aligned)
+{
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a.x), "r"(a.y), "r"(a.z),
+                     "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(at)[0] = a;
+        reinterpret_cast<uint4 *>(at)[1] = b;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant__ Kv4Chunk p)
 {
@@ -697,10 +710,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 l = __int_as_float(0x7fc00000);
                 m = 0.f;
             }
+            const bool whole_sectors = ((uintptr_t)p.out | (uintptr_t)(2 * p.out_stride)) % 32 == 0;
             const bool whole = sg.kt0 == 0 && sg.kt1 == sg.n_tiles;
             const size_t part = (size_t)blockIdx.x * 2 + (sg.first ? 0 : 1);
             const int pr = (dual ? 0 : half * 128) + r;  // row of the item's partial
             const float inv = p.vs / l;
+            const long long dst = row * p.out_stride + (size_t)head * D;
             const uint32_t oA = dual ? lanes + C::O0 : oT, oB = lanes + C::O0 + C::O_COL;
 #pragma unroll 1
             for (int c = c0; c < c1; c += 32) {
@@ -726,16 +741,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         if (nans >> (c / 16 + j / 16) & 1u)
                             v[j] = __int_as_float(0x7fc00000);
                 if (whole) {
-                    // through the Q tile, which no MMA reads any more
+                    if (r < valid)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float x[8];
+                        for (int k = 0; k < 2; ++k) {
+                            float x[2][8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            x[j] = v[8 * k + j] * inv;
-                        const int ch = c / 8 + k;
-                        *reinterpret_cast<uint4 *>(q + (ch >> 3) * C::BLK + swz(r, ch & 7)) = pack8_bf16(x);
-                    }
+                            for (int j = 0; j < 16; ++j)
+                                x[j / 8][j % 8] = v[16 * k + j] * inv;
+                            store_sector(p.out + dst + c + 16 * k, pack8_bf16(x[0]), pack8_bf16(x[1]), whole_sectors);
+                        }
                 } else if (r < valid) {
                     float4 *po = reinterpret_cast<float4 *>(p.part_o) + (part * (D / 4) + c / 4) * KC_ROWS + pr;
 #pragma unroll
@@ -744,20 +758,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 }
                 __syncwarp();
             }
-            if (whole) {
-                const long long dst = row * p.out_stride + (size_t)head * D;
-                const int shift = (D == 128 ? 4 : 3) - (dual ? 1 : 0);  // log2 of the 16-byte chunks of a row here
-                const int rl = lane >> shift, cl = (lane & ((1 << shift) - 1)) + c0 / 8;
-#pragma unroll 4
-                for (int i = 0; i < 32; i += 32 >> shift) {
-                    const long long at = __shfl_sync(0xffffffffu, dst, i + rl);
-                    const int rr = (warp & 3) * 32 + i + rl;
-                    if (rr < valid)
-                        reinterpret_cast<uint4 *>(p.out + at)[cl] =
-                            *reinterpret_cast<const uint4 *>(q + (cl >> 3) * C::BLK + swz(rr, cl & 7));
-                }
-                __syncwarp();  // the next segment's Q goes there
-            } else if (r < valid && (!dual || half == 0)) {
+            if (!whole && r < valid && (!dual || half == 0)) {
                 p.part_ml[part * KC_ROWS + pr] = make_float2(m, l);
             }
             tc_fence_before();  // the next segment's MMAs overwrite O

@@ -418,6 +418,51 @@ def test_large_chunk_with_queries_of_any_size(kv, group, d, offset, n):
                 assert good.all(), (i, h)
 
 
+def _odd_rows(n, width, fill=7.0):
+    """n rows of `width` bf16 values that start 16 bytes past a 32-byte border, in turn at one and off one."""
+    flat = torch.full((16 + n * (width + 8),), fill, dtype=torch.bfloat16, device="cuda")
+    return flat, flat[8:8 + n * (width + 8)].view(n, width + 8)[:, :width]
+
+
+@pytest.mark.parametrize("kv,group,d,offset,n", [(40, 1, 128, 1000, 130), (8, 4, 64, 700, 333), (2, 1, 64, 40, 9)])
+def test_rows_on_sixteen_byte_borders(kv, group, d, offset, n):
+    """Every call with rows at the least alignment that it allows: the results of aligned rows, and nothing beside them."""
+    heads = kv * group
+    f = Filled([offset + n], kv, d, 19)
+    k, v = torch.randn(n, kv, d, device="cuda").bfloat16(), torch.randn(n, kv, d, device="cuda").bfloat16()
+    q = torch.randn(n, heads, d, device="cuda").bfloat16()
+    odd = {}
+    for name, t in (("k", k), ("v", v), ("q", q)):
+        _, odd[name] = _odd_rows(n, t[0].numel())
+        odd[name].copy_(t.reshape(n, -1))
+        odd[name] = odd[name].unflatten(1, t.shape[1:])
+        assert odd[name].data_ptr() % 32 == 16
+    pos = torch.arange(offset, offset + n, device="cuda")
+    slots = (f.dev_tables[0].long()[pos // 16] * 16 + pos % 16).to(torch.int32)
+    cache.kv4_append(f.pool, k, v, slots)
+    held = f.pool.data.clone()
+    cache.kv4_append(f.pool, odd["k"], odd["v"], slots)
+    assert torch.equal(f.pool.data, held)
+    lens = torch.arange(offset, offset + n, dtype=torch.int32, device="cuda")
+    tables = f.dev_tables[0].repeat(n, 1)
+    for call in (lambda q, o: cache.kv4_chunk(f.pool, q, f.dev_tables[0], offset, o),
+                 lambda q, o: cache.kv4_decode(f.pool, q, tables, lens, offset + n - 1, o)):
+        want = torch.empty_like(q)
+        call(q, want)
+        flat, out = _odd_rows(n, heads * d)
+        call(odd["q"], out.unflatten(1, (heads, d)))
+        assert torch.equal(out, want.reshape(n, -1))
+        out.fill_(7.0)
+        assert (flat == 7.0).all()
+    kw, vw = torch.empty_like(k), torch.empty_like(v)
+    cache.kv4_read(f.pool, slots, kw, vw)
+    (fk, ko), (fv, vo) = _odd_rows(n, kv * d), _odd_rows(n, kv * d)
+    cache.kv4_read(f.pool, slots, ko.unflatten(1, (kv, d)), vo.unflatten(1, (kv, d)))
+    assert torch.equal(ko, kw.reshape(n, -1)) and torch.equal(vo, vw.reshape(n, -1))
+    ko.fill_(7.0), vo.fill_(7.0)
+    assert (fk == 7.0).all() and (fv == 7.0).all()
+
+
 def test_captured_large_chunks_replay_on_two_streams():
     """Chunks of both item sizes in two graphs with workspaces of their own, replayed at once with new queries and
     another block table; the same answers as calls made one by one."""
