@@ -317,7 +317,7 @@ extern "C" long long hb_kv4_pool_bytes(int num_blocks, int n_kv_heads, int head_
 
 extern "C" int hb_kv4_append(const hb_kv4_pool *pool, const void *k, long long k_stride, const void *v,
                              long long v_stride, const int32_t *slots, int n_tokens, void *cuda_stream)
-{
+try {
     int rc = kv4_check_pool(pool);
     if (rc)
         return rc;
@@ -340,11 +340,13 @@ extern "C" int hb_kv4_append(const hb_kv4_pool *pool, const void *k, long long k
                          n_tokens) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
+} catch (...) {
+    return HB_ENOMEM;
 }
 
 extern "C" int hb_kv4_read(const hb_kv4_pool *pool, const int32_t *slots, int n_tokens, void *k, long long k_stride,
                            void *v, long long v_stride, void *cuda_stream)
-{
+try {
     int rc = kv4_check_pool(pool);
     if (rc)
         return rc;
@@ -367,4 +369,6 @@ extern "C" int hb_kv4_read(const hb_kv4_pool *pool, const int32_t *slots, int n_
                          v_stride) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
+} catch (...) {
+    return HB_ENOMEM;
 }

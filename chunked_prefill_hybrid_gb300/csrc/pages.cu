@@ -121,7 +121,7 @@ using namespace hb;
 
 extern "C" int hb_copy_pages(void *data, long long pool_stride, int n_pools, long long page_bytes, int num_blocks,
                              const int32_t *src, const int32_t *dst, int n, void *cuda_stream)
-{
+try {
     if (!data || n < 0 || n_pools < 1 || num_blocks < 1 || page_bytes < 16 || page_bytes % 16 || pool_stride % 16 ||
         (uintptr_t)data % 16 || (n > 0 && (!src || !dst)))
         return HB_EINVAL;
@@ -138,10 +138,12 @@ extern "C" int hb_copy_pages(void *data, long long pool_stride, int n_pools, lon
                       &launches) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
+} catch (...) {
+    return HB_ENOMEM;
 }
 
 extern "C" int hb_copy_blocks(hb_ctx *ctx, const int32_t *src, const int32_t *dst, int n)
-{
+try {
     if (!ctx)
         return HB_EINVAL;
     if (n < 0 || (n > 0 && (!src || !dst)))
@@ -159,4 +161,6 @@ extern "C" int hb_copy_blocks(hb_ctx *ctx, const int32_t *src, const int32_t *ds
     if (e != cudaSuccess)
         return ctx->set_error(HB_ECUDA, "hb_copy_blocks: %s", cudaGetErrorString(e));
     return HB_OK;
+} catch (...) {
+    return HB_ENOMEM;
 }

@@ -19,7 +19,8 @@
  *
  * Conventions: return 0 (HB_OK) or a negative HB_E* code (hb.h).  Arguments
  * the host can see are checked before any launch; on an error code other
- * than HB_ECUDA nothing was enqueued.  Work is enqueued on cuda_stream (a
+ * than HB_ECUDA and HB_ENOMEM (no host memory, from any call) nothing was
+ * enqueued.  Work is enqueued on cuda_stream (a
  * cudaStream_t, NULL = the legacy default stream) of the current device,
  * which must be the one the pointers belong to; no call waits, allocates or
  * keeps state, so every call may be captured into a CUDA graph.  Calls on
