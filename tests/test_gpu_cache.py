@@ -498,6 +498,39 @@ def test_captured_large_chunks_replay_on_two_streams():
         assert torch.equal(want, x["out"])
 
 
+@pytest.mark.parametrize("n,kv,group,d,most", [(65535, 1, 1, 64, 20), (3, 1, 200, 64, 500), (2, 300, 1, 128, 100),
+                                               (1000, 2, 9, 64, 40)])
+def test_decode_of_many_rows_and_heads(n, kv, group, d, most):
+    """Rows that share the pages of a few sequences, up to as many as a call takes; heads far beyond a CTA's eight."""
+    lens = [1 + j * (most - 1) // (min(n, 16) - 1) for j in range(min(n, 16))]
+    f = Filled(lens, kv, d, 25)
+    seq = torch.arange(n, device="cuda") % len(lens)
+    ctx = (torch.tensor(lens, dtype=torch.int32, device="cuda") - 1)[seq]
+    q, q64 = _bf(np.random.default_rng(26).standard_normal((n, kv * group, d)))
+    out = torch.empty_like(q)
+    cache.kv4_decode(f.pool, q, f.dev_tables[seq].contiguous(), ctx, most - 1, out)
+    got = _f64(out)
+    for i in sorted({0, 1, n // 3, n // 2, n - 2, n - 1} & set(range(n))):
+        j = i % len(lens)
+        o, bound = ref.attention_row(q64[i], *f.kv_of(j, lens[j]))
+        assert (np.abs(got[i] - o) <= bound).all(), i
+    if n > 65000:
+        with pytest.raises(HbError):
+            cache.kv4_decode(f.pool, torch.cat([q, q[:1]]), f.dev_tables[torch.cat([seq, seq[:1]])].contiguous(),
+                             torch.cat([ctx, ctx[:1]]), most - 1, torch.cat([out, out[:1]]))
+
+
+@pytest.mark.parametrize("n,kv,group,d,offset", [(20000, 1, 1, 64, 0), (30, 1, 200, 64, 900), (20, 300, 2, 128, 300),
+                                                 (1, 1, 500, 128, 2000)])
+def test_chunk_of_many_rows_and_heads(n, kv, group, d, offset):
+    f = Filled([offset + n], kv, d, 27)
+    q, q64 = _bf(np.random.default_rng(28).standard_normal((n, kv * group, d)))
+    out = torch.empty_like(q)
+    cache.kv4_chunk(f.pool, q, f.dev_tables[0], offset, out)
+    k, v = f.kv_of(0, offset + n)
+    _check_rows(_f64(out), q64, k, v, offset, sorted({0, 1, 127, 128, 9999, n // 2, n - 2, n - 1} & set(range(n))))
+
+
 def test_captured_calls_replay_with_new_contents_and_other_streams():
     """A step (append, decode, chunk) in two graphs, each with a workspace of its own, replayed at once on two
     streams with changed inputs; the same answers as calls made one by one."""
