@@ -80,6 +80,7 @@ def _int32(x) -> int:
     return x
 
 
+_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its look at whether CUDA is up: a tensor is
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits as elsewhere in the package
 _I32 = torch.int32
 
@@ -101,7 +102,7 @@ def _refuse(rows, ints):
     raise ValueError("the tensors must lie on one CUDA device")
 
 
-# Each call below looks at its tensors in one expression (a call takes some 8 us
+# Each call below looks at its tensors in one expression (a call takes some 6 us
 # of host time, half of it here), and says what is wrong in _refuse.  Kernels
 # launch on the current device, so a call on tensors of another one makes that
 # current first.
@@ -152,7 +153,7 @@ def kv4_append(pool: Kv4Pool, k, v, slots, stream=None):
         _refuse(((k, "k", n, kv, d), (v, "v", n, kv, d)), ((slots, "slots", 1, n),))
     if not n:
         return
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return kv4_append(pool, k, v, slots, stream)
     rc = _lib().hb_kv4_append(pool._addr, k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(), n,
@@ -172,7 +173,7 @@ def kv4_read(pool: Kv4Pool, slots, k_out, v_out, stream=None):
         _refuse(((k_out, "k_out", n, kv, d), (v_out, "v_out", n, kv, d)), ((slots, "slots", 1, n),))
     if not n:
         return
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return kv4_read(pool, slots, k_out, v_out, stream)
     rc = _lib().hb_kv4_read(pool._addr, slots.data_ptr(), n, k_out.data_ptr(), ks[0], v_out.data_ptr(), vs[0],
@@ -223,7 +224,7 @@ def kv4_decode(pool: Kv4Pool, q, block_tables, ctx_lens, max_ctx: int, out, work
                 ((block_tables, "block_tables", 2, n), (ctx_lens, "ctx_lens", 1, n)))
     if not n:
         return
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return kv4_decode(pool, q, block_tables, ctx_lens, max_ctx, out, workspace, stream)
     ws = _work(workspace, stream, dev, kv4_decode_workspace, n, heads, pool._kv, d, max_ctx)
@@ -249,7 +250,7 @@ def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=N
         _refuse(((q, "q", n, heads, pool._d), (out, "out", n, heads, pool._d)), ((block_table, "block_table", 1, -1),))
     if not n:
         return
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return kv4_chunk(pool, q, block_table, chunk_offset, out, workspace, stream)
     ws = _work(workspace, stream, dev, kv4_chunk_workspace, chunk_offset, n, heads, pool._kv, d)
@@ -260,8 +261,11 @@ def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=N
         _check(rc, "hb_kv4_chunk")
 
 
+_NP32 = np.dtype(np.int32)
+
+
 def _host_pages(a, name: str) -> np.ndarray:
-    if type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.c_contiguous:
+    if type(a) is np.ndarray and a.dtype is _NP32 and a.ndim == 1 and a.flags.c_contiguous:
         return a
     v = np.asarray(a)
     if v.ndim != 1 or (v.size and v.dtype.kind not in "iu"):
@@ -285,26 +289,30 @@ def copy_pages(pools, src: Sequence[int], dst: Sequence[int], stream=None):
     n = len(s)
     if n != len(d):
         raise ValueError("src and dst must have the same length")
-    shape, strides = pools.shape, pools.stride()
-    page = 1
-    dense = len(shape) >= 3 and shape[0] > 0 and shape[1] > 0
-    for size, step in zip(shape[:1:-1], strides[:1:-1]):
-        dense = dense and (step == page or size == 1)
-        page *= size
-    if not dense or (strides[1] != page and shape[1] > 1):
-        raise ValueError("pools must be a tensor [n_pools][num_blocks][...] with the pages of each pool dense")
+    shape = pools.shape
+    n_pools, blocks = shape[:2] if len(shape) >= 3 else (0, 0)
+    if pools.is_contiguous() and n_pools and blocks:
+        page = pools.numel() // (n_pools * blocks)
+        stride = page * blocks
+    else:
+        strides, page, dense = pools.stride(), 1, n_pools > 0 and blocks > 0
+        for size, step in zip(shape[:1:-1], strides[:1:-1]):
+            dense = dense and (step == page or size == 1)
+            page *= size
+        if not dense or (strides[1] != page and blocks > 1):
+            raise ValueError("pools must be a tensor [n_pools][num_blocks][...] with the pages of each pool dense")
+        stride = strides[0] if n_pools > 1 else page * blocks
     dev = pools.get_device()
     if dev < 0:
         raise ValueError("pools must lie on a CUDA device")
     if not n:
         return
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         with torch.cuda.device(dev):
             return copy_pages(pools, s, d, stream)
     es = pools.element_size()
-    page *= es
-    rc = _lib().hb_copy_pages(pools.data_ptr(), strides[0] * es if shape[0] > 1 else page * shape[1], shape[0], page,
-                              shape[1], _page_addr(s), _page_addr(d), n, _raw_stream(dev, stream))
+    rc = _lib().hb_copy_pages(pools.data_ptr(), stride * es, n_pools, page * es, blocks, _page_addr(s), _page_addr(d), n,
+                              _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_copy_pages")
 
