@@ -80,7 +80,7 @@ def _int32(x) -> int:
     return x
 
 
-_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its look at whether CUDA is up: a tensor is
+_device = torch._C._cuda_getDevice  # torch.cuda.current_device, for when a tensor shows that CUDA is up
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bits as elsewhere in the package
 _I32 = torch.int32
 
