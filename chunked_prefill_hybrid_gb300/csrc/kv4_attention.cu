@@ -111,16 +111,16 @@ __device__ __forceinline__ void pair_tokens(const uint32_t (&vw)[2][KW], int w, 
 
 // Shared memory of a CTA: a ring of RING pages for each warp, and after the
 // key loop (in the same place) the warps' results.
-template <int D>
+template <int D, int W>
 struct Smem {
-    static constexpr int RINGS = WARPS * RING * Layout<D>::BYTES;
+    static constexpr int RINGS = W * RING * Layout<D>::BYTES;
     static constexpr int ROW = D + 4;  // floats of a result row, off the banks of the next
-    static constexpr int JOIN = WARPS * 8 * ROW * 4;
+    static constexpr int JOIN = W * 8 * ROW * 4;
     static constexpr int BYTES = (RINGS > JOIN ? RINGS : JOIN);
 };
 
 // A warp reads pages of its own through a ring of bulk copies, four under way,
-// and works on two at a time; four warps a CTA join their results in shared
+// and works on two at a time; the W warps of a CTA join their results in shared
 // memory.  128 rows of 128 to 2048 keys, 40 heads of 128, take 94 us (5.5 TB/s,
 // 0.81 of the copy rate); 18 rows of 1024 keys 23.4 us; one row of 130999 keys,
 // 8 kv heads of 8, 36.2 us with the join.  Bound by the issue of conversions (two
@@ -134,15 +134,15 @@ struct Smem {
 // alone (zeros for the others'), so that one accumulator of four registers
 // takes every channel: 128 rows as above take 197 us with a multiplied K and V
 // and one page at a time, 97 so.
-template <int D, bool FEW>
-__global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const Kv4Attn p)
+template <int D, bool FEW, int W>
+__global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_attention(const Kv4Attn p)
 {
     using L = Layout<D>;
     constexpr int NB = L::NB, KW = NB / 2;  // words of a lane's 8- or 16-byte load
     constexpr int COLS = FEW ? 8 / NB : 8;  // queries of a CTA
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[WARPS][RING];
-    __shared__ float s_scale[8], s_m[WARPS][8], s_l[WARPS][8];
+    __shared__ uint64_t full[W][RING];
+    __shared__ float s_scale[8], s_m[W][8], s_l[W][8];
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
@@ -165,14 +165,14 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     // bt_stride of them): the context's length comes in the same time.
     const int k0 = split * p.split_len, b0 = (k0 >> 4) + warp;
     const int *tab = p.tables + (size_t)seq * p.bt_stride + b0;
-    int ids = b0 + lane * WARPS < p.bt_stride ? __ldg(tab + lane * WARPS) : 0;  // lane i: page of tile i of the current 32
+    int ids = b0 + lane * W < p.bt_stride ? __ldg(tab + lane * W) : 0;  // lane i: page of tile i of the current 32
     if (p.chunk_len == 0) {
         const int ctx = p.ctx_lens[seq];
         if (ctx < 0 || ctx > p.max_ctx) {  // padding: zeros; outside what the grid was sized for: NaN
             if (split == 0)
                 for (int c = c0; c < c1; ++c) {
                     const Col co = column(p, seq, kvh, c);
-                    for (int e = threadIdx.x; e < D; e += WARPS * 32)
+                    for (int e = threadIdx.x; e < D; e += W * 32)
                         p.out[co.row * p.out_stride + (size_t)co.head * D + e] =
                             f2bf(ctx == -1 ? 0.f : __int_as_float(0x7fc00000));
                 }
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         return;
     const int fewest = column(p, seq, kvh, c0).nkeys;  // keys that every query sees
 
-    const int n_tiles = max(0, (((k1 + 15) >> 4) - b0 + WARPS - 1) / WARPS);
+    const int n_tiles = max(0, (((k1 + 15) >> 4) - b0 + W - 1) / W);
     uint8_t *ring = smem + warp * RING * L::BYTES;
     bool bad = false;
     const uint8_t *head = p.pool + (size_t)kvh * L::BYTES;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         if (tile >= n_tiles)
             return;
         if ((tile & 31) == 0 && tile > 0)
-            ids = tile + lane < n_tiles ? __ldg(tab + (tile + lane) * WARPS) : 0;
+            ids = tile + lane < n_tiles ? __ldg(tab + (tile + lane) * W) : 0;
         const int mine = tile + (lane & (N - 1));
         const int blk = __shfl_sync(0xffffffffu, ids, mine & 31);
         const bool ok = blk >= 0 && blk < p.num_blocks;
@@ -345,8 +345,8 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 }
             }
             // ---- softmax
-            const int base = (b0 + (i + my_x) * WARPS) * 16;
-            const bool edge = (b0 + (i + 1) * WARPS) * 16 + 16 > min(fewest, k1);
+            const int base = (b0 + (i + my_x) * W) * 16;
+            const bool edge = (b0 + (i + 1) * W) * 16 + 16 > min(fewest, k1);
             bool raise = false;
 #pragma unroll
             for (int j = 0; j < M; ++j) {
@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 }
             }
             // ---- softmax: rows are tokens, columns queries
-            const int key = (b0 + i * WARPS) * 16 + tok0;
-            const bool edge = (b0 + (i + 1) * WARPS) * 16 + 16 > min(fewest, k1);
+            const int key = (b0 + i * W) * 16 + tok0;
+            const bool edge = (b0 + (i + 1) * W) * 16 + 16 > min(fewest, k1);
             bool raise = false;
 #pragma unroll
             for (int j = 0; j < Q; ++j) {
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                     s[x][j] = __fmul_rn(s[x][j], sc[j]);
                     s[x][2 + j] = __fmul_rn(s[x][2 + j], sc[j]);
                     if (edge) {
-                        const int lim = min(seen[j], k1) - key - x * WARPS * 16;
+                        const int lim = min(seen[j], k1) - key - x * W * 16;
                         s[x][j] = lim > 0 ? s[x][j] : -INFINITY;
                         s[x][2 + j] = lim > 2 ? s[x][2 + j] : -INFINITY;
                     }
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
     // ---- join the warps
     bad = __any_sync(0xffffffffu, bad);
     __syncthreads();  // the rings are done with
-    float(*s_o)[8][Smem<D>::ROW] = reinterpret_cast<float(*)[8][Smem<D>::ROW]>(smem);
+    float(*s_o)[8][Smem<D, W>::ROW] = reinterpret_cast<float(*)[8][Smem<D, W>::ROW]>(smem);
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
         if (FEW)
@@ -583,14 +583,14 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
                 *reinterpret_cast<float2 *>(&s_o[warp][2 * t + j][16 * i + 2 * g]) = make_float2(o[i][j], o[i][2 + j]);
     }
     __syncthreads();
-    for (int c = c0 + warp; c < c1; c += WARPS) {
+    for (int c = c0 + warp; c < c1; c += W) {
         const Col co = column(p, seq, kvh, c);
-        float M = LOWEST, lsum = 0.f, f[WARPS];
+        float M = LOWEST, lsum = 0.f, f[W];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w)
+        for (int w = 0; w < W; ++w)
             M = fmaxf(M, s_m[w][c - c0]);
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < W; ++w) {
             f[w] = ex2(s_m[w][c - c0] - M);
             lsum += s_l[w][c - c0] * f[w];
         }
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(WARPS * 32, FEW ? 5 : 4) k_kv4_attention(const
         for (int e = 2 * lane; e < D; e += 64) {
             float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float2 x = *reinterpret_cast<const float2 *>(&s_o[w][c - c0][e]);
                 v0 += x.x * f[w];
                 v1 += x.y * f[w];
@@ -749,19 +749,33 @@ bool few(int cols, int d) { return cols <= (d == 128 ? 1 : 2); }
 // CTAs of the attention kernel that an SM holds (registers), for plan_split.
 int resident(int rows, int cols, int d) { return rows > 1 ? 1 << 30 : few(cols, d) ? 6 : d == 128 ? 4 : 5; }
 
-template <int D, bool FEW>
-cudaError_t launch_d(const Kv4Attn &p, dim3 grid, cudaStream_t s)
+template <int D, bool FEW, int W>
+cudaError_t launch_w(const Kv4Attn &p, dim3 grid, cudaStream_t s)
 {
     // Six CTAs fit an SM.  Where five on each hold the whole grid they lie
     // more evenly with no room for a sixth: 720 CTAs (18 rows of 1024 keys, 40
     // heads) take 23.3 us so and 25.9 with room; 5120 (128 rows) 95.7 and 94.1.
-    constexpr int PAD = FEW && D == 128 ? 1024 : 0;
+    constexpr int PAD = FEW && D == 128 && W == WARPS ? 1024 : 0;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = kv4_allow_smem((const void *)k_kv4_attention<D, FEW>, Smem<D>::BYTES + PAD, done);
+    const cudaError_t e = kv4_allow_smem((const void *)k_kv4_attention<D, FEW, W>, Smem<D, W>::BYTES + PAD, done);
     if (e != cudaSuccess)
         return e;
-    const int bytes = Smem<D>::BYTES + ((long long)grid.x * grid.y <= 5 * SMS ? PAD : 0);
-    return launch_kernel(true, k_kv4_attention<D, FEW>, grid, dim3(WARPS * 32), bytes, s, p);
+    const int bytes = Smem<D, W>::BYTES + ((long long)grid.x * grid.y <= 5 * SMS ? PAD : 0);
+    return launch_kernel(true, k_kv4_attention<D, FEW, W>, grid, dim3(W * 32), bytes, s, p);
+}
+
+// Short contexts of more rows than run at once: one warp a CTA, which has no
+// others to wait for and to join, and four times as many rows are under way.
+// 40 heads: 85 rows of 5 keys 6.9 us against 13.5 with four warps, 128 rows of
+// 61 keys 12.4 against 25.9, of 256 keys 35.5 against 40.0, but 64 rows of 1001
+// keys 67.9 against 59.8; 8 kv heads of 8: 128 rows of 121 keys 10.1 against
+// 10.5, of 501 keys 23.2 against 20.2.
+template <int D, bool FEW>
+cudaError_t launch_d(const Kv4Attn &p, dim3 grid, cudaStream_t s)
+{
+    if (p.chunk_len == 0 && p.max_ctx < (FEW ? 256 : 128) && (long long)grid.x * grid.y > 6 * SMS)
+        return launch_w<D, FEW, 1>(p, grid, s);
+    return launch_w<D, FEW, WARPS>(p, grid, s);
 }
 
 int launch(Kv4Attn &p, int d, int seqs, int rows, cudaStream_t s)
@@ -877,7 +891,7 @@ static int plan_chunk(Kv4Attn &p, Kv4Chunk &c, int offset, int len, int n_heads,
     c.n_heads = n_heads;
     c.offset = offset;
     const double few = decode_kernel_us(offset, len, group, n_kv);
-    const bool tensor = (long long)len * group > 8 && few > 8;
+    const bool tensor = (long long)len * group > 8 && few > 6;  // below, no plan is faster
     if (tensor && !kv4_chunk_plan(c, len, d))
         return -1;
     if (tensor && c.us < few) {

@@ -499,7 +499,7 @@ def test_captured_large_chunks_replay_on_two_streams():
 
 
 @pytest.mark.parametrize("n,kv,group,d,most", [(65535, 1, 1, 64, 20), (3, 1, 200, 64, 500), (2, 300, 1, 128, 100),
-                                               (1000, 2, 9, 64, 40)])
+                                               (1000, 2, 9, 64, 40), (300, 4, 1, 128, 256), (400, 3, 4, 128, 128)])
 def test_decode_of_many_rows_and_heads(n, kv, group, d, most):
     """Rows that share the pages of a few sequences, up to as many as a call takes; heads far beyond a CTA's eight."""
     lens = [1 + j * (most - 1) // (min(n, 16) - 1) for j in range(min(n, 16))]
@@ -514,6 +514,15 @@ def test_decode_of_many_rows_and_heads(n, kv, group, d, most):
         j = i % len(lens)
         o, bound = ref.attention_row(q64[i], *f.kv_of(j, lens[j]))
         assert (np.abs(got[i] - o) <= bound).all(), i
+    # padding, contexts out of range and a bad block, among rows that stay what they were
+    odd_ctx, odd_tables, other = ctx.clone(), f.dev_tables[seq].contiguous(), torch.full_like(out, 7.0)
+    odd_ctx[0], odd_ctx[n // 2] = -1, most
+    odd_tables[n - 1, 0] = f.pool.num_blocks
+    cache.kv4_decode(f.pool, q, odd_tables, odd_ctx, most - 1, other)
+    assert (other[0] == 0).all() and torch.isnan(other[n // 2]).all() and torch.isnan(other[n - 1]).all()
+    same = torch.ones(n, dtype=torch.bool, device="cuda")
+    same[[0, n // 2, n - 1]] = False
+    assert torch.equal(other[same], out[same])
     if n > 65000:
         with pytest.raises(HbError):
             cache.kv4_decode(f.pool, torch.cat([q, q[:1]]), f.dev_tables[torch.cat([seq, seq[:1]])].contiguous(),
