@@ -891,7 +891,7 @@ static int plan_chunk(Kv4Attn &p, Kv4Chunk &c, int offset, int len, int n_heads,
     c.n_heads = n_heads;
     c.offset = offset;
     const double few = decode_kernel_us(offset, len, group, n_kv);
-    const bool tensor = (long long)len * group > 8 && few > 6;  // below, no plan is faster
+    const bool tensor = (long long)len * group > 8 && few > 8;  // below, no plan is much faster
     if (tensor && !kv4_chunk_plan(c, len, d))
         return -1;
     if (tensor && c.us < few) {
