@@ -25,7 +25,7 @@
 // the registers that the others do not need.
 //
 // What bounds it: at 512 rows over 15872 keys, 40 heads of 128 (169 GFLOP in
-// 130 us, 1.3 PFLOP/s of f16), two thirds of the issue slots and 56% of the
+// 130 us, 1.3 PFLOP/s of f16), two thirds of the issue slots and 61% of the
 // tensor pipe's time are taken: the softmax warps, whose exponentials and
 // conversions share the schedulers with the conversion of K and V, are the
 // longest way.  Small chunks (256 rows at 768 keys, 14.5 us) spend 3 us until
