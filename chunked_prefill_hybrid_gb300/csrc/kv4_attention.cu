@@ -74,10 +74,10 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
     return r;
 }
 
-// All ones in each half of x that is not 0.
-__device__ __forceinline__ uint32_t nonzero_mask(uint32_t x)
+// All ones in the bytes of the first n of four tokens.
+__device__ __forceinline__ uint32_t first_bytes(int n)
 {
-    return ((x & 0x00007fffu) ? 0x0000ffffu : 0u) | ((x & 0x7fff0000u) ? 0xffff0000u : 0u);
+    return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
 }
 
 // Row, head and visible keys of query column c of kv head kvh.
@@ -272,6 +272,10 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
             o[i][j] = 0.f;
 
     const int tok0 = 4 * (g >> 1) + (g & 1);  // tokens tok0 and tok0 + 2 are rows g and g + 8 of S^T
+    // Keys that the query of column g sees.  A slot that it does not see may
+    // hold anything, a NaN scale among it, and is kept out of V by its place;
+    // a weight of 0 does not say so, as those of keys that are seen may vanish.
+    const int seen_g = min(column(p, seq, kvh, min(c0 + (FEW ? g / NB : g), c1 - 1)).nkeys, k1);
     // a page that did not come: the rows get NaN, and no copy may land after
     // the CTA has ended
     auto lost = [&](int i) {
@@ -396,19 +400,15 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint8_t *pg = page + x * L::BYTES;
-                const uint32_t vs = *reinterpret_cast<const uint32_t *>(pg + L::v_scale(4 * t, g % NB));
+                uint32_t vs = *reinterpret_cast<const uint32_t *>(pg + L::v_scale(4 * t, g % NB));
+                if (edge)
+                    vs &= first_bytes(seen_g - (b0 + (i + x) * W) * 16 - 4 * t);
                 load_words<KW>(pg + L::v_code(4 * t, g, 0), vw[x][0]);
                 load_words<KW>(pg + L::v_code(4 * t + 2, g, 0), vw[x][1]);
                 const uint32_t p0 = movmatrix(__byte_perm(pr[x], 0, 0x1010));  // tokens 4t, 4t + 1
                 const uint32_t p1 = movmatrix(__byte_perm(pr[x], 0, 0x3232));  // tokens 4t + 2, 4t + 3
                 pb[x][0] = hmul2(p0, from_e4m3x2(vs & 0xffffu));
                 pb[x][1] = hmul2(p1, from_e4m3x2(vs >> 16));
-                if (edge) {
-                    // a slot that a query does not see may hold anything, a NaN
-                    // scale among it: where P is 0 so is its product
-                    pb[x][0] &= nonzero_mask(p0);
-                    pb[x][1] &= nonzero_mask(p1);
-                }
             }
             __syncwarp();  // the slots are read
             issue(i + RING, std::integral_constant<int, 2>());
@@ -526,9 +526,7 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                 }
                 const uint32_t p0 = movmatrix(pack_h2(s[x][0], s[x][Q - 1]));      // column g, tokens 4t, 4t + 1
                 const uint32_t p1 = movmatrix(pack_h2(s[x][2], s[x][2 + Q - 1]));  // tokens 4t + 2, 4t + 3
-                // a slot that a query does not see may hold anything, a NaN
-                // scale among it: where P is 0 so is its product
-                const uint32_t z0 = edge ? nonzero_mask(p0) : 0xffffffffu, z1 = edge ? nonzero_mask(p1) : 0xffffffffu;
+                const uint32_t z = first_bytes(edge ? seen_g - (b0 + (i + x) * W) * 16 - 4 * t : 4);
 #pragma unroll
                 for (int w = 0; w < KW / 2; ++w) {
                     uint32_t a[4][4];
@@ -537,8 +535,8 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                     for (int j = 0; j < 4; ++j) {
                         uint32_t pb0 = hmul2(p0, from_e4m3x2(vst[4 * w + j])), pb1 = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16));
                         if (edge) {
-                            pb0 &= z0;
-                            pb1 &= z1;
+                            pb0 &= __byte_perm(z, 0, 0x1100);
+                            pb1 &= __byte_perm(z, 0, 0x3322);
                         }
                         mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb0, pb1);
                     }
