@@ -198,5 +198,13 @@ __device__ __forceinline__ float ex2(float x)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOWEST = -3e38f;  // below every score, and finite: differences with it are too
 
+// Where the weights P = 2^(s - m) lie in f16, whose range is 2^-24 (a
+// subnormal's last bit) to 2^16: the reference m is 2^LIFT below the largest
+// score when it moves, and moves when a score passes it by LIFT + RAISE.  So P
+// is at most 2^15, and a key of 2^-36 of the largest weight still counts; with
+// the reference at the largest score, keys behind an attention sink (2^-25 of
+// the largest weight) left the sum of V and stayed in the sum of P.
+constexpr float LIFT = 11.f, RAISE = 4.f;
+
 }  // namespace kv4
 }  // namespace hb

@@ -28,7 +28,6 @@ namespace {
 using namespace kv4;
 using namespace tc;
 
-constexpr float RAISE = 7.f;          // P <= 2^7: times a V scale (at most 448) it stays finite in f16
 constexpr int WARPS = 4;
 constexpr int RING = 4;               // pages a warp has in flight
 constexpr int JOIN_WARPS = 8;
@@ -121,9 +120,9 @@ struct Smem {
 
 // A warp reads pages of its own through a ring of bulk copies, four under way,
 // and works on two at a time; the W warps of a CTA join their results in shared
-// memory.  128 rows of 128 to 2048 keys, 40 heads of 128, take 94 us (5.5 TB/s,
-// 0.81 of the copy rate); 18 rows of 1024 keys 23.4 us; one row of 130999 keys,
-// 8 kv heads of 8, 36.2 us with the join.  Bound by the issue of conversions (two
+// memory.  128 rows of 128 to 2048 keys, 40 heads of 128, take 97 us (5.3 TB/s,
+// 0.79 of the copy rate); 18 rows of 1024 keys 23.4 us; one row of 130999 keys,
+// 8 kv heads of 8, 35.9 us with the join.  Bound by the issue of conversions (two
 // thirds of the slots) and, where there is one wave of CTAs, by their start.
 //
 // FEW: one query (d = 128) or two (d = 64) share the kv head.  The eight
@@ -133,9 +132,17 @@ struct Smem {
 // column (c, i) holds P times the scales of block i, for channel block i's MMA
 // alone (zeros for the others'), so that one accumulator of four registers
 // takes every channel: 128 rows as above take 197 us with a multiplied K and V
-// and one page at a time, 97 so.
+// and one page at a time, 97 so.  A small weight times a small scale would
+// leave f16's range, so the scales of a column are brought near 1 by a power of
+// two, and the accumulator back at the end: 3% of the time of 128 rows.  What a
+// key adds is lost only where its weight times its V scale is below 2^-34 of the
+// largest weight times the largest scale.
+//
+// Else the scales multiply V's codes, which is exact, and P is all that a
+// column holds: one power of two for each of eight blocks and eight queries
+// would cost as much.
 template <int D, bool FEW, int W>
-__global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_attention(const Kv4Attn p)
+__global__ void __launch_bounds__(W * 32, (FEW ? (D == 128 && W == WARPS ? 6 : 5) : 4) * WARPS / W) k_kv4_attention(const Kv4Attn p)
 {
     using L = Layout<D>;
     constexpr int NB = L::NB, KW = NB / 2;  // words of a lane's 8- or 16-byte load
@@ -248,10 +255,11 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
     __syncthreads();
 
     // Running reference of the softmax (log2).  It moves only when a score
-    // passes it by RAISE: P stays below 2^RAISE, and a tile costs one vote
-    // instead of a maximum over its lanes.  Scores may be so large that their
-    // last place is worth more than RAISE: the sum is rounded down, and the
-    // products that are compared are those that the exponent is taken of.
+    // passes it by LIFT + RAISE: P stays at 2^15 or below, and a tile costs one
+    // vote instead of a maximum over its lanes.  Scores may be so large that
+    // their last place is worth more than that: the sum that they are compared
+    // with is rounded down, the new reference up, and the products that are
+    // compared are those that the exponent is taken of.
     constexpr int Q = FEW ? 1 : 2;  // queries this lane keeps: its own column's, or columns 2t and 2t + 1
     const int myq = FEW ? (2 * t) / NB : 2 * t;
     float sc[Q], m[Q], l[Q];
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
     // Keys that the query of column g sees.  A slot that it does not see may
     // hold anything, a NaN scale among it, and is kept out of V by its place;
     // a weight of 0 does not say so, as those of keys that are seen may vanish.
-    const int seen_g = min(column(p, seq, kvh, min(c0 + (FEW ? g / NB : g), c1 - 1)).nkeys, k1);
+    const int seen_g = FEW ? min(column(p, seq, kvh, min(c0 + g / NB, c1 - 1)).nkeys, k1) : 0;
     // a page that did not come: the rows get NaN, and no copy may land after
     // the CTA has ended
     auto lost = [&](int i) {
@@ -299,6 +307,12 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
 #pragma unroll
         for (int i = 0; i < NB; ++i)
             only[i] = g % NB == i ? 0x3c003c00u : 0u;
+        // 2^lift_e that column g's V scales are multiplied by, as an f16 pair;
+        // and what carries a byte of a scale past 0x7f if it makes 2 or more.
+        // It moves to bring the largest to [1/4, 1/2): with [1, 2) pages whose
+        // scales grow a little cost 132 us in place of 129.
+        uint32_t lift = 0x58005800u, over = 0x78787878u;  // 2^7: the smallest scale is 2^-9
+        auto lift_e = [&]() { return (int)(lift >> 26) - 15; };
         for (int i = 0; i < n_tiles; i += 2) {
             if (!arrived(i, i + 1 < n_tiles)) {
                 lost(i);
@@ -351,13 +365,21 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
             // ---- softmax
             const int base = (b0 + (i + my_x) * W) * 16;
             const bool edge = (b0 + (i + 1) * W) * 16 + 16 > min(fewest, k1);
+            uint32_t vs[2];
             bool raise = false;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                vs[x] = *reinterpret_cast<const uint32_t *>(page + x * L::BYTES + L::v_scale(4 * t, g % NB));
+                if (edge)
+                    vs[x] &= first_bytes(seen_g - (b0 + (i + x) * W) * 16 - 4 * t);
+                raise |= (((vs[x] & 0x7f7f7f7fu) + over) & 0x80808080u) != 0;
+            }
 #pragma unroll
             for (int j = 0; j < M; ++j) {
                 s[j] = __fmul_rn(s[j], sc[0]);
                 if (edge)
                     s[j] = base + tok0 + 2 * (D == 128 ? (int)b0_ : j) < lim ? s[j] : -INFINITY;
-                raise |= s[j] > __fadd_rd(m[0], RAISE);
+                raise |= s[j] > __fadd_rd(m[0], LIFT + RAISE);
             }
             if (__any_sync(0xffffffffu, raise)) {
                 float mx = M == 2 ? fmaxf(s[0], s[M - 1]) : s[0];
@@ -367,14 +389,28 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float mn = fmaxf(m[0], mx), corr = ex2(m[0] - mn);
+                const float mn = fmaxf(m[0], __fadd_ru(mx, -LIFT)), corr = ex2(m[0] - mn);
                 m[0] = mn;
                 l[0] *= corr;
+                uint32_t top = 0;  // the largest V scale of column g
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t b = vs[j / 4] >> (8 * (j & 3)) & 0x7fu;
+                    top = b == 0x7fu ? top : max(top, b);
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = top >= 8 ? 5 - (int)(top >> 3) : top > 0 ? 7 - (31 - __clz(top)) : 7;
+                const int had = lift_e(), now = min(had, e);
+                lift = (uint32_t)(now + 15) * 0x04000400u;
+                over = (uint32_t)max(64 + 8 * now, 0) * 0x01010101u;  // 0x80 less the code of 2^(1 - now)
+                const float down = pow2(now - had);
+                const float f[2] = {__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4)};
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        o[x][j] *= corr;
+                        o[x][j] *= corr * f[j & 1];
             }
 #pragma unroll
             for (int j = 0; j < M; ++j) {
@@ -400,15 +436,12 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint8_t *pg = page + x * L::BYTES;
-                uint32_t vs = *reinterpret_cast<const uint32_t *>(pg + L::v_scale(4 * t, g % NB));
-                if (edge)
-                    vs &= first_bytes(seen_g - (b0 + (i + x) * W) * 16 - 4 * t);
                 load_words<KW>(pg + L::v_code(4 * t, g, 0), vw[x][0]);
                 load_words<KW>(pg + L::v_code(4 * t + 2, g, 0), vw[x][1]);
                 const uint32_t p0 = movmatrix(__byte_perm(pr[x], 0, 0x1010));  // tokens 4t, 4t + 1
                 const uint32_t p1 = movmatrix(__byte_perm(pr[x], 0, 0x3232));  // tokens 4t + 2, 4t + 3
-                pb[x][0] = hmul2(p0, from_e4m3x2(vs & 0xffffu));
-                pb[x][1] = hmul2(p1, from_e4m3x2(vs >> 16));
+                pb[x][0] = hmul2(p0, hmul2(from_e4m3x2(vs[x] & 0xffffu), lift));
+                pb[x][1] = hmul2(p1, hmul2(from_e4m3x2(vs[x] >> 16), lift));
             }
             __syncwarp();  // the slots are read
             issue(i + RING, std::integral_constant<int, 2>());
@@ -424,7 +457,36 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                                 hmul2(pb[x][1], only[4 * w + j]));
                 }
         }
+        const float down = pow2(-lift_e());
+        const float f[2] = {__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4)};
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[x][j] *= f[j & 1];
     } else {
+        // Slots that some queries see and others do not (a chunk's rows): a NaN
+        // scale among them is taken out and put into the sums of those that do.
+        auto hidden_nans = [&](uint32_t(&vst)[NB], int base) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < NB; ++w)
+                any |= (vst[w] & 0x7f7f7f7fu) + 0x01010101u;
+            if (!__any_sync(0xffffffffu, (any & 0x80808080u) != 0))
+                return;
+#pragma unroll
+            for (int w = 0; w < NB; ++w) {
+                const uint32_t nan = ((vst[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                vst[w] &= ~((nan >> 7) * 0xffu);
+                int first = nan ? base + (__ffs(nan) - 1) / 8 : MAX_KEYS;
+                first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+                first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (first < seen[j])
+                        o[w][j] = o[w][2 + j] = __int_as_float(0x7fc00000);
+            }
+        };
         // two pages at a time, scaled by their blocks' scales
         for (int i = 0; i < n_tiles; i += 2) {
             if (!arrived(i, i + 1 < n_tiles)) {
@@ -483,7 +545,7 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                         s[x][2 + j] = lim > 2 ? s[x][2 + j] : -INFINITY;
                     }
                 }
-                raise |= fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j])) > __fadd_rd(m[j], RAISE);
+                raise |= fmaxf(fmaxf(s[0][j], s[0][2 + j]), fmaxf(s[1][j], s[1][2 + j])) > __fadd_rd(m[j], LIFT + RAISE);
             }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -492,7 +554,7 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mn = fmaxf(m[j], mx), corr = ex2(m[j] - mn);
+                    const float mn = fmaxf(m[j], __fadd_ru(mx, -LIFT)), corr = ex2(m[j] - mn);
                     m[j] = mn;
                     l[j] *= corr;
 #pragma unroll
@@ -510,7 +572,7 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                     s[x][2 + j] = ex2(s[x][2 + j] - m[j]);
                     l[j] += s[x][j] + s[x][2 + j];
                 }
-            // ---- O^T += V^T P, a V scale times P in place of a scaled V
+            // ---- O^T += V^T P, V scaled
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint8_t *pg = page + x * L::BYTES;
@@ -526,19 +588,24 @@ __global__ void __launch_bounds__(W * 32, (FEW ? 5 : 4) * WARPS / W) k_kv4_atten
                 }
                 const uint32_t p0 = movmatrix(pack_h2(s[x][0], s[x][Q - 1]));      // column g, tokens 4t, 4t + 1
                 const uint32_t p1 = movmatrix(pack_h2(s[x][2], s[x][2 + Q - 1]));  // tokens 4t + 2, 4t + 3
-                const uint32_t z = first_bytes(edge ? seen_g - (b0 + (i + x) * W) * 16 - 4 * t : 4);
+                if (edge) {
+                    const int base = (b0 + (i + x) * W) * 16 + 4 * t;
+                    const uint32_t z = first_bytes(k1 - base);
+#pragma unroll
+                    for (int w = 0; w < NB; ++w)
+                        vst[w] &= z;  // slots that no query sees
+                    if (fewest < k1)
+                        hidden_nans(vst, base);
+                }
 #pragma unroll
                 for (int w = 0; w < KW / 2; ++w) {
                     uint32_t a[4][4];
                     pair_tokens<KW>(vw, w, a);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t pb0 = hmul2(p0, from_e4m3x2(vst[4 * w + j])), pb1 = hmul2(p1, from_e4m3x2(vst[4 * w + j] >> 16));
-                        if (edge) {
-                            pb0 &= __byte_perm(z, 0, 0x1100);
-                            pb1 &= __byte_perm(z, 0, 0x3322);
-                        }
-                        mma_f16(o[4 * w + j], a[0][j], a[1][j], a[2][j], a[3][j], pb0, pb1);
+                        const uint32_t s0 = from_e4m3x2(vst[4 * w + j]), s1 = from_e4m3x2(vst[4 * w + j] >> 16);
+                        mma_f16(o[4 * w + j], hmul2(a[0][j], s0), hmul2(a[1][j], s0), hmul2(a[2][j], s1),
+                                hmul2(a[3][j], s1), p0, p1);
                     }
                 }
             }

@@ -95,7 +95,11 @@ int hb_kv4_read(const hb_kv4_pool *pool, const int32_t *slots, int n_tokens, voi
  * 0..ctx_lens[j] of its own sequence, softmax(q k^T / sqrt(head_dim)) v, head
  * h reading kv head h / (n_heads / n_kv_heads).  The values are those that
  * hb_kv4_read gives, before their rounding to bf16; sums and softmax
- * statistics are fp32.
+ * statistics are fp32.  The weights lie in f16 (11 bits) about the row's
+ * largest: a key may add nothing to the sum of V where its weight is below
+ * 2^-36 of the largest, or, where one query (head_dim 128) or two (64) share a
+ * kv head, where its weight times its V scale is below 2^-34 of the largest
+ * weight times the largest V scale of the 16 channels.
  *   q, out:       device bf16, row j at q + j * q_stride elements, [n_heads]
  *                 [head_dim] dense inside a row; conditions as k above.
  *                 out may not overlap q or the pool

@@ -88,3 +88,47 @@ def test_a_nan_of_v_counts_however_small_its_weight(kv, group, d):
                 o, bound = ref.attention_row(q64[i], h.k[:m], clean[:m])
                 rest = np.r_[0:16, 32:d]
                 assert (np.abs(out[i].double().cpu().numpy() - o) <= bound)[:, rest].all(), (key, i, m)
+
+
+# V's sizes: small ones, 18 powers of two between blocks of a head, growing and shrinking along the sequence, and a
+# token far above the rest
+SIZES = {
+    "small": lambda n, kv, d, rng: np.full((n, 1, 1), 0.02),
+    "large": lambda n, kv, d, rng: np.full((n, 1, 1), 300.0),
+    "blocks": lambda n, kv, d, rng: np.repeat(2.0 ** np.linspace(-7, 9, d // 16), 16)[None, None],
+    "growing": lambda n, kv, d, rng: 2.0 ** np.linspace(-7, 5, n)[:, None, None],
+    "shrinking": lambda n, kv, d, rng: 2.0 ** np.linspace(5, -7, n)[:, None, None],
+    "outlier": lambda n, kv, d, rng: np.where(np.arange(n) == n // 3, 4.0, 0.02)[:, None, None],
+    "zeros first": lambda n, kv, d, rng: np.where(np.arange(n) < n // 2, 0.0, 0.02)[:, None, None],
+}
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("kv,group,d", FORMS)
+def test_a_sink_takes_no_bits_from_the_rest(kv, group, d, size):
+    """One key 2^18 to 2^24 above each of the others, its V near zero: what the others add is kept, whatever V's size."""
+    n = 3000
+    rng = np.random.default_rng(4)
+    for gap, at in ((18, 0), (24, 5)):
+        q, k = _peaked(rng, 4, n, kv, group, d, gap, at)
+        v = rng.standard_normal((n, kv, d)) * SIZES[size](n, kv, d, rng)
+        v[at] *= 0.001
+        h = Held(k, v)
+        qd, q64 = _bf(q)
+        lens = [n, 1000, n - 5, 70]
+        _near(h.decode(qd, lens), q64, h.k, h.v, list(enumerate(lens)))
+        _near(h.decode(qd[:1], [n]), q64, h.k, h.v, [(0, n)])                   # split over CTAs
+        _near(h.chunk(qd[:1], n - 1), q64, h.k, h.v, [(0, n)])
+        _near(h.chunk(qd, n - 4), q64, h.k, h.v, [(i, n - 3 + i) for i in range(4)])
+
+
+@pytest.mark.parametrize("kv,group,d", [(1, 1, 128), (1, 4, 64), (1, 8, 128)])
+def test_a_sink_over_many_keys(kv, group, d):
+    n = 40000
+    q, k = _peaked(np.random.default_rng(5), 2, n, kv, group, d, 27, 0)
+    v = np.random.default_rng(6).standard_normal((n, kv, d)) + 0.3
+    v[0] *= 0.001
+    h = Held(k, v)
+    qd, q64 = _bf(q)
+    _near(h.decode(qd[:1], [n]), q64, h.k, h.v, [(0, n)])
+    _near(h.decode(qd, [n, n - 100]), q64, h.k, h.v, [(0, n), (1, n - 100)])
