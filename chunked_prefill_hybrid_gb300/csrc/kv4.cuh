@@ -203,7 +203,9 @@ constexpr float LOWEST = -3e38f;  // below every score, and finite: differences 
 // score when it moves, and moves when a score passes it by LIFT + RAISE.  So P
 // is at most 2^15, and a key of 2^-36 of the largest weight still counts; with
 // the reference at the largest score, keys behind an attention sink (2^-25 of
-// the largest weight) left the sum of V and stayed in the sum of P.
+// the largest weight) left the sum of V and stayed in the sum of P.  512 rows at
+// 15872 keys take 130 us so, 135 with 13 and 2 (the reference moves oftener),
+// and 130 with 8 and 7.
 constexpr float LIFT = 11.f, RAISE = 4.f;
 
 }  // namespace kv4

@@ -9,8 +9,8 @@
 // CTAs share leaves fp32 partials, which a second kernel joins.
 //
 //   warps 0..7    softmax, one thread per query: S from tensor memory, P back
-//                 into it as f16; O is rescaled only when a maximum rises by
-//                 more than 2^8
+//                 into it as f16, at most 2^15; O is rescaled only when a
+//                 maximum has risen by more than 2^4 (RAISE)
 //   warps 8..19   three groups of four, a group a sub-tile of 64 keys, a warp a
 //                 page: codes and scales -> f16 rows of the K and V tiles
 //                 (128-byte swizzle); code x scale is exact in f16
@@ -59,7 +59,6 @@ constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 48;
 constexpr int RING = 24;                 // pages in flight
 constexpr int STAGES = 3;                // sub-tiles of 64 keys of K, and of V, in f16
 constexpr int STAGES_DUAL = 4;           // the same where both halves share one Q tile
-constexpr float RAISE = 8.f;             // P <= 2^8
 constexpr float HUGE_SCORE = 1 << 20;    // up to it v sc - m may be fused: m is rounded by 2^-4 at most, for all P alike
 constexpr uint64_t WAIT_NS = 2000000000ull;  // after which a wait is given up
 
@@ -619,10 +618,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 const float mx = __fmul_rn(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sc);
                 float by = sc, off = -m;  // P = 2^(v by + off)
                 if (__any_sync(0xffffffffu, mx > raise_at)) {
-                    const float mn = fmaxf(m, mx), corr = ex2(m - mn);
+                    const float mn = fmaxf(m, __fadd_ru(mx, -LIFT)), corr = ex2(m - mn);
                     m = mn;
                     l *= corr;
-                    raise_at = m + RAISE;
+                    raise_at = __fadd_rd(m, LIFT + RAISE);
                     off = -m;
                     if (fabsf(m) > HUGE_SCORE) {
                         // the product rounded as m was, then m off; and here again with every sub-tile

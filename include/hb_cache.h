@@ -132,7 +132,8 @@ long long hb_kv4_decode_workspace(int n_decodes, int n_heads, int n_kv_heads, in
  *                0..chunk_offset + chunk_len - 1 (HB_ERANGE if n_blocks is
  *                too small).  A block id outside the pool makes the rows that
  *                attend to it NaN (and may make other rows of the chunk NaN)
- * Workspace, errors and rounding as for hb_kv4_decode; chunk_offset +
+ * Workspace and errors as for hb_kv4_decode, rounding as there or with V scales
+ * of any size beside each other (2^-36 of the largest weight); chunk_offset +
  * chunk_len is at most 2^27, chunk_len times the heads of a kv head at most
  * 2^24 (HB_ERANGE, also for a chunk of more work than a launch can count, of
  * the order of 10^18 scores).  chunk_len = 0 does nothing. */

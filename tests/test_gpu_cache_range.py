@@ -132,3 +132,33 @@ def test_a_sink_over_many_keys(kv, group, d):
     qd, q64 = _bf(q)
     _near(h.decode(qd[:1], [n]), q64, h.k, h.v, [(0, n)])
     _near(h.decode(qd, [n, n - 100]), q64, h.k, h.v, [(0, n), (1, n - 100)])
+
+
+@pytest.mark.parametrize("kv,group,d,offset,n", [(40, 1, 128, 1000, 130), (4, 2, 64, 2000, 257), (1, 8, 128, 20000, 64),
+                                                 (2, 4, 128, 3000, 600)])
+@pytest.mark.parametrize("gap", [20, 27, 31])
+def test_a_sink_in_a_large_chunk(kv, group, d, offset, n, gap):
+    q, k = _peaked(np.random.default_rng(7), n, offset + n, kv, group, d, gap, 3)
+    v = np.random.default_rng(8).standard_normal((offset + n, kv, d)) + 0.3
+    v[3] = 0
+    h = Held(k, v)
+    qd, q64 = _bf(q)
+    rows = sorted({0, 1, 127 // group, 128 // group, n // 2, n - 1} & set(range(n)))
+    _near(h.chunk(qd, offset), q64, h.k, h.v, [(i, offset + i + 1) for i in rows])
+
+
+@pytest.mark.parametrize("kv,group,d,offset,n", [(2, 1, 128, 0, 700), (2, 1, 64, 100, 3), (2, 4, 128, 600, 200),
+                                                 (1, 8, 64, 2000, 2)])
+def test_scores_that_rise_all_along(kv, group, d, offset, n):
+    """Each key above the one before it: the running maximum moves in every tile."""
+    rng = np.random.default_rng(9)
+    m = offset + n
+    u = rng.standard_normal((kv, d))
+    q = np.repeat(u, group, axis=0)[None] + 0.05 * rng.standard_normal((n, kv * group, d))
+    for reach in (30.0, 400.0):                              # of the scores, from the first key to the last
+        k = u[None] * np.linspace(0, reach / np.sqrt(d), m)[:, None, None]
+        h = Held(k, rng.standard_normal((m, kv, d)) * 0.1 + 0.05)
+        qd, q64 = _bf(q)
+        rows = sorted({0, 1, n // 2, n - 1} & set(range(n)))
+        _near(h.chunk(qd, offset), q64, h.k, h.v, [(i, offset + i + 1) for i in rows])
+        _near(h.decode(qd[:3], [m, m // 2, 1][:min(3, n)]), q64, h.k, h.v, list(enumerate([m, m // 2, 1][:min(3, n)])))
