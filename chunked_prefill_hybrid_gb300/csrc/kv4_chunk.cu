@@ -1036,6 +1036,7 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
 namespace {
 
 constexpr double SWITCH_US = 5, JOIN_US = 2, PART_US = 0.25, BYTES_PER_US = 2.5e6;
+constexpr int MAX_UNITS = 1 << 28;  // of a CTA: the kernel counts pages, eight a unit, in 32 bits
 constexpr int MANY_ITEMS = 640;  // from here on an even cut loses little, and a search would cost the host
 
 enum Way { PARTS, WHOLE, EVEN };
@@ -1132,15 +1133,15 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int d)
     p.us = cut.us;
     p.shared = false;
     p.ctas = 0;
+    bool fits = true;
     auto add = [&](int kvh, int qt, int kt0, long long units) {
+        fits &= units < MAX_UNITS;
         p.start[p.ctas++] = KcStart{kvh, qt, kt0, (int)units};
         p.shared |= kt0 > 0;
     };
     const int change = change_tiles(p.rows, d);
     if (cut.way == EVEN) {
         const long long ctas = p.units < KC_CTAS ? p.units : KC_CTAS;
-        if (p.units / ctas >= 0x3fffffff)
-            return false;
         const long long all = p.units + (long long)p.n_qt * p.n_kv * change;
         // the item at hand: its load begins at `from`, its units at `before`
         long long from = 0, before = 0, at = 0;
@@ -1164,7 +1165,7 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int d)
             at = next;
             at_kvh = kvh, at_qt = qt, at_kt = kt;
         }
-        return true;
+        return fits;
     }
     long long load = 0;
     for (int kvh = 0; kvh < p.n_kv; ++kvh)
@@ -1184,7 +1185,7 @@ bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int d)
                 load += n + change;
             }
         }
-    return true;
+    return fits;  // WHOLE is for a few hundred items, whose tiles a CTA can always count
 }
 
 long long kv4_chunk_workspace_bytes(const Kv4Chunk &p, int d)

@@ -39,7 +39,7 @@ struct Kv4Chunk {
 };
 
 // Plan the work of a chunk (host): everything but the pointers.  False when a
-// CTA's units would not fit 32 bits.
+// CTA would have more units than it can count.
 bool kv4_chunk_plan(Kv4Chunk &p, int chunk_len, int head_dim);
 long long kv4_chunk_workspace_bytes(const Kv4Chunk &p, int head_dim);
 cudaError_t launch_kv4_chunk(const Kv4Chunk &p, int head_dim, cudaStream_t s);

@@ -136,7 +136,7 @@ long long hb_kv4_decode_workspace(int n_decodes, int n_heads, int n_kv_heads, in
  * of any size beside each other (2^-36 of the largest weight); chunk_offset +
  * chunk_len is at most 2^27, chunk_len times the heads of a kv head at most
  * 2^24 (HB_ERANGE, also for a chunk of more work than a launch can count, of
- * the order of 10^18 scores).  chunk_len = 0 does nothing. */
+ * the order of 10^15 scores).  chunk_len = 0 does nothing. */
 int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_stride, const int32_t *block_table, int n_blocks,
                  int chunk_offset, int chunk_len, int n_heads, void *out, long long out_stride, void *workspace,
                  long long workspace_bytes, void *cuda_stream);

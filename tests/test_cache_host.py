@@ -306,3 +306,13 @@ def test_binding_checks_tensors(L):
             cache.copy_pages(pools, src, dst)
     with pytest.raises(ValueError):
         cache.copy_pages(pools.transpose(1, 2), [0], [1])
+
+
+def test_chunks_of_more_work_than_a_cta_can_count_are_refused(L):
+    """A CTA counts its pages, eight a key tile, in 32 bits: 2^28 tiles are more than it may have."""
+    most, last = 1 << 27, 1 << 24
+    assert L.hb_kv4_chunk_workspace(most - last, last, 2, 2, 64) == HB_EINVAL       # some 8.5e8 tiles a CTA
+    assert _chunk(L, off=most - last, n=last, heads=2, qs=256, os=256, nb=most // 16) == HB_ERANGE
+    assert cache.kv4_chunk_workspace(most - last // 4, last // 4, 2, 2, 64) >= 0    # 2.2e8
+    assert L.hb_kv4_chunk_workspace(most - last // 2, last // 2, 2, 2, 64) == HB_EINVAL
+    assert cache.kv4_chunk_workspace(most - 512, 512, 64, 8, 128) >= 0
