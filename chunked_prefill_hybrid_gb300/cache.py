@@ -351,7 +351,7 @@ class PageTable:
 
     def compact(self, max_moves: Optional[int] = None) -> Tuple[np.ndarray, np.ndarray]:
         """(src, dst) of the page moves that bring held pages to the front, for copy_pages."""
-        m = self.num_blocks if max_moves is None else min(index(max_moves), self.num_blocks)
+        m = self.num_blocks if max_moves is None else _int32(min(index(max_moves), self.num_blocks))
         src, dst = np.empty(max(m, 1), np.int32), np.empty(max(m, 1), np.int32)
         n = _check(self.L.hb_pages_compact(self.h, src.ctypes.data, dst.ctypes.data, m), "hb_pages_compact")
         return src[:n], dst[:n]

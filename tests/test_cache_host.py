@@ -316,3 +316,17 @@ def test_chunks_of_more_work_than_a_cta_can_count_are_refused(L):
     assert cache.kv4_chunk_workspace(most - last // 4, last // 4, 2, 2, 64) >= 0    # 2.2e8
     assert L.hb_kv4_chunk_workspace(most - last // 2, last // 2, 2, 2, 64) == HB_EINVAL
     assert cache.kv4_chunk_workspace(most - 512, 512, 64, 8, 128) >= 0
+
+
+def test_compact_refuses_a_count_past_32_bits(L):
+    """-2^32 + 5 is not 5: the arrays for the moves would have room for one."""
+    t = cache.PageTable(8)
+    t.extend(1, 128)
+    for most in (-(1 << 32) + 5, -(1 << 32), -(1 << 40) + 1):
+        with pytest.raises(HbError) as e:
+            t.compact(most)
+        assert e.value.code == HB_ERANGE
+    with pytest.raises(HbError) as e:
+        t.compact(-1)
+    assert e.value.code == HB_EINVAL
+    assert t.table(1).tolist() == list(range(8))
