@@ -156,8 +156,8 @@ def kv4_append(pool: Kv4Pool, k, v, slots, stream=None):
     if dev != _device():
         with torch.cuda.device(dev):
             return kv4_append(pool, k, v, slots, stream)
-    rc = _lib().hb_kv4_append(pool._addr, k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(), n,
-                              _raw_stream(dev, stream))
+    rc = _lib().hb_kv4_append(pool._addr, k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(),
+                              _int32(n), _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_append")
 
@@ -176,7 +176,7 @@ def kv4_read(pool: Kv4Pool, slots, k_out, v_out, stream=None):
     if dev != _device():
         with torch.cuda.device(dev):
             return kv4_read(pool, slots, k_out, v_out, stream)
-    rc = _lib().hb_kv4_read(pool._addr, slots.data_ptr(), n, k_out.data_ptr(), ks[0], v_out.data_ptr(), vs[0],
+    rc = _lib().hb_kv4_read(pool._addr, slots.data_ptr(), _int32(n), k_out.data_ptr(), ks[0], v_out.data_ptr(), vs[0],
                             _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_read")
@@ -228,9 +228,9 @@ def kv4_decode(pool: Kv4Pool, q, block_tables, ctx_lens, max_ctx: int, out, work
         with torch.cuda.device(dev):
             return kv4_decode(pool, q, block_tables, ctx_lens, max_ctx, out, workspace, stream)
     ws = _work(workspace, stream, dev, kv4_decode_workspace, n, heads, pool._kv, d, max_ctx)
-    rc = _lib().hb_kv4_decode(pool._addr, q.data_ptr(), qs[0], block_tables.data_ptr(), block_tables.shape[1],
-                              ctx_lens.data_ptr(), n, heads, _int32(max_ctx), out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
-                              _raw_stream(dev, stream))
+    rc = _lib().hb_kv4_decode(pool._addr, q.data_ptr(), qs[0], block_tables.data_ptr(), _int32(block_tables.shape[1]),
+                              ctx_lens.data_ptr(), _int32(n), heads, _int32(max_ctx), out.data_ptr(), os_[0],
+                              ws.data_ptr(), ws.nbytes, _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_decode")
 
@@ -254,8 +254,8 @@ def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=N
         with torch.cuda.device(dev):
             return kv4_chunk(pool, q, block_table, chunk_offset, out, workspace, stream)
     ws = _work(workspace, stream, dev, kv4_chunk_workspace, chunk_offset, n, heads, pool._kv, d)
-    rc = _lib().hb_kv4_chunk(pool._addr, q.data_ptr(), qs[0], block_table.data_ptr(), block_table.shape[0],
-                             _int32(chunk_offset), n, heads, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
+    rc = _lib().hb_kv4_chunk(pool._addr, q.data_ptr(), qs[0], block_table.data_ptr(), _int32(block_table.shape[0]),
+                             _int32(chunk_offset), _int32(n), heads, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
                              _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_chunk")
@@ -311,8 +311,8 @@ def copy_pages(pools, src: Sequence[int], dst: Sequence[int], stream=None):
         with torch.cuda.device(dev):
             return copy_pages(pools, s, d, stream)
     es = pools.element_size()
-    rc = _lib().hb_copy_pages(pools.data_ptr(), stride * es, n_pools, page * es, blocks, _page_addr(s), _page_addr(d), n,
-                              _raw_stream(dev, stream))
+    rc = _lib().hb_copy_pages(pools.data_ptr(), stride * es, _int32(n_pools), page * es, _int32(blocks), _page_addr(s),
+                              _page_addr(d), _int32(n), _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_copy_pages")
 
@@ -322,7 +322,7 @@ def copy_blocks(ctx: "native.Context", src: Sequence[int], dst: Sequence[int]):
     s, d = _host_pages(src, "src"), _host_pages(dst, "dst")
     if len(s) != len(d):
         raise ValueError("src and dst must have the same length")
-    ctx._check(_lib().hb_copy_blocks(ctx.h, s.ctypes.data, d.ctypes.data, len(s)))
+    ctx._check(_lib().hb_copy_blocks(ctx.h, s.ctypes.data, d.ctypes.data, _int32(len(s))))
 
 
 class PageTable:

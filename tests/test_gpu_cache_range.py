@@ -6,6 +6,7 @@ import pytest
 
 import cache_ref as ref
 from chunked_prefill_hybrid_gb300 import cache
+from chunked_prefill_hybrid_gb300.native import HB_ERANGE, HbError
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -162,3 +163,22 @@ def test_scores_that_rise_all_along(kv, group, d, offset, n):
         rows = sorted({0, 1, n // 2, n - 1} & set(range(n)))
         _near(h.chunk(qd, offset), q64, h.k, h.v, [(i, offset + i + 1) for i in rows])
         _near(h.decode(qd[:3], [m, m // 2, 1][:min(3, n)]), q64, h.k, h.v, list(enumerate([m, m // 2, 1][:min(3, n)])))
+
+
+def test_shapes_past_32_bits_are_refused_not_cut():
+    """2^32 + 1 rows or pools are not one."""
+    many = (1 << 32) + 1
+    pool = cache.Kv4Pool.empty(2, 1, 64)
+    held = pool.data.clone()
+    rows = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda").expand(many, 1, 64)
+    slots = torch.zeros(many, dtype=torch.int32, device="cuda")
+    pages = torch.arange(64, device="cuda").view(1, 2, 32)
+    for call in (lambda: cache.kv4_append(pool, rows, rows, slots),
+                 lambda: cache.kv4_read(pool, slots, rows, rows),
+                 lambda: cache.kv4_decode(pool, rows, slots[:, None], slots, 0, rows),
+                 lambda: cache.copy_pages(pages.expand(many, 2, 32), [0], [1])):
+        with pytest.raises(HbError) as e:
+            call()
+        assert e.value.code == HB_ERANGE
+    assert torch.equal(pool.data, held) and torch.equal(pages.flatten(), torch.arange(64, device="cuda"))
+    assert (rows[0] == 1).all()
