@@ -196,6 +196,7 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LARGEST_SCALE = 3e38f;  // of scores: 0 times an infinite one (k_scale 2^60, queries of 2^70) would be NaN
 constexpr float LOWEST = -3e38f;  // below every score, and finite: differences with it are too
 
 // Where the weights P = 2^(s - m) lie in f16, whose range is 2^-24 (a

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(W * 32, (FEW ? (D == 128 && W == WARPS ? 6 : 5
             qf[i][1] = put ? pack_h2(x[i][2] * down, x[i][3] * down) : 0u;
         }
         if (warp == 0 && t == 0)
-            s_scale[g] = p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e);
+            s_scale[g] = fminf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(e), LARGEST_SCALE);
     }
     __syncthreads();
 

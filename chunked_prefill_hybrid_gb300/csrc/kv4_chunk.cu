@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
             if (dual)  // half of this warp's exponents are the other half's
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             // never 0: a masked score stays -inf
-            const float sc = fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(exps[r]), 1e-38f);
+            const float sc = fminf(fmaxf(p.ks * (rsqrtf((float)D) * LOG2E) * pow2(exps[r]), 1e-38f), LARGEST_SCALE);
             const int seen0 = p.offset + col0 / p.group + 1;  // of the half's first column
             float m = LOWEST, l = 0.f;
             float raise_at = LOWEST;  // a maximum above it moves m

@@ -182,3 +182,17 @@ def test_shapes_past_32_bits_are_refused_not_cut():
         assert e.value.code == HB_ERANGE
     assert torch.equal(pool.data, held) and torch.equal(pages.flatten(), torch.arange(64, device="cuda"))
     assert (rows[0] == 1).all()
+
+
+@pytest.mark.parametrize("kv,group,d", [(1, 1, 128), (1, 2, 64), (2, 4, 128)])
+def test_a_score_of_zero_stays_zero(kv, group, d):
+    """Keys of zeros score 0 whatever the query's size and k_scale make of the others' scores."""
+    n = 500
+    v = np.random.default_rng(11).standard_normal((n, kv, d))
+    h = Held(np.zeros((n, kv, d)), v, ks=2.0 ** 60)
+    for size in (1e30, 3e38, 1e-38):
+        qd, q64 = _bf(np.random.default_rng(12).choice((-1.0, 1.0), (300, kv * group, d)) * size)
+        zero = np.zeros_like(q64)
+        _near(h.decode(qd[:3], [n, 17, 1]), zero, h.k, h.v, [(0, n), (1, 17), (2, 1)])
+        _near(h.chunk(qd[:2], n - 2), zero, h.k, h.v, [(0, n - 1), (1, n)])
+        _near(h.chunk(qd, n - 300), zero, h.k, h.v, [(i, n - 299 + i) for i in (0, 1, 130, 299)])
