@@ -40,6 +40,7 @@ def _lib():
                 ("hb_kv4_decode_workspace", [ci, ci, ci, ci, ci], ll),
                 ("hb_kv4_chunk", [vp, vp, ll, vp, ci, ci, ci, ci, vp, ll, vp, ll, vp], ci),
                 ("hb_kv4_chunk_workspace", [ci, ci, ci, ci, ci], ll),
+                ("hb_kv4_test_lost_page", [], None),
                 ("hb_copy_pages", [vp, ll, ci, ll, ci, vp, vp, ci, vp], ci),
                 ("hb_copy_blocks", [vp, vp, vp, ci], ci),
                 ("hb_pages_create", [ci, P(vp)], ci),
@@ -259,6 +260,11 @@ def kv4_chunk(pool: Kv4Pool, q, block_table, chunk_offset: int, out, workspace=N
                              _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_kv4_chunk")
+
+
+def kv4_test_lost_page():
+    """Test hook: the next kv4_decode or kv4_chunk of this thread loses a page, and its waits for it run out."""
+    _lib().hb_kv4_test_lost_page()
 
 
 _NP32 = np.dtype(np.int32)

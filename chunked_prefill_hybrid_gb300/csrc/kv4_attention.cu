@@ -55,6 +55,7 @@ struct Kv4Attn {
     long long out_stride;
     float2 *part_ml;                  // [row][head][split] (m in log2, l)
     float *part_o;                    // [row][head][split][D]
+    bool lose;                        // the first CTA leaves out the copy of its first page (hb_kv4_test_lost_page)
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(W * 32, (FEW ? (D == 128 && W == WARPS ? 6 : 5
         const int mine = tile + (lane & (N - 1));
         const int blk = __shfl_sync(0xffffffffu, ids, mine & 31);
         const bool ok = blk >= 0 && blk < p.num_blocks;
-        if (lane < N && mine < n_tiles) {
+        const bool lose = N == RING && p.lose && blockIdx.x + blockIdx.y + threadIdx.x == 0;
+        if (lane < N && mine < n_tiles && !lose) {
             bad |= !ok;
             uint64_t *bar = &full[warp][mine % RING];
             if (ok) {
@@ -808,6 +810,15 @@ bool dims_ok(int n_heads, int n_kv, int d)
 
 long long ctas_of(int cols, int n_kv, int seqs) { return (long long)((cols + 7) / 8) * n_kv * seqs; }
 
+thread_local bool test_lose = false;  // of this thread's next attention launch
+
+bool take_lose()
+{
+    const bool lose = test_lose;
+    test_lose = false;
+    return lose;
+}
+
 // Queries a CTA takes: see k_kv4_attention.
 bool few(int cols, int d) { return cols <= (d == 128 ? 1 : 2); }
 
@@ -929,6 +940,7 @@ try {
         p.part_o = (float *)workspace;
         p.part_ml = (float2 *)(p.part_o + (size_t)n_decodes * n_heads * sp.n * d);
     }
+    p.lose = take_lose();
     return launch(p, d, n_decodes, n_decodes, (cudaStream_t)cuda_stream);
 } catch (...) {
     return HB_ENOMEM;
@@ -1034,6 +1046,7 @@ try {
         c.out_stride = out_stride;
         c.part_o = (float *)workspace;
         c.part_ml = (float2 *)(c.part_o + (size_t)2 * c.ctas * KC_ROWS * d);
+        c.lose = take_lose();
         return launch_kv4_chunk(c, d, (cudaStream_t)cuda_stream) == cudaSuccess ? HB_OK : HB_ECUDA;
     }
     p.pool = (const uint8_t *)pool->data;
@@ -1048,7 +1061,10 @@ try {
     p.out_stride = out_stride;
     p.part_o = (float *)workspace;
     p.part_ml = (float2 *)(p.part_o + (size_t)chunk_len * n_heads * p.n_splits * d);
+    p.lose = take_lose();
     return launch(p, d, 1, chunk_len, (cudaStream_t)cuda_stream);
 } catch (...) {
     return HB_ENOMEM;
 }
+
+extern "C" void hb_kv4_test_lost_page(void) { test_lose = true; }

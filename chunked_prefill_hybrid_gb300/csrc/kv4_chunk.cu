@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         ok = false;
                         break;
                     }
-                    if (lane < 8) {
+                    if (lane < 8 && !(p.lose && blockIdx.x == 0 && n == 0)) {
                         if (in) {
                             mbar_expect_tx(&raw_full[slot], C::RAW);
                             bulk_load(smem + C::R + slot * C::RAW, p.pool + ((size_t)blk * p.n_kv + sg.kvh) * C::RAW,

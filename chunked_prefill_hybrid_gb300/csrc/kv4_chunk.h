@@ -36,6 +36,7 @@ struct Kv4Chunk {
     KcStart start[KC_CTAS];
     float *part_o;              // [2 ctas][D / 4][256][4]: CTA c's segment that starts with it, and its last
     float2 *part_ml;            // [2 ctas][256] (m in log2, l)
+    bool lose;                  // the first CTA leaves out the copy of its first page (hb_kv4_test_lost_page)
 };
 
 // Plan the work of a chunk (host): everything but the pointers.  False when a

@@ -142,6 +142,14 @@ int hb_kv4_chunk(const hb_kv4_pool *pool, const void *q, long long q_stride, con
                  long long workspace_bytes, void *cuda_stream);
 long long hb_kv4_chunk_workspace(int chunk_offset, int chunk_len, int n_heads, int n_kv_heads, int head_dim);
 
+/* Test hook for the failure path of the two attention calls: in this thread's
+ * next hb_kv4_decode or hb_kv4_chunk that launches, the first CTA leaves out
+ * the copy of its first page, so that its waits run out (after 2 s at most,
+ * as they always would).  The rows and heads of that CTA become NaN, after
+ * its copies and products under way have ended; the others, and the calls
+ * after it, are as ever. */
+void hb_kv4_test_lost_page(void);
+
 /* ------------------------------------------------- pages on the device
  *
  * Copy page src[i] to page dst[i], i < n, in each of n_pools pools: pool p's
