@@ -729,10 +729,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             v[j] = v[j] * f + y[j] * f2;
-                } else {
+                } else {  // l is another warp's where both halves have the same columns, and that may not know yet
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[j] = 0.f;
+                        v[j] = __int_as_float(0x7fc00000);
                 }
                 if (nans >> (c / 16) & 3u)
 #pragma unroll
