@@ -876,10 +876,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                         issue_s();
                 }
             }
-            if (!ok) {
-                mma_commit_elect(&drain[h]);
-                mbar_wait(&drain[h], 0, nullptr, WAIT_NS / 4);
-            }
+            // no product may be under way, and no arrival, when the CTA ends:
+            // the other roles may have given up before this warp's last ones
+            mma_commit_elect(&drain[h]);
+            mbar_wait(&drain[h], 0, nullptr, WAIT_NS / 4);
         } else if (warp == MMA_WARP + 2) {
             // ---------------------------------------------------- loader
             uint32_t it = 0;
