@@ -196,3 +196,78 @@ def test_a_score_of_zero_stays_zero(kv, group, d):
         _near(h.decode(qd[:3], [n, 17, 1]), zero, h.k, h.v, [(0, n), (1, 17), (2, 1)])
         _near(h.chunk(qd[:2], n - 2), zero, h.k, h.v, [(0, n - 1), (1, n)])
         _near(h.chunk(qd, n - 300), zero, h.k, h.v, [(i, n - 299 + i) for i in (0, 1, 130, 299)])
+
+
+@pytest.mark.parametrize("n,kv,d,ks,vs", [(1, 1, 64, 1.0, 1.0), (37, 3, 64, 1.0, 0.3779644668), (19, 5, 128, 0.5, 2.0),
+                                          (200, 2, 128, 0.7071067691, 1.0)])
+@pytest.mark.parametrize("with_nan", [False, True])
+def test_append_writes_its_own_bytes_and_no_others(n, kv, d, ks, vs, with_nan):
+    """Every byte of the pool, among random ones, but for two that mean nothing: the codes of a block that held a NaN,
+    and the sign of a code of zero."""
+    ks, vs = float(np.float32(ks)), float(np.float32(vs))
+    rng = np.random.default_rng(13)
+    blocks = n // 16 + 4
+    x = rng.standard_normal((2, n, kv, d)) * np.exp(rng.standard_normal((1, 1, kv, d)))
+    x[:, 0, 0, :16] = 0
+    x[0, n // 2, 0, 16:32] = np.linspace(-6, 6, 16) * 0.8125  # ties
+    x[1, n // 3, 0, 32] = 1e5                                 # a scale that saturates
+    x[1, n - 1, -1, 3] = np.inf
+    if with_nan:
+        x[0, n // 2, -1, 40] = x[1, 0, 0, 17] = np.nan
+    slots = rng.permutation(blocks * 16)[:n].astype(np.int32)
+    if n > 8:
+        slots[7], slots[8] = -1, blocks * 16
+    before = rng.integers(0, 256, (blocks, kv, 18 * d)).astype(np.uint8)
+    pool = cache.Kv4Pool(torch.from_numpy(before).cuda(), ks, vs)
+    want, codes_at = before.copy(), ref.addresses(d)
+    given = []
+    for which, ps, rows in (("k", ks, x[0]), ("v", vs, x[1])):
+        t, x64 = _bf(rows)
+        given.append(t)
+        ref.store(want, slots, *ref.quantise(x64, ps), which)
+    cache.kv4_append(pool, *given, torch.from_numpy(slots).cuda())
+    got = pool.data.cpu().numpy()
+    assert torch.isnan(given[0]).any().item() == with_nan
+
+    def settled(data):
+        """The bytes with what means nothing in the written slots made 0."""
+        data = data.copy()
+        for s in slots[(slots >= 0) & (slots < 16 * blocks)]:
+            page, tok = data[s // 16], s % 16
+            for which in "kv":
+                sb = np.repeat(page[:, codes_at[which + "s"][tok]] & 0x7f, 16, axis=-1)  # [kv][d]
+                for nib in (0, 1):
+                    sel = codes_at["nib"][tok] == nib
+                    at = codes_at[which][tok][sel]
+                    code = page[:, at] >> (4 * nib) & 15
+                    code = np.where((sb[:, sel] == 0x7f) | (code == 8), 0, code)
+                    page[:, at] = (page[:, at] & (0xF0 if nib == 0 else 0x0F)) | (code << (4 * nib))
+        return data
+
+    assert np.array_equal(settled(got), settled(want))
+    untouched = np.ones(blocks * 16, bool)
+    untouched[slots[(slots >= 0) & (slots < 16 * blocks)]] = False
+    assert untouched.sum() >= 48 and not np.array_equal(got, before)
+
+
+@pytest.mark.parametrize("size", [300.0, 3e3, 3e4, 1e30])
+@pytest.mark.parametrize("kv,group,d", [(2, 1, 64), (2, 1, 128), (1, 4, 128)])
+def test_large_queries_keep_a_tie(kv, group, d, size):
+    """Two equal keys far above the rest share a row evenly, in whatever pages they lie, even where a score's last
+    place is worth more than one: the same sums of the same numbers."""
+    n = 300
+    rng = np.random.default_rng(14)
+    q, k = _peaked(rng, 150, n, kv, group, d, 0, 5)
+    k[101] = k[142] = 3 * q[0, ::group] / np.abs(q[0]).max()
+    h = Held(k, rng.standard_normal((n, kv, d)))
+    qd, q64 = _bf(q * size)
+    for out, rows in ((h.decode(qd[:2], [n, n]), (0, 1)), (h.decode(qd[:1], [n]), (0,)), (h.chunk(qd, n - 150), (0, 149)),
+                      (h.chunk(qd[:2], n - 2), (0, 1))):
+        for i in rows:
+            for head in range(kv * group):
+                s = h.k[:, head // group] @ q64[i, head] / np.sqrt(d)
+                top = np.sort(s)[-3:]
+                assert top[1] == top[2] > top[0] + 100
+                pair = h.v[[101, 142], head // group]
+                bound = 2.0 ** -8 * np.abs(pair.mean(0)) + 2.0 ** -10 * np.abs(pair).mean(0) + 1e-6
+                assert (np.abs(out[i, head].double().cpu().numpy() - pair.mean(0)) <= bound).all(), (i, head)
