@@ -151,7 +151,7 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N])
     }
 }
 
-// Power of two e that brings a query whose largest magnitude is a into [1, 4)
+// Power of two e that brings a query whose largest magnitude is a into [1, 2)
 // (0 for a = 0), and 2^e itself, e in [-126, 126].
 __device__ __forceinline__ int query_exponent(float a)
 {

@@ -10,8 +10,9 @@
 // A warp takes 16 keys at a time and up to eight queries that share a kv head
 // as the columns of m16n8k16 MMAs (f16 in, fp32 sums): S^T = K q, then
 // O^T += V^T P.  A code times its block's scale has at most six significant
-// bits, so it is exact in f16; q is brought to [1, 4) by a power of two per
-// query (bf16 fits f16 then).
+// bits, so it is exact in f16; q is brought to [1, 2) by a power of two per
+// query, where f16 holds all eight bits of a component down to 2^-17 of the
+// largest; a smaller one is rounded to a multiple of 2^-24 of the power.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -769,13 +770,16 @@ struct Split {
 
 // Keys of a split (a multiple of 16 WARPS) and the number of splits: the one
 // with the least estimated time.  An SM shares its throughput among its CTAs
-// and needs three of them to reach it (4, 5 or 8 were no better over the shapes
-// that were measured); joining splits takes about as long as an SM takes for 64
-// pages of a head.  Of one row (and of a chunk) the keys are known, and CTAs
-// beyond those that an SM holds run when others have ended: 30000 keys, 8 kv
-// heads of 4, take 17.5 us in 752 CTAs and 14.1 in 608.  Several rows are mostly
-// shorter than max_ctx, and a split more evens them out: 54 rows of 4000 to 8000
-// keys, 4 heads, 17.2 us, and 22.1 when counted as if all were of 8000.
+// and is taken to need three of them (FULL) to reach it; joining splits counts
+// as much as an SM's time for 64 pages of a head (JOIN), however many they are,
+// and a CTA's start and end nothing.  So a little better rounding may buy
+// hundreds of CTAs: of one row with 8 kv heads of 8, 130999 keys take 36 us in 57
+// splits, but 115000 keys 57 us in 360, 132000 46 and 155000 56; with FULL 3.5,
+// 4 or 5 it is 115000 keys that take 37, and 130999 that take 50.  Of one row
+// (and of a chunk) the keys are known, and CTAs beyond those that an SM holds
+// run when others have ended; several rows are mostly shorter than max_ctx, and
+// what is left over at the end is not counted (54 rows of 4000 to 8000 keys, 4
+// heads: 40.0 us, counted 40.3).
 Split plan_split(long long ctas, int resident, int max_keys)
 {
     constexpr int UNIT = 16 * WARPS;
@@ -830,7 +834,8 @@ cudaError_t launch_w(const Kv4Attn &p, dim3 grid, cudaStream_t s)
 {
     // Six CTAs fit an SM.  Where five on each hold the whole grid they lie
     // more evenly with no room for a sixth: 720 CTAs (18 rows of 1024 keys, 40
-    // heads) take 23.3 us so and 25.9 with room; 5120 (128 rows) 95.7 and 94.1.
+    // heads) take 23.5 us so and 26.3 with room; 5120 (128 rows of 128 to 2048
+    // keys, evenly spread) 131.5 and 129.4.
     constexpr int PAD = FEW && D == 128 && W == WARPS ? 1024 : 0;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = kv4_allow_smem((const void *)k_kv4_attention<D, FEW, W>, Smem<D, W>::BYTES + PAD, done);
@@ -842,10 +847,10 @@ cudaError_t launch_w(const Kv4Attn &p, dim3 grid, cudaStream_t s)
 
 // Short contexts of more rows than run at once: one warp a CTA, which has no
 // others to wait for and to join, and four times as many rows are under way.
-// 40 heads: 85 rows of 5 keys 6.9 us against 13.5 with four warps, 128 rows of
-// 61 keys 12.4 against 25.9, of 256 keys 35.5 against 40.0, but 64 rows of 1001
-// keys 67.9 against 59.8; 8 kv heads of 8: 128 rows of 121 keys 10.1 against
-// 10.5, of 501 keys 23.2 against 20.2.
+// 40 heads: 85 rows of 5 keys 7.3 us against 14.0 with four warps, 128 rows of
+// 61 keys 15.7 against 29.1, of 255 keys 35.5 against 41.3, but 64 rows of 1001
+// keys 78.2 against 61.5; 8 kv heads of 8: 128 rows of 121 keys 10.4 against
+// 11.2, of 501 keys 24.6 against 24.7.
 template <int D, bool FEW>
 cudaError_t launch_d(const Kv4Attn &p, dim3 grid, cudaStream_t s)
 {
@@ -946,13 +951,13 @@ try {
     return HB_ENOMEM;
 }
 
-// Microseconds that a chunk takes as columns of the decode kernel: a fit of
-// measured times, good to about a third, for the choice between it and the
-// tcgen05 kernel, whose plan has an estimate of its own.  With 40 heads of 128
-// and 1000 cached keys, 16 rows take 10.1 us against 12.9 on the tcgen05
-// kernel, 64 rows 20.8 against 12.4; with 16000 keys, 16 rows 52 against 58,
-// 32 rows 81 against 59; with eight heads on one kv head and 16000 keys, 16
-// rows 14.3 against 17.6, 64 rows 42 against 20.
+// Microseconds that a chunk takes as columns of the decode kernel, for the
+// choice between it and the tcgen05 kernel, whose plan has an estimate of its
+// own: 0.7 to 2.8 of the time over 196 shapes, nearest where the two are close,
+// so that the choice costs at most 1.3 of the better one.  With 40 heads of 128
+// and 1000 cached keys, 16 rows take 10.6 us against 12.1 on the tcgen05
+// kernel, 64 rows 20.7 against 12.7; with 16000 keys, 16 rows 53 against 56, 32
+// rows 82 against 56.
 static double decode_kernel_us(int offset, int len, int group, int n_kv)
 {
     const double pages = (offset + 0.5 * len) / 16 + 1;

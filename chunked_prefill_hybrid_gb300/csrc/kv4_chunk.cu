@@ -509,9 +509,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv4_chunk(const __grid_constant_
                 // this warp's 32 rows of Q as f16, or 16 of them where the
                 // other half has the same (past the last column, that column's
                 // again: their results go nowhere).  Rows of ordinary size go
-                // as they are; if any of a batch has its largest magnitude
-                // outside [2^-6, 2^15), each is scaled by a power of two into
-                // [1, 4) first
+                // as they are (components below 2^-17 lose bits: an error of
+                // 2^-25, at most 2^-19 of the row's largest); if any of a batch
+                // has its largest magnitude outside [2^-6, 2^15), each is
+                // scaled by a power of two into [1, 2) first
                 const long long src = row * p.q_stride + (size_t)head * D;
                 constexpr int N = 16 / RPI;  // 16 rows a batch, the next one's loads under way meanwhile
                 const int i0 = dual ? half * 16 : 0, i1 = dual ? i0 + 16 : 32;
@@ -1019,7 +1020,7 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
 }  // namespace
 
 // How the work of a chunk may be cut, and about how long each way takes: fits
-// of measured times of 210 shapes, most of them good to a quarter.
+// of measured times, 0.82 to 1.21 of them over 216 shapes.
 //
 //   parts  an item to one CTA, or to several that share its tiles evenly
 //   whole  more items than CTAs: each takes some that follow one another
@@ -1031,8 +1032,9 @@ cudaError_t launch_d(const Kv4Chunk &p, cudaStream_t s)
 // (the queries, the pipeline's start and end, the result).  Items of 256
 // columns convert each key once for both halves; items of 128 (both halves on
 // them) make twice as many.  With 40 heads of 128, 512 rows at offset 0 take
-// 24 us cut evenly into items of 128 and 15 as whole items; 512 rows at 15872
-// keys 133 us cut evenly into items of 256, 1.9 CTAs an item, and 215 as whole ones.
+// 14.6 us as whole items and 17.8 cut evenly, 256 rows at 768 keys 14.3 and
+// 18.7; 512 rows at 15872 keys 129 us cut evenly, 1.9 CTAs an item, and 208 as
+// whole items, or 164 cut into items of 128.
 namespace {
 
 constexpr double SWITCH_US = 5, JOIN_US = 2, PART_US = 0.25, BYTES_PER_US = 2.5e6;

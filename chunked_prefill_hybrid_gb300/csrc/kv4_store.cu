@@ -171,11 +171,13 @@ struct Place {
     }
 };
 
-// One thread per (row, kv head, 16 channels), K and V.  Bound by instructions:
-// with k_kv4_read 3565 rows of 40 heads of 128 take 38.2 us, of which the
-// 187 MB that the two move would take 27.6 at the copy rate; 274 rows 5.3 us;
-// 18 rows 3.6 (two launches).  A byte store for each two channels took 51.4 us,
-// 7.8 and 5.2.
+// One thread per (row, kv head, 16 channels), K and V.  With k_kv4_read 3565
+// rows of 40 heads of 128 take 38.1 us, of which the 187 MB that the two move
+// would take 27.6 at the copy rate; 274 rows 5.1 us; 18 rows 3.4 (two launches).
+// A byte store for each two channels took 51.4 us, 7.8 and 5.2.  Of a prompt this
+// kernel takes 22 us against 14 for its bytes: warps mostly wait for their loads
+// (8.3 cycles an instruction, the next stall 2.1; 60% of the issue slots taken),
+// as a thread has one item and nothing to do until it is there.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 6)
     k_kv4_append(uint8_t *pool, int num_blocks, int n_kv, int head_groups, float ks, float vs, float k6, float v6,
@@ -276,16 +278,6 @@ long long store_blocks(int n_kv, int n_tokens, int *head_groups)
     return (long long)*head_groups * ((n_tokens + (long long)ROWS - 1) / ROWS);
 }
 
-// Whether a row operand (k, v, q, out) is one the kernels can read or write.
-int check_rows(const void *p, long long stride, int n, int width)
-{
-    if (!p || (uintptr_t)p % 16)
-        return HB_EINVAL;
-    if (n > 1 && (stride % 8 || stride < width || stride > (1ll << 40)))
-        return HB_EINVAL;
-    return HB_OK;
-}
-
 }  // namespace
 
 int kv4_check_pool(const hb_kv4_pool *p)
@@ -300,7 +292,14 @@ int kv4_check_pool(const hb_kv4_pool *p)
     return HB_OK;
 }
 
-int kv4_check_rows(const void *p, long long stride, int n, int width) { return check_rows(p, stride, n, width); }
+int kv4_check_rows(const void *p, long long stride, int n, int width)
+{
+    if (!p || (uintptr_t)p % 16)
+        return HB_EINVAL;
+    if (n > 1 && (stride % 8 || stride < width || stride > (1ll << 40)))
+        return HB_EINVAL;
+    return HB_OK;
+}
 
 }  // namespace hb
 
@@ -326,7 +325,7 @@ try {
     if (n_tokens == 0)
         return HB_OK;
     const int width = pool->n_kv_heads * pool->head_dim;
-    if (!slots || check_rows(k, k_stride, n_tokens, width) || check_rows(v, v_stride, n_tokens, width))
+    if (!slots || kv4_check_rows(k, k_stride, n_tokens, width) || kv4_check_rows(v, v_stride, n_tokens, width))
         return HB_EINVAL;
     int hg = 0;
     const long long grid = pool->head_dim == 128 ? store_blocks<128>(pool->n_kv_heads, n_tokens, &hg)
@@ -336,8 +335,8 @@ try {
     auto kern = pool->head_dim == 128 ? k_kv4_append<128> : k_kv4_append<64>;
     return launch_kernel(true, kern, dim3((unsigned)grid), dim3(THREADS), 0, (cudaStream_t)cuda_stream,
                          (uint8_t *)pool->data, pool->num_blocks, pool->n_kv_heads, hg, pool->k_scale, pool->v_scale,
-                         1.f / (6.f * pool->k_scale), 1.f / (6.f * pool->v_scale), (const bf16 *)k, k_stride, (const bf16 *)v, v_stride, (const int *)slots,
-                         n_tokens) == cudaSuccess
+                         1.f / (6.f * pool->k_scale), 1.f / (6.f * pool->v_scale), (const bf16 *)k, k_stride,
+                         (const bf16 *)v, v_stride, (const int *)slots, n_tokens) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
 } catch (...) {
@@ -355,7 +354,7 @@ try {
     if (n_tokens == 0)
         return HB_OK;
     const int width = pool->n_kv_heads * pool->head_dim;
-    if (!slots || check_rows(k, k_stride, n_tokens, width) || check_rows(v, v_stride, n_tokens, width))
+    if (!slots || kv4_check_rows(k, k_stride, n_tokens, width) || kv4_check_rows(v, v_stride, n_tokens, width))
         return HB_EINVAL;
     int hg = 0;
     const long long grid = pool->head_dim == 128 ? store_blocks<128>(pool->n_kv_heads, n_tokens, &hg)

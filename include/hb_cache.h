@@ -84,9 +84,9 @@ long long hb_kv4_pool_bytes(int num_blocks, int n_kv_heads, int head_dim);
 int hb_kv4_append(const hb_kv4_pool *pool, const void *k, long long k_stride, const void *v, long long v_stride,
                   const int32_t *slots, int n_tokens, void *cuda_stream);
 
-/* Read back the values at slots as bf16 (rounded once), the layout and
- * conditions of hb_kv4_append.  A row whose slot lies outside the pool is
- * left as it was. */
+/* Read back the values at slots as bf16: code * (scale * k_scale) in fp32,
+ * rounded to bf16.  Layout and conditions of hb_kv4_append.  A row whose slot
+ * lies outside the pool is left as it was. */
 int hb_kv4_read(const hb_kv4_pool *pool, const int32_t *slots, int n_tokens, void *k, long long k_stride, void *v,
                 long long v_stride, void *cuda_stream);
 
