@@ -827,7 +827,7 @@ bool take_lose()
 bool few(int cols, int d) { return cols <= (d == 128 ? 1 : 2); }
 
 // CTAs of the attention kernel that an SM holds (registers), for plan_split.
-int resident(int rows, int cols, int d) { return rows > 1 ? 1 << 30 : few(cols, d) ? 6 : d == 128 ? 4 : 5; }
+int resident(int rows, int cols, int d) { return rows > 1 ? 1 << 30 : d == 64 ? 5 : few(cols, d) ? 6 : 4; }
 
 template <int D, bool FEW, int W>
 cudaError_t launch_w(const Kv4Attn &p, dim3 grid, cudaStream_t s)
