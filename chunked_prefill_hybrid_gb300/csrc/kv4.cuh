@@ -199,8 +199,10 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LARGEST_SCALE = 3e38f;  // of scores: 0 times an infinite one (k_scale 2^60, queries of 2^70) would be NaN
 constexpr float LOWEST = -3e38f;  // below every score, and finite: differences with it are too
 
-// Where the weights P = 2^(s - m) lie in f16, whose range is 2^-24 (a
-// subnormal's last bit) to 2^16: the reference m is 2^LIFT below the largest
+// The weights P = 2^(s - m) go to the tensor cores in f16, as V does (an MMA
+// takes one type): 11 bits, an error of 2^-12 a weight, some 2^-3 of a bf16
+// result's own rounding.  Where they lie in f16's range of 2^-24 (a subnormal's
+// last bit) to 2^16: the reference m is 2^LIFT below the largest
 // score when it moves, and moves when a score passes it by LIFT + RAISE.  So P
 // is at most 2^15, and a key of 2^-36 of the largest weight still counts; with
 // the reference at the largest score, keys behind an attention sink (2^-25 of

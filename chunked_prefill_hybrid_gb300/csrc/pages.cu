@@ -27,7 +27,7 @@ struct PagePairs {
 // One warp copies 2 KB of one page of one pool at a time, four 16-byte loads a
 // lane under way (with 2, 6, 8 or 16, or streaming hints, no faster).  Bound by
 // memory: 97 pages of 33 KB in 80 pools take 84 us, 0.89 of the copy rate; one
-// page of 164 KB in 80 pools 4.5 us.
+// page of 164 KB in 80 pools 4.0 us.
 template <int CAP>
 __global__ void __launch_bounds__(CP_WARPS * 32)
     k_copy_pages(const __grid_constant__ PagePairs<CAP> pairs, uint8_t *data, long long pool_stride, int n_pools,
