@@ -143,8 +143,12 @@ struct Smem {
 // Else the scales multiply V's codes, which is exact, and P is all that a
 // column holds: one power of two for each of eight blocks and eight queries
 // would cost as much.
+//
+// Six CTAs an SM of four warps need at most 80 registers, which the compiler
+// passes by four unless it is told: 133 us in place of 132.
 template <int D, bool FEW, int W>
-__global__ void __launch_bounds__(W * 32, (FEW ? (D == 128 && W == WARPS ? 6 : 5) : 4) * WARPS / W) k_kv4_attention(const Kv4Attn p)
+__global__ void __launch_bounds__(W * 32, (FEW ? (D == 128 && W == WARPS ? 6 : 5) : 4) * WARPS / W)
+    k_kv4_attention(const Kv4Attn p)
 {
     using L = Layout<D>;
     constexpr int NB = L::NB, KW = NB / 2;  // words of a lane's 8- or 16-byte load
