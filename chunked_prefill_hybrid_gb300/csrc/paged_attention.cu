@@ -1,0 +1,907 @@
+// paged_attention.cu -- decode attention over the paged bf16 cache: of rows
+// behind shared prefixes, and with the weight that each key gets
+// (include/hb_paged.h).
+//
+//   s_t = q . k_t,  p_t = 2^((s_t - m) c2),  o = sum p_t v_t / sum p_t,
+//   c2 = log2(e) / sqrt(d)
+//
+// in one pass over a row's keys with the running maximum m and sum of the
+// softmax; rows with many keys are split over CTAs and joined by a second
+// kernel.
+//
+// A warp takes a page (16 keys) at a time and 8 or 16 queries that share the kv
+// head as the columns of m16n8k16 MMAs (bf16 in, fp32 sums): S^T = K q, then
+// O^T += V^T P with P in two bf16 terms (16 significant bits: one term alone
+// would cost as much precision as rounding the result to bf16 does).
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "kv4_host.h"
+#include "paged.h"
+
+namespace hb {
+namespace {
+
+using namespace paged;
+
+constexpr int WARPS = 4;
+constexpr int JOIN_WARPS = 8;
+constexpr int SPLIT_MIN = 256;       // keys of a split at least
+constexpr int WEIGH_THREADS = 256;
+constexpr int WEIGH_KEYS = 4;        // keys of a thread of the weights' kernel
+constexpr float LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes to shared memory, zeros unless ok.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Two fp32 numbers as bf16 pairs hi + lo.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// A bf16 pair with an infinity or a NaN in it.
+__device__ __forceinline__ bool odd_pair(uint32_t x)
+{
+    return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int D>
+struct Ring {
+    static constexpr int ROW = D * 2;             // bytes of a key
+    static constexpr int HALF = 16 * ROW;         // K or V of a page
+    static constexpr int PAGE = 2 * HALF;
+    static constexpr int DEPTH = D == 128 ? 3 : 5;  // pages of a warp, one of them in use
+};
+
+// Shared memory: a ring of pages for each warp, and after the key loop, in the
+// same place, the warps' results.
+template <int D, int NT>
+struct Smem {
+    static constexpr int ROW = D + 4;  // floats of a result row, off the banks of the next
+    static constexpr int RINGS = WARPS * Ring<D>::DEPTH * Ring<D>::PAGE;
+    static constexpr int JOIN = WARPS * 8 * NT * ROW * 4;
+    static constexpr int BYTES = RINGS > JOIN ? RINGS : JOIN;
+};
+
+// Row chunks of 16 bytes lie at c ^ (key & 7), so that eight keys' chunks are on
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t place(int key, int c)
+{
+    return (uint32_t)(key * Ring<D>::ROW + ((c ^ (key & 7)) << 4));
+}
+
+// One CTA: a kv head's queries 8 NT tile.. of one sequence, and the keys of one
+// split.  The warps take its pages in turn, each with a ring and a softmax of
+// its own, and join their results in shared memory.
+template <int D, int NT, bool SCORES>
+__global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_constant__ Attn p)
+{
+    using R = Ring<D>;
+    using S = Smem<D, NT>;
+    constexpr int KS = D / 16;  // k-steps of S, channel tiles of O
+    constexpr int COLS = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_m[WARPS][COLS], s_l[WARPS][COLS];
+
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int g = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x % p.n_splits;
+    const int rest = blockIdx.x / p.n_splits;
+    const int tile = rest % p.col_tiles, kvh = rest / p.col_tiles;
+    const int seq = blockIdx.y;
+    const int ncols = p.nq * p.group;
+    const int c0 = tile * COLS;
+
+    pdl_wait();
+    pdl_trigger();
+    const int ctx = p.ctx_lens[seq];
+    int from = 0, least = 0;  // first own key, smallest context
+    int common = 0, row0 = seq;  // pages that are the group's, found through its first row's table
+    if (p.n_groups > 0) {
+        const Group gr = p.of(seq);
+        from = gr.shared;
+        least = gr.prefix > 0 ? gr.prefix - 1 : 0;
+        common = gr.prefix >> 4;
+        row0 = gr.row0;
+    }
+    // where a row's keys start and end is the same for all threads of the CTA
+    if (ctx < least || ctx > p.max_ctx) {  // padding: zeros; outside its range: NaN
+        if (p.n_slots == 1 && split == 0)
+            for (int i = threadIdx.x; i < COLS * D; i += WARPS * 32) {
+                const int c = c0 + i / D;
+                if (c < ncols)
+                    p.out[(long long)(seq * p.nq + c / p.group) * p.out_stride +
+                          (size_t)(kvh * p.group + c % p.group) * D + i % D] = f2bf(ctx == -1 ? 0.f : nan_f());
+            }
+        return;
+    }
+    const int k0 = from + split * p.split_len, k1 = min(ctx + 1, k0 + p.split_len);
+    if (k0 >= k1)
+        return;  // the join knows how many splits a row has
+
+    // ---- this warp's pages: b0 + 4 i, i < n
+    const int b0 = (k0 >> 4) + warp;
+    const int n = max(0, (((k1 + 15) >> 4) - b0 + WARPS - 1) / WARPS);
+    auto page_id = [&](int i) {
+        const int b = b0 + i * WARPS;
+        return __ldg(p.tables + (size_t)(b < common ? row0 : seq) * p.bt_stride + b);
+    };
+    uint8_t *ring = smem + warp * R::DEPTH * R::PAGE;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    int ids = lane < n ? page_id(lane) : 0;  // lane i: page i of the current 32
+    bool bad = false;
+    auto issue = [&](int i) {
+        if (i < n) {
+            if ((i & 31) == 0 && i > 0)
+                ids = i + lane < n ? page_id(i + lane) : 0;
+            const int blk = __shfl_sync(0xffffffffu, ids, i & 31);
+            const bool ok = blk >= 0 && blk < p.num_blocks;
+            bad |= !ok;
+            const size_t at = ((size_t)(ok ? blk : 0) * p.n_kv + kvh) * 16 * D;
+            const int left = ok ? k1 - (b0 + i * WARPS) * 16 : 0;  // keys of the page that count
+            const uint32_t dst = ring_at + (i % R::DEPTH) * R::PAGE;
+#pragma unroll
+            for (int j = 0; j < R::HALF / 512; ++j) {
+                const int e = j * 32 + lane, key = e / (D / 8), c = e % (D / 8);
+                copy16(dst + place<D>(key, c), p.k + at + (size_t)e * 8, key < left);
+                copy16(dst + R::HALF + place<D>(key, c), p.v + at + (size_t)e * 8, key < left);
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < R::DEPTH - 1; ++i)
+        issue(i);
+
+    // ---- q as B fragments: (channels 2t, 2t + 1 and 2t + 8, 2t + 9; column g)
+    uint32_t qf[NT][KS][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c = c0 + nt * 8 + g;
+        const bool have = c < ncols;
+        const bf16 *qr = p.q + (long long)(seq * p.nq + (have ? c / p.group : 0)) * p.q_stride +
+                         (size_t)(kvh * p.group + (have ? c % p.group : 0)) * D + 2 * t;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            qf[nt][ks][0] = have ? *reinterpret_cast<const uint32_t *>(qr + 16 * ks) : 0u;
+            qf[nt][ks][1] = have ? *reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8) : 0u;
+        }
+    }
+    // keys that this lane's columns see
+    int see[NT][2];
+    int fewest = ctx + 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = min(c0 + nt * 8 + 2 * t + j, ncols - 1);
+            see[nt][j] = min(k1, ctx + 1 - (p.nq - 1) + c / p.group);
+        }
+    if (p.nq > 1)
+        fewest = ctx + 1 - (p.nq - 1) + c0 / p.group;
+
+    float m[NT][2], l[NT][2], o[NT][KS][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+            o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+    float *score_at = nullptr;  // of column 2t of the first tile, key g
+    if (SCORES)
+        score_at = p.scores + (((size_t)seq * p.n_kv + kvh) * ncols + c0 + 2 * t) * p.score_stride + g;
+
+    const int mi = lane >> 3;
+    for (int i = 0; i < n; ++i) {
+        copy_wait<R::DEPTH - 2>();
+        __syncwarp();  // every lane's copies of page i are here, and page i - 1 is done with
+        issue(i + R::DEPTH - 1);
+        const uint32_t page = ring_at + (i % R::DEPTH) * R::PAGE;
+        const int key0 = (b0 + i * WARPS) * 16;
+
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a[4];
+            ldmatrix4(a, page + place<D>((lane & 7) + 8 * (mi & 1), 2 * ks + (mi >> 1)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_bf16(s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+        }
+        if (key0 + 16 > min(fewest, k1))  // keys that a query does not see
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (key0 + g + 8 * (j >> 1) >= see[nt][j & 1])
+                        s[nt][j] = -INFINITY;
+        if (SCORES)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + nt * 8 + 2 * t + (j & 1) < ncols)
+                        score_at[(size_t)(nt * 8 + (j & 1)) * p.score_stride + key0 + 8 * (j >> 1)] = s[nt][j];
+
+        uint32_t hi[NT][2], lo[NT][2];
+        float pr[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float corr[2], base[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = fmaxf(s[nt][j], s[nt][j + 2]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                mx = fmaxf(mx, m[nt][j]);
+                base[j] = mx == -INFINITY ? 0.f : mx;
+                corr[j] = ex2((m[nt][j] - base[j]) * p.c2);
+                m[nt][j] = mx;
+            }
+            // the difference first: a fused s c2 - m c2 would round a large maximum away
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                pr[nt][j] = ex2((s[nt][j] - base[j & 1]) * p.c2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                l[nt][j] = l[nt][j] * corr[j] + (pr[nt][j] + pr[nt][j + 2]);
+            if (corr[0] != 1.f || corr[1] != 1.f)
+#pragma unroll
+                for (int x = 0; x < KS; ++x)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[nt][x][j] *= corr[j & 1];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                split_bf16(pr[nt][2 * h], pr[nt][2 * h + 1], hi[nt][h], lo[nt][h]);
+                hi[nt][h] = movmatrix(hi[nt][h]);
+                lo[nt][h] = movmatrix(lo[nt][h]);
+            }
+        }
+        const uint32_t vpage = page + R::HALF;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+            uint32_t a[4];
+            ldmatrix4_trans(a, vpage + place<D>((lane & 7) + 8 * (mi >> 1), 2 * x + (mi & 1)));
+            if (p.nq == 1 || key0 + 16 <= fewest ||
+                !__any_sync(0xffffffffu, odd_pair(a[0]) || odd_pair(a[1]) || odd_pair(a[2]) || odd_pair(a[3]))) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_bf16(o[nt][x], a, hi[nt][0], hi[nt][1]);
+                    mma_bf16(o[nt][x], a, lo[nt][0], lo[nt][1]);
+                }
+                continue;
+            }
+            // an infinity or a NaN that not every query sees: key by key
+#pragma unroll 1
+            for (int key = 0; key < 16; ++key) {
+                const bf16 *vr = reinterpret_cast<const bf16 *>(ring + (i % R::DEPTH) * R::PAGE + R::HALF);
+                const float v0 = bf2f(vr[(place<D>(key, 2 * x) >> 1) + g]);
+                const float v1 = bf2f(vr[(place<D>(key, 2 * x + 1) >> 1) + g]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float a0 = __shfl_sync(0xffffffffu, pr[nt][j], (key & 7) * 4 + t);
+                        const float a1 = __shfl_sync(0xffffffffu, pr[nt][j + 2], (key & 7) * 4 + t);
+                        const float w = key < 8 ? a0 : a1;
+                        if (key0 + key < see[nt][j]) {
+                            o[nt][x][j] += w * v0;
+                            o[nt][x][j + 2] += w * v1;
+                        }
+                    }
+            }
+        }
+    }
+    copy_wait<0>();
+    bad = __any_sync(0xffffffffu, bad);
+
+    // ---- join the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float x = l[nt][j];
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            if (g == 0) {
+                s_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
+                s_l[warp][nt * 8 + 2 * t + j] = bad ? nan_f() : x;
+            }
+        }
+    __syncthreads();  // also: no warp's ring is in use any more
+    float *so = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = nt * 8 + 2 * t + j;
+            float mx = s_m[0][c];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w)
+                mx = fmaxf(mx, s_m[w][c]);
+            const float f = ex2((m[nt][j] - (mx == -INFINITY ? 0.f : mx)) * p.c2);
+            float *row = so + (warp * COLS + c) * S::ROW + g;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+                row[x * 16] = o[nt][x][j] * f;
+                row[x * 16 + 8] = o[nt][x][j + 2] * f;
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < COLS * (D / 4); i += WARPS * 32) {
+        const int cl = i / (D / 4), e = i % (D / 4) * 4, c = c0 + cl;
+        if (c >= ncols)
+            break;
+        float mx = s_m[0][cl];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w)
+            mx = fmaxf(mx, s_m[w][cl]);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            sum += s_l[w][cl] * ex2((s_m[w][cl] - (mx == -INFINITY ? 0.f : mx)) * p.c2);
+            const float4 a = *reinterpret_cast<const float4 *>(so + (w * COLS + cl) * S::ROW + e);
+            acc.x += a.x, acc.y += a.y, acc.z += a.z, acc.w += a.w;
+        }
+        const long long row = (long long)seq * p.nq + c / p.group;
+        const int head = kvh * p.group + c % p.group;
+        if (p.n_slots == 1) {
+            const bool none = ctx + 1 - (p.nq - 1) + c / p.group <= 0;
+            const float f = none ? 0.f : 1.f / sum;
+            uint2 u;
+            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+            h[0] = __floats2bfloat162_rn(none ? 0.f : acc.x * f, none ? 0.f : acc.y * f);
+            h[1] = __floats2bfloat162_rn(none ? 0.f : acc.z * f, none ? 0.f : acc.w * f);
+            *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + (size_t)head * D + e) = u;
+        }
+        if (p.n_slots > 1 || SCORES) {
+            const size_t slot = ((size_t)row * p.n_heads + head) * p.n_slots + p.first_slot + split;
+            if (e == 0)
+                p.part_ml[slot] = make_float2(mx, sum);
+            if (p.n_slots > 1)
+                *reinterpret_cast<float4 *>(p.part_o + slot * D + e) = acc;
+        }
+    }
+}
+
+// The join of a row's partials: a warp a (row, head).  The group's first
+// first_slot partials are its prefix's, the others the row's own splits.
+template <int D>
+__device__ __forceinline__ void join_row(const Attn &p, int row, int head, int lane)
+{
+    constexpr int E = D / 32;
+    const int seq = row / p.nq;
+    const int ctx = p.ctx_lens[seq];
+    int from = 0, least = 0;
+    if (p.n_groups > 0) {
+        const Group gr = p.of(seq);
+        from = gr.shared;
+        least = gr.prefix > 0 ? gr.prefix - 1 : 0;
+    }
+    const int keys = ctx + 1 - (p.nq - 1) + row % p.nq;  // that the row sees
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] = 0.f;
+    if (ctx < least || ctx > p.max_ctx) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = ctx == -1 ? 0.f : nan_f();
+    } else if (keys > 0) {
+        const int own = (ctx + 1 - from + p.split_len - 1) / p.split_len;
+        const int s0 = from > 0 ? 0 : p.first_slot, s1 = p.first_slot + own;
+        const size_t at = ((size_t)row * p.n_heads + head) * p.n_slots;
+        float mx = -INFINITY;
+        for (int s = s0 + lane; s < s1; s += 32)
+            mx = fmaxf(mx, __ldcg(&p.part_ml[at + s]).x);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        for (int s = s0; s < s1; ++s) {
+            const float2 ml = __ldcg(&p.part_ml[at + s]);
+            const float f = ex2((ml.x - base) * p.c2);
+            sum += ml.y * f;
+            const float *o = p.part_o + (at + s) * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o));
+                acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(o));
+                acc[0] += v.x * f, acc[1] += v.y * f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = acc[e] / sum;
+    }
+    bf16 *to = p.out + (long long)row * p.out_stride + (size_t)head * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<__nv_bfloat162 *>(to + e) = __floats2bfloat162_rn(acc[e], acc[e + 1]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
+{
+    pdl_wait();
+    pdl_trigger();
+    const long long i = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+    if (i < (long long)n_rows * p.n_heads)
+        join_row<D>(p, (int)(i / p.n_heads), (int)(i % p.n_heads), threadIdx.x & 31);
+}
+
+struct Weigh {
+    float *w;
+    int num_blocks;
+    const int *tables;
+    int stride;
+    float decay;
+    int chunks;      // CTAs of the keys of a kv head
+};
+
+// w = decay w + sum over the kv head's queries of 2^((s - M) c2) / L.  A thread
+// has four neighbouring keys; the queries' M and 1 / L pass through shared
+// memory.
+__global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_constant__ Attn p, const Weigh w)
+{
+    __shared__ float2 ml[WEIGH_THREADS];  // M, 1 / L (0: adds nothing)
+    pdl_wait();
+    pdl_trigger();
+    const int seq = blockIdx.y;
+    const int kvh = blockIdx.x / w.chunks, chunk = blockIdx.x % w.chunks;
+    const int ctx = p.ctx_lens[seq];
+    const int key = (chunk * WEIGH_THREADS + (int)threadIdx.x) * WEIGH_KEYS;
+    if (ctx < 0 || ctx > p.max_ctx || chunk * WEIGH_THREADS * WEIGH_KEYS > ctx)
+        return;
+    const int ncols = p.nq * p.group;
+    const int own = (ctx + p.split_len) / p.split_len;
+    float acc[WEIGH_KEYS] = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < ncols; c0 += WEIGH_THREADS) {
+        const int c = c0 + threadIdx.x;
+        if (c < ncols) {
+            const size_t at = ((size_t)(seq * p.nq + c / p.group) * p.n_heads + kvh * p.group + c % p.group) * p.n_slots;
+            float mx = -INFINITY, sum = 0.f;
+            for (int s = 0; s < own; ++s)
+                mx = fmaxf(mx, __ldcg(&p.part_ml[at + s]).x);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            for (int s = 0; s < own; ++s) {
+                const float2 x = __ldcg(&p.part_ml[at + s]);
+                sum += x.y * ex2((x.x - base) * p.c2);
+            }
+            ml[threadIdx.x] = make_float2(base, sum > 0.f ? 1.f / sum : 0.f);  // NaN: 0
+        }
+        __syncthreads();
+        if (key <= ctx) {
+            const float *s = p.scores + (((size_t)seq * p.n_kv + kvh) * ncols + c0) * p.score_stride + key;
+            const int n = min(WEIGH_THREADS, ncols - c0);
+            for (int i = 0; i < n; ++i, s += p.score_stride) {
+                const float2 x = ml[i];
+                if (x.y == 0.f)
+                    continue;
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(s));
+                acc[0] += ex2((v.x - x.x) * p.c2) * x.y;
+                acc[1] += ex2((v.y - x.x) * p.c2) * x.y;
+                acc[2] += ex2((v.z - x.x) * p.c2) * x.y;
+                acc[3] += ex2((v.w - x.x) * p.c2) * x.y;
+            }
+        }
+        __syncthreads();
+    }
+    if (key > ctx)
+        return;
+    const int blk = w.tables[(size_t)seq * w.stride + (key >> 4)];
+    if (blk < 0 || blk >= w.num_blocks)
+        return;
+    float *to = w.w + ((size_t)blk * p.n_kv + kvh) * 16 + (key & 15);
+#pragma unroll
+    for (int j = 0; j < WEIGH_KEYS; ++j)
+        if (key + j <= ctx) {
+            const bool fresh = w.decay == 0.f || key + j > ctx - p.nq;
+            to[j] = fresh ? acc[j] : w.decay * to[j] + acc[j];
+        }
+}
+
+__global__ void k_paged_groups(Group *to, const __grid_constant__ Attn p, int first, int n)
+{
+    pdl_wait();
+    if ((int)threadIdx.x < n)
+        to[first + threadIdx.x] = p.few[threadIdx.x];
+}
+
+// ------------------------------------------------------------------- host
+
+long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
+
+// Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split.
+void plan_splits(long long base, int keys, int *len, int *n)
+{
+    const long long want = 912 / (base > 0 ? base : 1);
+    long long s = keys / SPLIT_MIN;
+    s = s < want ? s : want;
+    s = s < 1 ? 1 : s;
+    const long long each = round_up((keys + s - 1) / s, 64);
+    *len = (int)(each > 0 ? each : 64);
+    *n = (int)((keys + *len - 1) / *len);
+    if (*n < 1)
+        *n = 1;
+}
+
+struct Layout {
+    long long ml, o, scores, groups, bytes;  // byte offsets of the workspace
+    long long score_stride;
+};
+
+Layout layout(long long rows, int heads, int d, int slots, int groups, bool scores, int max_ctx)
+{
+    Layout w;
+    w.ml = 0;
+    w.score_stride = scores ? round_up((long long)max_ctx + 1, 32) : 0;
+    const bool parts = slots > 1 || scores;
+    w.o = w.ml + (parts ? round_up(rows * heads * slots * 8, 256) : 0);
+    w.scores = w.o + (slots > 1 ? round_up(rows * heads * slots * d * 4, 256) : 0);
+    w.groups = w.scores + rows * heads * w.score_stride * 4;
+    w.bytes = w.groups + (groups > INLINE_GROUPS ? round_up((long long)groups * sizeof(Group), 256) : 0);
+    return w;
+}
+
+int tiles_of(long long cols, int nt) { return (int)((cols + 8 * nt - 1) / (8 * nt)); }
+
+template <int D, int NT, bool SCORES>
+int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    auto kernel = k_paged_attention<D, NT, SCORES>;
+    const long long gx = (long long)p.n_kv * p.col_tiles * p.n_splits;  // at most the heads, or 912
+    if (kv4_allow_smem((const void *)kernel, Smem<D, NT>::BYTES, done) != cudaSuccess)
+        return HB_ECUDA;
+    return launch_kernel(true, kernel, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WARPS * 32), Smem<D, NT>::BYTES, s,
+                         p) == cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
+}
+
+template <bool SCORES>
+int attention(const Attn &p, int d, int nt, int n_seqs, cudaStream_t s)
+{
+    if (d == 128)
+        return nt == 1 ? launch_attention<128, 1, SCORES>(p, n_seqs, s) : launch_attention<128, 2, SCORES>(p, n_seqs, s);
+    return nt == 1 ? launch_attention<64, 1, SCORES>(p, n_seqs, s) : launch_attention<64, 2, SCORES>(p, n_seqs, s);
+}
+
+// Checks that the attention calls share.  rows: of q and out.
+int check_attention(const hb_paged_pool *pool, const void *q, long long q_stride, const int32_t *tables, int bt_stride,
+                    const int32_t *ctx_lens, long long rows, int n_heads, int max_ctx, const void *out,
+                    long long out_stride)
+{
+    int rc = check_pool(pool);
+    if (rc)
+        return rc;
+    if (!tables || !ctx_lens || n_heads < 1 || n_heads % pool->n_kv_heads || max_ctx < 0)
+        return HB_EINVAL;
+    if ((uintptr_t)tables % 4 || (uintptr_t)ctx_lens % 4)
+        return HB_EINVAL;
+    if ((long long)n_heads * pool->head_dim > 0x7fffffffll)
+        return HB_ERANGE;
+    if ((rc = kv4_check_rows(q, q_stride, (int)rows, n_heads * pool->head_dim)) ||
+        (rc = kv4_check_rows(out, out_stride, (int)rows, n_heads * pool->head_dim)))
+        return rc;
+    if (max_ctx >= MAX_KEYS || bt_stride < max_ctx / 16 + 1 || rows > 65535 || rows * n_heads > 0x7fffffffll)
+        return HB_ERANGE;
+    return HB_OK;
+}
+
+struct Plan {
+    int nt, split_len, n_splits, col_tiles, first_slot, n_slots;
+    Layout at;
+};
+
+// What hb_decode_shared does with its groups; groups may be null.  HB_OK or an error.
+int plan_shared(int n_rows, int n_heads, int n_kv, int d, int max_ctx, const int32_t *group_rows,
+                const int32_t *prefix_lens, int n_groups, Plan *pl)
+{
+    if (!group_rows || !prefix_lens || n_groups < 1)
+        return HB_EINVAL;
+    long long rows = 0;
+    for (int i = 0; i < n_groups; ++i) {
+        if (group_rows[i] < 1 || prefix_lens[i] < 0)
+            return HB_EINVAL;
+        if (prefix_lens[i] > max_ctx + 1)
+            return HB_ERANGE;
+        rows += group_rows[i];
+    }
+    if (rows != n_rows)
+        return HB_EINVAL;
+    const int g = n_heads / n_kv;
+    pl->nt = g > 8 ? 2 : 1;
+    pl->col_tiles = tiles_of(g, pl->nt);
+    plan_splits((long long)n_rows * n_kv * pl->col_tiles, max_ctx + 1, &pl->split_len, &pl->n_splits);
+    pl->first_slot = 0;
+    pl->n_slots = pl->first_slot + pl->n_splits;
+    pl->at = layout(n_rows, n_heads, d, pl->n_slots, n_groups, false, max_ctx);
+    return HB_OK;
+}
+
+int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int max_ctx, Plan *pl)
+{
+    const int g = n_heads / n_kv;
+    const long long cols = (long long)nq * g;
+    if (cols > 1 << 24)
+        return HB_ERANGE;
+    pl->nt = cols > 8 ? 2 : 1;
+    pl->col_tiles = tiles_of(cols, pl->nt);
+    plan_splits(n_seqs * n_kv * pl->col_tiles, max_ctx + 1, &pl->split_len, &pl->n_splits);
+    pl->first_slot = 0;
+    pl->n_slots = pl->n_splits;
+    pl->at = layout(n_seqs * nq, n_heads, d, pl->n_slots, 0, true, max_ctx);
+    return HB_OK;
+}
+
+Attn params(const hb_paged_pool *pool, const void *q, long long q_stride, const int32_t *tables, int bt_stride,
+            const int32_t *ctx_lens, int n_heads, int max_ctx, int nq, void *out, long long out_stride, const Plan &pl,
+            void *workspace)
+{
+    Attn p = {};
+    p.k = (const bf16 *)pool->k;
+    p.v = (const bf16 *)pool->v;
+    p.num_blocks = pool->num_blocks;
+    p.n_kv = pool->n_kv_heads;
+    p.n_heads = n_heads;
+    p.group = n_heads / pool->n_kv_heads;
+    p.q = (const bf16 *)q;
+    p.q_stride = q_stride;
+    p.tables = tables;
+    p.bt_stride = bt_stride;
+    p.ctx_lens = ctx_lens;
+    p.max_ctx = max_ctx;
+    p.nq = nq;
+    p.c2 = LOG2E / sqrtf((float)pool->head_dim);
+    p.split_len = pl.split_len;
+    p.n_splits = pl.n_splits;
+    p.col_tiles = pl.col_tiles;
+    p.first_slot = pl.first_slot;
+    p.n_slots = pl.n_slots;
+    p.out = (bf16 *)out;
+    p.out_stride = out_stride;
+    char *w = (char *)workspace;
+    p.part_ml = (float2 *)(w + pl.at.ml);
+    p.part_o = (float *)(w + pl.at.o);
+    p.scores = (float *)(w + pl.at.scores);
+    p.score_stride = pl.at.score_stride;
+    return p;
+}
+
+int check_workspace(const void *workspace, long long bytes, long long need)
+{
+    if (need > 0 && (!workspace || (uintptr_t)workspace % 16))
+        return HB_EINVAL;
+    return bytes < need ? HB_ERANGE : HB_OK;
+}
+
+int check_heads(int n_heads, int n_kv, int d, int max_ctx)
+{
+    if (n_heads < 1 || n_kv < 1 || n_heads % n_kv || (d != 64 && d != 128) || max_ctx < 0)
+        return HB_EINVAL;
+    return max_ctx >= MAX_KEYS || (long long)n_heads * d > 0x7fffffffll ? HB_ERANGE : HB_OK;
+}
+
+}  // namespace
+
+namespace paged {
+
+int check_pool(const hb_paged_pool *p)
+{
+    if (!p || !p->k || !p->v || (uintptr_t)p->k % 16 || (uintptr_t)p->v % 16 || p->num_blocks < 1 ||
+        p->n_kv_heads < 1 || (p->head_dim != 64 && p->head_dim != 128))
+        return HB_EINVAL;
+    return HB_OK;
+}
+
+int check_weight_pool(const hb_weight_pool *p)
+{
+    return !p || !p->data || (uintptr_t)p->data % 16 || p->num_blocks < 1 || p->n_kv_heads < 1 ? HB_EINVAL : HB_OK;
+}
+
+}  // namespace paged
+}  // namespace hb
+
+using namespace hb;
+using namespace hb::paged;
+
+extern "C" long long hb_decode_shared_workspace(int n_rows, int n_heads, int n_kv_heads, int head_dim, int max_ctx,
+                                                const int32_t *group_rows, const int32_t *prefix_lens, int n_groups)
+{
+    if (n_rows < 0 || n_groups < 0 || (n_rows == 0) != (n_groups == 0))
+        return HB_EINVAL;
+    const int rc = check_heads(n_heads, n_kv_heads, head_dim, max_ctx);
+    if (rc)
+        return rc;
+    if (n_rows == 0)
+        return 0;
+    if (n_rows > 65535 || (long long)n_rows * n_heads > 0x7fffffffll)
+        return HB_ERANGE;
+    Plan pl;
+    const int rp = plan_shared(n_rows, n_heads, n_kv_heads, head_dim, max_ctx, group_rows, prefix_lens, n_groups, &pl);
+    return rp ? rp : pl.at.bytes;
+}
+
+extern "C" int hb_decode_shared(const hb_paged_pool *pool, const void *q, long long q_stride,
+                                const int32_t *block_tables, int bt_stride, const int32_t *ctx_lens, int n_rows,
+                                int n_heads, int max_ctx, const int32_t *group_rows, const int32_t *prefix_lens,
+                                int n_groups, void *out, long long out_stride, void *workspace,
+                                long long workspace_bytes, void *cuda_stream)
+try {
+    if (n_rows < 0 || n_groups < 0 || (n_rows == 0) != (n_groups == 0))
+        return HB_EINVAL;
+    if (n_rows == 0)
+        return check_pool(pool);
+    int rc = check_attention(pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_rows, n_heads, max_ctx, out,
+                             out_stride);
+    if (rc)
+        return rc;
+    Plan pl;
+    rc = plan_shared(n_rows, n_heads, pool->n_kv_heads, pool->head_dim, max_ctx, group_rows, prefix_lens, n_groups,
+                     &pl);
+    if (rc || (rc = check_workspace(workspace, workspace_bytes, pl.at.bytes)))
+        return rc;
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    Attn p = params(pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, 1, out, out_stride, pl,
+                    workspace);
+    p.n_groups = n_groups;
+    Group *list = (Group *)((char *)workspace + pl.at.groups);
+    int row = 0;
+    for (int i = 0; i < n_groups; ++i) {
+        const int at = n_groups <= INLINE_GROUPS ? i : i % INLINE_GROUPS;
+        p.few[at] = Group{row, group_rows[i], prefix_lens[i], 0};
+        row += group_rows[i];
+        if (n_groups > INLINE_GROUPS && (at == INLINE_GROUPS - 1 || i == n_groups - 1))
+            if (launch_kernel(true, k_paged_groups, dim3(1), dim3(32), 0, s, list, p, i - at, at + 1) != cudaSuccess)
+                return HB_ECUDA;
+    }
+    p.groups = n_groups > INLINE_GROUPS ? list : nullptr;
+    rc = attention<false>(p, pool->head_dim, pl.nt, n_rows, s);
+    if (rc || pl.n_slots == 1)
+        return rc;
+    const long long blocks = ((long long)n_rows * n_heads + JOIN_WARPS - 1) / JOIN_WARPS;
+    return launch_kernel(true, pool->head_dim == 128 ? k_paged_join<128> : k_paged_join<64>, dim3((unsigned)blocks),
+                         dim3(JOIN_WARPS * 32), 0, s, p, n_rows) == cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
+} catch (...) {
+    return HB_ENOMEM;
+}
+
+extern "C" long long hb_decode_weigh_workspace(int n_seqs, int n_queries, int n_heads, int n_kv_heads, int head_dim,
+                                               int max_ctx)
+{
+    if (n_seqs < 0 || n_queries < 1)
+        return HB_EINVAL;
+    const int rc = check_heads(n_heads, n_kv_heads, head_dim, max_ctx);
+    if (rc)
+        return rc;
+    if (n_queries > 1024 || (long long)n_seqs * n_queries > 65535 ||
+        (long long)n_seqs * n_queries * n_heads > 0x7fffffffll)
+        return HB_ERANGE;
+    if (n_seqs == 0)
+        return 0;
+    Plan pl;
+    const int rp = plan_weigh(n_seqs, n_queries, n_heads, n_kv_heads, head_dim, max_ctx, &pl);
+    return rp ? rp : pl.at.bytes;
+}
+
+extern "C" int hb_decode_weigh(const hb_paged_pool *pool, const void *q, long long q_stride,
+                               const int32_t *block_tables, int bt_stride, const int32_t *ctx_lens, int n_seqs,
+                               int n_queries, int n_heads, int max_ctx, const hb_weight_pool *weights,
+                               const int32_t *weight_tables, int wt_stride, float decay, void *out,
+                               long long out_stride, void *workspace, long long workspace_bytes, void *cuda_stream)
+try {
+    if (n_seqs < 0 || n_queries < 1 || !(decay >= 0.f && decay <= 1.f))
+        return HB_EINVAL;
+    int rc = check_pool(pool);
+    if (rc || (rc = check_weight_pool(weights)))
+        return rc;
+    if (weights->n_kv_heads != pool->n_kv_heads)
+        return HB_EINVAL;
+    if (n_queries > 1024)
+        return HB_ERANGE;
+    if (n_seqs == 0)
+        return HB_OK;
+    if ((long long)n_seqs * n_queries > 65535)
+        return HB_ERANGE;
+    const int rows = n_seqs * n_queries;
+    rc = check_attention(pool, q, q_stride, block_tables, bt_stride, ctx_lens, rows, n_heads, max_ctx, out, out_stride);
+    if (rc)
+        return rc;
+    if (!weight_tables || (uintptr_t)weight_tables % 4)
+        return HB_EINVAL;
+    if (wt_stride < max_ctx / 16 + 1)
+        return HB_ERANGE;
+    Plan pl;
+    if ((rc = plan_weigh(n_seqs, n_queries, n_heads, pool->n_kv_heads, pool->head_dim, max_ctx, &pl)) ||
+        (rc = check_workspace(workspace, workspace_bytes, pl.at.bytes)))
+        return rc;
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    const Attn p = params(pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, n_queries, out,
+                          out_stride, pl, workspace);
+    const int chunks = max_ctx / (WEIGH_THREADS * WEIGH_KEYS) + 1;
+    const long long gx = (long long)p.n_kv * chunks;
+    const long long jx = ((long long)rows * n_heads + JOIN_WARPS - 1) / JOIN_WARPS;
+    if (gx > 0x7fffffffll)
+        return HB_ERANGE;
+    if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)))
+        return rc;
+    if (pl.n_slots > 1 &&
+        launch_kernel(true, pool->head_dim == 128 ? k_paged_join<128> : k_paged_join<64>, dim3((unsigned)jx),
+                      dim3(JOIN_WARPS * 32), 0, s, p, rows) != cudaSuccess)
+        return HB_ECUDA;
+    const Weigh w = {weights->data, weights->num_blocks, weight_tables, wt_stride, decay, chunks};
+    return launch_kernel(true, k_paged_weigh, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WEIGH_THREADS), 0, s, p, w) ==
+                   cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
+} catch (...) {
+    return HB_ENOMEM;
+}

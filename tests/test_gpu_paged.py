@@ -1,0 +1,539 @@
+"""Attention over shared prefixes, attention weights and eviction on the GPU,
+against plain 64-bit forms (paged_ref.py)."""
+import numpy as np
+import pytest
+
+import paged_ref as ref
+from chunked_prefill_hybrid_gb300 import cache, native, paged
+from chunked_prefill_hybrid_gb300.native import HbError
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _dev(x, dtype=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype)).cuda()
+
+
+def _bf(rng, *shape, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16).cuda()
+
+
+class Case:
+    """Rows in groups over one pool: row j's table starts with its group's shared pages."""
+
+    def __init__(self, seed, kv, group, d, rows, prefix, ctx, spare=2, poison=True, scale=1.0):
+        rng = np.random.default_rng(seed)
+        self.kv, self.group, self.d, self.rows, self.prefix = kv, group, d, list(rows), list(prefix)
+        self.ctx = np.array(ctx, np.int64)
+        n = len(ctx)
+        assert n == sum(rows)
+        of = np.repeat(np.arange(len(rows)), rows)
+        shared = np.array(prefix)[of] // 16
+        width = max(1, int(max(max(self.ctx) // 16 + 1, max(shared))))
+        need = np.maximum(self.ctx // 16 + 1 - shared, 0)
+        blocks = int(need.sum()) + sum(p // 16 for p in prefix) + spare
+        perm = list(rng.permutation(blocks))
+        common = [[perm.pop() for _ in range(p // 16)] for p in prefix]
+        self.tables = np.full((n, width), -1, np.int64)  # entries that nothing needs are never read
+        for j in range(n):
+            t = common[of[j]] + [perm.pop() for _ in range(need[j])]
+            self.tables[j, :len(t)] = t
+        self.k, self.v = _bf(rng, blocks, kv, 16, d, scale=scale), _bf(rng, blocks, kv, 16, d)
+        first = np.cumsum(rows) - rows
+        for g, p in enumerate(prefix):  # the part-filled page: the same tokens in each row's copy
+            if p % 16:
+                for j in range(first[g] + 1, first[g] + rows[g]):
+                    a, b = self.tables[first[g], p // 16], self.tables[j, p // 16]
+                    if a >= 0 and b >= 0:
+                        for pool in (self.k, self.v):
+                            pool[b, :, :p % 16] = pool[a, :, :p % 16]
+        if poison:  # every slot that no row sees
+            seen = np.zeros((blocks, 16), bool)
+            for g, p in enumerate(prefix):
+                for b in common[g]:
+                    seen[b] = True
+            for j in range(n):
+                for t in range(self.ctx[j] + 1):
+                    seen[self.tables[j, t // 16], t % 16] = True
+            hide = torch.from_numpy(~seen).cuda()
+            for pool, bad in ((self.k, NAN), (self.v, float("inf"))):
+                pool.transpose(1, 2)[hide] = bad
+        self.q = _bf(rng, n, kv * group, d)
+        self.pool = paged.PagedPool(self.k, self.v)
+
+    def run(self, q=None, out=None, max_ctx=None, ctx=None, tables=None, workspace=None):
+        q = self.q if q is None else q
+        out = torch.full_like(self.q, 7.0) if out is None else out
+        max_ctx = max(0, int(self.ctx.max())) if max_ctx is None else max_ctx
+        tables = self.tables if tables is None else tables
+        if tables.shape[1] < max_ctx // 16 + 1:
+            tables = np.pad(tables, ((0, 0), (0, max_ctx // 16 + 1 - tables.shape[1])), constant_values=-1)
+        paged.decode_shared(self.pool, q, _dev(tables), _dev(self.ctx if ctx is None else ctx), max_ctx, self.rows,
+                            self.prefix, out, workspace)
+        torch.cuda.synchronize()
+        return out
+
+    def check(self, out, rows=None):
+        o, b = ref.shared(_f64(self.q), _f64(self.k), _f64(self.v), self.tables, self.ctx, self.group)
+        rows = range(len(self.ctx)) if rows is None else rows
+        got = _f64(out)
+        for j in rows:
+            assert (np.abs(got[j] - o[j]) <= b[j]).all(), (j, np.abs(got[j] - o[j]).max(), b[j].max())
+
+
+# ----------------------------------------------------------- shared prefixes
+
+@pytest.mark.parametrize("kv,group,d,rows,prefix,ctx", [
+    (1, 1, 64, [1], [0], [0]),                                          # one row, one key
+    (2, 1, 128, [4], [64], [64, 79, 80, 200]),
+    (3, 1, 64, [3], [16], [15, 16, 300]),                               # a row whose own keys are none
+    (2, 3, 128, [2, 3], [0, 37], [0, 5, 36, 37, 90]),                   # an odd prefix, part-filled pages
+    (1, 8, 128, [5], [1000], [1000, 1001, 1015, 1016, 2100]),
+    (2, 12, 64, [2, 1], [100, 50], [99, 130, 700]),                     # more than eight heads a kv head
+    (1, 20, 128, [3], [333], [333, 500, 340]),
+    (1, 5, 64, [2, 2], [15, 17], [14, 15, 16, 17]),                     # prefixes about one page
+    (5, 1, 128, [18], [768], [1024] * 18),
+    (2, 4, 128, [40], [513], [513 + 7 * j for j in range(40)]),         # more queries than a tile of 128
+    (1, 64, 64, [9, 1, 2], [640, 640, 0], [640 + j for j in range(9)] + [700, 3, 650]),
+    (1, 1, 128, [150], [2049], [2049 + j for j in range(150)]),
+])
+def test_shared_matches_the_plain_form(kv, group, d, rows, prefix, ctx):
+    c = Case(sum(ctx) + kv, kv, group, d, rows, prefix, ctx)
+    out = c.run()
+    c.check(out)
+    assert torch.equal(out, c.run())  # the same bits again
+    wide = c.run(max_ctx=max(ctx) + 4000)  # another split of the keys
+    c.check(wide)
+
+
+def test_shared_with_many_groups():
+    """More groups than the kernels' parameters hold, of every kind."""
+    rng = np.random.default_rng(5)
+    rows = [int(x) for x in rng.integers(1, 4, 45)]
+    prefix = [int(x) for x in rng.integers(0, 90, 45)]
+    ctx = [prefix[g] + int(rng.integers(0, 70)) for g in range(45) for _ in range(rows[g])]
+    c = Case(6, 2, 2, 64, rows, prefix, ctx)
+    c.check(c.run())
+
+
+def test_shared_padding_and_rows_out_of_range():
+    c = Case(7, 2, 2, 128, [4, 3], [40, 0], [60, 45, 50, 39, 10, 0, 30])
+    ctx = c.ctx.copy()
+    ctx[[1, 5]] = -1     # padding
+    ctx[2] = 38          # does not cover its prefix
+    ctx[4] = 1000        # past max_ctx
+    ctx[6] = -2
+    out = c.run(ctx=ctx, max_ctx=60)
+    assert (out[[1, 5]] == 0).all()
+    assert torch.isnan(out[[2, 4, 6]]).all()
+    c.check(out, [0, 3])
+    alone = Case(8, 1, 1, 64, [1, 1], [0, 0], [5, 9])  # the same without splits
+    out = alone.run(ctx=np.array([-1, 400]), max_ctx=16)
+    assert (out[0] == 0).all() and torch.isnan(out[1]).all()
+
+
+def test_shared_blocks_outside_the_pool():
+    c = Case(9, 2, 1, 64, [3, 2], [64, 0], [100, 90, 70, 40, 30])
+    bad = c.tables.copy()
+    bad[1, 5] = c.k.shape[0]         # an own page of row 1
+    bad[3, 0] = -7
+    out = c.run(tables=bad)
+    assert bool(torch.isnan(out[[1, 3]]).all())
+    c.check(out, [0, 2, 4])
+    bad = c.tables.copy()
+    bad[0, 1] = 1 << 30              # the prefix, through the first row's table
+    out = c.run(tables=bad)
+    assert bool(torch.isnan(out[:3]).all())
+    c.check(out, [3, 4])
+    bad[0, 1] = c.tables[0, 1]
+    bad[1:3, :4] = -1                # the others' entries of the shared pages are not read
+    c.check(c.run(tables=bad))
+
+
+@pytest.mark.parametrize("kv,group,d", [(3, 1, 128), (2, 4, 64)])
+def test_shared_takes_strided_rows_and_leaves_the_rest(kv, group, d):
+    c = Case(11, kv, group, d, [3, 1], [33, 5], [70, 80, 33, 90])
+    heads = kv * group
+    big = torch.full((4, heads + 3, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    big[:, 1:1 + heads] = c.q
+    out = torch.full((4, heads + 2, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    c.run(q=big[:, 1:1 + heads], out=out[:, 2:])
+    assert torch.equal(out[:, 2:], c.run())
+    assert (out[:, :2] == 3.0).all()
+
+
+def test_shared_large_and_infinite_scores():
+    c = Case(12, 1, 2, 64, [3], [100], [150, 100, 130], poison=False, scale=300.0)
+    c.q *= 100.0  # scores of 1e5: one key takes all
+    c.check(c.run())
+    c = Case(13, 1, 1, 64, [2], [32], [70, 80], poison=False)
+    c.k[c.tables[0, 0], 0, 3] = 0.0
+    c.k[c.tables[0, 0], 0, 3, 0] = -float("inf")  # a key of the prefix that no row with q[0] > 0 looks at
+    c.q[:, :, 0] = 1.0
+    out = c.run()
+    c.check(out)
+    c.v[c.tables[0, 1], 0, 2, 9] = NAN  # a NaN in the prefix is every row's
+    assert torch.isnan(c.run()[:, 0, 9]).all()
+
+
+def test_shared_pool_past_four_gigabytes():
+    """Pages whose bytes lie beyond 2^32: the last ones of a pool of 2^18 blocks of 8 kv heads."""
+    kv, d, blocks = 8, 128, (1 << 18) + 40
+    k = torch.empty(blocks, kv, 16, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    small = Case(14, kv, 1, d, [2], [48], [100, 60], poison=False)
+    m = small.k.shape[0]
+    k[-m:], v[-m:] = small.k, small.v
+    far = np.where(small.tables >= 0, small.tables + blocks - m, -1)
+    out, want = torch.empty_like(small.q), small.run()
+    paged.decode_shared(paged.PagedPool(k, v), small.q, _dev(far), _dev(small.ctx), 100, [2], [48], out)
+    assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------- weights
+
+def _weigh_case(seed, kv, group, d, ctx, nq, poison=True):
+    c = Case(seed, kv, group, d, [1] * len(ctx), [0] * len(ctx), ctx, poison=poison)
+    rng = np.random.default_rng(seed + 1)
+    c.q = _bf(rng, len(ctx) * nq, kv * group, d)
+    wb = c.k.shape[0] + 5
+    perm = rng.permutation(wb)
+    c.wtables = np.full((len(ctx), c.tables.shape[1]), -1, np.int64)
+    at = 0
+    for j, x in enumerate(ctx):
+        m = x // 16 + 1 if x >= 0 else 0
+        c.wtables[j, :m] = perm[at:at + m]
+        at += m
+    c.w = torch.from_numpy(rng.random((wb, kv, 16)).astype(np.float32)).cuda()
+    return c
+
+
+def _weigh(c, nq, decay, **over):
+    out = torch.full_like(c.q, 7.0)
+    w = c.w.clone()
+    max_ctx = over.get("max_ctx", max(0, int(c.ctx.max())))
+    pad = max(0, max_ctx // 16 + 1 - c.tables.shape[1])
+    tables, wtables = (np.pad(t, ((0, 0), (0, pad)), constant_values=-1) for t in (c.tables, c.wtables))
+    paged.decode_weigh(c.pool, c.q, _dev(over.get("tables", tables)), _dev(over.get("ctx", c.ctx)), max_ctx, w,
+                       _dev(over.get("wtables", wtables)), decay, out)
+    torch.cuda.synchronize()
+    return out, w
+
+
+@pytest.mark.parametrize("kv,group,d,ctx,nq,decay", [
+    (1, 1, 64, [0], 1, 1.0),
+    (2, 1, 128, [5, -1, 15, 16, 300], 1, 1.0),
+    (3, 4, 64, [1000, 31], 1, 0.5),
+    (1, 8, 128, [2300], 1, 0.96875),
+    (2, 12, 64, [100, 40], 1, 0.0),
+    (2, 1, 64, [1, 2, 50], 2, 1.0),
+    (1, 3, 128, [6, 300, 40], 7, 0.25),       # more than eight queries, the first row of all at position 0
+    (2, 2, 64, [10, 33, 700], 33, 1.0),       # queries before the start of their sequences
+    (1, 5, 64, [90], 64, 0.0),                # more queries than the weights' kernel takes at once
+])
+def test_weigh_matches_the_plain_form(kv, group, d, ctx, nq, decay):
+    c = _weigh_case(sum(ctx) + nq, kv, group, d, ctx, nq)
+    old = _f64(c.w)
+    if decay == 0:
+        c.w.fill_(NAN)  # what is not to count may be anything
+    out, w = _weigh(c, nq, decay)
+    o, b, want, wb = ref.weigh(_f64(c.q), _f64(c.k), _f64(c.v), c.tables, c.ctx, group, nq, old, c.wtables, decay)
+    assert (np.abs(_f64(out) - o) <= b).all()
+    touched = wb > 0
+    got = _f64(w)
+    assert (np.abs(got - want) <= wb)[touched].all(), np.abs(got - want)[touched].max()
+    assert np.array_equal(got[~touched], _f64(c.w)[~touched], equal_nan=True)  # other slots stay
+    again = _weigh(c, nq, decay)
+    assert torch.equal(again[0], out) and torch.equal(again[1][~torch.isnan(w)], w[~torch.isnan(w)])
+    far = _weigh(c, nq, decay, max_ctx=max(ctx) + 3000)
+    assert (np.abs(_f64(far[0]) - o) <= b).all() and (np.abs(_f64(far[1]) - want) <= wb)[touched].all()
+
+
+def test_weigh_new_tokens_start_from_zero():
+    c = _weigh_case(3, 2, 2, 64, [40, 20], 3)
+    dirty = c.w.clone()
+    for j, x in enumerate(c.ctx):
+        for t in range(x - 2, x + 1):
+            c.w[c.wtables[j, t // 16], :, t % 16] = NAN
+    out, w = _weigh(c, 3, 1.0)
+    o, b, want, wb = ref.weigh(_f64(c.q), _f64(c.k), _f64(c.v), c.tables, c.ctx, 2, 3, _f64(dirty), c.wtables, 1.0)
+    assert (np.abs(_f64(w) - want) <= wb)[wb > 0].all()
+
+
+def test_weigh_sequences_and_blocks_out_of_range():
+    c = _weigh_case(4, 2, 1, 64, [40, 100, 30, 20], 1)
+    ctx = c.ctx.copy()
+    ctx[0], ctx[1] = -1, 101
+    tables, wtables = c.tables.copy(), c.wtables.copy()
+    tables[2, 0] = c.k.shape[0]
+    wtables[3, 1] = -5
+    out, w = _weigh(c, 1, 0.5, ctx=ctx, max_ctx=100, tables=tables, wtables=wtables)
+    o, b, want, wb = ref.weigh(_f64(c.q), _f64(c.k), _f64(c.v), c.tables, c.ctx, 1, 1, _f64(c.w), c.wtables, 0.5)
+    assert (out[0] == 0).all() and torch.isnan(out[1]).all() and torch.isnan(out[2]).all()
+    assert (np.abs(_f64(out[3]) - o[3]) <= b[3]).all()
+    got, old = _f64(w), _f64(c.w)
+    for j in (0, 1):
+        used = [x for x in c.wtables[j] if x >= 0]
+        assert np.array_equal(got[used], old[used])
+    for t in range(31):  # a bad block: nothing is added, old weights fade all the same
+        x = (c.wtables[2, t // 16], slice(None), t % 16)
+        assert np.array_equal(got[x], 0.5 * old[x] if t < 30 else 0 * old[x])
+    for t in range(21):
+        x = (c.wtables[3, t // 16], slice(None), t % 16)
+        if t < 16:
+            assert (np.abs(got[x] - want[x]) <= wb[x]).all()
+        else:
+            assert np.array_equal(got[x], old[x])  # the block outside the pool: neither read nor written
+
+
+def test_weigh_a_head_that_is_not_a_number_adds_nothing():
+    c = _weigh_case(5, 1, 2, 64, [50], 1)
+    c.q[0, 1, 5] = NAN
+    out, w = _weigh(c, 1, 1.0)
+    assert torch.isnan(out[0, 1]).all() and torch.isfinite(out[0, 0]).all()
+    half = _weigh_case(5, 1, 2, 64, [50], 1)
+    half.q[0, 1] = half.q[0, 0]
+    _, twice = _weigh(half, 1, 0.0)
+    t = 7
+    x = (c.wtables[0, t // 16], 0, t % 16)
+    assert abs(float(w[x]) - float(c.w[x]) - 0.5 * float(twice[x])) <= 1e-6
+
+
+def test_weigh_queries_do_not_see_later_infinities():
+    """V of a later token of the call's own rows is infinite: rows before it are as ever."""
+    c = _weigh_case(6, 1, 3, 64, [40], 6)
+    o, b, _, _ = ref.weigh(_f64(c.q), _f64(c.k), _f64(c.v), c.tables, c.ctx, 3, 6, _f64(c.w), c.wtables, 1.0)
+    c.v[c.tables[0, 2], 0, 38 % 16] = float("inf")
+    c.v[c.tables[0, 2], 0, 40 % 16, 3] = NAN
+    out, w = _weigh(c, 6, 1.0)
+    got = _f64(out)
+    assert (np.abs(got[:3] - o[:3]) <= b[:3]).all()     # positions 35, 36, 37
+    assert np.isposinf(got[3:5]).all()                  # 38, 39
+    assert np.isnan(got[5, :, 3]).all() and np.isposinf(np.delete(got[5], 3, axis=1)).all()
+    assert torch.isfinite(w[c.wtables[0, :3]]).all()
+
+
+# ------------------------------------------------------------------ eviction
+
+def _weight_pool(rng, lens, kv, spare=3, stride=0):
+    need = [(int(m) + 15) // 16 for m in lens]
+    blocks = sum(need) + spare
+    perm = rng.permutation(blocks)
+    tables = np.full((len(lens), max(max(need), stride, 1)), -1, np.int64)
+    at = 0
+    for j, m in enumerate(need):
+        tables[j, :m] = perm[at:at + m]
+        at += m
+    return np.exp(2 * rng.standard_normal((blocks, kv, 16))).astype(np.float32), tables
+
+
+def _select(w, tables, lens, keep, first, recent, max_len=None):
+    kept = torch.full((len(lens), w.shape[1], keep), 12345, dtype=torch.int32, device="cuda")
+    paged.evict_select(_dev(w, np.float32), _dev(tables), _dev(lens), max(lens) if max_len is None else max_len, keep,
+                       first, recent, kept)
+    torch.cuda.synchronize()
+    return kept.cpu().numpy()
+
+
+@pytest.mark.parametrize("lens,kv,keep,first,recent", [
+    ([1], 1, 1, 0, 0), ([5, 1, 0, 17], 2, 1, 0, 0), ([5, 2, 33], 3, 2, 1, 1), ([100, 64, 65, 63], 2, 64, 4, 8),
+    ([200, 31, 129], 4, 32, 4, 8), ([300], 1, 299, 0, 0), ([1025, 513], 5, 512, 4, 128), ([4096, 4097], 1, 100, 0, 100),
+    ([4095], 2, 50, 50, 0), ([9000, 5000], 2, 4500, 100, 1000), ([70000], 1, 30000, 4, 64),
+])
+def test_select_keeps_the_heaviest(lens, kv, keep, first, recent):
+    rng = np.random.default_rng(sum(lens) + keep)
+    w, tables = _weight_pool(rng, lens, kv)
+    assert np.array_equal(_select(w, tables, lens, keep, first, recent), ref.select(w, tables, lens, keep, first, recent))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_select_ties_signs_and_numbers_that_are_none(seed):
+    """Few distinct values, both zeros, infinities, NaN, denormals and negative ones: the lower position first."""
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(1, 5000, 3)]
+    w, tables = _weight_pool(rng, lens, 2)
+    pick = np.array([0.0, -0.0, 1.0, 1.0, np.inf, -np.inf, NAN, -NAN, 1e-45, -1e-45, -3.0, 2.5, 2.5000002], np.float32)
+    w[:] = pick[rng.integers(0, len(pick), w.shape)] if seed < 3 else 0.0
+    for j in range(3):
+        if lens[j] > 40:
+            tables[j, 1] = [-1, w.shape[0], 1 << 30][j]  # weights outside the pool
+    for keep in (1, 7, max(1, min(lens) // 2), max(lens) // 2 + 1):
+        first, recent = min(2, keep // 3), min(3, keep // 3)
+        assert np.array_equal(_select(w, tables, lens, keep, first, recent),
+                              ref.select(w, tables, lens, keep, first, recent)), (lens, keep)
+
+
+def test_select_lengths_out_of_range():
+    rng = np.random.default_rng(1)
+    w, tables = _weight_pool(rng, [50, 50, 50], 2)
+    kept = _select(w, tables, [51, -1, 50], 20, 0, 0, max_len=50)
+    assert (kept[:2] == -1).all()
+    assert np.array_equal(kept[2:], ref.select(w, tables[2:], [50], 20, 0, 0))
+
+
+def _move_case(seed, d, kv, lens, keep, place):
+    """Pools of random bytes, kept as select gives it; place: new pages, the old tables, or every other page new."""
+    rng = np.random.default_rng(seed)
+    w, tables = _weight_pool(rng, lens, kv, spare=sum((min(m, keep) + 15) // 16 for m in lens) + 2)
+    blocks = w.shape[0]
+    free = [b for b in range(blocks) if b not in set(tables.ravel())]
+    width = (keep + 15) // 16
+    new = np.full((len(lens), width), -1, np.int64)
+    for j, m in enumerate(lens):
+        for i in range((min(m, keep) + 15) // 16):
+            fresh = place == "new" or (place == "mixed" and i % 2)
+            new[j, i] = free.pop() if fresh else tables[j, i]
+    k, v = _bf(rng, blocks, kv, 16, d), _bf(rng, blocks, kv, 16, d)
+    kept = ref.select(w, tables, lens, keep, min(2, keep), 0)
+    return w, tables, new, k, v, kept
+
+
+@pytest.mark.parametrize("place", ["new", "old", "mixed"])
+@pytest.mark.parametrize("d,kv,lens,keep", [
+    (64, 1, [1], 1), (128, 2, [40, 7, 0, 100], 30), (64, 3, [17, 33], 16), (128, 5, [600, 1000], 512),
+    (64, 1, [9000], 7000), (128, 1, [6000, 6500], 3001),
+])
+def test_move_brings_the_kept_tokens_to_the_front(place, d, kv, lens, keep):
+    w, tables, new, k, v, kept = _move_case(sum(lens) + keep, d, kv, lens, keep, place)
+    dw, dk, dv = _dev(w, np.float32), k.clone(), v.clone()
+    old_t, new_t = _dev(tables), _dev(new)
+    if place == "old" and tables.shape[1] >= new.shape[1]:
+        new_t = old_t  # the same memory
+    paged.evict_move(paged.PagedPool(dk, dv), old_t, new_t, _dev(kept), dw, old_t, new_t)
+    torch.cuda.synchronize()
+    for got, was in ((dk, k), (dv, v)):
+        assert np.array_equal(_f64(got), ref.move(_f64(was), tables, new, kept))
+    assert np.array_equal(dw.cpu().numpy(), ref.move(w, tables, new, kept))
+    dk2 = k.clone()  # K and V alone, the weights' tables left out
+    paged.evict_move(paged.PagedPool(dk2, v.clone()), old_t, new_t, _dev(kept))
+    assert torch.equal(dk2, dk)
+
+
+def test_move_skips_what_lies_outside():
+    w, tables, new, k, v, kept = _move_case(3, 64, 2, [80, 90], 40, "new")
+    tables[0, 1], new[0, 2], new[1, 0] = -1, k.shape[0], -3
+    tables[1, 2] = 1 << 30
+    kept[1, 0, 39] = 16 * tables.shape[1]  # beyond the table
+    dk, dv = k.clone(), v.clone()
+    paged.evict_move(paged.PagedPool(dk, dv), _dev(tables), _dev(new), _dev(kept))
+    assert np.array_equal(_f64(dk), ref.move(_f64(k), tables, new, kept))
+    assert np.array_equal(_f64(dv), ref.move(_f64(v), tables, new, kept))
+
+
+# ------------------------------------------------------------------ together
+
+def test_fork_decode_weigh_evict_and_decode_again():
+    """A prompt forked into three, decoded over the shared prefix; its weights from a window; two forks evicted, one to
+    pages of its own; then decoded again.  The page table says where everything lies."""
+    kv, group, d, prompt = 2, 2, 64, 150
+    heads = kv * group
+    rng = np.random.default_rng(21)
+    pt = cache.PageTable(64)
+    pt.extend(0, prompt)
+    k, v = _bf(rng, 64, kv, 16, d), _bf(rng, 64, kv, 16, d)
+    pool = paged.PagedPool(k, v)
+    w = torch.full((64, kv, 16), NAN, device="cuda")
+    # the prompt's last eight rows give the first weights
+    table = pt.table(0)
+    qw = _bf(rng, 8, heads, d)
+    ow = torch.empty_like(qw)
+    before = np.zeros((64, kv, 16))
+    paged.decode_weigh(pool, qw, _dev(table[None]), _dev([prompt - 1]), prompt - 1, w, _dev(table[None]), 0.0, ow)
+    o, b, want, wb = ref.weigh(_f64(qw), _f64(k), _f64(v), table[None], [prompt - 1], group, 8, before, table[None], 0.0)
+    assert (np.abs(_f64(ow) - o) <= b).all() and (np.abs(_f64(w) - want) <= wb)[wb > 0].all()
+    # three forks of it decode one token each
+    for child in (1, 2, 3):
+        pt.fork(0, child)
+        c = pt.extend(child, prompt + 1)
+        if c:
+            cache.copy_pages(k[None], [c[0]], [c[1]])
+            cache.copy_pages(v[None], [c[0]], [c[1]])
+            cache.copy_pages(w[None], [c[0]], [c[1]])
+    tables = np.stack([pt.table(s) for s in (1, 2, 3)])
+    assert (tables[0, :prompt // 16] == tables[2, :prompt // 16]).all()
+    q = _bf(rng, 3, heads, d)
+    out = torch.empty_like(q)
+    paged.decode_shared(pool, q, _dev(tables), _dev([prompt] * 3), prompt, [3], [prompt], out)
+    o, b = ref.shared(_f64(q), _f64(k), _f64(v), tables, [prompt] * 3, group)
+    assert (np.abs(_f64(out) - o) <= b).all()
+    # the first fork keeps 64 tokens in new pages, as the others still read the shared ones
+    pt.extend(9, 64)
+    new = pt.table(9)
+    kept = torch.empty(1, kv, 64, dtype=torch.int32, device="cuda")
+    paged.evict_select(w, _dev(tables[:1]), _dev([prompt]), prompt, 64, 4, 16, kept)
+    assert np.array_equal(kept.cpu().numpy(), ref.select(w.cpu().numpy(), tables[:1], [prompt], 64, 4, 16))
+    was = [_f64(x) for x in (k, v)]
+    paged.evict_move(pool, _dev(tables[:1]), _dev(new[None]), kept, w, _dev(tables[:1]), _dev(new[None]))
+    for x, y in zip((k, v), was):
+        assert np.array_equal(_f64(x), ref.move(y, tables[:1], new[None], kept.cpu().numpy()))
+    pt.release(1)
+    # and decodes on over them, its weights with it
+    pt.extend(9, 65)
+    t9 = pt.table(9)[None]
+    q = _bf(rng, 1, heads, d)
+    out = torch.empty_like(q)
+    old = _f64(w)
+    paged.decode_weigh(pool, q, _dev(t9), _dev([64]), 64, w, _dev(t9), 1.0, out)
+    o, b, want, wb = ref.weigh(_f64(q), _f64(k), _f64(v), t9, [64], group, 1, old, t9, 1.0)
+    assert (np.abs(_f64(out) - o) <= b).all() and (np.abs(_f64(w) - want) <= wb)[wb > 0].all()
+
+
+def test_captured_calls_replay_with_new_contents():
+    c = Case(31, 2, 2, 64, [3, 1], [100, 20], [130, 110, 120, 60], poison=False)
+    tables, ctx = _dev(np.where(c.tables < 0, 0, c.tables)), _dev(c.ctx)
+    keep = 32
+    kept = torch.zeros(4, 2, keep, dtype=torch.int32, device="cuda")
+    out, out2 = torch.zeros_like(c.q), torch.zeros_like(c.q)
+    ws = torch.empty(16 << 20, dtype=torch.uint8, device="cuda")
+    wt = torch.arange(4 * tables.shape[1], device="cuda", dtype=torch.int32).view(4, -1)
+    w = torch.zeros(wt.numel(), 2, 16, device="cuda")
+
+    def step():
+        paged.decode_shared(c.pool, c.q, tables, ctx, 130, c.rows, c.prefix, out, ws)
+        paged.decode_weigh(c.pool, c.q, tables, ctx, 130, w, wt, 0.0, out2, ws)
+        paged.evict_select(w, wt, ctx, 130, keep, 2, 4, kept)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rng = np.random.default_rng(1)
+    for _ in range(2):
+        c.q.copy_(_bf(rng, *c.q.shape))
+        ctx.copy_(_dev(c.ctx - rng.integers(0, 10, 4)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), out2.clone(), kept.clone()
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, out2, kept)))
+
+
+def test_a_stream_of_its_own_wants_a_workspace_of_its_own():
+    c = Case(32, 1, 1, 64, [2], [40], [3000, 2000], poison=False)
+    want = c.run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(c.q)
+    args = (c.pool, c.q, _dev(c.tables), _dev(c.ctx), 3000, c.rows, c.prefix, out)
+    with pytest.raises(ValueError):
+        paged.decode_shared(*args, None, s)
+    need = paged.decode_shared_workspace(2, 1, 1, 64, 3000, c.rows, c.prefix)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    paged.decode_shared(*args, ws, s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    with pytest.raises(HbError):
+        paged.decode_shared(*args, ws[:need - 16])
