@@ -2,17 +2,22 @@
 // choice of the tokens that stay, and their move (include/hb_paged.h).
 #include <cuda_runtime.h>
 
+#include <atomic>
+
+#include "kv4_host.h"
 #include "paged.h"
+#include "tc_ptx.cuh"
 
 namespace hb {
 namespace {
 
 using namespace paged;
 
-constexpr int SEL_THREADS = 1024;
-constexpr int SEL_KEYS = 4;  // neighbouring tokens of a thread
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_DEPTH = 8;  // pieces that a thread has under way, twice
+constexpr int MOVE_STAGES = 4;
+constexpr int CLUSTER = 8;  // CTAs of a long sequence's kv head
+
+// ------------------------------------------------------------------- choice
 
 // Order-preserving integers: a NaN is 0, below the lowest number's; both zeros
 // are equal; a token that stays in any case is above all.
@@ -35,123 +40,219 @@ struct Select {
     const int *lens;
     int max_len, keep, first, recent;
     int *kept;
+    int room;  // tokens of a CTA whose ranks fit its shared memory
 };
 
-// The ranks of tokens at .. at + 3 (at a multiple of 4) of a sequence of len.
-__device__ __forceinline__ void ranks(const Select &p, const int *tab, int kvh, int at, int len, uint32_t (&r)[SEL_KEYS])
+// Weights of tokens at .. at + 3 (at a multiple of 4), through their block.
+__device__ __forceinline__ float4 weights_at(const Select &p, int blk, int kvh, int at)
 {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool ok = false;
-    if (at < len) {
-        const int blk = __ldg(tab + (at >> 4));
-        ok = blk >= 0 && blk < p.num_blocks;
-        if (ok)
-            v = *reinterpret_cast<const float4 *>(p.w + ((size_t)blk * p.n_kv + kvh) * 16 + (at & 15));
-    }
-    const float x[SEL_KEYS] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < SEL_KEYS; ++j)
-        r[j] = at + j < p.first || at + j >= len - p.recent ? STAYS : ok ? rank_of(x[j]) : 0u;
+    if (blk < 0 || blk >= p.num_blocks)
+        return make_float4(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000), __int_as_float(0x7fc00000),
+                           __int_as_float(0x7fc00000));
+    return *reinterpret_cast<const float4 *>(p.w + ((size_t)blk * p.n_kv + kvh) * 16 + (at & 15));
 }
 
-// One CTA: a sequence's kv head.  The keep-th largest rank by its bytes from the
-// top, a histogram each; then the tokens above it, and the first of those that
-// equal it, in order.
-__global__ void __launch_bounds__(SEL_THREADS) k_evict_select(const Select p)
+// Their ranks in a sequence of len tokens.
+__device__ __forceinline__ uint4 ranks(const Select &p, const float4 &v, int at, int len)
 {
-    __shared__ int hist[256];
-    __shared__ int s_byte, s_left;
-    __shared__ int s_warp[32], s_total;
-    const int kvh = blockIdx.x, seq = blockIdx.y;
+    const int late = len - p.recent;
+    uint4 r;
+    r.x = at < p.first || at >= late ? STAYS : rank_of(v.x);
+    r.y = at + 1 < p.first || at + 1 >= late ? STAYS : rank_of(v.y);
+    r.z = at + 2 < p.first || at + 2 >= late ? STAYS : rank_of(v.z);
+    r.w = at + 3 < p.first || at + 3 >= late ? STAYS : rank_of(v.w);
+    return r;
+}
+
+__device__ __forceinline__ int remote(const int *at, uint32_t cta)
+{
+    int v;
+    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %1, %2;\nld.shared::cluster.s32 %0, [a];\n}\n"
+                 : "=r"(v)
+                 : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(cta)
+                 : "memory");
+    return v;
+}
+
+// Sum over the lanes before this one and itself.
+__device__ __forceinline__ int scan_warp(int v, int lane)
+{
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, x);
+        if (lane >= x)
+            v += y;
+    }
+    return v;
+}
+
+// A CTA, or a cluster of them with a piece of the tokens each: one sequence's
+// kv head.  The keep-th largest rank by its digits of BITS bits from the top, a
+// histogram each (added up over the cluster in its shared memory); then the
+// tokens above it, and the first of those that equal it, in order.
+template <int THREADS, int BITS, int CTAS>
+__global__ void __launch_bounds__(THREADS) k_evict_select(const Select p)
+{
+    constexpr int PASSES = (32 + BITS - 1) / BITS, BINS = 1 << BITS, EACH = BINS / THREADS, WARPS = THREADS / 32;
+    static_assert(EACH * THREADS == BINS);
+    extern __shared__ __align__(16) uint32_t cache[];
+    __shared__ int hist[PASSES][BINS];
+    __shared__ int s_digit, s_left, s_count[2];
+    __shared__ int s_warp[WARPS], s_total;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = blockIdx.x % CTAS, kvh = blockIdx.x / CTAS, seq = blockIdx.y;
+    for (int i = threadIdx.x; i < PASSES * BINS; i += THREADS)
+        hist[0][i] = 0;
+    if (threadIdx.x < 2)
+        s_count[threadIdx.x] = 0;
     pdl_wait();
     pdl_trigger();
     int len = p.lens[seq];
     if (len < 0 || len > p.max_len)
         len = 0;
     int *kept = p.kept + ((size_t)seq * p.n_kv + kvh) * p.keep;
-    if (len <= p.keep) {
-        for (int i = threadIdx.x; i < p.keep; i += SEL_THREADS)
+    if (len <= p.keep) {  // the same for the whole cluster
+        for (int i = part * THREADS + threadIdx.x; i < p.keep; i += CTAS * THREADS)
             kept[i] = i < len ? i : -1;
         return;
     }
     const int *tab = p.tables + (size_t)seq * p.stride;
+    const int piece = ((len + CTAS - 1) / CTAS + 15) & ~15;
+    const int t0 = min(len, part * piece), t1 = min(len, t0 + piece);
+    const bool cached = piece <= p.room;
+    auto fetch = [&](int at) {
+        return cached ? *reinterpret_cast<const uint4 *>(cache + (at - t0))
+                      : ranks(p, weights_at(p, __ldg(tab + (at >> 4)), kvh, at), at, len);
+    };
+    __syncthreads();  // the histograms are empty
     uint32_t prefix = 0, mask = 0;
     int left = p.keep;  // to be taken of the ranks that have the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (threadIdx.x < 256)
-            hist[threadIdx.x] = 0;
-        __syncthreads();
-        for (int at = threadIdx.x * SEL_KEYS; at < len; at += SEL_THREADS * SEL_KEYS) {
-            uint32_t r[SEL_KEYS];
-            ranks(p, tab, kvh, at, len, r);
+#pragma unroll 1
+    for (int pass = 0; pass < PASSES; ++pass) {
+        const int shift = max(0, 32 - BITS * (pass + 1));
+        const uint32_t bins = pass == PASSES - 1 ? (1u << (32 - BITS * (PASSES - 1))) - 1 : BINS - 1;
+        int *h = hist[pass];
+        auto count = [&](const uint4 &r, int at) {
+            if ((r.x & mask) == prefix)
+                atomicAdd(&h[(r.x >> shift) & bins], 1);
+            if (at + 1 < t1 && (r.y & mask) == prefix)
+                atomicAdd(&h[(r.y >> shift) & bins], 1);
+            if (at + 2 < t1 && (r.z & mask) == prefix)
+                atomicAdd(&h[(r.z >> shift) & bins], 1);
+            if (at + 3 < t1 && (r.w & mask) == prefix)
+                atomicAdd(&h[(r.w >> shift) & bins], 1);
+        };
+        if (pass == 0) {  // four rounds' loads at a time
+            for (int base = t0 + threadIdx.x * 4; base < t1; base += THREADS * 16) {
+                int blk[4];
+                float4 v[4];
 #pragma unroll
-            for (int j = 0; j < SEL_KEYS; ++j)
-                if (at + j < len && (r[j] & mask) == prefix)
-                    atomicAdd(&hist[(r[j] >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {  // the byte in whose bin the left-th largest lies
-            int mine[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                mine[j] = hist[255 - lane * 8 - j];
-                sum += mine[j];
-            }
-            int upto = sum;
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, x);
-                if (lane >= x)
-                    upto += y;
-            }
-            int before = upto - sum;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (before < left && before + mine[j] >= left) {
-                    s_byte = 255 - lane * 8 - j;
-                    s_left = left - before;
+                for (int u = 0; u < 4; ++u) {
+                    const int at = base + u * THREADS * 4;
+                    blk[u] = at < t1 ? __ldg(tab + (at >> 4)) : -1;
                 }
-                before += mine[j];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    v[u] = weights_at(p, blk[u], kvh, base + u * THREADS * 4);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int at = base + u * THREADS * 4;
+                    if (at < t1) {
+                        const uint4 r = ranks(p, v[u], at, len);
+                        if (cached)
+                            *reinterpret_cast<uint4 *>(cache + (at - t0)) = r;
+                        count(r, at);
+                    }
+                }
             }
+        } else {
+            for (int at = t0 + threadIdx.x * 4; at < t1; at += THREADS * 4)
+                count(fetch(at), at);
+        }
+        if constexpr (CTAS > 1)
+            tc::cluster_sync();
+        else
+            __syncthreads();
+        // the digit in whose bin the left-th largest lies; bins from the top
+        int mine[EACH], sum = 0;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+            const int b = BINS - 1 - ((int)threadIdx.x * EACH + j);
+            if constexpr (CTAS > 1) {
+                mine[j] = 0;
+#pragma unroll
+                for (int c = 0; c < CTAS; ++c)
+                    mine[j] += remote(&h[b], c);
+            } else {
+                mine[j] = h[b];
+            }
+            sum += mine[j];
+        }
+        int upto = scan_warp(sum, lane);
+        if (lane == 31)
+            s_warp[warp] = upto;
+        __syncthreads();
+        int before = upto - sum;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            before += w < warp ? s_warp[w] : 0;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+            if (before < left && before + mine[j] >= left) {
+                s_digit = BINS - 1 - ((int)threadIdx.x * EACH + j);
+                s_left = left - before;
+            }
+            before += mine[j];
         }
         __syncthreads();
-        prefix |= (uint32_t)s_byte << shift;
-        mask |= 0xffu << shift;
+        prefix |= (uint32_t)s_digit << shift;
+        mask |= bins << shift;
         left = s_left;
-        __syncthreads();
     }
     // all above prefix, and the first `left` that equal it
-    int done = 0, equal = 0;  // taken, and equals met, before this round
-    for (int base = 0; base < len; base += SEL_THREADS * SEL_KEYS) {
-        const int at = base + threadIdx.x * SEL_KEYS;
-        uint32_t r[SEL_KEYS];
-        ranks(p, tab, kvh, at, len, r);
+    int done = 0, equal = 0;      // taken, and equals met, before this round
+    if constexpr (CTAS > 1) {  // in the pieces before this one
+        int above = 0, same = 0;
+        for (int at = t0 + threadIdx.x * 4; at < t1; at += THREADS * 4) {
+            const uint4 r = fetch(at);
+            above += (r.x > prefix) + (at + 1 < t1 && r.y > prefix) + (at + 2 < t1 && r.z > prefix) +
+                     (at + 3 < t1 && r.w > prefix);
+            same += (r.x == prefix) + (at + 1 < t1 && r.y == prefix) + (at + 2 < t1 && r.z == prefix) +
+                    (at + 3 < t1 && r.w == prefix);
+        }
+        above = __reduce_add_sync(0xffffffffu, above);
+        same = __reduce_add_sync(0xffffffffu, same);
+        if (lane == 0) {
+            atomicAdd(&s_count[0], above);
+            atomicAdd(&s_count[1], same);
+        }
+        tc::cluster_sync();
+        for (int c = 0; c < part; ++c) {
+            done += remote(&s_count[0], c);
+            equal += remote(&s_count[1], c);
+        }
+        done += min(equal, left);
+    }
+    for (int base = t0; base < t1; base += THREADS * 4) {
+        const int at = base + threadIdx.x * 4;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (at < t1)
+            v = fetch(at);
+        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
         int count = 0;  // above in the low half, equal in the high
 #pragma unroll
-        for (int j = 0; j < SEL_KEYS; ++j)
-            if (at + j < len)
+        for (int j = 0; j < 4; ++j)
+            if (at + j < t1)
                 count += r[j] > prefix ? 1 : r[j] == prefix ? 1 << 16 : 0;
-        int upto = count;
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, x);
-            if (lane >= x)
-                upto += y;
-        }
+        const int upto = scan_warp(count, lane);
+        __syncthreads();  // s_warp of the round before is read
         if (lane == 31)
             s_warp[warp] = upto;
         __syncthreads();
         if (warp == 0) {
-            const int v = s_warp[lane];
-            int u = v;
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, u, x);
-                if (lane >= x)
-                    u += y;
-            }
-            s_warp[lane] = u - v;
+            const int x = lane < WARPS ? s_warp[lane] : 0, u = scan_warp(x, lane);
+            if (lane < WARPS)
+                s_warp[lane] = u - x;
             if (lane == 31)
                 s_total = u;
         }
@@ -160,19 +261,21 @@ __global__ void __launch_bounds__(SEL_THREADS) k_evict_select(const Select p)
         int above = before & 0xffff, same = equal + (before >> 16);
         const int met = min(equal, left);  // equals taken before this round
 #pragma unroll
-        for (int j = 0; j < SEL_KEYS; ++j)
-            if (at + j < len) {
-                const bool take = r[j] > prefix || (r[j] == prefix && same < left);
-                if (take)
+        for (int j = 0; j < 4; ++j)
+            if (at + j < t1) {
+                if (r[j] > prefix || (r[j] == prefix && same < left))
                     kept[done + above + (min(same, left) - met)] = at + j;
                 above += r[j] > prefix;
                 same += r[j] == prefix;
             }
         done += (total & 0xffff) + (min(equal + (total >> 16), left) - met);
         equal += total >> 16;
-        __syncthreads();
     }
+    if constexpr (CTAS > 1)
+        tc::cluster_sync();  // no CTA's shared memory goes while another reads it
 }
+
+// --------------------------------------------------------------------- move
 
 struct Move {
     uint8_t *pool[2];
@@ -180,78 +283,204 @@ struct Move {
     const int *from, *to;
     int from_stride, to_stride;
     const int *kept;
-    int keep, slices;
+    int keep;
     float *w;             // null: none
     int w_blocks;
     const int *w_from, *w_to;
     int w_from_stride, w_to_stride;
 };
 
-// Pieces of T of the tokens of one kv head, PER of them of each token (piece
-// first.. of a row of `row` bytes): token i from slot kept[i].  A CTA goes
-// through the tokens in order and stores a batch only when all its threads have
-// loaded it: kept[i] >= i, so what a batch overwrites belongs to it or to the
-// batches before, and the next one may be on its way already.
-template <typename T>
-__device__ __forceinline__ void move_rows(uint8_t *pool, int num_blocks, int n_kv, int kvh, int row, int first, int per,
-                                          const int *from, int from_stride, const int *to, int to_stride,
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Batches of tokens in shared memory: MOVE_STAGES of them, and where each token
+// goes.  16 KB of a batch where three CTAs share an SM, 32 KB where a CTA has
+// one to itself.
+template <int PIECES, int P, bool ALONE>
+struct MoveTile {
+    static constexpr int TOKENS = P == 4 ? 1024 : (ALONE ? 32768 : 16384) / (PIECES * P);
+    static constexpr int BYTES = TOKENS * PIECES * P;
+    static constexpr int SMEM = MOVE_STAGES * (BYTES + 8 * TOKENS);
+};
+
+// PIECES pieces of P bytes of each token of one kv head, from offset first of
+// its row of `row` bytes: token i from slot kept[i].  A CTA goes through the
+// tokens in order, in batches, and stores a batch only when all of it and of
+// those before it has been loaded: kept[i] >= i, so what a batch overwrites
+// belongs to it or to batches before, and later ones may be on their way
+// already.  Slots of a batch are looked up while the batches before it load.
+template <int PIECES, int P, bool ALONE>
+__device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_blocks, int n_kv, int kvh, int row,
+                                          int first, const int *from, int from_stride, const int *to, int to_stride,
                                           const int *kept, int keep)
 {
-    const int r = threadIdx.x / per, c = first + threadIdx.x % per;
-    const int rows = MOVE_THREADS / per, batch = rows * MOVE_DEPTH;
-    T v[2][MOVE_DEPTH];
-    T *dst[2][MOVE_DEPTH];
-    auto load = [&](int base, T (&x)[MOVE_DEPTH], T *(&d)[MOVE_DEPTH]) {
+    using T = MoveTile<PIECES, P, ALONE>;
+    constexpr int S = MOVE_STAGES, TOKENS = T::TOKENS, PER = TOKENS * PIECES / MOVE_THREADS;
+    constexpr int EACH = (TOKENS + MOVE_THREADS - 1) / MOVE_THREADS;  // tokens that a thread looks up
+    static_assert(PER * MOVE_THREADS == TOKENS * PIECES);
+    int *s_src = reinterpret_cast<int *>(ring + S * T::BYTES), *s_dst = s_src + S * TOKENS;  // slots; -1: not moved
+    const int n = (keep + TOKENS - 1) / TOKENS;
+    pool += (size_t)kvh * 16 * row + first;
+    const size_t page = (size_t)n_kv * 16 * row;
+    // the slots in two steps, a batch apart: a token's position, then its blocks
+    auto positions = [&](int b, int (&k)[EACH]) {
 #pragma unroll
-        for (int u = 0; u < MOVE_DEPTH; ++u) {
-            const int i = base + u * rows + r;
-            d[u] = nullptr;
-            const int src = i < keep && r < rows ? __ldg(kept + i) : -1;
-            if (src < 0 || (src >> 4) >= from_stride)
-                continue;
-            const int b0 = from[src >> 4], b1 = to[i >> 4];
-            if (b0 < 0 || b0 >= num_blocks || b1 < 0 || b1 >= num_blocks || (b0 == b1 && src == i))
-                continue;
-            const uint8_t *s = pool + (((size_t)b0 * n_kv + kvh) * 16 + (src & 15)) * row;
-            x[u] = reinterpret_cast<const T *>(s)[c];
-            d[u] = reinterpret_cast<T *>(pool + (((size_t)b1 * n_kv + kvh) * 16 + (i & 15)) * row) + c;
+        for (int u = 0; u < EACH; ++u) {
+            const int t = u * MOVE_THREADS + (int)threadIdx.x;
+            const long long i = (long long)b * TOKENS + t;
+            k[u] = t < TOKENS && i < keep ? __ldg(kept + i) : -1;
         }
     };
-    auto store = [&](const T (&x)[MOVE_DEPTH], T *const (&d)[MOVE_DEPTH]) {
+    auto blocks = [&](int b, const int (&k)[EACH], int (&b0)[EACH], int (&b1)[EACH]) {
 #pragma unroll
-        for (int u = 0; u < MOVE_DEPTH; ++u)
-            if (d[u])
-                *d[u] = x[u];
+        for (int u = 0; u < EACH; ++u) {
+            const int i = b * TOKENS + u * MOVE_THREADS + (int)threadIdx.x;
+            const bool ok = k[u] >= 0 && (k[u] >> 4) < from_stride;
+            b0[u] = ok ? __ldg(from + (k[u] >> 4)) : -1;
+            b1[u] = ok ? __ldg(to + (i >> 4)) : -1;
+        }
     };
-    load(0, v[0], dst[0]);
-    for (int base = 0; base < keep; base += 2 * batch) {
-        load(base + batch, v[1], dst[1]);
-        __syncthreads();
-        store(v[0], dst[0]);
-        load(base + 2 * batch, v[0], dst[0]);
-        __syncthreads();
-        store(v[1], dst[1]);
+    auto put = [&](int b, const int (&k)[EACH], const int (&b0)[EACH], const int (&b1)[EACH]) {
+#pragma unroll
+        for (int u = 0; u < EACH; ++u) {
+            const int t = u * MOVE_THREADS + (int)threadIdx.x, i = b * TOKENS + t;
+            const bool ok = b0[u] >= 0 && b0[u] < num_blocks && b1[u] >= 0 && b1[u] < num_blocks &&
+                            !(b0[u] == b1[u] && k[u] == i);
+            if (t < TOKENS) {
+                s_src[b % S * TOKENS + t] = ok ? b0[u] * 16 + (k[u] & 15) : -1;
+                s_dst[b % S * TOKENS + t] = ok ? b1[u] * 16 + (i & 15) : -1;
+            }
+        }
+    };
+    auto load = [&](int b) {
+        if (b < n) {
+            const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring + b % S * T::BYTES);
+#pragma unroll 8
+            for (int j = 0; j < PER; ++j) {
+                const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
+                const int src = s_src[b % S * TOKENS + e / PIECES];
+                if (src >= 0)
+                    copy_async<P>(at + e * P, pool + (src >> 4) * page + (src & 15) * row + c * P);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int k[EACH], b0[EACH], b1[EACH];
+#pragma unroll
+    for (int b = 0; b < S - 1; ++b) {
+        positions(b, k);
+        blocks(b, k, b0, b1);
+        put(b, k, b0, b1);
+    }
+    positions(S - 1, k);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < S - 2; ++b)
+        load(b);
+    for (int b = 0; b < n; ++b) {
+        int next[EACH];  // on their way while this thread waits
+        blocks(b + S - 1, k, b0, b1);
+        positions(b + S, next);
+        load(b + S - 2);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncthreads();  // batch b is here, all of it
+#pragma unroll 8
+        for (int j = 0; j < PER; ++j) {
+            const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
+            const int d = s_dst[b % S * TOKENS + e / PIECES];
+            if (d >= 0) {
+                uint8_t *o = pool + (d >> 4) * page + (d & 15) * row + c * P;
+                const uint8_t *x = ring + b % S * T::BYTES + e * P;
+                if constexpr (P == 16)
+                    *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(x);
+                else
+                    *reinterpret_cast<uint32_t *>(o) = *reinterpret_cast<const uint32_t *>(x);
+            }
+        }
+        put(b + S - 1, k, b0, b1);  // the place of batch b - 1, which is stored
+#pragma unroll
+        for (int u = 0; u < EACH; ++u)
+            k[u] = next[u];
+        __syncthreads();  // its slots are there, and batch b's place is free
     }
 }
 
-template <int D>
+template <int D, int SLICES>
 __global__ void __launch_bounds__(MOVE_THREADS) k_evict_move(const Move p)
 {
+    constexpr int PIECES = D / 8 / SLICES;
+    extern __shared__ __align__(16) uint8_t ring[];
     pdl_wait();
     pdl_trigger();
     const int seq = blockIdx.y;
-    const int each = 2 * p.slices + (p.w ? 1 : 0);
+    const int each = 2 * SLICES + (p.w ? 1 : 0);
     const int kvh = blockIdx.x / each, part = blockIdx.x % each;
     const int *kept = p.kept + ((size_t)seq * p.n_kv + kvh) * p.keep;
-    if (part < 2 * p.slices) {
-        const int per = D / 8 / p.slices;
-        move_rows<uint4>(p.pool[part & 1], p.num_blocks, p.n_kv, kvh, D * 2, (part >> 1) * per, per,
-                         p.from + (size_t)seq * p.from_stride, p.from_stride, p.to + (size_t)seq * p.to_stride,
-                         p.to_stride, kept, p.keep);
-    } else {
-        move_rows<float>((uint8_t *)p.w, p.w_blocks, p.n_kv, kvh, 4, 0, 1, p.w_from + (size_t)seq * p.w_from_stride,
-                         p.w_from_stride, p.w_to + (size_t)seq * p.w_to_stride, p.w_to_stride, kept, p.keep);
-    }
+    if (part < 2 * SLICES)
+        move_rows<PIECES, 16, (SLICES > 1)>(
+            ring, p.pool[part & 1], p.num_blocks, p.n_kv, kvh, D * 2, (part >> 1) * PIECES * 16,
+            p.from + (size_t)seq * p.from_stride, p.from_stride, p.to + (size_t)seq * p.to_stride, p.to_stride, kept,
+            p.keep);
+    else
+        move_rows<1, 4, (SLICES > 1)>(ring, (uint8_t *)p.w, p.w_blocks, p.n_kv, kvh, 4, 0,
+                                      p.w_from + (size_t)seq * p.w_from_stride, p.w_from_stride,
+                                      p.w_to + (size_t)seq * p.w_to_stride, p.w_to_stride, kept, p.keep);
+}
+
+// ------------------------------------------------------------------- host
+
+template <int D, int SLICES>
+int launch_move(const Move &p, int n_seqs, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr int smem = MoveTile<D / 8 / SLICES, 16, (SLICES > 1)>::SMEM;
+    static_assert(smem >= MoveTile<1, 4, (SLICES > 1)>::SMEM);
+    auto kernel = k_evict_move<D, SLICES>;
+    const long long gx = (long long)p.n_kv * (2 * SLICES + (p.w ? 1 : 0));
+    if (gx > 0x7fffffffll)
+        return HB_ERANGE;
+    if (kv4_allow_smem((const void *)kernel, smem, done) != cudaSuccess)
+        return HB_ECUDA;
+    return launch_kernel(true, kernel, dim3((unsigned)gx, (unsigned)n_seqs), dim3(MOVE_THREADS), smem, s, p) ==
+                   cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
+}
+
+template <int THREADS, int BITS, int CTAS>
+int launch_select(Select p, int n_seqs, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    constexpr int MOST = 192 * 1024;  // bytes of ranks
+    auto kernel = k_evict_select<THREADS, BITS, CTAS>;
+    const long long piece = (((long long)p.max_len + CTAS - 1) / CTAS + 15) & ~15ll;
+    const int smem = piece * 4 <= MOST ? (int)piece * 4 : 0;
+    p.room = smem / 4;
+    const long long gx = (long long)p.n_kv * CTAS;
+    if (gx > 0x7fffffffll)
+        return HB_ERANGE;
+    if (kv4_allow_smem((const void *)kernel, MOST, done) != cudaSuccess ||
+        max_carveout((const void *)kernel) != cudaSuccess)
+        return HB_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)gx, (unsigned)n_seqs);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {CTAS, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? HB_OK : HB_ECUDA;
 }
 
 }  // namespace
@@ -276,11 +505,13 @@ try {
     if (max_len > MAX_KEYS || keep > MAX_KEYS || wt_stride < (max_len + 15) / 16 || n_seqs > 65535)
         return HB_ERANGE;
     const Select p = {weights->data, weights->num_blocks, weights->n_kv_heads, weight_tables, wt_stride, lens,
-                      max_len,       keep,                n_first,             n_recent,      kept};
-    return launch_kernel(true, k_evict_select, dim3((unsigned)weights->n_kv_heads, (unsigned)n_seqs),
-                         dim3(SEL_THREADS), 0, (cudaStream_t)cuda_stream, p) == cudaSuccess
-               ? HB_OK
-               : HB_ECUDA;
+                      max_len,       keep,                n_first,             n_recent,      kept,      0};
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    if (max_len <= 4096)
+        return launch_select<256, 8, 1>(p, n_seqs, s);
+    const long long items = (long long)n_seqs * weights->n_kv_heads;
+    return items >= 152 && max_len <= 49152 ? launch_select<1024, 11, 1>(p, n_seqs, s)
+                                            : launch_select<1024, 11, CLUSTER>(p, n_seqs, s);
 } catch (...) {
     return HB_ENOMEM;
 }
@@ -317,7 +548,6 @@ try {
     p.to_stride = new_stride;
     p.kept = kept;
     p.keep = keep;
-    p.slices = 1;
     if (weights) {
         p.w = weights->data;
         p.w_blocks = weights->num_blocks;
@@ -326,14 +556,17 @@ try {
         p.w_to = new_weight_tables;
         p.w_to_stride = new_wt_stride;
     }
-    const long long gx = (long long)p.n_kv * (2 * p.slices + (weights ? 1 : 0));
-    if (gx > 0x7fffffffll)
-        return HB_ERANGE;
-    return launch_kernel(true, pool->head_dim == 128 ? k_evict_move<128> : k_evict_move<64>,
-                         dim3((unsigned)gx, (unsigned)n_seqs), dim3(MOVE_THREADS), 0, (cudaStream_t)cuda_stream,
-                         p) == cudaSuccess
-               ? HB_OK
-               : HB_ECUDA;
+    cudaStream_t s = (cudaStream_t)cuda_stream;
+    const long long items = (long long)n_seqs * p.n_kv;
+    const int slices = items * 2 >= 304 ? 1 : items * 4 >= 304 ? 2 : items * 8 >= 304 ? 4 : 8;
+    if (pool->head_dim == 128)
+        return slices == 1   ? launch_move<128, 1>(p, n_seqs, s)
+               : slices == 2 ? launch_move<128, 2>(p, n_seqs, s)
+               : slices == 4 ? launch_move<128, 4>(p, n_seqs, s)
+                             : launch_move<128, 8>(p, n_seqs, s);
+    return slices == 1   ? launch_move<64, 1>(p, n_seqs, s)
+           : slices == 2 ? launch_move<64, 2>(p, n_seqs, s)
+                         : launch_move<64, 4>(p, n_seqs, s);
 } catch (...) {
     return HB_ENOMEM;
 }

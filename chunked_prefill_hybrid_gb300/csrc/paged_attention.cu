@@ -755,14 +755,17 @@ namespace paged {
 int check_pool(const hb_paged_pool *p)
 {
     if (!p || !p->k || !p->v || (uintptr_t)p->k % 16 || (uintptr_t)p->v % 16 || p->num_blocks < 1 ||
-        p->n_kv_heads < 1 || (p->head_dim != 64 && p->head_dim != 128))
+        p->num_blocks >= MAX_KEYS || p->n_kv_heads < 1 || (p->head_dim != 64 && p->head_dim != 128))
         return HB_EINVAL;
     return HB_OK;
 }
 
 int check_weight_pool(const hb_weight_pool *p)
 {
-    return !p || !p->data || (uintptr_t)p->data % 16 || p->num_blocks < 1 || p->n_kv_heads < 1 ? HB_EINVAL : HB_OK;
+    return !p || !p->data || (uintptr_t)p->data % 16 || p->num_blocks < 1 || p->num_blocks >= MAX_KEYS ||
+                   p->n_kv_heads < 1
+               ? HB_EINVAL
+               : HB_OK;
 }
 
 }  // namespace paged

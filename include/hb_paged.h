@@ -42,7 +42,7 @@ extern "C" {
 #endif
 
 /* K (post-RoPE) and V pools: device bf16 [num_blocks][n_kv_heads][16]
- * [head_dim], 16-byte aligned, head_dim 64 or 128. */
+ * [head_dim], 16-byte aligned, head_dim 64 or 128, fewer than 2^27 blocks. */
 typedef struct {
     void *k, *v;
     int num_blocks, n_kv_heads, head_dim;
@@ -50,7 +50,7 @@ typedef struct {
 
 /* A pool of one fp32 number for each token and kv head: device fp32
  * [num_blocks][n_kv_heads][16], 16-byte aligned, found through block tables
- * of its own (which may be the cache's). */
+ * of its own (which may be the cache's); fewer than 2^27 blocks. */
 typedef struct {
     float *data;
     int num_blocks, n_kv_heads;

@@ -69,7 +69,8 @@ def _move(L, pool=None, w=None, **over):
 
 
 @pytest.mark.parametrize("over", [dict(k=None), dict(v=None), dict(k=8), dict(v=24), dict(num_blocks=0),
-                                  dict(n_kv_heads=0), dict(head_dim=80), dict(num_blocks=-1)])
+                                  dict(n_kv_heads=0), dict(head_dim=80), dict(num_blocks=-1),
+                                  dict(num_blocks=1 << 27)])
 def test_bad_pool_is_refused_by_every_call(L, over):
     assert _shared(L, _pool(**over)) == HB_EINVAL
     assert _shared(L, _pool(**over), n=0, rows=[], pre=[]) == HB_EINVAL
@@ -77,7 +78,8 @@ def test_bad_pool_is_refused_by_every_call(L, over):
     assert _move(L, _pool(**over)) == HB_EINVAL
 
 
-@pytest.mark.parametrize("over", [dict(data=None), dict(data=8), dict(num_blocks=0), dict(n_kv_heads=0)])
+@pytest.mark.parametrize("over", [dict(data=None), dict(data=8), dict(num_blocks=0), dict(n_kv_heads=0),
+                                  dict(num_blocks=1 << 27)])
 def test_bad_weights_are_refused_by_every_call(L, over):
     assert _weigh(L, w=_weights(**over)) == HB_EINVAL
     assert _select(L, w=_weights(**over)) == HB_EINVAL
