@@ -14,7 +14,6 @@ namespace {
 using namespace paged;
 
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_STAGES = 4;
 constexpr int CLUSTER = 8;  // CTAs of a long sequence's kv head
 
 // ------------------------------------------------------------------- choice
@@ -64,6 +63,7 @@ __device__ __forceinline__ uint4 ranks(const Select &p, const float4 &v, int at,
     return r;
 }
 
+// A number in the shared memory of another CTA of the cluster.
 __device__ __forceinline__ int remote(const int *at, uint32_t cta)
 {
     int v;
@@ -72,6 +72,14 @@ __device__ __forceinline__ int remote(const int *at, uint32_t cta)
                  : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(cta)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ void set_remote(const int *at, uint32_t cta, int v)
+{
+    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\nst.shared::cluster.s32 [a], %2;\n}\n" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(at)),
+                 "r"(cta), "r"(v)
+                 : "memory");
 }
 
 // Sum over the lanes before this one and itself.
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(const Select p)
     constexpr int PASSES = (32 + BITS - 1) / BITS, BINS = 1 << BITS, EACH = BINS / THREADS, WARPS = THREADS / 32;
     static_assert(EACH * THREADS == BINS);
     extern __shared__ __align__(16) uint32_t cache[];
-    __shared__ int hist[PASSES][BINS];
+    __shared__ int hist[PASSES][BINS], totals[CTAS > 1 ? BINS : 1];
     __shared__ int s_digit, s_left, s_count[2];
     __shared__ int s_warp[WARPS], s_total;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -169,23 +177,28 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(const Select p)
             for (int at = t0 + threadIdx.x * 4; at < t1; at += THREADS * 4)
                 count(fetch(at), at);
         }
-        if constexpr (CTAS > 1)
+        if constexpr (CTAS > 1) {  // each CTA adds up its share of the bins for all of them
             tc::cluster_sync();
-        else
+            for (int i = threadIdx.x; i < BINS / CTAS; i += THREADS) {
+                const int b = part * (BINS / CTAS) + i;
+                int sum = 0;
+#pragma unroll
+                for (int c = 0; c < CTAS; ++c)
+                    sum += remote(&h[b], c);
+#pragma unroll
+                for (int c = 0; c < CTAS; ++c)
+                    set_remote(&totals[b], c, sum);
+            }
+            tc::cluster_sync();
+            h = totals;
+        } else {
             __syncthreads();
+        }
         // the digit in whose bin the left-th largest lies; bins from the top
         int mine[EACH], sum = 0;
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
-            const int b = BINS - 1 - ((int)threadIdx.x * EACH + j);
-            if constexpr (CTAS > 1) {
-                mine[j] = 0;
-#pragma unroll
-                for (int c = 0; c < CTAS; ++c)
-                    mine[j] += remote(&h[b], c);
-            } else {
-                mine[j] = h[b];
-            }
+            mine[j] = h[BINS - 1 - ((int)threadIdx.x * EACH + j)];
             sum += mine[j];
         }
         int upto = scan_warp(sum, lane);
@@ -299,57 +312,61 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Batches of tokens in shared memory: MOVE_STAGES of them, and where each token
-// goes.  16 KB of a batch where three CTAs share an SM, 32 KB where a CTA has
-// one to itself.
-template <int PIECES, int P, bool ALONE>
+// Batches of tokens in shared memory, and where each token goes.  Three CTAs of
+// four stages share an SM; in a cluster, of which there are few, a CTA has six.
+template <int PIECES, int P, int CTAS>
 struct MoveTile {
-    static constexpr int TOKENS = P == 4 ? 1024 : (ALONE ? 32768 : 16384) / (PIECES * P);
+    static constexpr int STAGES = CTAS > 1 ? 6 : 4;
+    static constexpr int TOKENS = P == 4 ? 1024 : 16384 / (PIECES * P);
     static constexpr int BYTES = TOKENS * PIECES * P;
-    static constexpr int SMEM = MOVE_STAGES * (BYTES + 8 * TOKENS);
+    static constexpr int SMEM = STAGES * (BYTES + 8 * TOKENS);
 };
 
-// PIECES pieces of P bytes of each token of one kv head, from offset first of
-// its row of `row` bytes: token i from slot kept[i].  A CTA goes through the
-// tokens in order, in batches, and stores a batch only when all of it and of
-// those before it has been loaded: kept[i] >= i, so what a batch overwrites
-// belongs to it or to batches before, and later ones may be on their way
-// already.  Slots of a batch are looked up while the batches before it load.
-template <int PIECES, int P, bool ALONE>
-__device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_blocks, int n_kv, int kvh, int row,
-                                          int first, const int *from, int from_stride, const int *to, int to_stride,
+// Rows of PIECES pieces of P bytes, one a token of one kv head: token i from
+// slot kept[i].  A cluster of CTAS CTAs goes through the tokens in order, a
+// batch for each of them at a time, and stores those only when all of them and
+// those before have been loaded: kept[i] >= i, so what they overwrite belongs to
+// them or to batches before, and later ones may be on their way already.  In a
+// cluster a batch is stored one round after its barrier began.  Slots of a batch
+// are looked up while the batches before it load.
+template <int PIECES, int P, int CTAS>
+__device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_blocks, int n_kv, int kvh, int rank,
+                                          const int *from, int from_stride, const int *to, int to_stride,
                                           const int *kept, int keep)
 {
-    using T = MoveTile<PIECES, P, ALONE>;
-    constexpr int S = MOVE_STAGES, TOKENS = T::TOKENS, PER = TOKENS * PIECES / MOVE_THREADS;
+    using T = MoveTile<PIECES, P, CTAS>;
+    constexpr int S = T::STAGES, TOKENS = T::TOKENS, PER = TOKENS * PIECES / MOVE_THREADS, ROW = PIECES * P;
     constexpr int EACH = (TOKENS + MOVE_THREADS - 1) / MOVE_THREADS;  // tokens that a thread looks up
+    constexpr int LAG = CTAS > 1 ? 1 : 0, AHEAD = S - 2 - LAG;  // batches loading beside the one waited for
     static_assert(PER * MOVE_THREADS == TOKENS * PIECES);
     int *s_src = reinterpret_cast<int *>(ring + S * T::BYTES), *s_dst = s_src + S * TOKENS;  // slots; -1: not moved
-    const int n = (keep + TOKENS - 1) / TOKENS;
-    pool += (size_t)kvh * 16 * row + first;
-    const size_t page = (size_t)n_kv * 16 * row;
+    const int n = (keep + TOKENS * CTAS - 1) / (TOKENS * CTAS);
+    pool += (size_t)kvh * 16 * ROW;
+    const size_t page = (size_t)n_kv * 16 * ROW;
+    // token of thread's look-up u in this CTA's batch b
+    auto token = [&](int b, int u) {
+        return ((long long)b * CTAS + rank) * TOKENS + u * MOVE_THREADS + (int)threadIdx.x;
+    };
     // the slots in two steps, a batch apart: a token's position, then its blocks
     auto positions = [&](int b, int (&k)[EACH]) {
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
-            const int t = u * MOVE_THREADS + (int)threadIdx.x;
-            const long long i = (long long)b * TOKENS + t;
-            k[u] = t < TOKENS && i < keep ? __ldg(kept + i) : -1;
+            const long long i = token(b, u);
+            k[u] = u * MOVE_THREADS + (int)threadIdx.x < TOKENS && i < keep ? __ldg(kept + i) : -1;
         }
     };
     auto blocks = [&](int b, const int (&k)[EACH], int (&b0)[EACH], int (&b1)[EACH]) {
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
-            const int i = b * TOKENS + u * MOVE_THREADS + (int)threadIdx.x;
             const bool ok = k[u] >= 0 && (k[u] >> 4) < from_stride;
             b0[u] = ok ? __ldg(from + (k[u] >> 4)) : -1;
-            b1[u] = ok ? __ldg(to + (i >> 4)) : -1;
+            b1[u] = ok ? __ldg(to + (token(b, u) >> 4)) : -1;
         }
     };
     auto put = [&](int b, const int (&k)[EACH], const int (&b0)[EACH], const int (&b1)[EACH]) {
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
-            const int t = u * MOVE_THREADS + (int)threadIdx.x, i = b * TOKENS + t;
+            const int t = u * MOVE_THREADS + (int)threadIdx.x, i = (int)token(b, u);
             const bool ok = b0[u] >= 0 && b0[u] < num_blocks && b1[u] >= 0 && b1[u] < num_blocks &&
                             !(b0[u] == b1[u] && k[u] == i);
             if (t < TOKENS) {
@@ -361,41 +378,23 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
     auto load = [&](int b) {
         if (b < n) {
             const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring + b % S * T::BYTES);
-#pragma unroll 8
+#pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
                 const int src = s_src[b % S * TOKENS + e / PIECES];
                 if (src >= 0)
-                    copy_async<P>(at + e * P, pool + (src >> 4) * page + (src & 15) * row + c * P);
+                    copy_async<P>(at + e * P, pool + (src >> 4) * page + (src & 15) * ROW + c * P);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int k[EACH], b0[EACH], b1[EACH];
+    auto store = [&](int b) {
 #pragma unroll
-    for (int b = 0; b < S - 1; ++b) {
-        positions(b, k);
-        blocks(b, k, b0, b1);
-        put(b, k, b0, b1);
-    }
-    positions(S - 1, k);
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < S - 2; ++b)
-        load(b);
-    for (int b = 0; b < n; ++b) {
-        int next[EACH];  // on their way while this thread waits
-        blocks(b + S - 1, k, b0, b1);
-        positions(b + S, next);
-        load(b + S - 2);
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        __syncthreads();  // batch b is here, all of it
-#pragma unroll 8
         for (int j = 0; j < PER; ++j) {
             const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
             const int d = s_dst[b % S * TOKENS + e / PIECES];
             if (d >= 0) {
-                uint8_t *o = pool + (d >> 4) * page + (d & 15) * row + c * P;
+                uint8_t *o = pool + (d >> 4) * page + (d & 15) * ROW + c * P;
                 const uint8_t *x = ring + b % S * T::BYTES + e * P;
                 if constexpr (P == 16)
                     *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(x);
@@ -403,54 +402,113 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
                     *reinterpret_cast<uint32_t *>(o) = *reinterpret_cast<const uint32_t *>(x);
             }
         }
-        put(b + S - 1, k, b0, b1);  // the place of batch b - 1, which is stored
+    };
+    // of the batch to be put next: positions and blocks; of the one after: positions
+    int k[EACH], b0[EACH], b1[EACH], k2[EACH];
+    {
+        int ks[AHEAD + 1][EACH];
+#pragma unroll
+        for (int b = 0; b <= AHEAD; ++b)
+            positions(b, ks[b]);
+        positions(AHEAD + 1, k);
+        positions(AHEAD + 2, k2);
+#pragma unroll
+        for (int b = 0; b <= AHEAD; ++b) {
+            blocks(b, ks[b], b0, b1);
+            put(b, ks[b], b0, b1);
+        }
+        blocks(AHEAD + 1, k, b0, b1);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < AHEAD; ++b)
+        load(b);
+    for (int b = 0; b < n; ++b) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+        if constexpr (CTAS > 1) {
+            if (b > 0)  // every CTA has batch b - 1
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            // relaxed: this CTA's loads of batch b have returned, and that is all that
+            // the others wait for; a release would wait for its stores (1 us a round)
+            asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        } else {
+            __syncthreads();  // batch b is here, all of it
+        }
+        load(b + AHEAD);
+        put(b + AHEAD + 1, k, b0, b1);  // the place of a batch that was stored a round ago
 #pragma unroll
         for (int u = 0; u < EACH; ++u)
-            k[u] = next[u];
-        __syncthreads();  // its slots are there, and batch b's place is free
+            k[u] = k2[u];
+        blocks(b + AHEAD + 2, k, b0, b1);  // a round's time to come
+        positions(b + AHEAD + 3, k2);
+        if (b >= LAG)
+            store(b - LAG);
+        __syncthreads();  // the slots put are there, and the place of the batch just stored is free
+    }
+    if constexpr (CTAS > 1) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        store(n - 1);
     }
 }
 
-template <int D, int SLICES>
+template <int D, int CTAS>
 __global__ void __launch_bounds__(MOVE_THREADS) k_evict_move(const Move p)
 {
-    constexpr int PIECES = D / 8 / SLICES;
     extern __shared__ __align__(16) uint8_t ring[];
     pdl_wait();
     pdl_trigger();
     const int seq = blockIdx.y;
-    const int each = 2 * SLICES + (p.w ? 1 : 0);
-    const int kvh = blockIdx.x / each, part = blockIdx.x % each;
+    const int rank = blockIdx.x % CTAS, parts = p.w ? 3 : 2;  // K, V, weights
+    const int part = blockIdx.x / CTAS % parts, kvh = blockIdx.x / CTAS / parts;
     const int *kept = p.kept + ((size_t)seq * p.n_kv + kvh) * p.keep;
-    if (part < 2 * SLICES)
-        move_rows<PIECES, 16, (SLICES > 1)>(
-            ring, p.pool[part & 1], p.num_blocks, p.n_kv, kvh, D * 2, (part >> 1) * PIECES * 16,
-            p.from + (size_t)seq * p.from_stride, p.from_stride, p.to + (size_t)seq * p.to_stride, p.to_stride, kept,
-            p.keep);
+    if (part < 2)
+        move_rows<D / 8, 16, CTAS>(ring, p.pool[part], p.num_blocks, p.n_kv, kvh, rank,
+                                   p.from + (size_t)seq * p.from_stride, p.from_stride,
+                                   p.to + (size_t)seq * p.to_stride, p.to_stride, kept, p.keep);
     else
-        move_rows<1, 4, (SLICES > 1)>(ring, (uint8_t *)p.w, p.w_blocks, p.n_kv, kvh, 4, 0,
-                                      p.w_from + (size_t)seq * p.w_from_stride, p.w_from_stride,
-                                      p.w_to + (size_t)seq * p.w_to_stride, p.w_to_stride, kept, p.keep);
+        move_rows<1, 4, CTAS>(ring, (uint8_t *)p.w, p.w_blocks, p.n_kv, kvh, rank,
+                              p.w_from + (size_t)seq * p.w_from_stride, p.w_from_stride,
+                              p.w_to + (size_t)seq * p.w_to_stride, p.w_to_stride, kept, p.keep);
 }
 
 // ------------------------------------------------------------------- host
 
-template <int D, int SLICES>
+// A launch of clusters of CTAS CTAs.
+template <int CTAS, typename P>
+cudaError_t launch_clusters(void (*kernel)(P), long long gx, int gy, int threads, int smem, cudaStream_t s, const P &p)
+{
+    const cudaError_t e = max_carveout((const void *)kernel);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D, int CTAS>
 int launch_move(const Move &p, int n_seqs, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr int smem = MoveTile<D / 8 / SLICES, 16, (SLICES > 1)>::SMEM;
-    static_assert(smem >= MoveTile<1, 4, (SLICES > 1)>::SMEM);
-    auto kernel = k_evict_move<D, SLICES>;
-    const long long gx = (long long)p.n_kv * (2 * SLICES + (p.w ? 1 : 0));
+    constexpr int smem = MoveTile<D / 8, 16, CTAS>::SMEM;
+    static_assert(smem >= MoveTile<1, 4, CTAS>::SMEM);
+    auto kernel = k_evict_move<D, CTAS>;
+    const long long gx = (long long)p.n_kv * CTAS * (p.w ? 3 : 2);
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
     if (kv4_allow_smem((const void *)kernel, smem, done) != cudaSuccess)
         return HB_ECUDA;
-    return launch_kernel(true, kernel, dim3((unsigned)gx, (unsigned)n_seqs), dim3(MOVE_THREADS), smem, s, p) ==
-                   cudaSuccess
-               ? HB_OK
-               : HB_ECUDA;
+    return launch_clusters<CTAS>(kernel, gx, n_seqs, MOVE_THREADS, smem, s, p) == cudaSuccess ? HB_OK : HB_ECUDA;
 }
 
 template <int THREADS, int BITS, int CTAS>
@@ -465,22 +523,9 @@ int launch_select(Select p, int n_seqs, cudaStream_t s)
     const long long gx = (long long)p.n_kv * CTAS;
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
-    if (kv4_allow_smem((const void *)kernel, MOST, done) != cudaSuccess ||
-        max_carveout((const void *)kernel) != cudaSuccess)
+    if (kv4_allow_smem((const void *)kernel, MOST, done) != cudaSuccess)
         return HB_ECUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)gx, (unsigned)n_seqs);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {CTAS, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = CTAS > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? HB_OK : HB_ECUDA;
+    return launch_clusters<CTAS>(kernel, gx, n_seqs, THREADS, smem, s, p) == cudaSuccess ? HB_OK : HB_ECUDA;
 }
 
 }  // namespace
@@ -558,15 +603,9 @@ try {
     }
     cudaStream_t s = (cudaStream_t)cuda_stream;
     const long long items = (long long)n_seqs * p.n_kv;
-    const int slices = items * 2 >= 304 ? 1 : items * 4 >= 304 ? 2 : items * 8 >= 304 ? 4 : 8;
-    if (pool->head_dim == 128)
-        return slices == 1   ? launch_move<128, 1>(p, n_seqs, s)
-               : slices == 2 ? launch_move<128, 2>(p, n_seqs, s)
-               : slices == 4 ? launch_move<128, 4>(p, n_seqs, s)
-                             : launch_move<128, 8>(p, n_seqs, s);
-    return slices == 1   ? launch_move<64, 1>(p, n_seqs, s)
-           : slices == 2 ? launch_move<64, 2>(p, n_seqs, s)
-                         : launch_move<64, 4>(p, n_seqs, s);
+    if (items * 2 >= 304 || keep <= 2048)
+        return pool->head_dim == 128 ? launch_move<128, 1>(p, n_seqs, s) : launch_move<64, 1>(p, n_seqs, s);
+    return pool->head_dim == 128 ? launch_move<128, CLUSTER>(p, n_seqs, s) : launch_move<64, CLUSTER>(p, n_seqs, s);
 } catch (...) {
     return HB_ENOMEM;
 }
