@@ -14,9 +14,11 @@ constexpr int MAX_KEYS = 1 << 27;
 constexpr int INLINE_GROUPS = 16;  // groups that fit the kernels' parameters
 
 // Rows row0..row0 + rows - 1; prefix: tokens that they share, as the caller
-// says; shared: those of them that are attended once for the group.
+// says; shared: those of them that are attended once for the group, in whole
+// blocks, by the CTAs from cta0 on: `parts` runs of part_len sub-tiles of 64 keys.
 struct Group {
     int row0, rows, prefix, shared;
+    int cta0, parts, part_len;
 };
 
 // One attention over a paged cache: rows that attend their own keys from
@@ -34,7 +36,8 @@ struct Attn {
     float c2;                  // log2(e) / sqrt(d): weights are 2^((s - m) c2)
     int split_len, n_splits;   // of a row's own keys
     int col_tiles;             // CTAs of the queries of a kv head
-    int first_slot, n_slots;   // partials of a row: the group's prefix, then its own
+    int first_slot, n_slots;   // partials of a row: its group's parts, then from first_slot on its own splits
+    bool beside;               // the rows' own keys run beside the prefixes' kernel, launched before
     bf16 *out;
     long long out_stride;
     float2 *part_ml;           // [row][head][slot] (m, l)
@@ -60,6 +63,9 @@ struct Attn {
         return at(lo);
     }
 };
+
+// The groups' shared keys, for all rows of a group at once (prefix_attention.cu).
+int launch_prefix(const hb_paged_pool *pool, const Attn &p, int ctas, cudaStream_t s);
 
 int check_pool(const hb_paged_pool *p);
 int check_weight_pool(const hb_weight_pool *p);

@@ -28,6 +28,9 @@ using namespace paged;
 constexpr int WARPS = 4;
 constexpr int JOIN_WARPS = 8;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
+constexpr int SMS = 152;
+constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
+constexpr long long SHARE_BYTES = 1;
 constexpr int WEIGH_THREADS = 256;
 constexpr int WEIGH_KEYS = 4;        // keys of a thread of the weights' kernel
 constexpr float LOG2E = 1.4426950408889634f;
@@ -145,8 +148,16 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     const int ncols = p.nq * p.group;
     const int c0 = tile * COLS;
 
-    pdl_wait();
+    // Beside the prefixes' kernel, whose CTAs have all passed their wait for what
+    // came before when this one starts.  One CTA waits for its end, so that the
+    // join, which waits for this kernel, finds both done.
+    if (!p.beside)
+        pdl_wait();
     pdl_trigger();
+    auto leave = [&]() {
+        if (p.beside && blockIdx.x == 0 && blockIdx.y == 0)
+            pdl_wait();
+    };
     const int ctx = p.ctx_lens[seq];
     int from = 0, least = 0;  // first own key, smallest context
     int common = 0, row0 = seq;  // pages that are the group's, found through its first row's table
@@ -166,11 +177,11 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
                     p.out[(long long)(seq * p.nq + c / p.group) * p.out_stride +
                           (size_t)(kvh * p.group + c % p.group) * D + i % D] = f2bf(ctx == -1 ? 0.f : nan_f());
             }
-        return;
+        return leave();
     }
     const int k0 = from + split * p.split_len, k1 = min(ctx + 1, k0 + p.split_len);
     if (k0 >= k1)
-        return;  // the join knows how many splits a row has
+        return leave();  // the join knows how many splits a row has
 
     // ---- this warp's pages: b0 + 4 i, i < n
     const int b0 = (k0 >> 4) + warp;
@@ -424,21 +435,23 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
                 *reinterpret_cast<float4 *>(p.part_o + slot * D + e) = acc;
         }
     }
+    leave();
 }
 
-// The join of a row's partials: a warp a (row, head).  The group's first
-// first_slot partials are its prefix's, the others the row's own splits.
+// The join of a row's partials, of its group's prefix and of its own splits: a
+// warp a (row, head).
 template <int D>
 __device__ __forceinline__ void join_row(const Attn &p, int row, int head, int lane)
 {
     constexpr int E = D / 32;
     const int seq = row / p.nq;
     const int ctx = p.ctx_lens[seq];
-    int from = 0, least = 0;
+    int from = 0, least = 0, parts = 0;
     if (p.n_groups > 0) {
         const Group gr = p.of(seq);
         from = gr.shared;
         least = gr.prefix > 0 ? gr.prefix - 1 : 0;
+        parts = gr.parts;
     }
     const int keys = ctx + 1 - (p.nq - 1) + row % p.nq;  // that the row sees
     float acc[E];
@@ -451,21 +464,22 @@ __device__ __forceinline__ void join_row(const Attn &p, int row, int head, int l
             acc[e] = ctx == -1 ? 0.f : nan_f();
     } else if (keys > 0) {
         const int own = (ctx + 1 - from + p.split_len - 1) / p.split_len;
-        const int s0 = from > 0 ? 0 : p.first_slot, s1 = p.first_slot + own;
-        const size_t at = ((size_t)row * p.n_heads + head) * p.n_slots;
+        const int n = parts + own;
+        const size_t base_at = ((size_t)row * p.n_heads + head) * p.n_slots;
+        auto slot = [&](int i) { return base_at + (i < parts ? i : p.first_slot + i - parts); };
         float mx = -INFINITY;
-        for (int s = s0 + lane; s < s1; s += 32)
-            mx = fmaxf(mx, __ldcg(&p.part_ml[at + s]).x);
+        for (int i = lane; i < n; i += 32)
+            mx = fmaxf(mx, __ldcg(&p.part_ml[slot(i)]).x);
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
         const float base = mx == -INFINITY ? 0.f : mx;
         float sum = 0.f;
-        for (int s = s0; s < s1; ++s) {
-            const float2 ml = __ldcg(&p.part_ml[at + s]);
+        for (int i = 0; i < n; ++i) {
+            const float2 ml = __ldcg(&p.part_ml[slot(i)]);
             const float f = ex2((ml.x - base) * p.c2);
             sum += ml.y * f;
-            const float *o = p.part_o + (at + s) * D + lane * E;
+            const float *o = p.part_o + slot(i) * D + lane * E;
             if constexpr (E == 4) {
                 const float4 v = __ldcg(reinterpret_cast<const float4 *>(o));
                 acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
@@ -656,12 +670,41 @@ int check_attention(const hb_paged_pool *pool, const void *q, long long q_stride
 
 struct Plan {
     int nt, split_len, n_splits, col_tiles, first_slot, n_slots;
+    int ctas;  // of the prefixes' kernel
     Layout at;
 };
 
-// What hb_decode_shared does with its groups; groups may be null.  HB_OK or an error.
-int plan_shared(int n_rows, int n_heads, int n_kv, int d, int max_ctx, const int32_t *group_rows,
-                const int32_t *prefix_lens, int n_groups, Plan *pl)
+// What is attended once for group i, and how: its blocks are shared when the
+// reads that this saves pay for a second kernel and a join.
+Group shared_group(int row0, int rows, int prefix, int n_kv, int d, bool can)
+{
+    Group g = {row0, rows, prefix, 0, 0, 0, 1};
+    const int whole = prefix & ~15;
+    if (can && whole > 0 && (long long)(rows - 1) * whole * n_kv * 4 * d >= SHARE_BYTES)
+        g.shared = whole;
+    return g;
+}
+
+// CTAs of a group when none is to take more than `most` units (of a sub-tile's
+// time: 3 where a CTA has at most 128 rows, 4 with two Q tiles), and their cut.
+long long cut_group(Group *g, int heads, int n_kv, long long most)
+{
+    if (g->shared == 0)
+        return 0;
+    const long long cols = (long long)g->rows * heads, tiles = (cols + 255) / 256;
+    const int subs = (g->shared + 63) / 64;
+    const long long fit = most / (cols > 128 ? 4 : 3);
+    g->part_len = fit < PART_MIN ? PART_MIN : fit > subs ? subs : (int)fit;
+    g->parts = (subs + g->part_len - 1) / g->part_len;
+    g->part_len = (subs + g->parts - 1) / g->parts;
+    g->parts = (subs + g->part_len - 1) / g->part_len;
+    return tiles * n_kv * g->parts;
+}
+
+// What hb_decode_shared does with its groups, which `each` receives in order.  HB_OK or an error.
+template <typename F>
+int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int max_ctx, const int32_t *group_rows,
+                const int32_t *prefix_lens, int n_groups, Plan *pl, F each)
 {
     if (!group_rows || !prefix_lens || n_groups < 1)
         return HB_EINVAL;
@@ -676,10 +719,45 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int max_ctx, const int
     if (rows != n_rows)
         return HB_EINVAL;
     const int g = n_heads / n_kv;
+    // a copy's row coordinate is 32 bits wide, a group's queries are counted in as many
+    const bool can = (long long)num_blocks * n_kv * 16 <= 0x7fffffffll && (long long)n_rows * g <= 0x7fffffffll;
+    // the smallest load of a CTA for which all run at once, or else the whole of a prefix
+    auto total = [&](long long most) {
+        long long n = 0;
+        for (int i = 0; i < n_groups; ++i) {
+            Group gr = shared_group(0, group_rows[i], prefix_lens[i], n_kv, d, can);
+            n += cut_group(&gr, g, n_kv, most);
+        }
+        return n;
+    };
+    long long lo = 0, hi = 4ll * (MAX_KEYS / 64 + 1);
+    if (total(hi) <= SMS)
+        while (hi - lo > 1) {  // total(hi) fits
+            const long long mid = (lo + hi) / 2;
+            if (total(mid) <= SMS)
+                hi = mid;
+            else
+                lo = mid;
+        }
+    long long ctas = 0;
+    int row = 0, parts = 0, most = 0;
+    for (int i = 0; i < n_groups; ++i) {
+        Group gr = shared_group(row, group_rows[i], prefix_lens[i], n_kv, d, can);
+        const long long n = cut_group(&gr, g, n_kv, hi);
+        if (ctas + n > 0x7fffffffll)
+            return HB_ERANGE;
+        gr.cta0 = (int)ctas;
+        ctas += n;
+        parts = gr.parts > parts ? gr.parts : parts;
+        most = max_ctx + 1 - gr.shared > most ? max_ctx + 1 - gr.shared : most;
+        row += gr.rows;
+        each(i, gr);
+    }
+    pl->ctas = (int)ctas;
     pl->nt = g > 8 ? 2 : 1;
     pl->col_tiles = tiles_of(g, pl->nt);
-    plan_splits((long long)n_rows * n_kv * pl->col_tiles, max_ctx + 1, &pl->split_len, &pl->n_splits);
-    pl->first_slot = 0;
+    plan_splits((long long)n_rows * n_kv * pl->col_tiles, most, &pl->split_len, &pl->n_splits);
+    pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->at = layout(n_rows, n_heads, d, pl->n_slots, n_groups, false, max_ctx);
     return HB_OK;
@@ -700,11 +778,11 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int max_c
     return HB_OK;
 }
 
-Attn params(const hb_paged_pool *pool, const void *q, long long q_stride, const int32_t *tables, int bt_stride,
+void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_stride, const int32_t *tables, int bt_stride,
             const int32_t *ctx_lens, int n_heads, int max_ctx, int nq, void *out, long long out_stride, const Plan &pl,
             void *workspace)
 {
-    Attn p = {};
+    Attn &p = *a;
     p.k = (const bf16 *)pool->k;
     p.v = (const bf16 *)pool->v;
     p.num_blocks = pool->num_blocks;
@@ -731,7 +809,6 @@ Attn params(const hb_paged_pool *pool, const void *q, long long q_stride, const 
     p.part_o = (float *)(w + pl.at.o);
     p.scores = (float *)(w + pl.at.scores);
     p.score_stride = pl.at.score_stride;
-    return p;
 }
 
 int check_workspace(const void *workspace, long long bytes, long long need)
@@ -787,8 +864,15 @@ extern "C" long long hb_decode_shared_workspace(int n_rows, int n_heads, int n_k
     if (n_rows > 65535 || (long long)n_rows * n_heads > 0x7fffffffll)
         return HB_ERANGE;
     Plan pl;
-    const int rp = plan_shared(n_rows, n_heads, n_kv_heads, head_dim, max_ctx, group_rows, prefix_lens, n_groups, &pl);
-    return rp ? rp : pl.at.bytes;
+    auto none = [](int, const Group &) {};
+    // with shared prefixes, and without as for a pool too large for them
+    const int rp = plan_shared(n_rows, n_heads, n_kv_heads, head_dim, 1, max_ctx, group_rows, prefix_lens, n_groups,
+                               &pl, none);
+    if (rp)
+        return rp;
+    const long long bytes = pl.at.bytes;
+    plan_shared(n_rows, n_heads, n_kv_heads, head_dim, MAX_KEYS, max_ctx, group_rows, prefix_lens, n_groups, &pl, none);
+    return pl.at.bytes > bytes ? pl.at.bytes : bytes;
 }
 
 extern "C" int hb_decode_shared(const hb_paged_pool *pool, const void *q, long long q_stride,
@@ -806,25 +890,37 @@ try {
     if (rc)
         return rc;
     Plan pl;
-    rc = plan_shared(n_rows, n_heads, pool->n_kv_heads, pool->head_dim, max_ctx, group_rows, prefix_lens, n_groups,
-                     &pl);
+    Attn p = {};
+    rc = plan_shared(n_rows, n_heads, pool->n_kv_heads, pool->head_dim, pool->num_blocks, max_ctx, group_rows,
+                     prefix_lens, n_groups, &pl, [&](int i, const Group &g) {
+                         if (n_groups <= INLINE_GROUPS)
+                             p.few[i] = g;
+                     });
     if (rc || (rc = check_workspace(workspace, workspace_bytes, pl.at.bytes)))
         return rc;
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    Attn p = params(pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, 1, out, out_stride, pl,
-                    workspace);
+    params(&p, pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, 1, out, out_stride, pl, workspace);
     p.n_groups = n_groups;
-    Group *list = (Group *)((char *)workspace + pl.at.groups);
-    int row = 0;
-    for (int i = 0; i < n_groups; ++i) {
-        const int at = n_groups <= INLINE_GROUPS ? i : i % INLINE_GROUPS;
-        p.few[at] = Group{row, group_rows[i], prefix_lens[i], 0};
-        row += group_rows[i];
-        if (n_groups > INLINE_GROUPS && (at == INLINE_GROUPS - 1 || i == n_groups - 1))
-            if (launch_kernel(true, k_paged_groups, dim3(1), dim3(32), 0, s, list, p, i - at, at + 1) != cudaSuccess)
-                return HB_ECUDA;
+    if (n_groups > INLINE_GROUPS) {  // the groups go ahead into the workspace
+        Group *list = (Group *)((char *)workspace + pl.at.groups);
+        bool sent = true;
+        plan_shared(n_rows, n_heads, pool->n_kv_heads, pool->head_dim, pool->num_blocks, max_ctx, group_rows, prefix_lens,
+                    n_groups, &pl, [&](int i, const Group &g) {
+                        const int at = i % INLINE_GROUPS;
+                        p.few[at] = g;
+                        if (at == INLINE_GROUPS - 1 || i == n_groups - 1)
+                            sent = sent && launch_kernel(true, k_paged_groups, dim3(1), dim3(32), 0, s, list, p, i - at,
+                                                         at + 1) == cudaSuccess;
+                    });
+        if (!sent)
+            return HB_ECUDA;
+        p.groups = list;
     }
-    p.groups = n_groups > INLINE_GROUPS ? list : nullptr;
+    if (pl.ctas > 0) {
+        if ((rc = launch_prefix(pool, p, pl.ctas, s)))
+            return rc;
+        p.beside = true;
+    }
     rc = attention<false>(p, pool->head_dim, pl.nt, n_rows, s);
     if (rc || pl.n_slots == 1)
         return rc;
@@ -887,8 +983,9 @@ try {
         (rc = check_workspace(workspace, workspace_bytes, pl.at.bytes)))
         return rc;
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    const Attn p = params(pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, n_queries, out,
-                          out_stride, pl, workspace);
+    Attn p = {};
+    params(&p, pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, n_queries, out, out_stride, pl,
+           workspace);
     const int chunks = max_ctx / (WEIGH_THREADS * WEIGH_KEYS) + 1;
     const long long gx = (long long)p.n_kv * chunks;
     const long long jx = ((long long)rows * n_heads + JOIN_WARPS - 1) / JOIN_WARPS;

@@ -1,0 +1,561 @@
+// prefix_attention.cu -- attention of a group's rows to the prefix that they
+// share, on the tcgen05 tensor cores (include/hb_paged.h).
+//
+//   S = Q K^T,  P = 2^((S - m) c2),  O += P V;  partials (m, sum P, O)
+//
+// Q's rows are the group's (row, head) pairs of one kv head, up to 256 of them
+// in a CTA, which takes a run of the prefix's whole 16-token blocks: every row
+// sees every key, so nothing is masked.  Other CTAs have other runs of the same
+// keys; the join of the rows' partials follows with their own keys
+// (paged_attention.cu).
+//
+//   warps 0..7   softmax, one thread a row: S from tensor memory, P back over
+//                it in two bf16 terms (16 significant bits, as in
+//                paged_attention.cu); O is rescaled only when a maximum has
+//                risen by more than 2^8
+//   warps 8, 9   issue the MMAs of the two halves of 128 rows
+//   warp 10      loads sub-tiles of 64 keys of K and V by TMA, a box per block
+//                and 64 channels
+//
+// Two halves keep the tensor pipe busy: while one is in the softmax the other's
+// products run.  A CTA of more than 128 rows has a Q tile for each half; with
+// up to 128 ("dual") both have the same tile and take the sub-tiles in turn, and
+// the CTA joins their two results.  S has two buffers a half.
+//
+// Every wait is bounded; when one runs out, the CTA writes NaN for its rows,
+// drains and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "gemm_tc.h"
+#include "kv4.cuh"
+#include "kv4_host.h"
+#include "paged.h"
+#include "tc_ptx.cuh"
+
+namespace hb {
+namespace {
+
+using namespace paged;
+using namespace tc;
+using kv4::add_f2;
+using kv4::ex2;
+using kv4::fma_f2;
+using kv4::pack_f2;
+using kv4::unpack_f2;
+
+constexpr int MMA_WARP = 8, LOAD_WARP = 10;
+constexpr int THREADS = 11 * 32;
+constexpr float LOWEST = -3e38f;         // below every score, and finite: differences with it are too
+constexpr float RAISE = 8.f;             // in powers of two: how far a score may pass the maximum used
+constexpr float HUGE_SCORE = 1 << 20;    // up to it s c2 - m c2 may be fused: m c2 is rounded by 2^-4 at most, for all P alike
+constexpr uint64_t WAIT_NS = 2000000000ull;  // after which a wait is given up
+
+template <int D>
+struct Px {
+    static constexpr int CB = D / 64;               // column blocks of 64 channels
+    static constexpr int QBLK = 128 * 128;          // one column block of a 128-row tile
+    static constexpr int TILE = CB * QBLK;
+    static constexpr int BLK = 64 * 128;            // the same of a 64-key sub-tile
+    static constexpr int SUB = CB * BLK;            // K or V of a sub-tile
+    static constexpr int STAGES = D == 128 ? 5 : 8, STAGES_DUAL = D == 128 ? 6 : 10;
+    static constexpr int BAR = (2 * TILE + 2 * STAGES * SUB) > (TILE + 2 * STAGES_DUAL * SUB)
+                                   ? 2 * TILE + 2 * STAGES * SUB
+                                   : TILE + 2 * STAGES_DUAL * SUB;
+    static constexpr int BYTES = BAR + 512 + 1024;  // barriers, alignment
+    static_assert(BYTES <= 227 * 1024);
+    static constexpr uint32_t O0 = 256;             // S: 64 columns for each (half, buffer); then O of the halves
+};
+
+// byte offset of (row, 16-byte chunk c) in a 128-byte-swizzled column block
+__device__ __forceinline__ uint32_t swz(int row, int c)
+{
+    return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// MN-major operand, 128-byte swizzle: 64-element column blocks block_stride
+// bytes apart, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t block_stride)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((block_stride >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// One k-step of D (+)= A B with A (bf16) in tensor memory and B in shared
+// memory; one elected lane issues.
+__device__ __forceinline__ void mma_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A place in a ring of n stages: the stage, and the parity of its full barrier.
+struct Place {
+    uint32_t st = 0, ph = 0;
+    __device__ __forceinline__ void next(uint32_t n)
+    {
+        if (++st == n) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_prefix_attention(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ Attn p)
+{
+    using C = Px<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    constexpr int MOST = C::STAGES_DUAL;
+    uint64_t *k_full = (uint64_t *)(smem + C::BAR), *v_full = k_full + MOST, *empty = v_full + MOST;
+    uint64_t *s_full = empty + MOST, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][buffer]
+    uint64_t *q_full = pv_done + 4, *drain = q_full + 1;                           // [half]
+    uint32_t *tmem_slot = (uint32_t *)(drain + 2);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    volatile int *bad = abort_flag + 1;  // a block outside the pool was met
+    static_assert((3 * MOST + 15) * 8 + 12 <= 512);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    // ---- this CTA's group, kv head, rows and keys
+    if (p.groups)
+        pdl_wait();  // a kernel before this one puts them there
+    int gi = 0;
+    {
+        int hi = p.n_groups - 1;  // the last group that starts at or before this CTA
+        while (gi < hi) {
+            const int mid = (gi + hi + 1) >> 1;
+            if (p.at(mid).cta0 <= (int)blockIdx.x)
+                gi = mid;
+            else
+                hi = mid - 1;
+        }
+    }
+    const Group gr = p.at(gi);
+    const int local = (int)blockIdx.x - gr.cta0;
+    const int part = local % gr.parts, kvh = local / gr.parts % p.n_kv, tile = local / gr.parts / p.n_kv;
+    const int c0 = tile * 256, cols = min(256, gr.rows * p.group - c0);
+    const bool dual = cols <= 128;
+    const uint32_t stages = dual ? C::STAGES_DUAL : C::STAGES;
+    const int t0 = part * gr.part_len, subs = min((gr.shared + 63) / 64, t0 + gr.part_len) - t0;
+    auto blocks_of = [&](int t) { return min(4, (gr.shared >> 4) - (t0 + t) * 4); };  // of sub-tile t
+    uint8_t *sK = smem + (dual ? C::TILE : 2 * C::TILE), *sV = sK + stages * C::SUB;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < (int)stages; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&empty[i], dual ? 1 : 2);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(q_full, 8);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
+        *abort_flag = 0;
+        *bad = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == MMA_WARP)
+        tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    constexpr uint32_t tmem = 0;  // all 512 columns: they begin at 0
+    pdl_wait();
+    pdl_trigger();
+
+    bool ok = true;
+    // A whole warp's wait (the votes tell the compiler that the warp stays
+    // together).
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        uint32_t looks = 0;
+        uint64_t since = 0;
+#pragma unroll 1
+        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+            bool over = *abort_flag;
+            if ((++looks & 63u) == 0) {
+                const uint64_t now = globaltimer_ns();
+                since = since ? since : now;
+                over |= now - since > WAIT_NS;
+            }
+            if (__any_sync(0xffffffffu, over)) {
+                *abort_flag = 1;
+                return ok = false;
+            }
+        }
+        return ok;
+    };
+
+    if (warp < 8) {
+        // -------------------------------------------------------- softmax
+        // Q: the CTA's rows of (row, head) pairs, zeros past the last
+        for (int i = threadIdx.x; i < (dual ? 1 : 2) * 128 * (D / 8); i += 256) {
+            const int r = i / (D / 8), ch = i % (D / 8), c = c0 + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < cols)
+                v = __ldg(reinterpret_cast<const uint4 *>(p.q + (long long)(gr.row0 + c / p.group) * p.q_stride +
+                                                          (size_t)(kvh * p.group + c % p.group) * D) +
+                          ch);
+            *reinterpret_cast<uint4 *>(smem + (r >> 7) * C::TILE + (ch >> 3) * C::QBLK + swz(r & 127, ch & 7)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(q_full);
+
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t sT = lanes + half * 128, oT = lanes + C::O0 + half * D;
+        const int own = dual ? (subs + 1 - half) / 2 : subs;  // sub-tiles of this half
+        const int valid = min(128, cols - (dual ? 0 : half * 128));
+        const bool idle = (warp & 3) * 32 >= valid;  // no row in this warp
+        float m = LOWEST, l = 0.f;
+        float raise_at = LOWEST;  // a maximum above it moves m
+#pragma unroll 1
+        for (int i = 0; i < own; ++i) {
+            const uint32_t buf = i & 1u;
+            if (!wait(&s_full[2 * half + buf], (uint32_t)(i >> 1) & 1u))
+                break;
+            if (idle) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[2 * half + buf]);
+                continue;
+            }
+            tc_fence_after();
+            float v[2][32];
+            tmem_ld_x32(sT + buf * 64, v[0]);
+            tmem_ld_x32(sT + buf * 64 + 32, v[1]);
+            tmem_ld_wait();
+            const int n = blocks_of(dual ? 2 * i + half : i);
+            if (n < 4)  // the prefix's last blocks
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    v[0][j] = j < n * 16 ? v[0][j] : -INFINITY;
+                    v[1][j] = 32 + j < n * 16 ? v[1][j] : -INFINITY;
+                }
+            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
+            const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            float off = -m * p.c2;  // P = 2^(s c2 + off)
+            if (__any_sync(0xffffffffu, mx > raise_at)) {
+                const float mn = fmaxf(m, mx), corr = ex2((m - mn) * p.c2);
+                m = mn;
+                l *= corr;
+                raise_at = m + RAISE / p.c2;
+                off = -m * p.c2;
+                if (fabsf(off) > HUGE_SCORE) {  // the difference first; and here again with every sub-tile
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        v[0][j] -= m;
+                        v[1][j] -= m;
+                    }
+                    off = 0.f;
+                    raise_at = -INFINITY;
+                }
+                if (i > 0) {  // O holds the products before this one: let the last of them end
+                    if (!wait(&pv_done[2 * half + (buf ^ 1u)], (uint32_t)((i - 1) >> 1) & 1u))
+                        break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t y[16];
+                        tmem_ld_32x32b_x16(oT + c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+                        tmem_st_x16(oT + c, y);
+                    }
+                }
+            }
+            const uint64_t c2 = pack_f2(p.c2, p.c2), off2 = pack_f2(off, off), minus = pack_f2(-1.f, -1.f);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float a, b;
+                    unpack_f2(fma_f2(pack_f2(v[k][2 * j], v[k][2 * j + 1]), c2, off2), a, b);
+                    a = ex2(a);
+                    b = ex2(b);
+                    const uint64_t ab = pack_f2(a, b);
+                    sum2[j & 1] = add_f2(sum2[j & 1], ab);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                    hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+                    float ra, rb;
+                    unpack_f2(fma_f2(pack_f2(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xffff0000u)), minus,
+                                     ab),
+                              ra, rb);
+                    const __nv_bfloat162 q = __floats2bfloat162_rn(ra, rb);
+                    lo[j] = *reinterpret_cast<const uint32_t *>(&q);
+                }
+                tmem_st_x16(sT + buf * 64 + k * 16, hi);  // over S, which is read already
+                tmem_st_x16(sT + buf * 64 + 32 + k * 16, lo);
+            }
+            float a, b;
+            unpack_f2(add_f2(sum2[0], sum2[1]), a, b);
+            l += a + b;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&p_full[2 * half + buf]);
+        }
+        // ---- the result
+        if (ok && own > 0 && wait(&pv_done[2 * half + ((own - 1) & 1)], (uint32_t)((own - 1) >> 1) & 1u))
+            tc_fence_after();
+        // with both halves on the same rows, each takes half of the channels
+        // and joins the two O there: f, f2 are their factors
+        float f = 1.f, f2 = 0.f;
+        if (dual) {
+            // m and l pass through tensor memory, over this half's S: its products are done
+            float2 o;
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(sT), "f"(m), "f"(l) : "memory");
+            tmem_st_wait();
+            tc_fence_before();
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            tc_fence_after();
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                         : "=f"(o.x), "=f"(o.y)
+                         : "r"(lanes + (half ^ 1) * 128)
+                         : "memory");
+            tmem_ld_wait();
+            const float M = fmaxf(m, o.x);
+            f = ex2((m - M) * p.c2);
+            f2 = ex2((o.x - M) * p.c2);
+            l = l * f + o.y * f2;
+            m = M;
+            if (half == 1) {  // f belongs to the first half's O, f2 to the second's
+                const float y = f;
+                f = f2;
+                f2 = y;
+            }
+        }
+        __syncwarp();
+        ok = !__any_sync(0xffffffffu, !ok || *abort_flag);
+        const int k0 = dual ? half * (D / 2) : 0, k1 = dual ? k0 + D / 2 : D;
+        const bool two = dual && subs > 1;  // the second half has an O
+        const int c = c0 + (dual ? 0 : half * 128) + (r < valid ? r : 0);
+        const size_t slot =
+            ((size_t)(gr.row0 + c / p.group) * p.n_heads + kvh * p.group + c % p.group) * p.n_slots + part;
+        if (!idle) {
+            if (r < valid && (!dual || half == 0))
+                p.part_ml[slot] = make_float2(m, !ok || *bad ? __int_as_float(0x7fc00000) : l);
+#pragma unroll 1
+            for (int e = k0; e < k1; e += 16) {
+                uint32_t x[16], y[16];
+                if (ok) {
+                    tmem_ld_32x32b_x16((dual ? lanes + C::O0 : oT) + e, x);
+                    if (two)
+                        tmem_ld_32x32b_x16(lanes + C::O0 + D + e, y);
+                    tmem_ld_wait();
+                    if (dual)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            x[j] = __float_as_uint(__uint_as_float(x[j]) * f +
+                                                   (two ? __uint_as_float(y[j]) * f2 : 0.f));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        x[j] = 0;
+                }
+                if (r < valid)
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8)
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                         p.part_o + slot * D + e + j),
+                                     "r"(x[j]), "r"(x[j + 1]), "r"(x[j + 2]), "r"(x[j + 3]), "r"(x[j + 4]),
+                                     "r"(x[j + 5]), "r"(x[j + 6]), "r"(x[j + 7])
+                                     : "memory");
+                __syncwarp();
+            }
+        }
+    } else if (warp == MMA_WARP || (warp == MMA_WARP + 1 && !dual)) {
+        // ---------------------------------------------------- MMA issue
+        // a warp for each half; where the halves take the sub-tiles in turn,
+        // one for both, so that the stages are let go in order
+        const int h = warp - MMA_WARP;
+        const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
+        const uint64_t dQ = sdesc_kmajor_sw128(smem_u32(smem) + (dual ? 0 : h * C::TILE));
+        const uint64_t dK = sdesc_kmajor_sw128(smem_u32(sK)), dV = sdesc_mn(smem_u32(sV), C::BLK);
+        const uint32_t turn = dual ? 1 : 0;
+        const int ahead = 2 << turn;  // S is two sub-tiles of a half ahead of O
+        Place k, v;
+        auto half_of = [&](int t) { return dual ? (uint32_t)t & 1u : (uint32_t)h; };
+        auto slot_of = [&](int t) { return 2 * half_of(t) + ((uint32_t)t >> turn & 1u); };  // half and buffer
+        auto issue_s = [&](int t) {  // S of sub-tile t, which is at k
+            const uint32_t slot = slot_of(t), id_s = idesc_bf16_f32(128, 0) | (uint32_t)(2 * blocks_of(t)) << 17;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                mma_bf16_elect(tmem + slot * 64, dQ + (j >> 2) * (C::QBLK >> 4) + (j & 3) * 2,
+                               dK + k.st * (C::SUB >> 4) + (j >> 2) * (C::BLK >> 4) + (j & 3) * 2, id_s, j);
+            mma_commit_elect(&s_full[slot]);
+            k.next(stages);
+        };
+        wait(q_full, 0);
+#pragma unroll 1
+        for (int t = 0; t < min(ahead, subs) && ok; ++t) {
+            if (!wait(&k_full[k.st], k.ph))
+                break;
+            tc_fence_after();
+            issue_s(t);
+        }
+#pragma unroll 1
+        for (int t = 0; t < subs && ok; ++t) {
+            // lanes look at several barriers at once: P and V of this sub-tile,
+            // and K of the one whose S comes next
+            const uint32_t slot = slot_of(t);
+            uint64_t *bar = &p_full[slot];
+            uint32_t ph = (uint32_t)t >> (1 + turn) & 1u;
+            if (lane == 1)
+                bar = &v_full[v.st], ph = v.ph;
+            if (lane == 2 && t + ahead < subs)
+                bar = &k_full[k.st], ph = k.ph;
+            if (!wait(bar, ph))
+                break;
+            tc_fence_after();
+            const int n = blocks_of(t);
+            const uint32_t o = tmem + C::O0 + half_of(t) * D, pa = tmem + slot * 64;
+            const uint64_t vd = dV + v.st * (C::SUB >> 4);
+            if (n == 4) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    mma_ts_elect(o, pa + j * 8, vd + (j & 3) * 128, id_o, (t >> turn) | j);
+            } else {
+                for (int j = 0; j < n; ++j) {
+                    mma_ts_elect(o, pa + j * 8, vd + j * 128, id_o, (t >> turn) | j);
+                    mma_ts_elect(o, pa + 32 + j * 8, vd + j * 128, id_o, 1u);
+                }
+            }
+            mma_commit_elect(&pv_done[slot]);
+            mma_commit_elect(&empty[v.st]);
+            v.next(stages);
+            if (t + ahead < subs)
+                issue_s(t + ahead);
+        }
+        // no product may be under way, and no arrival, when the CTA ends: the
+        // other roles may have given up before this warp's last ones
+        mma_commit_elect(&drain[h]);
+        mbar_wait(&drain[h], 0, nullptr, WAIT_NS / 4);
+    } else if (warp == LOAD_WARP) {
+        // ---------------------------------------------------- loader
+        // lane i: box i of a sub-tile (block, column block; K, then V)
+        const int *tab = p.tables + (size_t)gr.row0 * p.bt_stride + (size_t)t0 * 4;
+        const int j = lane & 3, cb = (lane >> 2) % C::CB, is_v = (lane >> 2) / C::CB;
+        auto block = [&](int t) { return t < subs && j < blocks_of(t) ? __ldg(tab + t * 4 + j) : -1; };
+        int ids[4];  // of the next four sub-tiles: their latency is not in the loop
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            ids[u] = block(u);
+        Place at;
+        int it = 0;
+        for (; it < subs; ++it) {
+            if (it >= (int)stages && !wait(&empty[at.st], at.ph ^ 1u))
+                break;
+            const int n = blocks_of(it);
+            int blk = ids[0];
+            ids[0] = ids[1], ids[1] = ids[2], ids[2] = ids[3];
+            ids[3] = block(it + 4);
+            if (j < n && (blk < 0 || blk >= p.num_blocks)) {
+                *bad = 1;  // not read: the group's rows become NaN
+                blk = 0;
+            }
+            __syncwarp();
+            if (lane < 2)
+                mbar_expect_tx(lane ? &v_full[at.st] : &k_full[at.st], (uint32_t)(n * C::CB * 2048));
+            __syncwarp();
+            if (is_v < 2 && j < n)
+                tma_load_2d((is_v ? sV : sK) + at.st * C::SUB + cb * C::BLK + j * 2048, is_v ? &tm_v : &tm_k,
+                            is_v ? &v_full[at.st] : &k_full[at.st], cb * 64, (int)(((long long)blk * p.n_kv + kvh) * 16));
+            at.next(stages);
+        }
+        // no copy may land after the CTA has ended
+        for (int i = max(0, it - (int)stages); i < it; ++i) {
+            mbar_wait(&k_full[i % (int)stages], (uint32_t)(i / (int)stages) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
+            mbar_wait(&v_full[i % (int)stages], (uint32_t)(i / (int)stages) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
+        }
+        __threadfence_block();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+namespace paged {
+
+int launch_prefix(const hb_paged_pool *pool, const Attn &p, int ctas, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done[2];
+    CUtensorMap k, v;
+    if (!make_tmap_kv_pool(&k, pool->k, pool->num_blocks, pool->n_kv_heads, pool->head_dim) ||
+        !make_tmap_kv_pool(&v, pool->v, pool->num_blocks, pool->n_kv_heads, pool->head_dim))
+        return HB_ECUDA;
+    const bool wide = pool->head_dim == 128;
+    auto kernel = wide ? k_prefix_attention<128> : k_prefix_attention<64>;
+    const int smem = wide ? Px<128>::BYTES : Px<64>::BYTES;
+    if (kv4_allow_smem((const void *)kernel, smem, done[wide]) != cudaSuccess)
+        return HB_ECUDA;
+    return launch_kernel(true, kernel, dim3((unsigned)ctas), dim3(THREADS), smem, s, k, v, p) == cudaSuccess ? HB_OK
+                                                                                                             : HB_ECUDA;
+}
+
+}  // namespace paged
+}  // namespace hb
