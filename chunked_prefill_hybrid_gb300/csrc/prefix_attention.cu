@@ -14,7 +14,7 @@
 //                paged_attention.cu); O is rescaled only when a maximum has
 //                risen by more than 2^8
 //   warps 8, 9   issue the MMAs of the two halves of 128 rows
-//   warp 10      loads sub-tiles of 64 keys of K and V by TMA, a box per block
+//   warps 10, 11 load sub-tiles of 64 keys of K and of V by TMA, a box per block
 //                and 64 channels
 //
 // Two halves keep the tensor pipe busy: while one is in the softmax the other's
@@ -47,7 +47,7 @@ using kv4::pack_f2;
 using kv4::unpack_f2;
 
 constexpr int MMA_WARP = 8, LOAD_WARP = 10;
-constexpr int THREADS = 11 * 32;
+constexpr int THREADS = 12 * 32;
 constexpr float LOWEST = -3e38f;         // below every score, and finite: differences with it are too
 constexpr float RAISE = 8.f;             // in powers of two: how far a score may pass the maximum used
 constexpr float HUGE_SCORE = 1 << 20;    // up to it s c2 - m c2 may be fused: m c2 is rounded by 2^-4 at most, for all P alike
@@ -150,13 +150,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     constexpr int MOST = C::STAGES_DUAL;
-    uint64_t *k_full = (uint64_t *)(smem + C::BAR), *v_full = k_full + MOST, *empty = v_full + MOST;
-    uint64_t *s_full = empty + MOST, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][buffer]
+    uint64_t *k_full = (uint64_t *)(smem + C::BAR), *v_full = k_full + MOST, *k_empty = v_full + MOST;
+    uint64_t *v_empty = k_empty + MOST, *s_full = v_empty + MOST, *p_full = s_full + 4, *pv_done = p_full + 4;  // [half][buffer]
     uint64_t *q_full = pv_done + 4, *drain = q_full + 1;                           // [half]
     uint32_t *tmem_slot = (uint32_t *)(drain + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad = abort_flag + 1;  // a block outside the pool was met
-    static_assert((3 * MOST + 15) * 8 + 12 <= 512);
+    static_assert((4 * MOST + 15) * 8 + 12 <= 512);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < (int)stages; ++i) {
             mbar_init(&k_full[i], 1);
             mbar_init(&v_full[i], 1);
-            mbar_init(&empty[i], dual ? 1 : 2);
+            mbar_init(&k_empty[i], dual ? 1 : 2);
+            mbar_init(&v_empty[i], dual ? 1 : 2);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
@@ -443,6 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mma_bf16_elect(tmem + slot * 64, dQ + (j >> 2) * (C::QBLK >> 4) + (j & 3) * 2,
                                dK + k.st * (C::SUB >> 4) + (j >> 2) * (C::BLK >> 4) + (j & 3) * 2, id_s, j);
             mma_commit_elect(&s_full[slot]);
+            mma_commit_elect(&k_empty[k.st]);
             k.next(stages);
         };
         wait(q_full, 0);
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             mma_commit_elect(&pv_done[slot]);
-            mma_commit_elect(&empty[v.st]);
+            mma_commit_elect(&v_empty[v.st]);
             v.next(stages);
             if (t + ahead < subs)
                 issue_s(t + ahead);
@@ -490,44 +492,51 @@ __global__ void __launch_bounds__(THREADS, 1)
         // other roles may have given up before this warp's last ones
         mma_commit_elect(&drain[h]);
         mbar_wait(&drain[h], 0, nullptr, WAIT_NS / 4);
-    } else if (warp == LOAD_WARP) {
-        // ---------------------------------------------------- loader
-        // lane i: box i of a sub-tile (block, column block; K, then V)
+    } else if (warp >= LOAD_WARP) {
+        // ---------------------------------------------------- loaders
+        // one warp for K and one for V, whose stages are let go at other times.
+        // The whole warp stays together and one elected lane issues: a box a
+        // lane took 97 us for 128 rows over 130000 keys of 8 kv heads, @@ so.
+        const bool is_v = warp > LOAD_WARP;
+        uint8_t *ring = is_v ? sV : sK;
+        const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
+        uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
         const int *tab = p.tables + (size_t)gr.row0 * p.bt_stride + (size_t)t0 * 4;
-        const int j = lane & 3, cb = (lane >> 2) % C::CB, is_v = (lane >> 2) / C::CB;
-        auto block = [&](int t) { return t < subs && j < blocks_of(t) ? __ldg(tab + t * 4 + j) : -1; };
-        int ids[4];  // of the next four sub-tiles: their latency is not in the loop
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            ids[u] = block(u);
+        const int n_blocks = (gr.shared >> 4) - t0 * 4;
+        // block ids 32 at a time, eight sub-tiles' of them, the next ones under way
+        auto fetch = [&](int chunk) { return chunk * 32 + lane < n_blocks ? __ldg(tab + chunk * 32 + lane) : 0; };
+        int ids = fetch(0), next = fetch(1);
         Place at;
-        int it = 0;
-        for (; it < subs; ++it) {
-            if (it >= (int)stages && !wait(&empty[at.st], at.ph ^ 1u))
-                break;
-            const int n = blocks_of(it);
-            int blk = ids[0];
-            ids[0] = ids[1], ids[1] = ids[2], ids[2] = ids[3];
-            ids[3] = block(it + 4);
-            if (j < n && (blk < 0 || blk >= p.num_blocks)) {
-                *bad = 1;  // not read: the group's rows become NaN
-                blk = 0;
+        int t = 0;
+        for (; t < subs; ++t) {
+            if (t > 0 && (t & 7) == 0) {
+                ids = next;
+                next = fetch((t >> 3) + 1);
             }
-            __syncwarp();
-            if (lane < 2)
-                mbar_expect_tx(lane ? &v_full[at.st] : &k_full[at.st], (uint32_t)(n * C::CB * 2048));
-            __syncwarp();
-            if (is_v < 2 && j < n)
-                tma_load_2d((is_v ? sV : sK) + at.st * C::SUB + cb * C::BLK + j * 2048, is_v ? &tm_v : &tm_k,
-                            is_v ? &v_full[at.st] : &k_full[at.st], cb * 64, (int)(((long long)blk * p.n_kv + kvh) * 16));
+            if ((t & 7) == 0 && __any_sync(0xffffffffu, ids < 0 || ids >= p.num_blocks)) {
+                *bad = 1;  // not read: the group's rows become NaN
+                ids = ids < 0 || ids >= p.num_blocks ? 0 : ids;
+            }
+            if (t >= (int)stages && !wait(&empty[at.st], at.ph ^ 1u))
+                break;
+            const int n = blocks_of(t);
+            mbar_expect_tx_elect(&full[at.st], (uint32_t)(n * C::CB * 2048));
+            uint8_t *to = ring + at.st * C::SUB;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= n)
+                    break;
+                const int row = (int)(((long long)__shfl_sync(0xffffffffu, ids, (t & 7) * 4 + j) * p.n_kv + kvh) * 16);
+#pragma unroll
+                for (int cb = 0; cb < C::CB; ++cb)
+                    tma_load_2d_elect(to + cb * C::BLK + j * 2048, tm, &full[at.st], cb * 64, row);
+            }
             at.next(stages);
         }
         // no copy may land after the CTA has ended
-        for (int i = max(0, it - (int)stages); i < it; ++i) {
-            mbar_wait(&k_full[i % (int)stages], (uint32_t)(i / (int)stages) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
-            mbar_wait(&v_full[i % (int)stages], (uint32_t)(i / (int)stages) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
-        }
-        __threadfence_block();
+        const int st = (int)stages;
+        for (int i = max(0, t - st); i < t; ++i)
+            mbar_wait(&full[i % st], (uint32_t)(i / st) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
     }
     tc_fence_before();
     __syncthreads();
