@@ -21,9 +21,20 @@ struct Group {
     int cta0, parts, part_len;
 };
 
-// One attention over a paged cache: rows that attend their own keys from
-// their group's shared ones on (hb_decode_shared), or all of them with
-// nq queries a sequence (hb_decode_weigh).
+// A pool of attention weights, and what an attention does with it.
+struct Weigh {
+    float *w;
+    int num_blocks;
+    const int *tables;
+    int stride;
+    float decay;
+};
+
+// One attention over a paged cache: of rows in groups that share prefixes
+// (hb_decode_shared; every row has a table), or of nq rows a sequence
+// (hb_decode_weigh; every sequence has a table).  Either way a part of the keys
+// may be attended for a group or a sequence at once (prefix_attention.cu), and
+// the others, its "own", row by row.
 struct Attn {
     const bf16 *k, *v;
     int num_blocks, n_kv, n_heads, group;  // group: query heads of a kv head
@@ -32,18 +43,23 @@ struct Attn {
     const int *tables;
     int bt_stride;
     const int *ctx_lens;
-    int max_ctx, nq;
+    int max_ctx, n_seqs, nq;   // n_seqs: entries of ctx_lens
     float c2;                  // log2(e) / sqrt(d): weights are 2^((s - m) c2)
     int split_len, n_splits;   // of a row's own keys
     int col_tiles;             // CTAs of the queries of a kv head
-    int first_slot, n_slots;   // partials of a row: its group's parts, then from first_slot on its own splits
-    bool beside;               // the rows' own keys run beside the prefixes' kernel, launched before
+    int first_slot, n_slots;   // partials of a row: those of the common part, then from first_slot on its own splits
+    bool direct;               // a row has one partial, which is its result
+    bool beside;               // the own keys' kernel runs beside that of the common ones, launched before
     bf16 *out;
     long long out_stride;
     float2 *part_ml;           // [row][head][slot] (m, l)
     float *part_o;             // [row][head][slot][D]
-    float *scores;             // [seq][head of the kv head's queries][score_stride], or null
+    float *scores;             // [seq][kv head][query][score_stride]
     long long score_stride;
+    float2 *final_ml;          // [row][head] (m, 1 / l, or 0 where that is not a number)
+    bool fused;                // the attention's CTAs update the weights themselves
+    Weigh weigh;
+    int seq_parts, seq_part_len;  // without groups: runs of the common keys of a sequence (0: none is common)
     int n_groups;              // 0: no groups
     const Group *groups;       // device, where they do not fit here
     Group few[INLINE_GROUPS];
@@ -62,9 +78,21 @@ struct Attn {
         }
         return at(lo);
     }
+    // A sequence's rows as a group: common are the whole blocks that all of
+    // them see.  Its context is in range.
+    __device__ __forceinline__ Group sequence(int seq, int ctx) const
+    {
+        Group g = {seq * nq, nq, 0, 0, 0, 0, seq_part_len};
+        const int all = ctx + 1 - (nq - 1);
+        if (seq_parts > 0 && all >= 16) {
+            g.shared = all & ~15;
+            g.parts = ((g.shared + 63) / 64 + seq_part_len - 1) / seq_part_len;
+        }
+        return g;
+    }
 };
 
-// The groups' shared keys, for all rows of a group at once (prefix_attention.cu).
+// The common keys, for all rows of a group or sequence at once.
 int launch_prefix(const hb_paged_pool *pool, const Attn &p, int ctas, cudaStream_t s);
 
 int check_pool(const hb_paged_pool *p);

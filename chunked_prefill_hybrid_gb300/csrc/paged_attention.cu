@@ -25,14 +25,21 @@ namespace {
 
 using namespace paged;
 
-constexpr int WARPS = 4;
+#ifndef PA_WARPS
+#define PA_WARPS 4
+#define PA_DEPTH 2
+#endif
+constexpr int WARPS = PA_WARPS;
 constexpr int JOIN_WARPS = 8;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 1;
+constexpr int OWN_UNIT = 10240;
+constexpr long long COMMON_ITEMS = 76;
+constexpr int COMMON_MIN = 16;
 constexpr int WEIGH_THREADS = 256;
-constexpr int WEIGH_KEYS = 4;        // keys of a thread of the weights' kernel
+constexpr int WEIGH_SHARES = 4;      // threads that share the queries of four keys
 constexpr float LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
@@ -105,7 +112,7 @@ struct Ring {
     static constexpr int ROW = D * 2;             // bytes of a key
     static constexpr int HALF = 16 * ROW;         // K or V of a page
     static constexpr int PAGE = 2 * HALF;
-    static constexpr int DEPTH = D == 128 ? 3 : 5;  // pages of a warp, one of them in use
+    static constexpr int DEPTH = D == 128 ? PA_DEPTH : 2 * PA_DEPTH - 1;  // pages of a warp, one of them in use
 };
 
 // Shared memory: a ring of pages for each warp, and after the key loop, in the
@@ -126,6 +133,41 @@ __device__ __forceinline__ uint32_t place(int key, int c)
     return (uint32_t)(key * Ring<D>::ROW + ((c ^ (key & 7)) << 4));
 }
 
+// a[j] += the weight of key j of four, from their scores and a query's m and 1 / l
+// (0 where that is not a number: it adds nothing).
+__device__ __forceinline__ void add_weights(float (&a)[4], float4 v, float2 ml, float c2)
+{
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        a[j] += ml.y == 0.f ? 0.f : ex2((x[j] - ml.x) * c2) * ml.y;
+}
+
+// w = decay w + a of keys key .. key + 3 (key at most ctx, a multiple of 4).
+__device__ __forceinline__ void put_weights(const Attn &p, int seq, int kvh, int ctx, int key, const float (&a)[4])
+{
+    const Weigh &w = p.weigh;
+    const int blk = __ldg(w.tables + (size_t)seq * w.stride + (key >> 4));
+    if (blk < 0 || blk >= w.num_blocks)
+        return;
+    float *to = w.w + ((size_t)blk * p.n_kv + kvh) * 16 + (key & 15);
+    if (key + 3 <= ctx - p.nq) {
+        float4 x = make_float4(a[0], a[1], a[2], a[3]);
+        if (w.decay != 0.f) {
+            const float4 old = *reinterpret_cast<const float4 *>(to);
+            x.x += w.decay * old.x, x.y += w.decay * old.y, x.z += w.decay * old.z, x.w += w.decay * old.w;
+        }
+        *reinterpret_cast<float4 *>(to) = x;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (key + j <= ctx) {
+                const bool fresh = w.decay == 0.f || key + j > ctx - p.nq;
+                to[j] = fresh ? a[j] : a[j] + w.decay * to[j];
+            }
+    }
+}
+
 // One CTA: a kv head's queries 8 NT tile.. of one sequence, and the keys of one
 // split.  The warps take its pages in turn, each with a ring and a softmax of
 // its own, and join their results in shared memory.
@@ -138,6 +180,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[WARPS][COLS], s_l[WARPS][COLS];
+    __shared__ float2 s_final[COLS];
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
@@ -167,10 +210,12 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         least = gr.prefix > 0 ? gr.prefix - 1 : 0;
         common = gr.prefix >> 4;
         row0 = gr.row0;
+    } else if (ctx >= 0 && ctx <= p.max_ctx) {
+        from = p.sequence(seq, ctx).shared;
     }
     // where a row's keys start and end is the same for all threads of the CTA
     if (ctx < least || ctx > p.max_ctx) {  // padding: zeros; outside its range: NaN
-        if (p.n_slots == 1 && split == 0)
+        if (p.direct && split == 0)
             for (int i = threadIdx.x; i < COLS * D; i += WARPS * 32) {
                 const int c = c0 + i / D;
                 if (c < ncols)
@@ -418,7 +463,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         }
         const long long row = (long long)seq * p.nq + c / p.group;
         const int head = kvh * p.group + c % p.group;
-        if (p.n_slots == 1) {
+        if (p.direct) {
             const bool none = ctx + 1 - (p.nq - 1) + c / p.group <= 0;
             const float f = none ? 0.f : 1.f / sum;
             uint2 u;
@@ -426,24 +471,46 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             h[0] = __floats2bfloat162_rn(none ? 0.f : acc.x * f, none ? 0.f : acc.y * f);
             h[1] = __floats2bfloat162_rn(none ? 0.f : acc.z * f, none ? 0.f : acc.w * f);
             *reinterpret_cast<uint2 *>(p.out + row * p.out_stride + (size_t)head * D + e) = u;
-        }
-        if (p.n_slots > 1 || SCORES) {
+        } else {
             const size_t slot = ((size_t)row * p.n_heads + head) * p.n_slots + p.first_slot + split;
             if (e == 0)
                 p.part_ml[slot] = make_float2(mx, sum);
-            if (p.n_slots > 1)
-                *reinterpret_cast<float4 *>(p.part_o + slot * D + e) = acc;
+            *reinterpret_cast<float4 *>(p.part_o + slot * D + e) = acc;
+        }
+        if (SCORES && e == 0)
+            s_final[cl] = make_float2(mx == -INFINITY ? 0.f : mx, sum > 0.f ? 1.f / sum : 0.f);
+    }
+    if (SCORES && p.fused) {  // the CTA has all keys and queries: the weights, four keys a thread
+        __syncthreads();
+        const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride;
+        for (int key = threadIdx.x * 4; key <= ctx; key += WARPS * 32 * 4) {
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+                if (c < ncols)
+                    add_weights(a, __ldcg(reinterpret_cast<const float4 *>(s + c * p.score_stride + key)), s_final[c],
+                                p.c2);
+            put_weights(p, seq, kvh, ctx, key, a);
         }
     }
     leave();
 }
 
-// The join of a row's partials, of its group's prefix and of its own splits: a
-// warp a (row, head).
-template <int D>
-__device__ __forceinline__ void join_row(const Attn &p, int row, int head, int lane)
+// The join of a row's partials, those of the common keys and of its own splits:
+// W warps a (row, head), each with every W-th partial.
+template <int D, int W>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
 {
     constexpr int E = D / 32;
+    constexpr int BATCH = 8;  // partials whose loads are under way together
+    __shared__ float s_l[JOIN_WARPS], s_o[W > 1 ? JOIN_WARPS : 1][D];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
+    const long long item = (long long)blockIdx.x * (JOIN_WARPS / W) + warp / W;
+    if (W < JOIN_WARPS && item >= (long long)n_rows * p.n_heads)
+        return;
+    const int row = (int)(item / p.n_heads), head = (int)(item % p.n_heads);
     const int seq = row / p.nq;
     const int ctx = p.ctx_lens[seq];
     int from = 0, least = 0, parts = 0;
@@ -453,130 +520,127 @@ __device__ __forceinline__ void join_row(const Attn &p, int row, int head, int l
         least = gr.prefix > 0 ? gr.prefix - 1 : 0;
         parts = gr.parts;
     }
-    const int keys = ctx + 1 - (p.nq - 1) + row % p.nq;  // that the row sees
-    float acc[E];
+    const bool in = ctx >= least && ctx <= p.max_ctx;
+    if (p.n_groups == 0 && in) {
+        const Group gr = p.sequence(seq, ctx);
+        from = gr.shared;
+        parts = gr.parts;
+    }
+    const bool sees = ctx + 1 - (p.nq - 1) + row % p.nq > 0;
+    const int n = in ? parts + (ctx + 1 - from + p.split_len - 1) / p.split_len : 0;
+    const size_t first = ((size_t)row * p.n_heads + head) * p.n_slots;
+    auto slot = [&](int i) { return first + (i < parts ? i : p.first_slot + i - parts); };
+    float mx = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        mx = fmaxf(mx, __ldcg(&p.part_ml[slot(i)]).x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         acc[e] = 0.f;
-    if (ctx < least || ctx > p.max_ctx) {
+    for (int i0 = w0; i0 < n; i0 += BATCH * W) {
+        float2 ml[BATCH];
+        float v[BATCH][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = ctx == -1 ? 0.f : nan_f();
-    } else if (keys > 0) {
-        const int own = (ctx + 1 - from + p.split_len - 1) / p.split_len;
-        const int n = parts + own;
-        const size_t base_at = ((size_t)row * p.n_heads + head) * p.n_slots;
-        auto slot = [&](int i) { return base_at + (i < parts ? i : p.first_slot + i - parts); };
-        float mx = -INFINITY;
-        for (int i = lane; i < n; i += 32)
-            mx = fmaxf(mx, __ldcg(&p.part_ml[slot(i)]).x);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        const float base = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f;
-        for (int i = 0; i < n; ++i) {
-            const float2 ml = __ldcg(&p.part_ml[slot(i)]);
-            const float f = ex2((ml.x - base) * p.c2);
-            sum += ml.y * f;
-            const float *o = p.part_o + slot(i) * D + lane * E;
-            if constexpr (E == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o));
-                acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(o));
-                acc[0] += v.x * f, acc[1] += v.y * f;
+        for (int u = 0; u < BATCH; ++u)
+            if (i0 + u * W < n) {
+                const size_t at = slot(i0 + u * W);
+                ml[u] = __ldcg(&p.part_ml[at]);
+                const float *o = p.part_o + at * D + lane * E;
+                if constexpr (E == 4)
+                    *reinterpret_cast<float4 *>(v[u]) = __ldcg(reinterpret_cast<const float4 *>(o));
+                else
+                    *reinterpret_cast<float2 *>(v[u]) = __ldcg(reinterpret_cast<const float2 *>(o));
             }
-        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            if (i0 + u * W < n) {
+                const float f = ex2((ml[u].x - base) * p.c2);
+                sum += ml[u].y * f;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] += v[u][e] * f;
+            }
+    }
+    if constexpr (W > 1) {
+        if (lane == 0)
+            s_l[warp] = sum;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            acc[e] = acc[e] / sum;
+            s_o[warp][lane * E + e] = acc[e];
+        __syncthreads();
+        if (w0 != 0)
+            return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            sum += s_l[warp + w];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] += s_o[warp + w][lane * E + e];
+        }
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e)  // padding, and a row that sees no key: zeros; outside its range: NaN
+        acc[e] = in ? (sees ? acc[e] / sum : 0.f) : ctx == -1 ? 0.f : nan_f();
     bf16 *to = p.out + (long long)row * p.out_stride + (size_t)head * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<__nv_bfloat162 *>(to + e) = __floats2bfloat162_rn(acc[e], acc[e + 1]);
+    if (p.final_ml && lane == 0)
+        p.final_ml[(size_t)row * p.n_heads + head] = make_float2(base, sum > 0.f ? 1.f / sum : 0.f);
 }
 
-template <int D>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
+// The weights of a kv head's keys, summed over its queries' scores: four keys a
+// thread, a quarter of the queries each.
+__global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_constant__ Attn p, int chunks)
 {
-    pdl_wait();
-    pdl_trigger();
-    const long long i = (long long)blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
-    if (i < (long long)n_rows * p.n_heads)
-        join_row<D>(p, (int)(i / p.n_heads), (int)(i % p.n_heads), threadIdx.x & 31);
-}
-
-struct Weigh {
-    float *w;
-    int num_blocks;
-    const int *tables;
-    int stride;
-    float decay;
-    int chunks;      // CTAs of the keys of a kv head
-};
-
-// w = decay w + sum over the kv head's queries of 2^((s - M) c2) / L.  A thread
-// has four neighbouring keys; the queries' M and 1 / L pass through shared
-// memory.
-__global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_constant__ Attn p, const Weigh w)
-{
-    __shared__ float2 ml[WEIGH_THREADS];  // M, 1 / L (0: adds nothing)
+    constexpr int QUADS = WEIGH_THREADS / WEIGH_SHARES, BATCH = 4;
+    __shared__ float4 s_a[WEIGH_SHARES - 1][QUADS];
     pdl_wait();
     pdl_trigger();
     const int seq = blockIdx.y;
-    const int kvh = blockIdx.x / w.chunks, chunk = blockIdx.x % w.chunks;
+    const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     const int ctx = p.ctx_lens[seq];
-    const int key = (chunk * WEIGH_THREADS + (int)threadIdx.x) * WEIGH_KEYS;
-    if (ctx < 0 || ctx > p.max_ctx || chunk * WEIGH_THREADS * WEIGH_KEYS > ctx)
+    if (ctx < 0 || ctx > p.max_ctx || chunk * QUADS * 4 > ctx)
         return;
-    const int ncols = p.nq * p.group;
-    const int own = (ctx + p.split_len) / p.split_len;
-    float acc[WEIGH_KEYS] = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 0; c0 < ncols; c0 += WEIGH_THREADS) {
-        const int c = c0 + threadIdx.x;
-        if (c < ncols) {
-            const size_t at = ((size_t)(seq * p.nq + c / p.group) * p.n_heads + kvh * p.group + c % p.group) * p.n_slots;
-            float mx = -INFINITY, sum = 0.f;
-            for (int s = 0; s < own; ++s)
-                mx = fmaxf(mx, __ldcg(&p.part_ml[at + s]).x);
-            const float base = mx == -INFINITY ? 0.f : mx;
-            for (int s = 0; s < own; ++s) {
-                const float2 x = __ldcg(&p.part_ml[at + s]);
-                sum += x.y * ex2((x.x - base) * p.c2);
-            }
-            ml[threadIdx.x] = make_float2(base, sum > 0.f ? 1.f / sum : 0.f);  // NaN: 0
-        }
-        __syncthreads();
-        if (key <= ctx) {
-            const float *s = p.scores + (((size_t)seq * p.n_kv + kvh) * ncols + c0) * p.score_stride + key;
-            const int n = min(WEIGH_THREADS, ncols - c0);
-            for (int i = 0; i < n; ++i, s += p.score_stride) {
-                const float2 x = ml[i];
-                if (x.y == 0.f)
-                    continue;
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(s));
-                acc[0] += ex2((v.x - x.x) * p.c2) * x.y;
-                acc[1] += ex2((v.y - x.x) * p.c2) * x.y;
-                acc[2] += ex2((v.z - x.x) * p.c2) * x.y;
-                acc[3] += ex2((v.w - x.x) * p.c2) * x.y;
-            }
-        }
-        __syncthreads();
-    }
-    if (key > ctx)
-        return;
-    const int blk = w.tables[(size_t)seq * w.stride + (key >> 4)];
-    if (blk < 0 || blk >= w.num_blocks)
-        return;
-    float *to = w.w + ((size_t)blk * p.n_kv + kvh) * 16 + (key & 15);
+    const int quad = threadIdx.x % QUADS, share = threadIdx.x / QUADS;
+    const int key = (chunk * QUADS + quad) * 4;
+    const int ncols = p.nq * p.group, each = (ncols + WEIGH_SHARES - 1) / WEIGH_SHARES;
+    const int c1 = min(ncols, (share + 1) * each);
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (key <= ctx) {
+        const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride + key;
+        const float2 *ml = p.final_ml + (size_t)seq * p.nq * p.n_heads + kvh * p.group;
+        for (int c0 = share * each; c0 < c1; c0 += BATCH) {
+            float4 v[BATCH];
+            float2 x[BATCH];
 #pragma unroll
-    for (int j = 0; j < WEIGH_KEYS; ++j)
-        if (key + j <= ctx) {
-            const bool fresh = w.decay == 0.f || key + j > ctx - p.nq;
-            to[j] = fresh ? acc[j] : w.decay * to[j] + acc[j];
+            for (int u = 0; u < BATCH; ++u)
+                if (c0 + u < c1) {
+                    const int c = c0 + u, i = c / p.group;
+                    x[u] = __ldcg(ml + (size_t)i * p.n_heads + (c - i * p.group));
+                    v[u] = __ldcg(reinterpret_cast<const float4 *>(s + c * p.score_stride));
+                }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                if (c0 + u < c1)
+                    add_weights(a, v[u], x[u], p.c2);
         }
+    }
+    if (share > 0)
+        s_a[share - 1][quad] = make_float4(a[0], a[1], a[2], a[3]);
+    __syncthreads();
+    if (share > 0 || key > ctx)
+        return;
+#pragma unroll
+    for (int i = 0; i < WEIGH_SHARES - 1; ++i) {
+        const float4 b = s_a[i][quad];
+        a[0] += b.x, a[1] += b.y, a[2] += b.z, a[3] += b.w;
+    }
+    put_weights(p, seq, kvh, ctx, key, a);
 }
 
 __global__ void k_paged_groups(Group *to, const __grid_constant__ Attn p, int first, int n)
@@ -590,10 +654,11 @@ __global__ void k_paged_groups(Group *to, const __grid_constant__ Attn p, int fi
 
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
-// Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split.
+// Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split: as many
+// as the SMs hold at once, three each.
 void plan_splits(long long base, int keys, int *len, int *n)
 {
-    const long long want = 912 / (base > 0 ? base : 1);
+    const long long want = 3 * SMS / (base > 0 ? base : 1);
     long long s = keys / SPLIT_MIN;
     s = s < want ? s : want;
     s = s < 1 ? 1 : s;
@@ -605,19 +670,19 @@ void plan_splits(long long base, int keys, int *len, int *n)
 }
 
 struct Layout {
-    long long ml, o, scores, groups, bytes;  // byte offsets of the workspace
+    long long ml, o, scores, final_ml, groups, bytes;  // byte offsets of the workspace
     long long score_stride;
 };
 
-Layout layout(long long rows, int heads, int d, int slots, int groups, bool scores, int max_ctx)
+Layout layout(long long rows, int heads, int d, int slots, bool parts, int groups, bool scores, bool finals, int max_ctx)
 {
     Layout w;
     w.ml = 0;
-    w.score_stride = scores ? round_up((long long)max_ctx + 1, 32) : 0;
-    const bool parts = slots > 1 || scores;
+    w.score_stride = scores ? round_up((long long)max_ctx + 1, 64) : 0;
     w.o = w.ml + (parts ? round_up(rows * heads * slots * 8, 256) : 0);
-    w.scores = w.o + (slots > 1 ? round_up(rows * heads * slots * d * 4, 256) : 0);
-    w.groups = w.scores + rows * heads * w.score_stride * 4;
+    w.scores = w.o + (parts ? round_up(rows * heads * slots * d * 4, 256) : 0);
+    w.final_ml = w.scores + rows * heads * w.score_stride * 4;
+    w.groups = w.final_ml + (finals ? round_up(rows * heads * 8, 256) : 0);
     w.bytes = w.groups + (groups > INLINE_GROUPS ? round_up((long long)groups * sizeof(Group), 256) : 0);
     return w;
 }
@@ -670,7 +735,9 @@ int check_attention(const hb_paged_pool *pool, const void *q, long long q_stride
 
 struct Plan {
     int nt, split_len, n_splits, col_tiles, first_slot, n_slots;
-    int ctas;  // of the prefixes' kernel
+    int ctas;  // of the common keys' kernel
+    int seq_parts, seq_part_len;
+    bool direct, fused;
     Layout at;
 };
 
@@ -739,6 +806,22 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
             else
                 lo = mid;
         }
+    // The rows' own keys run beside: a prefix's CTA has an even share of all the
+    // work at least, in units of a third of a sub-tile's time (0.27 us), in which
+    // an SM streams about 10 KB of own keys
+    long long units = 0;
+    int own = max_ctx + 1;  // of a row, by the longest prefix: the others' own keys may be far fewer than max_ctx allows
+    for (int i = 0; i < n_groups; ++i) {
+        const Group gr = shared_group(0, group_rows[i], prefix_lens[i], n_kv, d, can);
+        own = max_ctx + 1 - gr.shared < own ? max_ctx + 1 - gr.shared : own;
+    }
+    for (int i = 0; i < n_groups; ++i) {
+        const Group gr = shared_group(0, group_rows[i], prefix_lens[i], n_kv, d, can);
+        const long long cols = (long long)gr.rows * g;
+        units += (cols + 255) / 256 * n_kv * ((gr.shared + 63) / 64) * (cols > 128 ? 4 : 3);
+        units += (long long)gr.rows * n_kv * (own / 16 + 1) * (64 * d) / OWN_UNIT;
+    }
+    hi = hi > units / SMS ? hi : units / SMS;
     long long ctas = 0;
     int row = 0, parts = 0, most = 0;
     for (int i = 0; i < n_groups; ++i) {
@@ -759,11 +842,14 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     plan_splits((long long)n_rows * n_kv * pl->col_tiles, most, &pl->split_len, &pl->n_splits);
     pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
-    pl->at = layout(n_rows, n_heads, d, pl->n_slots, n_groups, false, max_ctx);
+    pl->seq_parts = pl->seq_part_len = 0;
+    pl->direct = pl->n_slots == 1;
+    pl->fused = false;
+    pl->at = layout(n_rows, n_heads, d, pl->n_slots, !pl->direct, n_groups, false, false, max_ctx);
     return HB_OK;
 }
 
-int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int max_ctx, Plan *pl)
+int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_blocks, int max_ctx, Plan *pl)
 {
     const int g = n_heads / n_kv;
     const long long cols = (long long)nq * g;
@@ -771,10 +857,28 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int max_c
         return HB_ERANGE;
     pl->nt = cols > 8 ? 2 : 1;
     pl->col_tiles = tiles_of(cols, pl->nt);
-    plan_splits(n_seqs * n_kv * pl->col_tiles, max_ctx + 1, &pl->split_len, &pl->n_splits);
-    pl->first_slot = 0;
-    pl->n_slots = pl->n_splits;
-    pl->at = layout(n_seqs * nq, n_heads, d, pl->n_slots, 0, true, max_ctx);
+    pl->ctas = pl->seq_parts = pl->seq_part_len = pl->first_slot = 0;
+    // the keys that all rows of a sequence see go to the tensor cores' kernel
+    // where they are read more than once otherwise, or split in any case
+    const long long items = n_seqs * n_kv * ((cols + 255) / 256);
+    const int subs = (max_ctx + 64) / 64;
+    if ((long long)num_blocks * n_kv * 16 <= 0x7fffffffll && subs >= COMMON_MIN &&
+        (pl->col_tiles > 1 || items < COMMON_ITEMS) && items <= 0xffff) {
+        long long parts = items < SMS ? SMS / items : 1;
+        if (parts > subs / PART_MIN)
+            parts = subs / PART_MIN;
+        pl->seq_part_len = (int)((subs + parts - 1) / parts);
+        pl->seq_parts = (subs + pl->seq_part_len - 1) / pl->seq_part_len;
+        pl->ctas = (int)(items * pl->seq_parts);
+        pl->first_slot = pl->seq_parts;
+    }
+    // what is left with them: the last rows' own positions and less than a block
+    const int own = pl->ctas > 0 && nq + 15 < max_ctx + 1 ? nq + 15 : max_ctx + 1;
+    plan_splits(n_seqs * n_kv * pl->col_tiles, own, &pl->split_len, &pl->n_splits);
+    pl->n_slots = pl->first_slot + pl->n_splits;
+    pl->fused = pl->n_slots == 1 && pl->col_tiles == 1;
+    pl->direct = pl->fused;
+    pl->at = layout(n_seqs * nq, n_heads, d, pl->n_slots, !pl->direct, 0, true, !pl->fused, max_ctx);
     return HB_OK;
 }
 
@@ -802,6 +906,10 @@ void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_strid
     p.col_tiles = pl.col_tiles;
     p.first_slot = pl.first_slot;
     p.n_slots = pl.n_slots;
+    p.direct = pl.direct;
+    p.fused = pl.fused;
+    p.seq_parts = pl.seq_parts;
+    p.seq_part_len = pl.seq_part_len;
     p.out = (bf16 *)out;
     p.out_stride = out_stride;
     char *w = (char *)workspace;
@@ -809,6 +917,19 @@ void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_strid
     p.part_o = (float *)(w + pl.at.o);
     p.scores = (float *)(w + pl.at.scores);
     p.score_stride = pl.at.score_stride;
+}
+
+int launch_join(const Attn &p, int d, int rows, cudaStream_t s)
+{
+    // all warps of a CTA for a row and head where there are few, with many partials
+    const long long items = (long long)rows * p.n_heads;
+    const bool wide = items < 4 * SMS && p.n_slots > 8;
+    const long long blocks = wide ? items : (items + JOIN_WARPS - 1) / JOIN_WARPS;
+    auto kernel = d == 128 ? (wide ? k_paged_join<128, JOIN_WARPS> : k_paged_join<128, 1>)
+                           : (wide ? k_paged_join<64, JOIN_WARPS> : k_paged_join<64, 1>);
+    return launch_kernel(true, kernel, dim3((unsigned)blocks), dim3(JOIN_WARPS * 32), 0, s, p, rows) == cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
 }
 
 int check_workspace(const void *workspace, long long bytes, long long need)
@@ -900,6 +1021,7 @@ try {
         return rc;
     cudaStream_t s = (cudaStream_t)cuda_stream;
     params(&p, pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, 1, out, out_stride, pl, workspace);
+    p.n_seqs = n_rows;
     p.n_groups = n_groups;
     if (n_groups > INLINE_GROUPS) {  // the groups go ahead into the workspace
         Group *list = (Group *)((char *)workspace + pl.at.groups);
@@ -922,13 +1044,7 @@ try {
         p.beside = true;
     }
     rc = attention<false>(p, pool->head_dim, pl.nt, n_rows, s);
-    if (rc || pl.n_slots == 1)
-        return rc;
-    const long long blocks = ((long long)n_rows * n_heads + JOIN_WARPS - 1) / JOIN_WARPS;
-    return launch_kernel(true, pool->head_dim == 128 ? k_paged_join<128> : k_paged_join<64>, dim3((unsigned)blocks),
-                         dim3(JOIN_WARPS * 32), 0, s, p, n_rows) == cudaSuccess
-               ? HB_OK
-               : HB_ECUDA;
+    return rc || pl.direct ? rc : launch_join(p, pool->head_dim, n_rows, s);
 } catch (...) {
     return HB_ENOMEM;
 }
@@ -947,8 +1063,13 @@ extern "C" long long hb_decode_weigh_workspace(int n_seqs, int n_queries, int n_
     if (n_seqs == 0)
         return 0;
     Plan pl;
-    const int rp = plan_weigh(n_seqs, n_queries, n_heads, n_kv_heads, head_dim, max_ctx, &pl);
-    return rp ? rp : pl.at.bytes;
+    // with common keys, and without as for a pool too large for them
+    const int rp = plan_weigh(n_seqs, n_queries, n_heads, n_kv_heads, head_dim, 1, max_ctx, &pl);
+    if (rp)
+        return rp;
+    const long long bytes = pl.at.bytes;
+    plan_weigh(n_seqs, n_queries, n_heads, n_kv_heads, head_dim, MAX_KEYS, max_ctx, &pl);
+    return pl.at.bytes > bytes ? pl.at.bytes : bytes;
 }
 
 extern "C" int hb_decode_weigh(const hb_paged_pool *pool, const void *q, long long q_stride,
@@ -979,27 +1100,31 @@ try {
     if (wt_stride < max_ctx / 16 + 1)
         return HB_ERANGE;
     Plan pl;
-    if ((rc = plan_weigh(n_seqs, n_queries, n_heads, pool->n_kv_heads, pool->head_dim, max_ctx, &pl)) ||
+    if ((rc = plan_weigh(n_seqs, n_queries, n_heads, pool->n_kv_heads, pool->head_dim, pool->num_blocks, max_ctx, &pl)) ||
         (rc = check_workspace(workspace, workspace_bytes, pl.at.bytes)))
         return rc;
     cudaStream_t s = (cudaStream_t)cuda_stream;
     Attn p = {};
     params(&p, pool, q, q_stride, block_tables, bt_stride, ctx_lens, n_heads, max_ctx, n_queries, out, out_stride, pl,
            workspace);
-    const int chunks = max_ctx / (WEIGH_THREADS * WEIGH_KEYS) + 1;
+    p.n_seqs = n_seqs;
+    p.weigh = Weigh{weights->data, weights->num_blocks, weight_tables, wt_stride, decay};
+    const int chunks = max_ctx / (WEIGH_THREADS / WEIGH_SHARES * 4) + 1;
     const long long gx = (long long)p.n_kv * chunks;
-    const long long jx = ((long long)rows * n_heads + JOIN_WARPS - 1) / JOIN_WARPS;
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
-    if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)))
+    if (!pl.fused)
+        p.final_ml = (float2 *)((char *)workspace + pl.at.final_ml);
+    if (pl.ctas > 0) {
+        if ((rc = launch_prefix(pool, p, pl.ctas, s)))
+            return rc;
+        p.beside = true;
+    }
+    if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)) || pl.fused ||
+        (rc = launch_join(p, pool->head_dim, rows, s)))
         return rc;
-    if (pl.n_slots > 1 &&
-        launch_kernel(true, pool->head_dim == 128 ? k_paged_join<128> : k_paged_join<64>, dim3((unsigned)jx),
-                      dim3(JOIN_WARPS * 32), 0, s, p, rows) != cudaSuccess)
-        return HB_ECUDA;
-    const Weigh w = {weights->data, weights->num_blocks, weight_tables, wt_stride, decay, chunks};
-    return launch_kernel(true, k_paged_weigh, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WEIGH_THREADS), 0, s, p, w) ==
-                   cudaSuccess
+    return launch_kernel(true, k_paged_weigh, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WEIGH_THREADS), 0, s, p,
+                         chunks) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
 } catch (...) {

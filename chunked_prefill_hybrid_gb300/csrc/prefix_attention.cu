@@ -127,6 +127,14 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 
+// 32 bytes, a whole sector.
+__device__ __forceinline__ void store8(float *to, float a, float b, float c, float d, float e, float f, float g, float h)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(a), "f"(b), "f"(c), "f"(d),
+                 "f"(e), "f"(f), "f"(g), "f"(h)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A place in a ring of n stages: the stage, and the parity of its full barrier.
@@ -141,7 +149,7 @@ struct Place {
     }
 };
 
-template <int D>
+template <int D, bool SCORES>
 __global__ void __launch_bounds__(THREADS, 1)
     k_prefix_attention(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ Attn p)
@@ -160,12 +168,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-    // ---- this CTA's group, kv head, rows and keys
-    if (p.groups)
-        pdl_wait();  // a kernel before this one puts them there
-    int gi = 0;
-    {
-        int hi = p.n_groups - 1;  // the last group that starts at or before this CTA
+    // ---- this CTA's group (or sequence), kv head, rows and keys
+    Group gr;
+    int local, table;
+    if (SCORES) {
+        pdl_wait();
+        const int each = (int)gridDim.x / p.n_seqs;
+        table = (int)blockIdx.x / each;
+        local = (int)blockIdx.x % each;
+        const int ctx = p.ctx_lens[table];
+        gr = p.sequence(table, ctx < 0 || ctx > p.max_ctx ? -1 : ctx);
+        if (local % p.seq_parts >= gr.parts) {
+            pdl_trigger();
+            return;  // the join knows how many parts a sequence has
+        }
+    } else {
+        if (p.groups)
+            pdl_wait();  // a kernel before this one puts them there
+        int gi = 0, hi = p.n_groups - 1;  // the last group that starts at or before this CTA
         while (gi < hi) {
             const int mid = (gi + hi + 1) >> 1;
             if (p.at(mid).cta0 <= (int)blockIdx.x)
@@ -173,10 +193,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             else
                 hi = mid - 1;
         }
+        gr = p.at(gi);
+        local = (int)blockIdx.x - gr.cta0;
+        table = gr.row0;
     }
-    const Group gr = p.at(gi);
-    const int local = (int)blockIdx.x - gr.cta0;
-    const int part = local % gr.parts, kvh = local / gr.parts % p.n_kv, tile = local / gr.parts / p.n_kv;
+    const int parts = SCORES ? p.seq_parts : gr.parts;
+    const int part = local % parts, kvh = local / parts % p.n_kv, tile = local / parts / p.n_kv;
     const int c0 = tile * 256, cols = min(256, gr.rows * p.group - c0);
     const bool dual = cols <= 128;
     const uint32_t stages = dual ? C::STAGES_DUAL : C::STAGES;
@@ -261,6 +283,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool idle = (warp & 3) * 32 >= valid;  // no row in this warp
         float m = LOWEST, l = 0.f;
         float raise_at = LOWEST;  // a maximum above it moves m
+        float *score_at = nullptr;
+        if (SCORES)
+            score_at = p.scores + (((size_t)table * p.n_kv + kvh) * (gr.rows * p.group) + c0 + (dual ? 0 : half * 128) + r) *
+                                      p.score_stride;
 #pragma unroll 1
         for (int i = 0; i < own; ++i) {
             const uint32_t buf = i & 1u;
@@ -277,7 +303,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld_x32(sT + buf * 64, v[0]);
             tmem_ld_x32(sT + buf * 64 + 32, v[1]);
             tmem_ld_wait();
-            const int n = blocks_of(dual ? 2 * i + half : i);
+            const int t = dual ? 2 * i + half : i, n = blocks_of(t);
+            if (SCORES) {
+                float *to = score_at + (size_t)(t0 + t) * 64;
+                if (r < valid)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (2 * k < n)
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                if (j < 16 || 2 * k + 1 < n)
+                                    store8(to + 32 * k + j, v[k][j], v[k][j + 1], v[k][j + 2], v[k][j + 3], v[k][j + 4],
+                                           v[k][j + 5], v[k][j + 6], v[k][j + 7]);
+            }
             if (n < 4)  // the prefix's last blocks
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -416,11 +454,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (r < valid)
 #pragma unroll
                     for (int j = 0; j < 16; j += 8)
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                         p.part_o + slot * D + e + j),
-                                     "r"(x[j]), "r"(x[j + 1]), "r"(x[j + 2]), "r"(x[j + 3]), "r"(x[j + 4]),
-                                     "r"(x[j + 5]), "r"(x[j + 6]), "r"(x[j + 7])
-                                     : "memory");
+                        store8(p.part_o + slot * D + e + j, __uint_as_float(x[j]), __uint_as_float(x[j + 1]),
+                               __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]), __uint_as_float(x[j + 4]),
+                               __uint_as_float(x[j + 5]), __uint_as_float(x[j + 6]), __uint_as_float(x[j + 7]));
                 __syncwarp();
             }
         }
@@ -501,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t *ring = is_v ? sV : sK;
         const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
         uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-        const int *tab = p.tables + (size_t)gr.row0 * p.bt_stride + (size_t)t0 * 4;
+        const int *tab = p.tables + (size_t)table * p.bt_stride + (size_t)t0 * 4;
         const int n_blocks = (gr.shared >> 4) - t0 * 4;
         // block ids 32 at a time, eight sub-tiles' of them, the next ones under way
         auto fetch = [&](int chunk) { return chunk * 32 + lane < n_blocks ? __ldg(tab + chunk * 32 + lane) : 0; };
@@ -552,15 +588,16 @@ namespace paged {
 
 int launch_prefix(const hb_paged_pool *pool, const Attn &p, int ctas, cudaStream_t s)
 {
-    static std::atomic<uint64_t> done[2];
+    static std::atomic<uint64_t> done[4];
     CUtensorMap k, v;
     if (!make_tmap_kv_pool(&k, pool->k, pool->num_blocks, pool->n_kv_heads, pool->head_dim) ||
         !make_tmap_kv_pool(&v, pool->v, pool->num_blocks, pool->n_kv_heads, pool->head_dim))
         return HB_ECUDA;
-    const bool wide = pool->head_dim == 128;
-    auto kernel = wide ? k_prefix_attention<128> : k_prefix_attention<64>;
+    const bool wide = pool->head_dim == 128, scores = p.n_groups == 0;
+    auto kernel = scores ? (wide ? k_prefix_attention<128, true> : k_prefix_attention<64, true>)
+                         : (wide ? k_prefix_attention<128, false> : k_prefix_attention<64, false>);
     const int smem = wide ? Px<128>::BYTES : Px<64>::BYTES;
-    if (kv4_allow_smem((const void *)kernel, smem, done[wide]) != cudaSuccess)
+    if (kv4_allow_smem((const void *)kernel, smem, done[2 * scores + wide]) != cudaSuccess)
         return HB_ECUDA;
     return launch_kernel(true, kernel, dim3((unsigned)ctas), dim3(THREADS), smem, s, k, v, p) == cudaSuccess ? HB_OK
                                                                                                              : HB_ECUDA;
