@@ -35,7 +35,7 @@ constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 1;
-constexpr int OWN_UNIT = 10240;
+constexpr int OWN_UNIT = 20480;
 constexpr long long COMMON_ITEMS = 76;
 constexpr int COMMON_MIN = 16;
 constexpr int WEIGH_THREADS = 256;

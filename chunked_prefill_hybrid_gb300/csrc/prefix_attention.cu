@@ -9,12 +9,12 @@
 // keys; the join of the rows' partials follows with their own keys
 // (paged_attention.cu).
 //
-//   warps 0..7   softmax, one thread a row: S from tensor memory, P back over
+//   warps 0..15  softmax, two threads a row: S from tensor memory, P back over
 //                it in two bf16 terms (16 significant bits, as in
 //                paged_attention.cu); O is rescaled only when a maximum has
 //                risen by more than 2^8
-//   warps 8, 9   issue the MMAs of the two halves of 128 rows
-//   warps 10, 11 load sub-tiles of 64 keys of K and of V by TMA, a box per block
+//   warps 16, 17 issue the MMAs of the two halves of 128 rows
+//   warps 18, 19 load sub-tiles of 64 keys of K and of V by TMA, a box per block
 //                and 64 channels
 //
 // Two halves keep the tensor pipe busy: while one is in the softmax the other's
@@ -46,8 +46,8 @@ using kv4::fma_f2;
 using kv4::pack_f2;
 using kv4::unpack_f2;
 
-constexpr int MMA_WARP = 8, LOAD_WARP = 10;
-constexpr int THREADS = 12 * 32;
+constexpr int MMA_WARP = 16, LOAD_WARP = 18;
+constexpr int THREADS = 20 * 32;
 constexpr float LOWEST = -3e38f;         // below every score, and finite: differences with it are too
 constexpr float RAISE = 8.f;             // in powers of two: how far a score may pass the maximum used
 constexpr float HUGE_SCORE = 1 << 20;    // up to it s c2 - m c2 may be fused: m c2 is rounded by 2^-4 at most, for all P alike
@@ -60,11 +60,12 @@ struct Px {
     static constexpr int TILE = CB * QBLK;
     static constexpr int BLK = 64 * 128;            // the same of a 64-key sub-tile
     static constexpr int SUB = CB * BLK;            // K or V of a sub-tile
-    static constexpr int STAGES = D == 128 ? 5 : 8, STAGES_DUAL = D == 128 ? 6 : 10;
-    static constexpr int BAR = (2 * TILE + 2 * STAGES * SUB) > (TILE + 2 * STAGES_DUAL * SUB)
-                                   ? 2 * TILE + 2 * STAGES * SUB
-                                   : TILE + 2 * STAGES_DUAL * SUB;
-    static constexpr int BYTES = BAR + 512 + 1024;  // barriers, alignment
+    // of V, one more than of K, which is let go earlier
+    static constexpr int STAGES = D == 128 ? 5 : 10, STAGES_DUAL = D == 128 ? 6 : 11;
+    static constexpr int BAR = (2 * TILE + (2 * STAGES - 1) * SUB) > (TILE + (2 * STAGES_DUAL - 1) * SUB)
+                                   ? 2 * TILE + (2 * STAGES - 1) * SUB
+                                   : TILE + (2 * STAGES_DUAL - 1) * SUB;
+    static constexpr int BYTES = BAR + 512 + 4096 + 1024;  // barriers, maxima, alignment
     static_assert(BYTES <= 227 * 1024);
     static constexpr uint32_t O0 = 256;             // S: 64 columns for each (half, buffer); then O of the halves
 };
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad = abort_flag + 1;  // a block outside the pool was met
     static_assert((4 * MOST + 15) * 8 + 12 <= 512);
+    float *s_max = (float *)(smem + C::BAR + 512);  // [buffer][half][sub][128]
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -201,10 +203,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int part = local % parts, kvh = local / parts % p.n_kv, tile = local / parts / p.n_kv;
     const int c0 = tile * 256, cols = min(256, gr.rows * p.group - c0);
     const bool dual = cols <= 128;
-    const uint32_t stages = dual ? C::STAGES_DUAL : C::STAGES;
+    const uint32_t stages = dual ? C::STAGES_DUAL : C::STAGES;  // of V
     const int t0 = part * gr.part_len, subs = min((gr.shared + 63) / 64, t0 + gr.part_len) - t0;
     auto blocks_of = [&](int t) { return min(4, (gr.shared >> 4) - (t0 + t) * 4); };  // of sub-tile t
-    uint8_t *sK = smem + (dual ? C::TILE : 2 * C::TILE), *sV = sK + stages * C::SUB;
+    uint8_t *sK = smem + (dual ? C::TILE : 2 * C::TILE), *sV = sK + (stages - 1) * C::SUB;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < (int)stages; ++i) {
@@ -215,10 +217,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], 8);
             mbar_init(&pv_done[i], 1);
         }
-        mbar_init(q_full, 8);
+        mbar_init(q_full, 16);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         *abort_flag = 0;
@@ -258,10 +260,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         return ok;
     };
 
-    if (warp < 8) {
+    if (warp < MMA_WARP) {
         // -------------------------------------------------------- softmax
         // Q: the CTA's rows of (row, head) pairs, zeros past the last
-        for (int i = threadIdx.x; i < (dual ? 1 : 2) * 128 * (D / 8); i += 256) {
+        for (int i = threadIdx.x; i < (dual ? 1 : 2) * 128 * (D / 8); i += MMA_WARP * 32) {
             const int r = i / (D / 8), ch = i % (D / 8), c = c0 + r;
             uint4 v = make_uint4(0, 0, 0, 0);
             if (r < cols)
@@ -275,18 +277,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0)
             mbar_arrive(q_full);
 
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        // two threads a row, each with 32 of a sub-tile's 64 keys
+        const int half = warp >> 3, sub = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t sT = lanes + half * 128, oT = lanes + C::O0 + half * D;
         const int own = dual ? (subs + 1 - half) / 2 : subs;  // sub-tiles of this half
         const int valid = min(128, cols - (dual ? 0 : half * 128));
         const bool idle = (warp & 3) * 32 >= valid;  // no row in this warp
+        float *my_max = s_max + (half * 2 + sub) * 128 + r, *its_max = s_max + (half * 2 + (sub ^ 1)) * 128 + r;
+        auto pair_sync = [&]() {  // the two warps of 32 rows
+            asm volatile("bar.sync %0, 64;" ::"r"(2 + half * 4 + (warp & 3)) : "memory");
+        };
         float m = LOWEST, l = 0.f;
         float raise_at = LOWEST;  // a maximum above it moves m
         float *score_at = nullptr;
         if (SCORES)
             score_at = p.scores + (((size_t)table * p.n_kv + kvh) * (gr.rows * p.group) + c0 + (dual ? 0 : half * 128) + r) *
-                                      p.score_stride;
+                                      p.score_stride + sub * 32;
 #pragma unroll 1
         for (int i = 0; i < own; ++i) {
             const uint32_t buf = i & 1u;
@@ -299,36 +306,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                 continue;
             }
             tc_fence_after();
-            float v[2][32];
-            tmem_ld_x32(sT + buf * 64, v[0]);
-            tmem_ld_x32(sT + buf * 64 + 32, v[1]);
+            float v[32];
+            tmem_ld_x32(sT + buf * 64 + sub * 32, v);
             tmem_ld_wait();
-            const int t = dual ? 2 * i + half : i, n = blocks_of(t);
+            const int t = dual ? 2 * i + half : i, n = blocks_of(t) - 2 * sub;  // blocks of this thread's two
             if (SCORES) {
                 float *to = score_at + (size_t)(t0 + t) * 64;
                 if (r < valid)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (2 * k < n)
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                if (j < 16 || 2 * k + 1 < n)
-                                    store8(to + 32 * k + j, v[k][j], v[k][j + 1], v[k][j + 2], v[k][j + 3], v[k][j + 4],
-                                           v[k][j + 5], v[k][j + 6], v[k][j + 7]);
+                    for (int j = 0; j < 32; j += 8)
+                        if (j / 16 < n)
+                            store8(to + j, v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
             }
-            if (n < 4)  // the prefix's last blocks
+            if (n < 2)  // the last blocks
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[0][j] = j < n * 16 ? v[0][j] : -INFINITY;
-                    v[1][j] = 32 + j < n * 16 ? v[1][j] : -INFINITY;
-                }
+                for (int j = 0; j < 32; ++j)
+                    v[j] = j < n * 16 ? v[j] : -INFINITY;
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                x[j & 3] = fmaxf(fmaxf(x[j & 3], v[0][j]), v[1][j]);
-            const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            for (int j = 0; j < 32; j += 2)
+                x[(j >> 1) & 3] = fmaxf(fmaxf(x[(j >> 1) & 3], v[j]), v[j + 1]);
+            float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            my_max[buf * 512] = mx;
+            pair_sync();
+            mx = fmaxf(mx, its_max[buf * 512]);
             float off = -m * p.c2;  // P = 2^(s c2 + off)
-            if (__any_sync(0xffffffffu, mx > raise_at)) {
+            if (__any_sync(0xffffffffu, mx > raise_at)) {  // as the other warp finds: it has the same maxima
                 const float mn = fmaxf(m, mx), corr = ex2((m - mn) * p.c2);
                 m = mn;
                 l *= corr;
@@ -336,10 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 off = -m * p.c2;
                 if (fabsf(off) > HUGE_SCORE) {  // the difference first; and here again with every sub-tile
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        v[0][j] -= m;
-                        v[1][j] -= m;
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        v[j] -= m;
                     off = 0.f;
                     raise_at = -INFINITY;
                 }
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = sub * (D / 2); c < (sub + 1) * (D / 2); c += 16) {
                         uint32_t y[16];
                         tmem_ld_32x32b_x16(oT + c, y);
                         tmem_ld_wait();
@@ -361,29 +362,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const uint64_t c2 = pack_f2(p.c2, p.c2), off2 = pack_f2(off, off), minus = pack_f2(-1.f, -1.f);
             uint64_t sum2[2] = {0, 0};
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float a, b;
-                    unpack_f2(fma_f2(pack_f2(v[k][2 * j], v[k][2 * j + 1]), c2, off2), a, b);
-                    a = ex2(a);
-                    b = ex2(b);
-                    const uint64_t ab = pack_f2(a, b);
-                    sum2[j & 1] = add_f2(sum2[j & 1], ab);
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                    hi[j] = *reinterpret_cast<const uint32_t *>(&h);
-                    float ra, rb;
-                    unpack_f2(fma_f2(pack_f2(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xffff0000u)), minus,
-                                     ab),
-                              ra, rb);
-                    const __nv_bfloat162 q = __floats2bfloat162_rn(ra, rb);
-                    lo[j] = *reinterpret_cast<const uint32_t *>(&q);
-                }
-                tmem_st_x16(sT + buf * 64 + k * 16, hi);  // over S, which is read already
-                tmem_st_x16(sT + buf * 64 + 32 + k * 16, lo);
+            for (int j = 0; j < 16; ++j) {
+                float a, b;
+                unpack_f2(fma_f2(pack_f2(v[2 * j], v[2 * j + 1]), c2, off2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                const uint64_t ab = pack_f2(a, b);
+                sum2[j & 1] = add_f2(sum2[j & 1], ab);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+                float ra, rb;
+                unpack_f2(fma_f2(pack_f2(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xffff0000u)), minus, ab),
+                          ra, rb);
+                const __nv_bfloat162 q = __floats2bfloat162_rn(ra, rb);
+                lo[j] = *reinterpret_cast<const uint32_t *>(&q);
             }
+            // over S, which both warps have read: pair_sync() was after that
+            tmem_st_x16(sT + buf * 64 + sub * 16, hi);
+            tmem_st_x16(sT + buf * 64 + 32 + sub * 16, lo);
             float a, b;
             unpack_f2(add_f2(sum2[0], sum2[1]), a, b);
             l += a + b;
@@ -396,45 +394,52 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---- the result
         if (ok && own > 0 && wait(&pv_done[2 * half + ((own - 1) & 1)], (uint32_t)((own - 1) >> 1) & 1u))
             tc_fence_after();
-        // with both halves on the same rows, each takes half of the channels
-        // and joins the two O there: f, f2 are their factors
-        float f = 1.f, f2 = 0.f;
-        if (dual) {
-            // m and l pass through tensor memory, over this half's S: its products are done
-            float2 o;
-            asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(sT), "f"(m), "f"(l) : "memory");
-            tmem_st_wait();
-            tc_fence_before();
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            tc_fence_after();
+        // the row's other threads' m and l, through tensor memory, over this
+        // half's S: its products are done
+        float2 o[4];  // [half][sub]
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(sT + 2 * sub), "f"(m), "f"(l) : "memory");
+        tmem_st_wait();
+        tc_fence_before();
+        if (dual)
+            asm volatile("bar.sync 1, %0;" ::"n"(MMA_WARP * 32) : "memory");
+        else
+            pair_sync();
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t from = lanes + (dual ? k : half) * 128;
             asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
-                         : "=f"(o.x), "=f"(o.y)
-                         : "r"(lanes + (half ^ 1) * 128)
+                         : "=f"(o[2 * k].x), "=f"(o[2 * k].y)
+                         : "r"(from)
                          : "memory");
-            tmem_ld_wait();
-            const float M = fmaxf(m, o.x);
-            f = ex2((m - M) * p.c2);
-            f2 = ex2((o.x - M) * p.c2);
-            l = l * f + o.y * f2;
-            m = M;
-            if (half == 1) {  // f belongs to the first half's O, f2 to the second's
-                const float y = f;
-                f = f2;
-                f2 = y;
-            }
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                         : "=f"(o[2 * k + 1].x), "=f"(o[2 * k + 1].y)
+                         : "r"(from + 2)
+                         : "memory");
+        }
+        tmem_ld_wait();
+        // f, f2: factors of the two halves' O, where both are of the same rows
+        float f = 1.f, f2 = 0.f;
+        l = o[0].y + o[1].y;
+        if (dual) {
+            m = fmaxf(o[0].x, o[2].x);
+            f = ex2((o[0].x - m) * p.c2);
+            f2 = ex2((o[2].x - m) * p.c2);
+            l = l * f + (o[2].y + o[3].y) * f2;
         }
         __syncwarp();
         ok = !__any_sync(0xffffffffu, !ok || *abort_flag);
-        const int k0 = dual ? half * (D / 2) : 0, k1 = dual ? k0 + D / 2 : D;
+        const int width = dual ? D / 4 : D / 2;  // channels of this thread
+        const int e0 = (dual ? 2 * half + sub : sub) * width;
         const bool two = dual && subs > 1;  // the second half has an O
         const int c = c0 + (dual ? 0 : half * 128) + (r < valid ? r : 0);
         const size_t slot =
             ((size_t)(gr.row0 + c / p.group) * p.n_heads + kvh * p.group + c % p.group) * p.n_slots + part;
         if (!idle) {
-            if (r < valid && (!dual || half == 0))
+            if (r < valid && e0 == 0)
                 p.part_ml[slot] = make_float2(m, !ok || *bad ? __int_as_float(0x7fc00000) : l);
 #pragma unroll 1
-            for (int e = k0; e < k1; e += 16) {
+            for (int e = e0; e < e0 + width; e += 16) {
                 uint32_t x[16], y[16];
                 if (ok) {
                     tmem_ld_32x32b_x16((dual ? lanes + C::O0 : oT) + e, x);
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                dK + k.st * (C::SUB >> 4) + (j >> 2) * (C::BLK >> 4) + (j & 3) * 2, id_s, j);
             mma_commit_elect(&s_full[slot]);
             mma_commit_elect(&k_empty[k.st]);
-            k.next(stages);
+            k.next(stages - 1);
         };
         wait(q_full, 0);
 #pragma unroll 1
@@ -534,6 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The whole warp stays together and one elected lane issues: a box a
         // lane took 97 us for 128 rows over 130000 keys of 8 kv heads, @@ so.
         const bool is_v = warp > LOAD_WARP;
+        const int st = is_v ? (int)stages : (int)stages - 1;
         uint8_t *ring = is_v ? sV : sK;
         const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
         uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 *bad = 1;  // not read: the group's rows become NaN
                 ids = ids < 0 || ids >= p.num_blocks ? 0 : ids;
             }
-            if (t >= (int)stages && !wait(&empty[at.st], at.ph ^ 1u))
+            if (t >= st && !wait(&empty[at.st], at.ph ^ 1u))
                 break;
             const int n = blocks_of(t);
             mbar_expect_tx_elect(&full[at.st], (uint32_t)(n * C::CB * 2048));
@@ -567,10 +573,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int cb = 0; cb < C::CB; ++cb)
                     tma_load_2d_elect(to + cb * C::BLK + j * 2048, tm, &full[at.st], cb * 64, row);
             }
-            at.next(stages);
+            at.next(st);
         }
         // no copy may land after the CTA has ended
-        const int st = (int)stages;
         for (int i = max(0, t - st); i < t; ++i)
             mbar_wait(&full[i % st], (uint32_t)(i / st) & 1u, nullptr, ok ? WAIT_NS : WAIT_NS / 8);
     }
