@@ -39,7 +39,6 @@ constexpr int OWN_UNIT = 20480;
 constexpr long long COMMON_ITEMS = 76;
 constexpr int COMMON_MIN = 16;
 constexpr int WEIGH_THREADS = 256;
-constexpr int WEIGH_SHARES = 4;      // threads that share the queries of four keys
 constexpr float LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
@@ -143,28 +142,29 @@ __device__ __forceinline__ void add_weights(float (&a)[4], float4 v, float2 ml, 
         a[j] += ml.y == 0.f ? 0.f : ex2((x[j] - ml.x) * c2) * ml.y;
 }
 
-// w = decay w + a of keys key .. key + 3 (key at most ctx, a multiple of 4).
-__device__ __forceinline__ void put_weights(const Attn &p, int seq, int kvh, int ctx, int key, const float (&a)[4])
+// Where the weights of keys key .. key + 3 lie (key a multiple of 4), or null.
+__device__ __forceinline__ float *weights_of(const Attn &p, int seq, int kvh, int key)
 {
     const Weigh &w = p.weigh;
     const int blk = __ldg(w.tables + (size_t)seq * w.stride + (key >> 4));
-    if (blk < 0 || blk >= w.num_blocks)
-        return;
-    float *to = w.w + ((size_t)blk * p.n_kv + kvh) * 16 + (key & 15);
-    if (key + 3 <= ctx - p.nq) {
-        float4 x = make_float4(a[0], a[1], a[2], a[3]);
-        if (w.decay != 0.f) {
-            const float4 old = *reinterpret_cast<const float4 *>(to);
-            x.x += w.decay * old.x, x.y += w.decay * old.y, x.z += w.decay * old.z, x.w += w.decay * old.w;
-        }
-        *reinterpret_cast<float4 *>(to) = x;
+    return blk < 0 || blk >= w.num_blocks ? nullptr : w.w + ((size_t)blk * p.n_kv + kvh) * 16 + (key & 15);
+}
+
+// w = decay w + a there, of the keys up to ctx; the call's own rows' start from 0.
+__device__ __forceinline__ void put_weights(const Attn &p, float *to, float4 old, int ctx, int key, const float (&a)[4])
+{
+    const float decay = p.weigh.decay, o[4] = {old.x, old.y, old.z, old.w};
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        x[j] = decay == 0.f || key + j > ctx - p.nq ? a[j] : a[j] + decay * o[j];
+    if (key + 3 <= ctx) {
+        *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (key + j <= ctx) {
-                const bool fresh = w.decay == 0.f || key + j > ctx - p.nq;
-                to[j] = fresh ? a[j] : a[j] + w.decay * to[j];
-            }
+        for (int j = 0; j < 3; ++j)
+            if (key + j <= ctx)
+                to[j] = x[j];
     }
 }
 
@@ -484,13 +484,19 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         __syncthreads();
         const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride;
         for (int key = threadIdx.x * 4; key <= ctx; key += WARPS * 32 * 4) {
+            float *to = weights_of(p, seq, kvh, key);
+            if (!to)
+                continue;
+            float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.weigh.decay != 0.f)
+                old = *reinterpret_cast<const float4 *>(to);
             float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < COLS; ++c)
                 if (c < ncols)
                     add_weights(a, __ldcg(reinterpret_cast<const float4 *>(s + c * p.score_stride + key)), s_final[c],
                                 p.c2);
-            put_weights(p, seq, kvh, ctx, key, a);
+            put_weights(p, to, old, ctx, key, a);
         }
     }
     leave();
@@ -594,21 +600,32 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
 }
 
 // The weights of a kv head's keys, summed over its queries' scores: four keys a
-// thread, a quarter of the queries each.
+// thread, and SHARES threads for the queries of the same keys.
+template <int SHARES>
 __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_constant__ Attn p, int chunks)
 {
-    constexpr int QUADS = WEIGH_THREADS / WEIGH_SHARES, BATCH = 4;
-    __shared__ float4 s_a[WEIGH_SHARES - 1][QUADS];
-    pdl_wait();
-    pdl_trigger();
+    constexpr int QUADS = WEIGH_THREADS / SHARES, BATCH = 8;
+    __shared__ float4 s_a[SHARES > 1 ? SHARES - 1 : 1][QUADS];
     const int seq = blockIdx.y;
     const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+    // When this kernel starts the join has passed its wait: what was there
+    // before this call can be read, only its own results not yet
     const int ctx = p.ctx_lens[seq];
-    if (ctx < 0 || ctx > p.max_ctx || chunk * QUADS * 4 > ctx)
-        return;
     const int quad = threadIdx.x % QUADS, share = threadIdx.x / QUADS;
     const int key = (chunk * QUADS + quad) * 4;
-    const int ncols = p.nq * p.group, each = (ncols + WEIGH_SHARES - 1) / WEIGH_SHARES;
+    const bool none = ctx > p.max_ctx || chunk * QUADS * 4 > ctx;
+    float *to = nullptr;
+    float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!none && share == 0 && key <= ctx) {
+        to = weights_of(p, seq, kvh, key);
+        if (to && p.weigh.decay != 0.f)
+            old = *reinterpret_cast<const float4 *>(to);
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (none)
+        return;
+    const int ncols = p.nq * p.group, each = (ncols + SHARES - 1) / SHARES;
     const int c1 = min(ncols, (share + 1) * each);
     float a[4] = {0.f, 0.f, 0.f, 0.f};
     if (key <= ctx) {
@@ -630,17 +647,20 @@ __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_cons
                     add_weights(a, v[u], x[u], p.c2);
         }
     }
-    if (share > 0)
-        s_a[share - 1][quad] = make_float4(a[0], a[1], a[2], a[3]);
-    __syncthreads();
-    if (share > 0 || key > ctx)
-        return;
+    if constexpr (SHARES > 1) {
+        if (share > 0)
+            s_a[share - 1][quad] = make_float4(a[0], a[1], a[2], a[3]);
+        __syncthreads();
+        if (share > 0)
+            return;
 #pragma unroll
-    for (int i = 0; i < WEIGH_SHARES - 1; ++i) {
-        const float4 b = s_a[i][quad];
-        a[0] += b.x, a[1] += b.y, a[2] += b.z, a[3] += b.w;
+        for (int i = 0; i < SHARES - 1; ++i) {
+            const float4 b = s_a[i][quad];
+            a[0] += b.x, a[1] += b.y, a[2] += b.z, a[3] += b.w;
+        }
     }
-    put_weights(p, seq, kvh, ctx, key, a);
+    if (to)
+        put_weights(p, to, old, ctx, key, a);
 }
 
 __global__ void k_paged_groups(Group *to, const __grid_constant__ Attn p, int first, int n)
@@ -1109,7 +1129,8 @@ try {
            workspace);
     p.n_seqs = n_seqs;
     p.weigh = Weigh{weights->data, weights->num_blocks, weight_tables, wt_stride, decay};
-    const int chunks = max_ctx / (WEIGH_THREADS / WEIGH_SHARES * 4) + 1;
+    const bool many = n_queries * p.group > 16;  // queries of a kv head: eight threads for them
+    const int chunks = max_ctx / (WEIGH_THREADS / (many ? 8 : 1) * 4) + 1;
     const long long gx = (long long)p.n_kv * chunks;
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
@@ -1123,8 +1144,8 @@ try {
     if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)) || pl.fused ||
         (rc = launch_join(p, pool->head_dim, rows, s)))
         return rc;
-    return launch_kernel(true, k_paged_weigh, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WEIGH_THREADS), 0, s, p,
-                         chunks) == cudaSuccess
+    return launch_kernel(true, many ? k_paged_weigh<8> : k_paged_weigh<1>, dim3((unsigned)gx, (unsigned)n_seqs),
+                         dim3(WEIGH_THREADS), 0, s, p, chunks) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
 } catch (...) {
