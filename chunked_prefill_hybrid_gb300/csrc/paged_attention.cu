@@ -34,10 +34,12 @@ constexpr int JOIN_WARPS = 8;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
-constexpr long long SHARE_BYTES = 1;
+#ifndef PA_SHARE
+#define PA_SHARE 1
+#endif
+constexpr long long SHARE_BYTES = PA_SHARE;
 constexpr int OWN_UNIT = 20480;
-constexpr long long COMMON_ITEMS = 76;
-constexpr int COMMON_MIN = 16;
+constexpr int COMMON_MIN = 8;        // sub-tiles
 constexpr int WEIGH_THREADS = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -883,7 +885,7 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     const long long items = n_seqs * n_kv * ((cols + 255) / 256);
     const int subs = (max_ctx + 64) / 64;
     if ((long long)num_blocks * n_kv * 16 <= 0x7fffffffll && subs >= COMMON_MIN &&
-        (pl->col_tiles > 1 || items < COMMON_ITEMS) && items <= 0xffff) {
+        pl->col_tiles > 1 && items <= 0xffff) {
         long long parts = items < SMS ? SMS / items : 1;
         if (parts > subs / PART_MIN)
             parts = subs / PART_MIN;
