@@ -170,10 +170,11 @@ __device__ __forceinline__ void put_weights(const Attn &p, float *to, float4 old
     }
 }
 
-// One CTA: a kv head's queries 8 NT tile.. of one sequence, and the keys of one
-// split.  The warps take its pages in turn, each with a ring and a softmax of
-// its own, and join their results in shared memory.
-template <int D, int NT, bool SCORES>
+// A tile of 8 NT of a kv head's queries of one sequence, and the keys of one
+// split.  KW = WARPS: a CTA has one tile, whose warps take the pages in turn, each
+// with a ring and a softmax of its own, and join their results in shared memory.
+// KW = 1, for many queries: each warp has a tile of its own and all pages.
+template <int D, int NT, bool SCORES, int KW>
 __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_constant__ Attn p)
 {
     using R = Ring<D>;
@@ -188,7 +189,9 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     const int g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.n_splits;
     const int rest = blockIdx.x / p.n_splits;
-    const int tile = rest % p.col_tiles, kvh = rest / p.col_tiles;
+    const int tiles = (p.col_tiles * KW + WARPS - 1) / WARPS;  // CTAs for them
+    const int tile = rest % tiles * (WARPS / KW) + (KW == 1 ? warp : 0), kvh = rest / tiles;
+    const int kw = KW == 1 ? 0 : warp;  // this warp's turn among the pages
     const int seq = blockIdx.y;
     const int ncols = p.nq * p.group;
     const int c0 = tile * COLS;
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     // where a row's keys start and end is the same for all threads of the CTA
     if (ctx < least || ctx > p.max_ctx) {  // padding: zeros; outside its range: NaN
         if (p.direct && split == 0)
-            for (int i = threadIdx.x; i < COLS * D; i += WARPS * 32) {
+            for (int i = kw * 32 + lane; i < COLS * D; i += KW * 32) {
                 const int c = c0 + i / D;
                 if (c < ncols)
                     p.out[(long long)(seq * p.nq + c / p.group) * p.out_stride +
@@ -227,14 +230,14 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         return leave();
     }
     const int k0 = from + split * p.split_len, k1 = min(ctx + 1, k0 + p.split_len);
-    if (k0 >= k1)
+    if (k0 >= k1 || tile >= p.col_tiles)
         return leave();  // the join knows how many splits a row has
 
-    // ---- this warp's pages: b0 + 4 i, i < n
-    const int b0 = (k0 >> 4) + warp;
-    const int n = max(0, (((k1 + 15) >> 4) - b0 + WARPS - 1) / WARPS);
+    // ---- this warp's pages: b0 + KW i, i < n
+    const int b0 = (k0 >> 4) + kw;
+    const int n = max(0, (((k1 + 15) >> 4) - b0 + KW - 1) / KW);
     auto page_id = [&](int i) {
-        const int b = b0 + i * WARPS;
+        const int b = b0 + i * KW;
         return __ldg(p.tables + (size_t)(b < common ? row0 : seq) * p.bt_stride + b);
     };
     uint8_t *ring = smem + warp * R::DEPTH * R::PAGE;
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             const bool ok = blk >= 0 && blk < p.num_blocks;
             bad |= !ok;
             const size_t at = ((size_t)(ok ? blk : 0) * p.n_kv + kvh) * 16 * D;
-            const int left = ok ? k1 - (b0 + i * WARPS) * 16 : 0;  // keys of the page that count
+            const int left = ok ? k1 - (b0 + i * KW) * 16 : 0;  // keys of the page that count
             const uint32_t dst = ring_at + (i % R::DEPTH) * R::PAGE;
 #pragma unroll
             for (int j = 0; j < R::HALF / 512; ++j) {
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         __syncwarp();  // every lane's copies of page i are here, and page i - 1 is done with
         issue(i + R::DEPTH - 1);
         const uint32_t page = ring_at + (i % R::DEPTH) * R::PAGE;
-        const int key0 = (b0 + i * WARPS) * 16;
+        const int key0 = (b0 + i * KW) * 16;
 
         float s[NT][4];
 #pragma unroll
@@ -427,39 +430,47 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
                 s_l[warp][nt * 8 + 2 * t + j] = bad ? nan_f() : x;
             }
         }
-    __syncthreads();  // also: no warp's ring is in use any more
-    float *so = reinterpret_cast<float *>(smem);
+    auto sync = [&]() {
+        if constexpr (KW == 1)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
+    sync();  // also: no warp's ring is in use any more (KW = 1: this warp's)
+    const int first = KW == 1 ? warp : 0;  // of the warps that share the tile
+    float *so = reinterpret_cast<float *>(KW == 1 ? ring : smem);
+    static_assert(COLS * S::ROW * 4 <= R::DEPTH * R::PAGE);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int c = nt * 8 + 2 * t + j;
-            float mx = s_m[0][c];
+            float mx = s_m[first][c];
 #pragma unroll
-            for (int w = 1; w < WARPS; ++w)
+            for (int w = 1; w < KW; ++w)
                 mx = fmaxf(mx, s_m[w][c]);
-            const float f = ex2((m[nt][j] - (mx == -INFINITY ? 0.f : mx)) * p.c2);
-            float *row = so + (warp * COLS + c) * S::ROW + g;
+            const float f = KW == 1 ? 1.f : ex2((m[nt][j] - (mx == -INFINITY ? 0.f : mx)) * p.c2);
+            float *row = so + (kw * COLS + c) * S::ROW + g;
 #pragma unroll
             for (int x = 0; x < KS; ++x) {
                 row[x * 16] = o[nt][x][j] * f;
                 row[x * 16 + 8] = o[nt][x][j + 2] * f;
             }
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < COLS * (D / 4); i += WARPS * 32) {
+    sync();
+    for (int i = kw * 32 + lane; i < COLS * (D / 4); i += KW * 32) {
         const int cl = i / (D / 4), e = i % (D / 4) * 4, c = c0 + cl;
         if (c >= ncols)
             break;
-        float mx = s_m[0][cl];
+        float mx = s_m[first][cl];
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w)
+        for (int w = 1; w < KW; ++w)
             mx = fmaxf(mx, s_m[w][cl]);
         float sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            sum += s_l[w][cl] * ex2((s_m[w][cl] - (mx == -INFINITY ? 0.f : mx)) * p.c2);
+        for (int w = 0; w < KW; ++w) {
+            sum += s_l[first + w][cl] * ex2((s_m[first + w][cl] - (mx == -INFINITY ? 0.f : mx)) * p.c2);
             const float4 a = *reinterpret_cast<const float4 *>(so + (w * COLS + cl) * S::ROW + e);
             acc.x += a.x, acc.y += a.y, acc.z += a.z, acc.w += a.w;
         }
@@ -479,10 +490,15 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
                 p.part_ml[slot] = make_float2(mx, sum);
             *reinterpret_cast<float4 *>(p.part_o + slot * D + e) = acc;
         }
-        if (SCORES && e == 0)
-            s_final[cl] = make_float2(mx == -INFINITY ? 0.f : mx, sum > 0.f ? 1.f / sum : 0.f);
+        if (SCORES && p.direct && e == 0) {
+            const float2 x = make_float2(mx == -INFINITY ? 0.f : mx, sum > 0.f ? 1.f / sum : 0.f);
+            if (p.fused)
+                s_final[cl] = x;
+            else
+                p.final_ml[(size_t)row * p.n_heads + head] = x;
+        }
     }
-    if (SCORES && p.fused) {  // the CTA has all keys and queries: the weights, four keys a thread
+    if (SCORES && KW == WARPS && p.fused) {  // the CTA has all keys and queries: the weights, four keys a thread
         __syncthreads();
         const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride;
         for (int key = threadIdx.x * 4; key <= ctx; key += WARPS * 32 * 4) {
@@ -510,8 +526,8 @@ template <int D, int W>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
 {
     constexpr int E = D / 32;
-    constexpr int BATCH = 8;  // partials whose loads are under way together
-    __shared__ float s_l[JOIN_WARPS], s_o[W > 1 ? JOIN_WARPS : 1][D];
+    constexpr int BATCH = 4;  // partials whose loads are under way together
+    __shared__ float s_o[W > 1 ? JOIN_WARPS : 1][D];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
@@ -538,8 +554,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
     const int n = in ? parts + (ctx + 1 - from + p.split_len - 1) / p.split_len : 0;
     const size_t first = ((size_t)row * p.n_heads + head) * p.n_slots;
     auto slot = [&](int i) { return first + (i < parts ? i : p.first_slot + i - parts); };
-    float mx = -INFINITY;
-    for (int i = lane; i < n; i += 32)
+    // (m, l) of the first 32 partials, a lane each, and the greatest m of all
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (lane < n)
+        mine = __ldcg(&p.part_ml[slot(lane)]);
+    float mx = mine.x;
+    for (int i = lane + 32; i < n; i += 32)
         mx = fmaxf(mx, __ldcg(&p.part_ml[slot(i)]).x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1)
@@ -549,33 +569,38 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
 #pragma unroll
     for (int e = 0; e < E; ++e)
         acc[e] = 0.f;
-    for (int i0 = w0; i0 < n; i0 += BATCH * W) {
-        float2 ml[BATCH];
-        float v[BATCH][E];
+    for (int j0 = 0; j0 < n; j0 += 32) {
+        if (j0 > 0)
+            mine = j0 + lane < n ? __ldcg(&p.part_ml[slot(j0 + lane)]) : make_float2(-INFINITY, 0.f);
+        const float f = ex2((mine.x - base) * p.c2);
+        float part = j0 + lane < n ? mine.y * f : 0.f;
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            if (i0 + u * W < n) {
-                const size_t at = slot(i0 + u * W);
-                ml[u] = __ldcg(&p.part_ml[at]);
-                const float *o = p.part_o + at * D + lane * E;
-                if constexpr (E == 4)
-                    *reinterpret_cast<float4 *>(v[u]) = __ldcg(reinterpret_cast<const float4 *>(o));
-                else
-                    *reinterpret_cast<float2 *>(v[u]) = __ldcg(reinterpret_cast<const float2 *>(o));
-            }
+        for (int x = 16; x > 0; x >>= 1)
+            part += __shfl_xor_sync(0xffffffffu, part, x);
+        sum += part;
+        const int upto = min(32, n - j0);
+        for (int i0 = w0; i0 < upto; i0 += BATCH * W) {
+            float v[BATCH][E];
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            if (i0 + u * W < n) {
-                const float f = ex2((ml[u].x - base) * p.c2);
-                sum += ml[u].y * f;
+            for (int u = 0; u < BATCH; ++u)
+                if (i0 + u * W < upto) {
+                    const float *o = p.part_o + slot(j0 + i0 + u * W) * D + lane * E;
+                    if constexpr (E == 4)
+                        *reinterpret_cast<float4 *>(v[u]) = __ldcg(reinterpret_cast<const float4 *>(o));
+                    else
+                        *reinterpret_cast<float2 *>(v[u]) = __ldcg(reinterpret_cast<const float2 *>(o));
+                }
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    acc[e] += v[u][e] * f;
-            }
+            for (int u = 0; u < BATCH; ++u)
+                if (i0 + u * W < upto) {
+                    const float x = __shfl_sync(0xffffffffu, f, i0 + u * W);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        acc[e] += v[u][e] * x;
+                }
+        }
     }
     if constexpr (W > 1) {
-        if (lane == 0)
-            s_l[warp] = sum;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             s_o[warp][lane * E + e] = acc[e];
@@ -584,7 +609,6 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
             return;
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            sum += s_l[warp + w];
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 acc[e] += s_o[warp + w][lane * E + e];
@@ -610,8 +634,8 @@ __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_cons
     __shared__ float4 s_a[SHARES > 1 ? SHARES - 1 : 1][QUADS];
     const int seq = blockIdx.y;
     const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-    // When this kernel starts the join has passed its wait: what was there
-    // before this call can be read, only its own results not yet
+    // When this kernel starts the one before it has passed its wait: what was
+    // there before this call can be read, only its own results not yet
     const int ctx = p.ctx_lens[seq];
     const int quad = threadIdx.x % QUADS, share = threadIdx.x / QUADS;
     const int key = (chunk * QUADS + quad) * 4;
@@ -711,12 +735,13 @@ Layout layout(long long rows, int heads, int d, int slots, bool parts, int group
 
 int tiles_of(long long cols, int nt) { return (int)((cols + 8 * nt - 1) / (8 * nt)); }
 
-template <int D, int NT, bool SCORES>
+template <int D, int NT, bool SCORES, int KW>
 int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    auto kernel = k_paged_attention<D, NT, SCORES>;
-    const long long gx = (long long)p.n_kv * p.col_tiles * p.n_splits;  // at most the heads, or 912
+    auto kernel = k_paged_attention<D, NT, SCORES, KW>;
+    const long long tiles = ((long long)p.col_tiles * KW + WARPS - 1) / WARPS;
+    const long long gx = (long long)p.n_kv * tiles * p.n_splits;  // at most the heads and queries, or 3 SMS
     if (kv4_allow_smem((const void *)kernel, Smem<D, NT>::BYTES, done) != cudaSuccess)
         return HB_ECUDA;
     return launch_kernel(true, kernel, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WARPS * 32), Smem<D, NT>::BYTES, s,
@@ -725,12 +750,19 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
                : HB_ECUDA;
 }
 
+template <int D, bool SCORES>
+int attention_of(const Attn &p, int nt, int n_seqs, cudaStream_t s)
+{
+    if (p.col_tiles >= WARPS)
+        return nt == 1 ? launch_attention<D, 1, SCORES, 1>(p, n_seqs, s) : launch_attention<D, 2, SCORES, 1>(p, n_seqs, s);
+    return nt == 1 ? launch_attention<D, 1, SCORES, WARPS>(p, n_seqs, s)
+                   : launch_attention<D, 2, SCORES, WARPS>(p, n_seqs, s);
+}
+
 template <bool SCORES>
 int attention(const Attn &p, int d, int nt, int n_seqs, cudaStream_t s)
 {
-    if (d == 128)
-        return nt == 1 ? launch_attention<128, 1, SCORES>(p, n_seqs, s) : launch_attention<128, 2, SCORES>(p, n_seqs, s);
-    return nt == 1 ? launch_attention<64, 1, SCORES>(p, n_seqs, s) : launch_attention<64, 2, SCORES>(p, n_seqs, s);
+    return d == 128 ? attention_of<128, SCORES>(p, nt, n_seqs, s) : attention_of<64, SCORES>(p, nt, n_seqs, s);
 }
 
 // Checks that the attention calls share.  rows: of q and out.
@@ -898,8 +930,8 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     const int own = pl->ctas > 0 && nq + 15 < max_ctx + 1 ? nq + 15 : max_ctx + 1;
     plan_splits(n_seqs * n_kv * pl->col_tiles, own, &pl->split_len, &pl->n_splits);
     pl->n_slots = pl->first_slot + pl->n_splits;
-    pl->fused = pl->n_slots == 1 && pl->col_tiles == 1;
-    pl->direct = pl->fused;
+    pl->direct = pl->n_slots == 1;
+    pl->fused = pl->direct && pl->col_tiles == 1;
     pl->at = layout(n_seqs * nq, n_heads, d, pl->n_slots, !pl->direct, 0, true, !pl->fused, max_ctx);
     return HB_OK;
 }
@@ -1144,7 +1176,7 @@ try {
         p.beside = true;
     }
     if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)) || pl.fused ||
-        (rc = launch_join(p, pool->head_dim, rows, s)))
+        (!pl.direct && (rc = launch_join(p, pool->head_dim, rows, s))))
         return rc;
     return launch_kernel(true, many ? k_paged_weigh<8> : k_paged_weigh<1>, dim3((unsigned)gx, (unsigned)n_seqs),
                          dim3(WEIGH_THREADS), 0, s, p, chunks) == cudaSuccess
