@@ -263,14 +263,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp < MMA_WARP) {
         // -------------------------------------------------------- softmax
         // Q: the CTA's rows of (row, head) pairs, zeros past the last
-        for (int i = threadIdx.x; i < (dual ? 1 : 2) * 128 * (D / 8); i += MMA_WARP * 32) {
-            const int r = i / (D / 8), ch = i % (D / 8), c = c0 + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < cols)
-                v = __ldg(reinterpret_cast<const uint4 *>(p.q + (long long)(gr.row0 + c / p.group) * p.q_stride +
-                                                          (size_t)(kvh * p.group + c % p.group) * D) +
-                          ch);
-            *reinterpret_cast<uint4 *>(smem + (r >> 7) * C::TILE + (ch >> 3) * C::QBLK + swz(r & 127, ch & 7)) = v;
+        {
+            constexpr int LANES = D / 8, STEP = MMA_WARP * 32 / LANES, N = 128 / STEP;  // threads a row, rows a round
+            const int ch = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
+#pragma unroll 1
+            for (int t = 0; t < (dual ? 1 : 2); ++t) {
+                uint4 v[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int c = c0 + t * 128 + r0 + k * STEP, row = c / p.group;
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (c - c0 < cols)
+                        v[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + (long long)(gr.row0 + row) * p.q_stride +
+                                                                     (size_t)(kvh * p.group + c - row * p.group) * D) +
+                                     ch);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    *reinterpret_cast<uint4 *>(smem + t * C::TILE + (ch >> 3) * C::QBLK + swz(r0 + k * STEP, ch & 7)) = v[k];
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
