@@ -319,7 +319,12 @@ struct MoveTile {
     static constexpr int STAGES = CTAS > 1 ? 6 : 4;
     static constexpr int TOKENS = P == 4 ? 1024 : 16384 / (PIECES * P);
     static constexpr int BYTES = TOKENS * PIECES * P;
-    static constexpr int SMEM = STAGES * (BYTES + 8 * TOKENS);
+    static constexpr int LAG = CTAS > 1 ? 1 : 0, AHEAD = STAGES - 2 - LAG;  // batches loading beside the one waited for
+    // Slots are looked up for all threads' worth of batches at a time: BATCHES of
+    // them, PUT groups ahead of the one whose first batch is waited for.
+    static constexpr int BATCHES = TOKENS < MOVE_THREADS ? MOVE_THREADS / TOKENS : 1, GROUP = BATCHES * TOKENS;
+    static constexpr int PUT = (BATCHES - 1 + AHEAD) / BATCHES + 1, GROUPS = PUT + 2;
+    static constexpr int SMEM = STAGES * BYTES + 8 * GROUPS * GROUP;
 };
 
 // Rows of PIECES pieces of P bytes, one a token of one kv head: token i from
@@ -336,52 +341,52 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
 {
     using T = MoveTile<PIECES, P, CTAS>;
     constexpr int S = T::STAGES, TOKENS = T::TOKENS, PER = TOKENS * PIECES / MOVE_THREADS, ROW = PIECES * P;
-    constexpr int EACH = (TOKENS + MOVE_THREADS - 1) / MOVE_THREADS;  // tokens that a thread looks up
-    constexpr int LAG = CTAS > 1 ? 1 : 0, AHEAD = S - 2 - LAG;  // batches loading beside the one waited for
-    static_assert(PER * MOVE_THREADS == TOKENS * PIECES);
-    int *s_src = reinterpret_cast<int *>(ring + S * T::BYTES), *s_dst = s_src + S * TOKENS;  // slots; -1: not moved
+    constexpr int LAG = T::LAG, AHEAD = T::AHEAD, GB = T::BATCHES, EACH = T::GROUP / MOVE_THREADS;
+    static_assert(PER * MOVE_THREADS == TOKENS * PIECES && LAG <= GB);
+    int *s_src = reinterpret_cast<int *>(ring + S * T::BYTES), *s_dst = s_src + T::GROUPS * T::GROUP;  // -1: not moved
     const int n = (keep + TOKENS * CTAS - 1) / (TOKENS * CTAS);
     pool += (size_t)kvh * 16 * ROW;
     const size_t page = (size_t)n_kv * 16 * ROW;
-    // token of thread's look-up u in this CTA's batch b
-    auto token = [&](int b, int u) {
-        return ((long long)b * CTAS + rank) * TOKENS + u * MOVE_THREADS + (int)threadIdx.x;
+    // token of a thread's look-up u in group q of this CTA's batches
+    auto token = [&](int q, int u) {
+        const int x = u * MOVE_THREADS + (int)threadIdx.x;
+        return (((long long)q * GB + x / TOKENS) * CTAS + rank) * TOKENS + x % TOKENS;
     };
-    // the slots in two steps, a batch apart: a token's position, then its blocks
-    auto positions = [&](int b, int (&k)[EACH]) {
+    // the slots in two steps, a group apart: a token's position, then its blocks
+    auto positions = [&](int q, int (&k)[EACH]) {
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
-            const long long i = token(b, u);
-            k[u] = u * MOVE_THREADS + (int)threadIdx.x < TOKENS && i < keep ? __ldg(kept + i) : -1;
+            const long long i = token(q, u);
+            k[u] = i < keep ? __ldg(kept + i) : -1;
         }
     };
-    auto blocks = [&](int b, const int (&k)[EACH], int (&b0)[EACH], int (&b1)[EACH]) {
+    auto blocks = [&](int q, const int (&k)[EACH], int (&b0)[EACH], int (&b1)[EACH]) {
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
             const bool ok = k[u] >= 0 && (k[u] >> 4) < from_stride;
             b0[u] = ok ? __ldg(from + (k[u] >> 4)) : -1;
-            b1[u] = ok ? __ldg(to + (token(b, u) >> 4)) : -1;
+            b1[u] = ok ? __ldg(to + (token(q, u) >> 4)) : -1;
         }
     };
-    auto put = [&](int b, const int (&k)[EACH], const int (&b0)[EACH], const int (&b1)[EACH]) {
+    auto put = [&](int q, const int (&k)[EACH], const int (&b0)[EACH], const int (&b1)[EACH]) {
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
-            const int t = u * MOVE_THREADS + (int)threadIdx.x, i = (int)token(b, u);
+            const int at = q % T::GROUPS * T::GROUP + u * MOVE_THREADS + (int)threadIdx.x, i = (int)token(q, u);
             const bool ok = b0[u] >= 0 && b0[u] < num_blocks && b1[u] >= 0 && b1[u] < num_blocks &&
                             !(b0[u] == b1[u] && k[u] == i);
-            if (t < TOKENS) {
-                s_src[b % S * TOKENS + t] = ok ? b0[u] * 16 + (k[u] & 15) : -1;
-                s_dst[b % S * TOKENS + t] = ok ? b1[u] * 16 + (i & 15) : -1;
-            }
+            s_src[at] = ok ? b0[u] * 16 + (k[u] & 15) : -1;
+            s_dst[at] = ok ? b1[u] * 16 + (i & 15) : -1;
         }
     };
+    auto slots = [&](int b) { return b / GB % T::GROUPS * T::GROUP + b % GB * TOKENS; };  // of batch b
     auto load = [&](int b) {
         if (b < n) {
             const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring + b % S * T::BYTES);
+            const int *from_slot = s_src + slots(b);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
-                const int src = s_src[b % S * TOKENS + e / PIECES];
+                const int src = from_slot[e / PIECES];
                 if (src >= 0)
                     copy_async<P>(at + e * P, pool + (src >> 4) * page + (src & 15) * ROW + c * P);
             }
@@ -389,10 +394,11 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto store = [&](int b) {
+        const int *to_slot = s_dst + slots(b);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
-            const int d = s_dst[b % S * TOKENS + e / PIECES];
+            const int d = to_slot[e / PIECES];
             if (d >= 0) {
                 uint8_t *o = pool + (d >> 4) * page + (d & 15) * ROW + c * P;
                 const uint8_t *x = ring + b % S * T::BYTES + e * P;
@@ -403,21 +409,24 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
             }
         }
     };
-    // of the batch to be put next: positions and blocks; of the one after: positions
+    // of the group to be put next: positions and blocks; of the one after: positions
     int k[EACH], b0[EACH], b1[EACH], k2[EACH];
+    const int groups = (n + GB - 1) / GB;
     {
-        int ks[AHEAD + 1][EACH];
+        int ks[T::PUT][EACH];
 #pragma unroll
-        for (int b = 0; b <= AHEAD; ++b)
-            positions(b, ks[b]);
-        positions(AHEAD + 1, k);
-        positions(AHEAD + 2, k2);
+        for (int q = 0; q < T::PUT; ++q)
+            if (q < groups)
+                positions(q, ks[q]);
+        positions(T::PUT, k);
+        positions(T::PUT + 1, k2);
 #pragma unroll
-        for (int b = 0; b <= AHEAD; ++b) {
-            blocks(b, ks[b], b0, b1);
-            put(b, ks[b], b0, b1);
-        }
-        blocks(AHEAD + 1, k, b0, b1);
+        for (int q = 0; q < T::PUT; ++q)
+            if (q < groups) {
+                blocks(q, ks[q], b0, b1);
+                put(q, ks[q], b0, b1);
+            }
+        blocks(T::PUT, k, b0, b1);
     }
     __syncthreads();
 #pragma unroll
@@ -435,12 +444,15 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
             __syncthreads();  // batch b is here, all of it
         }
         load(b + AHEAD);
-        put(b + AHEAD + 1, k, b0, b1);  // the place of a batch that was stored a round ago
+        if (b % GB == 0) {
+            const int q = b / GB;
+            put(q + T::PUT, k, b0, b1);  // the place of a group that is stored
 #pragma unroll
-        for (int u = 0; u < EACH; ++u)
-            k[u] = k2[u];
-        blocks(b + AHEAD + 2, k, b0, b1);  // a round's time to come
-        positions(b + AHEAD + 3, k2);
+            for (int u = 0; u < EACH; ++u)
+                k[u] = k2[u];
+            blocks(q + T::PUT + 1, k, b0, b1);  // a group's time to come
+            positions(q + T::PUT + 2, k2);
+        }
         if (b >= LAG)
             store(b - LAG);
         __syncthreads();  // the slots put are there, and the place of the batch just stored is free
