@@ -25,19 +25,15 @@ namespace {
 
 using namespace paged;
 
-#ifndef PA_WARPS
-#define PA_WARPS 4
-#define PA_DEPTH 2
+constexpr int WARPS = 4;
+#ifndef RING_D
+#define RING_D 2
 #endif
-constexpr int WARPS = PA_WARPS;
 constexpr int JOIN_WARPS = 8;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
-#ifndef PA_SHARE
-#define PA_SHARE 1
-#endif
-constexpr long long SHARE_BYTES = PA_SHARE;
+constexpr long long SHARE_BYTES = 24 << 20;
 constexpr int OWN_UNIT = 20480;
 constexpr int COMMON_MIN = 8;        // sub-tiles
 constexpr int WEIGH_THREADS = 256;
@@ -113,7 +109,7 @@ struct Ring {
     static constexpr int ROW = D * 2;             // bytes of a key
     static constexpr int HALF = 16 * ROW;         // K or V of a page
     static constexpr int PAGE = 2 * HALF;
-    static constexpr int DEPTH = D == 128 ? PA_DEPTH : 2 * PA_DEPTH - 1;  // pages of a warp, one of them in use
+    static constexpr int DEPTH = D == 128 ? RING_D : (2 * RING_D - 1);  // pages of a warp, one of them in use
 };
 
 // Shared memory: a ring of pages for each warp, and after the key loop, in the
