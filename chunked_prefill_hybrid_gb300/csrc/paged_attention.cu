@@ -34,7 +34,12 @@ constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 24 << 20;
-constexpr int OWN_UNIT = 20480;
+// Bytes of own keys that an SM streams in a third of a sub-tile's time, halved
+// where contexts are taken to be half of max_ctx on average; more beside prefixes
+// bound by their products, which leave the memory to the others: 53.1 us so and
+// 47.5 with 30720 (1 + 7 + 56 rows, prefixes of 0, 333 and 16389), but 25.6 and
+// 27.5 (18 rows over 768 keys).
+constexpr int OWN_UNIT = 20480, OWN_UNIT_BESIDE = 30720;
 constexpr int COMMON_MIN = 8;        // sub-tiles
 constexpr int WEIGH_THREADS = 256;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -857,19 +862,21 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
                 lo = mid;
         }
     // The rows' own keys run beside: a prefix's CTA has an even share of all the
-    // work at least, in units of a third of a sub-tile's time (0.27 us), in which
-    // an SM streams about 10 KB of own keys
+    // work at least, in units of a third of a sub-tile's time (0.27 us)
     long long units = 0;
+    int own_unit = OWN_UNIT;
     int own = max_ctx + 1;  // of a row, by the longest prefix: the others' own keys may be far fewer than max_ctx allows
     for (int i = 0; i < n_groups; ++i) {
         const Group gr = shared_group(0, group_rows[i], prefix_lens[i], n_kv, d, can);
         own = max_ctx + 1 - gr.shared < own ? max_ctx + 1 - gr.shared : own;
+        if (gr.shared > 0 && (long long)gr.rows * g > 128)
+            own_unit = OWN_UNIT_BESIDE;
     }
     for (int i = 0; i < n_groups; ++i) {
         const Group gr = shared_group(0, group_rows[i], prefix_lens[i], n_kv, d, can);
         const long long cols = (long long)gr.rows * g;
         units += (cols + 255) / 256 * n_kv * ((gr.shared + 63) / 64) * (cols > 128 ? 4 : 3);
-        units += (long long)gr.rows * n_kv * (own / 16 + 1) * (64 * d) / OWN_UNIT;
+        units += (long long)gr.rows * n_kv * (own / 16 + 1) * (64 * d) / own_unit;
     }
     hi = hi > units / SMS ? hi : units / SMS;
     long long ctas = 0;
