@@ -10,22 +10,20 @@ the library refuses) or ValueError (what only the tensors show).
 from __future__ import annotations
 
 import ctypes
+import struct
+from operator import index
 from typing import Sequence
 
 import torch
 
 from . import native
-from .cache import _BF16, _I32, _check, _device, _host_pages, _int32, _page_addr, _raw_stream, _refuse, _work
+from .cache import _BF16, _I32, _check, _device, _host_pages, _int32, _raw_stream, _refuse, _work
 
-
-class _Pool(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_blocks", ctypes.c_int),
-                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
-
-
-class _Weights(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("num_blocks", ctypes.c_int), ("n_kv_heads", ctypes.c_int)]
-
+_F32 = torch.float32
+_MOST = 0x7FFFFFFF
+# hb_paged_pool and hb_weight_pool: packed bytes take a third of a ctypes structure's time
+_pack_pool = struct.Struct("@PPiii4x").pack
+_pack_weights = struct.Struct("@Pii").pack
 
 _bound = None
 
@@ -49,55 +47,61 @@ def _lib():
     return _bound
 
 
+# As in cache.py, each call looks at its tensors in one expression (most of a
+# small call's time is the host's) and says what is wrong in _refuse.  Kernels
+# launch on the current device, so a call on tensors of another one makes that
+# current first.
+
+
 class PagedPool:
     """K and V pools, bf16 tensors [num_blocks][n_kv_heads][16][head_dim], whose memory must stay where it is.
     Read-only once made."""
-    __slots__ = ("_k", "_v", "_c", "_addr", "_dev", "_kv", "_d")
+    __slots__ = ("_k", "_v", "_c", "_dev", "_kv", "_d")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         shape = k.shape
-        dev = k.get_device()
+        self._dev = dev = k.get_device()
         if (len(shape) != 4 or shape[2] != 16 or v.shape != shape or k.dtype not in _BF16 or v.dtype not in _BF16
                 or not k.is_contiguous() or not v.is_contiguous() or v.get_device() != dev):
             raise ValueError("the pools are contiguous bf16 tensors [num_blocks][n_kv_heads][16][head_dim] on one device")
-        self._kv, self._d = shape[1], shape[3]
-        self._k, self._v, self._dev = k, v, dev
-        self._c = _Pool(k.data_ptr(), v.data_ptr(), shape[0], self._kv, self._d)
-        self._addr = ctypes.addressof(self._c)
+        blocks, self._kv, _, self._d = shape
+        self._k, self._v = k, v
+        self._c = _pack_pool(k.data_ptr(), v.data_ptr(), _int32(blocks), self._kv, self._d)
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
-    num_blocks = property(lambda self: self._c.num_blocks)
+    num_blocks = property(lambda self: self._k.shape[0])
     n_kv_heads = property(lambda self: self._kv)
     head_dim = property(lambda self: self._d)
 
 
-def _weight_pool(weights, kv: int, dev: int) -> _Weights:
+def _weight_pool(weights, kv: int, dev: int) -> bytes:
     shape = weights.shape
-    if len(shape) != 3 or shape[1] != kv or shape[2] != 16 or weights.dtype != torch.float32 or not weights.is_contiguous():
+    if (len(shape) != 3 or shape[1] != kv or shape[2] != 16 or weights.dtype != _F32 or not weights.is_contiguous()
+            or dev < 0 or weights.get_device() != dev):
+        if dev < 0 or weights.get_device() != dev:
+            raise ValueError("the tensors must lie on one CUDA device")
         raise ValueError(f"weights must be a contiguous fp32 tensor [blocks][{kv}][16]")
-    if dev < 0 or weights.get_device() != dev:
-        raise ValueError("the tensors must lie on one CUDA device")
-    return _Weights(weights.data_ptr(), shape[0], kv)
+    return _pack_weights(weights.data_ptr(), _int32(shape[0]), kv)
 
 
-def _rows_ok(t, shape, d, heads, dev):
-    return (t.shape == shape and t.dtype in _BF16 and (s := t.stride())[2] == 1 and (heads == 1 or s[1] == d)
-            and t.get_device() == dev)
+def _groups(group_rows, prefix_lens):
+    r, p = _host_pages(group_rows, "group_rows"), _host_pages(prefix_lens, "prefix_lens")
+    n = len(r)
+    if n != len(p):
+        raise ValueError("group_rows and prefix_lens must have the same length")
+    return r.tobytes(), p.tobytes(), n
 
 
-def _ints_ok(t, dim, n, dev):
-    return t.dtype == _I32 and t.dim() == dim and t.shape[0] == n and t.is_contiguous() and t.get_device() == dev
+def _shared_workspace(n, heads, kv, d, max_ctx, rows, prefix, groups) -> int:
+    return _check(_lib().hb_decode_shared_workspace(n, heads, kv, d, max_ctx, rows, prefix, groups),
+                  "hb_decode_shared_workspace")
 
 
 def decode_shared_workspace(n_rows: int, n_heads: int, n_kv_heads: int, head_dim: int, max_ctx: int,
                             group_rows: Sequence[int], prefix_lens: Sequence[int]) -> int:
-    r, p = _host_pages(group_rows, "group_rows"), _host_pages(prefix_lens, "prefix_lens")
-    if len(r) != len(p):
-        raise ValueError("group_rows and prefix_lens must have the same length")
-    return _check(
-        _lib().hb_decode_shared_workspace(*map(_int32, (n_rows, n_heads, n_kv_heads, head_dim, max_ctx)), _page_addr(r),
-                                          _page_addr(p), len(r)), "hb_decode_shared_workspace")
+    return _shared_workspace(*map(_int32, (n_rows, n_heads, n_kv_heads, head_dim, max_ctx)),
+                             *_groups(group_rows, prefix_lens))
 
 
 def decode_shared(pool: PagedPool, q, block_tables, ctx_lens, max_ctx: int, group_rows: Sequence[int],
@@ -105,29 +109,34 @@ def decode_shared(pool: PagedPool, q, block_tables, ctx_lens, max_ctx: int, grou
     """hb_decode_shared: q, out [n][n_heads][head_dim] bf16; block_tables int32 [n][stride], ctx_lens int32 [n] on the
     device; group_rows, prefix_lens: host lists or int32 arrays.  workspace: a tensor of at least
     decode_shared_workspace() bytes, or None for a new one (only on the current stream)."""
-    if q.dim() != 3:
+    shape, tshape = q.shape, block_tables.shape
+    if len(shape) != 3:
         raise ValueError("q must be [n][n_heads][head_dim]")
-    n, heads, d = shape = q.shape
+    n, heads, d = shape
     dev = pool._dev
-    r, p = _host_pages(group_rows, "group_rows"), _host_pages(prefix_lens, "prefix_lens")
-    if len(r) != len(p):
-        raise ValueError("group_rows and prefix_lens must have the same length")
-    if (d != pool._d or dev < 0 or not _rows_ok(q, shape, d, heads, dev) or not _rows_ok(out, shape, d, heads, dev)
-            or not _ints_ok(block_tables, 2, n, dev) or not _ints_ok(ctx_lens, 1, n, dev)):
+    rows, prefix, groups = _groups(group_rows, prefix_lens)
+    if (d != pool._d or out.shape != shape or q.dtype not in _BF16 or out.dtype not in _BF16
+            or (qs := q.stride())[2] != 1 or (os_ := out.stride())[2] != 1
+            or (heads > 1 and (qs[1] != d or os_[1] != d)) or len(tshape) != 2 or tshape[0] != n
+            or ctx_lens.shape != tshape[:1] or block_tables.dtype != _I32 or ctx_lens.dtype != _I32
+            or not block_tables.is_contiguous() or not ctx_lens.is_contiguous() or dev < 0 or q.get_device() != dev
+            or out.get_device() != dev or block_tables.get_device() != dev or ctx_lens.get_device() != dev):
         _refuse(((q, "q", n, heads, pool._d), (out, "out", n, heads, pool._d)),
                 ((block_tables, "block_tables", 2, n), (ctx_lens, "ctx_lens", 1, n)))
+    max_ctx = index(max_ctx)
+    if tshape[1] > _MOST or n > _MOST or not -_MOST <= max_ctx <= _MOST:
+        raise native.HbError(native.HB_ERANGE, "a size does not fit 32 bits")
     if not n:
-        if len(r):
+        if groups:
             _check(native.HB_EINVAL, "hb_decode_shared")
         return
     if dev != _device():
         with torch.cuda.device(dev):
-            return decode_shared(pool, q, block_tables, ctx_lens, max_ctx, r, p, out, workspace, stream)
-    ws = _work(workspace, stream, dev, decode_shared_workspace, n, heads, pool._kv, d, max_ctx, r, p)
-    rc = _lib().hb_decode_shared(pool._addr, q.data_ptr(), q.stride(0), block_tables.data_ptr(),
-                                 _int32(block_tables.shape[1]), ctx_lens.data_ptr(), _int32(n), heads, _int32(max_ctx),
-                                 _page_addr(r), _page_addr(p), len(r), out.data_ptr(), out.stride(0), ws.data_ptr(),
-                                 ws.nbytes, _raw_stream(dev, stream))
+            return decode_shared(pool, q, block_tables, ctx_lens, max_ctx, group_rows, prefix_lens, out, workspace, stream)
+    ws = _work(workspace, stream, dev, _shared_workspace, n, heads, pool._kv, d, max_ctx, rows, prefix, groups)
+    rc = _lib().hb_decode_shared(pool._c, q.data_ptr(), qs[0], block_tables.data_ptr(), tshape[1], ctx_lens.data_ptr(), n,
+                                 heads, max_ctx, rows, prefix, groups, out.data_ptr(), os_[0], ws.data_ptr(), ws.nbytes,
+                                 _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_decode_shared")
 
@@ -144,20 +153,28 @@ def decode_weigh(pool: PagedPool, q, block_tables, ctx_lens, max_ctx: int, weigh
     """hb_decode_weigh: q, out [n * n_queries][n_heads][head_dim] bf16, n_queries rows for each of the n entries of
     ctx_lens; weights fp32 [blocks][n_kv_heads][16], updated in place; weight_tables int32 [n][stride].  workspace: as
     for decode_shared, of decode_weigh_workspace() bytes."""
-    if q.dim() != 3:
+    shape, tshape, wshape = q.shape, block_tables.shape, weight_tables.shape
+    if len(shape) != 3:
         raise ValueError("q must be [n * n_queries][n_heads][head_dim]")
-    rows, heads, d = shape = q.shape
+    rows, heads, d = shape
     dev, n = pool._dev, ctx_lens.numel()
     nq = rows // n if n else 1
     if rows != n * nq or (n and not rows):
         raise ValueError(f"q must have a multiple of {n} rows, not {rows}")
-    if (d != pool._d or dev < 0 or not _rows_ok(q, shape, d, heads, dev) or not _rows_ok(out, shape, d, heads, dev)
-            or not _ints_ok(block_tables, 2, n, dev) or not _ints_ok(ctx_lens, 1, n, dev)
-            or not _ints_ok(weight_tables, 2, n, dev)):
+    if (d != pool._d or out.shape != shape or q.dtype not in _BF16 or out.dtype not in _BF16
+            or (qs := q.stride())[2] != 1 or (os_ := out.stride())[2] != 1
+            or (heads > 1 and (qs[1] != d or os_[1] != d)) or len(tshape) != 2 or tshape[0] != n or len(wshape) != 2
+            or wshape[0] != n or ctx_lens.dim() != 1 or block_tables.dtype != _I32 or ctx_lens.dtype != _I32
+            or weight_tables.dtype != _I32 or not block_tables.is_contiguous() or not ctx_lens.is_contiguous()
+            or not weight_tables.is_contiguous() or dev < 0 or q.get_device() != dev or out.get_device() != dev
+            or block_tables.get_device() != dev or ctx_lens.get_device() != dev or weight_tables.get_device() != dev):
         _refuse(((q, "q", rows, heads, pool._d), (out, "out", rows, heads, pool._d)),
                 ((block_tables, "block_tables", 2, n), (ctx_lens, "ctx_lens", 1, n),
                  (weight_tables, "weight_tables", 2, n)))
     w = _weight_pool(weights, pool._kv, dev)
+    max_ctx = index(max_ctx)
+    if tshape[1] > _MOST or wshape[1] > _MOST or rows > _MOST or not -_MOST <= max_ctx <= _MOST:
+        raise native.HbError(native.HB_ERANGE, "a size does not fit 32 bits")
     if not n:
         return
     if dev != _device():
@@ -165,11 +182,9 @@ def decode_weigh(pool: PagedPool, q, block_tables, ctx_lens, max_ctx: int, weigh
             return decode_weigh(pool, q, block_tables, ctx_lens, max_ctx, weights, weight_tables, decay, out, workspace,
                                 stream)
     ws = _work(workspace, stream, dev, decode_weigh_workspace, n, nq, heads, pool._kv, d, max_ctx)
-    rc = _lib().hb_decode_weigh(pool._addr, q.data_ptr(), q.stride(0), block_tables.data_ptr(),
-                                _int32(block_tables.shape[1]), ctx_lens.data_ptr(), _int32(n), _int32(nq), heads,
-                                _int32(max_ctx), ctypes.addressof(w), weight_tables.data_ptr(),
-                                _int32(weight_tables.shape[1]), decay, out.data_ptr(), out.stride(0), ws.data_ptr(),
-                                ws.nbytes, _raw_stream(dev, stream))
+    rc = _lib().hb_decode_weigh(pool._c, q.data_ptr(), qs[0], block_tables.data_ptr(), tshape[1], ctx_lens.data_ptr(), n,
+                                nq, heads, max_ctx, w, weight_tables.data_ptr(), wshape[1], decay, out.data_ptr(),
+                                os_[0], ws.data_ptr(), ws.nbytes, _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_decode_weigh")
 
@@ -177,20 +192,22 @@ def decode_weigh(pool: PagedPool, q, block_tables, ctx_lens, max_ctx: int, weigh
 def evict_select(weights, weight_tables, lens, max_len: int, keep: int, n_first: int, n_recent: int, kept, stream=None):
     """hb_evict_select: weights fp32 [blocks][n_kv_heads][16]; weight_tables int32 [n][stride], lens int32 [n] on the
     device; kept int32 [n][n_kv_heads][keep] receives the positions that stay, ascending, then -1."""
-    if weights.dim() != 3:
-        raise ValueError("weights must be [blocks][n_kv_heads][16]")
-    dev, kv, n = weights.get_device(), weights.shape[1], lens.numel()
-    w = _weight_pool(weights, kv, dev)
-    if not _ints_ok(weight_tables, 2, n, dev) or not _ints_ok(lens, 1, n, dev) or not _ints_ok(kept, 3, n, dev):
+    shape, tshape, kshape = weights.shape, weight_tables.shape, kept.shape
+    dev, n = weights.get_device(), lens.numel()
+    w = _weight_pool(weights, shape[1] if len(shape) == 3 else 0, dev)
+    if (len(tshape) != 2 or tshape[0] != n or lens.dim() != 1 or len(kshape) != 3 or kshape[0] != n
+            or weight_tables.dtype != _I32 or lens.dtype != _I32 or kept.dtype != _I32
+            or not weight_tables.is_contiguous() or not lens.is_contiguous() or not kept.is_contiguous()
+            or weight_tables.get_device() != dev or lens.get_device() != dev or kept.get_device() != dev):
         _refuse((), ((weight_tables, "weight_tables", 2, n), (lens, "lens", 1, n), (kept, "kept", 3, n)))
-    if kept.shape != (n, kv, keep):
-        raise ValueError(f"kept must be [{n}][{kv}][{keep}], not {list(kept.shape)}")
+    if kshape[1] != shape[1] or kshape[2] != keep:
+        raise ValueError(f"kept must be [{n}][{shape[1]}][{keep}], not {list(kshape)}")
     if dev != _device():
         with torch.cuda.device(dev):
             return evict_select(weights, weight_tables, lens, max_len, keep, n_first, n_recent, kept, stream)
-    rc = _lib().hb_evict_select(ctypes.addressof(w), weight_tables.data_ptr(), _int32(weight_tables.shape[1]),
-                                lens.data_ptr(), _int32(n), _int32(max_len), _int32(keep), _int32(n_first),
-                                _int32(n_recent), kept.data_ptr(), _raw_stream(dev, stream))
+    rc = _lib().hb_evict_select(w, weight_tables.data_ptr(), _int32(tshape[1]), lens.data_ptr(), _int32(n),
+                                _int32(max_len), _int32(keep), _int32(n_first), _int32(n_recent), kept.data_ptr(),
+                                _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_evict_select")
 
@@ -201,27 +218,36 @@ def evict_move(pool: PagedPool, block_tables, new_tables, kept, weights=None, we
     block_tables.  Tables int32 [n][stride], kept int32 [n][n_kv_heads][keep] on the device, as evict_select writes
     it."""
     dev, kv = pool._dev, pool._kv
-    if kept.dim() != 3 or kept.shape[1] != kv:
+    kshape, fshape, tshape = kept.shape, block_tables.shape, new_tables.shape
+    if len(kshape) != 3 or kshape[1] != kv:
         raise ValueError(f"kept must be [n][{kv}][keep]")
-    n, _, keep = kept.shape
-    if dev < 0 or not _ints_ok(kept, 3, n, dev) or not _ints_ok(block_tables, 2, n, dev) or not _ints_ok(new_tables, 2, n, dev):
+    n, _, keep = kshape
+    if (len(fshape) != 2 or fshape[0] != n or len(tshape) != 2 or tshape[0] != n or kept.dtype != _I32
+            or block_tables.dtype != _I32 or new_tables.dtype != _I32 or not kept.is_contiguous()
+            or not block_tables.is_contiguous() or not new_tables.is_contiguous() or dev < 0 or kept.get_device() != dev
+            or block_tables.get_device() != dev or new_tables.get_device() != dev):
         _refuse((), ((kept, "kept", 3, n), (block_tables, "block_tables", 2, n), (new_tables, "new_tables", 2, n)))
-    w, args = None, (None, 0, None, 0)
+    w = from_w = to_w = None
+    ws = ns = 0
     if weights is not None:
         if weight_tables is None or new_weight_tables is None:
             raise ValueError("weights are moved between weight_tables and new_weight_tables")
         w = _weight_pool(weights, kv, dev)
-        if not _ints_ok(weight_tables, 2, n, dev) or not _ints_ok(new_weight_tables, 2, n, dev):
+        wshape, nshape = weight_tables.shape, new_weight_tables.shape
+        if (len(wshape) != 2 or wshape[0] != n or len(nshape) != 2 or nshape[0] != n or weight_tables.dtype != _I32
+                or new_weight_tables.dtype != _I32 or not weight_tables.is_contiguous()
+                or not new_weight_tables.is_contiguous() or weight_tables.get_device() != dev
+                or new_weight_tables.get_device() != dev):
             _refuse((), ((weight_tables, "weight_tables", 2, n), (new_weight_tables, "new_weight_tables", 2, n)))
-        args = (weight_tables.data_ptr(), _int32(weight_tables.shape[1]), new_weight_tables.data_ptr(),
-                _int32(new_weight_tables.shape[1]))
+        from_w, ws, to_w, ns = weight_tables.data_ptr(), wshape[1], new_weight_tables.data_ptr(), nshape[1]
     elif weight_tables is not None or new_weight_tables is not None:
         raise ValueError("the tables of weights come with the weights")
+    if fshape[1] > _MOST or tshape[1] > _MOST or ws > _MOST or ns > _MOST or n > _MOST or keep > _MOST:
+        raise native.HbError(native.HB_ERANGE, "a size does not fit 32 bits")
     if dev != _device():
         with torch.cuda.device(dev):
             return evict_move(pool, block_tables, new_tables, kept, weights, weight_tables, new_weight_tables, stream)
-    rc = _lib().hb_evict_move(pool._addr, block_tables.data_ptr(), _int32(block_tables.shape[1]), new_tables.data_ptr(),
-                              _int32(new_tables.shape[1]), kept.data_ptr(), _int32(n), _int32(keep),
-                              None if w is None else ctypes.addressof(w), *args, _raw_stream(dev, stream))
+    rc = _lib().hb_evict_move(pool._c, block_tables.data_ptr(), fshape[1], new_tables.data_ptr(), tshape[1],
+                              kept.data_ptr(), n, keep, w, from_w, ws, to_w, ns, _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_evict_move")

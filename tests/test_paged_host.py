@@ -21,13 +21,13 @@ def L():
 def _pool(**over):
     a = dict(k=16, v=16, num_blocks=8, n_kv_heads=2, head_dim=128)
     a.update(over)
-    return paged._Pool(*[a[n] for n, _ in paged._Pool._fields_])
+    return paged._pack_pool(*[a[n] or 0 for n in ("k", "v", "num_blocks", "n_kv_heads", "head_dim")])
 
 
 def _weights(**over):
     a = dict(data=16, num_blocks=8, n_kv_heads=2)
     a.update(over)
-    return paged._Weights(*[a[n] for n, _ in paged._Weights._fields_])
+    return paged._pack_weights(*[a[n] or 0 for n in ("data", "num_blocks", "n_kv_heads")])
 
 
 def _ints(x):
@@ -39,7 +39,7 @@ def _shared(L, pool=None, **over):
              os=512, ws=16, wn=1 << 40)
     a.update(over)
     ng = a.get("ng", len(a["rows"]) if a["rows"] is not None else 0)
-    return L.hb_decode_shared(ctypes.byref(pool or _pool()), a["q"], a["qs"], a["bt"], a["stride"], a["ctx"], a["n"],
+    return L.hb_decode_shared(pool or _pool(), a["q"], a["qs"], a["bt"], a["stride"], a["ctx"], a["n"],
                               a["heads"], a["max_ctx"], _ints(a["rows"]), _ints(a["pre"]), ng, a["out"], a["os"],
                               a["ws"], a["wn"], None)
 
@@ -48,23 +48,23 @@ def _weigh(L, pool=None, w=None, **over):
     a = dict(q=16, qs=512, bt=16, stride=64, ctx=16, n=2, nq=2, heads=4, max_ctx=1000, wt=16, wstride=64, decay=1.0,
              out=16, os=512, ws=16, wn=1 << 40)
     a.update(over)
-    return L.hb_decode_weigh(ctypes.byref(pool or _pool()), a["q"], a["qs"], a["bt"], a["stride"], a["ctx"], a["n"],
-                             a["nq"], a["heads"], a["max_ctx"], ctypes.byref(w or _weights()), a["wt"], a["wstride"],
+    return L.hb_decode_weigh(pool or _pool(), a["q"], a["qs"], a["bt"], a["stride"], a["ctx"], a["n"],
+                             a["nq"], a["heads"], a["max_ctx"], w or _weights(), a["wt"], a["wstride"],
                              a["decay"], a["out"], a["os"], a["ws"], a["wn"], None)
 
 
 def _select(L, w=None, **over):
     a = dict(wt=16, stride=64, lens=16, n=3, max_len=1000, keep=100, first=4, recent=10, kept=16)
     a.update(over)
-    return L.hb_evict_select(ctypes.byref(w or _weights()), a["wt"], a["stride"], a["lens"], a["n"], a["max_len"],
+    return L.hb_evict_select(w or _weights(), a["wt"], a["stride"], a["lens"], a["n"], a["max_len"],
                              a["keep"], a["first"], a["recent"], a["kept"], None)
 
 
 def _move(L, pool=None, w=None, **over):
     a = dict(bt=16, stride=64, new=16, nstride=7, kept=16, n=3, keep=100, wt=16, wstride=64, nwt=16, nwstride=7)
     a.update(over)
-    return L.hb_evict_move(ctypes.byref(pool or _pool()), a["bt"], a["stride"], a["new"], a["nstride"], a["kept"], a["n"],
-                           a["keep"], None if w is None else ctypes.byref(w), a["wt"], a["wstride"], a["nwt"],
+    return L.hb_evict_move(pool or _pool(), a["bt"], a["stride"], a["new"], a["nstride"], a["kept"], a["n"],
+                           a["keep"], w, a["wt"], a["wstride"], a["nwt"],
                            a["nwstride"], None)
 
 
