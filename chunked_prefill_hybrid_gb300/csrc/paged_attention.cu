@@ -125,6 +125,7 @@ struct Smem {
     static constexpr int RINGS = WARPS * Ring<D>::DEPTH * Ring<D>::PAGE;
     static constexpr int JOIN = WARPS * 8 * NT * ROW * 4;
     static constexpr int BYTES = RINGS > JOIN ? RINGS : JOIN;
+    static constexpr int SCORES = 2048;  // numbers that follow where a CTA keeps its scores: three CTAs an SM still fit
 };
 
 // Row chunks of 16 bytes lie at c ^ (key & 7), so that eight keys' chunks are on
@@ -305,8 +306,13 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
     float *score_at = nullptr;  // of column 2t of the first tile, key g
-    if (SCORES)
-        score_at = p.scores + (((size_t)seq * p.n_kv + kvh) * ncols + c0 + 2 * t) * p.score_stride + g;
+    const bool keep = SCORES && KW == WARPS && p.fused && ncols * p.score_stride <= S::SCORES;  // scores in shared memory
+    float *scores = nullptr;
+    if (SCORES) {
+        scores = keep ? reinterpret_cast<float *>(smem + S::BYTES)
+                      : p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride;
+        score_at = scores + (size_t)(c0 + 2 * t) * p.score_stride + g;
+    }
 
     const int mi = lane >> 3;
     for (int i = 0; i < n; ++i) {
@@ -501,7 +507,6 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     }
     if (SCORES && KW == WARPS && p.fused) {  // the CTA has all keys and queries: the weights, four keys a thread
         __syncthreads();
-        const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride;
         for (int key = threadIdx.x * 4; key <= ctx; key += WARPS * 32 * 4) {
             float *to = weights_of(p, seq, kvh, key);
             if (!to)
@@ -512,9 +517,11 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < COLS; ++c)
-                if (c < ncols)
-                    add_weights(a, __ldcg(reinterpret_cast<const float4 *>(s + c * p.score_stride + key)), s_final[c],
-                                p.c2);
+                if (c < ncols) {
+                    const float *s = scores + c * p.score_stride + key;
+                    add_weights(a, keep ? *reinterpret_cast<const float4 *>(s) : __ldcg(reinterpret_cast<const float4 *>(s)),
+                                s_final[c], p.c2);
+                }
             put_weights(p, to, old, ctx, key, a);
         }
     }
@@ -743,10 +750,12 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
     auto kernel = k_paged_attention<D, NT, SCORES, KW>;
     const long long tiles = ((long long)p.col_tiles * KW + WARPS - 1) / WARPS;
     const long long gx = (long long)p.n_kv * tiles * p.n_splits;  // at most the heads and queries, or 3 SMS
-    if (kv4_allow_smem((const void *)kernel, Smem<D, NT>::BYTES, done) != cudaSuccess)
+    using S = Smem<D, NT>;
+    constexpr int most = S::BYTES + (SCORES && KW == WARPS ? 4 * S::SCORES : 0);
+    if (kv4_allow_smem((const void *)kernel, most, done) != cudaSuccess)
         return HB_ECUDA;
-    return launch_kernel(true, kernel, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WARPS * 32), Smem<D, NT>::BYTES, s,
-                         p) == cudaSuccess
+    const int smem = p.fused ? most : S::BYTES;
+    return launch_kernel(true, kernel, dim3((unsigned)gx, (unsigned)n_seqs), dim3(WARPS * 32), smem, s, p) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
 }
@@ -853,7 +862,8 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
         return n;
     };
     long long lo = 0, hi = 4ll * (MAX_KEYS / 64 + 1);
-    if (total(hi) <= SMS)
+    const long long least = total(hi);
+    if (least > 0 && least <= SMS)
         while (hi - lo > 1) {  // total(hi) fits
             const long long mid = (lo + hi) / 2;
             if (total(mid) <= SMS)
