@@ -643,43 +643,54 @@ __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_cons
     const int seq = blockIdx.y;
     const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     // When this kernel starts the one before it has passed its wait: what was
-    // there before this call can be read, only its own results not yet
+    // there before that one can be read, old weights and (where it is the join)
+    // scores; only its own results not yet
     const int ctx = p.ctx_lens[seq];
     const int quad = threadIdx.x % QUADS, share = threadIdx.x / QUADS;
     const int key = (chunk * QUADS + quad) * 4;
-    const bool none = ctx > p.max_ctx || chunk * QUADS * 4 > ctx;
+    const bool none = ctx > p.max_ctx || chunk * QUADS * 4 > ctx, some = !none && key <= ctx;
     float *to = nullptr;
     float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!none && share == 0 && key <= ctx) {
+    if (some && share == 0) {
         to = weights_of(p, seq, kvh, key);
         if (to && p.weigh.decay != 0.f)
             old = *reinterpret_cast<const float4 *>(to);
     }
+    const int ncols = p.nq * p.group, each = (ncols + SHARES - 1) / SHARES;
+    const int c1 = some ? min(ncols, (share + 1) * each) : 0;
+    const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride + key;
+    float4 v[BATCH];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            if (c0 + u < c1)
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(s + (c0 + u) * p.score_stride));
+    };
+    int c0 = share * each;
+    if (!p.direct)
+        load(c0);
     pdl_wait();
     pdl_trigger();
     if (none)
         return;
-    const int ncols = p.nq * p.group, each = (ncols + SHARES - 1) / SHARES;
-    const int c1 = min(ncols, (share + 1) * each);
+    if (p.direct)
+        load(c0);
+    const float2 *ml = p.final_ml + (size_t)seq * p.nq * p.n_heads + kvh * p.group;
     float a[4] = {0.f, 0.f, 0.f, 0.f};
-    if (key <= ctx) {
-        const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride + key;
-        const float2 *ml = p.final_ml + (size_t)seq * p.nq * p.n_heads + kvh * p.group;
-        for (int c0 = share * each; c0 < c1; c0 += BATCH) {
-            float4 v[BATCH];
-            float2 x[BATCH];
+    while (c0 < c1) {
+        float2 x[BATCH];
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u)
-                if (c0 + u < c1) {
-                    const int c = c0 + u, i = c / p.group;
-                    x[u] = __ldcg(ml + (size_t)i * p.n_heads + (c - i * p.group));
-                    v[u] = __ldcg(reinterpret_cast<const float4 *>(s + c * p.score_stride));
-                }
+        for (int u = 0; u < BATCH; ++u)
+            if (c0 + u < c1) {
+                const int c = c0 + u, i = c / p.group;
+                x[u] = __ldcg(ml + (size_t)i * p.n_heads + (c - i * p.group));
+            }
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u)
-                if (c0 + u < c1)
-                    add_weights(a, v[u], x[u], p.c2);
-        }
+        for (int u = 0; u < BATCH; ++u)
+            if (c0 + u < c1)
+                add_weights(a, v[u], x[u], p.c2);
+        c0 += BATCH;
+        load(c0);
     }
     if constexpr (SHARES > 1) {
         if (share > 0)

@@ -237,6 +237,7 @@ def _weigh(c, nq, decay, **over):
     (1, 3, 128, [6, 300, 40], 7, 0.25),       # more than eight queries, the first row of all at position 0
     (2, 2, 64, [10, 33, 700], 33, 1.0),       # queries before the start of their sequences
     (1, 5, 64, [90], 64, 0.0),                # more queries than the weights' kernel takes at once
+    (1, 8, 64, [400, 17], 1, 0.5),                  # one split, more scores than a CTA keeps
     (2, 1, 128, [1500, 1008, 16, 1023], 1, 0.5),    # long enough for the tensor cores' kernel, and not
     (1, 8, 64, [1200, -1, 1030], 20, 1.0),          # 160 queries: two tiles of Q
     (1, 4, 128, [1300, 40, 3], 70, 0.0),            # 280 queries: one CTA more, and sequences shorter than the window
