@@ -140,10 +140,12 @@ __device__ __forceinline__ uint32_t place(int key, int c)
 // (0 where that is not a number: it adds nothing).
 __device__ __forceinline__ void add_weights(float (&a)[4], float4 v, float2 ml, float c2)
 {
+    if (ml.y == 0.f)
+        return;
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        a[j] += ml.y == 0.f ? 0.f : ex2((x[j] - ml.x) * c2) * ml.y;
+        a[j] += ex2((x[j] - ml.x) * c2) * ml.y;
 }
 
 // Where the weights of keys key .. key + 3 lie (key a multiple of 4), or null.
@@ -638,7 +640,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
 template <int SHARES>
 __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_constant__ Attn p, int chunks)
 {
-    constexpr int QUADS = WEIGH_THREADS / SHARES, BATCH = 8;
+    constexpr int QUADS = WEIGH_THREADS / SHARES, BATCH = 8, CHUNK = 256;
+    __shared__ float2 s_ml[CHUNK];
     __shared__ float4 s_a[SHARES > 1 ? SHARES - 1 : 1][QUADS];
     const int seq = blockIdx.y;
     const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
@@ -656,41 +659,45 @@ __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_cons
         if (to && p.weigh.decay != 0.f)
             old = *reinterpret_cast<const float4 *>(to);
     }
-    const int ncols = p.nq * p.group, each = (ncols + SHARES - 1) / SHARES;
-    const int c1 = some ? min(ncols, (share + 1) * each) : 0;
+    // queries CHUNK at a time, an equal number for each of the shares
+    const int ncols = p.nq * p.group;
     const float *s = p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride + key;
     float4 v[BATCH];
-    auto load = [&](int c0) {
+    auto load = [&](int c0, int c1) {
+        const float *at = s + (size_t)c0 * p.score_stride;
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u)
+        for (int u = 0; u < BATCH; ++u, at += p.score_stride)
             if (c0 + u < c1)
-                v[u] = __ldcg(reinterpret_cast<const float4 *>(s + (c0 + u) * p.score_stride));
+                v[u] = __ldcg(reinterpret_cast<const float4 *>(at));
     };
-    int c0 = share * each;
-    if (!p.direct)
-        load(c0);
+    const int each0 = (min(CHUNK, ncols) + SHARES - 1) / SHARES;  // of the first chunk
+    if (!p.direct && some)
+        load(share * each0, min(min(CHUNK, ncols), (share + 1) * each0));
     pdl_wait();
     pdl_trigger();
     if (none)
         return;
-    if (p.direct)
-        load(c0);
-    const float2 *ml = p.final_ml + (size_t)seq * p.nq * p.n_heads + kvh * p.group;
     float a[4] = {0.f, 0.f, 0.f, 0.f};
-    while (c0 < c1) {
-        float2 x[BATCH];
+    for (int q0 = 0; q0 < ncols; q0 += CHUNK) {
+        const int n = min(CHUNK, ncols - q0), each = (n + SHARES - 1) / SHARES;
+        if (q0 > 0)
+            __syncthreads();  // the chunk before is done with
+        for (int c = threadIdx.x; c < n; c += WEIGH_THREADS) {
+            const int i = (q0 + c) / p.group;
+            s_ml[c] = __ldcg(p.final_ml + ((size_t)seq * p.nq + i) * p.n_heads + kvh * p.group + (q0 + c - i * p.group));
+        }
+        __syncthreads();
+        if (!some)
+            continue;
+        const int c1 = min(n, (share + 1) * each);
+        for (int c0 = share * each; c0 < c1; c0 += BATCH) {
+            if (q0 > 0 || c0 > share * each || p.direct)
+                load(q0 + c0, q0 + c1);
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            if (c0 + u < c1) {
-                const int c = c0 + u, i = c / p.group;
-                x[u] = __ldcg(ml + (size_t)i * p.n_heads + (c - i * p.group));
-            }
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u)
-            if (c0 + u < c1)
-                add_weights(a, v[u], x[u], p.c2);
-        c0 += BATCH;
-        load(c0);
+            for (int u = 0; u < BATCH; ++u)
+                if (c0 + u < c1)
+                    add_weights(a, v[u], s_ml[c0 + u], p.c2);
+        }
     }
     if constexpr (SHARES > 1) {
         if (share > 0)
