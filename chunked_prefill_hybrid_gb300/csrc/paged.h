@@ -58,6 +58,7 @@ struct Attn {
     long long score_stride;
     float2 *final_ml;          // [row][head] (m, 1 / l, or 0 where that is not a number)
     bool fused;                // the attention's CTAs update the weights themselves
+    bool lose;                 // the common keys' first CTA leaves out its first copy (hb_paged_test_lost_block)
     Weigh weigh;
     int seq_parts, seq_part_len;  // without groups: runs of the common keys of a sequence (0: none is common)
     int n_groups;              // 0: no groups

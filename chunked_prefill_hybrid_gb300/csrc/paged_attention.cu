@@ -724,6 +724,8 @@ __global__ void k_paged_groups(Group *to, const __grid_constant__ Attn p, int fi
 
 // ------------------------------------------------------------------- host
 
+thread_local bool test_lose = false;  // of this thread's next launch of the common keys' kernel
+
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
 // Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split: as many
@@ -1124,6 +1126,8 @@ try {
         p.groups = list;
     }
     if (pl.ctas > 0) {
+        p.lose = test_lose;
+        test_lose = false;
         if ((rc = launch_prefix(pool, p, pl.ctas, s)))
             return rc;
         p.beside = true;
@@ -1202,6 +1206,8 @@ try {
     if (!pl.fused)
         p.final_ml = (float2 *)((char *)workspace + pl.at.final_ml);
     if (pl.ctas > 0) {
+        p.lose = test_lose;
+        test_lose = false;
         if ((rc = launch_prefix(pool, p, pl.ctas, s)))
             return rc;
         p.beside = true;
@@ -1216,3 +1222,5 @@ try {
 } catch (...) {
     return HB_ENOMEM;
 }
+
+extern "C" void hb_paged_test_lost_block(void) { test_lose = true; }

@@ -308,8 +308,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
         for (int i = 0; i < own; ++i) {
             const uint32_t buf = i & 1u;
-            if (!wait(&s_full[2 * half + buf], (uint32_t)(i >> 1) & 1u))
-                break;
+            if (ok)
+                wait(&s_full[2 * half + buf], (uint32_t)(i >> 1) & 1u);
+            if (!ok) {  // a wait ran out: no more work, but as many barriers as the other warp of the rows
+                if (!idle)
+                    pair_sync();
+                continue;
+            }
             if (idle) {
                 __syncwarp();
                 if (lane == 0)
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (i > 0) {  // O holds the products before this one: let the last of them end
                     if (!wait(&pv_done[2 * half + (buf ^ 1u)], (uint32_t)((i - 1) >> 1) & 1u))
-                        break;
+                        continue;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = sub * (D / 2); c < (sub + 1) * (D / 2); c += 16) {
@@ -582,7 +587,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int row = (int)(((long long)__shfl_sync(0xffffffffu, ids, (t & 7) * 4 + j) * p.n_kv + kvh) * 16);
 #pragma unroll
                 for (int cb = 0; cb < C::CB; ++cb)
-                    tma_load_2d_elect(to + cb * C::BLK + j * 2048, tm, &full[at.st], cb * 64, row);
+                    if (!(p.lose && !is_v && blockIdx.x + t + j + cb == 0))
+                        tma_load_2d_elect(to + cb * C::BLK + j * 2048, tm, &full[at.st], cb * 64, row);
             }
             at.next(st);
         }

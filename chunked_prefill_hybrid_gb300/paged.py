@@ -38,6 +38,7 @@ def _lib():
                 ("hb_decode_shared_workspace", [ci, ci, ci, ci, ci, vp, vp, ci], ll),
                 ("hb_decode_weigh", [vp, vp, ll, vp, ci, vp, ci, ci, ci, ci, vp, vp, ci, cf, vp, ll, vp, ll, vp], ci),
                 ("hb_decode_weigh_workspace", [ci, ci, ci, ci, ci, ci], ll),
+                ("hb_paged_test_lost_block", [], None),
                 ("hb_evict_select", [vp, vp, ci, vp, ci, ci, ci, ci, ci, vp, vp], ci),
                 ("hb_evict_move", [vp, vp, ci, vp, ci, vp, ci, ci, vp, vp, ci, vp, ci, vp], ci)):
             f = getattr(L, name)
@@ -187,6 +188,12 @@ def decode_weigh(pool: PagedPool, q, block_tables, ctx_lens, max_ctx: int, weigh
                                 os_[0], ws.data_ptr(), ws.nbytes, _raw_stream(dev, stream))
     if rc:
         _check(rc, "hb_decode_weigh")
+
+
+def paged_test_lost_block():
+    """Test hook: this thread's next decode_shared or decode_weigh that attends keys for several rows at once loses a
+    copy, and its waits for it run out."""
+    _lib().hb_paged_test_lost_block()
 
 
 def evict_select(weights, weight_tables, lens, max_len: int, keep: int, n_first: int, n_recent: int, kept, stream=None):

@@ -85,8 +85,8 @@ typedef struct {
  * A row whose ctx_lens entry lies outside its range, or whose keys lie in a
  * block id outside the pool, gets NaN and reads nothing there; a bad block of
  * a prefix makes its group's rows NaN.  Bytes of slots past a row's context
- * never reach its result.  Sums and softmax statistics are fp32, the weights
- * keep 16 significant bits; results of differently shaped calls agree to
+ * never reach its result.  Sums and softmax statistics are fp32 (a q . k that
+ * overflows it makes its row NaN), the weights keep 16 significant bits; results of differently shaped calls agree to
  * fp32 rounding, not bit for bit; one call repeated gives the same bits.
  * Errors: HB_EINVAL, HB_ERANGE (bt_stride or workspace too small, max_ctx of
  * 2^27 or more, more than 65535 rows, more work than one launch holds),
@@ -132,6 +132,14 @@ int hb_decode_weigh(const hb_paged_pool *pool, const void *q, long long q_stride
                     const hb_weight_pool *weights, const int32_t *weight_tables, int wt_stride, float decay, void *out,
                     long long out_stride, void *workspace, long long workspace_bytes, void *cuda_stream);
 long long hb_decode_weigh_workspace(int n_seqs, int n_queries, int n_heads, int n_kv_heads, int head_dim, int max_ctx);
+
+/* Test hook for the failure path of the two attention calls: in this thread's
+ * next hb_decode_shared or hb_decode_weigh that attends keys for several rows
+ * at once, the first CTA to do so leaves out one copy, so that its waits run
+ * out (after 2 s, as they always would).  The rows and heads of that CTA become
+ * NaN, after its copies and products under way have ended, and add nothing to
+ * weights; the others, and the calls after it, are as ever. */
+void hb_paged_test_lost_block(void);
 
 /* ------------------------------------------------- eviction
  *

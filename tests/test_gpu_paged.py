@@ -80,6 +80,22 @@ class Case:
         torch.cuda.synchronize()
         return out
 
+    def check_large(self, out, rows=None):
+        """check() on the GPU, in 64 bits as well."""
+        n, heads, d = self.q.shape
+        for j in range(n) if rows is None else rows:
+            m = int(self.ctx[j]) + 1
+            page = _dev(self.tables[j, :(m + 15) // 16]).long()
+            k, v = (pool[page].double().transpose(0, 1).flatten(1, 2)[:, :m] for pool in (self.k, self.v))
+            q = self.q[j].double().view(self.kv, self.group, d)
+            p = torch.softmax(torch.einsum("hgd,hkd->hgk", q, k) / d ** 0.5, -1)
+            o, w = torch.einsum("hgk,hkd->hgd", p, v), torch.einsum("hgk,hkd->hgd", p, v.abs())
+            a = torch.einsum("hgd,hkd->hgk", q.abs(), k.abs()).amax(-1, keepdim=True) / d ** 0.5
+            eps = 2.0 ** -21 + (d + 8) * 2.0 ** -23 * a
+            bound = 2.0 ** -8 * o.abs() + w * (2.0 ** -16 + 2 * eps + (m / 16 + 64) * 2.0 ** -23) + 1e-37
+            off = (out[j].double().view_as(o) - o).abs()
+            assert (off <= bound).all(), (j, off.max(), bound.max())
+
     def check(self, out, rows=None):
         o, b = ref.shared(_f64(self.q), _f64(self.k), _f64(self.v), self.tables, self.ctx, self.group)
         rows = range(len(self.ctx)) if rows is None else rows
@@ -111,6 +127,95 @@ def test_shared_matches_the_plain_form(kv, group, d, rows, prefix, ctx):
     assert torch.equal(out, c.run())  # the same bits again
     wide = c.run(max_ctx=max(ctx) + 4000)  # another split of the keys
     c.check(wide)
+
+
+SHARE = 24 << 20  # bytes of reads that are saved from which on a prefix is read once
+
+
+@pytest.mark.parametrize("kv,group,d,rows,prefix,own", [
+    (2, 1, 128, [18], [1500], 300),         # one Q tile
+    (1, 8, 128, [16], [3500], 40),          # exactly 128 queries, an odd prefix
+    (1, 3, 128, [43], [1616], 5),           # 129: a second tile with one row; a last sub-tile of one block
+    (4, 2, 128, [128], [112], 20),          # 256: two sub-tiles, the last of three blocks
+    (1, 1, 128, [257], [208], 33),          # 257: a CTA with one row
+    (40, 1, 64, [130], [64], 17),           # one sub-tile, two Q tiles
+    (50, 1, 128, [21], [64], 17),           # one sub-tile, one Q tile: the second half has nothing
+    (1, 20, 64, [30], [3603], 100),         # 600 queries
+    (1, 5, 64, [30, 1, 60], [5000, 700, 2500], 64),   # two prefixes shared, one not
+    (2, 1, 128, [20, 20], [1400, 50], 900),           # one shared, one too short for it
+])
+def test_shared_prefix_in_one_pass(kv, group, d, rows, prefix, own):
+    """Prefixes long enough to be read once for their groups, on the tensor cores."""
+    rng = np.random.default_rng(len(rows) + d)
+    assert (rows[0] - 1) * (prefix[0] // 16 * 16) * kv * 4 * d >= SHARE
+    ctx = [p + int(rng.integers(0, own)) for r, p in zip(rows, prefix) for _ in range(r)]
+    ctx[0] = prefix[0] - 1  # a row whose own keys are none but the part-filled block's
+    c = Case(sum(rows), kv, group, d, rows, prefix, ctx)
+    out = c.run()
+    c.check_large(out)
+    assert torch.equal(out, c.run())
+    c.check_large(c.run(max_ctx=max(ctx) + 3000))
+
+
+def test_shared_prefix_in_one_pass_of_many_groups():
+    """More groups than the kernels' parameters hold, some of them shared."""
+    rows, prefix = [1, 30] * 10, [50, 900] * 10
+    ctx = [p + 7 * (i % 9) for i, (r, p) in enumerate(zip(rows, prefix)) for _ in range(r)]
+    c = Case(44, 2, 1, 128, rows, prefix, ctx)
+    assert (30 - 1) * 896 * 2 * 512 >= SHARE
+    c.check_large(c.run())
+
+
+def test_shared_prefix_in_one_pass_padding_and_bad_blocks():
+    c = Case(45, 2, 2, 128, [40, 3], [700, 0], [700 + j for j in range(40)] + [9, 40, 3])
+    assert 39 * 688 * 2 * 512 >= SHARE
+    ctx = c.ctx.copy()
+    ctx[[0, 17]], ctx[3], ctx[4] = -1, 698, 100000   # padding, not covering the prefix, past max_ctx
+    out = c.run(ctx=ctx, max_ctx=760)
+    assert (out[[0, 17]] == 0).all() and torch.isnan(out[[3, 4]]).all()
+    c.check_large(out, [j for j in range(43) if j not in (0, 17, 3, 4)])
+    bad = c.tables.copy()
+    bad[0, 43] = c.k.shape[0]         # the prefix's last whole block would be 42: this is row 0's own
+    bad[5, 2] = -9                    # not read: the first row's is
+    bad[41, 1] = 1 << 28
+    out = c.run(tables=bad)
+    assert torch.isnan(out[[0, 41]]).all()
+    c.check_large(out, [j for j in range(43) if j not in (0, 41)])
+    bad = c.tables.copy()
+    bad[0, 30] = -1
+    out = c.run(tables=bad)
+    assert torch.isnan(out[:40]).all()
+    c.check_large(out, [40, 41, 42])
+
+
+def test_shared_prefix_in_one_pass_large_and_infinite_scores():
+    c = Case(46, 1, 2, 64, [60], [4000], [4100 - j for j in range(60)], poison=False, scale=300.0)
+    assert 59 * 4000 * 256 >= SHARE
+    c.q *= 100.0
+    c.check_large(c.run())
+    c = Case(47, 2, 1, 128, [40], [700], [760] * 40, poison=False)
+    page = c.tables[0, 7]
+    c.k[page, 0, 3] = 0.0
+    c.k[page, 0, 3, 0] = -float("inf")    # a key that no row looks at
+    c.q[:, :, 0] = 1.0
+    c.check_large(c.run())
+    c.k[page, 0, 3, 0] = 3e38             # one whose score, 9e38, is infinite in 32 bits: inf - inf
+    c.q[:, 0, 0] = 3.0
+    out = c.run()
+    assert torch.isnan(out[:, 0]).all() and torch.isfinite(out[:, 1]).all()
+    c.q[:, 0, 0] = 1.0                    # 3e38: it takes all of kv head 0's weight
+    out = c.run()
+    assert torch.equal(out[:, 0], c.v[page, 0, 3].expand(40, -1)) and torch.isfinite(out).all()
+    c.k[page, 0, 3, 0] = NAN
+    out = c.run()
+    assert torch.isnan(out[:, 0]).all() and torch.isfinite(out[:, 1]).all()
+    c = Case(48, 2, 1, 128, [40], [700], [760] * 40, poison=False)
+    c.v[c.tables[0, 3], 1, 2, 9] = NAN    # a channel of every row
+    out = c.run()
+    assert torch.isnan(out[:, 1, 9]).all() and torch.isfinite(out[:, 1, :9]).all() and torch.isfinite(out[:, 0]).all()
+    c.k[:] = -float("inf")                # nothing to look at: not a number, as the formula
+    c.q[:] = 1.0
+    assert torch.isnan(c.run()).all()
 
 
 def test_shared_with_many_groups():
