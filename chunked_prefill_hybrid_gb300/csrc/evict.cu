@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv4_host.h"
 #include "paged.h"
@@ -342,11 +343,16 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
     using T = MoveTile<PIECES, P, CTAS>;
     constexpr int S = T::STAGES, TOKENS = T::TOKENS, PER = TOKENS * PIECES / MOVE_THREADS, ROW = PIECES * P;
     constexpr int LAG = T::LAG, AHEAD = T::AHEAD, GB = T::BATCHES, EACH = T::GROUP / MOVE_THREADS;
-    static_assert(PER * MOVE_THREADS == TOKENS * PIECES && LAG <= GB);
-    int *s_src = reinterpret_cast<int *>(ring + S * T::BYTES), *s_dst = s_src + T::GROUPS * T::GROUP;  // -1: not moved
+    static_assert(PER == 4 && PER * MOVE_THREADS == TOKENS * PIECES && LAG <= GB);
+    // where tokens come from and go to, as rows of the pool from this kv head's
+    // first on; NONE: not moved
+    constexpr uint32_t NONE = 0xffffffffu;
+    uint32_t *s_src = reinterpret_cast<uint32_t *>(ring + S * T::BYTES), *s_dst = s_src + T::GROUPS * T::GROUP;
     const int n = (keep + TOKENS * CTAS - 1) / (TOKENS * CTAS);
-    pool += (size_t)kvh * 16 * ROW;
-    const size_t page = (size_t)n_kv * 16 * ROW;
+    const uint32_t page = (uint32_t)n_kv * 16;  // rows
+    // a thread has piece c of four neighbouring tokens of a batch
+    const int c = threadIdx.x % PIECES, t0 = threadIdx.x / PIECES * PER;
+    pool += (size_t)kvh * 16 * ROW + c * P;
     // token of a thread's look-up u in group q of this CTA's batches
     auto token = [&](int q, int u) {
         const int x = u * MOVE_THREADS + (int)threadIdx.x;
@@ -374,40 +380,36 @@ __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_
             const int at = q % T::GROUPS * T::GROUP + u * MOVE_THREADS + (int)threadIdx.x, i = (int)token(q, u);
             const bool ok = b0[u] >= 0 && b0[u] < num_blocks && b1[u] >= 0 && b1[u] < num_blocks &&
                             !(b0[u] == b1[u] && k[u] == i);
-            s_src[at] = ok ? b0[u] * 16 + (k[u] & 15) : -1;
-            s_dst[at] = ok ? b1[u] * 16 + (i & 15) : -1;
+            s_src[at] = ok ? b0[u] * page + (k[u] & 15) : NONE;
+            s_dst[at] = ok ? b1[u] * page + (i & 15) : NONE;
         }
     };
     auto slots = [&](int b) { return b / GB % T::GROUPS * T::GROUP + b % GB * TOKENS; };  // of batch b
     auto load = [&](int b) {
         if (b < n) {
-            const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring + b % S * T::BYTES);
-            const int *from_slot = s_src + slots(b);
+            const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring + b % S * T::BYTES) + t0 * ROW + c * P;
+            const uint4 src = *reinterpret_cast<const uint4 *>(s_src + slots(b) + t0);
+            const uint32_t r[PER] = {src.x, src.y, src.z, src.w};
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
-                const int src = from_slot[e / PIECES];
-                if (src >= 0)
-                    copy_async<P>(at + e * P, pool + (src >> 4) * page + (src & 15) * ROW + c * P);
-            }
+            for (int j = 0; j < PER; ++j)
+                if (r[j] != NONE)
+                    copy_async<P>(at + j * ROW, pool + (size_t)r[j] * ROW);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto store = [&](int b) {
-        const int *to_slot = s_dst + slots(b);
+        using V = typename std::conditional<P == 16, uint4, uint32_t>::type;
+        const uint8_t *at = ring + b % S * T::BYTES + t0 * ROW + c * P;
+        const uint4 dst = *reinterpret_cast<const uint4 *>(s_dst + slots(b) + t0);
+        const uint32_t r[PER] = {dst.x, dst.y, dst.z, dst.w};
+        V v[PER];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = j * MOVE_THREADS + threadIdx.x, c = e % PIECES;
-            const int d = to_slot[e / PIECES];
-            if (d >= 0) {
-                uint8_t *o = pool + (d >> 4) * page + (d & 15) * ROW + c * P;
-                const uint8_t *x = ring + b % S * T::BYTES + e * P;
-                if constexpr (P == 16)
-                    *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(x);
-                else
-                    *reinterpret_cast<uint32_t *>(o) = *reinterpret_cast<const uint32_t *>(x);
-            }
-        }
+        for (int j = 0; j < PER; ++j)
+            v[j] = *reinterpret_cast<const V *>(at + j * ROW);
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (r[j] != NONE)
+                *reinterpret_cast<V *>(pool + (size_t)r[j] * ROW) = v[j];
     };
     // of the group to be put next: positions and blocks; of the one after: positions
     int k[EACH], b0[EACH], b1[EACH], k2[EACH];
@@ -614,6 +616,10 @@ try {
         p.w_to_stride = new_wt_stride;
     }
     cudaStream_t s = (cudaStream_t)cuda_stream;
+    // a token's row in its pool is counted in 32 bits
+    const long long most = weights && weights->num_blocks > p.num_blocks ? weights->num_blocks : p.num_blocks;
+    if (most * p.n_kv * 16 > 0xfffffffell)
+        return HB_ERANGE;
     const long long items = (long long)n_seqs * p.n_kv;
     if (items * 2 >= 304 || keep <= 2048)
         return pool->head_dim == 128 ? launch_move<128, 1>(p, n_seqs, s) : launch_move<64, 1>(p, n_seqs, s);
