@@ -15,7 +15,8 @@ namespace {
 using namespace paged;
 
 constexpr int MOVE_THREADS = 256;
-constexpr int CLUSTER = 8;  // CTAs of a long sequence's kv head
+constexpr int CLUSTER = 8;         // CTAs of a long sequence's kv head
+constexpr int MOST_RANKS = 49152;  // of tokens that a CTA keeps in shared memory
 
 // ------------------------------------------------------------------- choice
 
@@ -529,15 +530,14 @@ template <int THREADS, int BITS, int CTAS>
 int launch_select(Select p, int n_seqs, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    constexpr int MOST = 192 * 1024;  // bytes of ranks
     auto kernel = k_evict_select<THREADS, BITS, CTAS>;
     const long long piece = (((long long)p.max_len + CTAS - 1) / CTAS + 15) & ~15ll;
-    const int smem = piece * 4 <= MOST ? (int)piece * 4 : 0;
+    const int smem = piece <= MOST_RANKS ? (int)piece * 4 : 0;
     p.room = smem / 4;
     const long long gx = (long long)p.n_kv * CTAS;
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
-    if (kv4_allow_smem((const void *)kernel, MOST, done) != cudaSuccess)
+    if (kv4_allow_smem((const void *)kernel, MOST_RANKS * 4, done) != cudaSuccess)
         return HB_ECUDA;
     return launch_clusters<CTAS>(kernel, gx, n_seqs, THREADS, smem, s, p) == cudaSuccess ? HB_OK : HB_ECUDA;
 }
@@ -566,11 +566,17 @@ try {
     const Select p = {weights->data, weights->num_blocks, weights->n_kv_heads, weight_tables, wt_stride, lens,
                       max_len,       keep,                n_first,             n_recent,      kept,      0};
     cudaStream_t s = (cudaStream_t)cuda_stream;
-    if (max_len <= 4096)
-        return launch_select<256, 8, 1>(p, n_seqs, s);
+    // One CTA, or a cluster that shares the tokens, for a sequence's kv head
+    // (us): 1 of them with 12000 tokens 13.7 and 8.6 to 10.0; 16 with 6000 9.1 and
+    // 9.6, with 30000 27.8 and 13.9; 64 with 12000 13.8 and 13.7; 256 with 12000
+    // 20.3 and 34.7, with 30000 54 and 50.  256 threads for few tokens: 16 with
+    // 2000 6.0 and 7.3 (1024 threads).  In a cluster 512 threads and digits of 11
+    // bits for few: 8 with 131000 20.6, 30.2 with 256; 64 with 40000 34 and 22.
     const long long items = (long long)n_seqs * weights->n_kv_heads;
-    return items >= 152 && max_len <= 49152 ? launch_select<1024, 11, 1>(p, n_seqs, s)
-                                            : launch_select<1024, 11, CLUSTER>(p, n_seqs, s);
+    if (max_len > 5500 + 78 * items || max_len > MOST_RANKS)
+        return items <= 24 ? launch_select<512, 11, CLUSTER>(p, n_seqs, s)
+                           : launch_select<256, 8, CLUSTER>(p, n_seqs, s);
+    return max_len <= 3000 ? launch_select<256, 8, 1>(p, n_seqs, s) : launch_select<512, 9, 1>(p, n_seqs, s);
 } catch (...) {
     return HB_ENOMEM;
 }
@@ -621,7 +627,10 @@ try {
     if (most * p.n_kv * 16 > 0xfffffffell)
         return HB_ERANGE;
     const long long items = (long long)n_seqs * p.n_kv;
-    if (items * 2 >= 304 || keep <= 2048)
+    // One CTA or a cluster of them for a stream (us): 1 kv head that keeps 1000
+    // tokens 7.9 and 3.5; 16 that keep 250 3.6 and 5.4, 1000 8.3 and 6.7; 64 that
+    // keep 1000 14.2 and 19.8, 3000 42.9 and 40.9
+    if (keep <= 64 + 36 * items)
         return pool->head_dim == 128 ? launch_move<128, 1>(p, n_seqs, s) : launch_move<64, 1>(p, n_seqs, s);
     return pool->head_dim == 128 ? launch_move<128, CLUSTER>(p, n_seqs, s) : launch_move<64, CLUSTER>(p, n_seqs, s);
 } catch (...) {

@@ -26,14 +26,18 @@ namespace {
 using namespace paged;
 
 constexpr int WARPS = 4;
-#ifndef RING_D
-#define RING_D 2
-#endif
 constexpr int JOIN_WARPS = 8;
+// A warp takes a tile's keys alone up to so many of them, where there are so many
+// tiles: 88 sequences of 15 to 177 keys, 16 queries and 16 kv heads, 44 us with
+// four warps a tile and 35 so; 18 rows of 1024 keys and 40 heads, 65 and 77.
+constexpr int ALONE_KEYS = 320;
+constexpr long long ALONE_UNITS = 456;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
+constexpr int SPLIT_MOST = 2048;     // and at most
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
-constexpr long long SHARE_BYTES = 24 << 20;
+constexpr long long SHARE_BYTES = 24 << 20;  // of all groups
+constexpr long long SHARE_GROUP = 1 << 20;   // of one, where others are shared anyway
 // Bytes of own keys that an SM streams in a third of a sub-tile's time, halved
 // where contexts are taken to be half of max_ctx on average; more beside prefixes
 // bound by their products, which leave the memory to the others: 53.1 us so and
@@ -114,7 +118,7 @@ struct Ring {
     static constexpr int ROW = D * 2;             // bytes of a key
     static constexpr int HALF = 16 * ROW;         // K or V of a page
     static constexpr int PAGE = 2 * HALF;
-    static constexpr int DEPTH = D == 128 ? RING_D : (2 * RING_D - 1);  // pages of a warp, one of them in use
+    static constexpr int DEPTH = D == 128 ? 2 : 3;  // pages of a warp, one of them in use
 };
 
 // Shared memory: a ring of pages for each warp, and after the key loop, in the
@@ -177,7 +181,8 @@ __device__ __forceinline__ void put_weights(const Attn &p, float *to, float4 old
 // A tile of 8 NT of a kv head's queries of one sequence, and the keys of one
 // split.  KW = WARPS: a CTA has one tile, whose warps take the pages in turn, each
 // with a ring and a softmax of its own, and join their results in shared memory.
-// KW = 1, for many queries: each warp has a tile of its own and all pages.
+// KW = 1, for many queries or few keys: each warp has a tile of its own, or a kv
+// head, and all pages.
 template <int D, int NT, bool SCORES, int KW>
 __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_constant__ Attn p)
 {
@@ -187,14 +192,13 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[WARPS][COLS], s_l[WARPS][COLS];
-    __shared__ float2 s_final[COLS];
+    __shared__ float2 s_final[WARPS / KW][COLS];
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.n_splits;
     const int rest = blockIdx.x / p.n_splits;
-    const int tiles = (p.col_tiles * KW + WARPS - 1) / WARPS;  // CTAs for them
-    const int tile = rest % tiles * (WARPS / KW) + (KW == 1 ? warp : 0), kvh = rest / tiles;
+    const int unit = rest * (WARPS / KW) + (KW == 1 ? warp : 0), tile = unit % p.col_tiles, kvh = unit / p.col_tiles;
     const int kw = KW == 1 ? 0 : warp;  // this warp's turn among the pages
     const int seq = blockIdx.y;
     const int ncols = p.nq * p.group;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     }
     // where a row's keys start and end is the same for all threads of the CTA
     if (ctx < least || ctx > p.max_ctx) {  // padding: zeros; outside its range: NaN
-        if (p.direct && split == 0)
+        if (p.direct && split == 0 && kvh < p.n_kv)
             for (int i = kw * 32 + lane; i < COLS * D; i += KW * 32) {
                 const int c = c0 + i / D;
                 if (c < ncols)
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         return leave();
     }
     const int k0 = from + split * p.split_len, k1 = min(ctx + 1, k0 + p.split_len);
-    if (k0 >= k1 || tile >= p.col_tiles)
+    if (k0 >= k1 || (KW == 1 && kvh >= p.n_kv))
         return leave();  // the join knows how many splits a row has
 
     // ---- this warp's pages: b0 + KW i, i < n
@@ -308,10 +312,11 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
     float *score_at = nullptr;  // of column 2t of the first tile, key g
-    const bool keep = SCORES && KW == WARPS && p.fused && ncols * p.score_stride <= S::SCORES;  // scores in shared memory
+    // scores in shared memory
+    const bool keep = SCORES && p.fused && ncols * p.score_stride <= S::SCORES * KW / WARPS;
     float *scores = nullptr;
     if (SCORES) {
-        scores = keep ? reinterpret_cast<float *>(smem + S::BYTES)
+        scores = keep ? reinterpret_cast<float *>(smem + S::BYTES) + (KW == 1 ? warp : 0) * (S::SCORES / WARPS)
                       : p.scores + ((size_t)seq * p.n_kv + kvh) * ncols * p.score_stride;
         score_at = scores + (size_t)(c0 + 2 * t) * p.score_stride + g;
     }
@@ -502,14 +507,14 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
         if (SCORES && p.direct && e == 0) {
             const float2 x = make_float2(mx == -INFINITY ? 0.f : mx, sum > 0.f ? 1.f / sum : 0.f);
             if (p.fused)
-                s_final[cl] = x;
+                s_final[KW == 1 ? warp : 0][cl] = x;
             else
                 p.final_ml[(size_t)row * p.n_heads + head] = x;
         }
     }
-    if (SCORES && KW == WARPS && p.fused) {  // the CTA has all keys and queries: the weights, four keys a thread
-        __syncthreads();
-        for (int key = threadIdx.x * 4; key <= ctx; key += WARPS * 32 * 4) {
+    if (SCORES && p.fused) {  // the CTA (or warp) has all keys and queries: the weights, four keys a thread
+        sync();
+        for (int key = (kw * 32 + lane) * 4; key <= ctx; key += KW * 32 * 4) {
             float *to = weights_of(p, seq, kvh, key);
             if (!to)
                 continue;
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
                 if (c < ncols) {
                     const float *s = scores + c * p.score_stride + key;
                     add_weights(a, keep ? *reinterpret_cast<const float4 *>(s) : __ldcg(reinterpret_cast<const float4 *>(s)),
-                                s_final[c], p.c2);
+                                s_final[KW == 1 ? warp : 0][c], p.c2);
                 }
             put_weights(p, to, old, ctx, key, a);
         }
@@ -729,13 +734,15 @@ thread_local bool test_lose = false;  // of this thread's next launch of the com
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
 // Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split: as many
-// as the SMs hold at once, three each.
+// as the SMs hold at once, three each, where all rows are as long.
 void plan_splits(long long base, int keys, int *len, int *n)
 {
     const long long want = 3 * SMS / (base > 0 ? base : 1);
     long long s = keys / SPLIT_MIN;
     s = s < want ? s : want;
     s = s < 1 ? 1 : s;
+    const long long least = (keys + SPLIT_MOST - 1) / SPLIT_MOST;  // where few of the rows are long
+    s = s < least ? least : s;
     const long long each = round_up((keys + s - 1) / s, 64);
     *len = (int)(each > 0 ? each : 64);
     *n = (int)((keys + *len - 1) / *len);
@@ -768,10 +775,10 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
     auto kernel = k_paged_attention<D, NT, SCORES, KW>;
-    const long long tiles = ((long long)p.col_tiles * KW + WARPS - 1) / WARPS;
-    const long long gx = (long long)p.n_kv * tiles * p.n_splits;  // at most the heads and queries, or 3 SMS
+    const long long units = (long long)p.n_kv * p.col_tiles;
+    const long long gx = (units * KW + WARPS - 1) / WARPS * p.n_splits;  // at most the heads and queries, or 3 SMS
     using S = Smem<D, NT>;
-    constexpr int most = S::BYTES + (SCORES && KW == WARPS ? 4 * S::SCORES : 0);
+    constexpr int most = S::BYTES + (SCORES ? 4 * S::SCORES : 0);
     if (kv4_allow_smem((const void *)kernel, most, done) != cudaSuccess)
         return HB_ECUDA;
     const int smem = p.fused ? most : S::BYTES;
@@ -780,10 +787,17 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
                : HB_ECUDA;
 }
 
+// Whether a warp takes a tile's keys alone: where there are many tiles of queries,
+// or enough of everything else for splits this short.
+bool alone(const Attn &p, int n_seqs)
+{
+    return p.col_tiles >= WARPS || (p.split_len <= ALONE_KEYS && (long long)n_seqs * p.n_kv * p.col_tiles >= ALONE_UNITS);
+}
+
 template <int D, bool SCORES>
 int attention_of(const Attn &p, int nt, int n_seqs, cudaStream_t s)
 {
-    if (p.col_tiles >= WARPS)
+    if (alone(p, n_seqs))
         return nt == 1 ? launch_attention<D, 1, SCORES, 1>(p, n_seqs, s) : launch_attention<D, 2, SCORES, 1>(p, n_seqs, s);
     return nt == 1 ? launch_attention<D, 1, SCORES, WARPS>(p, n_seqs, s)
                    : launch_attention<D, 2, SCORES, WARPS>(p, n_seqs, s);
@@ -825,14 +839,14 @@ struct Plan {
     Layout at;
 };
 
-// What is attended once for group i, and how: its blocks are shared when the
-// reads that this saves pay for a second kernel and a join.
-Group shared_group(int row0, int rows, int prefix, int n_kv, int d, bool can)
+// Bytes that are read once only if a group's whole blocks are shared.
+long long saved_bytes(int rows, int prefix, int n_kv, int d) { return (long long)(rows - 1) * (prefix & ~15) * n_kv * 4 * d; }
+
+Group shared_group(int row0, int rows, int prefix, int n_kv, int d, bool share)
 {
     Group g = {row0, rows, prefix, 0, 0, 0, 1};
-    const int whole = prefix & ~15;
-    if (can && whole > 0 && (long long)(rows - 1) * whole * n_kv * 4 * d >= SHARE_BYTES)
-        g.shared = whole;
+    if (share && saved_bytes(rows, prefix, n_kv, d) >= SHARE_GROUP)
+        g.shared = prefix & ~15;
     return g;
 }
 
@@ -871,7 +885,12 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
         return HB_EINVAL;
     const int g = n_heads / n_kv;
     // a copy's row coordinate is 32 bits wide, a group's queries are counted in as many
-    const bool can = (long long)num_blocks * n_kv * 16 <= 0x7fffffffll && (long long)n_rows * g <= 0x7fffffffll;
+    bool can = (long long)num_blocks * n_kv * 16 <= 0x7fffffffll && (long long)n_rows * g <= 0x7fffffffll;
+    // the reads saved have to pay for a second kernel and a join
+    long long saved = 0;
+    for (int i = 0; i < n_groups; ++i)
+        saved += saved_bytes(group_rows[i], prefix_lens[i], n_kv, d);
+    can = can && saved >= SHARE_BYTES;
     // the smallest load of a CTA for which all run at once, or else the whole of a prefix
     auto total = [&](long long most) {
         long long n = 0;

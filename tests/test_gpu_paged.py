@@ -455,6 +455,8 @@ def _select(w, tables, lens, keep, first, recent, max_len=None):
     ([1], 1, 1, 0, 0), ([5, 1, 0, 17], 2, 1, 0, 0), ([5, 2, 33], 3, 2, 1, 1), ([100, 64, 65, 63], 2, 64, 4, 8),
     ([200, 31, 129], 4, 32, 4, 8), ([300], 1, 299, 0, 0), ([1025, 513], 5, 512, 4, 128), ([4096, 4097], 1, 100, 0, 100),
     ([4095], 2, 50, 50, 0), ([9000, 5000], 2, 4500, 100, 1000), ([70000], 1, 30000, 4, 64),
+    ([3001, 5900], 3, 1000, 3, 7), ([10000, 100, 7] + [9] * 27, 1, 5000, 0, 5),
+    ([500, 60001], 13, 100, 4, 8),
 ])
 def test_select_keeps_the_heaviest(lens, kv, keep, first, recent):
     rng = np.random.default_rng(sum(lens) + keep)
@@ -477,6 +479,21 @@ def test_select_ties_signs_and_numbers_that_are_none(seed):
         first, recent = min(2, keep // 3), min(3, keep // 3)
         assert np.array_equal(_select(w, tables, lens, keep, first, recent),
                               ref.select(w, tables, lens, keep, first, recent)), (lens, keep)
+
+
+@pytest.mark.parametrize("kv,keep", [(1, 300000), (30, 100)])
+def test_select_of_more_tokens_than_a_cluster_keeps(kv, keep):
+    """Longer than eight CTAs' shared memory: the weights are read again in every pass.  Whole numbers, many of them
+    equal, so that the choice is by position too."""
+    n = 450000
+    tables = np.random.default_rng(2).permutation(n // 16 + 1)[None]
+    w = torch.randint(0, 1000 if keep > 1000 else n, (n // 16 + 1, kv, 16), device="cuda").float()
+    kept = torch.empty(1, kv, keep, dtype=torch.int32, device="cuda")
+    paged.evict_select(w, _dev(tables), _dev([n]), n, keep, 3, 50, kept)
+    flat = w[torch.from_numpy(tables[0]).cuda()].transpose(0, 1).reshape(kv, -1)[:, :n].clone()
+    flat[:, :3], flat[:, n - 50:] = float("inf"), float("inf")
+    want = torch.sort(torch.sort(flat, dim=1, descending=True, stable=True).indices[:, :keep], dim=1).values
+    assert torch.equal(kept[0].long(), want)
 
 
 def test_select_lengths_out_of_range():
