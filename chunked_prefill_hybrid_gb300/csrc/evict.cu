@@ -290,6 +290,65 @@ __global__ void __launch_bounds__(THREADS) k_evict_select(const Select p)
         tc::cluster_sync();  // no CTA's shared memory goes while another reads it
 }
 
+// Up to 64 tokens: a warp a sequence's kv head.  A token stays if fewer than keep
+// others come before it, by rank and then by position: a lane's compares, not
+// memory, are its time, and they grow with the square.  us, a CTA of k_evict_select
+// and a warp: 720 heads of 30 tokens 7.3 and 4.0, 16 of them 4.6 and 4.1; 5120 of
+// 64 tokens 31.6 and 15.3, 720 of them 7.3 and 7.5, 16 of them 4.6 and 7.3.
+constexpr int FEW_WARPS = 8, FEW_TOKENS = 64, FEW_ITEMS = 720;
+
+template <int N>  // tokens of a lane
+__global__ void __launch_bounds__(FEW_WARPS * 32) k_evict_select_few(const Select p, long long items)
+{
+    pdl_wait();
+    pdl_trigger();
+    const long long item = (long long)blockIdx.x * FEW_WARPS + (threadIdx.x >> 5);
+    if (item >= items)
+        return;
+    const int lane = threadIdx.x & 31, seq = (int)(item / p.n_kv), kvh = (int)(item % p.n_kv);
+    int len = p.lens[seq];
+    if (len < 0 || len > p.max_len)
+        len = 0;
+    int *kept = p.kept + item * p.keep;
+    uint32_t r[N];
+    int before[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        const int i = t * 32 + lane;
+        r[t] = 0u;
+        before[t] = 0;
+        if (i < len) {
+            const int blk = __ldg(p.tables + (size_t)seq * p.stride + (i >> 4));
+            if (i < p.first || i >= len - p.recent)
+                r[t] = STAYS;
+            else if (blk >= 0 && blk < p.num_blocks)
+                r[t] = rank_of(p.w[((size_t)blk * p.n_kv + kvh) * 16 + (i & 15)]);
+        }
+    }
+    if (len > p.keep)
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const int n = min(32, len - q * 32);
+            for (int l = 0; l < n; ++l) {
+                const uint32_t x = __shfl_sync(0xffffffffu, r[q], l);
+#pragma unroll
+                for (int t = 0; t < N; ++t)
+                    before[t] += x > r[t] || (x == r[t] && q * 32 + l < t * 32 + lane);
+            }
+        }
+    int done = 0;
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        const bool take = t * 32 + lane < len && before[t] < p.keep;
+        const uint32_t mask = __ballot_sync(0xffffffffu, take);
+        if (take)
+            kept[done + __popc(mask & ((1u << lane) - 1u))] = t * 32 + lane;
+        done += __popc(mask);
+    }
+    for (int i = done + lane; i < p.keep; i += 32)
+        kept[i] = -1;
+}
+
 // --------------------------------------------------------------------- move
 
 struct Move {
@@ -486,6 +545,59 @@ __global__ void __launch_bounds__(MOVE_THREADS) k_evict_move(const Move p)
                               p.w_to + (size_t)seq * p.w_to_stride, p.w_to_stride, kept, p.keep);
 }
 
+// Up to 32 tokens: a warp the K, V or weights of a sequence's kv head, all loaded
+// before any is stored.  us, a CTA of k_evict_move and a warp: 720 heads of 128
+// channels that keep 32 tokens 13.2 and 5.3, 32 of them 4.1 and 3.9, 16 of them
+// 2.8 and 3.9; 5120 of them 95 and 43.5, at 3.9 TB/s.
+constexpr int MOVE_FEW_ITEMS = 32;
+
+template <int D>
+__global__ void __launch_bounds__(FEW_WARPS * 32) k_evict_move_few(const Move p, long long units)
+{
+    constexpr int PIECES = D / 8, ROW = D * 2;
+    pdl_wait();
+    pdl_trigger();
+    const long long unit = (long long)blockIdx.x * FEW_WARPS + (threadIdx.x >> 5);
+    if (unit >= units)
+        return;
+    const int lane = threadIdx.x & 31, parts = p.w ? 3 : 2;
+    const int part = (int)(unit % parts), kvh = (int)(unit / parts % p.n_kv), seq = (int)(unit / parts / p.n_kv);
+    const bool weights = part == 2;
+    const int *from = (weights ? p.w_from : p.from) + (size_t)seq * (weights ? p.w_from_stride : p.from_stride);
+    const int *to = (weights ? p.w_to : p.to) + (size_t)seq * (weights ? p.w_to_stride : p.to_stride);
+    const int from_stride = weights ? p.w_from_stride : p.from_stride, blocks = weights ? p.w_blocks : p.num_blocks;
+    const int k = lane < p.keep ? __ldg(p.kept + ((size_t)seq * p.n_kv + kvh) * p.keep + lane) : -1;
+    bool ok = k >= 0 && (k >> 4) < from_stride;
+    const int b0 = ok ? __ldg(from + (k >> 4)) : -1, b1 = ok ? __ldg(to + (lane >> 4)) : -1;
+    ok = b0 >= 0 && b0 < blocks && b1 >= 0 && b1 < blocks && !(b0 == b1 && k == lane);
+    const long long src = ok ? ((long long)b0 * p.n_kv + kvh) * 16 + (k & 15) : -1;
+    const long long dst = ok ? ((long long)b1 * p.n_kv + kvh) * 16 + (lane & 15) : -1;
+    if (weights) {
+        const float x = ok ? p.w[src] : 0.f;
+        __syncwarp();
+        if (ok)
+            p.w[dst] = x;
+        return;
+    }
+    uint8_t *pool = p.pool[part];
+    uint4 v[PIECES];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e = u * 32 + lane;
+        const long long row = __shfl_sync(0xffffffffu, src, e / PIECES);
+        if (row >= 0)
+            v[u] = *reinterpret_cast<const uint4 *>(pool + row * ROW + e % PIECES * 16);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e = u * 32 + lane;
+        const long long row = __shfl_sync(0xffffffffu, dst, e / PIECES);
+        if (row >= 0)
+            *reinterpret_cast<uint4 *>(pool + row * ROW + e % PIECES * 16) = v[u];
+    }
+}
+
 // ------------------------------------------------------------------- host
 
 // A launch of clusters of CTAS CTAs.
@@ -573,6 +685,16 @@ try {
     // 2000 6.0 and 7.3 (1024 threads).  In a cluster 512 threads and digits of 11
     // bits for few: 8 with 131000 20.6, 30.2 with 256; 64 with 40000 34 and 22.
     const long long items = (long long)n_seqs * weights->n_kv_heads;
+    if (max_len <= 32 || (max_len <= FEW_TOKENS && items > FEW_ITEMS)) {
+        static_assert(FEW_TOKENS == 64);
+        const long long blocks = (items + FEW_WARPS - 1) / FEW_WARPS;
+        if (blocks > 0x7fffffffll)
+            return HB_ERANGE;
+        auto kernel = max_len <= 32 ? k_evict_select_few<1> : k_evict_select_few<2>;
+        return launch_kernel(true, kernel, dim3((unsigned)blocks), dim3(FEW_WARPS * 32), 0, s, p, items) == cudaSuccess
+                   ? HB_OK
+                   : HB_ECUDA;
+    }
     if (max_len > 5500 + 78 * items || max_len > MOST_RANKS)
         return items <= 24 ? launch_select<512, 11, CLUSTER>(p, n_seqs, s)
                            : launch_select<256, 8, CLUSTER>(p, n_seqs, s);
@@ -627,10 +749,19 @@ try {
     if (most * p.n_kv * 16 > 0xfffffffell)
         return HB_ERANGE;
     const long long items = (long long)n_seqs * p.n_kv;
+    if (keep <= 32 && items >= MOVE_FEW_ITEMS) {
+        const long long units = items * (p.w ? 3 : 2), blocks = (units + FEW_WARPS - 1) / FEW_WARPS;
+        if (blocks > 0x7fffffffll)
+            return HB_ERANGE;
+        return launch_kernel(true, pool->head_dim == 128 ? k_evict_move_few<128> : k_evict_move_few<64>,
+                             dim3((unsigned)blocks), dim3(FEW_WARPS * 32), 0, s, p, units) == cudaSuccess
+                   ? HB_OK
+                   : HB_ECUDA;
+    }
     // One CTA or a cluster of them for a stream (us): 1 kv head that keeps 1000
     // tokens 7.9 and 3.5; 16 that keep 250 3.6 and 5.4, 1000 8.3 and 6.7; 64 that
     // keep 1000 14.2 and 19.8, 3000 42.9 and 40.9
-    if (keep <= 64 + 36 * items)
+    if ((long long)keep * pool->head_dim <= 128 * (64 + 36 * items))
         return pool->head_dim == 128 ? launch_move<128, 1>(p, n_seqs, s) : launch_move<64, 1>(p, n_seqs, s);
     return pool->head_dim == 128 ? launch_move<128, CLUSTER>(p, n_seqs, s) : launch_move<64, CLUSTER>(p, n_seqs, s);
 } catch (...) {

@@ -33,7 +33,7 @@ constexpr int JOIN_WARPS = 8;
 constexpr int ALONE_KEYS = 320;
 constexpr long long ALONE_UNITS = 456;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
-constexpr int SPLIT_MOST = 2048;     // and at most
+constexpr int SPLIT_MOST = 2048;     // and at most, where some rows are known to be long
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 24 << 20;  // of all groups
@@ -44,7 +44,11 @@ constexpr long long SHARE_GROUP = 1 << 20;   // of one, where others are shared 
 // 47.5 with 30720 (1 + 7 + 56 rows, prefixes of 0, 333 and 16389), but 25.6 and
 // 27.5 (18 rows over 768 keys).
 constexpr int OWN_UNIT = 20480, OWN_UNIT_BESIDE = 30720;
-constexpr int COMMON_MIN = 8;        // sub-tiles
+// Sub-tiles from which on a window's keys go to the tensor cores' kernel, with
+// many queries of a kv head and with 17 to 48 (us): 4 sequences of 8 kv heads x
+// 8 x 16 queries at 200 keys 17.5 against 14.4, at 600 21 and 24, at 3000 41 and
+// 93; 4 of 40 kv heads x 32 queries at 600 keys 35 and 29, at 3000 104 and 107.
+constexpr int COMMON_MIN = 8, COMMON_MIN_FEW = 24;
 constexpr int WEIGH_THREADS = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -734,15 +738,17 @@ thread_local bool test_lose = false;  // of this thread's next launch of the com
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
 // Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split: as many
-// as the SMs hold at once, three each, where all rows are as long.
-void plan_splits(long long base, int keys, int *len, int *n)
+// as the SMs hold at once, three each.  Where a row is known to have more than
+// SPLIT_MOST, which others may not, one CTA's way through them would take longest
+// (rows of 34 to 99 and one of 9500 keys, 40 heads: 120 us, 45 with the limit).
+void plan_splits(long long base, int keys, int known, int *len, int *n)
 {
     const long long want = 3 * SMS / (base > 0 ? base : 1);
     long long s = keys / SPLIT_MIN;
     s = s < want ? s : want;
     s = s < 1 ? 1 : s;
-    const long long least = (keys + SPLIT_MOST - 1) / SPLIT_MOST;  // where few of the rows are long
-    s = s < least ? least : s;
+    if (known > SPLIT_MOST && s < (keys + SPLIT_MOST - 1) / SPLIT_MOST)
+        s = (keys + SPLIT_MOST - 1) / SPLIT_MOST;
     const long long each = round_up((keys + s - 1) / s, 64);
     *len = (int)(each > 0 ? each : 64);
     *n = (int)((keys + *len - 1) / *len);
@@ -787,11 +793,10 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
                : HB_ECUDA;
 }
 
-// Whether a warp takes a tile's keys alone: where there are many tiles of queries,
-// or enough of everything else for splits this short.
+// Whether a warp takes a tile's keys alone.
 bool alone(const Attn &p, int n_seqs)
 {
-    return p.col_tiles >= WARPS || (p.split_len <= ALONE_KEYS && (long long)n_seqs * p.n_kv * p.col_tiles >= ALONE_UNITS);
+    return p.split_len <= ALONE_KEYS && (long long)n_seqs * p.n_kv * p.col_tiles >= ALONE_UNITS;
 }
 
 template <int D, bool SCORES>
@@ -929,7 +934,7 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     }
     hi = hi > units / SMS ? hi : units / SMS;
     long long ctas = 0;
-    int row = 0, parts = 0, most = 0;
+    int row = 0, parts = 0, most = 0, known = 0;  // most, least of the own keys of the longest row
     for (int i = 0; i < n_groups; ++i) {
         Group gr = shared_group(row, group_rows[i], prefix_lens[i], n_kv, d, can);
         const long long n = cut_group(&gr, g, n_kv, hi);
@@ -939,13 +944,14 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
         ctas += n;
         parts = gr.parts > parts ? gr.parts : parts;
         most = max_ctx + 1 - gr.shared > most ? max_ctx + 1 - gr.shared : most;
+        known = gr.prefix - gr.shared > known ? gr.prefix - gr.shared : known;
         row += gr.rows;
         each(i, gr);
     }
     pl->ctas = (int)ctas;
     pl->nt = g > 8 ? 2 : 1;
     pl->col_tiles = tiles_of(g, pl->nt);
-    plan_splits((long long)n_rows * n_kv * pl->col_tiles, most, &pl->split_len, &pl->n_splits);
+    plan_splits((long long)n_rows * n_kv * pl->col_tiles, most, known, &pl->split_len, &pl->n_splits);
     pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->seq_parts = pl->seq_part_len = 0;
@@ -968,7 +974,7 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     // where they are read more than once otherwise, or split in any case
     const long long items = n_seqs * n_kv * ((cols + 255) / 256);
     const int subs = (max_ctx + 64) / 64;
-    if ((long long)num_blocks * n_kv * 16 <= 0x7fffffffll && subs >= COMMON_MIN &&
+    if ((long long)num_blocks * n_kv * 16 <= 0x7fffffffll && subs >= (pl->col_tiles >= WARPS ? COMMON_MIN : COMMON_MIN_FEW) &&
         pl->col_tiles > 1 && items <= 0xffff) {
         long long parts = items < SMS ? SMS / items : 1;
         if (parts > subs / PART_MIN)
@@ -980,7 +986,7 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     }
     // what is left with them: the last rows' own positions and less than a block
     const int own = pl->ctas > 0 && nq + 15 < max_ctx + 1 ? nq + 15 : max_ctx + 1;
-    plan_splits(n_seqs * n_kv * pl->col_tiles, own, &pl->split_len, &pl->n_splits);
+    plan_splits(n_seqs * n_kv * pl->col_tiles, own, 0, &pl->split_len, &pl->n_splits);
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->direct = pl->n_slots == 1;
     pl->fused = pl->direct && pl->col_tiles == 1;

@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---------------------------------------------------- loaders
         // one warp for K and one for V, whose stages are let go at other times.
         // The whole warp stays together and one elected lane issues: a box a
-        // lane took 97 us for 128 rows over 130000 keys of 8 kv heads, @@ so.
+        // lane took 97 us for 16 rows x 8 heads over 130000 keys of 8 kv heads, 87 so.
         const bool is_v = warp > LOAD_WARP;
         const int st = is_v ? (int)stages : (int)stages - 1;
         uint8_t *ring = is_v ? sV : sK;

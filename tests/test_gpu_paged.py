@@ -455,6 +455,8 @@ def _select(w, tables, lens, keep, first, recent, max_len=None):
     ([1], 1, 1, 0, 0), ([5, 1, 0, 17], 2, 1, 0, 0), ([5, 2, 33], 3, 2, 1, 1), ([100, 64, 65, 63], 2, 64, 4, 8),
     ([200, 31, 129], 4, 32, 4, 8), ([300], 1, 299, 0, 0), ([1025, 513], 5, 512, 4, 128), ([4096, 4097], 1, 100, 0, 100),
     ([4095], 2, 50, 50, 0), ([9000, 5000], 2, 4500, 100, 1000), ([70000], 1, 30000, 4, 64),
+    ([128, 127, 33, 32, 1, 0, 64, 65, 100], 3, 40, 2, 3), ([128, 96], 1, 127, 0, 0), ([31, 128, 129], 2, 32, 32, 0),
+    ([32, 31, 0, 1, 17], 3, 8, 1, 2), ([20, 32], 5, 32, 0, 0), ([64, 33, 63, 0, 48, 2, 32] * 4, 26, 24, 4, 3),
     ([3001, 5900], 3, 1000, 3, 7), ([10000, 100, 7] + [9] * 27, 1, 5000, 0, 5),
     ([500, 60001], 13, 100, 4, 8),
 ])
@@ -464,14 +466,14 @@ def test_select_keeps_the_heaviest(lens, kv, keep, first, recent):
     assert np.array_equal(_select(w, tables, lens, keep, first, recent), ref.select(w, tables, lens, keep, first, recent))
 
 
-@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("seed", range(8))
 def test_select_ties_signs_and_numbers_that_are_none(seed):
     """Few distinct values, both zeros, infinities, NaN, denormals and negative ones: the lower position first."""
     rng = np.random.default_rng(seed)
-    lens = [int(x) for x in rng.integers(1, 5000, 3)]
+    lens = [int(x) for x in rng.integers(1, 5000 if seed < 4 else 200 if seed < 6 else 32, 3)]
     w, tables = _weight_pool(rng, lens, 2)
     pick = np.array([0.0, -0.0, 1.0, 1.0, np.inf, -np.inf, NAN, -NAN, 1e-45, -1e-45, -3.0, 2.5, 2.5000002], np.float32)
-    w[:] = pick[rng.integers(0, len(pick), w.shape)] if seed < 3 else 0.0
+    w[:] = pick[rng.integers(0, len(pick), w.shape)] if seed not in (3, 5) else 0.0
     for j in range(3):
         if lens[j] > 40:
             tables[j, 1] = [-1, w.shape[0], 1 << 30][j]  # weights outside the pool
@@ -524,7 +526,9 @@ def _move_case(seed, d, kv, lens, keep, place):
 @pytest.mark.parametrize("place", ["new", "old", "mixed"])
 @pytest.mark.parametrize("d,kv,lens,keep", [
     (64, 1, [1], 1), (128, 2, [40, 7, 0, 100], 30), (64, 3, [17, 33], 16), (128, 5, [600, 1000], 512),
-    (64, 1, [9000], 7000), (128, 1, [6000, 6500], 3001),
+    (64, 1, [9000], 7000), (128, 1, [6000, 6500], 3001), (128, 3, [100, 33, 20], 32), (64, 2, [70] * 19, 31),
+    (128, 5, [30, 1, 0, 90, 33, 32, 17], 32), (64, 33, [15, 40], 3),
+    (128, 1, [12000], 11000), (64, 4, [900, 2000, 1500], 800),
 ])
 def test_move_brings_the_kept_tokens_to_the_front(place, d, kv, lens, keep):
     w, tables, new, k, v, kept = _move_case(sum(lens) + keep, d, kv, lens, keep, place)
