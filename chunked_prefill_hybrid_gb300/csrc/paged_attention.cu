@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_cons
     if (some && share == 0) {
         to = weights_of(p, seq, kvh, key);
         if (to && p.weigh.decay != 0.f)
-            old = *reinterpret_cast<const float4 *>(to);
+            old = __ldcg(reinterpret_cast<const float4 *>(to));
     }
     // queries CHUNK at a time, an equal number for each of the shares
     const int ncols = p.nq * p.group;
@@ -782,7 +782,7 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
     static std::atomic<uint64_t> done{0};
     auto kernel = k_paged_attention<D, NT, SCORES, KW>;
     const long long units = (long long)p.n_kv * p.col_tiles;
-    const long long gx = (units * KW + WARPS - 1) / WARPS * p.n_splits;  // at most the heads and queries, or 3 SMS
+    const long long gx = (units * KW + WARPS - 1) / WARPS * p.n_splits;
     using S = Smem<D, NT>;
     constexpr int most = S::BYTES + (SCORES ? 4 * S::SCORES : 0);
     if (kv4_allow_smem((const void *)kernel, most, done) != cudaSuccess)
@@ -952,6 +952,8 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     pl->nt = g > 8 ? 2 : 1;
     pl->col_tiles = tiles_of(g, pl->nt);
     plan_splits((long long)n_rows * n_kv * pl->col_tiles, most, known, &pl->split_len, &pl->n_splits);
+    if ((long long)n_kv * pl->col_tiles * pl->n_splits > 0x7fffffffll)  // CTAs of a row
+        return HB_ERANGE;
     pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->seq_parts = pl->seq_part_len = 0;

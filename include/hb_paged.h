@@ -66,7 +66,7 @@ typedef struct {
  * of all rows of group g are the same (a fork's shared pages, and the same
  * tokens in each row's copy of a part-filled one); their keys are read once
  * for the whole group, whole blocks of them through the table of the group's
- * first row.
+ * first row (also where that is a padding row).
  *   q, out:       device bf16, row j at q + j * q_stride elements, [n_heads]
  *                 [head_dim] dense inside a row; 16-byte aligned, strides
  *                 multiples of 8 and >= n_heads * head_dim (any stride for
@@ -86,8 +86,9 @@ typedef struct {
  * block id outside the pool, gets NaN and reads nothing there; a bad block of
  * a prefix makes its group's rows NaN.  Bytes of slots past a row's context
  * never reach its result.  Sums and softmax statistics are fp32 (a q . k that
- * overflows it makes its row NaN), the weights keep 16 significant bits; results of differently shaped calls agree to
- * fp32 rounding, not bit for bit; one call repeated gives the same bits.
+ * overflows it makes its row NaN), the weights keep 16 significant bits;
+ * results of differently shaped calls agree to fp32 rounding, not bit for bit;
+ * one call repeated gives the same bits.
  * Errors: HB_EINVAL, HB_ERANGE (bt_stride or workspace too small, max_ctx of
  * 2^27 or more, more than 65535 rows, more work than one launch holds),
  * HB_ECUDA.  n_rows = n_groups = 0 does nothing. */
@@ -115,7 +116,8 @@ long long hb_decode_shared_workspace(int n_rows, int n_heads, int n_kv_heads, in
  *                  zeros and whose weights stay as they are
  *   weights, weight_tables: device int32 [n_seqs][wt_stride], wt_stride >=
  *                  max_ctx / 16 + 1.  No two sequences of a call may have a
- *                  weight block in common: its slots would hold either's sums
+ *                  weight block in common, nor has one sequence a block twice:
+ *                  its slots would hold either's sums
  *   decay:         finite, in [0, 1]
  *   workspace:     as above, hb_decode_weigh_workspace() bytes (4 for each row,
  *                  head and key of max_ctx, and partial results)
@@ -169,11 +171,12 @@ int hb_evict_select(const hb_weight_pool *weights, const int32_t *weight_tables,
  *     [n_seqs][new_stride]; new_stride >= (keep + 15) / 16
  * A new block is either one that no sequence of the call reads, or the old
  * table's own at the same place (a cache compacted where it is: the two
- * tables may be the same memory), and no two sequences write the same block.
+ * tables may be the same memory), and no block is written twice.
  * The same holds for the weights' tables (strides wt_stride, new_wt_stride).
  * A position beyond the old table, or a block id outside the pool, old or new,
  * is skipped: the new slot stays as it was.
- * Errors: as for hb_evict_select. */
+ * Errors: as for hb_evict_select; HB_ERANGE also where num_blocks * n_kv_heads
+ * * 16 of either pool passes 2^32 - 2. */
 int hb_evict_move(const hb_paged_pool *pool, const int32_t *block_tables, int bt_stride, const int32_t *new_tables,
                   int new_stride, const int32_t *kept, int n_seqs, int keep, const hb_weight_pool *weights,
                   const int32_t *weight_tables, int wt_stride, const int32_t *new_weight_tables, int new_wt_stride,

@@ -557,6 +557,19 @@ def test_move_skips_what_lies_outside():
     assert np.array_equal(_f64(dv), ref.move(_f64(v), tables, new, kept))
 
 
+def test_move_of_few_tokens_skips_what_lies_outside():
+    """Many sequences that keep at most 32 tokens: a warp each."""
+    w, tables, new, k, v, kept = _move_case(4, 128, 3, [40 + j for j in range(12)], 20, "new")
+    tables[0, 1], new[1, 1], new[2, 0] = -1, k.shape[0], -3
+    tables[3, 0] = 1 << 30
+    kept[4, 0, 19] = 16 * tables.shape[1]  # beyond the table
+    dk, dv, dw = k.clone(), v.clone(), _dev(w, np.float32)
+    paged.evict_move(paged.PagedPool(dk, dv), _dev(tables), _dev(new), _dev(kept), dw, _dev(tables), _dev(new))
+    assert np.array_equal(_f64(dk), ref.move(_f64(k), tables, new, kept))
+    assert np.array_equal(_f64(dv), ref.move(_f64(v), tables, new, kept))
+    assert np.array_equal(dw.cpu().numpy(), ref.move(w, tables, new, kept))
+
+
 # ------------------------------------------------------------------ together
 
 def test_fork_decode_weigh_evict_and_decode_again():
@@ -667,3 +680,98 @@ def test_a_stream_of_its_own_wants_a_workspace_of_its_own():
     assert torch.equal(out, want)
     with pytest.raises(HbError):
         paged.decode_shared(*args, ws[:need - 16])
+
+
+class Chain:
+    """A decode behind a shared prefix, a window's weights over keys common to its rows, and an eviction by them."""
+
+    def __init__(self, seed):
+        self.c = c = Case(seed, 2, 4, 128, [20], [1500], [1500 + 13 * j for j in range(20)], poison=False)
+        assert 19 * 1488 * 2 * 512 >= SHARE
+        rng = np.random.default_rng(seed)
+        self.tables, self.ctx = _dev(np.where(c.tables < 0, 0, c.tables)), _dev(c.ctx)
+        self.lens = _dev([700, 1200])
+        self.q = _bf(rng, 32, 8, 128)
+        self.wt = torch.arange(2 * self.tables.shape[1], device="cuda", dtype=torch.int32).view(2, -1)
+        self.w = torch.zeros(self.wt.numel(), 2, 16, device="cuda")
+        self.out, self.out2 = torch.zeros_like(c.q), torch.zeros_like(self.q)
+        self.kept = torch.zeros(2, 2, 600, dtype=torch.int32, device="cuda")
+        self.ws = torch.empty(max(
+            paged.decode_shared_workspace(20, 8, 2, 128, 1747, c.rows, c.prefix),
+            paged.decode_weigh_workspace(2, 16, 8, 2, 128, 1200)), dtype=torch.uint8, device="cuda")
+
+    def step(self, stream=None):
+        c = self.c
+        paged.decode_shared(c.pool, c.q, self.tables, self.ctx, 1747, c.rows, c.prefix, self.out, self.ws, stream)
+        paged.decode_weigh(c.pool, self.q, self.tables[:2], self.lens, 1200, self.w, self.wt, 0.5, self.out2, self.ws,
+                           stream)
+        paged.evict_select(self.w, self.wt, self.lens, 1200, 600, 4, 32, self.kept, stream)
+
+    def results(self):
+        return [x.clone() for x in (self.out, self.out2, self.w, self.kept)]
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Two chains of calls on streams of their own, and as graphs that run side by side, each with its own workspace:
+    the bits that each gives alone."""
+    chains = [Chain(41), Chain(42)]
+    alone = []
+    for x in chains:
+        for _ in range(5):
+            x.step()
+        torch.cuda.synchronize()
+        alone.append(x.results())
+        x.c.check_large(x.out, rows=(0, 7, 19))
+    streams = [torch.cuda.Stream() for _ in chains]
+
+    def compare():
+        torch.cuda.synchronize()
+        for x, want in zip(chains, alone):
+            assert all(torch.equal(a, b) for a, b in zip(x.results(), want))
+            x.w.zero_()
+            for t in (x.out, x.out2, x.kept):
+                t.zero_()
+        torch.cuda.synchronize()
+
+    compare()
+    for _ in range(5):
+        for x, s in zip(chains, streams):
+            x.step(s)
+    compare()
+    graphs = []
+    for x in chains:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.step()
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    compare()
+
+
+def test_calls_that_follow_one_another_see_new_contents():
+    """Common keys: q, contexts and K are written by a kernel right before the call, again and again."""
+    x = Chain(43)
+    rng = np.random.default_rng(2)
+    qs = [_bf(rng, *x.c.q.shape) for _ in range(6)]
+    ctxs = [_dev(np.maximum(x.c.ctx - int(rng.integers(0, 40)), 1499)) for _ in qs]
+    ks = [x.c.k * f for f in (1.0, 0.5, 0.25, 2.0, 1.0, 0.5)]
+    want = []
+    for q, ctx, k in zip(qs, ctxs, ks):
+        for to, new in ((x.c.q, q), (x.ctx, ctx), (x.c.k, k)):
+            to.copy_(new)
+        torch.cuda.synchronize()
+        x.step()
+        torch.cuda.synchronize()
+        want.append(x.results())
+    x.w.zero_()
+    got = []
+    for q, ctx, k in zip(qs, ctxs, ks):
+        for to, new in ((x.c.k, k), (x.c.q, q), (x.ctx, ctx)):
+            to.copy_(new)
+        x.step()
+        got.append(x.results())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for p, r in zip(got, want) for a, b in zip(p, r))

@@ -100,6 +100,10 @@ def test_shared_refusals(L):
     assert need > 0 and _shared(L, wn=need - 1) == HB_ERANGE
     assert _shared(L, n=0, rows=[], pre=[], q=None, out=None, bt=None, ctx=None, ws=None, wn=0) == HB_OK
     assert paged.decode_shared_workspace(0, 4, 2, 64, 10, [], []) == 0
+    # a grid of 40000 heads x 65536 splits
+    with pytest.raises(HbError) as e:
+        paged.decode_shared_workspace(1, 40000, 40000, 64, (1 << 27) - 1, [1], [(1 << 27) - 1])
+    assert e.value.code == HB_ERANGE
     for bad, code in (((-1, 4, 2, 128, 10), HB_EINVAL), ((4, 3, 2, 128, 10), HB_EINVAL), ((4, 4, 2, 96, 10), HB_EINVAL),
                       ((4, 4, 2, 64, -1), HB_EINVAL), ((65536, 4, 2, 64, 10), HB_ERANGE),
                       ((4, 4, 2, 64, 1 << 27), HB_ERANGE)):
@@ -156,6 +160,9 @@ def test_move_refusals(L):
     for over in (dict(nstride=6), dict(n=65536), dict(keep=(1 << 27) + 1, nstride=1 << 24)):
         assert _move(L, **over) == HB_ERANGE, over
     assert _move(L, w=_weights(), nwstride=6) == HB_ERANGE
+    big = (1 << 27) - 1  # rows of a pool past 32 bits
+    assert _move(L, _pool(num_blocks=big, n_kv_heads=3)) == HB_ERANGE
+    assert _move(L, _pool(n_kv_heads=3), w=_weights(num_blocks=big, n_kv_heads=3)) == HB_ERANGE
     assert _move(L, n=0, bt=None, new=None, kept=None) == HB_OK
 
 
