@@ -29,8 +29,9 @@ constexpr int WARPS = 4;
 constexpr int JOIN_WARPS = 8;
 // A warp takes a tile's keys alone up to so many of them, where there are so many
 // tiles: 88 sequences of 15 to 177 keys, 16 queries and 16 kv heads, 44 us with
-// four warps a tile and 35 so; 18 rows of 1024 keys and 40 heads, 65 and 77.
-constexpr int ALONE_KEYS = 320;
+// four warps a tile and 35 so; 16 rows of 281 keys and 52 heads behind a prefix of
+// 4798, 46.4 and 52.8; 18 rows of 1024 keys and 40 heads, 65 and 77.
+constexpr int ALONE_KEYS = 192;
 constexpr long long ALONE_UNITS = 456;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SPLIT_MOST = 2048;     // and at most, where some rows are known to be long
