@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "kv4_host.h"
 #include "paged.h"
@@ -34,7 +35,6 @@ constexpr int JOIN_WARPS = 8;
 constexpr int ALONE_KEYS = 192;
 constexpr long long ALONE_UNITS = 456;
 constexpr int SPLIT_MIN = 256;       // keys of a split at least
-constexpr int SPLIT_MOST = 2048;     // and at most, where some rows are known to be long
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 24 << 20;  // of all groups
@@ -738,18 +738,27 @@ thread_local bool test_lose = false;  // of this thread's next launch of the com
 
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
-// Splits of `keys` keys (a multiple of 64 each) for `base` CTAs a split: as many
-// as the SMs hold at once, three each.  Where a row is known to have more than
-// SPLIT_MOST, which others may not, one CTA's way through them would take longest
-// (rows of 34 to 99 and one of 9500 keys, 40 heads: 120 us, 45 with the limit).
-void plan_splits(long long base, int keys, int known, int *len, int *n)
+// Splits of at most `keys` own keys (a multiple of 64 each) of n_rows rows with
+// `tiles` CTAs a split each: as many as the SMs hold at once, three each.  Where
+// rows differ, counted are those that there will be: by `sum` of the lengths that
+// the caller's prefixes tell, the longest of them `longest`.  A CTA's way through
+// its keys is then weighed against the CTAs of the other rows, which find nothing
+// to do: ROUND_US a round of 64 keys, for up to eight queries and for more, and
+// EMPTY_US.  (33 rows, two of 4000 to 5700 keys among them, 5 kv heads x 12: 62 us
+// with splits by the number of rows alone, 33 so; 21 rows, one of 4800, 40 heads:
+// 30 and 25, and 49 with splits of 256.)
+constexpr double ROUND_US[2] = {0.6, 1.1}, EMPTY_US = 1.55e-3;
+void plan_splits(long long n_rows, long long tiles, int keys, long long longest, long long sum, int nt, int *len, int *n)
 {
-    const long long want = 3 * SMS / (base > 0 ? base : 1);
-    long long s = keys / SPLIT_MIN;
-    s = s < want ? s : want;
+    const long long base = n_rows * tiles, most = keys / SPLIT_MIN;
+    long long s = 3 * SMS / (base > 0 ? base : 1);
+    const double least = sqrt((double)base * keys * 64 * EMPTY_US / ROUND_US[nt - 1]);
+    if (longest > least && sum < n_rows * keys) {
+        const long long w = (long long)(3. * SMS * keys / ((double)tiles * sum)), fit = (long long)(keys / least);
+        s = s > w || s > fit ? s : w < fit ? w : fit;
+    }
+    s = s < most ? s : most;
     s = s < 1 ? 1 : s;
-    if (known > SPLIT_MOST && s < (keys + SPLIT_MOST - 1) / SPLIT_MOST)
-        s = (keys + SPLIT_MOST - 1) / SPLIT_MOST;
     const long long each = round_up((keys + s - 1) / s, 64);
     *len = (int)(each > 0 ? each : 64);
     *n = (int)((keys + *len - 1) / *len);
@@ -783,6 +792,7 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
     static std::atomic<uint64_t> done{0};
     auto kernel = k_paged_attention<D, NT, SCORES, KW>;
     const long long units = (long long)p.n_kv * p.col_tiles;
+    // fits 31 bits: plan_splits() gives at most 3 SMS CTAs, a split a tile, or 2^11 sqrt(keys / tiles) splits
     const long long gx = (units * KW + WARPS - 1) / WARPS * p.n_splits;
     using S = Smem<D, NT>;
     constexpr int most = S::BYTES + (SCORES ? 4 * S::SCORES : 0);
@@ -880,12 +890,14 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     if (!group_rows || !prefix_lens || n_groups < 1)
         return HB_EINVAL;
     long long rows = 0;
+    int deepest = 0;
     for (int i = 0; i < n_groups; ++i) {
         if (group_rows[i] < 1 || prefix_lens[i] < 0)
             return HB_EINVAL;
         if (prefix_lens[i] > max_ctx + 1)
             return HB_ERANGE;
         rows += group_rows[i];
+        deepest = prefix_lens[i] > deepest ? prefix_lens[i] : deepest;
     }
     if (rows != n_rows)
         return HB_EINVAL;
@@ -935,7 +947,8 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     }
     hi = hi > units / SMS ? hi : units / SMS;
     long long ctas = 0;
-    int row = 0, parts = 0, most = 0, known = 0;  // most, least of the own keys of the longest row
+    int row = 0, parts = 0, most = 0, longest = 0;  // own keys of a row at most, and as the prefixes tell
+    long long sum = 0;
     for (int i = 0; i < n_groups; ++i) {
         Group gr = shared_group(row, group_rows[i], prefix_lens[i], n_kv, d, can);
         const long long n = cut_group(&gr, g, n_kv, hi);
@@ -945,16 +958,16 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
         ctas += n;
         parts = gr.parts > parts ? gr.parts : parts;
         most = max_ctx + 1 - gr.shared > most ? max_ctx + 1 - gr.shared : most;
-        known = gr.prefix - gr.shared > known ? gr.prefix - gr.shared : known;
+        const int mine = gr.prefix - gr.shared + max_ctx + 1 - deepest;
+        longest = mine > longest ? mine : longest;
+        sum += (long long)gr.rows * mine;
         row += gr.rows;
         each(i, gr);
     }
     pl->ctas = (int)ctas;
     pl->nt = g > 8 ? 2 : 1;
     pl->col_tiles = tiles_of(g, pl->nt);
-    plan_splits((long long)n_rows * n_kv * pl->col_tiles, most, known, &pl->split_len, &pl->n_splits);
-    if ((long long)n_kv * pl->col_tiles * pl->n_splits > 0x7fffffffll)  // CTAs of a row
-        return HB_ERANGE;
+    plan_splits(n_rows, (long long)n_kv * pl->col_tiles, most, longest, sum, pl->nt, &pl->split_len, &pl->n_splits);
     pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->seq_parts = pl->seq_part_len = 0;
@@ -989,7 +1002,7 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     }
     // what is left with them: the last rows' own positions and less than a block
     const int own = pl->ctas > 0 && nq + 15 < max_ctx + 1 ? nq + 15 : max_ctx + 1;
-    plan_splits(n_seqs * n_kv * pl->col_tiles, own, 0, &pl->split_len, &pl->n_splits);
+    plan_splits(n_seqs, (long long)n_kv * pl->col_tiles, own, own, n_seqs * own, pl->nt, &pl->split_len, &pl->n_splits);
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->direct = pl->n_slots == 1;
     pl->fused = pl->direct && pl->col_tiles == 1;

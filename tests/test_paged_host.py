@@ -100,10 +100,8 @@ def test_shared_refusals(L):
     assert need > 0 and _shared(L, wn=need - 1) == HB_ERANGE
     assert _shared(L, n=0, rows=[], pre=[], q=None, out=None, bt=None, ctx=None, ws=None, wn=0) == HB_OK
     assert paged.decode_shared_workspace(0, 4, 2, 64, 10, [], []) == 0
-    # a grid of 40000 heads x 65536 splits
-    with pytest.raises(HbError) as e:
-        paged.decode_shared_workspace(1, 40000, 40000, 64, (1 << 27) - 1, [1], [(1 << 27) - 1])
-    assert e.value.code == HB_ERANGE
+    # the most keys there can be: a few splits of 40000 heads, which are tiles enough
+    assert paged.decode_shared_workspace(1, 40000, 40000, 64, (1 << 27) - 1, [1], [(1 << 27) - 1]) < 1 << 30
     for bad, code in (((-1, 4, 2, 128, 10), HB_EINVAL), ((4, 3, 2, 128, 10), HB_EINVAL), ((4, 4, 2, 96, 10), HB_EINVAL),
                       ((4, 4, 2, 64, -1), HB_EINVAL), ((65536, 4, 2, 64, 10), HB_ERANGE),
                       ((4, 4, 2, 64, 1 << 27), HB_ERANGE)):
