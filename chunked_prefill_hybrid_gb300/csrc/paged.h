@@ -12,6 +12,9 @@ namespace paged {
 
 constexpr int MAX_KEYS = 1 << 27;
 constexpr int INLINE_GROUPS = 16;  // groups that fit the kernels' parameters
+constexpr int SLOTS = 3 * 152;     // CTAs of the own keys' kernel that run at once
+constexpr int SPLIT_MIN = 256;     // keys of a split at least
+constexpr int BALANCE_SEQS = 256;
 
 // Rows row0..row0 + rows - 1; prefix: tokens that they share, as the caller
 // says; shared: those of them that are attended once for the group, in whole
@@ -45,7 +48,8 @@ struct Attn {
     const int *ctx_lens;
     int max_ctx, n_seqs, nq;   // n_seqs: entries of ctx_lens
     float c2;                  // log2(e) / sqrt(d): weights are 2^((s - m) c2)
-    int split_len, n_splits;   // of a row's own keys
+    int split_len, n_splits;   // of a row's own keys, unless
+    bool balance;              // splits go by the lengths that the sequences have, BALANCE_SEQS of them at most
     int col_tiles;             // CTAs of the queries of a kv head
     int first_slot, n_slots;   // partials of a row: those of the common part, then from first_slot on its own splits
     bool direct;               // a row has one partial, which is its result
@@ -78,6 +82,39 @@ struct Attn {
                 hi = mid - 1;
         }
         return at(lo);
+    }
+    // balance: keys of a split, by a whole warp.  As many CTAs as run at once for all
+    // keys there are, or with up to twice as many keys each where the rows' last
+    // splits, which are not full, would make more of them; n_splits hold the longest.
+    __device__ __forceinline__ int balanced() const
+    {
+        constexpr int EACH = BALANCE_SEQS / 32;
+        const int tiles = n_kv * col_tiles;
+        int subs[EACH], sum = 0, most = 0;  // sub-tiles of 64 keys
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int j = i * 32 + (int)(threadIdx.x & 31);
+            const int ctx = j < n_seqs ? ctx_lens[j] : -1;
+            subs[i] = ctx < 0 || ctx > max_ctx ? 0 : (ctx + 64) >> 6;
+            sum += subs[i];
+            most = max(most, subs[i]);
+        }
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int least = max(SPLIT_MIN / 64, (most + n_splits - 1) / n_splits);
+        int len = 0;
+#pragma unroll 1
+        for (int c = 8; c <= 16; ++c) {
+            len = max(least, (int)(((long long)sum * tiles * c + 8 * SLOTS - 1) / (8 * SLOTS)));
+            const float inv = __frcp_rn((float)len);
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                n += (int)ceilf(__fmul_rn(subs[i] - 0.5f, inv));
+            if (__reduce_add_sync(0xffffffffu, n) * tiles <= SLOTS)
+                break;
+        }
+        return len * 64;
     }
     // A sequence's rows as a group: common are the whole blocks that all of
     // them see.  Its context is in range.

@@ -34,7 +34,6 @@ constexpr int JOIN_WARPS = 8;
 // 4798, 46.4 and 52.8; 18 rows of 1024 keys and 40 heads, 65 and 77.
 constexpr int ALONE_KEYS = 192;
 constexpr long long ALONE_UNITS = 456;
-constexpr int SPLIT_MIN = 256;       // keys of a split at least
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 24 << 20;  // of all groups
@@ -188,7 +187,7 @@ __device__ __forceinline__ void put_weights(const Attn &p, float *to, float4 old
 // with a ring and a softmax of its own, and join their results in shared memory.
 // KW = 1, for many queries or few keys: each warp has a tile of its own, or a kv
 // head, and all pages.
-template <int D, int NT, bool SCORES, int KW>
+template <int D, int NT, bool SCORES, int KW, bool BALANCE>
 __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_constant__ Attn p)
 {
     using R = Ring<D>;
@@ -242,7 +241,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             }
         return leave();
     }
-    const int k0 = from + split * p.split_len, k1 = min(ctx + 1, k0 + p.split_len);
+    const int split_len = BALANCE ? p.balanced() : p.split_len;
+    const int k0 = from + split * split_len, k1 = min(ctx + 1, k0 + split_len);
     if (k0 >= k1 || (KW == 1 && kvh >= p.n_kv))
         return leave();  // the join knows how many splits a row has
 
@@ -542,12 +542,13 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
 
 // The join of a row's partials, those of the common keys and of its own splits:
 // W warps a (row, head), each with every W-th partial.
-template <int D, int W>
+template <int D, int W, bool BALANCE>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
 {
     constexpr int E = D / 32;
     constexpr int BATCH = 4;  // partials whose loads are under way together
     __shared__ float s_o[W > 1 ? JOIN_WARPS : 1][D];
+    const int split_len = BALANCE ? p.balanced() : p.split_len;  // the contexts were there before the kernel before this one
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
         parts = gr.parts;
     }
     const bool sees = ctx + 1 - (p.nq - 1) + row % p.nq > 0;
-    const int n = in ? parts + (ctx + 1 - from + p.split_len - 1) / p.split_len : 0;
+    const int n = in ? parts + (ctx + 1 - from + split_len - 1) / split_len : 0;
     const size_t first = ((size_t)row * p.n_heads + head) * p.n_slots;
     auto slot = [&](int i) { return first + (i < parts ? i : p.first_slot + i - parts); };
     // (m, l) of the first 32 partials, a lane each, and the greatest m of all
@@ -751,10 +752,10 @@ constexpr double ROUND_US[2] = {0.6, 1.1}, EMPTY_US = 1.55e-3;
 void plan_splits(long long n_rows, long long tiles, int keys, long long longest, long long sum, int nt, int *len, int *n)
 {
     const long long base = n_rows * tiles, most = keys / SPLIT_MIN;
-    long long s = 3 * SMS / (base > 0 ? base : 1);
+    long long s = SLOTS / (base > 0 ? base : 1);
     const double least = sqrt((double)base * keys * 64 * EMPTY_US / ROUND_US[nt - 1]);
     if (longest > least && sum < n_rows * keys) {
-        const long long w = (long long)(3. * SMS * keys / ((double)tiles * sum)), fit = (long long)(keys / least);
+        const long long w = (long long)((double)SLOTS * keys / ((double)tiles * sum)), fit = (long long)(keys / least);
         s = s > w || s > fit ? s : w < fit ? w : fit;
     }
     s = s < most ? s : most;
@@ -786,11 +787,11 @@ Layout layout(long long rows, int heads, int d, int slots, bool parts, int group
 
 int tiles_of(long long cols, int nt) { return (int)((cols + 8 * nt - 1) / (8 * nt)); }
 
-template <int D, int NT, bool SCORES, int KW>
+template <int D, int NT, bool SCORES, int KW, bool BALANCE>
 int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
 {
     static std::atomic<uint64_t> done{0};
-    auto kernel = k_paged_attention<D, NT, SCORES, KW>;
+    auto kernel = k_paged_attention<D, NT, SCORES, KW, BALANCE>;
     const long long units = (long long)p.n_kv * p.col_tiles;
     // fits 31 bits: plan_splits() gives at most 3 SMS CTAs, a split a tile, or 2^11 sqrt(keys / tiles) splits
     const long long gx = (units * KW + WARPS - 1) / WARPS * p.n_splits;
@@ -810,19 +811,21 @@ bool alone(const Attn &p, int n_seqs)
     return p.split_len <= ALONE_KEYS && (long long)n_seqs * p.n_kv * p.col_tiles >= ALONE_UNITS;
 }
 
-template <int D, bool SCORES>
-int attention_of(const Attn &p, int nt, int n_seqs, cudaStream_t s)
+template <int D, int NT, bool SCORES>
+int attention_of(const Attn &p, int n_seqs, cudaStream_t s)
 {
-    if (alone(p, n_seqs))
-        return nt == 1 ? launch_attention<D, 1, SCORES, 1>(p, n_seqs, s) : launch_attention<D, 2, SCORES, 1>(p, n_seqs, s);
-    return nt == 1 ? launch_attention<D, 1, SCORES, WARPS>(p, n_seqs, s)
-                   : launch_attention<D, 2, SCORES, WARPS>(p, n_seqs, s);
+    if (p.balance)  // at most SLOTS / 2 tiles: too few for a warp each
+        return launch_attention<D, NT, SCORES, WARPS, true>(p, n_seqs, s);
+    return alone(p, n_seqs) ? launch_attention<D, NT, SCORES, 1, false>(p, n_seqs, s)
+                            : launch_attention<D, NT, SCORES, WARPS, false>(p, n_seqs, s);
 }
 
 template <bool SCORES>
 int attention(const Attn &p, int d, int nt, int n_seqs, cudaStream_t s)
 {
-    return d == 128 ? attention_of<128, SCORES>(p, nt, n_seqs, s) : attention_of<64, SCORES>(p, nt, n_seqs, s);
+    if (d == 128)
+        return nt == 1 ? attention_of<128, 1, SCORES>(p, n_seqs, s) : attention_of<128, 2, SCORES>(p, n_seqs, s);
+    return nt == 1 ? attention_of<64, 1, SCORES>(p, n_seqs, s) : attention_of<64, 2, SCORES>(p, n_seqs, s);
 }
 
 // Checks that the attention calls share.  rows: of q and out.
@@ -850,10 +853,24 @@ int check_attention(const hb_paged_pool *pool, const void *q, long long q_stride
 struct Plan {
     int nt, split_len, n_splits, col_tiles, first_slot, n_slots;
     int ctas;  // of the common keys' kernel
+    bool balance;
     int seq_parts, seq_part_len;
     bool direct, fused;
     Layout at;
 };
+
+// Where all keys are the rows' own, splits go by the lengths that the rows have
+// (Attn::balanced), with twice as many of them as rows of one length have, for those
+// longer than the others (us): one row of 4000 keys, 8 kv heads x 8, in a call that
+// allows 131071, 32 with splits by max_ctx and 10 so; weights of 6 sequences of 2517
+// to 40293 keys, 4 kv heads x 5, 47 and 34; of 20 of 5928 keys, 5 kv heads, 55 and 58.
+void balance(long long n_seqs, long long tiles, int keys, Plan *pl)
+{
+    const long long room = 2ll * pl->n_splits, all = SLOTS / tiles, most = keys / SPLIT_MIN;
+    const long long n = room < all ? room : all, m = n < most ? n : most;
+    pl->balance = true;
+    pl->n_splits = n_seqs > 1 && m > pl->n_splits ? (int)m : pl->n_splits;
+}
 
 // Bytes that are read once only if a group's whole blocks are shared.
 long long saved_bytes(int rows, int prefix, int n_kv, int d) { return (long long)(rows - 1) * (prefix & ~15) * n_kv * 4 * d; }
@@ -968,6 +985,9 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     pl->nt = g > 8 ? 2 : 1;
     pl->col_tiles = tiles_of(g, pl->nt);
     plan_splits(n_rows, (long long)n_kv * pl->col_tiles, most, longest, sum, pl->nt, &pl->split_len, &pl->n_splits);
+    pl->balance = false;  // unless the prefixes tell that some rows are longer
+    if (ctas == 0 && pl->n_splits > 1 && n_rows <= BALANCE_SEQS && sum == (long long)n_rows * most)
+        balance(n_rows, (long long)n_kv * pl->col_tiles, most, pl);
     pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->seq_parts = pl->seq_part_len = 0;
@@ -1003,6 +1023,9 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     // what is left with them: the last rows' own positions and less than a block
     const int own = pl->ctas > 0 && nq + 15 < max_ctx + 1 ? nq + 15 : max_ctx + 1;
     plan_splits(n_seqs, (long long)n_kv * pl->col_tiles, own, own, n_seqs * own, pl->nt, &pl->split_len, &pl->n_splits);
+    pl->balance = false;
+    if (pl->ctas == 0 && pl->n_splits > 1 && n_seqs <= BALANCE_SEQS)
+        balance(n_seqs, (long long)n_kv * pl->col_tiles, own, pl);
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->direct = pl->n_slots == 1;
     pl->fused = pl->direct && pl->col_tiles == 1;
@@ -1031,6 +1054,7 @@ void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_strid
     p.c2 = LOG2E / sqrtf((float)pool->head_dim);
     p.split_len = pl.split_len;
     p.n_splits = pl.n_splits;
+    p.balance = pl.balance;
     p.col_tiles = pl.col_tiles;
     p.first_slot = pl.first_slot;
     p.n_slots = pl.n_slots;
@@ -1047,17 +1071,23 @@ void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_strid
     p.score_stride = pl.at.score_stride;
 }
 
+template <int D, int W>
+int launch_join(const Attn &p, int rows, cudaStream_t s)
+{
+    const long long blocks = ((long long)rows * p.n_heads * W + JOIN_WARPS - 1) / JOIN_WARPS;
+    return launch_kernel(true, p.balance ? k_paged_join<D, W, true> : k_paged_join<D, W, false>, dim3((unsigned)blocks),
+                         dim3(JOIN_WARPS * 32), 0, s, p, rows) == cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
+}
+
 int launch_join(const Attn &p, int d, int rows, cudaStream_t s)
 {
     // all warps of a CTA for a row and head where there are few, with many partials
-    const long long items = (long long)rows * p.n_heads;
-    const bool wide = items < 4 * SMS && p.n_slots > 8;
-    const long long blocks = wide ? items : (items + JOIN_WARPS - 1) / JOIN_WARPS;
-    auto kernel = d == 128 ? (wide ? k_paged_join<128, JOIN_WARPS> : k_paged_join<128, 1>)
-                           : (wide ? k_paged_join<64, JOIN_WARPS> : k_paged_join<64, 1>);
-    return launch_kernel(true, kernel, dim3((unsigned)blocks), dim3(JOIN_WARPS * 32), 0, s, p, rows) == cudaSuccess
-               ? HB_OK
-               : HB_ECUDA;
+    const bool wide = (long long)rows * p.n_heads < 4 * SMS && p.n_slots > 8;
+    if (d == 128)
+        return wide ? launch_join<128, JOIN_WARPS>(p, rows, s) : launch_join<128, 1>(p, rows, s);
+    return wide ? launch_join<64, JOIN_WARPS>(p, rows, s) : launch_join<64, 1>(p, rows, s);
 }
 
 int check_workspace(const void *workspace, long long bytes, long long need)

@@ -365,6 +365,30 @@ def test_weigh_matches_the_plain_form(kv, group, d, ctx, nq, decay):
     assert (np.abs(_f64(far[0]) - o) <= b).all() and (np.abs(_f64(far[1]) - want) <= wb)[touched].all()
 
 
+@pytest.mark.parametrize("kv,group,d,ctx,nq,max_ctx", [
+    (1, 1, 64, [9000, 3, 700], 1, 9000),                      # one long row has most splits
+    (2, 2, 64, [5000, 4999, 64, 63, -1, 0], 2, 20000),        # far below what the call allows
+    (1, 4, 128, [2000], 1, 60000),
+    (1, 1, 64, [-1, -1], 1, 8000),                            # padding alone
+    (1, 1, 64, [12000] + [5] * 99, 1, 12000),                 # the splits of one row are all there are
+    (1, 1, 64, [40 + 7 * j for j in range(200)], 1, 4000),
+    (1, 1, 64, [900] * 227, 1, 1700),                         # no room for more CTAs than rows
+    (1, 1, 64, [900] * 257, 1, 70000),                        # more sequences than are looked at
+])
+def test_weigh_splits_by_the_lengths_there_are(kv, group, d, ctx, nq, max_ctx):
+    c = _weigh_case(len(ctx) + ctx[0] + 7, kv, group, d, ctx, nq)
+    o, b, want, wb = ref.weigh(_f64(c.q), _f64(c.k), _f64(c.v), c.tables, c.ctx, group, nq, _f64(c.w), c.wtables, 0.5)
+    out, w = _weigh(c, nq, 0.5, max_ctx=max_ctx)
+    assert (np.abs(_f64(out) - o) <= b).all()
+    assert (np.abs(_f64(w) - want) <= wb)[wb > 0].all()
+    assert np.array_equal(_f64(w)[wb == 0], _f64(c.w)[wb == 0])
+    beyond = np.where(np.arange(len(ctx)) == 0, max_ctx + 1, c.ctx)  # the first out of its range: NaN, and it counts for nothing
+    out2, w2 = _weigh(c, nq, 0.5, max_ctx=max_ctx, ctx=beyond)
+    assert torch.isnan(out2[:nq]).all() and (np.abs(_f64(out2) - o) <= b)[nq:].all()
+    mine = c.wtables[0][c.wtables[0] >= 0]
+    assert torch.equal(w2[mine], c.w[mine])
+
+
 def test_weigh_new_tokens_start_from_zero():
     c = _weigh_case(3, 2, 2, 64, [40, 20], 3)
     dirty = c.w.clone()
