@@ -50,6 +50,7 @@ constexpr int OWN_UNIT = 20480, OWN_UNIT_BESIDE = 30720;
 // 93; 4 of 40 kv heads x 32 queries at 600 keys 35 and 29, at 3000 104 and 107.
 constexpr int COMMON_MIN = 8, COMMON_MIN_FEW = 24;
 constexpr int WEIGH_THREADS = 256;
+constexpr int JOIN_CTAS = 2 * SMS;   // CTAs of weights up to which their kernel takes the join along
 constexpr float LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
@@ -542,17 +543,14 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
 
 // The join of a row's partials, those of the common keys and of its own splits:
 // W warps a (row, head), each with every W-th partial.
-template <int D, int W, bool BALANCE>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
+template <int D, int W>
+__device__ __forceinline__ void join(const Attn &p, int split_len, int block, int n_rows)
 {
     constexpr int E = D / 32;
     constexpr int BATCH = 4;  // partials whose loads are under way together
     __shared__ float s_o[W > 1 ? JOIN_WARPS : 1][D];
-    const int split_len = BALANCE ? p.balanced() : p.split_len;  // the contexts were there before the kernel before this one
-    pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
-    const long long item = (long long)blockIdx.x * (JOIN_WARPS / W) + warp / W;
+    const long long item = (long long)block * (JOIN_WARPS / W) + warp / W;
     if (W < JOIN_WARPS && item >= (long long)n_rows * p.n_heads)
         return;
     const int row = (int)(item / p.n_heads), head = (int)(item % p.n_heads);
@@ -646,19 +644,46 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
         p.final_ml[(size_t)row * p.n_heads + head] = make_float2(base, sum > 0.f ? 1.f / sum : 0.f);
 }
 
-// The weights of a kv head's keys, summed over its queries' scores: four keys a
-// thread, and SHARES threads for the queries of the same keys.
-template <int SHARES>
-__global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_constant__ Attn p, int chunks)
+template <int D, int W, bool BALANCE>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_constant__ Attn p, int n_rows)
 {
-    constexpr int QUADS = WEIGH_THREADS / SHARES, BATCH = 8, CHUNK = 256;
+    const int split_len = BALANCE ? p.balanced() : p.split_len;  // the contexts were there before the kernel before this one
+    pdl_wait();
+    pdl_trigger();
+    join<D, W>(p, split_len, blockIdx.x, n_rows);
+}
+
+// The weights of a kv head's keys, summed over its queries' scores: four keys a
+// thread, and SHARES threads for the queries of the same keys.  The (m, l) of the
+// rows come from the join's kernel before this one, and the first scores are fetched
+// while it runs.  JOIN, for few CTAs: the join runs in this kernel's first CTAs,
+// and each of the others joins the (m, l) that it needs for itself, so that neither
+// waits for the other (us, as chosen and the other way: 2 rows of 30550 keys, 4
+// heads, 14.0 and 16.4; one of 131000, 8 x 8 heads, 101.5 and 107.9; 2 x 32
+// queries, 8 x 4 heads, 27.7 and 30.0).
+template <int SHARES, bool JOIN, int D, int W>
+__global__ void __launch_bounds__(WEIGH_THREADS)
+    k_paged_weigh(const __grid_constant__ Attn p, int n_rows, int join_blocks, int chunks)
+{
+    constexpr int QUADS = WEIGH_THREADS / SHARES, BATCH = 8, CHUNK = 256, LANES = 8;
+    static_assert(WEIGH_THREADS == JOIN_WARPS * 32);
     __shared__ float2 s_ml[CHUNK];
     __shared__ float4 s_a[SHARES > 1 ? SHARES - 1 : 1][QUADS];
-    const int seq = blockIdx.y;
-    const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-    // When this kernel starts the one before it has passed its wait: what was
-    // there before that one can be read, old weights and (where it is the join)
-    // scores; only its own results not yet
+    const int split_len = JOIN ? p.balanced() : 0;  // JOIN: at most 16 queries a kv head, no common keys, several splits
+    if constexpr (JOIN)
+        if ((int)blockIdx.x < join_blocks) {
+            pdl_wait();
+            pdl_trigger();
+            return join<D, W>(p, split_len, blockIdx.x, n_rows);
+        }
+    int seq = blockIdx.y, kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+    if constexpr (JOIN) {  // all in one row of the grid
+        const int at = (int)blockIdx.x - join_blocks;
+        seq = at / (p.n_kv * chunks), kvh = at / chunks % p.n_kv, chunk = at % chunks;
+    }
+    // When this kernel starts those before it have passed their waits: what was
+    // there before the last of them can be read, old weights and (where that is the
+    // join) scores; only its own results not yet
     const int ctx = p.ctx_lens[seq];
     const int quad = threadIdx.x % QUADS, share = threadIdx.x / QUADS;
     const int key = (chunk * QUADS + quad) * 4;
@@ -682,27 +707,58 @@ __global__ void __launch_bounds__(WEIGH_THREADS) k_paged_weigh(const __grid_cons
                 v[u] = __ldcg(reinterpret_cast<const float4 *>(at));
     };
     const int each0 = (min(CHUNK, ncols) + SHARES - 1) / SHARES;  // of the first chunk
-    if (!p.direct && some)
+    const bool early = !JOIN && !p.direct;
+    if (early && some)
         load(share * each0, min(min(CHUNK, ncols), (share + 1) * each0));
     pdl_wait();
     pdl_trigger();
     if (none)
         return;
+    if (!early && some)
+        load(share * each0, min(min(CHUNK, ncols), (share + 1) * each0));
+    const Group gr = p.sequence(seq, ctx);
+    const int parts = gr.parts, n_parts = parts + (ctx + 1 - gr.shared + split_len - 1) / split_len;
     float a[4] = {0.f, 0.f, 0.f, 0.f};
     for (int q0 = 0; q0 < ncols; q0 += CHUNK) {
         const int n = min(CHUNK, ncols - q0), each = (n + SHARES - 1) / SHARES;
         if (q0 > 0)
             __syncthreads();  // the chunk before is done with
-        for (int c = threadIdx.x; c < n; c += WEIGH_THREADS) {
+        auto row_head = [&](int c) {
             const int i = (q0 + c) / p.group;
-            s_ml[c] = __ldcg(p.final_ml + ((size_t)seq * p.nq + i) * p.n_heads + kvh * p.group + (q0 + c - i * p.group));
+            return ((size_t)seq * p.nq + i) * p.n_heads + kvh * p.group + (q0 + c - i * p.group);
+        };
+        if constexpr (!JOIN) {
+            for (int c = threadIdx.x; c < n; c += WEIGH_THREADS)
+                s_ml[c] = __ldcg(p.final_ml + row_head(c));
+        } else {  // LANES threads a query, each with every LANES-th partial
+            for (int b = 0; b < n; b += WEIGH_THREADS / LANES) {
+                const int c = b + (int)threadIdx.x / LANES;
+                const float2 *ml = p.part_ml + row_head(min(c, n - 1)) * p.n_slots;
+                float m = -INFINITY, l = 0.f;
+                auto add = [&](float m1, float l1) {
+                    const float mx = fmaxf(m, m1), base = mx == -INFINITY ? 0.f : mx;
+                    l = l * ex2((m - base) * p.c2) + l1 * ex2((m1 - base) * p.c2);
+                    m = mx;
+                };
+#pragma unroll 4
+                for (int x = threadIdx.x % LANES; x < n_parts; x += LANES) {
+                    const float2 y = __ldcg(ml + (x < parts ? x : p.first_slot + x - parts));
+                    add(y.x, y.y);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int x = 1; x < LANES; x <<= 1)
+                    add(__shfl_xor_sync(0xffffffffu, m, x), __shfl_xor_sync(0xffffffffu, l, x));
+                if (threadIdx.x % LANES == 0 && c < n)
+                    s_ml[c] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
+            }
         }
         __syncthreads();
         if (!some)
             continue;
         const int c1 = min(n, (share + 1) * each);
         for (int c0 = share * each; c0 < c1; c0 += BATCH) {
-            if (q0 > 0 || c0 > share * each || p.direct)
+            if (q0 > 0 || c0 > share * each)
                 load(q0 + c0, q0 + c1);
 #pragma unroll
             for (int u = 0; u < BATCH; ++u)
@@ -868,6 +924,7 @@ void balance(long long n_seqs, long long tiles, int keys, Plan *pl)
 {
     const long long room = 2ll * pl->n_splits, all = SLOTS / tiles, most = keys / SPLIT_MIN;
     const long long n = room < all ? room : all, m = n < most ? n : most;
+    static_assert(SLOTS / 2 <= BALANCE_SEQS);  // with two splits each no more of them have room
     pl->balance = true;
     pl->n_splits = n_seqs > 1 && m > pl->n_splits ? (int)m : pl->n_splits;
 }
@@ -986,7 +1043,7 @@ int plan_shared(int n_rows, int n_heads, int n_kv, int d, int num_blocks, int ma
     pl->col_tiles = tiles_of(g, pl->nt);
     plan_splits(n_rows, (long long)n_kv * pl->col_tiles, most, longest, sum, pl->nt, &pl->split_len, &pl->n_splits);
     pl->balance = false;  // unless the prefixes tell that some rows are longer
-    if (ctas == 0 && pl->n_splits > 1 && n_rows <= BALANCE_SEQS && sum == (long long)n_rows * most)
+    if (ctas == 0 && pl->n_splits > 1 && sum == (long long)n_rows * most)
         balance(n_rows, (long long)n_kv * pl->col_tiles, most, pl);
     pl->first_slot = parts;
     pl->n_slots = pl->first_slot + pl->n_splits;
@@ -1024,7 +1081,7 @@ int plan_weigh(long long n_seqs, int nq, int n_heads, int n_kv, int d, int num_b
     const int own = pl->ctas > 0 && nq + 15 < max_ctx + 1 ? nq + 15 : max_ctx + 1;
     plan_splits(n_seqs, (long long)n_kv * pl->col_tiles, own, own, n_seqs * own, pl->nt, &pl->split_len, &pl->n_splits);
     pl->balance = false;
-    if (pl->ctas == 0 && pl->n_splits > 1 && n_seqs <= BALANCE_SEQS)
+    if (pl->ctas == 0 && pl->n_splits > 1)
         balance(n_seqs, (long long)n_kv * pl->col_tiles, own, pl);
     pl->n_slots = pl->first_slot + pl->n_splits;
     pl->direct = pl->n_slots == 1;
@@ -1071,23 +1128,63 @@ void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_strid
     p.score_stride = pl.at.score_stride;
 }
 
+// All warps of a CTA of the join for a row and head where there are few, with many partials.
+bool wide_join(const Attn &p, int rows) { return (long long)rows * p.n_heads < 4 * SMS && p.n_slots > 8; }
+
+long long join_blocks(const Attn &p, int rows, int warps)
+{
+    return ((long long)rows * p.n_heads * warps + JOIN_WARPS - 1) / JOIN_WARPS;
+}
+
 template <int D, int W>
 int launch_join(const Attn &p, int rows, cudaStream_t s)
 {
-    const long long blocks = ((long long)rows * p.n_heads * W + JOIN_WARPS - 1) / JOIN_WARPS;
-    return launch_kernel(true, p.balance ? k_paged_join<D, W, true> : k_paged_join<D, W, false>, dim3((unsigned)blocks),
-                         dim3(JOIN_WARPS * 32), 0, s, p, rows) == cudaSuccess
+    return launch_kernel(true, p.balance ? k_paged_join<D, W, true> : k_paged_join<D, W, false>,
+                         dim3((unsigned)join_blocks(p, rows, W)), dim3(JOIN_WARPS * 32), 0, s, p, rows) == cudaSuccess
                ? HB_OK
                : HB_ECUDA;
 }
 
 int launch_join(const Attn &p, int d, int rows, cudaStream_t s)
 {
-    // all warps of a CTA for a row and head where there are few, with many partials
-    const bool wide = (long long)rows * p.n_heads < 4 * SMS && p.n_slots > 8;
     if (d == 128)
-        return wide ? launch_join<128, JOIN_WARPS>(p, rows, s) : launch_join<128, 1>(p, rows, s);
-    return wide ? launch_join<64, JOIN_WARPS>(p, rows, s) : launch_join<64, 1>(p, rows, s);
+        return wide_join(p, rows) ? launch_join<128, JOIN_WARPS>(p, rows, s) : launch_join<128, 1>(p, rows, s);
+    return wide_join(p, rows) ? launch_join<64, JOIN_WARPS>(p, rows, s) : launch_join<64, 1>(p, rows, s);
+}
+
+// Threads for the queries of the same keys: with more than sixteen queries of a kv head eight.
+int weigh_shares(int cols) { return cols > 16 ? 8 : 1; }
+
+template <int SHARES, bool JOIN, int D, int W>
+int launch_weigh(const Attn &p, int rows, int chunks, cudaStream_t s)
+{
+    const long long blocks = (long long)p.n_kv * chunks, first = JOIN ? join_blocks(p, rows, W) : 0;
+    const dim3 grid = JOIN ? dim3((unsigned)(first + blocks * p.n_seqs)) : dim3((unsigned)blocks, (unsigned)p.n_seqs);
+    return launch_kernel(true, k_paged_weigh<SHARES, JOIN, D, W>, grid, dim3(WEIGH_THREADS), 0, s, p, rows,
+                         (int)first, chunks) == cudaSuccess
+               ? HB_OK
+               : HB_ECUDA;
+}
+
+template <int D>
+int launch_weigh_and_join(const Attn &p, int rows, int chunks, cudaStream_t s)
+{
+    return wide_join(p, rows) ? launch_weigh<1, true, D, JOIN_WARPS>(p, rows, chunks, s)
+                              : launch_weigh<1, true, D, 1>(p, rows, chunks, s);
+}
+
+// The rows' results and the weights after the attention, `chunks` CTAs of weights a
+// sequence's kv head.
+int finish_weigh(const Attn &p, int d, int rows, int chunks, cudaStream_t s)
+{
+    const int shares = weigh_shares(p.nq * p.group);
+    if (p.balance && shares == 1 && (long long)p.n_seqs * p.n_kv * chunks <= JOIN_CTAS)
+        return d == 128 ? launch_weigh_and_join<128>(p, rows, chunks, s)
+                        : launch_weigh_and_join<64>(p, rows, chunks, s);
+    const int rc = p.direct ? HB_OK : launch_join(p, d, rows, s);
+    if (rc)
+        return rc;
+    return shares > 1 ? launch_weigh<8, false, 0, 0>(p, rows, chunks, s) : launch_weigh<1, false, 0, 0>(p, rows, chunks, s);
 }
 
 int check_workspace(const void *workspace, long long bytes, long long need)
@@ -1269,10 +1366,8 @@ try {
            workspace);
     p.n_seqs = n_seqs;
     p.weigh = Weigh{weights->data, weights->num_blocks, weight_tables, wt_stride, decay};
-    const bool many = n_queries * p.group > 16;  // queries of a kv head: eight threads for them
-    const int chunks = max_ctx / (WEIGH_THREADS / (many ? 8 : 1) * 4) + 1;
-    const long long gx = (long long)p.n_kv * chunks;
-    if (gx > 0x7fffffffll)
+    const int chunks = max_ctx / (WEIGH_THREADS / weigh_shares(n_queries * p.group) * 4) + 1;
+    if ((long long)p.n_kv * chunks > 0x7fffffffll)
         return HB_ERANGE;
     if (!pl.fused)
         p.final_ml = (float2 *)((char *)workspace + pl.at.final_ml);
@@ -1283,13 +1378,9 @@ try {
             return rc;
         p.beside = true;
     }
-    if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)) || pl.fused ||
-        (!pl.direct && (rc = launch_join(p, pool->head_dim, rows, s))))
+    if ((rc = attention<true>(p, pool->head_dim, pl.nt, n_seqs, s)) || pl.fused)
         return rc;
-    return launch_kernel(true, many ? k_paged_weigh<8> : k_paged_weigh<1>, dim3((unsigned)gx, (unsigned)n_seqs),
-                         dim3(WEIGH_THREADS), 0, s, p, chunks) == cudaSuccess
-               ? HB_OK
-               : HB_ECUDA;
+    return finish_weigh(p, pool->head_dim, rows, chunks, s);
 } catch (...) {
     return HB_ENOMEM;
 }
