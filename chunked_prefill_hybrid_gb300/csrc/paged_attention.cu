@@ -29,11 +29,12 @@ using namespace paged;
 constexpr int WARPS = 4;
 constexpr int JOIN_WARPS = 8;
 // A warp takes a tile's keys alone up to so many of them, where there are so many
-// tiles: 88 sequences of 15 to 177 keys, 16 queries and 16 kv heads, 44 us with
-// four warps a tile and 35 so; 16 rows of 281 keys and 52 heads behind a prefix of
-// 4798, 46.4 and 52.8; 18 rows of 1024 keys and 40 heads, 65 and 77.
-constexpr int ALONE_KEYS = 192;
-constexpr long long ALONE_UNITS = 456;
+// tiles, and up to more where many tiles share their keys (us, four warps a tile and
+// so): 71 rows of 14 to 31 keys, 32 heads, 19.3 and 10.1; 16 rows of 281 behind a
+// prefix, 52 heads, 46.4 and 52.8; windows of 16 queries, 58 x 10 kv heads x 8 at
+// 260 keys, 160 and 127, 16 x 4 x 12 at 260, 22.1 and 23.8.
+constexpr int ALONE_KEYS = 192, ALONE_KEYS_SHARED = 512;
+constexpr long long ALONE_UNITS = 456, ALONE_UNITS_SHARED = 1200;
 constexpr int SMS = 152;
 constexpr int PART_MIN = 2;          // sub-tiles of a CTA of the prefixes' kernel at least
 constexpr long long SHARE_BYTES = 24 << 20;  // of all groups
@@ -864,7 +865,9 @@ int launch_attention(const Attn &p, int n_seqs, cudaStream_t s)
 // Whether a warp takes a tile's keys alone.
 bool alone(const Attn &p, int n_seqs)
 {
-    return p.split_len <= ALONE_KEYS && (long long)n_seqs * p.n_kv * p.col_tiles >= ALONE_UNITS;
+    const long long units = (long long)n_seqs * p.n_kv * p.col_tiles;
+    const bool shared = p.col_tiles > 1 && units >= ALONE_UNITS_SHARED;
+    return units >= ALONE_UNITS && p.split_len <= (shared ? ALONE_KEYS_SHARED : ALONE_KEYS);
 }
 
 template <int D, int NT, bool SCORES>
