@@ -490,6 +490,24 @@ def test_select_keeps_the_heaviest(lens, kv, keep, first, recent):
     assert np.array_equal(_select(w, tables, lens, keep, first, recent), ref.select(w, tables, lens, keep, first, recent))
 
 
+@pytest.mark.parametrize("lens,kv", [([500, 90, 70], 2), ([4000, 3500], 1), ([9000], 1), ([12000, 9000, 7000], 30)])
+@pytest.mark.parametrize("bits", [0, 1, 8, 12, 22])
+def test_select_where_the_first_digits_tell(lens, kv, bits):
+    """The heavier tokens, `keep` of them or a few more, differ from the others in their first bits only or in none."""
+    rng = np.random.default_rng(bits + kv)
+    w, tables = _weight_pool(rng, lens, kv)
+    keep = 64
+    low = rng.integers(0, 4, w.shape).astype(np.uint32)
+    w[:] = (np.uint32(0x3f000000) + low).view(np.float32)
+    for extra, m in zip((0, 3, 0), lens):
+        j = lens.index(m)
+        for h in range(kv):
+            at = rng.choice(m, keep + extra, replace=False)
+            x = (tables[j, at // 16], h, at % 16)
+            w[x] = (np.uint32(0x3f000000) + np.uint32(1 << (31 - bits) if 8 <= bits < 31 else bits << 24) + low[x]).view(np.float32)
+    assert np.array_equal(_select(w, tables, lens, keep, 2, 5), ref.select(w, tables, lens, keep, 2, 5))
+
+
 @pytest.mark.parametrize("seed", range(8))
 def test_select_ties_signs_and_numbers_that_are_none(seed):
     """Few distinct values, both zeros, infinities, NaN, denormals and negative ones: the lower position first."""
