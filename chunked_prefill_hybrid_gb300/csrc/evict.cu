@@ -404,6 +404,11 @@ struct MoveTile {
 // them or to batches before, and later ones may be on their way already.  In a
 // cluster a batch is stored one round after its barrier began.  Slots of a batch
 // are looked up while the batches before it load.
+//
+// Memory bounds it, by rows of 128 or 256 bytes that are gathered: 18 x 40 heads
+// that keep 512 of 1025 tokens 62 us, 5.8 TB/s read and written; 8 heads that keep
+// 65536 of 131000, 24 streams of 8 CTAs, 110 us, 4.6 TB/s (the same within 5 us with
+// clusters of 4 or 16, with 5 to 12 stages, and with no barriers).
 template <int PIECES, int P, int CTAS>
 __device__ __forceinline__ void move_rows(uint8_t *ring, uint8_t *pool, int num_blocks, int n_kv, int kvh, int rank,
                                           const int *from, int from_stride, const int *to, int to_stride,

@@ -188,7 +188,13 @@ __device__ __forceinline__ void put_weights(const Attn &p, float *to, float4 old
 // split.  KW = WARPS: a CTA has one tile, whose warps take the pages in turn, each
 // with a ring and a softmax of its own, and join their results in shared memory.
 // KW = 1, for many queries or few keys: each warp has a tile of its own, or a kv
-// head, and all pages.
+// head, and all pages.  BALANCE: splits go by the rows' lengths.
+//
+// The keys' stream bounds it: twelve warps an SM with a page of 8 KB each under way
+// beside the one in use (18 rows of 1024 keys, 40 heads, with weights: 64.6 us, 0.88
+// of a copy's rate; two pages a warp and three CTAs in place of three and two took 7
+// of 82 us).  That most of the MMAs' columns are idle for one query costs nothing
+// then; for more than eight a page's time is the MMAs' and the softmax's latency.
 template <int D, int NT, bool SCORES, int KW, bool BALANCE>
 __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_constant__ Attn p)
 {
@@ -543,7 +549,9 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
 }
 
 // The join of a row's partials, those of the common keys and of its own splits:
-// W warps a (row, head), each with every W-th partial.
+// W warps a (row, head), each with every W-th partial.  o = sum 2^((m_i - m) c2) o_i
+// / sum 2^((m_i - m) c2) l_i.  Latency bounds it, two reads that follow one another:
+// 3 to 4 us behind the attention (64 heads of 57 partials, 128 channels).
 template <int D, int W>
 __device__ __forceinline__ void join(const Attn &p, int split_len, int block, int n_rows)
 {
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_paged_join(const __grid_con
 // while it runs.  JOIN, for few CTAs: the join runs in this kernel's first CTAs,
 // and each of the others joins the (m, l) that it needs for itself, so that neither
 // waits for the other (us, as chosen and the other way: 2 rows of 30550 keys, 4
-// heads, 14.0 and 16.4; one of 131000, 8 x 8 heads, 101.5 and 107.9; 2 x 32
+// heads, 14.0 and 16.4; one of 131000, 8 x 8 heads, 102.6 and 107.9; 2 x 32
 // queries, 8 x 4 heads, 27.7 and 30.0).
 template <int SHARES, bool JOIN, int D, int W>
 __global__ void __launch_bounds__(WEIGH_THREADS)

@@ -22,6 +22,14 @@
 // up to 128 ("dual") both have the same tile and take the sub-tiles in turn, and
 // the CTA joins their two results.  S has two buffers a half.
 //
+// What bounds it: for up to 128 rows the stream of K and V (16 rows x 8 heads of 8
+// kv heads over 130000 keys: 87 us, 0.90 of a copy's rate; 64 keys are 0.75 us of an
+// SM's stream and 0.45 of its products).  For two tiles the products: a tile's S of
+// 64 keys and 128 channels takes 384 cycles (Q and K come from shared memory), P V
+// in two terms 512, the two in turn 875, the softmax less: 56 rows x 8 heads over
+// 16384 keys 46 us, the tensor pipe 70 % busy.  Boxes of 64 keys rather than 128 let
+// both halves have two buffers of S beside O in 512 columns.
+//
 // Every wait is bounded; when one runs out, the CTA writes NaN for its rows,
 // drains and returns.
 #include <cuda.h>

@@ -87,8 +87,8 @@ typedef struct {
  * a prefix makes its group's rows NaN.  Bytes of slots past a row's context
  * never reach its result.  Sums and softmax statistics are fp32 (a q . k that
  * overflows it makes its row NaN), the weights keep 16 significant bits;
- * results of differently shaped calls agree to fp32 rounding, not bit for bit;
- * one call repeated gives the same bits.
+ * results of differently shaped calls, or beside rows of other lengths, agree to
+ * fp32 rounding, not bit for bit; one call repeated gives the same bits.
  * Errors: HB_EINVAL, HB_ERANGE (bt_stride or workspace too small, max_ctx of
  * 2^27 or more, more than 65535 rows, more work than one launch holds),
  * HB_ECUDA.  n_rows = n_groups = 0 does nothing. */
