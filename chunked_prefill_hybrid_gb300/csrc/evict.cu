@@ -16,6 +16,7 @@ using namespace paged;
 
 constexpr int MOVE_THREADS = 256;
 constexpr int CLUSTER = 8;         // CTAs of a long sequence's kv head
+constexpr int WIDE = 16;            // or, for very few of them, sixteen
 constexpr int MOST_RANKS = 49152;  // of tokens that a CTA keeps in shared memory
 
 // ------------------------------------------------------------------- choice
@@ -614,6 +615,29 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) k_evict_move_few(const Move p,
 
 // ------------------------------------------------------------------- host
 
+// Whether clusters of sixteen CTAs run, for `items` kv heads of all sequences: they
+// need more of an SM group to be free, so that a kernel does not begin while another
+// ends.  Choice and move of half of the tokens, 128 channels (us, eight and sixteen):
+// 1 head of 6000 tokens 11.9 and 10.6, of 100000 68 and 41; 4 heads of 6000 12.2 and
+// 14.0, of 100000 79 and 66; 8 heads of 12000 22.0 and 25.1, of 131000 135 and 138.
+bool wide(long long items, int keep) { return items <= 2 || (items <= 4 && keep >= 16384); }
+
+// What a kernel needs once on each device (`done`: a bit for each): its shared
+// memory, and leave for clusters of more than eight CTAs.
+template <typename P>
+cudaError_t allow(void (*kernel)(P), int smem, int ctas, std::atomic<uint64_t> &done)
+{
+    if (ctas > 8) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && !(dev < 64 && done.load(std::memory_order_acquire) >> dev & 1))
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return kv4_allow_smem((const void *)kernel, smem, done);
+}
+
 // A launch of clusters of CTAS CTAs.
 template <int CTAS, typename P>
 cudaError_t launch_clusters(void (*kernel)(P), long long gx, int gy, int threads, int smem, cudaStream_t s, const P &p)
@@ -647,7 +671,7 @@ int launch_move(const Move &p, int n_seqs, cudaStream_t s)
     const long long gx = (long long)p.n_kv * CTAS * (p.w ? 3 : 2);
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
-    if (kv4_allow_smem((const void *)kernel, smem, done) != cudaSuccess)
+    if (allow(kernel, smem, CTAS, done) != cudaSuccess)
         return HB_ECUDA;
     return launch_clusters<CTAS>(kernel, gx, n_seqs, MOVE_THREADS, smem, s, p) == cudaSuccess ? HB_OK : HB_ECUDA;
 }
@@ -663,7 +687,7 @@ int launch_select(Select p, int n_seqs, cudaStream_t s)
     const long long gx = (long long)p.n_kv * CTAS;
     if (gx > 0x7fffffffll)
         return HB_ERANGE;
-    if (kv4_allow_smem((const void *)kernel, MOST_RANKS * 4, done) != cudaSuccess)
+    if (allow(kernel, MOST_RANKS * 4, CTAS, done) != cudaSuccess)
         return HB_ECUDA;
     return launch_clusters<CTAS>(kernel, gx, n_seqs, THREADS, smem, s, p) == cudaSuccess ? HB_OK : HB_ECUDA;
 }
@@ -710,8 +734,9 @@ try {
                    : HB_ECUDA;
     }
     if (max_len > 5500 + 78 * items || max_len > MOST_RANKS)
-        return items <= 24 ? launch_select<512, 11, CLUSTER>(p, n_seqs, s)
-                           : launch_select<256, 8, CLUSTER>(p, n_seqs, s);
+        return max_len > 50000 && wide(items, keep) ? launch_select<512, 11, WIDE>(p, n_seqs, s)
+               : items <= 24                        ? launch_select<512, 11, CLUSTER>(p, n_seqs, s)
+                                                    : launch_select<256, 8, CLUSTER>(p, n_seqs, s);
     return max_len <= 3000 ? launch_select<256, 8, 1>(p, n_seqs, s) : launch_select<512, 9, 1>(p, n_seqs, s);
 } catch (...) {
     return HB_ENOMEM;
@@ -777,6 +802,8 @@ try {
     // keep 1000 14.2 and 19.8, 3000 42.9 and 40.9
     if ((long long)keep * pool->head_dim <= 128 * (64 + 36 * items))
         return pool->head_dim == 128 ? launch_move<128, 1>(p, n_seqs, s) : launch_move<64, 1>(p, n_seqs, s);
+    if (wide(items, keep))
+        return pool->head_dim == 128 ? launch_move<128, WIDE>(p, n_seqs, s) : launch_move<64, WIDE>(p, n_seqs, s);
     return pool->head_dim == 128 ? launch_move<128, CLUSTER>(p, n_seqs, s) : launch_move<64, CLUSTER>(p, n_seqs, s);
 } catch (...) {
     return HB_ENOMEM;

@@ -42,9 +42,9 @@ constexpr long long SHARE_GROUP = 1 << 20;   // of one, where others are shared 
 // Bytes of own keys that an SM streams in a third of a sub-tile's time, halved
 // where contexts are taken to be half of max_ctx on average; more beside prefixes
 // bound by their products, which leave the memory to the others: 53.1 us so and
-// 47.5 with 30720 (1 + 7 + 56 rows, prefixes of 0, 333 and 16389), but 25.6 and
+// 47.5 with 32768 (1 + 7 + 56 rows, prefixes of 0, 333 and 16389), but 25.6 and
 // 27.5 (18 rows over 768 keys).
-constexpr int OWN_UNIT = 20480, OWN_UNIT_BESIDE = 30720;
+constexpr int OWN_UNIT = 20480, OWN_UNIT_BESIDE = 32768;
 // Sub-tiles from which on a window's keys go to the tensor cores' kernel, with
 // many queries of a kv head and with 17 to 48 (us): 4 sequences of 8 kv heads x
 // 8 x 16 queries at 200 keys 17.5 against 14.4, at 600 21 and 24, at 3000 41 and

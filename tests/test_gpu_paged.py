@@ -483,6 +483,7 @@ def _select(w, tables, lens, keep, first, recent, max_len=None):
     ([32, 31, 0, 1, 17], 3, 8, 1, 2), ([20, 32], 5, 32, 0, 0), ([64, 33, 63, 0, 48, 2, 32] * 4, 26, 24, 4, 3),
     ([3001, 5900], 3, 1000, 3, 7), ([10000, 100, 7] + [9] * 27, 1, 5000, 0, 5),
     ([500, 60001], 13, 100, 4, 8),
+    ([60001], 2, 100, 4, 8), ([51000, 16384, 70], 1, 16384, 0, 1000), ([90000, 55000], 2, 30000, 4, 64),  # clusters of 16
 ])
 def test_select_keeps_the_heaviest(lens, kv, keep, first, recent):
     rng = np.random.default_rng(sum(lens) + keep)
@@ -525,11 +526,10 @@ def test_select_ties_signs_and_numbers_that_are_none(seed):
                               ref.select(w, tables, lens, keep, first, recent)), (lens, keep)
 
 
-@pytest.mark.parametrize("kv,keep", [(1, 300000), (30, 100)])
-def test_select_of_more_tokens_than_a_cluster_keeps(kv, keep):
-    """Longer than eight CTAs' shared memory: the weights are read again in every pass.  Whole numbers, many of them
-    equal, so that the choice is by position too."""
-    n = 450000
+@pytest.mark.parametrize("kv,keep,n", [(1, 300000, 450000), (30, 100, 450000), (1, 300000, 900000)])
+def test_select_of_more_tokens_than_a_cluster_keeps(kv, keep, n):
+    """Longer than the shared memory of eight CTAs, or of sixteen: the weights are read again in every pass.  Whole
+    numbers, many of them equal, so that the choice is by position too."""
     tables = np.random.default_rng(2).permutation(n // 16 + 1)[None]
     w = torch.randint(0, 1000 if keep > 1000 else n, (n // 16 + 1, kv, 16), device="cuda").float()
     kept = torch.empty(1, kv, keep, dtype=torch.int32, device="cuda")
@@ -571,6 +571,7 @@ def _move_case(seed, d, kv, lens, keep, place):
     (64, 1, [9000], 7000), (128, 1, [6000, 6500], 3001), (128, 3, [100, 33, 20], 32), (64, 2, [70] * 19, 31),
     (128, 5, [30, 1, 0, 90, 33, 32, 17], 32), (64, 33, [15, 40], 3),
     (128, 1, [12000], 11000), (64, 4, [900, 2000, 1500], 800),
+    (64, 2, [20000, 17000], 16500), (128, 4, [17000], 16384), (128, 1, [3000], 1999),
 ])
 def test_move_brings_the_kept_tokens_to_the_front(place, d, kv, lens, keep):
     w, tables, new, k, v, kept = _move_case(sum(lens) + keep, d, kv, lens, keep, place)
