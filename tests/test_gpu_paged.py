@@ -373,7 +373,7 @@ def test_weigh_matches_the_plain_form(kv, group, d, ctx, nq, decay):
     (1, 1, 64, [12000] + [5] * 99, 1, 12000),                 # the splits of one row are all there are
     (1, 1, 64, [40 + 7 * j for j in range(200)], 1, 4000),
     (1, 1, 64, [900] * 227, 1, 1700),                         # no room for more CTAs than rows
-    (1, 1, 64, [900] * 257, 1, 70000),                        # more sequences than are looked at
+    (1, 1, 64, [900] * 257, 1, 70000),                        # one split: nothing to balance
 ])
 def test_weigh_splits_by_the_lengths_there_are(kv, group, d, ctx, nq, max_ctx):
     c = _weigh_case(len(ctx) + ctx[0] + 7, kv, group, d, ctx, nq)
