@@ -832,10 +832,18 @@ void plan_splits(long long n_rows, long long tiles, int keys, long long longest,
         *n = 1;
 }
 
+// Byte offsets of the workspace, from its first multiple of 32 on: partials and
+// scores are stored 32 bytes at a time, and a caller's workspace begins at 16.
+constexpr int WORK_ALIGN = 32, WORK_GIVEN = 16;
 struct Layout {
-    long long ml, o, scores, final_ml, groups, bytes;  // byte offsets of the workspace
+    long long ml, o, scores, final_ml, groups, bytes;
     long long score_stride;
 };
+
+char *work_base(void *workspace)
+{
+    return (char *)(((uintptr_t)workspace + WORK_ALIGN - 1) & ~(uintptr_t)(WORK_ALIGN - 1));
+}
 
 Layout layout(long long rows, int heads, int d, int slots, bool parts, int groups, bool scores, bool finals, int max_ctx)
 {
@@ -847,6 +855,8 @@ Layout layout(long long rows, int heads, int d, int slots, bool parts, int group
     w.final_ml = w.scores + rows * heads * w.score_stride * 4;
     w.groups = w.final_ml + (finals ? round_up(rows * heads * 8, 256) : 0);
     w.bytes = w.groups + (groups > INLINE_GROUPS ? round_up((long long)groups * sizeof(Group), 256) : 0);
+    if (w.bytes > 0)
+        w.bytes += WORK_ALIGN - WORK_GIVEN;
     return w;
 }
 
@@ -1132,7 +1142,7 @@ void params(Attn *a, const hb_paged_pool *pool, const void *q, long long q_strid
     p.seq_part_len = pl.seq_part_len;
     p.out = (bf16 *)out;
     p.out_stride = out_stride;
-    char *w = (char *)workspace;
+    char *w = work_base(workspace);
     p.part_ml = (float2 *)(w + pl.at.ml);
     p.part_o = (float *)(w + pl.at.o);
     p.scores = (float *)(w + pl.at.scores);
@@ -1200,7 +1210,7 @@ int finish_weigh(const Attn &p, int d, int rows, int chunks, cudaStream_t s)
 
 int check_workspace(const void *workspace, long long bytes, long long need)
 {
-    if (need > 0 && (!workspace || (uintptr_t)workspace % 16))
+    if (need > 0 && (!workspace || (uintptr_t)workspace % WORK_GIVEN))
         return HB_EINVAL;
     return bytes < need ? HB_ERANGE : HB_OK;
 }
@@ -1290,7 +1300,7 @@ try {
     p.n_seqs = n_rows;
     p.n_groups = n_groups;
     if (n_groups > INLINE_GROUPS) {  // the groups go ahead into the workspace
-        Group *list = (Group *)((char *)workspace + pl.at.groups);
+        Group *list = (Group *)(work_base(workspace) + pl.at.groups);
         bool sent = true;
         plan_shared(n_rows, n_heads, pool->n_kv_heads, pool->head_dim, pool->num_blocks, max_ctx, group_rows, prefix_lens,
                     n_groups, &pl, [&](int i, const Group &g) {
@@ -1381,7 +1391,7 @@ try {
     if ((long long)p.n_kv * chunks > 0x7fffffffll)
         return HB_ERANGE;
     if (!pl.fused)
-        p.final_ml = (float2 *)((char *)workspace + pl.at.final_ml);
+        p.final_ml = (float2 *)(work_base(workspace) + pl.at.final_ml);
     if (pl.ctas > 0) {
         p.lose = test_lose;
         test_lose = false;
