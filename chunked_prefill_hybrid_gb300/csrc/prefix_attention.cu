@@ -58,7 +58,9 @@ constexpr int MMA_WARP = 16, LOAD_WARP = 18;
 constexpr int THREADS = 20 * 32;
 constexpr float LOWEST = -3e38f;         // below every score, and finite: differences with it are too
 constexpr float RAISE = 8.f;             // in powers of two: how far a score may pass the maximum used
-constexpr float HUGE_SCORE = 1 << 20;    // up to it s c2 - m c2 may be fused: m c2 is rounded by 2^-4 at most, for all P alike
+// Up to it P = 2^(s c2 - m c2) with one fused step a score: m c2 is rounded, by 2^-4
+// at most, and the sums have that factor until m changes or they are given out.
+constexpr float HUGE_SCORE = 1 << 20;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // after which a wait is given up
 
 template <int D>
@@ -309,6 +311,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         };
         float m = LOWEST, l = 0.f;
         float raise_at = LOWEST;  // a maximum above it moves m
+        // P = 2^(s c2 + offset(m)), or of the difference where that is huge; sums of it
+        // times 2^residue(m) are those of 2^((s - m) c2)
+        auto offset = [&](float max) { return __fmul_rn(-max, p.c2); };
+        auto residue = [&](float max) {
+            const float off = offset(max);
+            return fabsf(off) > HUGE_SCORE ? 0.f : __fmaf_rn(-max, p.c2, -off);
+        };
         float *score_at = nullptr;
         if (SCORES)
             score_at = p.scores + (((size_t)table * p.n_kv + kvh) * (gr.rows * p.group) + c0 + (dual ? 0 : half * 128) + r) *
@@ -354,13 +363,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             my_max[buf * 512] = mx;
             pair_sync();
             mx = fmaxf(mx, its_max[buf * 512]);
-            float off = -m * p.c2;  // P = 2^(s c2 + off)
+            float off = offset(m);
             if (__any_sync(0xffffffffu, mx > raise_at)) {  // as the other warp finds: it has the same maxima
-                const float mn = fmaxf(m, mx), corr = ex2((m - mn) * p.c2);
+                const float mn = fmaxf(m, mx), corr = ex2((m - mn) * p.c2 + (residue(m) - residue(mn)));
                 m = mn;
                 l *= corr;
                 raise_at = m + RAISE / p.c2;
-                off = -m * p.c2;
+                off = offset(m);
                 if (fabsf(off) > HUGE_SCORE) {  // the difference first; and here again with every sub-tile
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -442,15 +451,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                          : "memory");
         }
         tmem_ld_wait();
-        // f, f2: factors of the two halves' O, where both are of the same rows
-        float f = 1.f, f2 = 0.f;
-        l = o[0].y + o[1].y;
-        if (dual) {
+        // f, f2: factors of the two halves' sums, where both are of the same rows
+        if (dual)
             m = fmaxf(o[0].x, o[2].x);
-            f = ex2((o[0].x - m) * p.c2);
-            f2 = ex2((o[2].x - m) * p.c2);
-            l = l * f + (o[2].y + o[3].y) * f2;
-        }
+        const float f = ex2((o[0].x - m) * p.c2 + residue(o[0].x));
+        const float f2 = dual ? ex2((o[2].x - m) * p.c2 + residue(o[2].x)) : 0.f;
+        l = (o[0].y + o[1].y) * f;
+        if (dual)
+            l += (o[2].y + o[3].y) * f2;
         __syncwarp();
         ok = !__any_sync(0xffffffffu, !ok || *abort_flag);
         const int width = dual ? D / 4 : D / 2;  // channels of this thread
@@ -470,11 +478,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (two)
                         tmem_ld_32x32b_x16(lanes + C::O0 + D + e, y);
                     tmem_ld_wait();
-                    if (dual)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            x[j] = __float_as_uint(__uint_as_float(x[j]) * f +
-                                                   (two ? __uint_as_float(y[j]) * f2 : 0.f));
+                    for (int j = 0; j < 16; ++j)
+                        x[j] = __float_as_uint(__uint_as_float(x[j]) * f + (two ? __uint_as_float(y[j]) * f2 : 0.f));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)

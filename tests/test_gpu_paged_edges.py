@@ -1,6 +1,7 @@
 """The attention calls of include/hb_paged.h on the GPU where workspaces and
 numbers are the least usual that they allow, against plain 64-bit forms
 (paged_ref.py)."""
+import numpy as np
 import pytest
 
 from chunked_prefill_hybrid_gb300 import paged
@@ -60,3 +61,86 @@ def test_weigh_takes_any_workspace_at_sixteen_bytes(kv, group, d, ctx, nq):
         got = _weigh(c, nq, 0.5, ws)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), offset
         assert whole(), offset
+
+
+def _level_scores(c, rng, scale):
+    """K and q so that every score is exact in 32 bits, of magnitude `scale` to twice that, and the keys of a row lie within 24 of one
+    another: q . k = q0 k0 + q1 k1 with few bits in each, rising with the position.  V tells where a key lies."""
+    n, heads, d = c.q.shape
+    for j in range(len(c.ctx)):
+        t = np.arange(int(c.ctx[j]) + 1)
+        p = c.prefix[int(np.searchsorted(np.cumsum(c.rows), j, side="right"))]
+        level = np.where(t < p, 8 * t // max(1, p), 3 + j % 4)
+        page, slot = _dev(c.tables[j, t // 16], np.int64), _dev(t % 16, np.int64)
+        # the last digit of a token's level goes by its position alone, as rows share the prefix' tokens
+        value = torch.from_numpy((level + (t * 7919 % 13) % 5).astype(np.float32)).cuda()
+        c.k[page, :, slot, 0] = 2.0 ** 6
+        c.k[page, :, slot, 1] = value.to(torch.bfloat16)[:, None]
+        c.v[page, :, slot] = (0.25 * torch.randn(c.kv, len(t), d, generator=rng, device="cuda").transpose(0, 1)
+                              + torch.where(torch.from_numpy(t % 512 < 256).cuda(), 1.0, -1.0)[:, None, None]).to(torch.bfloat16)
+    c.q.zero_()
+    at = torch.arange(n * heads, device="cuda").view(n, heads) % 32
+    c.q[:, :, 0] = ((1 + at / 64) * scale * 2.0 ** -6 * torch.where(at % 3 == 2, -1.0, 1.0)).to(torch.bfloat16)
+    c.q[:, :, 1] = 2.0
+
+
+def _exact(c, j, row, see):
+    """o, p and sum p |v| of one row whose scores are exact."""
+    d = c.d
+    page = _dev(c.tables[j, :(see + 15) // 16]).long()
+    k, v = (pool[page].double().transpose(0, 1).flatten(1, 2)[:, :see] for pool in (c.k, c.v))
+    s = torch.einsum("hgd,hkd->hgk", c.q[row].double().view(c.kv, c.group, d), k)
+    assert torch.equal(s, s.float().double()) and float((s.amax(-1) - s.amin(-1)).max()) <= 24
+    p = torch.softmax(s / d ** 0.5, -1)
+    return torch.einsum("hgk,hkd->hgd", p, v), p, torch.einsum("hgk,hkd->hgd", p, v.abs())
+
+
+# A weight 2^((s - m) log2(e) / sqrt d) of exact scores at most 24 apart: an exponent of at most 24 x 1.45 / 8 < 5 with
+# log2(e) / sqrt d off by 2^-23 of it and a product rounded by 2^-24 (together < 2^-20), and four exponentials (its own,
+# a rescaled maximum's, the halves' and the join's) of 2^-22 each
+EXACT_EPS = 2.0 ** -20 + 4 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 6, 2.0 ** 15, 2.0 ** 20, 2.0 ** 21, 2.0 ** 22, 2.0 ** 23])
+@pytest.mark.parametrize("kv,group,d,rows,prefix", [
+    (1, 1, 128, 20, 6000),       # one Q tile
+    (1, 8, 128, 20, 6000),       # two
+    (2, 3, 64, 30, 4001),        # one
+])
+def test_shared_large_scores_that_are_exact(kv, group, d, rows, prefix, scale):
+    """Whatever the scores' magnitude, keys of all parts of a prefix and own keys are weighed by their differences."""
+    ctx = [prefix + 30 + 11 * j for j in range(rows)]
+    c = Case(81, kv, group, d, [rows], [prefix], ctx, poison=False)
+    assert (rows - 1) * (prefix // 16 * 16) * kv * 4 * d >= 24 << 20
+    _level_scores(c, torch.Generator(device="cuda").manual_seed(3), scale)
+    for max_ctx in (max(ctx), max(ctx) + 3000):
+        out = c.run(max_ctx=max_ctx)
+        for j in range(rows):
+            m = ctx[j] + 1
+            o, _, w = _exact(c, j, j, m)
+            bound = 2.0 ** -8 * o.abs() + w * (2.0 ** -16 + 2 * EXACT_EPS + (m / 16 + 64) * 2.0 ** -23)
+            off = (out[j].double().view_as(o) - o).abs()
+            assert (off <= bound).all(), (j, (off / bound).max(), off.max())
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 6, 2.0 ** 15, 2.0 ** 20, 2.0 ** 21, 2.0 ** 22, 2.0 ** 23])
+@pytest.mark.parametrize("kv,group,d,nq", [(1, 4, 128, 32), (2, 2, 64, 70)])
+def test_weigh_large_scores_that_are_exact(kv, group, d, nq, scale):
+    """The same for a window's rows and their weights."""
+    ctx = [4000, 2600]
+    c = _weigh_case(82, kv, group, d, ctx, nq, poison=False)
+    c.prefix = [x + 1 for x in ctx]
+    _level_scores(c, torch.Generator(device="cuda").manual_seed(4), scale)
+    out, w = _weigh(c, nq, 0.0)
+    for j, x in enumerate(ctx):
+        total = torch.zeros(kv, x + 1, dtype=torch.float64, device="cuda")
+        for i in range(nq):
+            see = x + 1 - (nq - 1) + i
+            o, p, mass = _exact(c, j, j * nq + i, see)
+            bound = 2.0 ** -8 * o.abs() + mass * (2.0 ** -16 + 2 * EXACT_EPS + (see / 16 + 64) * 2.0 ** -23)
+            off = (out[j * nq + i].double().view_as(o) - o).abs()
+            assert (off <= bound).all(), (j, i, (off / bound).max())
+            total[:, :see] += p.sum(1)
+        got = w[_dev(c.wtables[j, :(x + 16) // 16]).long()].double().transpose(0, 1).flatten(1, 2)[:, :x + 1]
+        # a weight and the sum that it is divided by are off by EXACT_EPS each, and sums of see and nq x group numbers
+        assert ((got - total).abs() <= total * (2 * EXACT_EPS + (x / 16 + 64 + nq * group) * 2.0 ** -23)).all()
