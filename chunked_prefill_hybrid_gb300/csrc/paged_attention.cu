@@ -16,7 +16,9 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "kv4_host.h"
 #include "paged.h"
@@ -111,6 +113,16 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
     const __nv_bfloat162 r = __floats2bfloat162_rn(x - f.x, y - f.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// A bf16 pair with what is beyond the finite numbers brought back to the largest of
+// its sign.  V is multiplied by P = hi + lo, of which lo may be 0 or negative: an
+// infinity is the high term's alone.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x)
+{
+    uint32_t y;
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7f7f7f7fu));
+    return y;
 }
 
 // A bf16 pair with an infinity or a NaN in it.
@@ -412,10 +424,11 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
             ldmatrix4_trans(a, vpage + place<D>((lane & 7) + 8 * (mi >> 1), 2 * x + (mi & 1)));
             if (p.nq == 1 || key0 + 16 <= fewest ||
                 !__any_sync(0xffffffffu, odd_pair(a[0]) || odd_pair(a[1]) || odd_pair(a[2]) || odd_pair(a[3]))) {
+                const uint32_t b[4] = {finite_pair(a[0]), finite_pair(a[1]), finite_pair(a[2]), finite_pair(a[3])};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_bf16(o[nt][x], a, hi[nt][0], hi[nt][1]);
-                    mma_bf16(o[nt][x], a, lo[nt][0], lo[nt][1]);
+                    mma_bf16(o[nt][x], b, lo[nt][0], lo[nt][1]);
                 }
                 continue;
             }
@@ -548,6 +561,40 @@ __global__ void __launch_bounds__(WARPS * 32) k_paged_attention(const __grid_con
     leave();
 }
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
+
+// Infinities and NaN of V in E channels, of a table's first keys (a multiple of 16),
+// added up without their weights; 0 where there are none.
+template <int D, int E>
+__device__ __forceinline__ void odd_values(const Attn &p, const int *table, int kvh, int keys, int channel, float (&s)[E])
+{
+    constexpr int BATCH = 8;
+    using V = typename std::conditional<E == 4, uint2, uint32_t>::type;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        s[e] = 0.f;
+    int next = __ldg(table);
+#pragma unroll 1
+    for (int t = 0; t < keys; t += BATCH) {
+        const int blk = next;
+        next = __ldg(table + (min(t + BATCH, keys - 1) >> 4));
+        if (blk < 0 || blk >= p.num_blocks)
+            continue;
+        const bf16 *at = p.v + (((size_t)blk * p.n_kv + kvh) * 16 + (t & 15)) * D + channel;
+        V v[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            v[u] = *reinterpret_cast<const V *>(at + u * D);
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = bf2f(reinterpret_cast<const bf16 *>(&v[u])[e]);
+                s[e] += finite(x) ? 0.f : x;
+            }
+    }
+}
+
 // The join of a row's partials, those of the common keys and of its own splits:
 // W warps a (row, head), each with every W-th partial.  o = sum 2^((m_i - m) c2) o_i
 // / sum 2^((m_i - m) c2) l_i.  Latency bounds it, two reads that follow one another:
@@ -565,12 +612,13 @@ __device__ __forceinline__ void join(const Attn &p, int split_len, int block, in
     const int row = (int)(item / p.n_heads), head = (int)(item % p.n_heads);
     const int seq = row / p.nq;
     const int ctx = p.ctx_lens[seq];
-    int from = 0, least = 0, parts = 0;
+    int from = 0, least = 0, parts = 0, row0 = seq;
     if (p.n_groups > 0) {
         const Group gr = p.of(seq);
         from = gr.shared;
         least = gr.prefix > 0 ? gr.prefix - 1 : 0;
         parts = gr.parts;
+        row0 = gr.row0;
     }
     const bool in = ctx >= least && ctx <= p.max_ctx;
     if (p.n_groups == 0 && in) {
@@ -641,6 +689,26 @@ __device__ __forceinline__ void join(const Attn &p, int split_len, int block, in
             for (int e = 0; e < E; ++e)
                 acc[e] += s_o[warp + w][lane * E + e];
         }
+    }
+    float all = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        all += acc[e];
+    if (all * 0.f != 0.f && sum > 0.f && parts > 0) {
+        // An infinity in V: the common keys' products have both terms of P with V as it
+        // is, and what they give for it says nothing.  So the infinities themselves, and
+        // those of the own keys' results.
+        float odd[E];
+        odd_values<D>(p, p.tables + (size_t)row0 * p.bt_stride, head / p.group, from, lane * E, odd);
+        for (int i = parts; i < n; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = __ldcg(p.part_o + slot(i) * D + lane * E + e);
+                odd[e] += finite(x) ? 0.f : x;
+            }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = finite(acc[e]) || odd[e] == 0.f ? acc[e] : odd[e];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e)  // padding, and a row that sees no key: zeros; outside its range: NaN

@@ -87,6 +87,8 @@ typedef struct {
  * a prefix makes its group's rows NaN.  Bytes of slots past a row's context
  * never reach its result.  Sums and softmax statistics are fp32 (a q . k that
  * overflows it makes its row NaN), the weights keep 16 significant bits;
+ * an infinity in V that a row sees is its result in that channel, beside the
+ * opposite one NaN, and either where its weight is 0 in fp32;
  * results of differently shaped calls, or beside rows of other lengths, agree to
  * fp32 rounding, not bit for bit; one call repeated gives the same bits.
  * Errors: HB_EINVAL, HB_ERANGE (bt_stride or workspace too small, max_ctx of

@@ -144,3 +144,104 @@ def test_weigh_large_scores_that_are_exact(kv, group, d, nq, scale):
         got = w[_dev(c.wtables[j, :(x + 16) // 16]).long()].double().transpose(0, 1).flatten(1, 2)[:, :x + 1]
         # a weight and the sum that it is divided by are off by EXACT_EPS each, and sums of see and nq x group numbers
         assert ((got - total).abs() <= total * (2 * EXACT_EPS + (x / 16 + 64 + nq * group) * 2.0 ** -23)).all()
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+def _plant(c, j, at):
+    """Infinities and NaN in V of row j's tokens, of every kv head: channel -> token, value.  Channels 1 to 5 become
+    +inf, -inf, +inf of two tokens, NaN of two infinities, NaN."""
+    a, b = at
+    for t, e, x in ((a, 1, INF), (b, 2, -INF), (a, 3, INF), (b, 3, INF), (a, 4, INF), (b, 4, -INF), (b, 5, NAN)):
+        c.v[int(c.tables[j, t // 16]), :, t % 16, e] = x
+
+
+def _planted(out, was, seen, by_key=False):
+    """out against the call without them: rows `seen` have what _plant says, everything else has the same bits.  by_key:
+    the channels beside them are summed in another order, each within 2^-8 of itself and 2^-15 of sum p |v| < 1 of the
+    formula's."""
+    got, want = out.clone(), was.clone()
+    want[seen, :, 1], want[seen, :, 2], want[seen, :, 3] = INF, -INF, INF
+    want[seen, :, 4:6] = NAN
+    bad = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), bad)
+    if by_key:
+        bad |= torch.isinf(want)
+        assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)])
+        assert ((got - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -14)[~bad].all()
+    else:
+        assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("kv,group,d,ctx,at", [
+    (1, 1, 64, [0, 4], (0, 0)),               # one key, whose weight is 1
+    (2, 1, 128, [5, 40], (2, 3)),
+    (1, 12, 64, [333, 100], (17, 300)),       # four warps, more than eight heads
+    (1, 2, 128, [3000, 2100], (5, 2999)),     # splits and their join
+    (2, 1, 64, [60000], (100, 59999)),        # many splits
+    (4, 1, 64, [100] * 150, (3, 99)),         # a warp a row and head
+])
+def test_shared_infinities_in_v(kv, group, d, ctx, at):
+    """An infinity of V that a row sees is that row's, in its channel alone."""
+    c = Case(91, kv, group, d, [1] * len(ctx), [0] * len(ctx), ctx)
+    was = c.run()
+    if at[0] == at[1]:
+        c.v[int(c.tables[0, 0]), :, 0, 1], c.v[int(c.tables[0, 0]), :, 0, 2] = INF, -INF
+        out = c.run()
+        want = was.clone()
+        want[0, :, 1], want[0, :, 2] = INF, -INF
+        assert torch.equal(out, want)
+        return
+    _plant(c, 0, at)
+    _planted(c.run(), was, [0])
+
+
+@pytest.mark.parametrize("kv,group,d,rows,prefix,at", [
+    (2, 1, 128, 18, 1500, (3, 1400)),         # one Q tile
+    (1, 20, 64, 30, 3603, (64, 65)),          # several, neighbours
+    (50, 1, 128, 21, 64, (0, 63)),            # one sub-tile
+    (2, 1, 128, 18, 1500, (1501, 1510)),      # a row's own keys
+    (1, 8, 128, 20, 6000, (5999, 3000)),
+])
+def test_shared_prefix_infinities_in_v(kv, group, d, rows, prefix, at):
+    assert (rows - 1) * (prefix // 16 * 16) * kv * 4 * d >= 24 << 20
+    c = Case(92, kv, group, d, [rows], [prefix], [prefix + 20 + j for j in range(rows)])
+    was = c.run()
+    _plant(c, 0, at)
+    everyone = all(t < prefix // 16 * 16 for t in at)
+    _planted(c.run(), was, list(range(rows)) if everyone else [0])
+
+
+def test_shared_infinity_of_a_key_that_weighs_nothing():
+    """A weight that is 0 in 32 bits: its channel is infinite or not a number, and the others have the same bits."""
+    for rows, prefix, ctx in (([1], [0], [3000]), ([20], [2000], [2100] * 20), ([3], [0], [200, 180, 150])):
+        c = Case(93, 2, 1, 128, rows, prefix, ctx, poison=False)
+        t = 77
+        c.k[int(c.tables[0, t // 16]), :, t % 16] = 0.0
+        c.k[int(c.tables[0, t // 16]), :, t % 16, 0] = -30000.0
+        c.q[:, :, 0] = 5.0
+        was = c.run()
+        c.v[int(c.tables[0, t // 16]), :, t % 16, 7] = INF
+        out = c.run()
+        seen = slice(0, None if prefix[0] else 1)
+        assert (torch.isnan(out) | (out == INF))[seen, :, 7].all()
+        out[seen, :, 7] = was[seen, :, 7]
+        assert torch.equal(out, was)
+
+
+@pytest.mark.parametrize("kv,group,d,ctx,nq,at", [
+    (1, 3, 64, [60], 6, (10, 20)),            # pages that all queries see, no common keys
+    (2, 1, 128, [40, 30], 1, (3, 39)),
+    (1, 8, 64, [9000, 40], 1, (100, 8999)),   # splits, the join beside the weights
+    (1, 4, 128, [1300, 200], 70, (5, 1000)),  # common keys
+    (2, 2, 64, [1500, 70], 16, (700, 1484)),  # common keys and a page that not all of them see in whole
+])
+def test_weigh_infinities_in_v(kv, group, d, ctx, nq, at):
+    """The same, and the weights do not change."""
+    c = _weigh_case(94, kv, group, d, ctx, nq)
+    was, weights = _weigh(c, nq, 0.5)
+    _plant(c, 0, at)
+    out, w = _weigh(c, nq, 0.5)
+    _planted(out, was, list(range(nq)), by_key=at[1] > ctx[0] - 17 and nq > 1)
+    assert torch.equal(w, weights)
