@@ -746,13 +746,15 @@ __global__ void __launch_bounds__(WEIGH_THREADS)
     static_assert(WEIGH_THREADS == JOIN_WARPS * 32);
     __shared__ float2 s_ml[CHUNK];
     __shared__ float4 s_a[SHARES > 1 ? SHARES - 1 : 1][QUADS];
-    const int split_len = JOIN ? p.balanced() : 0;  // JOIN: at most 16 queries a kv head, no common keys, several splits
-    if constexpr (JOIN)
+    [[maybe_unused]] int split_len;
+    if constexpr (JOIN) {  // at most 16 queries a kv head, no common keys, several splits
+        split_len = p.balanced();
         if ((int)blockIdx.x < join_blocks) {
             pdl_wait();
             pdl_trigger();
             return join<D, W>(p, split_len, blockIdx.x, n_rows);
         }
+    }
     int seq = blockIdx.y, kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     if constexpr (JOIN) {  // all in one row of the grid
         const int at = (int)blockIdx.x - join_blocks;
@@ -793,8 +795,6 @@ __global__ void __launch_bounds__(WEIGH_THREADS)
         return;
     if (!early && some)
         load(share * each0, min(min(CHUNK, ncols), (share + 1) * each0));
-    const Group gr = p.sequence(seq, ctx);
-    const int parts = gr.parts, n_parts = parts + (ctx + 1 - gr.shared + split_len - 1) / split_len;
     float a[4] = {0.f, 0.f, 0.f, 0.f};
     for (int q0 = 0; q0 < ncols; q0 += CHUNK) {
         const int n = min(CHUNK, ncols - q0), each = (n + SHARES - 1) / SHARES;
@@ -808,6 +808,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS)
             for (int c = threadIdx.x; c < n; c += WEIGH_THREADS)
                 s_ml[c] = __ldcg(p.final_ml + row_head(c));
         } else {  // LANES threads a query, each with every LANES-th partial
+            const int n_parts = (ctx + split_len) / split_len;
             for (int b = 0; b < n; b += WEIGH_THREADS / LANES) {
                 const int c = b + (int)threadIdx.x / LANES;
                 const float2 *ml = p.part_ml + row_head(min(c, n - 1)) * p.n_slots;
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(WEIGH_THREADS)
                 };
 #pragma unroll 4
                 for (int x = threadIdx.x % LANES; x < n_parts; x += LANES) {
-                    const float2 y = __ldcg(ml + (x < parts ? x : p.first_slot + x - parts));
+                    const float2 y = __ldcg(ml + x);
                     add(y.x, y.y);
                 }
                 __syncwarp();
