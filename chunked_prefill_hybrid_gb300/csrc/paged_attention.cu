@@ -117,7 +117,8 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
 
 // A bf16 pair with what is beyond the finite numbers brought back to the largest of
 // its sign.  V is multiplied by P = hi + lo, of which lo may be 0 or negative: an
-// infinity is the high term's alone.
+// infinity is the high term's alone.  128 rows' own keys beside a prefix take 103.6 us
+// with it and 103.1 without, 4 short rows 4.00 and 3.94.
 __device__ __forceinline__ uint32_t finite_pair(uint32_t x)
 {
     uint32_t y;
@@ -203,7 +204,7 @@ __device__ __forceinline__ void put_weights(const Attn &p, float *to, float4 old
 // head, and all pages.  BALANCE: splits go by the rows' lengths.
 //
 // The keys' stream bounds it: twelve warps an SM with a page of 8 KB each under way
-// beside the one in use (18 rows of 1024 keys, 40 heads, with weights: 64.6 us, 0.88
+// beside the one in use (18 rows of 1024 keys, 40 heads, with weights: 64.7 us, 0.87
 // of a copy's rate; two pages a warp and three CTAs in place of three and two took 7
 // of 82 us).  That most of the MMAs' columns are idle for one query costs nothing
 // then; for more than eight a page's time is the MMAs' and the softmax's latency.
@@ -697,7 +698,7 @@ __device__ __forceinline__ void join(const Attn &p, int split_len, int block, in
     if (all * 0.f != 0.f && sum > 0.f && parts > 0) {
         // An infinity in V: the common keys' products have both terms of P with V as it
         // is, and what they give for it says nothing.  So the infinities themselves, and
-        // those of the own keys' results.
+        // those of the own keys' results (16 rows x 64 heads behind 60000 keys: 4.5 ms).
         float odd[E];
         odd_values<D>(p, p.tables + (size_t)row0 * p.bt_stride, head / p.group, from, lane * E, odd);
         for (int i = parts; i < n; ++i)

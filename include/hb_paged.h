@@ -79,6 +79,9 @@ typedef struct {
  *                 attends nothing and gets zeros
  *   group_rows:   host int32 [n_groups], each > 0, n_rows in all
  *   prefix_lens:  host int32 [n_groups], each in [0, max_ctx + 1]
+ *   max_ctx:      what ctx_lens may be at most.  Prefixes are cut beside own keys
+ *                 as long as it allows: one far above them is right, but leaves a
+ *                 prefix of few kv heads to few SMs
  *   workspace:    device, 16-byte aligned, of at least
  *                 hb_decode_shared_workspace() bytes (which may be 0); its
  *                 contents mean nothing before and after the call
@@ -120,6 +123,7 @@ long long hb_decode_shared_workspace(int n_rows, int n_heads, int n_kv_heads, in
  *                  max_ctx / 16 + 1.  No two sequences of a call may have a
  *                  weight block in common, nor has one sequence a block twice:
  *                  its slots would hold either's sums
+ *   max_ctx:       as above: a window's common keys are cut by it
  *   decay:         finite, in [0, 1]
  *   workspace:     as above, hb_decode_weigh_workspace() bytes (4 for each row,
  *                  head and key of max_ctx, and partial results)
